@@ -78,7 +78,9 @@ typedef enum {
     SSM_ERR_HIP = -6,       /* the HIP runtime reported a launch error          */
     SSM_ERR_ALIAS = -7,     /* an output overlaps an input                      */
     SSM_ERR_WAIT = -8,      /* a segment's bounded wait gave up (ssm_scan_status) */
-    SSM_ERR_SCRATCH = -9    /* the shape needs more than SSM_SCRATCH_BYTES (noalloc) */
+    SSM_ERR_SCRATCH = -9,   /* the shape needs more than SSM_SCRATCH_BYTES (noalloc) */
+    SSM_ERR_VALUE = -10,    /* eps or max_norm is negative or not finite          */
+    SSM_ERR_HOST = -11      /* host memory for checking a list could not be had   */
 } ssm_status_t;
 
 /*
@@ -422,6 +424,176 @@ size_t ssd_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, i
                                 int64_t dstate, int io_dtype);
 
 /*
+ * ssm_gated_scan_fwd -- the gated linear recurrence: a scan whose decay is a
+ * gate of its own per step and channel, with no B / C readout (the discrete
+ * recurrence of the youngju.dev guide, section 2, with an input-dependent
+ * decay as in section 5, one state per channel as on the "Windows SM1" page,
+ * and the block's SiLU gate).  For every batch b, channel d and step t:
+ *     v        = g[b,t,d] + gate_bias[d]              (bias optional)
+ *     a        = sigmoid(v)
+ *     h        = a * h + (1 - a) * x[b,t,d]           (1 - a taken as sigmoid(-v))
+ *     y[b,t,d] = h * SiLU(z[b,t,d])                   (y = h without z)
+ * from h0[b,d] (or 0); last_state[b,d] = h after the last step (h0 when
+ * seqlen = 0).  An infinite gate is exact: g = +inf keeps the state (the way
+ * to pad a batch of unequal lengths), g = -inf restarts it (h = x: the way to
+ * pack several sequences into one row); x has to be finite there.
+ *   x, g, z      : (batch, seqlen, d_inner) io dtype; step (b, t) starts
+ *                  ldx, ldg, ldz elements after the one before it, so each may
+ *                  be a column range of a wider tensor (ld >= d_inner when there
+ *                  is more than one step; SSM_ERR_SHAPE otherwise)
+ *   gate_bias    : (d_inner) fp32, optional
+ *   h0, last_state : (batch, d_inner) fp32, optional
+ *   y            : (batch, seqlen, d_inner) io dtype, contiguous
+ *   ckpt         : optional output, fp32 (batch, ceil(seqlen / 128), d_inner):
+ *                  ckpt[b,j,d] is the state entering step 128 j, for
+ *                  ssm_gated_scan_bwd; 4-byte aligned
+ *   128 steps of a row stride (128 * ld elements) must span less than 2 GiB
+ *   (SSM_ERR_SHAPE).  Workspace: ssm_gated_scan_workspace_bytes, 256-byte
+ *   aligned (NULL when that is 0).  Calls that overlap in time need workspaces
+ *   of their own; calls on one stream may share one.
+ *   Long sequences are cut into time tiles that hand their aggregates on
+ *   through the workspace, folded in a fixed order: results are deterministic.
+ *   ssm_scan_status applies to this call's workspace, when it is not 0 bytes.
+ */
+int ssm_gated_scan_fwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+                       const void *z, int64_t ldz, const float *h0, void *y, float *last_state,
+                       float *ckpt, int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes ssm_gated_scan_fwd needs (0 = none); (size_t)-1 for invalid
+ * arguments. */
+size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype);
+
+/* Bytes of ssm_gated_scan_fwd's checkpoints: batch x ceil(seqlen / 128) x
+ * d_inner fp32; (size_t)-1 for invalid arguments. */
+size_t ssm_gated_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t d_inner);
+
+/*
+ * ssm_gated_scan_bwd -- the gradient of ssm_gated_scan_fwd, exactly as
+ * defined above.  With e_t = dL/dh_t:
+ *     e_t  = dout_t SiLU(z_t) + a_{t+1} e_{t+1}   (+ dlast at the last step)
+ *     dx   = (1 - a) e     dg = e (h_{t-1} - x) a (1 - a)
+ *     dz   = dout h SiLU'(z)     dgate_bias = sum over b, t of dg     dh0 = a_0 e_0
+ *   Inputs: the forward's (same strides), plus
+ *     dout : (batch, seqlen, d_inner) io dtype, contiguous   -- dL/dy
+ *     dlast: (batch, d_inner) fp32, optional                 -- dL/dlast_state
+ *     ckpt : what ssm_gated_scan_fwd recorded on the same inputs, or NULL: the
+ *            call then computes it first (one more read of x and g)
+ *   Outputs (overwritten): dx, dg (batch, seqlen, d_inner) io dtype, required;
+ *     dz the same, required when z is given; dgate_bias (d_inner) fp32,
+ *     optional (written even when gate_bias is NULL); dh0 (batch, d_inner)
+ *     fp32, optional (written even when h0 is NULL)
+ *   Workspace: ssm_gated_scan_bwd_workspace_bytes, 256-byte aligned.  Sums
+ *   are added in a fixed order: results are deterministic.
+ *   seqlen == 0 gives dh0 = dlast (or 0) and a zero dgate_bias; batch == 0 a
+ *   zero dgate_bias.
+ */
+int ssm_gated_scan_bwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+                       const void *z, int64_t ldz, const float *h0, const void *dout,
+                       const float *dlast, const float *ckpt, void *dx, void *dg, void *dz,
+                       float *dgate_bias, float *dh0, int64_t batch, int64_t seqlen, int64_t d_inner,
+                       int io_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes ssm_gated_scan_bwd needs (with or without ckpt); (size_t)-1
+ * for invalid arguments. */
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype);
+
+/*
+ * ssm_gated_state_update -- one decode token of the same recurrence:
+ *   state (batch, d_inner) fp32 is read and overwritten in place; x, g, z, y
+ *   (batch, d_inner) io dtype, contiguous; gate_bias, z optional.
+ */
+int ssm_gated_state_update(float *state, const void *x, const void *g, const float *gate_bias,
+                           const void *z, void *y, int64_t batch, int64_t d_inner, int io_dtype,
+                           void *stream);
+
+/*
+ * ssm_add_rms_norm_fwd -- the entrance of a pre-norm residual block (the
+ * stacked model of the youngju.dev guide, section 5, normalises before each
+ * mixer and adds its output to the residual stream), with the root mean
+ * square as the norm.  For each row:
+ *     r = x + residual                                    (r = x without residual)
+ *     y = r / sqrt(mean(r^2) + eps) * weight
+ *   x            : (rows, dim) io dtype, rows ldx elements apart (ldx >= dim)
+ *   residual     : (rows, dim) residual dtype, contiguous, optional
+ *   weight       : (dim) fp32, required
+ *   y            : (rows, dim) io dtype, contiguous
+ *   residual_out : (rows, dim) residual dtype, optional: r rounded to it.  It
+ *                  may be residual itself (updated in place); no other overlap.
+ *   residual dtype: SSM_F32, or the io dtype.  r is normalised in fp32 before
+ *   it is rounded.  eps finite and >= 0 (SSM_ERR_VALUE).  dim in
+ *   [1, SSM_MAX_NORM_DIM].
+ */
+#define SSM_MAX_NORM_DIM 32768
+int ssm_add_rms_norm_fwd(const void *x, int64_t ldx, const void *residual, const float *weight, void *y,
+                         void *residual_out, int64_t rows, int64_t dim, float eps, int io_dtype,
+                         int residual_dtype, void *stream);
+
+/*
+ * ssm_add_rms_norm_quant -- the same with an 8-bit output for a projection
+ * that multiplies 8-bit rows: instead of y,
+ *     scale[row] = max(max_d |y| / 448, 2^-126)          fp32
+ *     q[row, d]  = e4m3(y / scale)                       (OCP e4m3, nearest even)
+ * so q * scale stands for y, the row's largest value at the format's largest.
+ * A row with a NaN has a NaN scale and NaN in q.
+ */
+int ssm_add_rms_norm_quant(const void *x, int64_t ldx, const void *residual, const float *weight, void *q,
+                           float *scale, void *residual_out, int64_t rows, int64_t dim, float eps,
+                           int io_dtype, int residual_dtype, void *stream);
+
+/*
+ * ssm_add_rms_norm_bwd -- the gradient of ssm_add_rms_norm_fwd at the stored
+ * r.  With n = r / sqrt(mean(r^2) + eps):
+ *     dr = (weight dy - n mean(n weight dy)) / sqrt(mean(r^2) + eps) + dresidual_out
+ *     dweight = sum over rows of dy n
+ *   dy            : (rows, dim) io dtype;  r : (rows, dim) residual dtype
+ *   dresidual_out : (rows, dim) residual dtype, optional -- dL/dresidual_out
+ *   dx            : (rows, dim) io dtype, required: dr, the gradient of x
+ *   dresidual     : (rows, dim) residual dtype, optional: dr, the gradient of
+ *                   residual; it may be dresidual_out itself (in place)
+ *   dweight       : (dim) fp32, required
+ *   All contiguous.  Workspace: ssm_add_rms_norm_bwd_workspace_bytes (partial
+ *   sums of dweight, added in a fixed order), 256-byte aligned.
+ *   rows == 0 gives a zero dweight.
+ */
+int ssm_add_rms_norm_bwd(const void *dy, const void *r, const float *weight, const void *dresidual_out,
+                         void *dx, void *dresidual, float *dweight, int64_t rows, int64_t dim, float eps,
+                         int io_dtype, int residual_dtype, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* Workspace bytes ssm_add_rms_norm_bwd needs; (size_t)-1 for invalid arguments. */
+size_t ssm_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
+/*
+ * ssm_grad_norm, ssm_grad_clip -- the clipping step of the training loop
+ * (youngju.dev guide, practical section: AdamW, warmup, clip) over a list of
+ * `count` gradient tensors:
+ *     norm = sqrt(sum over all tensors of g^2)            (64-bit sums)
+ *     coef = min(1, max_norm / (norm + eps))              (a NaN norm gives NaN)
+ *     out  = g * coef                                     (rounded to out's dtype)
+ *   grads, outs    : HOST arrays of device pointers (NULL entries only where
+ *                    numel is 0); numel, dtypes, out_dtypes: host arrays.  All
+ *                    are read before the call returns.  outs NULL: in place.
+ *   outs[i] may be grads[i] itself with the same dtype; outputs otherwise
+ *   overlap nothing (SSM_ERR_ALIAS), so in place no tensor may be listed twice.
+ *   norm           : one fp32 on the device, required, written
+ *   max_norm, eps  : >= 0, not NaN, eps finite (SSM_ERR_VALUE); max_norm may be
+ *                    infinite
+ *   In place with coef == 1 nothing is written.  count in [0, 2^20]; a tensor
+ *   holds fewer than 2^40 elements.  Workspace: ssm_grad_norm_workspace_bytes
+ *   (one partial sum per workgroup, added in a fixed order), 256-byte aligned.
+ */
+int ssm_grad_norm(const void *const *grads, const int64_t *numel, const int *dtypes, int64_t count,
+                  float *norm, void *workspace, size_t workspace_bytes, void *stream);
+int ssm_grad_clip(const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
+                  const int *out_dtypes, int64_t count, float max_norm, float eps, float *norm,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes both need for a list of `count` tensors; (size_t)-1 for an
+ * invalid count. */
+size_t ssm_grad_norm_workspace_bytes(int64_t count);
+
+/*
  * ssm_scan_status -- whether the last forward scan that used `workspace`
  * completed its segment hand-offs.  No page covers this; it is the error
  * path of this library's own time split.
@@ -441,8 +613,8 @@ size_t ssd_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, i
  *   SSM_ERR_HIP   the synchronisation or the copy failed (for example a
  *                 fault of an earlier kernel on the stream).
  * `workspace` is the workspace of the last ssm_scan_fwd, ssm_scan_fwd_ckpt,
- * ssm_conv_scan_fwd or ssm_scan_fwd_2d call on `stream` (or of an sm1_scan_fwd call whose
- * sm1_scan_workspace_bytes was nonzero), not yet reused.  The error word is
+ * ssm_conv_scan_fwd, ssm_scan_fwd_2d or ssm_gated_scan_fwd / _bwd call on `stream` (or of
+ * an sm1_scan_fwd call whose sm1_scan_workspace_bytes was nonzero), not yet reused.  The error word is
  * cleared at the start of every such call.  Not capturable in a HIP graph
  * (it synchronises); call it outside a capture.
  */

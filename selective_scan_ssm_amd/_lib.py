@@ -25,6 +25,10 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_workspace_bytes", "sm1_scan_fwd", "sm1_scan
            "ssm_dt_proj", "ssm_scan_status", "ssm_testing_scan_fwd_no_handoff", "ssm_scan_fwd_noalloc",
            "ssm_conv_scan_fwd", "ssm_conv_scan_workspace_bytes", "ssm_testing_bwd_segments",
            "ssd_scan_workspace_bytes", "ssm_testing_ssd_segments",
+           "ssm_gated_scan_fwd", "ssm_gated_scan_workspace_bytes", "ssm_gated_ckpt_bytes", "ssm_gated_scan_bwd",
+           "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_state_update", "ssm_add_rms_norm_fwd",
+           "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_add_rms_norm_bwd_workspace_bytes",
+           "ssm_grad_norm", "ssm_grad_clip", "ssm_grad_norm_workspace_bytes",
            "ssm_status_string", "ssm_abi_version")
 BENCH_LIB_PATH = os.path.join(PKG, "libssmbench.so")
 BENCH_EXPORTS = ("ssm_mb_copy", "ssm_mb_valu")
@@ -32,6 +36,7 @@ ABI_VERSION = 3
 SSM_ERR_WAIT = -8
 SSM_ERR_SCRATCH = -9
 SSM_SCRATCH_BYTES = 16 << 20
+GATED_BLOCK = 128            # steps between two checkpoints of the gated recurrence
 
 _lib = None
 _lock = threading.Lock()
@@ -40,6 +45,7 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 class LibraryMissing(RuntimeError):
@@ -112,6 +118,28 @@ def _bind(lib):
     lib.ssm_testing_bwd_segments.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.POINTER(_int),
                                              ctypes.POINTER(_int)]
     lib.ssm_testing_bwd_segments.restype = _int
+    lib.ssm_gated_scan_fwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                       _i64, _i64, _i64, _int, _vp, _sz, _vp]
+    lib.ssm_gated_scan_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
+    lib.ssm_gated_ckpt_bytes.argtypes = [_i64, _i64, _i64]
+    lib.ssm_gated_scan_bwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                       _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp]
+    lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
+    lib.ssm_gated_state_update.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp]
+    lib.ssm_add_rms_norm_fwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp]
+    lib.ssm_add_rms_norm_quant.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp]
+    lib.ssm_add_rms_norm_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp,
+                                         _sz, _vp]
+    lib.ssm_add_rms_norm_bwd_workspace_bytes.argtypes = [_i64, _i64]
+    lib.ssm_grad_norm.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
+    lib.ssm_grad_clip.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _sz, _vp]
+    lib.ssm_grad_norm_workspace_bytes.argtypes = [_i64]
+    for name in ("ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_state_update", "ssm_add_rms_norm_fwd",
+                 "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_grad_norm", "ssm_grad_clip"):
+        getattr(lib, name).restype = _int
+    for name in ("ssm_gated_scan_workspace_bytes", "ssm_gated_ckpt_bytes", "ssm_gated_scan_bwd_workspace_bytes",
+                 "ssm_add_rms_norm_bwd_workspace_bytes", "ssm_grad_norm_workspace_bytes"):
+        getattr(lib, name).restype = _sz
     lib.ssm_status_string.argtypes = [_int]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_abi_version.argtypes = []

@@ -27,7 +27,9 @@ ARCH = "gfx950"
 SOURCES = ["scan_fwd.hip", "scan_rows_bf16.hip", "scan_rows_f32.hip", "scan_rows_2d_bf16.hip",
            "scan_rows_2d_f32.hip", "scan_general_bf16.hip", "scan_general_bf16_xf32.hip", "scan_general_f32.hip",
            "sm1_scan.hip", "state_update.hip", "scan_bwd.hip", "conv1d.hip", "scan_2d.hip",
-           "ssd_scan.hip", "dt_proj.hip", "scan_noalloc.hip", "ssm_abi.cpp"]
+           "ssd_scan.hip", "dt_proj.hip", "scan_noalloc.hip", "gated_scan.hip", "add_rms_norm.hip", "grad_clip.hip",
+           "ssm_abi.cpp", "block_abi.cpp"]
+ABI_SOURCES = ["ssm_abi.cpp", "block_abi.cpp"]          # host code: argument checks, then launches
 BENCH_SOURCES = ["microbench.hip"]
 
 # Packed fp32 VALU forms are switched off (plain fp32 VALU only); code object
@@ -76,23 +78,26 @@ def build(verbose: bool = False) -> str:
 
 def build_host_sanitized(out: str) -> str:
     """libssmscan.so with its host-side C ABI (argument validation, aliasing
-    and size arithmetic, ssm_abi.cpp) compiled under AddressSanitizer and
+    and size arithmetic, ABI_SOURCES) compiled under AddressSanitizer and
     UndefinedBehaviorSanitizer; the kernels' objects are the regular ones
     (GPU code is not sanitized: -fsanitize goes to the host pass only)."""
     os.makedirs(BUILD, exist_ok=True)
-    objs = [os.path.join(BUILD, os.path.basename(src) + ".o") for src in SOURCES if src != "ssm_abi.cpp"]
+    objs = [os.path.join(BUILD, os.path.basename(src) + ".o") for src in SOURCES if src not in ABI_SOURCES]
     if not all(os.path.exists(o) for o in objs):
         build()
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
            "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer", "-g"]
-    abi_obj = os.path.join(BUILD, "ssm_abi.cpp.asan.o")
-    cmd = [hipcc(), "-x", "hip", *HIP_FLAGS, *san, "-c", os.path.join(CSRC, "ssm_abi.cpp"), "-o", abi_obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed for the sanitized ssm_abi.cpp:\n{r.stdout}\n{r.stderr}")
+    abi_objs = []
+    for src in ABI_SOURCES:
+        obj = os.path.join(BUILD, src + ".asan.o")
+        cmd = [hipcc(), "-x", "hip", *HIP_FLAGS, *san, "-c", os.path.join(CSRC, src), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed for the sanitized {src}:\n{r.stdout}\n{r.stderr}")
+        abi_objs.append(obj)
     os.makedirs(os.path.dirname(os.path.abspath(out)), exist_ok=True)
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-Xarch_host", "-shared-libasan",
-           "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined", *objs, abi_obj,
+           "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined", *objs, *abi_objs,
            "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -8,41 +8,13 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <limits>
 
+#include "ssm_abi_check.h"
 #include "ssm_kernels.h"
 
+using namespace ssm::abi;
+
 namespace {
-
-constexpr int64_t kMaxGridY = 65535;   // batch rides on gridDim.y in the scan kernels
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// byte range [p, p + bytes) of one tensor, for overlap checks
-struct Range {
-    uintptr_t lo, hi;
-};
-Range range(const void *p, int64_t elems, size_t esize) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + static_cast<uintptr_t>(elems) * esize};
-}
-bool overlap(Range a, Range b) {
-    if (a.lo == 0 || b.lo == 0 || a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-// a*b*c without int64 overflow; -1 on overflow
-int64_t mul3(int64_t a, int64_t b, int64_t c) {
-    const int64_t big = std::numeric_limits<int64_t>::max() / 16;
-    if (a < 0 || b < 0 || c < 0) return -1;
-    if (a && b > big / a) return -1;
-    const int64_t ab = a * b;
-    if (ab && c > big / ab) return -1;
-    return ab * c;
-}
-
-int check_dtype(int io) { return (io == SSM_F32 || io == SSM_BF16) ? SSM_OK : SSM_ERR_DTYPE; }
-size_t io_size(int io) { return io == SSM_BF16 ? 2 : 4; }
 
 // Validation shared by the two whole-sequence scans.
 int validate_scan(const void *x, const void *delta, const float *delta_bias, const float *A,
@@ -98,8 +70,6 @@ ssm::ScanArgs make_args(const void *x, const void *delta, const float *delta_bia
     return a;
 }
 
-int hip_status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
-
 }  // namespace
 
 extern "C" {
@@ -118,6 +88,8 @@ const char *ssm_status_string(int status) {
     case SSM_ERR_ALIAS: return "SSM_ERR_ALIAS: an output overlaps an input";
     case SSM_ERR_WAIT: return "SSM_ERR_WAIT: a segment's bounded wait gave up; that call's outputs are invalid";
     case SSM_ERR_SCRATCH: return "SSM_ERR_SCRATCH: the shape needs more scratch than SSM_SCRATCH_BYTES (ssm_scan_fwd_noalloc)";
+    case SSM_ERR_VALUE: return "SSM_ERR_VALUE: a scalar argument is negative or not finite";
+    case SSM_ERR_HOST: return "SSM_ERR_HOST: host memory for checking a list could not be had";
     default: return "unknown ssm status";
     }
 }

@@ -173,4 +173,81 @@ size_t conv_scan_workspace(const ScanArgs &a);
 hipError_t launch_conv_scan_fwd(const ScanArgs &a, void *conv_state_out, hipStream_t s);
 hipError_t launch_conv1d_update(const ConvUpdateArgs &a, hipStream_t s);
 
+// The gated linear recurrence.  Rows of x, g, z are ldx, ldg, ldz elements
+// apart; everything else is contiguous.
+constexpr int kGatedBlock = 128;          // steps between two checkpoints
+struct GatedArgs {
+    const void *x, *g, *z;                // io dtype
+    int64_t ldx, ldg, ldz;
+    const float *gate_bias, *h0;
+    void *y;                              // may be null when ckpt is given
+    float *last_state, *ckpt;
+    int64_t batch, seqlen, dim;
+    int bf16;
+    void *workspace;
+    size_t workspace_bytes;
+    // error-path tests only, as ScanArgs::test_spin_limit
+    uint32_t test_spin_limit = 0;
+};
+struct GatedBwdArgs {
+    GatedArgs fwd;                        // y, last_state, ckpt unused
+    const void *dout;
+    const float *dlast, *ckpt;            // ckpt null: computed into the workspace
+    void *dx, *dg, *dz;
+    float *dgate_bias, *dh0;
+};
+struct GatedStepArgs {
+    float *state;
+    const void *x, *g, *z;
+    const float *gate_bias;
+    void *y;
+    int64_t batch, dim;
+    int bf16;
+};
+size_t gated_scan_workspace(int64_t batch, int64_t seqlen, int64_t dim, int bf16);
+size_t gated_scan_bwd_workspace(int64_t batch, int64_t seqlen, int64_t dim, int bf16);
+hipError_t launch_gated_scan(const GatedArgs &a, hipStream_t s);
+hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s);
+hipError_t launch_gated_update(const GatedStepArgs &a, hipStream_t s);
+
+// RMS norm with the residual's addition.
+struct NormArgs {
+    const void *x, *residual;             // io dtype (rows ldx apart), residual dtype
+    const float *weight;
+    void *y;                              // io dtype, or e4m3 when scale is given
+    float *scale;                         // (rows): the 8-bit form
+    void *residual_out;                   // residual dtype, may be residual
+    int64_t rows, dim, ldx;
+    float eps;
+    int bf16, res_bf16;
+};
+struct NormBwdArgs {
+    const void *dy, *r, *dres_out;
+    const float *weight;
+    void *dx, *dres;
+    float *dweight;
+    int64_t rows, dim;
+    float eps;
+    int bf16, res_bf16;
+    void *workspace;
+};
+size_t norm_bwd_workspace(int64_t rows, int64_t dim);
+hipError_t launch_add_rms_norm(const NormArgs &a, hipStream_t s);
+hipError_t launch_add_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s);
+
+// Global gradient norm and clipping.
+struct ClipArgs {
+    const void *const *grads;
+    void *const *outs;                    // null: in place (or no scaling, see scale)
+    const int64_t *numel;
+    const int *dtypes, *out_dtypes;
+    int64_t count;
+    float max_norm, eps;
+    float *norm;
+    bool scale;                           // false: the norm alone
+    void *workspace;
+};
+size_t grad_norm_workspace(int64_t count);
+hipError_t launch_grad_clip(const ClipArgs &a, hipStream_t s);
+
 }  // namespace ssm

@@ -7,6 +7,7 @@ RuntimeError.  Every step of the computation runs in the library's kernels.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -446,3 +447,308 @@ def conv_scan_fwd(x, conv_weight, delta, A, B, C, conv_bias=None, conv_state=Non
     if return_conv_state:
         res += (win,)
     return res if len(res) > 1 else y
+
+
+# ------------------------------------------------- the gated recurrent block
+def _on(dev, **tensors):
+    """Every tensor given is on dev."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _run(dev, fn, *args):
+    """fn(*args, stream) with dev as the current device, on its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(dev))
+
+
+def _rows(t, name, dtype, shape):
+    """The stride between consecutive rows of t, whose last axis is contiguous
+    and whose other axes step evenly (a column range of a wider tensor)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    dim = shape[-1]
+    if t.is_contiguous():
+        return dim
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last axis")
+    lead = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    for (_, outer), (n, inner) in zip(lead, lead[1:]):
+        if outer != n * inner:
+            raise ValueError(f"the rows of {name} must be evenly strided")
+    ld = lead[-1][1] if lead else dim
+    if ld < dim:
+        raise ValueError(f"the rows of {name} overlap")
+    return ld
+
+
+def _workspace(need, what, workspace, dev):
+    if need == (1 << 64) - 1:
+        raise RuntimeError(f"{what}: invalid arguments")
+    if not need:
+        return None
+    if workspace is not None and workspace.numel() >= need:
+        _dev(workspace, "workspace", torch.uint8)
+        _on(dev, workspace=workspace)
+        return workspace
+    return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def gated_ckpt_shape(batch, seqlen, d_inner):
+    """Shape of gated_scan_fwd's checkpoints: (batch, ceil(seqlen / 128), d_inner)."""
+    return (batch, -(-seqlen // _lib.GATED_BLOCK), d_inner)
+
+
+def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=False, out=None, last_state_out=None,
+                   ckpt_out=None, workspace=None):
+    """Gated linear recurrence: a = sigmoid(g + gate_bias), h <- a h + (1 - a) x,
+    y = h SiLU(z) (y = h without z).  x, g, z: (batch, seqlen, d_inner) fp32 or
+    bf16 with a contiguous last axis and evenly strided rows (thirds of one
+    projection's output need no copy); gate_bias: (d_inner,) fp32; h0: (batch,
+    d_inner) fp32.  g = +inf keeps the state, g = -inf restarts it.  Returns y
+    (same dtype as x) or (y, last_state fp32).  ckpt_out: an fp32 tensor of
+    gated_ckpt_shape(...) that also receives the state entering every 128-step
+    block, for gated_scan_bwd(..., ckpt=ckpt_out)."""
+    lib = _lib.load()
+    if x.dtype not in _IO:
+        raise ValueError("x must be float32 or bfloat16")
+    io, dev = x.dtype, x.device
+    Bt, T, Dd = x.shape
+    ldx, ldg = _rows(x, "x", io, x.shape), _rows(g, "g", io, x.shape)
+    ldz = _rows(z, "z", io, x.shape) if z is not None else 0
+    _dev(gate_bias, "gate_bias", torch.float32, (Dd,))
+    _dev(h0, "h0", torch.float32, (Bt, Dd))
+    y = out if out is not None else torch.empty(x.shape, dtype=io, device=dev)
+    _dev(y, "out", io, x.shape)
+    last = None
+    if return_last_state:
+        last = last_state_out if last_state_out is not None else torch.empty((Bt, Dd), dtype=torch.float32, device=dev)
+        _dev(last, "last_state_out", torch.float32, (Bt, Dd))
+    _dev(ckpt_out, "ckpt_out", torch.float32, gated_ckpt_shape(Bt, T, Dd))
+    _on(dev, g=g, z=z, gate_bias=gate_bias, h0=h0, out=y, last_state_out=last, ckpt_out=ckpt_out)
+    need = lib.ssm_gated_scan_workspace_bytes(Bt, T, Dd, _IO[io])
+    ws = _workspace(need, "ssm_gated_scan_workspace_bytes", workspace, dev)
+    rc = _run(dev, lib.ssm_gated_scan_fwd, _ptr(x), ldx, _ptr(g), ldg, _ptr(gate_bias), _ptr(z), ldz, _ptr(h0), _ptr(y),
+              _ptr(last), _ptr(ckpt_out), Bt, T, Dd, _IO[io], _ptr(ws), need)
+    _check(rc, "ssm_gated_scan_fwd")
+    return (y, last) if return_last_state else y
+
+
+def gated_scan_bwd(x, g, dout, z=None, gate_bias=None, h0=None, dlast=None, ckpt=None, workspace=None):
+    """Gradient of gated_scan_fwd.  Same inputs, plus dout = dL/dy (contiguous,
+    like y) and dlast = dL/dlast_state ((batch, d_inner) fp32, optional).
+    Returns a dict: dx, dg (dtype of x), dh0 (fp32), and dz, dgate_bias (fp32)
+    when z, gate_bias are given (None otherwise).  ckpt: what
+    gated_scan_fwd(..., ckpt_out=) recorded on the same inputs; without it the
+    call reads x and g once more."""
+    lib = _lib.load()
+    if x.dtype not in _IO:
+        raise ValueError("x must be float32 or bfloat16")
+    io, dev = x.dtype, x.device
+    Bt, T, Dd = x.shape
+    ldx, ldg = _rows(x, "x", io, x.shape), _rows(g, "g", io, x.shape)
+    ldz = _rows(z, "z", io, x.shape) if z is not None else 0
+    _dev(dout, "dout", io, x.shape)
+    _dev(gate_bias, "gate_bias", torch.float32, (Dd,))
+    _dev(h0, "h0", torch.float32, (Bt, Dd))
+    _dev(dlast, "dlast", torch.float32, (Bt, Dd))
+    _dev(ckpt, "ckpt", torch.float32, gated_ckpt_shape(Bt, T, Dd))
+    _on(dev, g=g, z=z, dout=dout, gate_bias=gate_bias, h0=h0, dlast=dlast, ckpt=ckpt)
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+    grads = dict(dx=new(x.shape, io), dg=new(x.shape, io), dz=new(x.shape, io) if z is not None else None,
+                 dgate_bias=new((Dd,), torch.float32) if gate_bias is not None else None,
+                 dh0=new((Bt, Dd), torch.float32))
+    need = lib.ssm_gated_scan_bwd_workspace_bytes(Bt, T, Dd, _IO[io])
+    ws = _workspace(need, "ssm_gated_scan_bwd_workspace_bytes", workspace, dev)
+    rc = _run(dev, lib.ssm_gated_scan_bwd, _ptr(x), ldx, _ptr(g), ldg, _ptr(gate_bias), _ptr(z), ldz, _ptr(h0), _ptr(dout),
+              _ptr(dlast), _ptr(ckpt), _ptr(grads["dx"]), _ptr(grads["dg"]), _ptr(grads["dz"]),
+              _ptr(grads["dgate_bias"]), _ptr(grads["dh0"]), Bt, T, Dd, _IO[io], _ptr(ws), need)
+    _check(rc, "ssm_gated_scan_bwd")
+    return grads
+
+
+def gated_state_update(state, x, g, z=None, gate_bias=None, out=None):
+    """One decode token of gated_scan_fwd; `state` (batch, d_inner) fp32 is
+    updated in place.  x, g, z: (batch, d_inner).  Returns y."""
+    lib = _lib.load()
+    if x.dtype not in _IO:
+        raise ValueError("x must be float32 or bfloat16")
+    io, dev = x.dtype, x.device
+    Bt, Dd = x.shape
+    _dev(x, "x", io)
+    _dev(g, "g", io, x.shape)
+    _dev(z, "z", io, x.shape)
+    _dev(state, "state", torch.float32, (Bt, Dd))
+    _dev(gate_bias, "gate_bias", torch.float32, (Dd,))
+    y = out if out is not None else torch.empty_like(x)
+    _dev(y, "out", io, x.shape)
+    _on(dev, state=state, g=g, z=z, gate_bias=gate_bias, out=y)
+    rc = _run(dev, lib.ssm_gated_state_update, _ptr(state), _ptr(x), _ptr(g), _ptr(gate_bias), _ptr(z), _ptr(y), Bt, Dd,
+              _IO[io])
+    _check(rc, "ssm_gated_state_update")
+    return y
+
+
+def _norm_args(x, weight, residual, residual_dtype, residual_out):
+    """(io, rows, dim, ldx, residual dtype, residual_out) of the two forwards."""
+    if x.dtype not in _IO:
+        raise ValueError("x must be float32 or bfloat16")
+    io, dev = x.dtype, x.device
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    ldx = _rows(x, "x", io, x.shape)
+    _dev(weight, "weight", torch.float32, (dim,))
+    if residual is not None:
+        if residual_dtype is not None and residual_dtype != residual.dtype:
+            raise ValueError("residual_dtype differs from residual's dtype")
+        residual_dtype = residual.dtype
+    res = residual_dtype if residual_dtype is not None else residual_out.dtype if residual_out is not None else io
+    if res not in (torch.float32, io):
+        raise ValueError(f"the residual must be float32 or {io}, got {res}")
+    _dev(residual, "residual", res, x.shape)
+    if residual_out is None and (residual is not None or residual_dtype is not None):
+        residual_out = torch.empty(x.shape, dtype=res, device=dev)
+    _dev(residual_out, "residual_out", res, x.shape)
+    _on(dev, weight=weight, residual=residual, residual_out=residual_out)
+    return io, rows, dim, ldx, res, residual_out
+
+
+def add_rms_norm(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=None, residual_out=None):
+    """r = x + residual, y = r / sqrt(mean(r^2) + eps) * weight over the last
+    axis.  x: (..., dim) fp32 or bf16, rows evenly strided; weight: (dim,) fp32;
+    residual: like x, in x's dtype or fp32.  Returns (y, r): y in x's dtype, r
+    in the residual's (residual_dtype when there is no residual; without either
+    r is None, as it would be x itself).  residual_out may be residual, which is
+    then updated in place."""
+    lib = _lib.load()
+    io, rows, dim, ldx, res, r = _norm_args(x, weight, residual, residual_dtype, residual_out)
+    y = out if out is not None else torch.empty(x.shape, dtype=io, device=x.device)
+    _dev(y, "out", io, x.shape)
+    _on(x.device, out=y)
+    rc = _run(x.device, lib.ssm_add_rms_norm_fwd, _ptr(x), ldx, _ptr(residual), _ptr(weight), _ptr(y), _ptr(r), rows, dim,
+              eps, _IO[io], _IO[res])
+    _check(rc, "ssm_add_rms_norm_fwd")
+    return y, r
+
+
+def add_rms_norm_quant(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=None, scale_out=None,
+                       residual_out=None):
+    """add_rms_norm with an 8-bit output: returns (q, scale, r), q in
+    float8_e4m3fn and scale (x.shape[:-1]) fp32 with q * scale standing for y,
+    scale = max(max |y| / 448, 2^-126) per row."""
+    lib = _lib.load()
+    io, rows, dim, ldx, res, r = _norm_args(x, weight, residual, residual_dtype, residual_out)
+    q = out if out is not None else torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    _dev(q, "out", torch.float8_e4m3fn, x.shape)
+    scale = scale_out if scale_out is not None else torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _dev(scale, "scale_out", torch.float32, x.shape[:-1])
+    _on(x.device, out=q, scale_out=scale)
+    rc = _run(x.device, lib.ssm_add_rms_norm_quant, _ptr(x), ldx, _ptr(residual), _ptr(weight), _ptr(q), _ptr(scale),
+              _ptr(r), rows, dim, eps, _IO[io], _IO[res])
+    _check(rc, "ssm_add_rms_norm_quant")
+    return q, scale, r
+
+
+def add_rms_norm_bwd(dy, r, weight, dresidual=None, eps=1e-5, dresidual_out=None, workspace=None):
+    """Gradient of add_rms_norm at the r it returned (x itself when it returned
+    None).  dy: dL/dy (..., dim) fp32 or bf16; r: like dy, in its dtype or fp32;
+    dresidual: dL/dr from the residual stream, r's dtype, optional.  Returns a
+    dict: dx (dy's dtype), dresidual (the gradient of residual: dx itself when
+    the dtypes are the same, else in r's dtype) and dweight (dim,) fp32.
+    dresidual_out: where dresidual goes, may be dresidual itself."""
+    lib = _lib.load()
+    if dy.dtype not in _IO:
+        raise ValueError("dy must be float32 or bfloat16")
+    io, dev = dy.dtype, dy.device
+    res = r.dtype
+    if res not in (torch.float32, io):
+        raise ValueError(f"r must be float32 or {io}, got {res}")
+    if dy.dim() < 1:
+        raise ValueError("dy must have at least one axis")
+    dim = dy.shape[-1]
+    rows = dy.numel() // dim if dim else 0
+    _dev(dy, "dy", io)
+    _dev(r, "r", res, dy.shape)
+    _dev(weight, "weight", torch.float32, (dim,))
+    _dev(dresidual, "dresidual", res, dy.shape)
+    dx = torch.empty_like(dy)
+    own = dresidual_out if dresidual_out is not None else (torch.empty_like(r) if res != io else None)
+    _dev(own, "dresidual_out", res, dy.shape)
+    dw = torch.empty((dim,), dtype=torch.float32, device=dev)
+    _on(dev, r=r, weight=weight, dresidual=dresidual, dresidual_out=own)
+    need = lib.ssm_add_rms_norm_bwd_workspace_bytes(rows, dim)
+    ws = _workspace(need, "ssm_add_rms_norm_bwd_workspace_bytes", workspace, dev)
+    rc = _run(dev, lib.ssm_add_rms_norm_bwd, _ptr(dy), _ptr(r), _ptr(weight), _ptr(dresidual), _ptr(dx), _ptr(own),
+              _ptr(dw), rows, dim, eps, _IO[io], _IO[res], _ptr(ws), need)
+    _check(rc, "ssm_add_rms_norm_bwd")
+    return dict(dx=dx, dresidual=dx if own is None else own, dweight=dw)
+
+
+def _grad_list(tensors, name, dev):
+    """Host arrays (pointers, dtypes) of a list of tensors on dev."""
+    for t in tensors:
+        if t.dtype not in _IO:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} are on {t.device} and {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    n = len(tensors)
+    return (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int * n)(*[_IO[t.dtype] for t in tensors])
+
+
+def _clip(grads, max_norm, out, eps, norm_out, workspace):
+    lib = _lib.load()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("the list of gradients is empty")
+    dev = grads[0].device
+    if dev.type != "cuda":
+        raise ValueError("gradients must be GPU tensors")
+    ptrs, dtypes = _grad_list(grads, "gradients", dev)
+    n = len(grads)
+    numel = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    norm = norm_out if norm_out is not None else torch.empty((), dtype=torch.float32, device=dev)
+    if norm.numel() != 1:
+        raise ValueError("norm_out must hold one value")
+    _dev(norm, "norm_out", torch.float32)
+    _on(dev, norm_out=norm)
+    need = lib.ssm_grad_norm_workspace_bytes(n)
+    ws = _workspace(need, "ssm_grad_norm_workspace_bytes", workspace, dev)
+    if max_norm is None:
+        _check(_run(dev, lib.ssm_grad_norm, ptrs, numel, dtypes, n, _ptr(norm), _ptr(ws), need), "ssm_grad_norm")
+        return norm
+    outs, out_dtypes = None, None
+    if out is not None:
+        out = list(out)
+        if [t.shape for t in out] != [t.shape for t in grads]:
+            raise ValueError("out must have the gradients' shapes")
+        outs, out_dtypes = _grad_list(out, "out", dev)
+    rc = _run(dev, lib.ssm_grad_clip, ptrs, outs, numel, dtypes, out_dtypes, n, max_norm, eps, _ptr(norm), _ptr(ws), need)
+    _check(rc, "ssm_grad_clip")
+    return norm
+
+
+def grad_norm(grads, norm_out=None, workspace=None):
+    """sqrt(sum of squares) over a list of contiguous fp32 / bf16 tensors, as
+    an fp32 scalar on their device."""
+    return _clip(grads, None, None, 0.0, norm_out, workspace)
+
+
+def clip_grads(grads, max_norm, out=None, eps=1e-6, norm_out=None, workspace=None):
+    """Scales a list of contiguous fp32 / bf16 tensors by min(1, max_norm /
+    (norm + eps)), norm being grad_norm(grads): in place, or into the tensors
+    of `out` (same shapes, fp32 or bf16 each: an optimizer's fp32 gradients
+    from bf16 ones).  Returns the norm before clipping.  The host never waits."""
+    if max_norm is None:
+        raise ValueError("max_norm must be a number")
+    return _clip(grads, float(max_norm), out, float(eps), norm_out, workspace)

@@ -1,0 +1,212 @@
+"""The RMS norm with the residual's addition on the GPU against its fp64
+definition, within the rounding bounds derived beside it."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_util as U
+from oracle import recurrent_block as R
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+TYPES = [(F32, F32), (BF16, BF16), (BF16, F32)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_scan_ssm_amd import _lib, ops
+    _lib.load()
+    return ops
+
+
+def e4m3_half_step(v):
+    """Half the distance between neighbours of e4m3 around |v| <= 448."""
+    e = np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6)))
+    return 2.0 ** (e - 4)
+
+
+def check_quant(q, scale, y, by):
+    want = R.add_rms_norm_scale(y)
+    rel = by.max(-1) / np.maximum(np.abs(y).max(-1), 1e-300) + 4 * R.U
+    s = U.f64(scale)
+    assert np.all(np.abs(s - want) <= want * rel), "scale"
+    v = y / want[..., None]
+    off = np.abs(U.f64(q) - v)
+    # half a step of the format, plus the fp32 error of y / scale before it is rounded
+    tol = e4m3_half_step(v) * (1 + 1e-6) + by / want[..., None] + np.abs(v) * (rel[..., None] + 4 * R.U)
+    assert np.all(off <= tol), f"q: {np.max(off - tol)}"
+
+
+SIZES = [(1, 1), (3, 2), (5, 63), (2, 64), (7, 65), (4, 130), (9, 256), (3, 257), (130, 768), (5, 1000), (17, 1536), (3, 2049),
+         (33, 2560), (2, 4097), (6, 5120), (2, 8192), (1, 10001), (2, 16384), (1, 32768), (1, 32767)]
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16", "bf16-f32"])
+@pytest.mark.parametrize("rows,dim", SIZES)
+def test_forward_and_quant(ops, rows, dim, types):
+    io, rt = types
+    x, res = U.rand(1, rows, dim, dtype=io), U.rand(2, rows, dim, dtype=rt, scale=3.0)
+    w = 1.0 + 0.2 * U.rand(3, dim)
+    y, gy = U.guarded((rows, dim), io)
+    r, gr = U.guarded((rows, dim), rt)
+    ops.add_rms_norm(x, w, res, out=y, residual_out=r)
+    q, gq = U.guarded((rows, dim), torch.float8_e4m3fn)
+    sc, gs = U.guarded((rows,), F32)
+    _, _, r2 = ops.add_rms_norm_quant(x, w, res, out=q, scale_out=sc)
+    torch.cuda.synchronize()
+    for g in (gy, gr, gq, gs):
+        g()
+    ro, yo, by = R.add_rms_norm(U.f64(x), U.f64(w), U.f64(res), bounds=True)
+    U.close(r, ro, R.U * np.abs(ro), "r")
+    assert torch.equal(r, r2)
+    U.close(y, yo, by, "y")
+    check_quant(q, sc, yo, by)
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16", "bf16-f32"])
+@pytest.mark.parametrize("rows,dim", SIZES + [(1000, 96), (700, 40), (4100, 768)])
+def test_backward(ops, rows, dim, types):
+    io, rt = types
+    dy, r, dr = U.rand(4, rows, dim, dtype=io), U.rand(5, rows, dim, dtype=rt, scale=2.0), U.rand(6, rows, dim, dtype=rt)
+    w = 1.0 + 0.2 * U.rand(7, dim)
+    for add in (dr, None):
+        got = ops.add_rms_norm_bwd(dy, r, w, dresidual=add)
+        dro, dwo, bdr, bdw = R.add_rms_norm_bwd(U.f64(dy), U.f64(r), U.f64(w), U.f64(add), bounds=True)
+        U.close(got["dx"], dro, bdr, "dx")
+        U.close(got["dresidual"], dro, bdr, "dresidual")
+        U.close(got["dweight"], dwo, bdw, "dweight")
+        assert (got["dresidual"] is got["dx"]) == (io == rt)
+
+
+def test_without_a_residual(ops):
+    x, w = U.rand(1, 6, 200, dtype=BF16), 1.0 + 0.1 * U.rand(2, 200)
+    y, r = ops.add_rms_norm(x, w)
+    assert r is None
+    _, yo, by = R.add_rms_norm(U.f64(x), U.f64(w), bounds=True)
+    U.close(y, yo, by)
+    y2, r2 = ops.add_rms_norm(x, w, residual_dtype=F32)           # the residual stream starts here, in fp32
+    assert torch.equal(y2, y) and torch.equal(r2, x.float())
+    q, s, r3 = ops.add_rms_norm_quant(x, w)
+    assert r3 is None
+    check_quant(q, s, yo, by)
+
+
+def test_the_residual_in_place(ops):
+    for io, rt in TYPES:
+        for dim in (768, 77):
+            x, res, w = U.rand(1, 40, dim, dtype=io), U.rand(2, 40, dim, dtype=rt), 1.0 + 0.1 * U.rand(3, dim)
+            y, r = ops.add_rms_norm(x, w, res)
+            own = res.clone()
+            y2, r2 = ops.add_rms_norm(x, w, own, residual_out=own)
+            assert r2 is own and torch.equal(own, r) and torch.equal(y, y2)
+            dy, dr = U.rand(4, 40, dim, dtype=io), U.rand(5, 40, dim, dtype=rt)
+            want = ops.add_rms_norm_bwd(dy, r, w, dresidual=dr)
+            got = ops.add_rms_norm_bwd(dy, r, w, dresidual=dr, dresidual_out=dr)
+            assert got["dresidual"] is dr and torch.equal(dr, want["dresidual"]) and torch.equal(got["dx"], want["dx"])
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_strided_and_unaligned_rows(ops, io):
+    for dim, off, width in ((256, 256, 768), (256, 1, 300), (65, 3, 140)):
+        wide = U.rand(1, 2, 9, width, dtype=io)
+        x = wide[..., off:off + dim]
+        res, w = U.rand(2, 2, 9, dim, dtype=io), 1.0 + 0.1 * U.rand(3, dim)
+        y, r = ops.add_rms_norm(x, w, res)
+        y2, r2 = ops.add_rms_norm(x.contiguous(), w, res)
+        _, yo, by = R.add_rms_norm(U.f64(x), U.f64(w), U.f64(res), bounds=True)
+        U.close(y, yo, by)
+        U.close(y2, yo, by)
+        assert torch.equal(r, r2)
+        # the other tensors off their alignment as well
+        buf = U.rand(4, 18 * dim + 1, dtype=io)[1:].view(2, 9, dim)
+        U.close(ops.add_rms_norm(buf, w, res)[0], *R.add_rms_norm(U.f64(buf), U.f64(w), U.f64(res), bounds=True)[1:])
+        got = ops.add_rms_norm_bwd(buf, res, w)
+        dro, dwo, bdr, bdw = R.add_rms_norm_bwd(U.f64(buf).reshape(18, dim), U.f64(res).reshape(18, dim), U.f64(w), bounds=True)
+        U.close(got["dx"].view(18, dim), dro, bdr)
+        U.close(got["dweight"], dwo, bdw)
+
+
+def test_zero_tiny_huge_and_nan_rows(ops):
+    x = U.rand(1, 8, 96)
+    x[0] = 0.0
+    x[1] *= 1e-30
+    x[2] *= 1e15
+    x[3, 5] = float("nan")
+    x[4, 5] = float("inf")
+    w = 1.0 + 0.1 * U.rand(2, 96)
+    w1 = w.clone()
+    w1[7] = 1e-42
+    y, _ = ops.add_rms_norm(x, w)
+    q, s, _ = ops.add_rms_norm_quant(x, w)
+    assert not bool(y[0].any()) and not bool(q[0].float().any()) and float(s[0]) == 2.0 ** -126
+    for i in (1, 2, 5, 6, 7):
+        _, yo, by = R.add_rms_norm(U.f64(x[i:i + 1]), U.f64(w), bounds=True)
+        U.close(y[i:i + 1], yo, by)
+        check_quant(q[i:i + 1], s[i:i + 1], yo, by)
+    assert bool(torch.isnan(y[3]).all()) and bool(torch.isnan(q[3].float()).all()) and bool(torch.isnan(s[3]))
+    # an infinity: its square makes the row's rms infinite, every other value 0
+    assert bool(torch.isnan(y[4, 5])) and not bool(y[4, :5].any()) and bool(torch.isnan(s[4]))
+    tiny = ops.add_rms_norm_quant(x[5:6], torch.full_like(w, 1e-40))
+    assert float(tiny[1]) == 2.0 ** -126 and bool(torch.isfinite(tiny[0].float()).all())
+
+
+def test_weight_gradient_over_many_rows_repeats_to_the_bit(ops):
+    dy, r, w = U.rand(1, 20000, 130, dtype=BF16), U.rand(2, 20000, 130, dtype=BF16), 1.0 + 0.1 * U.rand(3, 130)
+    a, b = ops.add_rms_norm_bwd(dy, r, w), ops.add_rms_norm_bwd(dy, r, w)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    _, dwo, _, bdw = R.add_rms_norm_bwd(U.f64(dy), U.f64(r), U.f64(w), bounds=True)
+    U.close(a["dweight"], dwo, bdw)
+
+
+def test_no_rows(ops):
+    x, w = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda")
+    assert ops.add_rms_norm(x, w)[0].shape == (0, 64)
+    assert not bool(ops.add_rms_norm_bwd(x, x, w)["dweight"].any())
+
+
+def test_graph_replays(ops):
+    from test_gpu_graph import replay_matches_eager
+    t = dict(x=U.rand(1, 300, 768, dtype=BF16), res=U.rand(2, 300, 768), w=1.0 + 0.1 * U.rand(3, 768),
+             dy=U.rand(4, 300, 768, dtype=BF16))
+
+    def fn(t):
+        y, r = ops.add_rms_norm(t["x"], t["w"], t["res"])
+        q, s, _ = ops.add_rms_norm_quant(t["x"], t["w"], t["res"])
+        g = ops.add_rms_norm_bwd(t["dy"], r, t["w"], dresidual=t["res"])
+        return [y, r, q.view(torch.uint8), s] + list(g.values())
+
+    def refill(t, r):
+        for k in ("x", "res", "dy"):
+            t[k].copy_(torch.randn(t[k].shape, device="cuda"))
+    replay_matches_eager(t, fn, refill)
+
+
+def test_offsets_past_32_bits(ops):
+    rows, dim = 300000, 8192                                       # 4.9 GB of bf16
+    x = torch.empty(rows, dim, dtype=BF16, device="cuda").normal_()
+    w = 1.0 + 0.1 * U.rand(3, dim)
+    y, _ = ops.add_rms_norm(x, w)
+    assert torch.equal(y[-7:], ops.add_rms_norm(x[-7:], w)[0])
+    q, s, _ = ops.add_rms_norm_quant(x, w)
+    q7, s7, _ = ops.add_rms_norm_quant(x[-7:], w)
+    assert torch.equal(q[-7:].view(torch.uint8), q7.view(torch.uint8)) and torch.equal(s[-7:], s7)
+    got = ops.add_rms_norm_bwd(y, x, w)
+    assert torch.equal(got["dx"][-7:], ops.add_rms_norm_bwd(y[-7:], x[-7:], w)["dx"])
+
+
+def test_refusals(ops):
+    x, w = U.rand(1, 4, 64, dtype=BF16), torch.ones(64, device="cuda")
+    for bad in (lambda: ops.add_rms_norm(x.half(), w), lambda: ops.add_rms_norm(x, w.bfloat16()),
+                lambda: ops.add_rms_norm(x, w[:32]), lambda: ops.add_rms_norm(x, w, x[:2]),
+                lambda: ops.add_rms_norm(x.float(), w, x), lambda: ops.add_rms_norm(x, w, x.half()),
+                lambda: ops.add_rms_norm(x, w, x, residual_dtype=F32), lambda: ops.add_rms_norm(x, w, eps=-1.0),
+                lambda: ops.add_rms_norm(x.cpu(), w), lambda: ops.add_rms_norm(x.t(), w[:4]),
+                lambda: ops.add_rms_norm_bwd(x, x[:2], w), lambda: ops.add_rms_norm_bwd(x.float(), x, w),
+                lambda: ops.add_rms_norm(torch.empty(2, 32769, device="cuda"), torch.empty(32769, device="cuda"))):
+        with pytest.raises((ValueError, RuntimeError)):
+            bad()
+    with pytest.raises(RuntimeError, match="ALIAS"):
+        ops.add_rms_norm(x, w, out=x)
