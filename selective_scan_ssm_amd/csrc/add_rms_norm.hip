@@ -1,151 +1,400 @@
 // RMS norm with the residual's addition, with an output in the io dtype or in
-// 8 bits with a scale per row, and its gradient.
-// First form: one workgroup per row, the row kept in LDS between the sum of
-// squares and the output.
+// 8 bits with a scale per row, and its gradient:
+//     r = x + residual,  y = r / sqrt(mean(r^2) + eps) w
+//     dr = rstd (w dy - n mean(n w dy)) + dresidual,  dw = sum over rows of dy n,  n = r rstd
+//
+// HBM-bound: a row is read once, kept in registers across the reduction(s), and
+// written once.  R waves share a row (1 where a row fits one wave's registers)
+// and each lane holds P chunks of V consecutive elements (V = 8: 16-byte
+// accesses; V = 1 where the width or an address does not allow them), so
+// nothing but the reduction crosses lanes.  Waves walk the rows with a grid
+// stride and keep the weight in registers; the gradient also keeps its lane's
+// share of dw there, and one partial sum per workgroup goes through the
+// workspace.
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.1754943508222875e-38f;   // 2^-126: scales stay normal numbers
-constexpr int kPartRows = 64;                          // rows per workgroup of the gradient
 
-template <typename F> __device__ __forceinline__ float block_reduce(float v, float *tmp, F f) {
-    for (int o = 32; o > 0; o /= 2) v = f(v, __shfl_xor(v, o));
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) tmp[threadIdx.x / 64] = v;
-    __syncthreads();
-    v = tmp[0];
-    for (int w = 1; w < kThreads / 64; ++w) v = f(v, tmp[w]);
-    return v;
-}
-struct Add {
-    __device__ float operator()(float a, float b) const { return a + b; }
-};
 // the larger of two magnitudes, a NaN above everything (its bits are)
 struct MaxAbs {
-    __device__ float operator()(float a, float b) const {
+    __device__ __forceinline__ float operator()(float a, float b) const {
         const uint32_t i = __float_as_uint(a) & 0x7fffffffu, j = __float_as_uint(b) & 0x7fffffffu;
         return __uint_as_float(i > j ? i : j);
     }
 };
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-    return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+// f over the row's R waves; one barrier, tmp of the calls alternating
+template <int R, typename F> __device__ __forceinline__ float row_fold(float v, float *tmp, F f) {
+    v = wave_fold(v, f);
+    if constexpr (R > 1) {
+        if (threadIdx.x % 64 == 0) tmp[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = tmp[0];
+#pragma unroll
+        for (int w = 1; w < R; ++w) v = f(v, tmp[w]);
+    }
+    return v;
 }
 
-template <typename T, typename R> __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs p) {
-    extern __shared__ float row[];
-    __shared__ float tmp[kThreads / 64];
-    const int64_t r = blockIdx.x;
-    const int dim = static_cast<int>(p.dim);
-    const T *x = static_cast<const T *>(p.x) + r * p.ldx;
-    const R *res = p.residual ? static_cast<const R *>(p.residual) + r * p.dim : nullptr;
-    R *res_out = p.residual_out ? static_cast<R *>(p.residual_out) + r * p.dim : nullptr;
-    float ss = 0.0f;
-    for (int i = threadIdx.x; i < dim; i += kThreads) {
-        float v = to_f32(x[i]);
-        if (res) v += to_f32(res[i]);
-        if (res_out) res_out[i] = from_f32<R>(v);
-        row[i] = v;
-        ss = fmaf(v, v, ss);
+// -------------------------------------------- V consecutive elements of a row
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+template <typename T, int V> struct Chunk;
+template <> struct Chunk<bf16_t, 8> {
+    u4 q;
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) { q = __builtin_amdgcn_raw_buffer_load_b128(r, e * 2, 0, kStream); }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i % 2 ? (q[i / 2] & 0xffff0000u) : (q[i / 2] << 16));
     }
-    ss = block_reduce(ss, tmp, Add());
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(dim) + p.eps);
-    if (!p.scale) {
-        for (int i = threadIdx.x; i < dim; i += kThreads)
-            (static_cast<T *>(p.y) + r * p.dim)[i] = from_f32<T>(row[i] * rstd * p.weight[i]);
-        return;
+    static __device__ __forceinline__ void store(const float *v, rsrc_t r, uint32_t e) {
+        u4 q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i]).bits) |
+                   (static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i + 1]).bits) << 16);
+        __builtin_amdgcn_raw_buffer_store_b128(q, r, e * 2, 0, kStream);
     }
-    float m = 0.0f;
-    for (int i = threadIdx.x; i < dim; i += kThreads) {
-        row[i] = row[i] * rstd * p.weight[i];
-        m = MaxAbs()(m, row[i]);
+};
+template <> struct Chunk<float, 8> {
+    u4 q[2];
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) {
+        q[0] = __builtin_amdgcn_raw_buffer_load_b128(r, e * 4, 0, kStream);
+        q[1] = __builtin_amdgcn_raw_buffer_load_b128(r, e * 4 + 16, 0, kStream);
     }
-    m = block_reduce(m, tmp, MaxAbs());
-    float scale = m / kE4m3Max;
-    scale = scale < kMinScale ? kMinScale : scale;     // false for NaN, which stays
-    if (threadIdx.x == 0) p.scale[r] = scale;
-    for (int i = threadIdx.x; i < dim; i += kThreads)
-        (static_cast<uint8_t *>(p.y) + r * p.dim)[i] = to_e4m3(row[i] / scale);
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(q[i / 4][i % 4]); }
+    static __device__ __forceinline__ void store(const float *v, rsrc_t r, uint32_t e) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u4 q = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                          __float_as_uint(v[4 * h + 3])};
+            __builtin_amdgcn_raw_buffer_store_b128(q, r, e * 4 + 16 * h, 0, kStream);
+        }
+    }
+};
+template <typename T> struct Chunk<T, 1> {
+    typename Io<T>::raw q;
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) { q = Io<T>::template load<kStream>(r, e * sizeof(T), 0); }
+    __device__ __forceinline__ float get(int) const { return Io<T>::f32(q); }
+    static __device__ __forceinline__ void store(const float *v, rsrc_t r, uint32_t e) {
+        Io<T>::template store<kStream>(v[0], r, e * sizeof(T), 0);
+    }
+};
+
+template <int V> __device__ __forceinline__ void store_e4m3(const float *v, rsrc_t r, uint32_t e) {
+    if constexpr (V == 8) {
+        u2 q;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+            q[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], p, true));
+        }
+        __builtin_amdgcn_raw_buffer_store_b64(q, r, e, 0, kStream);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b8(
+            static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false) & 0xff), r, e, 0, kStream);
+    }
 }
 
-template <typename T, typename R> __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs p) {
-    __shared__ float tmp[kThreads / 64];
+// row `row` of a (rows, dim) tensor with rows ld apart: accesses past dim read 0 and store nothing
+template <typename T> __device__ __forceinline__ rsrc_t row_rsrc(const void *p, int64_t row, int64_t ld, int dim) {
+    return make_rsrc(static_cast<const char *>(p) + row * ld * static_cast<int64_t>(sizeof(T)),
+                     static_cast<uint32_t>(dim * sizeof(T)));
+}
+
+// ----------------------------------------------------------------- forward
+// T: io dtype; S: the residual's; Q: 8-bit output.  A workgroup is R waves on
+// one row, or (R = 1) up to four waves on a row each.
+template <typename T, typename S, bool Q, int V, int P, int R>
+__global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_kernel(NormArgs p) {
+    __shared__ float tmp[2][2][R];
+    const int lane = threadIdx.x % 64;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int dim = static_cast<int>(p.dim);
-    float *part = static_cast<float *>(p.workspace) + static_cast<int64_t>(blockIdx.x) * p.dim;
-    for (int i = threadIdx.x; i < dim; i += kThreads) part[i] = 0.0f;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPartRows;
-    for (int64_t r = r0; r < r0 + kPartRows && r < p.rows; ++r) {
-        const T *dy = static_cast<const T *>(p.dy) + r * p.dim;
-        const R *rr = static_cast<const R *>(p.r) + r * p.dim;
-        const R *add = p.dres_out ? static_cast<const R *>(p.dres_out) + r * p.dim : nullptr;
+    const int per_wg = R == 1 ? blockDim.x / 64 : 1;
+    const uint32_t e0 = static_cast<uint32_t>(((R == 1 ? 0 : w) * 64 + lane) * V);   // the lane's first element
+    constexpr uint32_t step = R * 64 * V;
+    float wt[P][V];
+    const rsrc_t rw = make_rsrc(p.weight, static_cast<uint32_t>(dim * 4));
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+        Chunk<float, V> q;
+        q.load(rw, e0 + c * step);
+#pragma unroll
+        for (int i = 0; i < V; ++i) wt[c][i] = q.get(i);
+    }
+    const float inv_dim = 1.0f / static_cast<float>(dim);
+    int par = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_wg + (R == 1 ? w : 0); row < p.rows;
+         row += static_cast<int64_t>(gridDim.x) * per_wg, par ^= 1) {
+        Chunk<T, V> x[P];
+        Chunk<S, V> res[P];
+        const rsrc_t rx = row_rsrc<T>(p.x, row, p.ldx, dim);
+#pragma unroll
+        for (int c = 0; c < P; ++c) x[c].load(rx, e0 + c * step);
+        if (p.residual) {
+            const rsrc_t rr = row_rsrc<S>(p.residual, row, p.dim, dim);
+#pragma unroll
+            for (int c = 0; c < P; ++c) res[c].load(rr, e0 + c * step);
+        }
+        float v[P][V], ss = 0.0f;
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[c][i] = x[c].get(i);
+                if (p.residual) v[c][i] += res[c].get(i);
+                ss = fmaf(v[c][i], v[c][i], ss);
+            }
+        if (p.residual_out) {
+            const rsrc_t ro = row_rsrc<S>(p.residual_out, row, p.dim, dim);
+#pragma unroll
+            for (int c = 0; c < P; ++c) Chunk<S, V>::store(v[c], ro, e0 + c * step);
+        }
+        ss = row_fold<R>(ss, tmp[0][par], AddOp());
+        const float rstd = 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps));
+        float m = 0.0f;
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[c][i] *= rstd * wt[c][i];
+                if constexpr (Q) m = MaxAbs()(m, v[c][i]);
+            }
+        if constexpr (Q) {
+            m = row_fold<R>(m, tmp[1][par], MaxAbs());
+            float scale = m / kE4m3Max;
+            scale = scale < kMinScale ? kMinScale : scale;     // false for NaN, which stays
+            const float inv = 1.0f / scale;
+            if (lane == 0 && (R == 1 || w == 0)) p.scale[row] = scale;
+            const rsrc_t ry = make_rsrc(static_cast<char *>(p.y) + row * p.dim, static_cast<uint32_t>(dim));
+#pragma unroll
+            for (int c = 0; c < P; ++c) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[c][i] *= inv;
+                store_e4m3<V>(v[c], ry, e0 + c * step);
+            }
+        } else {
+            const rsrc_t ry = row_rsrc<T>(p.y, row, p.dim, dim);
+#pragma unroll
+            for (int c = 0; c < P; ++c) Chunk<T, V>::store(v[c], ry, e0 + c * step);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// A workgroup is four rows' waves (R = 1) or R waves on one row; its sum of
+// dy n over its rows is one row of `part`.
+constexpr int kBwdRows1 = 4;            // waves, and rows at a time, of a workgroup with R = 1
+
+template <typename T, typename S, int V, int P, int R>
+__global__ __launch_bounds__(R == 1 ? kBwdRows1 * 64 : R * 64) void norm_bwd_kernel(NormBwdArgs p) {
+    constexpr int NW = R == 1 ? kBwdRows1 : R;
+    __shared__ float tmp[2][2][NW];
+    __shared__ float sW[R == 1 ? NW - 1 : 1][R == 1 ? 64 * V * P : 1];
+    const int lane = threadIdx.x % 64;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int dim = static_cast<int>(p.dim);
+    constexpr int per_wg = R == 1 ? kBwdRows1 : 1;
+    const uint32_t e0 = static_cast<uint32_t>(((R == 1 ? 0 : w) * 64 + lane) * V);
+    constexpr uint32_t step = R * 64 * V;
+    float wt[P][V], dw[P][V];
+    const rsrc_t rw = make_rsrc(p.weight, static_cast<uint32_t>(dim * 4));
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+        Chunk<float, V> q;
+        q.load(rw, e0 + c * step);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            wt[c][i] = q.get(i);
+            dw[c][i] = 0.0f;
+        }
+    }
+    const float inv_dim = 1.0f / static_cast<float>(dim);
+    int par = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_wg + (R == 1 ? w : 0); row < p.rows;
+         row += static_cast<int64_t>(gridDim.x) * per_wg, par ^= 1) {
+        Chunk<T, V> dy[P];
+        Chunk<S, V> r[P], add[P];
+        const rsrc_t rr = row_rsrc<S>(p.r, row, p.dim, dim), rd = row_rsrc<T>(p.dy, row, p.dim, dim);
+#pragma unroll
+        for (int c = 0; c < P; ++c) r[c].load(rr, e0 + c * step);
+#pragma unroll
+        for (int c = 0; c < P; ++c) dy[c].load(rd, e0 + c * step);
+        if (p.dres_out) {
+            const rsrc_t ra = row_rsrc<S>(p.dres_out, row, p.dim, dim);
+#pragma unroll
+            for (int c = 0; c < P; ++c) add[c].load(ra, e0 + c * step);
+        }
         float ss = 0.0f, dot = 0.0f;
-        for (int i = threadIdx.x; i < dim; i += kThreads) {
-            const float v = to_f32(rr[i]);
-            ss = fmaf(v, v, ss);
-            dot = fmaf(v, p.weight[i] * to_f32(dy[i]), dot);
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float v = r[c].get(i);
+                ss = fmaf(v, v, ss);
+                dot = fmaf(v, wt[c][i] * dy[c].get(i), dot);
+            }
+        ss = row_fold<R>(ss, tmp[0][par], AddOp());
+        dot = row_fold<R>(dot, tmp[1][par], AddOp());
+        const float rstd = 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps));
+        const float k = dot * inv_dim * rstd * rstd;           // mean(n w dy) rstd
+        const rsrc_t wx = row_rsrc<T>(p.dx, row, p.dim, dim);
+        const rsrc_t wr = p.dres ? row_rsrc<S>(p.dres, row, p.dim, dim) : make_rsrc(p.dx, 0u);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float g = dy[c].get(i), v = r[c].get(i);
+                o[i] = rstd * fmaf(-v, k, wt[c][i] * g);
+                if (p.dres_out) o[i] += add[c].get(i);
+                dw[c][i] = fmaf(g, v * rstd, dw[c][i]);
+            }
+            Chunk<T, V>::store(o, wx, e0 + c * step);
+            if (p.dres) Chunk<S, V>::store(o, wr, e0 + c * step);
         }
-        ss = block_reduce(ss, tmp, Add());
-        dot = block_reduce(dot, tmp, Add());
-        const float rstd = 1.0f / sqrtf(ss / static_cast<float>(dim) + p.eps);
-        const float c = dot * rstd / static_cast<float>(dim);
-        for (int i = threadIdx.x; i < dim; i += kThreads) {
-            const float n = to_f32(rr[i]) * rstd, g = to_f32(dy[i]);
-            float v = rstd * (p.weight[i] * g - n * c);
-            if (add) v += to_f32(add[i]);
-            static_cast<T *>(p.dx)[r * p.dim + i] = from_f32<T>(v);
-            if (p.dres) static_cast<R *>(p.dres)[r * p.dim + i] = from_f32<R>(v);
-            part[i] += g * n;
-        }
+    }
+    if constexpr (R == 1) {                            // the waves' sums, in wave order
+        if (w > 0)
+#pragma unroll
+            for (int c = 0; c < P; ++c)
+#pragma unroll
+                for (int i = 0; i < V; ++i) sW[w - 1][(c * V + i) * 64 + lane] = dw[c][i];
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                for (int u = 0; u < NW - 1; ++u) dw[c][i] += sW[u][(c * V + i) * 64 + lane];
+    }
+    const rsrc_t rp = row_rsrc<float>(p.workspace, blockIdx.x, p.dim, dim);
+#pragma unroll
+    for (int c = 0; c < P; ++c) Chunk<float, V>::store(dw[c], rp, e0 + c * step);
+}
+
+// dw: 32 columns x 32 stripes of the partial sums per workgroup, the stripes
+// added in order
+__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *part, float *out, int parts, int dim) {
+    __shared__ float sums[32][33];
+    const int col = threadIdx.x % 32, stripe = threadIdx.x / 32;
+    const int d = blockIdx.x * 32 + col;
+    float s = 0.0f;
+    if (d < dim)
+        for (int i = stripe; i < parts; i += 32) s += part[static_cast<int64_t>(i) * dim + d];
+    sums[stripe][col] = s;
+    __syncthreads();
+    if (stripe == 0 && d < dim) {
+        for (int i = 1; i < 32; ++i) s += sums[i][col];
+        out[d] = s;
     }
 }
 
-__global__ __launch_bounds__(kThreads) void norm_dweight_kernel(const float *part, float *out, int64_t parts, int64_t dim) {
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (d >= dim) return;
-    float s = 0.0f;
-    for (int64_t i = 0; i < parts; ++i) s += part[i * dim + d];
-    out[d] = s;
+// ------------------------------------------------------------------- host
+bool wide(const void *p, int64_t ld, size_t es) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<int64_t>(es) % 16 == 0;
 }
 
-int64_t parts_of(int64_t rows) { return (rows + kPartRows - 1) / kPartRows; }
+constexpr int64_t kMaxGrid = 2048;      // workgroups: 8 of four waves per CU
+constexpr int64_t kMaxParts = 512;      // workgroups of the gradient, each with a partial sum
+
+template <typename T, typename S, bool Q, int V, int P, int R> hipError_t launch_fwd(const NormArgs &a, hipStream_t s) {
+    const int per_wg = R == 1 ? 4 : 1;
+    const int64_t wgs = (a.rows + per_wg - 1) / per_wg;
+    hipLaunchKernelGGL((norm_kernel<T, S, Q, V, P, R>), dim3(static_cast<unsigned>(wgs < kMaxGrid ? wgs : kMaxGrid)),
+                       dim3(R == 1 ? 256 : R * 64), 0, s, a);
+    return hipGetLastError();
+}
+int64_t parts_of(int64_t rows, int per_wg) {
+    const int64_t wgs = (rows + per_wg - 1) / per_wg;
+    return wgs < kMaxParts ? wgs : kMaxParts;
+}
+template <typename T, typename S, int V, int P, int R> hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
+    const int parts = static_cast<int>(parts_of(a.rows, R == 1 ? kBwdRows1 : 1));
+    if (parts > 0)
+        hipLaunchKernelGGL((norm_bwd_kernel<T, S, V, P, R>), dim3(parts), dim3(R == 1 ? kBwdRows1 * 64 : R * 64), 0, s, a);
+    hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((a.dim + 31) / 32)), dim3(1024), 0, s,
+                       static_cast<const float *>(a.workspace), a.dweight, parts, static_cast<int>(a.dim));
+    return hipGetLastError();
+}
+
+// The chunks per lane and waves per row for a width of `chunks` x 64 V elements.
+// The gradient holds three tensors and dw beside the weight, so it takes
+// fewer chunks per lane.
+#define SSM_FWD_PICK8(CALL)                                                        \
+    return chunks <= 1    ? CALL(8, 1, 1)                                          \
+           : chunks <= 2  ? CALL(8, 2, 1)                                          \
+           : chunks <= 3  ? CALL(8, 3, 1)                                          \
+           : chunks <= 4  ? CALL(8, 4, 1)                                          \
+           : chunks <= 5  ? CALL(8, 5, 1)                                          \
+           : chunks <= 8  ? CALL(8, 2, 4)                                          \
+           : chunks <= 12 ? CALL(8, 3, 4)                                          \
+           : chunks <= 16 ? CALL(8, 4, 4)                                          \
+           : chunks <= 32 ? CALL(8, 2, 16)                                         \
+                          : CALL(8, 4, 16)
+#define SSM_BWD_PICK8(CALL)                                                        \
+    return chunks <= 1    ? CALL(8, 1, 1)                                          \
+           : chunks <= 2  ? CALL(8, 2, 1)                                          \
+           : chunks <= 4  ? CALL(8, 1, 4)                                          \
+           : chunks <= 8  ? CALL(8, 2, 4)                                          \
+           : chunks <= 16 ? CALL(8, 1, 16)                                         \
+           : chunks <= 32 ? CALL(8, 2, 16)                                         \
+                          : CALL(8, 4, 16)
+#define SSM_PICK1(CALL)                                                            \
+    return chunks <= 4     ? CALL(1, 4, 1)                                         \
+           : chunks <= 16  ? CALL(1, 4, 4)                                         \
+           : chunks <= 64  ? CALL(1, 4, 16)                                        \
+           : chunks <= 128 ? CALL(1, 8, 16)                                        \
+           : chunks <= 256 ? CALL(1, 16, 16)                                       \
+                           : CALL(1, 32, 16)
+
+template <typename T, typename S, bool Q> hipError_t pick_fwd(const NormArgs &a, hipStream_t s) {
+#define SSM_CALL(V, P, R) (launch_fwd<T, S, Q, V, P, R>(a, s))
+    if (a.dim % 8 == 0 && wide(a.x, a.ldx, sizeof(T)) && wide(a.residual, a.dim, sizeof(S)) &&
+        wide(a.residual_out, a.dim, sizeof(S)) && wide(a.weight, a.dim, 4) &&
+        reinterpret_cast<uintptr_t>(a.y) % (Q ? 8 : 16) == 0) {
+        const int64_t chunks = (a.dim + 511) / 512;
+        SSM_FWD_PICK8(SSM_CALL);
+    }
+    const int64_t chunks = (a.dim + 63) / 64;
+    SSM_PICK1(SSM_CALL);
+#undef SSM_CALL
+}
+template <typename T, typename S> hipError_t pick_bwd(const NormBwdArgs &a, hipStream_t s) {
+#define SSM_CALL(V, P, R) (launch_bwd<T, S, V, P, R>(a, s))
+    if (a.dim % 8 == 0 && wide(a.dy, a.dim, sizeof(T)) && wide(a.dx, a.dim, sizeof(T)) && wide(a.r, a.dim, sizeof(S)) &&
+        wide(a.dres_out, a.dim, sizeof(S)) && wide(a.dres, a.dim, sizeof(S)) && wide(a.weight, a.dim, 4)) {
+        const int64_t chunks = (a.dim + 511) / 512;
+        SSM_BWD_PICK8(SSM_CALL);
+    }
+    const int64_t chunks = (a.dim + 63) / 64;
+    SSM_PICK1(SSM_CALL);
+#undef SSM_CALL
+}
+template <typename T, typename S> hipError_t pick_fwd_q(const NormArgs &a, hipStream_t s) {
+    return a.scale ? pick_fwd<T, S, true>(a, s) : pick_fwd<T, S, false>(a, s);
+}
 
 }  // namespace
 
-size_t norm_bwd_workspace(int64_t rows, int64_t dim) { return static_cast<size_t>(parts_of(rows) * dim) * 4; }
+size_t norm_bwd_workspace(int64_t rows, int64_t dim) {
+    return static_cast<size_t>(parts_of(rows, 1) * ((dim + 3) / 4 * 4)) * 4;
+}
 
 hipError_t launch_add_rms_norm(const NormArgs &a, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.rows)), block(kThreads);
-    const size_t lds = static_cast<size_t>(a.dim) * 4;
-    const void *f = a.bf16 ? (a.res_bf16 ? reinterpret_cast<const void *>(norm_kernel<bf16_t, bf16_t>)
-                                         : reinterpret_cast<const void *>(norm_kernel<bf16_t, float>))
-                           : reinterpret_cast<const void *>(norm_kernel<float, float>);
-    if (lds > 60000)
-        if (hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)))
-            return e;
-    NormArgs p = a;
-    void *args[] = {&p};
-    return hipLaunchKernel(f, grid, block, args, lds, s);
+    if (!a.bf16) return pick_fwd_q<float, float>(a, s);
+    return a.res_bf16 ? pick_fwd_q<bf16_t, bf16_t>(a, s) : pick_fwd_q<bf16_t, float>(a, s);
 }
 
 hipError_t launch_add_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s) {
-    const int64_t parts = parts_of(a.rows);
-    if (parts > 0) {
-        const dim3 grid(static_cast<unsigned>(parts)), block(kThreads);
-        if (a.bf16 && a.res_bf16)
-            hipLaunchKernelGGL((norm_bwd_kernel<bf16_t, bf16_t>), grid, block, 0, s, a);
-        else if (a.bf16)
-            hipLaunchKernelGGL((norm_bwd_kernel<bf16_t, float>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((norm_bwd_kernel<float, float>), grid, block, 0, s, a);
-    }
-    hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((a.dim + kThreads - 1) / kThreads)), dim3(kThreads),
-                       0, s, static_cast<const float *>(a.workspace), a.dweight, parts, a.dim);
-    return hipGetLastError();
+    if (!a.bf16) return pick_bwd<float, float>(a, s);
+    return a.res_bf16 ? pick_bwd<bf16_t, bf16_t>(a, s) : pick_bwd<bf16_t, float>(a, s);
 }
 
 }  // namespace ssm
