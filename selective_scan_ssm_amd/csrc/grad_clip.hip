@@ -5,7 +5,11 @@
 // so nothing is copied to the device beforehand and a captured call replays by
 // itself.  Squares are summed in 64 bits: an fp32 square overflows above 1.8e19
 // and a sum over 10^9 values would lose its small ones.
-// First form: a workgroup takes chunks of kChunk elements in turn.
+// HBM-bound: a workgroup takes chunks of kChunk elements in turn and reads each
+// with 16-byte loads from the first aligned address on (gradients are often
+// views into one bucket, at any offset); the elements before and after go one
+// by one.  Every workgroup leaves one partial sum; the scaling kernel adds them
+// all itself, in the same order everywhere, which saves a launch between the two.
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
@@ -50,19 +54,136 @@ __device__ __forceinline__ double block_sum(double v) {
     return v;
 }
 
-__device__ __forceinline__ float load(const void *p, int64_t i, bool bf16) {
-    return bf16 ? to_f32(static_cast<const bf16_t *>(p)[i]) : static_cast<const float *>(p)[i];
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// V consecutive elements of 16 bytes as fp32
+template <typename T> struct Vec {
+    static constexpr int V = 16 / sizeof(T);
+    static __device__ __forceinline__ void widen(u4 q, float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (V == 8)
+                v[i] = __uint_as_float(i % 2 ? (q[i / 2] & 0xffff0000u) : (q[i / 2] << 16));
+            else
+                v[i] = __uint_as_float(q[i]);
+        }
+    }
+};
+
+// The 16-byte vectors inside elements [i0, i1) of p: `head` elements come
+// before the first, `vecs` vectors follow, the rest comes after.
+struct Cut {
+    int head, vecs;
+};
+template <typename T> __device__ __forceinline__ Cut cut(const T *p, int64_t i0, int n) {
+    constexpr int V = Vec<T>::V;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p + i0) % 16) / sizeof(T));
+    const int head = off ? (V - off < n ? V - off : n) : 0;
+    return {head, (n - head) / V};
+}
+
+template <typename T> __device__ __forceinline__ double sum_chunk(const T *p, int64_t i0, int n) {
+    constexpr int V = Vec<T>::V, kUnroll = 4;
+    const Cut c = cut(p, i0, n);
+    const T *q = p + i0 + c.head;
+    const u4 *b = reinterpret_cast<const u4 *>(q);
+    double s = 0.0;
+    auto add = [&](u4 w) {
+        float v[V];
+        Vec<T>::widen(w, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), s);
+    };
+    int k = threadIdx.x;
+    for (; k + (kUnroll - 1) * kThreads < c.vecs; k += kUnroll * kThreads) {
+        u4 w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) w[i] = b[k + i * kThreads];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) add(w[i]);
+    }
+    for (; k < c.vecs; k += kThreads) add(b[k]);
+    auto one = [&](const T *e) {
+        const double v = to_f32(*e);
+        s = fma(v, v, s);
+    };
+    if (static_cast<int>(threadIdx.x) < c.head) one(p + i0 + threadIdx.x);
+    const int tail = c.head + c.vecs * V + threadIdx.x;
+    if (tail < n) one(p + i0 + tail);
+    return s;
+}
+
+template <typename O> __device__ __forceinline__ void put(O *p, float v) { *p = from_f32<O>(v); }
+// V fp32 values at out: 16-byte stores when its address allows them
+template <typename O, int V> __device__ __forceinline__ void put_vec(O *out, const float (&v)[V], bool aligned) {
+    constexpr int VO = 16 / sizeof(O);
+    if (!aligned) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) put(out + i, v[i]);
+        return;
+    }
+    if constexpr (V >= VO) {
+#pragma unroll
+        for (int h = 0; h < V / VO; ++h) {
+            u4 q;
+            if constexpr (VO == 8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[i] = static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i]).bits) |
+                           (static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i + 1]).bits) << 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(v[4 * h + i]);
+            }
+            reinterpret_cast<u4 *>(out)[h] = q;
+        }
+    } else {                                           // four fp32 values to bf16: 8 bytes
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        u2 q;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            q[i] = static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i]).bits) |
+                   (static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i + 1]).bits) << 16);
+        *reinterpret_cast<u2 *>(out) = q;
+    }
+}
+
+template <typename T, typename O> __device__ __forceinline__ void scale_chunk(const T *p, O *out, int64_t i0, int n, float coef) {
+    constexpr int V = Vec<T>::V, kUnroll = 4;
+    constexpr int kOutBytes = V * sizeof(O) < 16 ? V * sizeof(O) : 16;
+    const Cut c = cut(p, i0, n);
+    const u4 *b = reinterpret_cast<const u4 *>(p + i0 + c.head);
+    O *o = out + i0 + c.head;
+    const bool aligned = reinterpret_cast<uintptr_t>(o) % kOutBytes == 0;
+    auto scale = [&](u4 w, int k) {
+        float v[V];
+        Vec<T>::widen(w, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= coef;
+        put_vec<O, V>(o + static_cast<int64_t>(k) * V, v, aligned);
+    };
+    int k = threadIdx.x;
+    for (; k + (kUnroll - 1) * kThreads < c.vecs; k += kUnroll * kThreads) {
+        u4 w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) w[i] = b[k + i * kThreads];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) scale(w[i], k + i * kThreads);
+    }
+    for (; k < c.vecs; k += kThreads) scale(b[k], k);
+    if (static_cast<int>(threadIdx.x) < c.head) put(out + i0 + threadIdx.x, to_f32(p[i0 + threadIdx.x]) * coef);
+    const int tail = c.head + c.vecs * V + threadIdx.x;
+    if (tail < n) put(out + i0 + tail, to_f32(p[i0 + tail]) * coef);
 }
 
 __global__ __launch_bounds__(kThreads) void sumsq_kernel(Table t, double *part) {
     double s = 0.0;
     for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Entry &e = t.e[find(t, c)];
-        const int64_t n = e.n_flags >> 2, i0 = (c - e.first) * kChunk, i1 = i0 + kChunk < n ? i0 + kChunk : n;
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const double v = load(e.in, i, e.n_flags & 1);
-            s = fma(v, v, s);
-        }
+        const int64_t i0 = (c - e.first) * kChunk, left = (e.n_flags >> 2) - i0;
+        const int n = static_cast<int>(left < kChunk ? left : kChunk);
+        s += e.n_flags & 1 ? sum_chunk(static_cast<const bf16_t *>(e.in), i0, n)
+                           : sum_chunk(static_cast<const float *>(e.in), i0, n);
     }
     s = block_sum(s);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -89,13 +210,13 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Table t, const double *p
     for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Entry &e = t.e[find(t, c)];
         if (coef == 1.0f && e.out == e.in) continue;   // nothing changes
-        const int64_t n = e.n_flags >> 2, i0 = (c - e.first) * kChunk, i1 = i0 + kChunk < n ? i0 + kChunk : n;
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const float v = load(e.in, i, e.n_flags & 1) * coef;
-            if (e.n_flags & 2)
-                static_cast<bf16_t *>(e.out)[i] = from_f32<bf16_t>(v);
-            else
-                static_cast<float *>(e.out)[i] = v;
+        const int64_t i0 = (c - e.first) * kChunk, left = (e.n_flags >> 2) - i0;
+        const int n = static_cast<int>(left < kChunk ? left : kChunk);
+        switch (e.n_flags & 3) {
+        case 0: scale_chunk(static_cast<const float *>(e.in), static_cast<float *>(e.out), i0, n, coef); break;
+        case 1: scale_chunk(static_cast<const bf16_t *>(e.in), static_cast<float *>(e.out), i0, n, coef); break;
+        case 2: scale_chunk(static_cast<const float *>(e.in), static_cast<bf16_t *>(e.out), i0, n, coef); break;
+        default: scale_chunk(static_cast<const bf16_t *>(e.in), static_cast<bf16_t *>(e.out), i0, n, coef);
         }
     }
 }
