@@ -11,6 +11,7 @@
 // stride and keep the weight in registers; the gradient also keeps its lane's
 // share of dw there, and one partial sum per workgroup goes through the
 // workspace.
+#include "column_sum.h"
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
@@ -279,21 +280,8 @@ __global__ __launch_bounds__(R == 1 ? kBwdRows1 * 64 : R * 64) void norm_bwd_ker
     for (int c = 0; c < P; ++c) Chunk<float, V>::store(dw[c], rp, e0 + c * step);
 }
 
-// dw: 32 columns x 32 stripes of the partial sums per workgroup, the stripes
-// added in order
-__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *part, float *out, int parts, int dim) {
-    __shared__ float sums[32][33];
-    const int col = threadIdx.x % 32, stripe = threadIdx.x / 32;
-    const int d = blockIdx.x * 32 + col;
-    float s = 0.0f;
-    if (d < dim)
-        for (int i = stripe; i < parts; i += 32) s += part[static_cast<int64_t>(i) * dim + d];
-    sums[stripe][col] = s;
-    __syncthreads();
-    if (stripe == 0 && d < dim) {
-        for (int i = 1; i < 32; ++i) s += sums[i][col];
-        out[d] = s;
-    }
+__global__ __launch_bounds__(kSumThreads) void norm_dweight_kernel(const float *part, float *out, int64_t parts, int64_t dim) {
+    column_sums(part, out, parts, dim);
 }
 
 // ------------------------------------------------------------------- host
@@ -319,8 +307,9 @@ template <typename T, typename S, int V, int P, int R> hipError_t launch_bwd(con
     const int parts = static_cast<int>(parts_of(a.rows, R == 1 ? kBwdRows1 : 1));
     if (parts > 0)
         hipLaunchKernelGGL((norm_bwd_kernel<T, S, V, P, R>), dim3(parts), dim3(R == 1 ? kBwdRows1 * 64 : R * 64), 0, s, a);
-    hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((a.dim + 31) / 32)), dim3(1024), 0, s,
-                       static_cast<const float *>(a.workspace), a.dweight, parts, static_cast<int>(a.dim));
+    hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((a.dim + kSumCols - 1) / kSumCols)),
+                       dim3(kSumThreads), 0, s, static_cast<const float *>(a.workspace), a.dweight,
+                       static_cast<int64_t>(parts), a.dim);
     return hipGetLastError();
 }
 

@@ -1,0 +1,32 @@
+// Column sums of an fp32 (rows, dim) array of partial sums, in a fixed order.
+#pragma once
+
+#include "ssm_device.h"
+
+namespace ssm {
+
+constexpr int kSumCols = 16;      // columns of a workgroup
+constexpr int kSumThreads = 1024; // 64 stripes of rows x 16 columns
+
+// A thread adds every 64th row of its column (its loads are independent, so a
+// few hundred rows cost one or two memory latencies); the 64 stripes of a column
+// then meet in one wave.  512 rows x 768 columns: 4 us against 9 us with 32
+// columns and stripes added one after the other.
+__device__ __forceinline__ void column_sums(const float *part, float *out, int64_t rows, int64_t dim) {
+    __shared__ float sums[64][kSumCols + 1];
+    const int col = threadIdx.x % kSumCols, stripe = threadIdx.x / kSumCols;
+    const int64_t d = static_cast<int64_t>(blockIdx.x) * kSumCols + col;
+    float s = 0.0f;
+    if (d < dim) {
+#pragma unroll 8
+        for (int64_t r = stripe; r < rows; r += 64) s += part[r * dim + d];
+    }
+    sums[stripe][col] = s;
+    __syncthreads();
+    const int w = threadIdx.x / 64, lane = threadIdx.x % 64;
+    s = wave_fold(sums[lane][w], AddOp());
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * kSumCols + w;
+    if (lane == 0 && o < dim) out[o] = s;
+}
+
+}  // namespace ssm

@@ -21,6 +21,7 @@
 // gradient of h: e_t = d_t + c_{t+1}, tiles in falling order.  It needs the
 // states h_{t-1}: they are recomputed inside a tile from the state entering it,
 // which the forward saves (one fp32 per channel and 128 steps).
+#include "column_sum.h"
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
@@ -540,21 +541,9 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     }
 }
 
-// dgate_bias: the tiles' partial sums, 16 waves of a workgroup taking every
-// 16th row each, their sums added in wave order
-__global__ __launch_bounds__(1024) void gated_dbias_kernel(const float *part, float *out, int64_t rows, int64_t dim) {
-    __shared__ float sums[16][64];
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-    float s = 0.0f;
-    if (d < dim)
-        for (int64_t r = w; r < rows; r += 16) s += part[r * dim + d];
-    sums[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && d < dim) {
-        for (int i = 1; i < 16; ++i) s += sums[i][lane];
-        out[d] = s;
-    }
+// dgate_bias: the sum of the tiles' partial sums
+__global__ __launch_bounds__(kSumThreads) void gated_dbias_kernel(const float *part, float *out, int64_t rows, int64_t dim) {
+    column_sums(part, out, rows, dim);
 }
 
 // an empty sequence: the carry passes through
@@ -724,7 +713,7 @@ hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (a.dgate_bias) {
         const Layout l = layout(f.batch, f.seqlen, f.dim);
-        hipLaunchKernelGGL(gated_dbias_kernel, dim3(static_cast<unsigned>((f.dim + 63) / 64)), dim3(1024), 0, s,
+        hipLaunchKernelGGL(gated_dbias_kernel, dim3(static_cast<unsigned>((f.dim + kSumCols - 1) / kSumCols)), dim3(kSumThreads), 0, s,
                            reinterpret_cast<const float *>(static_cast<char *>(f.workspace) + l.total), a.dgate_bias,
                            f.batch * l.n_tiles, f.dim);
     }

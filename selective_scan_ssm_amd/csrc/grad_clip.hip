@@ -1,10 +1,14 @@
 // The global norm of a list of gradient tensors, and their clipping.
 //     norm = sqrt(sum g^2),  coef = min(1, max_norm / (norm + eps)),  out = g coef
 //
-// The list travels in the kernel arguments, up to kEntries tensors per launch,
-// so nothing is copied to the device beforehand and a captured call replays by
-// itself.  Squares are summed in 64 bits: an fp32 square overflows above 1.8e19
-// and a sum over 10^9 values would lose its small ones.
+// Squares are summed in 64 bits: an fp32 square overflows above 1.8e19 and a sum
+// over 10^9 values would lose its small ones.
+//
+// The list travels in the kernel arguments, so no copy from host memory is
+// enqueued and a captured call replays by itself: directly up to kEntries
+// tensors, and for longer lists by small kernels that write their share of the
+// table into the workspace first, so that the two passes over the gradients stay
+// one launch each.
 // HBM-bound: a workgroup takes chunks of kChunk elements in turn and reads each
 // with 16-byte loads from the first aligned address on (gradients are often
 // views into one bucket, at any offset); the elements before and after go one
@@ -17,31 +21,28 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEntries = 112;           // 32 bytes each: the table stays under 4 KB of kernel arguments
-constexpr int64_t kChunk = 16384;       // elements
-constexpr int kGrid = 1024;             // workgroups, and partial sums, per launch
+constexpr int kEntries = 120;           // 32 bytes each: a table stays under 4 KB of kernel arguments
+constexpr int64_t kChunk = 8192;        // elements
+constexpr int kGrid = 2048;             // workgroups (8 per CU), and partial sums
 
 struct Entry {
     const void *in;
     void *out;
     int64_t n_flags;                    // elements * 4 + (in is bf16) + 2 * (out is bf16)
-    int64_t first;                      // index of the entry's first chunk in this launch
+    int64_t first;                      // index of the entry's first chunk
 };
 struct Table {
     Entry e[kEntries];
-    int count;
-    int grid;
-    int64_t chunks;
 };
 
-// the entry whose chunks hold chunk c
-__device__ __forceinline__ int find(const Table &t, int64_t c) {
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (t.e[mid].first <= c) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+// The entry whose chunks hold chunk c: the last with first <= c.  Every lane
+// tests one entry, so a list of a few hundred costs one memory latency.
+__device__ __forceinline__ int find(const Entry *e, int count, int64_t c) {
+    const int lane = threadIdx.x % 64;
+    int n = 0;
+    for (int i = 0; i < count; i += 64)
+        n += __popcll(__ballot(i + lane < count && e[i + lane < count ? i + lane : 0].first <= c));
+    return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 __device__ __forceinline__ double block_sum(double v) {
@@ -176,10 +177,10 @@ template <typename T, typename O> __device__ __forceinline__ void scale_chunk(co
     if (tail < n) put(out + i0 + tail, to_f32(p[i0 + tail]) * coef);
 }
 
-__global__ __launch_bounds__(kThreads) void sumsq_kernel(Table t, double *part) {
+__device__ __forceinline__ void sumsq(const Entry *tab, int count, int64_t chunks, double *part) {
     double s = 0.0;
-    for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const Entry &e = t.e[find(t, c)];
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Entry &e = tab[find(tab, count, c)];
         const int64_t i0 = (c - e.first) * kChunk, left = (e.n_flags >> 2) - i0;
         const int n = static_cast<int>(left < kChunk ? left : kChunk);
         s += e.n_flags & 1 ? sum_chunk(static_cast<const bf16_t *>(e.in), i0, n)
@@ -190,25 +191,23 @@ __global__ __launch_bounds__(kThreads) void sumsq_kernel(Table t, double *part) 
 }
 
 // every workgroup adds the partial sums, in the same order
-__device__ __forceinline__ float norm_of(const double *part, int64_t parts) {
+__device__ __forceinline__ float norm_of(const double *part, int parts) {
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+#pragma unroll 8
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
     return static_cast<float>(sqrt(block_sum(s)));
 }
 
-__global__ __launch_bounds__(kThreads) void norm_only_kernel(const double *part, int64_t parts, float *norm) {
-    const float v = norm_of(part, parts);
-    if (threadIdx.x == 0) *norm = v;
-}
-
-__global__ __launch_bounds__(kThreads) void clip_kernel(Table t, const double *part, int64_t parts, float max_norm,
-                                                        float eps, float *norm) {
+// Chunks are taken from the last one down: the sums have just been over them,
+// so the last ones read are the likeliest to be in a cache still.
+__device__ __forceinline__ void clip(const Entry *tab, int count, int64_t chunks, const double *part, int parts,
+                                     float max_norm, float eps, float *norm) {
     const float total = norm_of(part, parts);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     float coef = max_norm / (total + eps);
     coef = coef > 1.0f ? 1.0f : coef;                  // false for NaN, which stays
-    for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const Entry &e = t.e[find(t, c)];
+    for (int64_t c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+        const Entry &e = tab[find(tab, count, c)];
         if (coef == 1.0f && e.out == e.in) continue;   // nothing changes
         const int64_t i0 = (c - e.first) * kChunk, left = (e.n_flags >> 2) - i0;
         const int n = static_cast<int>(left < kChunk ? left : kChunk);
@@ -221,51 +220,79 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Table t, const double *p
     }
 }
 
+__global__ __launch_bounds__(kThreads) void sumsq_kernel(Table t, int count, int64_t chunks, double *part) {
+    sumsq(t.e, count, chunks, part);
+}
+__global__ __launch_bounds__(kThreads) void sumsq_long_kernel(const Entry *tab, int count, int64_t chunks, double *part) {
+    sumsq(tab, count, chunks, part);
+}
+__global__ __launch_bounds__(kThreads) void clip_kernel(Table t, int count, int64_t chunks, const double *part, int parts,
+                                                        float max_norm, float eps, float *norm) {
+    clip(t.e, count, chunks, part, parts, max_norm, eps, norm);
+}
+__global__ __launch_bounds__(kThreads) void clip_long_kernel(const Entry *tab, int count, int64_t chunks, const double *part,
+                                                             int parts, float max_norm, float eps, float *norm) {
+    clip(tab, count, chunks, part, parts, max_norm, eps, norm);
+}
+__global__ __launch_bounds__(kThreads) void norm_kernel(const double *part, int parts, float *norm) {
+    const float v = norm_of(part, parts);
+    if (threadIdx.x == 0) *norm = v;
+}
+__global__ __launch_bounds__(kThreads) void table_kernel(Table t, int count, Entry *tab) {
+    if (static_cast<int>(threadIdx.x) < count) tab[threadIdx.x] = t.e[threadIdx.x];
+}
+static_assert(kEntries <= kThreads, "one thread writes one entry");
+
 // the next entries of the list that hold anything, from index i on
-int64_t fill(Table &t, const ClipArgs &a, int64_t i) {
-    t.count = 0;
-    t.chunks = 0;
-    for (; i < a.count && t.count < kEntries; ++i) {
+int64_t fill(Table &t, int &count, int64_t &chunks, const ClipArgs &a, int64_t i) {
+    for (count = 0; i < a.count && count < kEntries; ++i) {
         const int64_t n = a.numel[i];
         if (n == 0) continue;
-        Entry &e = t.e[t.count++];
+        Entry &e = t.e[count++];
         e.in = a.grads[i];
         e.out = a.outs ? a.outs[i] : const_cast<void *>(a.grads[i]);
         e.n_flags = n * 4 + (a.dtypes[i] != 0 ? 1 : 0) + (a.out_dtypes[i] != 0 ? 2 : 0);
-        e.first = t.chunks;
-        t.chunks += (n + kChunk - 1) / kChunk;
+        e.first = chunks;
+        chunks += (n + kChunk - 1) / kChunk;
     }
-    t.grid = static_cast<int>(t.chunks < kGrid ? t.chunks : kGrid);
     return i;
 }
 
 }  // namespace
 
+// the partial sums, then the table of a long list
 size_t grad_norm_workspace(int64_t count) {
-    return static_cast<size_t>((count + kEntries - 1) / kEntries * kGrid) * sizeof(double);
+    return kGrid * sizeof(double) + static_cast<size_t>(count > kEntries ? count : 0) * sizeof(Entry);
 }
 
 hipError_t launch_grad_clip(const ClipArgs &a, hipStream_t s) {
     Table t;
     double *part = static_cast<double *>(a.workspace);
-    int64_t parts = 0;
+    Entry *tab = reinterpret_cast<Entry *>(part + kGrid);
+    int count = 0, total = 0;
+    int64_t chunks = 0;
+    const bool is_long = a.count > kEntries;
     for (int64_t i = 0; i < a.count;) {
-        i = fill(t, a, i);
-        if (t.count == 0) break;
-        hipLaunchKernelGGL(sumsq_kernel, dim3(t.grid), dim3(kThreads), 0, s, t, part + parts);
-        parts += t.grid;
+        i = fill(t, count, chunks, a, i);
+        if (is_long && count > 0)
+            hipLaunchKernelGGL(table_kernel, dim3(1), dim3(kThreads), 0, s, t, count, tab + total);
+        total += count;
     }
-    if (!a.scale || parts == 0) {
-        hipLaunchKernelGGL(norm_only_kernel, dim3(1), dim3(kThreads), 0, s, part, parts, a.norm);
-        return hipGetLastError();
+    const int grid = static_cast<int>(chunks < kGrid ? chunks : kGrid);
+    if (grid > 0) {
+        if (is_long)
+            hipLaunchKernelGGL(sumsq_long_kernel, dim3(grid), dim3(kThreads), 0, s, tab, total, chunks, part);
+        else
+            hipLaunchKernelGGL(sumsq_kernel, dim3(grid), dim3(kThreads), 0, s, t, total, chunks, part);
     }
-    float *norm = a.norm;
-    for (int64_t i = 0; i < a.count;) {
-        i = fill(t, a, i);
-        if (t.count == 0) break;
-        hipLaunchKernelGGL(clip_kernel, dim3(t.grid), dim3(kThreads), 0, s, t, part, parts, a.max_norm, a.eps, norm);
-        norm = nullptr;                                // the first launch writes it
-    }
+    if (!a.scale || grid == 0)
+        hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(kThreads), 0, s, part, grid, a.norm);
+    else if (is_long)
+        hipLaunchKernelGGL(clip_long_kernel, dim3(grid), dim3(kThreads), 0, s, tab, total, chunks, part, grid, a.max_norm,
+                           a.eps, a.norm);
+    else
+        hipLaunchKernelGGL(clip_kernel, dim3(grid), dim3(kThreads), 0, s, t, total, chunks, part, grid, a.max_norm, a.eps,
+                           a.norm);
     return hipGetLastError();
 }
 

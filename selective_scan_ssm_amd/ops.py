@@ -8,6 +8,7 @@ RuntimeError.  Every step of the computation runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional
 
 import torch
@@ -450,33 +451,45 @@ def conv_scan_fwd(x, conv_weight, delta, A, B, C, conv_bias=None, conv_state=Non
 
 
 # ------------------------------------------------- the gated recurrent block
-def _on(dev, **tensors):
-    """Every tensor given is on dev."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+# A decode step's kernels run for a few microseconds, so these wrappers check
+# each tensor with one test that passes (its message is put together only when
+# it fails) and take the stream handle without building a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BAD = (1 << 64) - 1
 
 
-def _run(dev, fn, *args):
-    """fn(*args, stream) with dev as the current device, on its current stream."""
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, _stream(dev))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream(dev))
-
-
-def _rows(t, name, dtype, shape):
-    """The stride between consecutive rows of t, whose last axis is contiguous
-    and whose other axes step evenly (a column range of a wider tensor)."""
+def _device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _arg(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this dtype and shape on dev (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, dev):
+    """The address of t and the stride between its consecutive rows: its last
+    axis is contiguous and its other axes step evenly (a column range of a
+    wider tensor)."""
+    if t is None:
+        return None, 0
+    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    _device(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     dim = shape[-1]
-    if t.is_contiguous():
-        return dim
     if dim > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have a contiguous last axis")
     lead = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
@@ -486,19 +499,28 @@ def _rows(t, name, dtype, shape):
     ld = lead[-1][1] if lead else dim
     if ld < dim:
         raise ValueError(f"the rows of {name} overlap")
-    return ld
+    return t.data_ptr(), ld
 
 
-def _workspace(need, what, workspace, dev):
-    if need == (1 << 64) - 1:
+def _run(dev, fn, *args):
+    """fn(*args, stream) with dev as the current device, on its current stream."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(dev):
+        return fn(*args, _raw_stream(index))
+
+
+def _scratch(need, what, workspace, dev):
+    """A workspace of `need` bytes: the caller's if it is large enough.  Returns
+    it (the caller holds it until the launch) and its address."""
+    if need == _BAD:
         raise RuntimeError(f"{what}: invalid arguments")
     if not need:
-        return None
-    if workspace is not None and workspace.numel() >= need:
-        _dev(workspace, "workspace", torch.uint8)
-        _on(dev, workspace=workspace)
-        return workspace
-    return torch.empty(need, dtype=torch.uint8, device=dev)
+        return None, None
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, _arg(workspace, "workspace", torch.uint8, workspace.shape, dev)
 
 
 def gated_ckpt_shape(batch, seqlen, d_inner):
@@ -517,26 +539,24 @@ def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=Fals
     gated_ckpt_shape(...) that also receives the state entering every 128-step
     block, for gated_scan_bwd(..., ckpt=ckpt_out)."""
     lib = _lib.load()
-    if x.dtype not in _IO:
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO:
         raise ValueError("x must be float32 or bfloat16")
-    io, dev = x.dtype, x.device
-    Bt, T, Dd = x.shape
-    ldx, ldg = _rows(x, "x", io, x.shape), _rows(g, "g", io, x.shape)
-    ldz = _rows(z, "z", io, x.shape) if z is not None else 0
-    _dev(gate_bias, "gate_bias", torch.float32, (Dd,))
-    _dev(h0, "h0", torch.float32, (Bt, Dd))
-    y = out if out is not None else torch.empty(x.shape, dtype=io, device=dev)
-    _dev(y, "out", io, x.shape)
+    Bt, T, Dd = shape
+    px, ldx = _rows(x, "x", io, shape, dev)
+    pg, ldg = _rows(g, "g", io, shape, dev)
+    pz, ldz = _rows(z, "z", io, shape, dev)
+    y = out if out is not None else torch.empty(shape, dtype=io, device=dev)
     last = None
     if return_last_state:
         last = last_state_out if last_state_out is not None else torch.empty((Bt, Dd), dtype=torch.float32, device=dev)
-        _dev(last, "last_state_out", torch.float32, (Bt, Dd))
-    _dev(ckpt_out, "ckpt_out", torch.float32, gated_ckpt_shape(Bt, T, Dd))
-    _on(dev, g=g, z=z, gate_bias=gate_bias, h0=h0, out=y, last_state_out=last, ckpt_out=ckpt_out)
-    need = lib.ssm_gated_scan_workspace_bytes(Bt, T, Dd, _IO[io])
-    ws = _workspace(need, "ssm_gated_scan_workspace_bytes", workspace, dev)
-    rc = _run(dev, lib.ssm_gated_scan_fwd, _ptr(x), ldx, _ptr(g), ldg, _ptr(gate_bias), _ptr(z), ldz, _ptr(h0), _ptr(y),
-              _ptr(last), _ptr(ckpt_out), Bt, T, Dd, _IO[io], _ptr(ws), need)
+    ws, pws = _scratch(lib.ssm_gated_scan_workspace_bytes(Bt, T, Dd, _IO[io]), "ssm_gated_scan_workspace_bytes",
+                       workspace, dev)
+    rc = _run(dev, lib.ssm_gated_scan_fwd, px, ldx, pg, ldg, _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev), pz,
+              ldz, _arg(h0, "h0", torch.float32, (Bt, Dd), dev), _arg(y, "out", io, shape, dev),
+              _arg(last, "last_state_out", torch.float32, (Bt, Dd), dev),
+              _arg(ckpt_out, "ckpt_out", torch.float32, gated_ckpt_shape(Bt, T, Dd), dev), Bt, T, Dd, _IO[io], pws,
+              0 if ws is None else ws.numel())
     _check(rc, "ssm_gated_scan_fwd")
     return (y, last) if return_last_state else y
 
@@ -549,77 +569,60 @@ def gated_scan_bwd(x, g, dout, z=None, gate_bias=None, h0=None, dlast=None, ckpt
     gated_scan_fwd(..., ckpt_out=) recorded on the same inputs; without it the
     call reads x and g once more."""
     lib = _lib.load()
-    if x.dtype not in _IO:
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO:
         raise ValueError("x must be float32 or bfloat16")
-    io, dev = x.dtype, x.device
-    Bt, T, Dd = x.shape
-    ldx, ldg = _rows(x, "x", io, x.shape), _rows(g, "g", io, x.shape)
-    ldz = _rows(z, "z", io, x.shape) if z is not None else 0
-    _dev(dout, "dout", io, x.shape)
-    _dev(gate_bias, "gate_bias", torch.float32, (Dd,))
-    _dev(h0, "h0", torch.float32, (Bt, Dd))
-    _dev(dlast, "dlast", torch.float32, (Bt, Dd))
-    _dev(ckpt, "ckpt", torch.float32, gated_ckpt_shape(Bt, T, Dd))
-    _on(dev, g=g, z=z, dout=dout, gate_bias=gate_bias, h0=h0, dlast=dlast, ckpt=ckpt)
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
-    grads = dict(dx=new(x.shape, io), dg=new(x.shape, io), dz=new(x.shape, io) if z is not None else None,
-                 dgate_bias=new((Dd,), torch.float32) if gate_bias is not None else None,
-                 dh0=new((Bt, Dd), torch.float32))
-    need = lib.ssm_gated_scan_bwd_workspace_bytes(Bt, T, Dd, _IO[io])
-    ws = _workspace(need, "ssm_gated_scan_bwd_workspace_bytes", workspace, dev)
-    rc = _run(dev, lib.ssm_gated_scan_bwd, _ptr(x), ldx, _ptr(g), ldg, _ptr(gate_bias), _ptr(z), ldz, _ptr(h0), _ptr(dout),
-              _ptr(dlast), _ptr(ckpt), _ptr(grads["dx"]), _ptr(grads["dg"]), _ptr(grads["dz"]),
-              _ptr(grads["dgate_bias"]), _ptr(grads["dh0"]), Bt, T, Dd, _IO[io], _ptr(ws), need)
+    Bt, T, Dd = shape
+    px, ldx = _rows(x, "x", io, shape, dev)
+    pg, ldg = _rows(g, "g", io, shape, dev)
+    pz, ldz = _rows(z, "z", io, shape, dev)
+    new = lambda size, dtype: torch.empty(size, dtype=dtype, device=dev)
+    dx, dg, dz = new(shape, io), new(shape, io), new(shape, io) if z is not None else None
+    dbias = new((Dd,), torch.float32) if gate_bias is not None else None
+    dh0 = new((Bt, Dd), torch.float32)
+    ws, pws = _scratch(lib.ssm_gated_scan_bwd_workspace_bytes(Bt, T, Dd, _IO[io]), "ssm_gated_scan_bwd_workspace_bytes",
+                       workspace, dev)
+    rc = _run(dev, lib.ssm_gated_scan_bwd, px, ldx, pg, ldg, _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev), pz,
+              ldz, _arg(h0, "h0", torch.float32, (Bt, Dd), dev), _arg(dout, "dout", io, shape, dev),
+              _arg(dlast, "dlast", torch.float32, (Bt, Dd), dev),
+              _arg(ckpt, "ckpt", torch.float32, gated_ckpt_shape(Bt, T, Dd), dev), _ptr(dx), _ptr(dg), _ptr(dz),
+              _ptr(dbias), _ptr(dh0), Bt, T, Dd, _IO[io], pws, 0 if ws is None else ws.numel())
     _check(rc, "ssm_gated_scan_bwd")
-    return grads
+    return dict(dx=dx, dg=dg, dz=dz, dgate_bias=dbias, dh0=dh0)
 
 
 def gated_state_update(state, x, g, z=None, gate_bias=None, out=None):
     """One decode token of gated_scan_fwd; `state` (batch, d_inner) fp32 is
     updated in place.  x, g, z: (batch, d_inner).  Returns y."""
     lib = _lib.load()
-    if x.dtype not in _IO:
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO:
         raise ValueError("x must be float32 or bfloat16")
-    io, dev = x.dtype, x.device
-    Bt, Dd = x.shape
-    _dev(x, "x", io)
-    _dev(g, "g", io, x.shape)
-    _dev(z, "z", io, x.shape)
-    _dev(state, "state", torch.float32, (Bt, Dd))
-    _dev(gate_bias, "gate_bias", torch.float32, (Dd,))
+    Bt, Dd = shape
+    px = _arg(x, "x", io, shape, dev)
     y = out if out is not None else torch.empty_like(x)
-    _dev(y, "out", io, x.shape)
-    _on(dev, state=state, g=g, z=z, gate_bias=gate_bias, out=y)
-    rc = _run(dev, lib.ssm_gated_state_update, _ptr(state), _ptr(x), _ptr(g), _ptr(gate_bias), _ptr(z), _ptr(y), Bt, Dd,
-              _IO[io])
+    rc = _run(dev, lib.ssm_gated_state_update, _arg(state, "state", torch.float32, shape, dev), px,
+              _arg(g, "g", io, shape, dev), _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev),
+              _arg(z, "z", io, shape, dev), _arg(y, "out", io, shape, dev), Bt, Dd, _IO[io])
     _check(rc, "ssm_gated_state_update")
     return y
 
 
-def _norm_args(x, weight, residual, residual_dtype, residual_out):
-    """(io, rows, dim, ldx, residual dtype, residual_out) of the two forwards."""
-    if x.dtype not in _IO:
-        raise ValueError("x must be float32 or bfloat16")
-    io, dev = x.dtype, x.device
-    if x.dim() < 1:
-        raise ValueError("x must have at least one axis")
-    dim = x.shape[-1]
-    rows = x.numel() // dim if dim else 0
-    ldx = _rows(x, "x", io, x.shape)
-    _dev(weight, "weight", torch.float32, (dim,))
+def _norm_residual(x, io, residual, residual_dtype, residual_out, dev):
+    """The residual's dtype, and the tensor that r goes to (None: r is x itself)."""
     if residual is not None:
         if residual_dtype is not None and residual_dtype != residual.dtype:
             raise ValueError("residual_dtype differs from residual's dtype")
-        residual_dtype = residual.dtype
-    res = residual_dtype if residual_dtype is not None else residual_out.dtype if residual_out is not None else io
-    if res not in (torch.float32, io):
+        res = residual.dtype
+    elif residual_dtype is not None:
+        res = residual_dtype
+    else:
+        res = residual_out.dtype if residual_out is not None else io
+    if res != io and res != torch.float32:
         raise ValueError(f"the residual must be float32 or {io}, got {res}")
-    _dev(residual, "residual", res, x.shape)
     if residual_out is None and (residual is not None or residual_dtype is not None):
         residual_out = torch.empty(x.shape, dtype=res, device=dev)
-    _dev(residual_out, "residual_out", res, x.shape)
-    _on(dev, weight=weight, residual=residual, residual_out=residual_out)
-    return io, rows, dim, ldx, res, residual_out
+    return res, residual_out
 
 
 def add_rms_norm(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=None, residual_out=None):
@@ -630,12 +633,16 @@ def add_rms_norm(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=No
     r is None, as it would be x itself).  residual_out may be residual, which is
     then updated in place."""
     lib = _lib.load()
-    io, rows, dim, ldx, res, r = _norm_args(x, weight, residual, residual_dtype, residual_out)
-    y = out if out is not None else torch.empty(x.shape, dtype=io, device=x.device)
-    _dev(y, "out", io, x.shape)
-    _on(x.device, out=y)
-    rc = _run(x.device, lib.ssm_add_rms_norm_fwd, _ptr(x), ldx, _ptr(residual), _ptr(weight), _ptr(y), _ptr(r), rows, dim,
-              eps, _IO[io], _IO[res])
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO or not shape:
+        raise ValueError("x must be float32 or bfloat16, with at least one axis")
+    dim = shape[-1]
+    px, ldx = _rows(x, "x", io, shape, dev)
+    res, r = _norm_residual(x, io, residual, residual_dtype, residual_out, dev)
+    y = out if out is not None else torch.empty(shape, dtype=io, device=dev)
+    rc = _run(dev, lib.ssm_add_rms_norm_fwd, px, ldx, _arg(residual, "residual", res, shape, dev),
+              _arg(weight, "weight", torch.float32, (dim,), dev), _arg(y, "out", io, shape, dev),
+              _arg(r, "residual_out", res, shape, dev), x.numel() // dim if dim else 0, dim, eps, _IO[io], _IO[res])
     _check(rc, "ssm_add_rms_norm_fwd")
     return y, r
 
@@ -646,14 +653,18 @@ def add_rms_norm_quant(x, weight, residual=None, eps=1e-5, residual_dtype=None, 
     float8_e4m3fn and scale (x.shape[:-1]) fp32 with q * scale standing for y,
     scale = max(max |y| / 448, 2^-126) per row."""
     lib = _lib.load()
-    io, rows, dim, ldx, res, r = _norm_args(x, weight, residual, residual_dtype, residual_out)
-    q = out if out is not None else torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    _dev(q, "out", torch.float8_e4m3fn, x.shape)
-    scale = scale_out if scale_out is not None else torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _dev(scale, "scale_out", torch.float32, x.shape[:-1])
-    _on(x.device, out=q, scale_out=scale)
-    rc = _run(x.device, lib.ssm_add_rms_norm_quant, _ptr(x), ldx, _ptr(residual), _ptr(weight), _ptr(q), _ptr(scale),
-              _ptr(r), rows, dim, eps, _IO[io], _IO[res])
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO or not shape:
+        raise ValueError("x must be float32 or bfloat16, with at least one axis")
+    dim = shape[-1]
+    px, ldx = _rows(x, "x", io, shape, dev)
+    res, r = _norm_residual(x, io, residual, residual_dtype, residual_out, dev)
+    q = out if out is not None else torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    scale = scale_out if scale_out is not None else torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rc = _run(dev, lib.ssm_add_rms_norm_quant, px, ldx, _arg(residual, "residual", res, shape, dev),
+              _arg(weight, "weight", torch.float32, (dim,), dev), _arg(q, "out", torch.float8_e4m3fn, shape, dev),
+              _arg(scale, "scale_out", torch.float32, shape[:-1], dev), _arg(r, "residual_out", res, shape, dev),
+              x.numel() // dim if dim else 0, dim, eps, _IO[io], _IO[res])
     _check(rc, "ssm_add_rms_norm_quant")
     return q, scale, r
 
@@ -666,44 +677,45 @@ def add_rms_norm_bwd(dy, r, weight, dresidual=None, eps=1e-5, dresidual_out=None
     the dtypes are the same, else in r's dtype) and dweight (dim,) fp32.
     dresidual_out: where dresidual goes, may be dresidual itself."""
     lib = _lib.load()
-    if dy.dtype not in _IO:
-        raise ValueError("dy must be float32 or bfloat16")
-    io, dev = dy.dtype, dy.device
-    res = r.dtype
-    if res not in (torch.float32, io):
+    io, dev, shape, res = dy.dtype, _device(dy, "dy"), dy.shape, r.dtype
+    if io not in _IO or not shape:
+        raise ValueError("dy must be float32 or bfloat16, with at least one axis")
+    if res != io and res != torch.float32:
         raise ValueError(f"r must be float32 or {io}, got {res}")
-    if dy.dim() < 1:
-        raise ValueError("dy must have at least one axis")
-    dim = dy.shape[-1]
+    dim = shape[-1]
     rows = dy.numel() // dim if dim else 0
-    _dev(dy, "dy", io)
-    _dev(r, "r", res, dy.shape)
-    _dev(weight, "weight", torch.float32, (dim,))
-    _dev(dresidual, "dresidual", res, dy.shape)
+    pdy = _arg(dy, "dy", io, shape, dev)
     dx = torch.empty_like(dy)
     own = dresidual_out if dresidual_out is not None else (torch.empty_like(r) if res != io else None)
-    _dev(own, "dresidual_out", res, dy.shape)
     dw = torch.empty((dim,), dtype=torch.float32, device=dev)
-    _on(dev, r=r, weight=weight, dresidual=dresidual, dresidual_out=own)
-    need = lib.ssm_add_rms_norm_bwd_workspace_bytes(rows, dim)
-    ws = _workspace(need, "ssm_add_rms_norm_bwd_workspace_bytes", workspace, dev)
-    rc = _run(dev, lib.ssm_add_rms_norm_bwd, _ptr(dy), _ptr(r), _ptr(weight), _ptr(dresidual), _ptr(dx), _ptr(own),
-              _ptr(dw), rows, dim, eps, _IO[io], _IO[res], _ptr(ws), need)
+    ws, pws = _scratch(lib.ssm_add_rms_norm_bwd_workspace_bytes(rows, dim), "ssm_add_rms_norm_bwd_workspace_bytes",
+                       workspace, dev)
+    rc = _run(dev, lib.ssm_add_rms_norm_bwd, pdy, _arg(r, "r", res, shape, dev),
+              _arg(weight, "weight", torch.float32, (dim,), dev), _arg(dresidual, "dresidual", res, shape, dev), _ptr(dx),
+              _arg(own, "dresidual_out", res, shape, dev), _ptr(dw), rows, dim, eps, _IO[io], _IO[res], pws,
+              0 if ws is None else ws.numel())
     _check(rc, "ssm_add_rms_norm_bwd")
     return dict(dx=dx, dresidual=dx if own is None else own, dweight=dw)
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _grad_list(tensors, name, dev):
-    """Host arrays (pointers, dtypes) of a list of tensors on dev."""
-    for t in tensors:
-        if t.dtype not in _IO:
-            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name} are on {t.device} and {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    """Host arrays (addresses, element counts, dtypes) of a list of tensors on dev."""
     n = len(tensors)
-    return (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int * n)(*[_IO[t.dtype] for t in tensors])
+    dtypes = list(map(_dtype_of, tensors))
+    kinds = set(dtypes)
+    if not kinds <= _IO.keys():
+        raise ValueError(f"{name} must be float32 or bfloat16, got {kinds}")
+    # get_device() is -1 for a CPU tensor
+    if set(map(torch.Tensor.get_device, tensors)) != {dev.index}:
+        raise ValueError(f"{name} must all be on {dev}")
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    codes = [_IO[dtypes[0]]] * n if len(kinds) == 1 else [_IO[d] for d in dtypes]
+    return ((ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, tensors)),
+            (ctypes.c_int64 * n)(*map(torch.Tensor.numel, tensors)), (ctypes.c_int * n)(*codes))
 
 
 def _clip(grads, max_norm, out, eps, norm_out, workspace):
@@ -711,29 +723,24 @@ def _clip(grads, max_norm, out, eps, norm_out, workspace):
     grads = list(grads)
     if not grads:
         raise ValueError("the list of gradients is empty")
-    dev = grads[0].device
-    if dev.type != "cuda":
-        raise ValueError("gradients must be GPU tensors")
-    ptrs, dtypes = _grad_list(grads, "gradients", dev)
+    dev = _device(grads[0], "every gradient")
     n = len(grads)
-    numel = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    ptrs, numel, dtypes = _grad_list(grads, "gradients", dev)
     norm = norm_out if norm_out is not None else torch.empty((), dtype=torch.float32, device=dev)
     if norm.numel() != 1:
         raise ValueError("norm_out must hold one value")
-    _dev(norm, "norm_out", torch.float32)
-    _on(dev, norm_out=norm)
-    need = lib.ssm_grad_norm_workspace_bytes(n)
-    ws = _workspace(need, "ssm_grad_norm_workspace_bytes", workspace, dev)
+    pn = _arg(norm, "norm_out", torch.float32, norm.shape, dev)
+    ws, pws = _scratch(lib.ssm_grad_norm_workspace_bytes(n), "ssm_grad_norm_workspace_bytes", workspace, dev)
     if max_norm is None:
-        _check(_run(dev, lib.ssm_grad_norm, ptrs, numel, dtypes, n, _ptr(norm), _ptr(ws), need), "ssm_grad_norm")
+        _check(_run(dev, lib.ssm_grad_norm, ptrs, numel, dtypes, n, pn, pws, ws.numel()), "ssm_grad_norm")
         return norm
     outs, out_dtypes = None, None
     if out is not None:
         out = list(out)
-        if [t.shape for t in out] != [t.shape for t in grads]:
+        if len(out) != n or any(o.shape != g.shape for o, g in zip(out, grads)):
             raise ValueError("out must have the gradients' shapes")
-        outs, out_dtypes = _grad_list(out, "out", dev)
-    rc = _run(dev, lib.ssm_grad_clip, ptrs, outs, numel, dtypes, out_dtypes, n, max_norm, eps, _ptr(norm), _ptr(ws), need)
+        outs, _, out_dtypes = _grad_list(out, "out", dev)
+    rc = _run(dev, lib.ssm_grad_clip, ptrs, outs, numel, dtypes, out_dtypes, n, max_norm, eps, pn, pws, ws.numel())
     _check(rc, "ssm_grad_clip")
     return norm
 
