@@ -30,7 +30,8 @@ int check_gated_sizes(int64_t batch, int64_t seqlen, int64_t dim, int io) {
     if (batch < 0 || seqlen < 0 || dim < 0 || batch > kMaxGridY) return SSM_ERR_SHAPE;
     if (mul3(batch, seqlen, dim) < 0 || mul3(batch, dim, 4) < 0) return SSM_ERR_SHAPE;
     // one block of steps is addressed with 32-bit byte offsets; the grid's lanes
-    // (up to 1024 per tile of 128 steps x 64 channels) are counted in 32 bits
+    // (up to 1024 per tile of 128 steps x 64 channels) are counted in 32 bits,
+    // which also keeps seqlen under 2^29
     if (mul3(ssm::kGatedBlock, dim, 4) < 0 || mul3(ssm::kGatedBlock, dim, 4) > kMaxSpan) return SSM_ERR_SHAPE;
     const int64_t tiles = mul3(batch, (dim + 63) / 64, (seqlen + ssm::kGatedBlock - 1) / ssm::kGatedBlock + 1);
     if (tiles < 0 || tiles >= (int64_t(1) << 22)) return SSM_ERR_SHAPE;

@@ -29,83 +29,89 @@ namespace ssm {
 namespace {
 
 constexpr int kBlock = kGatedBlock;        // steps of a tile
-constexpr int kGroup = 8;                  // tiles of a group
+constexpr int kGroup = 8;                  // tiles of a group, and groups of a state
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up
 constexpr uint32_t kReady = 0x80000000u;   // set in a published word: a decay is never negative
-#ifndef SSM_GATED_FWD_WAVES
-#define SSM_GATED_FWD_WAVES 8              // waves of a tile, forward and gradient
-#endif
-#ifndef SSM_GATED_BWD_WAVES
-#define SSM_GATED_BWD_WAVES 16
-#endif
+constexpr int kWaves = 8;                  // waves of a tile
 constexpr size_t kHeader = 256;            // ticket and error word
 
 // ------------------------------------------------------------------- gates
-// a = sigmoid(v) and 1 - a = sigmoid(-v) are carried as one number: the smaller
-// of the two, e / (1 + e) with e = exp(-|v|), with v's sign.  The larger is 1
-// minus it, rounded once, so neither a decay near 1 nor its complement loses
-// its leading digits.  An infinite v gives exactly 0 and 1.
-template <bool Precise> __device__ __forceinline__ float signed_gate(float v) {
-    float e, small;
-    if constexpr (Precise) {
-        // v log2(e) in two parts, as its rounding alone would cost |v| units in
-        // the last place; the quotient corrected by one Newton step
+// a = sigmoid(v) and s = 1 - a = sigmoid(-v) from e = exp(-|v|): the smaller of
+// the two is e / (1 + e), the larger 1 / (1 + e), so neither a decay near 1 nor
+// its complement loses its leading digits.  An infinite v gives exactly 0 and 1.
+struct Gate {
+    float a, s;
+};
+// fp32 io: a few ulp.  v log2(e) is taken in two parts, as its rounding alone
+// would cost |v| ulp; the quotient is corrected by one Newton step; the larger
+// side is 1 minus the smaller, rounded once: a biased decay near 1 would
+// compound over thousands of steps.
+struct PreciseGate {
+    static __device__ __forceinline__ float prep_bias(float b) { return b; }
+    static __device__ __forceinline__ Gate eval(float g, float bias) {
         constexpr float kLog2eLo = 1.925963033500411e-08f;   // log2(e) - float(log2(e))
+        const float v = g + bias;
         float av = fabsf(v);
         av = av > 128.0f ? 128.0f : av;                       // false for NaN, which stays
         const float t = av * kLog2e;
         const float lo = fmaf(av, kLog2eLo, fmaf(av, kLog2e, -t));
-        e = fast_exp2(-t);
+        float e = fast_exp2(-t);
         e = fmaf(e * -kLn2, lo, e);
         const float q = 1.0f + e, r = fast_rcp(q);
-        small = e * r;
+        float small = e * r;
         small = fmaf(fmaf(-q, small, e), r, small);
-    } else {
-        e = fast_exp2(-fabsf(v) * kLog2e);
-        small = e * fast_rcp(1.0f + e);
+        const float large = 1.0f - small;
+        return v < 0.0f ? Gate{small, large} : Gate{large, small};
     }
-    return copysignf(small, v);
-}
-struct Gate {
-    float a, s;
 };
-__device__ __forceinline__ Gate split(float sg) {
-    const float small = fabsf(sg), large = 1.0f - small;
-    const bool neg = static_cast<int>(__float_as_uint(sg)) < 0;
-    return {neg ? small : large, neg ? large : small};
-}
+// bf16 io: the hardware exponential and reciprocal as they are (1 ulp each, the
+// output rounds at 2^-9), log2(e) folded into the sum with the bias.
+struct FastGate {
+    static __device__ __forceinline__ float prep_bias(float b) { return b * kLog2e; }
+    static __device__ __forceinline__ Gate eval(float g, float bias) {
+        const float v = fmaf(g, kLog2e, bias);
+        const float e = fast_exp2(-fabsf(v));
+        const float r = fast_rcp(1.0f + e), small = e * r;
+        return v < 0.0f ? Gate{small, r} : Gate{r, small};
+    }
+};
+template <typename T> struct GateFor;
+template <> struct GateFor<float> { using type = PreciseGate; };
+template <> struct GateFor<bf16_t> { using type = FastGate; };
 
-// Makes the compiler take a register as new, so that what was derived from it
-// before a barrier is derived again after it (a few instructions) and not kept
-// in registers across.
+// Makes the compiler take a register as new: its value is computed here and not
+// sunk to where it is used, and what was derived from it before is derived again
+// and not kept.
 template <typename V> __device__ __forceinline__ void renew(V &v) { asm volatile("" : "+v"(v)); }
 
 // ------------------------------------------------- VEC channels of one row
 template <typename T, int VEC> struct Cell;
 template <> struct Cell<bf16_t, 2> {
     using raw = uint32_t;
-    static __device__ __forceinline__ raw load(rsrc_t r, uint32_t off) {
-        return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kStream);
+    static __device__ __forceinline__ raw load(rsrc_t r, uint32_t col, uint32_t row) {
+        return __builtin_amdgcn_raw_buffer_load_b32(r, col, row, kStream);
     }
     static __device__ __forceinline__ float get(raw v, int i) { return __uint_as_float(i ? (v & 0xffff0000u) : (v << 16)); }
-    static __device__ __forceinline__ void store(const float (&v)[2], rsrc_t r, uint32_t off) {
+    static __device__ __forceinline__ void store(const float (&v)[2], rsrc_t r, uint32_t col, uint32_t row) {
         const uint32_t lo = from_f32<bf16_t>(v[0]).bits, hi = from_f32<bf16_t>(v[1]).bits;
-        __builtin_amdgcn_raw_buffer_store_b32(lo | (hi << 16), r, off, 0, kStream);
+        __builtin_amdgcn_raw_buffer_store_b32(lo | (hi << 16), r, col, row, kStream);
     }
 };
 template <typename T> struct Cell<T, 1> {
     using raw = typename Io<T>::raw;
-    static __device__ __forceinline__ raw load(rsrc_t r, uint32_t off) { return Io<T>::template load<kStream>(r, off, 0); }
+    static __device__ __forceinline__ raw load(rsrc_t r, uint32_t col, uint32_t row) {
+        return Io<T>::template load<kStream>(r, col, row);
+    }
     static __device__ __forceinline__ float get(raw v, int) { return Io<T>::f32(v); }
-    static __device__ __forceinline__ void store(const float (&v)[1], rsrc_t r, uint32_t off) {
-        Io<T>::template store<kStream>(v[0], r, off, 0);
+    static __device__ __forceinline__ void store(const float (&v)[1], rsrc_t r, uint32_t col, uint32_t row) {
+        Io<T>::template store<kStream>(v[0], r, col, row);
     }
 };
 
 // --------------------------------------------------------------- hand-over
 struct Link {
     uint32_t *words;             // [0] ticket, [1] error
-    uint64_t *agg, *state;       // per (chain, tile) and per (chain, group): 64 VEC words each
+    uint64_t *agg, *group, *state;   // 64 VEC words per (chain, tile), (chain, group), (chain, 8 groups)
     uint32_t spin_limit;
     int publish;
 };
@@ -136,58 +142,99 @@ __device__ __forceinline__ float word_offset(uint64_t v) {
     return (static_cast<uint32_t>(v) & kReady) ? f : __builtin_nanf("");   // gave up: poison
 }
 
-// The carry entering tile k of a chain (k counts in scan order): `first` for
-// the chain's first group, else the published state of the group before, folded
-// over the group's tiles before k.  All W >= kGroup waves take part; `h` is the
-// result in every wave.  Publishes this tile's aggregate beforehand, and the
-// state leaving the group when k is its last tile.
-template <int W, int VEC>
-__device__ __forceinline__ void chain_carry(const Link &lk, int64_t chain, int n_tiles, int k, const float (&A)[VEC],
-                                            const float (&U)[VEC], const float (&first)[VEC],
-                                            float2 (*slot)[64 * VEC], int w, int lane, float (&h)[VEC]) {
-    static_assert(W >= kGroup, "one wave waits for one tile");
-    constexpr int kW = 64 * VEC;
-    const int in_group = k % kGroup, n_groups = (n_tiles + kGroup - 1) / kGroup;
-    uint64_t *mine = lk.agg + (chain * n_tiles + k) * kW;
-    uint64_t *states = lk.state + chain * n_groups * kW;
-    const bool more = k + 1 < n_tiles;
-    if (w == 0 && more && in_group != kGroup - 1 && lk.publish) {
+// Waits for the map of one published word per lane and channel.
+template <int VEC>
+__device__ __forceinline__ void wait_map(const uint64_t *p, const Link &lk, int lane, float2 *slot) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) publish_word(mine + e * 64 + lane, A[e], U[e]);
+    for (int e = 0; e < VEC; ++e) {
+        const uint64_t v = wait_word(p + e * 64 + lane, lk);
+        slot[e * 64 + lane] = make_float2(word_decay(v), word_offset(v));
     }
-    // wave w < in_group: the aggregate of the group's tile w; wave kGroup - 1: the
-    // state before the group
-    if (w < in_group) {
-        const uint64_t *p = lk.agg + (chain * n_tiles + (k - in_group + w)) * kW;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const uint64_t v = wait_word(p + e * 64 + lane, lk);
-            slot[w][e * 64 + lane] = make_float2(word_decay(v), word_offset(v));
-        }
-    } else if (w == kGroup - 1) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float s = first[e];
-            if (k >= kGroup) s = word_offset(wait_word(states + (k / kGroup - 1) * kW + e * 64 + lane, lk));
-            slot[w][e * 64 + lane] = make_float2(0.0f, s);
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = slot[kGroup - 1][e * 64 + lane].y;
-    for (int i = 0; i < in_group; ++i) {
+}
+// slot[0 .. n) composed onto (A, U), first to last
+template <int VEC>
+__device__ __forceinline__ void fold_maps(const float2 (*slot)[64 * VEC], int n, int lane, float (&A)[VEC], float (&U)[VEC]) {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float2 m = slot[i][e * 64 + lane];
-            h[e] = fmaf(m.x, h[e], m.y);
+            U[e] = fmaf(m.x, U[e], m.y);
+            A[e] *= m.x;
         }
     }
-    if (w == 0 && more && in_group == kGroup - 1 && lk.publish) {
+}
+
+// The carry entering tile k of a chain (k counts in scan order).  Three levels:
+// the tiles of a group of 8 publish their maps, the last tile of a group the
+// group's map, and the last tile of 8 groups the state leaving them.  So a tile
+// waits for at most 7 maps of tiles, 7 of groups and one state, each by a wave of
+// its own, and only the states form a chain, one link per 64 tiles.  (With group
+// states only, one link per 8 tiles, 65536 steps took 122 us.)
+// (A, U) is the tile's own map, known to the wave that `publishes`, `first` the
+// chain's initial carry, `h` the result, the same in every wave.
+template <int W, int VEC>
+__device__ __forceinline__ void chain_carry(const Link &lk, int64_t chain, int n_tiles, int k, const float (&A)[VEC],
+                                            const float (&U)[VEC], const float (&first)[VEC],
+                                            float2 (*slot)[64 * VEC], bool publishes, int w, int lane,
+                                            float (&h)[VEC]) {
+    static_assert(W >= kGroup, "one wave waits for one map of each level");
+    constexpr int kW = 64 * VEC, kSuper = kGroup * kGroup;
+    const int in_group = k % kGroup, group = k / kGroup, in_super = group % kGroup, super = k / kSuper;
+    const int n_groups = (n_tiles + kGroup - 1) / kGroup, n_supers = (n_tiles + kSuper - 1) / kSuper;
+    uint64_t *tiles = lk.agg + (chain * n_tiles + (k - in_group)) * kW;
+    uint64_t *groups = lk.group + (chain * n_groups + (group - in_super)) * kW;
+    uint64_t *states = lk.state + chain * n_supers * kW;
+    const bool more = k + 1 < n_tiles && lk.publish, last = in_group == kGroup - 1;
+    float2 (*slot_g)[64 * VEC] = slot + kGroup;
+    if (publishes && more && !last) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            publish_word(states + (k / kGroup) * kW + e * 64 + lane, 0.0f, fmaf(A[e], h[e], U[e]));
+        for (int e = 0; e < VEC; ++e) publish_word(tiles + in_group * kW + e * 64 + lane, A[e], U[e]);
+    }
+    if (w < in_group) wait_map<VEC>(tiles + w * kW, lk, lane, slot[w]);
+    if (last && in_super != kGroup - 1 && more) {    // the group's map, before anything else is waited for
+        __syncthreads();
+        if (publishes) {
+            float Ag[VEC], Ug[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                Ag[e] = 1.0f;
+                Ug[e] = 0.0f;
+            }
+            fold_maps<VEC>(slot, in_group, lane, Ag, Ug);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                publish_word(groups + in_super * kW + e * 64 + lane, Ag[e] * A[e], fmaf(A[e], Ug[e], U[e]));
+        }
+    }
+    if (w < in_super) wait_map<VEC>(groups + w * kW, lk, lane, slot_g[w]);
+    if (w == kGroup - 1 && super > 0) wait_map<VEC>(states + (super - 1) * kW, lk, lane, slot_g[kGroup - 1]);
+    __syncthreads();
+    float unused[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        h[e] = super > 0 ? slot_g[kGroup - 1][e * 64 + lane].y : first[e];
+        unused[e] = 0.0f;
+    }
+    fold_maps<VEC>(slot_g, in_super, lane, unused, h);
+    fold_maps<VEC>(slot, in_group, lane, unused, h);
+    if (publishes && last && in_super == kGroup - 1 && more) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) publish_word(states + super * kW + e * 64 + lane, 0.0f, fmaf(A[e], h[e], U[e]));
     }
 }
+
+// Row i of a wave's steps, in the scalar offset of its accesses: a step past the
+// sequence reads the last valid row again (its values are replaced) and its stores
+// are dropped by their lane offset, so both stay in range however the buffer unit
+// counts the scalar offset.  No lane register holds a row's address.
+struct RowPick {
+    int n;
+    __device__ __forceinline__ uint32_t operator()(int i) const {
+        const int last = (n > 1 ? n : 1) - 1;        // a maximum first: a clamped subtraction is not scalar
+        return static_cast<uint32_t>(i < last ? i : last);
+    }
+};
 
 // ----------------------------------------------------------------- forward
 struct FwdParams {
@@ -196,8 +243,7 @@ struct FwdParams {
     const float *bias, *h0;
     void *y;
     float *last, *ckpt;
-    int64_t seqlen;
-    int dim, n_ct, n_tiles;
+    int seqlen, dim, n_ct, n_tiles;
     uint32_t chains;             // batch x column tiles
     Link link;
 };
@@ -211,11 +257,11 @@ template <typename T> __device__ __forceinline__ rsrc_t rows_rsrc(const void *p,
 template <typename T, int VEC, int W, bool Z, bool Multi>
 __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     using C = Cell<T, VEC>;
+    using G = typename GateFor<T>::type;
     using raw = typename C::raw;
     constexpr int S = kBlock / W;
-    constexpr bool Precise = sizeof(T) == 4;
     __shared__ float2 sAgg[W][64 * VEC];
-    __shared__ float2 sLink[Multi ? kGroup : 1][64 * VEC];
+    __shared__ float2 sLink[Multi ? 2 * kGroup : 1][64 * VEC];
     __shared__ uint32_t sTicket;
 
     const int tid = threadIdx.x, lane = tid % 64;
@@ -228,50 +274,67 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     }
     const uint32_t chain = ticket % p.chains;
     const int k = static_cast<int>(ticket / p.chains);
-    const int64_t b = chain / p.n_ct;
-    const int c0 = static_cast<int>(chain % p.n_ct) * 64 * VEC;
+    const int b = static_cast<int>(chain / static_cast<uint32_t>(p.n_ct));
+    const int c0 = static_cast<int>(chain % static_cast<uint32_t>(p.n_ct)) * 64 * VEC;
     const int ch = c0 + lane * VEC;
     const bool active = ch < p.dim;
-    const int64_t t0 = static_cast<int64_t>(k) * kBlock + w * S;     // first step of the wave
-    const int64_t left = p.seqlen - t0;
-    const int n = static_cast<int>(left < 0 ? 0 : (left < S ? left : S));
-    const int64_t row = b * p.seqlen + t0;
+    const int t0 = k * kBlock + w * S;     // first step of the wave
+    const int left = p.seqlen - t0;                  // 32-bit: 64-bit compares would leave the scalar unit
+    const int n = left < 0 ? 0 : (left < S ? left : S);
+    const int64_t row = static_cast<int64_t>(b) * p.seqlen + t0;
 
     const uint32_t col = active ? static_cast<uint32_t>(lane * VEC * sizeof(T)) : kOffNone;
+    const RowPick at{n};
+    auto keep = [&](int i) { return i < n ? col : kOffNone; };
     const rsrc_t rx = rows_rsrc<T>(p.x, row, p.ldx, c0, p.dim, n), rg = rows_rsrc<T>(p.g, row, p.ldg, c0, p.dim, n);
     const uint32_t bx = static_cast<uint32_t>(p.ldx * sizeof(T)), bg = static_cast<uint32_t>(p.ldg * sizeof(T));
     raw xr[S], gr[S], zr[Z ? S : 1];
 #pragma unroll
-    for (int i = 0; i < S; ++i) gr[i] = C::load(rg, col + i * bg);
+    for (int i = 0; i < S; ++i) gr[i] = C::load(rg, col, at(i) * bg);
 #pragma unroll
-    for (int i = 0; i < S; ++i) xr[i] = C::load(rx, col + i * bx);
+    for (int i = 0; i < S; ++i) xr[i] = C::load(rx, col, at(i) * bx);
     if constexpr (Z) {
         const rsrc_t rz = rows_rsrc<T>(p.z, row, p.ldz, c0, p.dim, n);
         const uint32_t bz = static_cast<uint32_t>(p.ldz * sizeof(T));
 #pragma unroll
-        for (int i = 0; i < S; ++i) zr[i] = C::load(rz, col + i * bz);
+        for (int i = 0; i < S; ++i) zr[i] = C::load(rz, col, at(i) * bz);
     }
     float bias[VEC], first[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        bias[e] = (p.bias && active) ? p.bias[ch + e] : 0.0f;
-        first[e] = (p.h0 && active) ? p.h0[b * p.dim + ch + e] : 0.0f;
+        bias[e] = (p.bias && active) ? G::prep_bias(p.bias[ch + e]) : 0.0f;
+        first[e] = (p.h0 && active) ? p.h0[static_cast<int64_t>(b) * p.dim + ch + e] : 0.0f;
     }
 
     // discretise and fold; steps past the sequence are the identity
     float a[S][VEC], u[S][VEC], A[VEC], U[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        A[e] = 1.0f;
-        U[e] = 0.0f;
-    }
-#pragma unroll
     for (int i = 0; i < S; ++i) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const Gate q = split(signed_gate<Precise>(C::get(gr[i], e) + bias[e]));
-            a[i][e] = i < n ? q.a : 1.0f;
-            u[i][e] = i < n ? q.s * C::get(xr[i], e) : 0.0f;
+            const Gate q = G::eval(C::get(gr[i], e), bias[e]);
+            a[i][e] = q.a;
+            u[i][e] = q.s * C::get(xr[i], e);
+        }
+    }
+    if (n < S) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                a[i][e] = i < n ? a[i][e] : 1.0f;
+                u[i][e] = i < n ? u[i][e] : 0.0f;
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        A[e] = a[0][e];
+        U[e] = u[0][e];
+    }
+#pragma unroll
+    for (int i = 1; i < S; ++i) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
             U[e] = fmaf(a[i][e], U[e], u[i][e]);
             A[e] *= a[i][e];
         }
@@ -282,37 +345,34 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     float Ap[VEC], Up[VEC];                          // the waves before this one
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        A[e] = 1.0f;
-        U[e] = 0.0f;
+        Ap[e] = 1.0f;
+        Up[e] = 0.0f;
     }
-#pragma unroll 4
-    for (int i = 0; i < W; ++i) {
+    fold_maps<VEC>(sAgg, w, lane, Ap, Up);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (i == w) {
-                Ap[e] = A[e];
-                Up[e] = U[e];
-            }
-            const float2 m = sAgg[i][e * 64 + lane];
-            U[e] = fmaf(m.x, U[e], m.y);
-            A[e] *= m.x;
-        }
+    for (int e = 0; e < VEC; ++e) {                  // up to this wave's end; the last wave's is the tile's
+        U[e] = fmaf(A[e], Up[e], U[e]);
+        A[e] *= Ap[e];
     }
     float h[VEC];
     if constexpr (Multi) {
-        chain_carry<W, VEC>(p.link, chain, p.n_tiles, k, A, U, first, sLink, w, lane, h);
+        chain_carry<W, VEC>(p.link, chain, p.n_tiles, k, A, U, first, sLink, w == W - 1, w, lane, h);
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) h[e] = first[e];
     }
-    if (w == 0 && active) {
+    if (w == W - 1 && active) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            if (p.ckpt) p.ckpt[(b * p.n_tiles + k) * p.dim + ch + e] = h[e];
-            if (p.last && k + 1 == p.n_tiles) p.last[b * p.dim + ch + e] = fmaf(A[e], h[e], U[e]);
+            if (p.ckpt) p.ckpt[(static_cast<int64_t>(b) * p.n_tiles + k) * p.dim + ch + e] = h[e];
+            if (p.last && k + 1 == p.n_tiles) p.last[static_cast<int64_t>(b) * p.dim + ch + e] = fmaf(A[e], h[e], U[e]);
         }
     }
     if (!p.y) return;
+    if constexpr (Z) {                               // or SiLU(z) is held from before the carry, in twice the registers
+#pragma unroll
+        for (int i = 0; i < S; ++i) renew(zr[i]);
+    }
     const rsrc_t ry = rows_rsrc<T>(p.y, row, p.dim, c0, p.dim, n);
     const uint32_t by = static_cast<uint32_t>(p.dim * sizeof(T));
 #pragma unroll
@@ -325,7 +385,7 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
             h[e] = fmaf(a[i][e], h[e], u[i][e]);
             o[e] = Z ? h[e] * silu(C::get(zr[i], e)) : h[e];
         }
-        C::store(o, ry, col + i * by);
+        C::store(o, ry, keep(i), at(i) * by);
     }
 }
 
@@ -336,21 +396,23 @@ struct BwdParams {
     const float *bias, *ckpt, *dlast;
     void *dx, *dg, *dz;
     float *part, *dh0;           // part: dgate_bias of each (batch row, tile), or null
-    int64_t seqlen;
-    int dim, n_ct, n_tiles;
+    int seqlen, dim, n_ct, n_tiles;
     uint32_t chains;
     Link link;
 };
 
-template <typename T, int VEC, int W, bool Z, bool Multi>
+// One channel per lane: a step's values (a, 1 - a, x, the two factors of dout and
+// the state) take six registers per step and channel, and two workgroups per CU
+// overlap better than wider lanes at one (at the 130m layer 82 us against 97 us).
+template <typename T, int W, bool Z, bool Multi>
 __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
-    using C = Cell<T, VEC>;
+    using C = Cell<T, 1>;
+    using G = typename GateFor<T>::type;
     using raw = typename C::raw;
     constexpr int S = kBlock / W;
-    constexpr bool Precise = sizeof(T) == 4;
-    __shared__ float2 sAgg[W][64 * VEC];             // (A, U) of the waves, forward
-    __shared__ float sRev[W][64 * VEC];              // offset of the reverse map (its decay is A too)
-    __shared__ float2 sLink[Multi ? kGroup : 1][64 * VEC];
+    __shared__ float2 sAgg[W][64];                   // (A, U) of the waves, forward
+    __shared__ float2 sRev[W][64];                   // the reverse maps (the same A, R)
+    __shared__ float2 sLink[Multi ? 2 * kGroup : 1][64];
     __shared__ uint32_t sTicket;
 
     const int tid = threadIdx.x, lane = tid % 64;
@@ -364,179 +426,139 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     const uint32_t chain = ticket % p.chains;
     const int k = static_cast<int>(ticket / p.chains);               // in scan order: from the last tile down
     const int j = p.n_tiles - 1 - k;
-    const int64_t b = chain / p.n_ct;
-    const int c0 = static_cast<int>(chain % p.n_ct) * 64 * VEC;
-    const int ch = c0 + lane * VEC;
+    const int b = static_cast<int>(chain / static_cast<uint32_t>(p.n_ct));
+    const int c0 = static_cast<int>(chain % static_cast<uint32_t>(p.n_ct)) * 64;
+    const int ch = c0 + lane;
     const bool active = ch < p.dim;
-    const int64_t t0 = static_cast<int64_t>(j) * kBlock + w * S;
-    const int64_t left = p.seqlen - t0;
-    const int n = static_cast<int>(left < 0 ? 0 : (left < S ? left : S));
-    const int64_t row = b * p.seqlen + t0;
+    const int t0 = j * kBlock + w * S;
+    const int left = p.seqlen - t0;                  // 32-bit: 64-bit compares would leave the scalar unit
+    const int n = left < 0 ? 0 : (left < S ? left : S);
+    const int64_t row = static_cast<int64_t>(b) * p.seqlen + t0;
 
-    const uint32_t col = active ? static_cast<uint32_t>(lane * VEC * sizeof(T)) : kOffNone;
+    const uint32_t col = active ? static_cast<uint32_t>(lane * sizeof(T)) : kOffNone;
+    const RowPick at{n};
+    auto keep = [&](int i) { return i < n ? col : kOffNone; };
     const rsrc_t rx = rows_rsrc<T>(p.x, row, p.ldx, c0, p.dim, n), rg = rows_rsrc<T>(p.g, row, p.ldg, c0, p.dim, n);
     const rsrc_t rd = rows_rsrc<T>(p.dout, row, p.dim, c0, p.dim, n);
     const uint32_t bx = static_cast<uint32_t>(p.ldx * sizeof(T)), bg = static_cast<uint32_t>(p.ldg * sizeof(T));
     const uint32_t bd = static_cast<uint32_t>(p.dim * sizeof(T));
     raw xr[S], gr[S], dr[S], zr[Z ? S : 1];
 #pragma unroll
-    for (int i = 0; i < S; ++i) gr[i] = C::load(rg, col + i * bg);
+    for (int i = 0; i < S; ++i) gr[i] = C::load(rg, col, at(i) * bg);
 #pragma unroll
-    for (int i = 0; i < S; ++i) xr[i] = C::load(rx, col + i * bx);
+    for (int i = 0; i < S; ++i) xr[i] = C::load(rx, col, at(i) * bx);
     if constexpr (Z) {
         const rsrc_t rz = rows_rsrc<T>(p.z, row, p.ldz, c0, p.dim, n);
         const uint32_t bz = static_cast<uint32_t>(p.ldz * sizeof(T));
 #pragma unroll
-        for (int i = 0; i < S; ++i) zr[i] = C::load(rz, col + i * bz);
+        for (int i = 0; i < S; ++i) zr[i] = C::load(rz, col, at(i) * bz);
     }
 #pragma unroll
-    for (int i = 0; i < S; ++i) dr[i] = C::load(rd, col + i * bd);
-    float bias[VEC], first[VEC], h[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        bias[e] = (p.bias && active) ? p.bias[ch + e] : 0.0f;
-        first[e] = (p.dlast && active) ? p.dlast[b * p.dim + ch + e] : 0.0f;
-        h[e] = active ? p.ckpt[(b * p.n_tiles + j) * p.dim + ch + e] : 0.0f;
-    }
+    for (int i = 0; i < S; ++i) dr[i] = C::load(rd, col, at(i) * bd);
+    const float bias = (p.bias && active) ? G::prep_bias(p.bias[ch]) : 0.0f;
+    const float first[1] = {(p.dlast && active) ? p.dlast[static_cast<int64_t>(b) * p.dim + ch] : 0.0f};
+    float h = active ? p.ckpt[(static_cast<int64_t>(b) * p.n_tiles + j) * p.dim + ch] : 0.0f;
 
-    // the forward map of the wave's steps and, from its last step down, the
-    // offset of c -> a (d + c).  A step past the sequence is the identity: its
-    // gate is +inf (kept as 0), and its x and dout were read as 0.
-    float sg[S][VEC], A[VEC], U[VEC], R[VEC];
+    // The gates, x, and dout's factors: dh = dout SiLU(z) (dout without z) and
+    // dz / h = dout SiLU'(z), SiLU' = s + SiLU (1 - s) with s = sigmoid(z).  A
+    // step past the sequence is the identity: a = 1 and no gradient of its own.
+    float a[S], s[S], x[S], dh[S], dzh[Z ? S : 1];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        A[e] = 1.0f;
-        U[e] = 0.0f;
-        R[e] = 0.0f;
+    for (int i = 0; i < S; ++i) {
+        const Gate q = G::eval(C::get(gr[i], 0), bias);
+        a[i] = q.a;
+        s[i] = q.s;
+        x[i] = C::get(xr[i], 0);
     }
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float v = signed_gate<Precise>(C::get(gr[i], e) + bias[e]);
-            sg[i][e] = i < n ? v : 0.0f;
-            const Gate q = split(sg[i][e]);
-            U[e] = fmaf(q.a, U[e], q.s * C::get(xr[i], e));
-            A[e] *= q.a;
+        dh[i] = C::get(dr[i], 0);
+        if constexpr (Z) {
+            const float zv = C::get(zr[i], 0);
+            const Gate y = G::eval(zv, 0.0f);
+            const float sl = zv * y.a;
+            dzh[i] = dh[i] * fmaf(sl, y.s, y.a);
+            dh[i] *= sl;
+            renew(dzh[i]);                           // or its factors wait for the last loop in two registers
+            renew(dh[i]);
         }
     }
+    if (n < S) {
 #pragma unroll
-    for (int i = S - 1; i >= 0; --i) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float d = C::get(dr[i], e);
-            if constexpr (Z) d *= silu(C::get(zr[i], e));
-            R[e] = split(sg[i][e]).a * (d + R[e]);
+        for (int i = 0; i < S; ++i) {
+            a[i] = i < n ? a[i] : 1.0f;
+            s[i] = i < n ? s[i] : 0.0f;
+            x[i] = i < n ? x[i] : 0.0f;
+            dh[i] = i < n ? dh[i] : 0.0f;
         }
     }
+    // the forward map of the wave's steps, and the reverse map c -> a (dh + c)
+    // from its last step down
+    float A[1] = {a[0]}, U = s[0] * x[0], R[1] = {a[S - 1] * dh[S - 1]};
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        sAgg[w][e * 64 + lane] = make_float2(A[e], U[e]);
-        sRev[w][e * 64 + lane] = R[e];
+    for (int i = 1; i < S; ++i) {
+        U = fmaf(a[i], U, s[i] * x[i]);
+        A[0] *= a[i];
     }
+#pragma unroll
+    for (int i = S - 2; i >= 0; --i) R[0] = a[i] * (dh[i] + R[0]);
+    sAgg[w][lane] = make_float2(A[0], U);
+    sRev[w][lane] = make_float2(A[0], R[0]);
     __syncthreads();
-    float Ap[VEC], Rp[VEC];                          // the reverse map of the waves after this one
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        A[e] = 1.0f;
-        R[e] = 0.0f;
-    }
+    float Ap = 1.0f, Rp = 0.0f;                      // the reverse map of the waves after this one
 #pragma unroll 4
-    for (int i = W - 1; i >= 0; --i) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (i == w) {
-                Ap[e] = A[e];
-                Rp[e] = R[e];
-            }
-            const float m = sAgg[i][e * 64 + lane].x;
-            R[e] = fmaf(m, R[e], sRev[i][e * 64 + lane]);
-            A[e] *= m;
-        }
+    for (int i = W - 1; i > w; --i) {
+        const float2 m = sRev[i][lane];
+        Rp = fmaf(m.x, Rp, m.y);
+        Ap *= m.x;
     }
+    R[0] = fmaf(A[0], Rp, R[0]);                     // down to this wave's first step; wave 0's is the tile's
+    A[0] *= Ap;
 #pragma unroll 4
     for (int i = 0; i < w; ++i) {                    // the state entering this wave's steps
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float2 m = sAgg[i][e * 64 + lane];
-            h[e] = fmaf(m.x, h[e], m.y);
-        }
+        const float2 m = sAgg[i][lane];
+        h = fmaf(m.x, h, m.y);
     }
-    float c[VEC];
-    if constexpr (Multi) {
-        chain_carry<W, VEC>(p.link, chain, p.n_tiles, k, A, R, first, sLink, w, lane, c);
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) c[e] = first[e];
-    }
-    if (w == 0 && active && p.dh0 && j == 0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) p.dh0[b * p.dim + ch + e] = fmaf(A[e], c[e], R[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) c[e] = fmaf(Ap[e], c[e], Rp[e]);
+    float c[1];
+    if constexpr (Multi)
+        chain_carry<W, 1>(p.link, chain, p.n_tiles, k, A, R, first, sLink, w == 0, w, lane, c);
+    else
+        c[0] = first[0];
+    if (w == 0 && active && p.dh0 && j == 0) p.dh0[static_cast<int64_t>(b) * p.dim + ch] = fmaf(A[0], c[0], R[0]);
+    float cc = fmaf(Ap, c[0], Rp);
 
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        if constexpr (Z) renew(zr[i]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) renew(sg[i][e]);
-    }
-    float hb[S][VEC];                                // the state before each step
+    for (int i = 0; i < S; ++i) renew(x[i]);
+    float hb[S];                                     // the state before each step
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            hb[i][e] = h[e];
-            const Gate q = split(sg[i][e]);
-            h[e] = fmaf(q.a, h[e], q.s * C::get(xr[i], e));
-        }
+        hb[i] = h;
+        h = fmaf(a[i], h, s[i] * x[i]);
     }
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) renew(sg[i][e]);
     const rsrc_t wx = rows_rsrc<T>(p.dx, row, p.dim, c0, p.dim, n), wg = rows_rsrc<T>(p.dg, row, p.dim, c0, p.dim, n);
     const rsrc_t wz = rows_rsrc<T>(Z ? p.dz : p.dx, row, p.dim, c0, p.dim, n);
-    float db[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) db[e] = 0.0f;
+    float db = 0.0f;
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
-        float ox[VEC], og[VEC], oz[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const Gate q = split(sg[i][e]);
-            const float xv = C::get(xr[i], e);
-            float d = C::get(dr[i], e);
-            if constexpr (Z) {
-                const float zv = C::get(zr[i], e), hv = i + 1 < S ? hb[i + 1 < S ? i + 1 : i][e] : h[e];
-                const Gate y = split(signed_gate<Precise>(zv));
-                oz[e] = d * hv * (y.a * fmaf(zv, y.s, 1.0f));
-                d *= zv * y.a;
-            }
-            const float ev = d + c[e];
-            ox[e] = q.s * ev;
-            og[e] = ev * (hb[i][e] - xv) * (q.a * q.s);
-            db[e] += og[e];
-            c[e] = q.a * ev;
+        const float ev = dh[i] + cc;
+        const float ox[1] = {s[i] * ev}, og[1] = {ev * (hb[i] - x[i]) * (a[i] * s[i])};
+        db += og[0];
+        cc = a[i] * ev;
+        C::store(ox, wx, keep(i), at(i) * bd);
+        C::store(og, wg, keep(i), at(i) * bd);
+        if constexpr (Z) {
+            const float oz[1] = {dzh[i] * (i + 1 < S ? hb[i + 1 < S ? i + 1 : i] : h)};
+            C::store(oz, wz, keep(i), at(i) * bd);
         }
-        C::store(ox, wx, col + i * bd);
-        C::store(og, wg, col + i * bd);
-        if constexpr (Z) C::store(oz, wz, col + i * bd);
     }
     if (p.part) {                                    // the waves' sums, added in wave order
-        __syncthreads();                             // sRev was last read before the fold
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) sRev[w][e * 64 + lane] = db[e];
+        __syncthreads();                             // sRev was last read before the carry
+        sRev[w][lane].x = db;
         __syncthreads();
         if (w == 0 && active) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float s = 0.0f;
-                for (int i = 0; i < W; ++i) s += sRev[i][e * 64 + lane];
-                p.part[(b * p.n_tiles + j) * p.dim + ch + e] = s;
-            }
+            float sum = 0.0f;
+            for (int i = 0; i < W; ++i) sum += sRev[i][lane].x;
+            p.part[(static_cast<int64_t>(b) * p.n_tiles + j) * p.dim + ch] = sum;
         }
     }
 }
@@ -552,20 +574,24 @@ __global__ __launch_bounds__(256) void gated_copy_kernel(const float *in, float 
     if (i < n) out[i] = in ? in[i] : 0.0f;
 }
 
-__global__ __launch_bounds__(256) void gated_clear_kernel(uint64_t *p, int64_t n, uint32_t *words, int keep_error) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i == 0) {                                    // the header: ticket and error word
+// the hand-over words (16 bytes at a time) and the header: ticket, error word
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+__global__ __launch_bounds__(256) void gated_clear_kernel(u4 *p, int64_t n, uint32_t *words, int keep_error) {
+    const u4 zero = {0, 0, 0, 0};
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         words[0] = 0;
         if (!keep_error) words[1] = 0;
     }
-    if (i < n) p[i] = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+        p[i] = zero;
 }
 
 template <typename T> __global__ __launch_bounds__(256) void gated_update_kernel(GatedStepArgs p) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= p.batch * p.dim) return;
-    const float bias = p.gate_bias ? p.gate_bias[i % p.dim] : 0.0f;
-    const Gate k = split(signed_gate<sizeof(T) == 4>(to_f32(static_cast<const T *>(p.g)[i]) + bias));
+    using G = typename GateFor<T>::type;
+    const float bias = p.gate_bias ? G::prep_bias(p.gate_bias[i % p.dim]) : 0.0f;
+    const Gate k = G::eval(to_f32(static_cast<const T *>(p.g)[i]), bias);
     const float h = fmaf(k.a, p.state[i], k.s * to_f32(static_cast<const T *>(p.x)[i]));
     p.state[i] = h;
     static_cast<T *>(p.y)[i] = from_f32<T>(p.z ? h * silu(to_f32(static_cast<const T *>(p.z)[i])) : h);
@@ -577,17 +603,18 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // Sizes do not depend on the vector width: column tiles are counted in lanes of
 // one channel, of which a tile of 2 per lane takes two.
 struct Layout {
-    int64_t n_tiles, n_groups, cols;     // cols: d_inner rounded up to whole tiles
-    size_t agg, state, total;
+    int64_t n_tiles, cols;               // cols: d_inner rounded up to whole tiles
+    size_t agg, group, state, total;
 };
 Layout layout(int64_t batch, int64_t seqlen, int64_t dim) {
     Layout l;
     l.n_tiles = (seqlen + kBlock - 1) / kBlock;
-    l.n_groups = (l.n_tiles + kGroup - 1) / kGroup;
+    const int64_t n_groups = (l.n_tiles + kGroup - 1) / kGroup, n_supers = (n_groups + kGroup - 1) / kGroup;
     l.cols = (dim + 127) / 128 * 128;
     l.agg = kHeader;
-    l.state = l.agg + static_cast<size_t>(batch * l.cols * l.n_tiles) * 8;
-    l.total = l.n_tiles > 1 ? round256(l.state + static_cast<size_t>(batch * l.cols * l.n_groups) * 8) : 0;
+    l.group = l.agg + static_cast<size_t>(batch * l.cols * l.n_tiles) * 8;
+    l.state = l.group + static_cast<size_t>(batch * l.cols * n_groups) * 8;
+    l.total = l.n_tiles > 1 ? round256(l.state + static_cast<size_t>(batch * l.cols * n_supers) * 8) : 0;
     return l;
 }
 
@@ -596,49 +623,57 @@ Link make_link(const Layout &l, void *ws, uint32_t test_spin_limit) {
     Link k;
     k.words = reinterpret_cast<uint32_t *>(p);
     k.agg = reinterpret_cast<uint64_t *>(p + l.agg);
+    k.group = reinterpret_cast<uint64_t *>(p + l.group);
     k.state = reinterpret_cast<uint64_t *>(p + l.state);
     k.spin_limit = test_spin_limit ? test_spin_limit : kSpinLimit;
     k.publish = test_spin_limit ? 0 : 1;
     return k;
 }
 void clear(const Layout &l, const Link &k, bool keep_error, hipStream_t s) {
-    const int64_t n = static_cast<int64_t>((l.total - kHeader) / 8);
-    hipLaunchKernelGGL(gated_clear_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, k.agg, n,
-                       k.words, keep_error ? 1 : 0);
+    const int64_t n = static_cast<int64_t>((l.total - kHeader) / 16), wgs = (n + 255) / 256;
+    hipLaunchKernelGGL(gated_clear_kernel, dim3(static_cast<unsigned>(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s,
+                       reinterpret_cast<u4 *>(k.agg), n, k.words, keep_error ? 1 : 0);
 }
 
 bool even(const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 
-template <typename T, int VEC, int W> hipError_t launch_fwd(const GatedArgs &a, hipStream_t s) {
+template <typename T, int VEC> hipError_t launch_fwd(const GatedArgs &a, hipStream_t s) {
     const Layout l = layout(a.batch, a.seqlen, a.dim);
     FwdParams p{};
     p.x = a.x; p.g = a.g; p.z = a.z; p.ldx = a.ldx; p.ldg = a.ldg; p.ldz = a.ldz;
     p.bias = a.gate_bias; p.h0 = a.h0; p.y = a.y; p.last = a.last_state; p.ckpt = a.ckpt;
-    p.seqlen = a.seqlen; p.dim = static_cast<int>(a.dim);
+    p.seqlen = static_cast<int>(a.seqlen); p.dim = static_cast<int>(a.dim);
     p.n_ct = static_cast<int>((a.dim + 64 * VEC - 1) / (64 * VEC));
     p.n_tiles = static_cast<int>(l.n_tiles);
     p.chains = static_cast<uint32_t>(a.batch * p.n_ct);
-    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(W * 64);
+    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     const bool z = a.z && a.y;
     if (l.n_tiles > 1) {
         p.link = make_link(l, a.workspace, a.test_spin_limit);
         clear(l, p.link, false, s);
         if (z)
-            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, W, true, true>), grid, block, 0, s, p);
+            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, true, true>), grid, block, 0, s, p);
         else
-            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, W, false, true>), grid, block, 0, s, p);
+            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, false, true>), grid, block, 0, s, p);
     } else if (z) {
-        hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, W, true, false>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, true, false>), grid, block, 0, s, p);
     } else {
-        hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, W, false, false>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, false, false>), grid, block, 0, s, p);
     }
     return hipGetLastError();
+}
+
+// bf16 in pairs of channels where every row starts on 4 bytes
+hipError_t dispatch_fwd(const GatedArgs &a, hipStream_t s) {
+    if (!a.bf16) return launch_fwd<float, 1>(a, s);
+    const bool two = even(a.x, a.ldx) && even(a.g, a.ldg) && even(a.z, a.z ? a.ldz : 0) && even(a.y, a.dim);
+    return two ? launch_fwd<bf16_t, 2>(a, s) : launch_fwd<bf16_t, 1>(a, s);
 }
 
 // the partial sums and checkpoints of the gradient, behind the hand-over words
 size_t part_bytes(int64_t batch, int64_t n_tiles, int64_t dim) { return round256(static_cast<size_t>(batch * n_tiles * dim) * 4); }
 
-template <typename T, int VEC, int W> hipError_t launch_bwd(const GatedBwdArgs &a, hipStream_t s) {
+template <typename T> hipError_t launch_bwd(const GatedBwdArgs &a, hipStream_t s) {
     const GatedArgs &f = a.fwd;
     const Layout l = layout(f.batch, f.seqlen, f.dim);
     char *ws = static_cast<char *>(f.workspace);
@@ -648,28 +683,28 @@ template <typename T, int VEC, int W> hipError_t launch_bwd(const GatedBwdArgs &
     if (!a.ckpt) {                                   // the states entering the tiles, y unwritten
         GatedArgs q = f;
         q.y = nullptr; q.last_state = nullptr; q.ckpt = ckpt; q.z = nullptr;
-        if (hipError_t e = launch_fwd<T, VEC, SSM_GATED_FWD_WAVES>(q, s)) return e;
+        if (hipError_t e = dispatch_fwd(q, s)) return e;
     }
     p.x = f.x; p.g = f.g; p.z = f.z; p.dout = a.dout; p.ldx = f.ldx; p.ldg = f.ldg; p.ldz = f.ldz;
     p.bias = f.gate_bias; p.ckpt = a.ckpt ? a.ckpt : ckpt; p.dlast = a.dlast;
     p.dx = a.dx; p.dg = a.dg; p.dz = a.dz; p.dh0 = a.dh0;
     p.part = a.dgate_bias ? part : nullptr;
-    p.seqlen = f.seqlen; p.dim = static_cast<int>(f.dim);
-    p.n_ct = static_cast<int>((f.dim + 64 * VEC - 1) / (64 * VEC));
+    p.seqlen = static_cast<int>(f.seqlen); p.dim = static_cast<int>(f.dim);
+    p.n_ct = static_cast<int>((f.dim + 63) / 64);
     p.n_tiles = static_cast<int>(l.n_tiles);
     p.chains = static_cast<uint32_t>(f.batch * p.n_ct);
-    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(W * 64);
+    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     if (l.n_tiles > 1) {
         p.link = make_link(l, ws, f.test_spin_limit);
         clear(l, p.link, !a.ckpt, s);
         if (f.z)
-            hipLaunchKernelGGL((gated_bwd_kernel<T, VEC, W, true, true>), grid, block, 0, s, p);
+            hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, true, true>), grid, block, 0, s, p);
         else
-            hipLaunchKernelGGL((gated_bwd_kernel<T, VEC, W, false, true>), grid, block, 0, s, p);
+            hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, false, true>), grid, block, 0, s, p);
     } else if (f.z) {
-        hipLaunchKernelGGL((gated_bwd_kernel<T, VEC, W, true, false>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, true, false>), grid, block, 0, s, p);
     } else {
-        hipLaunchKernelGGL((gated_bwd_kernel<T, VEC, W, false, false>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, false, false>), grid, block, 0, s, p);
     }
     return hipGetLastError();
 }
@@ -684,7 +719,6 @@ size_t gated_scan_bwd_workspace(int64_t batch, int64_t seqlen, int64_t dim, int)
 }
 
 hipError_t launch_gated_scan(const GatedArgs &a, hipStream_t s) {
-    constexpr int W = SSM_GATED_FWD_WAVES;
     if (a.seqlen == 0) {
         const int64_t n = a.batch * a.dim;
         if (a.last_state)
@@ -692,19 +726,14 @@ hipError_t launch_gated_scan(const GatedArgs &a, hipStream_t s) {
                                a.last_state, n);
         return hipGetLastError();
     }
-    if (!a.bf16) return launch_fwd<float, 1, W>(a, s);
-    const bool two = even(a.x, a.ldx) && even(a.g, a.ldg) && even(a.z, a.z ? a.ldz : 0) && even(a.y, a.dim);
-    return two ? launch_fwd<bf16_t, 2, W>(a, s) : launch_fwd<bf16_t, 1, W>(a, s);
+    return dispatch_fwd(a, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s) {
-    constexpr int W = SSM_GATED_BWD_WAVES;
     const GatedArgs &f = a.fwd;
     hipError_t e = hipSuccess;
     if (f.batch > 0 && f.seqlen > 0) {
-        const bool two = even(f.x, f.ldx) && even(f.g, f.ldg) && even(f.z, f.z ? f.ldz : 0) && even(a.dout, f.dim) &&
-                         even(a.dx, f.dim) && even(a.dg, f.dim) && even(a.dz, f.dim);
-        e = !f.bf16 ? launch_bwd<float, 1, W>(a, s) : two ? launch_bwd<bf16_t, 2, W>(a, s) : launch_bwd<bf16_t, 1, W>(a, s);
+        e = f.bf16 ? launch_bwd<bf16_t>(a, s) : launch_bwd<float>(a, s);
     } else if (a.dh0 && f.batch > 0) {
         const int64_t n = f.batch * f.dim;
         hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, a.dlast,
