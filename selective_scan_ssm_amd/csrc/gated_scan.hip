@@ -33,7 +33,9 @@ constexpr int kGroup = 8;                  // tiles of a group, and groups of a 
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up
 constexpr uint32_t kReady = 0x80000000u;   // set in a published word: a decay is never negative
 constexpr int kWaves = 8;                  // waves of a tile
-constexpr size_t kHeader = 256;            // ticket and error word
+constexpr int kCounters = 8;               // ticket counters, each on a cache line of its own
+constexpr int kCounterWords = 32;          // counter c is word (c + 1) kCounterWords; word 1 is the error word
+constexpr size_t kHeader = 1280;
 
 // ------------------------------------------------------------------- gates
 // a = sigmoid(v) and s = 1 - a = sigmoid(-v) from e = exp(-|v|): the smaller of
@@ -110,15 +112,15 @@ template <typename T> struct Cell<T, 1> {
 
 // --------------------------------------------------------------- hand-over
 struct Link {
-    uint32_t *words;             // [0] ticket, [1] error
+    uint32_t *words;                 // the header: error word, ticket counters
     uint64_t *agg, *group, *state;   // 64 VEC words per (chain, tile), (chain, group), (chain, 8 groups)
     uint32_t spin_limit;
     int publish;
+    uint32_t counters;
 };
 
-// one word once it is ready; 0 when the wait gave up
-__device__ __forceinline__ uint64_t wait_word(const uint64_t *p, const Link &k) {
-    uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// one word (seen as v before) once it is ready; 0 when the wait gave up
+__device__ __forceinline__ uint64_t wait_word(const uint64_t *p, uint64_t v, const Link &k) {
     uint32_t spins = 0;
     while (!(static_cast<uint32_t>(v) & kReady)) {
         if (++spins > k.spin_limit) {
@@ -142,12 +144,71 @@ __device__ __forceinline__ float word_offset(uint64_t v) {
     return (static_cast<uint32_t>(v) & kReady) ? f : __builtin_nanf("");   // gave up: poison
 }
 
-// Waits for the map of one published word per lane and channel.
+// A workgroup's tile: chain and position k in scan order.  Tickets are taken in
+// order, so a tile only ever waits for tiles that are running or done, whatever
+// else runs on the GPU.  One counter serves one ticket in about 17 ns (a
+// 3072-tile pass that reads 200 MB took 58 us), so the chains are dealt to up to
+// eight counters (48 us) in runs of neighbours: with every eighth chain to a
+// counter the 2.8b layer took 258 us instead of 237, as workgroups then no longer
+// read neighbouring columns together.  Fewer counters where the shares would not
+// come out even (a short share runs ahead and leaves the rest to few workgroups).
+// A workgroup starts at the counter of its XCD's number and goes on to the next
+// when that one has no tiles left; as many workgroups as tiles: each finds one.
+struct Tile {
+    uint32_t chain;
+    int k;
+};
+__device__ __forceinline__ Tile take_tile(const Link &lk, uint32_t chains, int n_tiles, uint32_t (&shared)[2]) {
+    if (threadIdx.x == 0) {
+        const uint32_t n = lk.counters;                              // a power of two, at most `chains`
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint32_t c = (blockIdx.x + i) & (n - 1);
+            const uint32_t first = chains * c / n, mine = chains * (c + 1) / n - first;
+            const uint32_t t = atomicAdd(&lk.words[(c + 1) * kCounterWords], 1u);
+            const uint32_t k = t / mine;
+            if (k < static_cast<uint32_t>(n_tiles)) {
+                shared[0] = first + (t - k * mine);
+                shared[1] = k;
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    return {static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(shared[0])),
+            static_cast<int>(__builtin_amdgcn_readfirstlane(shared[1]))};
+}
+
+// Where a wave looks for the maps that its tile waits for: a tile of its own
+// group, a group of its own state's 8 groups (or, for the last wave, that state).
+// The first look is taken before the waves' folds: mostly the words are there by
+// then, and their round trip is hidden.
+template <int VEC> struct Ahead {
+    const uint64_t *tile, *group;                    // this wave's words, or null (uniform)
+    uint64_t *tiles, *groups, *states;               // of the chain, group and state at hand, to publish
+    uint64_t tv[VEC], gv[VEC];
+};
 template <int VEC>
-__device__ __forceinline__ void wait_map(const uint64_t *p, const Link &lk, int lane, float2 *slot) {
+__device__ __forceinline__ void look_ahead(Ahead<VEC> &q, const Link &lk, int64_t chain, int n_tiles, int k, int w, int lane) {
+    constexpr int kW = 64 * VEC, kSuper = kGroup * kGroup;
+    const int in_group = k % kGroup, group = k / kGroup, in_super = group % kGroup, super = k / kSuper;
+    const int n_groups = (n_tiles + kGroup - 1) / kGroup, n_supers = (n_tiles + kSuper - 1) / kSuper;
+    q.tiles = lk.agg + (chain * n_tiles + (k - in_group)) * kW;
+    q.groups = lk.group + (chain * n_groups + (group - in_super)) * kW;
+    q.states = lk.state + (chain * n_supers + super) * kW;
+    q.tile = w < in_group ? q.tiles + w * kW : nullptr;
+    q.group = w < in_super ? q.groups + w * kW : w == kGroup - 1 && super > 0 ? q.states - kW : nullptr;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        const uint64_t v = wait_word(p + e * 64 + lane, lk);
+        q.tv[e] = q.gv[e] = 0;
+        if (q.tile) q.tv[e] = __hip_atomic_load(q.tile + e * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (q.group) q.gv[e] = __hip_atomic_load(q.group + e * 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void wait_map(const uint64_t *p, const uint64_t (&seen)[VEC], const Link &lk, int lane, float2 *slot) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const uint64_t v = wait_word(p + e * 64 + lane, seen[e], lk);
         slot[e * 64 + lane] = make_float2(word_decay(v), word_offset(v));
     }
 }
@@ -174,24 +235,20 @@ __device__ __forceinline__ void fold_maps(const float2 (*slot)[64 * VEC], int n,
 // (A, U) is the tile's own map, known to the wave that `publishes`, `first` the
 // chain's initial carry, `h` the result, the same in every wave.
 template <int W, int VEC>
-__device__ __forceinline__ void chain_carry(const Link &lk, int64_t chain, int n_tiles, int k, const float (&A)[VEC],
+__device__ __forceinline__ void chain_carry(const Link &lk, const Ahead<VEC> &q, int n_tiles, int k, const float (&A)[VEC],
                                             const float (&U)[VEC], const float (&first)[VEC],
                                             float2 (*slot)[64 * VEC], bool publishes, int w, int lane,
                                             float (&h)[VEC]) {
     static_assert(W >= kGroup, "one wave waits for one map of each level");
     constexpr int kW = 64 * VEC, kSuper = kGroup * kGroup;
-    const int in_group = k % kGroup, group = k / kGroup, in_super = group % kGroup, super = k / kSuper;
-    const int n_groups = (n_tiles + kGroup - 1) / kGroup, n_supers = (n_tiles + kSuper - 1) / kSuper;
-    uint64_t *tiles = lk.agg + (chain * n_tiles + (k - in_group)) * kW;
-    uint64_t *groups = lk.group + (chain * n_groups + (group - in_super)) * kW;
-    uint64_t *states = lk.state + chain * n_supers * kW;
+    const int in_group = k % kGroup, in_super = k / kGroup % kGroup, super = k / kSuper;
     const bool more = k + 1 < n_tiles && lk.publish, last = in_group == kGroup - 1;
     float2 (*slot_g)[64 * VEC] = slot + kGroup;
     if (publishes && more && !last) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) publish_word(tiles + in_group * kW + e * 64 + lane, A[e], U[e]);
+        for (int e = 0; e < VEC; ++e) publish_word(q.tiles + in_group * kW + e * 64 + lane, A[e], U[e]);
     }
-    if (w < in_group) wait_map<VEC>(tiles + w * kW, lk, lane, slot[w]);
+    if (q.tile) wait_map<VEC>(q.tile, q.tv, lk, lane, slot[w]);
     if (last && in_super != kGroup - 1 && more) {    // the group's map, before anything else is waited for
         __syncthreads();
         if (publishes) {
@@ -204,11 +261,10 @@ __device__ __forceinline__ void chain_carry(const Link &lk, int64_t chain, int n
             fold_maps<VEC>(slot, in_group, lane, Ag, Ug);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                publish_word(groups + in_super * kW + e * 64 + lane, Ag[e] * A[e], fmaf(A[e], Ug[e], U[e]));
+                publish_word(q.groups + in_super * kW + e * 64 + lane, Ag[e] * A[e], fmaf(A[e], Ug[e], U[e]));
         }
     }
-    if (w < in_super) wait_map<VEC>(groups + w * kW, lk, lane, slot_g[w]);
-    if (w == kGroup - 1 && super > 0) wait_map<VEC>(states + (super - 1) * kW, lk, lane, slot_g[kGroup - 1]);
+    if (q.group) wait_map<VEC>(q.group, q.gv, lk, lane, slot_g[w]);
     __syncthreads();
     float unused[VEC];
 #pragma unroll
@@ -220,7 +276,7 @@ __device__ __forceinline__ void chain_carry(const Link &lk, int64_t chain, int n
     fold_maps<VEC>(slot, in_group, lane, unused, h);
     if (publishes && last && in_super == kGroup - 1 && more) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) publish_word(states + super * kW + e * 64 + lane, 0.0f, fmaf(A[e], h[e], U[e]));
+        for (int e = 0; e < VEC; ++e) publish_word(q.states + e * 64 + lane, 0.0f, fmaf(A[e], h[e], U[e]));
     }
 }
 
@@ -262,18 +318,14 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     constexpr int S = kBlock / W;
     __shared__ float2 sAgg[W][64 * VEC];
     __shared__ float2 sLink[Multi ? 2 * kGroup : 1][64 * VEC];
-    __shared__ uint32_t sTicket;
+    __shared__ uint32_t sTile[2];
 
     const int tid = threadIdx.x, lane = tid % 64;
     const int w = __builtin_amdgcn_readfirstlane(tid / 64);
-    uint32_t ticket = blockIdx.x;
-    if constexpr (Multi) {
-        if (tid == 0) sTicket = atomicAdd(&p.link.words[0], 1u);
-        __syncthreads();
-        ticket = __builtin_amdgcn_readfirstlane(sTicket);
-    }
-    const uint32_t chain = ticket % p.chains;
-    const int k = static_cast<int>(ticket / p.chains);
+    Tile tile{blockIdx.x, 0};
+    if constexpr (Multi) tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
+    const uint32_t chain = tile.chain;
+    const int k = tile.k;
     const int b = static_cast<int>(chain / static_cast<uint32_t>(p.n_ct));
     const int c0 = static_cast<int>(chain % static_cast<uint32_t>(p.n_ct)) * 64 * VEC;
     const int ch = c0 + lane * VEC;
@@ -326,6 +378,8 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
                 u[i][e] = i < n ? u[i][e] : 0.0f;
             }
     }
+    Ahead<VEC> ahead;
+    if constexpr (Multi) look_ahead<VEC>(ahead, p.link, chain, p.n_tiles, k, w, lane);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         A[e] = a[0][e];
@@ -356,7 +410,7 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     }
     float h[VEC];
     if constexpr (Multi) {
-        chain_carry<W, VEC>(p.link, chain, p.n_tiles, k, A, U, first, sLink, w == W - 1, w, lane, h);
+        chain_carry<W, VEC>(p.link, ahead, p.n_tiles, k, A, U, first, sLink, w == W - 1, w, lane, h);
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) h[e] = first[e];
@@ -413,18 +467,14 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     __shared__ float2 sAgg[W][64];                   // (A, U) of the waves, forward
     __shared__ float2 sRev[W][64];                   // the reverse maps (the same A, R)
     __shared__ float2 sLink[Multi ? 2 * kGroup : 1][64];
-    __shared__ uint32_t sTicket;
+    __shared__ uint32_t sTile[2];
 
     const int tid = threadIdx.x, lane = tid % 64;
     const int w = __builtin_amdgcn_readfirstlane(tid / 64);
-    uint32_t ticket = blockIdx.x;
-    if constexpr (Multi) {
-        if (tid == 0) sTicket = atomicAdd(&p.link.words[0], 1u);
-        __syncthreads();
-        ticket = __builtin_amdgcn_readfirstlane(sTicket);
-    }
-    const uint32_t chain = ticket % p.chains;
-    const int k = static_cast<int>(ticket / p.chains);               // in scan order: from the last tile down
+    Tile tile{blockIdx.x, 0};
+    if constexpr (Multi) tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
+    const uint32_t chain = tile.chain;
+    const int k = tile.k;                            // in scan order: from the last tile down
     const int j = p.n_tiles - 1 - k;
     const int b = static_cast<int>(chain / static_cast<uint32_t>(p.n_ct));
     const int c0 = static_cast<int>(chain % static_cast<uint32_t>(p.n_ct)) * 64;
@@ -492,6 +542,8 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
             dh[i] = i < n ? dh[i] : 0.0f;
         }
     }
+    Ahead<1> ahead;
+    if constexpr (Multi) look_ahead<1>(ahead, p.link, chain, p.n_tiles, k, w, lane);
     // the forward map of the wave's steps, and the reverse map c -> a (dh + c)
     // from its last step down
     float A[1] = {a[0]}, U = s[0] * x[0], R[1] = {a[S - 1] * dh[S - 1]};
@@ -521,7 +573,7 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     }
     float c[1];
     if constexpr (Multi)
-        chain_carry<W, 1>(p.link, chain, p.n_tiles, k, A, R, first, sLink, w == 0, w, lane, c);
+        chain_carry<W, 1>(p.link, ahead, p.n_tiles, k, A, R, first, sLink, w == 0, w, lane, c);
     else
         c[0] = first[0];
     if (w == 0 && active && p.dh0 && j == 0) p.dh0[static_cast<int64_t>(b) * p.dim + ch] = fmaf(A[0], c[0], R[0]);
@@ -574,14 +626,13 @@ __global__ __launch_bounds__(256) void gated_copy_kernel(const float *in, float 
     if (i < n) out[i] = in ? in[i] : 0.0f;
 }
 
-// the hand-over words (16 bytes at a time) and the header: ticket, error word
+// the hand-over words (16 bytes at a time) and the header: error word, ticket counters
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 __global__ __launch_bounds__(256) void gated_clear_kernel(u4 *p, int64_t n, uint32_t *words, int keep_error) {
     const u4 zero = {0, 0, 0, 0};
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        words[0] = 0;
-        if (!keep_error) words[1] = 0;
-    }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < static_cast<int>(kHeader / 4); i += 256)
+            if (!(keep_error && i == 1)) words[i] = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
         p[i] = zero;
 }
@@ -618,9 +669,14 @@ Layout layout(int64_t batch, int64_t seqlen, int64_t dim) {
     return l;
 }
 
-Link make_link(const Layout &l, void *ws, uint32_t test_spin_limit) {
+Link make_link(const Layout &l, void *ws, uint32_t chains, uint32_t test_spin_limit) {
     char *p = static_cast<char *>(ws);
     Link k;
+    // shares of at least 6 chains (12 chains on four counters: 127 us for 65536
+    // steps, on two: 122 us), and even ones below 20
+    k.counters = kCounters;
+    while (k.counters > 1 && (chains < 6 * k.counters || (chains % k.counters != 0 && chains < 20 * k.counters)))
+        k.counters /= 2;
     k.words = reinterpret_cast<uint32_t *>(p);
     k.agg = reinterpret_cast<uint64_t *>(p + l.agg);
     k.group = reinterpret_cast<uint64_t *>(p + l.group);
@@ -649,7 +705,7 @@ template <typename T, int VEC> hipError_t launch_fwd(const GatedArgs &a, hipStre
     const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     const bool z = a.z && a.y;
     if (l.n_tiles > 1) {
-        p.link = make_link(l, a.workspace, a.test_spin_limit);
+        p.link = make_link(l, a.workspace, p.chains, a.test_spin_limit);
         clear(l, p.link, false, s);
         if (z)
             hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, true, true>), grid, block, 0, s, p);
@@ -695,7 +751,7 @@ template <typename T> hipError_t launch_bwd(const GatedBwdArgs &a, hipStream_t s
     p.chains = static_cast<uint32_t>(f.batch * p.n_ct);
     const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     if (l.n_tiles > 1) {
-        p.link = make_link(l, ws, f.test_spin_limit);
+        p.link = make_link(l, ws, p.chains, f.test_spin_limit);
         clear(l, p.link, !a.ckpt, s);
         if (f.z)
             hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, true, true>), grid, block, 0, s, p);
