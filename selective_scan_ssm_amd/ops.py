@@ -7,7 +7,7 @@ RuntimeError.  Every step of the computation runs in the library's kernels.
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import operator
 from typing import Optional
 
@@ -474,6 +474,15 @@ def _arg(t, name, dtype, shape, dev):
     return t.data_ptr()
 
 
+def _out(t, name, like, dtype, shape, dev):
+    """The caller's output tensor, or a new one of like's shape; and its address."""
+    if t is not None:
+        return t, _arg(t, name, dtype, shape, dev)
+    # empty_like is the cheapest allocation, but keeps a strided tensor's gaps
+    t = torch.empty_like(like, dtype=dtype) if like.is_contiguous() else torch.empty(shape, dtype=dtype, device=dev)
+    return t, t.data_ptr()
+
+
 def _rows(t, name, dtype, shape, dev):
     """The address of t and the stride between its consecutive rows: its last
     axis is contiguous and its other axes step evenly (a column range of a
@@ -546,14 +555,14 @@ def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=Fals
     px, ldx = _rows(x, "x", io, shape, dev)
     pg, ldg = _rows(g, "g", io, shape, dev)
     pz, ldz = _rows(z, "z", io, shape, dev)
-    y = out if out is not None else torch.empty(shape, dtype=io, device=dev)
+    y, py = _out(out, "out", x, io, shape, dev)
     last = None
     if return_last_state:
         last = last_state_out if last_state_out is not None else torch.empty((Bt, Dd), dtype=torch.float32, device=dev)
     ws, pws = _scratch(lib.ssm_gated_scan_workspace_bytes(Bt, T, Dd, _IO[io]), "ssm_gated_scan_workspace_bytes",
                        workspace, dev)
     rc = _run(dev, lib.ssm_gated_scan_fwd, px, ldx, pg, ldg, _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev), pz,
-              ldz, _arg(h0, "h0", torch.float32, (Bt, Dd), dev), _arg(y, "out", io, shape, dev),
+              ldz, _arg(h0, "h0", torch.float32, (Bt, Dd), dev), py,
               _arg(last, "last_state_out", torch.float32, (Bt, Dd), dev),
               _arg(ckpt_out, "ckpt_out", torch.float32, gated_ckpt_shape(Bt, T, Dd), dev), Bt, T, Dd, _IO[io], pws,
               0 if ws is None else ws.numel())
@@ -600,16 +609,17 @@ def gated_state_update(state, x, g, z=None, gate_bias=None, out=None):
         raise ValueError("x must be float32 or bfloat16")
     Bt, Dd = shape
     px = _arg(x, "x", io, shape, dev)
-    y = out if out is not None else torch.empty_like(x)
+    y, py = _out(out, "out", x, io, shape, dev)
     rc = _run(dev, lib.ssm_gated_state_update, _arg(state, "state", torch.float32, shape, dev), px,
               _arg(g, "g", io, shape, dev), _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev),
-              _arg(z, "z", io, shape, dev), _arg(y, "out", io, shape, dev), Bt, Dd, _IO[io])
+              _arg(z, "z", io, shape, dev), py, Bt, Dd, _IO[io])
     _check(rc, "ssm_gated_state_update")
     return y
 
 
 def _norm_residual(x, io, residual, residual_dtype, residual_out, dev):
-    """The residual's dtype, and the tensor that r goes to (None: r is x itself)."""
+    """The residual's dtype and address, the tensor that r goes to (None: r is x
+    itself) and its address."""
     if residual is not None:
         if residual_dtype is not None and residual_dtype != residual.dtype:
             raise ValueError("residual_dtype differs from residual's dtype")
@@ -620,9 +630,12 @@ def _norm_residual(x, io, residual, residual_dtype, residual_out, dev):
         res = residual_out.dtype if residual_out is not None else io
     if res != io and res != torch.float32:
         raise ValueError(f"the residual must be float32 or {io}, got {res}")
-    if residual_out is None and (residual is not None or residual_dtype is not None):
-        residual_out = torch.empty(x.shape, dtype=res, device=dev)
-    return res, residual_out
+    shape = x.shape
+    pr = _arg(residual, "residual", res, shape, dev)
+    if residual is None and residual_dtype is None and residual_out is None:
+        return res, None, None, None
+    r, po = _out(residual_out, "residual_out", x if residual is None else residual, res, shape, dev)
+    return res, pr, r, po
 
 
 def add_rms_norm(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=None, residual_out=None):
@@ -638,11 +651,10 @@ def add_rms_norm(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=No
         raise ValueError("x must be float32 or bfloat16, with at least one axis")
     dim = shape[-1]
     px, ldx = _rows(x, "x", io, shape, dev)
-    res, r = _norm_residual(x, io, residual, residual_dtype, residual_out, dev)
-    y = out if out is not None else torch.empty(shape, dtype=io, device=dev)
-    rc = _run(dev, lib.ssm_add_rms_norm_fwd, px, ldx, _arg(residual, "residual", res, shape, dev),
-              _arg(weight, "weight", torch.float32, (dim,), dev), _arg(y, "out", io, shape, dev),
-              _arg(r, "residual_out", res, shape, dev), x.numel() // dim if dim else 0, dim, eps, _IO[io], _IO[res])
+    res, pr, r, po = _norm_residual(x, io, residual, residual_dtype, residual_out, dev)
+    y, py = _out(out, "out", x, io, shape, dev)
+    rc = _run(dev, lib.ssm_add_rms_norm_fwd, px, ldx, pr, _arg(weight, "weight", torch.float32, (dim,), dev), py, po,
+              x.numel() // dim if dim else 0, dim, eps, _IO[io], _IO[res])
     _check(rc, "ssm_add_rms_norm_fwd")
     return y, r
 
@@ -658,13 +670,12 @@ def add_rms_norm_quant(x, weight, residual=None, eps=1e-5, residual_dtype=None, 
         raise ValueError("x must be float32 or bfloat16, with at least one axis")
     dim = shape[-1]
     px, ldx = _rows(x, "x", io, shape, dev)
-    res, r = _norm_residual(x, io, residual, residual_dtype, residual_out, dev)
-    q = out if out is not None else torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    res, pr, r, po = _norm_residual(x, io, residual, residual_dtype, residual_out, dev)
+    q, pq = _out(out, "out", x, torch.float8_e4m3fn, shape, dev)
     scale = scale_out if scale_out is not None else torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    rc = _run(dev, lib.ssm_add_rms_norm_quant, px, ldx, _arg(residual, "residual", res, shape, dev),
-              _arg(weight, "weight", torch.float32, (dim,), dev), _arg(q, "out", torch.float8_e4m3fn, shape, dev),
-              _arg(scale, "scale_out", torch.float32, shape[:-1], dev), _arg(r, "residual_out", res, shape, dev),
-              x.numel() // dim if dim else 0, dim, eps, _IO[io], _IO[res])
+    rc = _run(dev, lib.ssm_add_rms_norm_quant, px, ldx, pr, _arg(weight, "weight", torch.float32, (dim,), dev), pq,
+              _arg(scale, "scale_out", torch.float32, shape[:-1], dev), po, x.numel() // dim if dim else 0, dim, eps,
+              _IO[io], _IO[res])
     _check(rc, "ssm_add_rms_norm_quant")
     return q, scale, r
 
@@ -702,10 +713,10 @@ _dtype_of = operator.attrgetter("dtype")
 
 
 def _grad_list(tensors, name, dev):
-    """Host arrays (addresses, element counts, dtypes) of a list of tensors on dev."""
-    n = len(tensors)
-    dtypes = list(map(_dtype_of, tensors))
-    kinds = set(dtypes)
+    """Host arrays (addresses, dtypes) of a list of contiguous tensors on dev.
+    A few hundred tensors cost more here than on the GPU, so every attribute is
+    read in one C-level pass."""
+    kinds = set(map(_dtype_of, tensors))
     if not kinds <= _IO.keys():
         raise ValueError(f"{name} must be float32 or bfloat16, got {kinds}")
     # get_device() is -1 for a CPU tensor
@@ -713,9 +724,16 @@ def _grad_list(tensors, name, dev):
         raise ValueError(f"{name} must all be on {dev}")
     if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    codes = [_IO[dtypes[0]]] * n if len(kinds) == 1 else [_IO[d] for d in dtypes]
-    return ((ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, tensors)),
-            (ctypes.c_int64 * n)(*map(torch.Tensor.numel, tensors)), (ctypes.c_int * n)(*codes))
+    if len(kinds) == 1:
+        codes = array.array("i", (_IO[kinds.pop()],)) * len(tensors)
+    else:
+        codes = array.array("i", map(_IO.__getitem__, map(_dtype_of, tensors)))
+    return array.array("Q", map(torch.Tensor.data_ptr, tensors)), codes
+
+
+def _at(host):
+    """The address of a host array."""
+    return host.buffer_info()[0]
 
 
 def _clip(grads, max_norm, out, eps, norm_out, workspace):
@@ -725,22 +743,26 @@ def _clip(grads, max_norm, out, eps, norm_out, workspace):
         raise ValueError("the list of gradients is empty")
     dev = _device(grads[0], "every gradient")
     n = len(grads)
-    ptrs, numel, dtypes = _grad_list(grads, "gradients", dev)
+    ptrs, dtypes = _grad_list(grads, "gradients", dev)
+    sizes = list(map(torch.Tensor.numel, grads))
+    numel = array.array("q", sizes)
     norm = norm_out if norm_out is not None else torch.empty((), dtype=torch.float32, device=dev)
     if norm.numel() != 1:
         raise ValueError("norm_out must hold one value")
     pn = _arg(norm, "norm_out", torch.float32, norm.shape, dev)
     ws, pws = _scratch(lib.ssm_grad_norm_workspace_bytes(n), "ssm_grad_norm_workspace_bytes", workspace, dev)
     if max_norm is None:
-        _check(_run(dev, lib.ssm_grad_norm, ptrs, numel, dtypes, n, pn, pws, ws.numel()), "ssm_grad_norm")
+        rc = _run(dev, lib.ssm_grad_norm, _at(ptrs), _at(numel), _at(dtypes), n, pn, pws, ws.numel())
+        _check(rc, "ssm_grad_norm")
         return norm
-    outs, out_dtypes = None, None
+    outs = out_dtypes = None
     if out is not None:
         out = list(out)
-        if len(out) != n or any(o.shape != g.shape for o, g in zip(out, grads)):
-            raise ValueError("out must have the gradients' shapes")
-        outs, _, out_dtypes = _grad_list(out, "out", dev)
-    rc = _run(dev, lib.ssm_grad_clip, ptrs, outs, numel, dtypes, out_dtypes, n, max_norm, eps, pn, pws, ws.numel())
+        if list(map(torch.Tensor.numel, out)) != sizes:
+            raise ValueError("out must have the gradients' sizes")
+        outs, out_dtypes = _grad_list(out, "out", dev)
+    rc = _run(dev, lib.ssm_grad_clip, _at(ptrs), None if outs is None else _at(outs), _at(numel), _at(dtypes),
+              None if outs is None else _at(out_dtypes), n, max_norm, eps, pn, pws, ws.numel())
     _check(rc, "ssm_grad_clip")
     return norm
 
@@ -754,7 +776,7 @@ def grad_norm(grads, norm_out=None, workspace=None):
 def clip_grads(grads, max_norm, out=None, eps=1e-6, norm_out=None, workspace=None):
     """Scales a list of contiguous fp32 / bf16 tensors by min(1, max_norm /
     (norm + eps)), norm being grad_norm(grads): in place, or into the tensors
-    of `out` (same shapes, fp32 or bf16 each: an optimizer's fp32 gradients
+    of `out` (same numbers of elements, fp32 or bf16 each: an optimizer's fp32 gradients
     from bf16 ones).  Returns the norm before clipping.  The host never waits."""
     if max_norm is None:
         raise ValueError("max_norm must be a number")
