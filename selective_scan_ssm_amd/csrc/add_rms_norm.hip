@@ -5,12 +5,11 @@
 //
 // HBM-bound: a row is read once, kept in registers across the reduction(s), and
 // written once.  R waves share a row (1 where a row fits one wave's registers)
-// and each lane holds P chunks of V consecutive elements (V = 8: 16-byte
-// accesses; V = 1 where the width or an address does not allow them), so
-// nothing but the reduction crosses lanes.  Waves walk the rows with a grid
-// stride and keep the weight in registers; the gradient also keeps its lane's
-// share of dw there, and one partial sum per workgroup goes through the
-// workspace.
+// and each lane holds P chunks of V consecutive elements (16 bytes of the widest
+// tensor; V = 1 where the width or an address does not allow that), so nothing
+// but the reduction crosses lanes.  Waves walk the rows with a grid stride and
+// keep the weight in registers; the gradient also keeps its lane's share of dw
+// there, and one partial sum per workgroup goes through the workspace.
 #include "column_sum.h"
 #include "ssm_device.h"
 #include "ssm_kernels.h"
@@ -62,20 +61,41 @@ template <> struct Chunk<bf16_t, 8> {
         __builtin_amdgcn_raw_buffer_store_b128(q, r, e * 2, 0, kStream);
     }
 };
-template <> struct Chunk<float, 8> {
-    u4 q[2];
-    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) {
-        q[0] = __builtin_amdgcn_raw_buffer_load_b128(r, e * 4, 0, kStream);
-        q[1] = __builtin_amdgcn_raw_buffer_load_b128(r, e * 4 + 16, 0, kStream);
+template <> struct Chunk<bf16_t, 4> {
+    u2 q;
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) { q = __builtin_amdgcn_raw_buffer_load_b64(r, e * 2, 0, kStream); }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i % 2 ? (q[i / 2] & 0xffff0000u) : (q[i / 2] << 16));
     }
-    __device__ __forceinline__ float get(int i) const { return __uint_as_float(q[i / 4][i % 4]); }
     static __device__ __forceinline__ void store(const float *v, rsrc_t r, uint32_t e) {
+        u2 q;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const u4 q = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
-                          __float_as_uint(v[4 * h + 3])};
-            __builtin_amdgcn_raw_buffer_store_b128(q, r, e * 4 + 16 * h, 0, kStream);
-        }
+        for (int i = 0; i < 2; ++i)
+            q[i] = static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i]).bits) |
+                   (static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i + 1]).bits) << 16);
+        __builtin_amdgcn_raw_buffer_store_b64(q, r, e * 2, 0, kStream);
+    }
+};
+template <> struct Chunk<float, 4> {
+    u4 q;
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) { q = __builtin_amdgcn_raw_buffer_load_b128(r, e * 4, 0, kStream); }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(q[i]); }
+    static __device__ __forceinline__ void store(const float *v, rsrc_t r, uint32_t e) {
+        const u4 q = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        __builtin_amdgcn_raw_buffer_store_b128(q, r, e * 4, 0, kStream);
+    }
+};
+// the weight and its gradient beside eight bf16 values: two accesses of 16 bytes
+template <> struct Chunk<float, 8> {
+    Chunk<float, 4> h[2];
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t e) {
+        h[0].load(r, e);
+        h[1].load(r, e + 4);
+    }
+    __device__ __forceinline__ float get(int i) const { return h[i / 4].get(i % 4); }
+    static __device__ __forceinline__ void store(const float *v, rsrc_t r, uint32_t e) {
+        Chunk<float, 4>::store(v, r, e);
+        Chunk<float, 4>::store(v + 4, r, e + 4);
     }
 };
 template <typename T> struct Chunk<T, 1> {
@@ -96,6 +116,10 @@ template <int V> __device__ __forceinline__ void store_e4m3(const float *v, rsrc
             q[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], p, true));
         }
         __builtin_amdgcn_raw_buffer_store_b64(q, r, e, 0, kStream);
+    } else if constexpr (V == 4) {
+        const int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+        __builtin_amdgcn_raw_buffer_store_b32(static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true)), r, e,
+                                              0, kStream);
     } else {
         __builtin_amdgcn_raw_buffer_store_b8(
             static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false) & 0xff), r, e, 0, kStream);
@@ -285,8 +309,9 @@ __global__ __launch_bounds__(kSumThreads) void norm_dweight_kernel(const float *
 }
 
 // ------------------------------------------------------------------- host
-bool wide(const void *p, int64_t ld, size_t es) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<int64_t>(es) % 16 == 0;
+// accesses of V elements stay aligned in every row (and end with it)
+template <int V, typename T> bool wide(const void *p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % (V * sizeof(T)) == 0 && ld % V == 0;
 }
 
 constexpr int64_t kMaxGrid = 2048;      // workgroups: 8 of four waves per CU
@@ -313,56 +338,62 @@ template <typename T, typename S, int V, int P, int R> hipError_t launch_bwd(con
     return hipGetLastError();
 }
 
-// The chunks per lane and waves per row for a width of `chunks` x 64 V elements.
-// The gradient holds three tensors and dw beside the weight, so it takes
-// fewer chunks per lane.
-#define SSM_FWD_PICK8(CALL)                                                        \
-    return chunks <= 1    ? CALL(8, 1, 1)                                          \
-           : chunks <= 2  ? CALL(8, 2, 1)                                          \
-           : chunks <= 3  ? CALL(8, 3, 1)                                          \
-           : chunks <= 4  ? CALL(8, 4, 1)                                          \
-           : chunks <= 5  ? CALL(8, 5, 1)                                          \
-           : chunks <= 8  ? CALL(8, 2, 4)                                          \
-           : chunks <= 12 ? CALL(8, 3, 4)                                          \
-           : chunks <= 16 ? CALL(8, 4, 4)                                          \
-           : chunks <= 32 ? CALL(8, 2, 16)                                         \
-                          : CALL(8, 4, 16)
-#define SSM_BWD_PICK8(CALL)                                                        \
-    return chunks <= 1    ? CALL(8, 1, 1)                                          \
-           : chunks <= 2  ? CALL(8, 2, 1)                                          \
-           : chunks <= 4  ? CALL(8, 1, 4)                                          \
-           : chunks <= 8  ? CALL(8, 2, 4)                                          \
-           : chunks <= 16 ? CALL(8, 1, 16)                                         \
-           : chunks <= 32 ? CALL(8, 2, 16)                                         \
-                          : CALL(8, 4, 16)
+// The chunks per lane and waves per row for a width, in units of 512 elements
+// (V = 8 or 4) or 64 (V = 1).  The gradient holds three tensors and dw beside the
+// weight, so it takes fewer chunks per lane.
+#define SSM_FWD_PICK(CALL, V)                                                      \
+    return units <= 1    ? CALL(V, 8 / V, 1)                                       \
+           : units <= 2  ? CALL(V, 16 / V, 1)                                      \
+           : units <= 3  ? CALL(V, 24 / V, 1)                                      \
+           : units <= 4  ? CALL(V, 32 / V, 1)                                      \
+           : units <= 5  ? CALL(V, 40 / V, 1)                                      \
+           : units <= 8  ? CALL(V, 16 / V, 4)                                      \
+           : units <= 12 ? CALL(V, 24 / V, 4)                                      \
+           : units <= 16 ? CALL(V, 32 / V, 4)                                      \
+           : units <= 32 ? CALL(V, 16 / V, 16)                                     \
+                         : CALL(V, 32 / V, 16)
+#define SSM_BWD_PICK(CALL, V)                                                      \
+    return units <= 1    ? CALL(V, 8 / V, 1)                                       \
+           : units <= 2  ? CALL(V, 16 / V, 1)                                      \
+           : units <= 4  ? CALL(V, 8 / V, 4)                                       \
+           : units <= 8  ? CALL(V, 16 / V, 4)                                      \
+           : units <= 16 ? CALL(V, 8 / V, 16)                                      \
+           : units <= 32 ? CALL(V, 16 / V, 16)                                     \
+                         : CALL(V, 32 / V, 16)
 #define SSM_PICK1(CALL)                                                            \
-    return chunks <= 4     ? CALL(1, 4, 1)                                         \
-           : chunks <= 16  ? CALL(1, 4, 4)                                         \
-           : chunks <= 64  ? CALL(1, 4, 16)                                        \
-           : chunks <= 128 ? CALL(1, 8, 16)                                        \
-           : chunks <= 256 ? CALL(1, 16, 16)                                       \
-                           : CALL(1, 32, 16)
+    return units <= 4     ? CALL(1, 4, 1)                                          \
+           : units <= 16  ? CALL(1, 4, 4)                                          \
+           : units <= 64  ? CALL(1, 4, 16)                                         \
+           : units <= 128 ? CALL(1, 8, 16)                                         \
+           : units <= 256 ? CALL(1, 16, 16)                                        \
+                          : CALL(1, 32, 16)
+
+// 16 bytes of the widest tensor: the lanes of a store then fill whole lines (a row
+// of fp32 written as two 16-byte halves per lane took 195 us instead of 179 us at
+// 32768 x 2560)
+template <typename T, typename S> constexpr int kVec = sizeof(T) == 4 || sizeof(S) == 4 ? 4 : 8;
 
 template <typename T, typename S, bool Q> hipError_t pick_fwd(const NormArgs &a, hipStream_t s) {
 #define SSM_CALL(V, P, R) (launch_fwd<T, S, Q, V, P, R>(a, s))
-    if (a.dim % 8 == 0 && wide(a.x, a.ldx, sizeof(T)) && wide(a.residual, a.dim, sizeof(S)) &&
-        wide(a.residual_out, a.dim, sizeof(S)) && wide(a.weight, a.dim, 4) &&
-        reinterpret_cast<uintptr_t>(a.y) % (Q ? 8 : 16) == 0) {
-        const int64_t chunks = (a.dim + 511) / 512;
-        SSM_FWD_PICK8(SSM_CALL);
+    constexpr int W = kVec<T, S>;
+    if (wide<W, T>(a.x, a.ldx) && wide<W, S>(a.residual, a.dim) && wide<W, S>(a.residual_out, a.dim) &&
+        wide<4, float>(a.weight, a.dim) && (Q ? wide<W, uint8_t>(a.y, a.dim) : wide<W, T>(a.y, a.dim))) {
+        const int64_t units = (a.dim + 511) / 512;
+        SSM_FWD_PICK(SSM_CALL, W);
     }
-    const int64_t chunks = (a.dim + 63) / 64;
+    const int64_t units = (a.dim + 63) / 64;
     SSM_PICK1(SSM_CALL);
 #undef SSM_CALL
 }
 template <typename T, typename S> hipError_t pick_bwd(const NormBwdArgs &a, hipStream_t s) {
 #define SSM_CALL(V, P, R) (launch_bwd<T, S, V, P, R>(a, s))
-    if (a.dim % 8 == 0 && wide(a.dy, a.dim, sizeof(T)) && wide(a.dx, a.dim, sizeof(T)) && wide(a.r, a.dim, sizeof(S)) &&
-        wide(a.dres_out, a.dim, sizeof(S)) && wide(a.dres, a.dim, sizeof(S)) && wide(a.weight, a.dim, 4)) {
-        const int64_t chunks = (a.dim + 511) / 512;
-        SSM_BWD_PICK8(SSM_CALL);
+    constexpr int W = kVec<T, S>;
+    if (wide<W, T>(a.dy, a.dim) && wide<W, T>(a.dx, a.dim) && wide<W, S>(a.r, a.dim) && wide<W, S>(a.dres_out, a.dim) &&
+        wide<W, S>(a.dres, a.dim) && wide<4, float>(a.weight, a.dim)) {
+        const int64_t units = (a.dim + 511) / 512;
+        SSM_BWD_PICK(SSM_CALL, W);
     }
-    const int64_t chunks = (a.dim + 63) / 64;
+    const int64_t units = (a.dim + 63) / 64;
     SSM_PICK1(SSM_CALL);
 #undef SSM_CALL
 }

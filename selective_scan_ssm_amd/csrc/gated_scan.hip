@@ -637,15 +637,32 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(u4 *p, int64_t n, uint
         p[i] = zero;
 }
 
-template <typename T> __global__ __launch_bounds__(256) void gated_update_kernel(GatedStepArgs p) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.batch * p.dim) return;
+// One token: V channels per lane (4 where the width and the addresses allow 8- and
+// 16-byte accesses).
+template <typename T, int V> __global__ __launch_bounds__(256) void gated_update_kernel(GatedStepArgs p) {
     using G = typename GateFor<T>::type;
-    const float bias = p.gate_bias ? G::prep_bias(p.gate_bias[i % p.dim]) : 0.0f;
-    const Gate k = G::eval(to_f32(static_cast<const T *>(p.g)[i]), bias);
-    const float h = fmaf(k.a, p.state[i], k.s * to_f32(static_cast<const T *>(p.x)[i]));
-    p.state[i] = h;
-    static_cast<T *>(p.y)[i] = from_f32<T>(p.z ? h * silu(to_f32(static_cast<const T *>(p.z)[i])) : h);
+    struct alignas(V * sizeof(T)) Io4 {
+        T v[V];
+    };
+    struct alignas(V * 4) F4 {
+        float v[V];
+    };
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, n = static_cast<uint32_t>(p.batch * p.dim / V);
+    if (i >= n) return;
+    const uint32_t d = i % static_cast<uint32_t>(p.dim / V);
+    const Io4 g = static_cast<const Io4 *>(p.g)[i], x = static_cast<const Io4 *>(p.x)[i];
+    F4 h = reinterpret_cast<const F4 *>(p.state)[i], bias{};
+    Io4 z{}, y;
+    if (p.z) z = static_cast<const Io4 *>(p.z)[i];
+    if (p.gate_bias) bias = reinterpret_cast<const F4 *>(p.gate_bias)[d];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const Gate k = G::eval(to_f32(g.v[e]), G::prep_bias(bias.v[e]));
+        h.v[e] = fmaf(k.a, h.v[e], k.s * to_f32(x.v[e]));
+        y.v[e] = from_f32<T>(p.z ? h.v[e] * silu(to_f32(z.v[e])) : h.v[e]);
+    }
+    reinterpret_cast<F4 *>(p.state)[i] = h;
+    static_cast<Io4 *>(p.y)[i] = y;
 }
 
 // ------------------------------------------------------------------- host
@@ -805,13 +822,24 @@ hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_gated_update(const GatedStepArgs &a, hipStream_t s) {
-    const unsigned grid = static_cast<unsigned>((a.batch * a.dim + 255) / 256);
-    if (a.bf16)
-        hipLaunchKernelGGL(gated_update_kernel<bf16_t>, dim3(grid), dim3(256), 0, s, a);
+namespace {
+template <typename T> hipError_t launch_update(const GatedStepArgs &a, hipStream_t s) {
+    const uintptr_t io = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.g) |
+                         reinterpret_cast<uintptr_t>(a.z) | reinterpret_cast<uintptr_t>(a.y);
+    const uintptr_t f32 = reinterpret_cast<uintptr_t>(a.state) | reinterpret_cast<uintptr_t>(a.gate_bias);
+    const bool four = a.dim % 4 == 0 && io % (4 * sizeof(T)) == 0 && f32 % 16 == 0;
+    const int64_t lanes = a.batch * a.dim / (four ? 4 : 1);
+    const dim3 grid(static_cast<unsigned>((lanes + 255) / 256)), block(256);
+    if (four)
+        hipLaunchKernelGGL((gated_update_kernel<T, 4>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL(gated_update_kernel<float>, dim3(grid), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((gated_update_kernel<T, 1>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_gated_update(const GatedStepArgs &a, hipStream_t s) {
+    return a.bf16 ? launch_update<bf16_t>(a, s) : launch_update<float>(a, s);
 }
 
 }  // namespace ssm
