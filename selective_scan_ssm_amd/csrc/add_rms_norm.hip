@@ -28,9 +28,9 @@ struct MaxAbs {
     }
 };
 
-// f over the row's R waves; one barrier, tmp of the calls alternating
-template <int R, typename F> __device__ __forceinline__ float row_fold(float v, float *tmp, F f) {
-    v = wave_fold(v, f);
+// f over the row's R waves, or its L lanes; one barrier, tmp of the calls alternating
+template <int R, int L, typename F> __device__ __forceinline__ float row_fold(float v, float *tmp, F f) {
+    v = wave_fold<L>(v, f);
     if constexpr (R > 1) {
         if (threadIdx.x % 64 == 0) tmp[threadIdx.x / 64] = v;
         __syncthreads();
@@ -126,24 +126,35 @@ template <int V> __device__ __forceinline__ void store_e4m3(const float *v, rsrc
     }
 }
 
-// row `row` of a (rows, dim) tensor with rows ld apart: accesses past dim read 0 and store nothing
-template <typename T> __device__ __forceinline__ rsrc_t row_rsrc(const void *p, int64_t row, int64_t ld, int dim) {
+// n rows of a (rows, dim) tensor with rows ld apart, from row `row` on: accesses
+// past the last one's end read 0 and store nothing
+template <typename T> __device__ __forceinline__ rsrc_t row_rsrc(const void *p, int64_t row, int64_t ld, int dim, int n = 1) {
     return make_rsrc(static_cast<const char *>(p) + row * ld * static_cast<int64_t>(sizeof(T)),
-                     static_cast<uint32_t>(dim * sizeof(T)));
+                     static_cast<uint32_t>(((n - 1) * ld + dim) * static_cast<int64_t>(sizeof(T))));
 }
+// an element index past every such range, in bytes too (rows that share a wave span under 2^29 bytes)
+constexpr uint32_t kNoElem = 0x30000000u;
+constexpr int64_t kMaxSharedLd = int64_t(1) << 24;
 
 // ----------------------------------------------------------------- forward
 // T: io dtype; S: the residual's; Q: 8-bit output.  A workgroup is R waves on
-// one row, or (R = 1) up to four waves on a row each.
-template <typename T, typename S, bool Q, int V, int P, int R>
+// one row, or (R = 1) four waves on a row each, or (L < 64) on 64 / L rows each:
+// narrow rows, as of a norm per head, would leave most lanes idle.
+template <typename T, typename S, bool Q, int V, int P, int R, int L>
 __global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_kernel(NormArgs p) {
     __shared__ float tmp[2][2][R];
     const int lane = threadIdx.x % 64;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int dim = static_cast<int>(p.dim);
-    const int per_wg = R == 1 ? blockDim.x / 64 : 1;
-    const uint32_t e0 = static_cast<uint32_t>(((R == 1 ? 0 : w) * 64 + lane) * V);   // the lane's first element
+    static_assert(L == 64 || (P == 1 && R == 1), "rows that share a wave");
+    constexpr int G = 64 / L;                                        // rows of a wave
+    constexpr int per_wg = (R == 1 ? 4 : 1) * G;
+    const int sub = lane / L;
+    const uint32_t e0 = static_cast<uint32_t>(((R == 1 ? 0 : w) * 64 + lane % L) * V);   // the lane's first element
     constexpr uint32_t step = R * 64 * V;
+    const bool inside = L == 64 || static_cast<int>(e0) < dim;       // L = 64: past dim is past the descriptor
+    const uint32_t ed = inside ? sub * static_cast<uint32_t>(dim) + e0 : kNoElem;
+    const uint32_t ex = inside ? sub * static_cast<uint32_t>(p.ldx) + e0 : kNoElem;
     float wt[P][V];
     const rsrc_t rw = make_rsrc(p.weight, static_cast<uint32_t>(dim * 4));
 #pragma unroll
@@ -155,17 +166,18 @@ __global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_kernel(NormArgs p)
     }
     const float inv_dim = 1.0f / static_cast<float>(dim);
     int par = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_wg + (R == 1 ? w : 0); row < p.rows;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_wg + (R == 1 ? w * G : 0); row < p.rows;
          row += static_cast<int64_t>(gridDim.x) * per_wg, par ^= 1) {
+        const int n = L == 64 ? 1 : static_cast<int>(p.rows - row < G ? p.rows - row : G);
         Chunk<T, V> x[P];
         Chunk<S, V> res[P];
-        const rsrc_t rx = row_rsrc<T>(p.x, row, p.ldx, dim);
+        const rsrc_t rx = row_rsrc<T>(p.x, row, p.ldx, dim, n);
 #pragma unroll
-        for (int c = 0; c < P; ++c) x[c].load(rx, e0 + c * step);
+        for (int c = 0; c < P; ++c) x[c].load(rx, ex + c * step);
         if (p.residual) {
-            const rsrc_t rr = row_rsrc<S>(p.residual, row, p.dim, dim);
+            const rsrc_t rr = row_rsrc<S>(p.residual, row, p.dim, dim, n);
 #pragma unroll
-            for (int c = 0; c < P; ++c) res[c].load(rr, e0 + c * step);
+            for (int c = 0; c < P; ++c) res[c].load(rr, ed + c * step);
         }
         float v[P][V], ss = 0.0f;
 #pragma unroll
@@ -177,11 +189,11 @@ __global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_kernel(NormArgs p)
                 ss = fmaf(v[c][i], v[c][i], ss);
             }
         if (p.residual_out) {
-            const rsrc_t ro = row_rsrc<S>(p.residual_out, row, p.dim, dim);
+            const rsrc_t ro = row_rsrc<S>(p.residual_out, row, p.dim, dim, n);
 #pragma unroll
-            for (int c = 0; c < P; ++c) Chunk<S, V>::store(v[c], ro, e0 + c * step);
+            for (int c = 0; c < P; ++c) Chunk<S, V>::store(v[c], ro, ed + c * step);
         }
-        ss = row_fold<R>(ss, tmp[0][par], AddOp());
+        ss = row_fold<R, L>(ss, tmp[0][par], AddOp());
         const float rstd = 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps));
         float m = 0.0f;
 #pragma unroll
@@ -192,42 +204,45 @@ __global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_kernel(NormArgs p)
                 if constexpr (Q) m = MaxAbs()(m, v[c][i]);
             }
         if constexpr (Q) {
-            m = row_fold<R>(m, tmp[1][par], MaxAbs());
+            m = row_fold<R, L>(m, tmp[1][par], MaxAbs());
             float scale = m / kE4m3Max;
             scale = scale < kMinScale ? kMinScale : scale;     // false for NaN, which stays
             const float inv = 1.0f / scale;
-            if (lane == 0 && (R == 1 || w == 0)) p.scale[row] = scale;
-            const rsrc_t ry = make_rsrc(static_cast<char *>(p.y) + row * p.dim, static_cast<uint32_t>(dim));
+            if (lane % L == 0 && (R == 1 || w == 0) && sub < n) p.scale[row + sub] = scale;
+            const rsrc_t ry = row_rsrc<uint8_t>(p.y, row, p.dim, dim, n);
 #pragma unroll
             for (int c = 0; c < P; ++c) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[c][i] *= inv;
-                store_e4m3<V>(v[c], ry, e0 + c * step);
+                store_e4m3<V>(v[c], ry, ed + c * step);
             }
         } else {
-            const rsrc_t ry = row_rsrc<T>(p.y, row, p.dim, dim);
+            const rsrc_t ry = row_rsrc<T>(p.y, row, p.dim, dim, n);
 #pragma unroll
-            for (int c = 0; c < P; ++c) Chunk<T, V>::store(v[c], ry, e0 + c * step);
+            for (int c = 0; c < P; ++c) Chunk<T, V>::store(v[c], ry, ed + c * step);
         }
     }
 }
 
 // ---------------------------------------------------------------- gradient
-// A workgroup is four rows' waves (R = 1) or R waves on one row; its sum of
-// dy n over its rows is one row of `part`.
-constexpr int kBwdRows1 = 4;            // waves, and rows at a time, of a workgroup with R = 1
-
-template <typename T, typename S, int V, int P, int R>
-__global__ __launch_bounds__(R == 1 ? kBwdRows1 * 64 : R * 64) void norm_bwd_kernel(NormBwdArgs p) {
-    constexpr int NW = R == 1 ? kBwdRows1 : R;
+// Workgroups as in the forward; a workgroup's sum of dy n over its rows is one
+// row of `part`.
+template <typename T, typename S, int V, int P, int R, int L>
+__global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_bwd_kernel(NormBwdArgs p) {
+    constexpr int NW = R == 1 ? 4 : R;
     __shared__ float tmp[2][2][NW];
-    __shared__ float sW[R == 1 ? NW - 1 : 1][R == 1 ? 64 * V * P : 1];
+    __shared__ float sW[R == 1 ? NW : 1][R == 1 ? 64 * V * P : 1];
     const int lane = threadIdx.x % 64;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int dim = static_cast<int>(p.dim);
-    constexpr int per_wg = R == 1 ? kBwdRows1 : 1;
-    const uint32_t e0 = static_cast<uint32_t>(((R == 1 ? 0 : w) * 64 + lane) * V);
+    static_assert(L == 64 || (P == 1 && R == 1), "rows that share a wave");
+    constexpr int G = 64 / L;                                        // rows of a wave
+    constexpr int per_wg = (R == 1 ? 4 : 1) * G;
+    const int sub = lane / L;
+    const uint32_t e0 = static_cast<uint32_t>(((R == 1 ? 0 : w) * 64 + lane % L) * V);   // the lane's first element
     constexpr uint32_t step = R * 64 * V;
+    const bool inside = L == 64 || static_cast<int>(e0) < dim;       // L = 64: past dim is past the descriptor
+    const uint32_t ed = inside ? sub * static_cast<uint32_t>(dim) + e0 : kNoElem;
     float wt[P][V], dw[P][V];
     const rsrc_t rw = make_rsrc(p.weight, static_cast<uint32_t>(dim * 4));
 #pragma unroll
@@ -242,19 +257,20 @@ __global__ __launch_bounds__(R == 1 ? kBwdRows1 * 64 : R * 64) void norm_bwd_ker
     }
     const float inv_dim = 1.0f / static_cast<float>(dim);
     int par = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_wg + (R == 1 ? w : 0); row < p.rows;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_wg + (R == 1 ? w * G : 0); row < p.rows;
          row += static_cast<int64_t>(gridDim.x) * per_wg, par ^= 1) {
+        const int n = L == 64 ? 1 : static_cast<int>(p.rows - row < G ? p.rows - row : G);
         Chunk<T, V> dy[P];
         Chunk<S, V> r[P], add[P];
-        const rsrc_t rr = row_rsrc<S>(p.r, row, p.dim, dim), rd = row_rsrc<T>(p.dy, row, p.dim, dim);
+        const rsrc_t rr = row_rsrc<S>(p.r, row, p.dim, dim, n), rd = row_rsrc<T>(p.dy, row, p.dim, dim, n);
 #pragma unroll
-        for (int c = 0; c < P; ++c) r[c].load(rr, e0 + c * step);
+        for (int c = 0; c < P; ++c) r[c].load(rr, ed + c * step);
 #pragma unroll
-        for (int c = 0; c < P; ++c) dy[c].load(rd, e0 + c * step);
+        for (int c = 0; c < P; ++c) dy[c].load(rd, ed + c * step);
         if (p.dres_out) {
-            const rsrc_t ra = row_rsrc<S>(p.dres_out, row, p.dim, dim);
+            const rsrc_t ra = row_rsrc<S>(p.dres_out, row, p.dim, dim, n);
 #pragma unroll
-            for (int c = 0; c < P; ++c) add[c].load(ra, e0 + c * step);
+            for (int c = 0; c < P; ++c) add[c].load(ra, ed + c * step);
         }
         float ss = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -265,12 +281,13 @@ __global__ __launch_bounds__(R == 1 ? kBwdRows1 * 64 : R * 64) void norm_bwd_ker
                 ss = fmaf(v, v, ss);
                 dot = fmaf(v, wt[c][i] * dy[c].get(i), dot);
             }
-        ss = row_fold<R>(ss, tmp[0][par], AddOp());
-        dot = row_fold<R>(dot, tmp[1][par], AddOp());
-        const float rstd = 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps));
+        ss = row_fold<R, L>(ss, tmp[0][par], AddOp());
+        dot = row_fold<R, L>(dot, tmp[1][par], AddOp());
+        // a row past the last one has no part in dw, whatever eps
+        const float rstd = L == 64 || sub < n ? 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps)) : 0.0f;
         const float k = dot * inv_dim * rstd * rstd;           // mean(n w dy) rstd
-        const rsrc_t wx = row_rsrc<T>(p.dx, row, p.dim, dim);
-        const rsrc_t wr = p.dres ? row_rsrc<S>(p.dres, row, p.dim, dim) : make_rsrc(p.dx, 0u);
+        const rsrc_t wx = row_rsrc<T>(p.dx, row, p.dim, dim, n);
+        const rsrc_t wr = p.dres ? row_rsrc<S>(p.dres, row, p.dim, dim, n) : make_rsrc(p.dx, 0u);
 #pragma unroll
         for (int c = 0; c < P; ++c) {
             float o[V];
@@ -281,27 +298,29 @@ __global__ __launch_bounds__(R == 1 ? kBwdRows1 * 64 : R * 64) void norm_bwd_ker
                 if (p.dres_out) o[i] += add[c].get(i);
                 dw[c][i] = fmaf(g, v * rstd, dw[c][i]);
             }
-            Chunk<T, V>::store(o, wx, e0 + c * step);
-            if (p.dres) Chunk<S, V>::store(o, wr, e0 + c * step);
+            Chunk<T, V>::store(o, wx, ed + c * step);
+            if (p.dres) Chunk<S, V>::store(o, wr, ed + c * step);
         }
     }
-    if constexpr (R == 1) {                            // the waves' sums, in wave order
-        if (w > 0)
-#pragma unroll
-            for (int c = 0; c < P; ++c)
-#pragma unroll
-                for (int i = 0; i < V; ++i) sW[w - 1][(c * V + i) * 64 + lane] = dw[c][i];
-        __syncthreads();
-        if (w > 0) return;
+    if constexpr (R == 1) {                            // the waves' sums, in wave and row order
 #pragma unroll
         for (int c = 0; c < P; ++c)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                for (int u = 0; u < NW - 1; ++u) dw[c][i] += sW[u][(c * V + i) * 64 + lane];
+            for (int i = 0; i < V; ++i) sW[w][(c * V + i) * 64 + lane] = dw[c][i];
+        __syncthreads();
+        if (w > 0 || lane >= L) return;
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dw[c][i] = 0.0f;
+                for (int u = 0; u < NW; ++u)
+                    for (int q = 0; q < G; ++q) dw[c][i] += sW[u][(c * V + i) * 64 + q * L + lane];
+            }
     }
     const rsrc_t rp = row_rsrc<float>(p.workspace, blockIdx.x, p.dim, dim);
 #pragma unroll
-    for (int c = 0; c < P; ++c) Chunk<float, V>::store(dw[c], rp, e0 + c * step);
+    for (int c = 0; c < P; ++c) Chunk<float, V>::store(dw[c], rp, (inside ? e0 : kNoElem) + c * step);
 }
 
 __global__ __launch_bounds__(kSumThreads) void norm_dweight_kernel(const float *part, float *out, int64_t parts, int64_t dim) {
@@ -317,10 +336,11 @@ template <int V, typename T> bool wide(const void *p, int64_t ld) {
 constexpr int64_t kMaxGrid = 2048;      // workgroups: 8 of four waves per CU
 constexpr int64_t kMaxParts = 512;      // workgroups of the gradient, each with a partial sum
 
-template <typename T, typename S, bool Q, int V, int P, int R> hipError_t launch_fwd(const NormArgs &a, hipStream_t s) {
-    const int per_wg = R == 1 ? 4 : 1;
+template <typename T, typename S, bool Q, int V, int P, int R, int L = 64>
+hipError_t launch_fwd(const NormArgs &a, hipStream_t s) {
+    const int per_wg = (R == 1 ? 4 : 1) * (64 / L);
     const int64_t wgs = (a.rows + per_wg - 1) / per_wg;
-    hipLaunchKernelGGL((norm_kernel<T, S, Q, V, P, R>), dim3(static_cast<unsigned>(wgs < kMaxGrid ? wgs : kMaxGrid)),
+    hipLaunchKernelGGL((norm_kernel<T, S, Q, V, P, R, L>), dim3(static_cast<unsigned>(wgs < kMaxGrid ? wgs : kMaxGrid)),
                        dim3(R == 1 ? 256 : R * 64), 0, s, a);
     return hipGetLastError();
 }
@@ -328,15 +348,22 @@ int64_t parts_of(int64_t rows, int per_wg) {
     const int64_t wgs = (rows + per_wg - 1) / per_wg;
     return wgs < kMaxParts ? wgs : kMaxParts;
 }
-template <typename T, typename S, int V, int P, int R> hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
-    const int parts = static_cast<int>(parts_of(a.rows, R == 1 ? kBwdRows1 : 1));
+template <typename T, typename S, int V, int P, int R, int L = 64>
+hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
+    const int parts = static_cast<int>(parts_of(a.rows, (R == 1 ? 4 : 1) * (64 / L)));
     if (parts > 0)
-        hipLaunchKernelGGL((norm_bwd_kernel<T, S, V, P, R>), dim3(parts), dim3(R == 1 ? kBwdRows1 * 64 : R * 64), 0, s, a);
+        hipLaunchKernelGGL((norm_bwd_kernel<T, S, V, P, R, L>), dim3(parts), dim3(R == 1 ? 256 : R * 64), 0, s, a);
     hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((a.dim + kSumCols - 1) / kSumCols)),
                        dim3(kSumThreads), 0, s, static_cast<const float *>(a.workspace), a.dweight,
                        static_cast<int64_t>(parts), a.dim);
     return hipGetLastError();
 }
+
+// Rows of up to 32 V elements share a wave.
+#define SSM_NARROW(CALL, V)                                                        \
+    if (a.dim <= 8 * V) return CALL(V, 1, 1, 8);                                   \
+    if (a.dim <= 16 * V) return CALL(V, 1, 1, 16);                                 \
+    if (a.dim <= 32 * V) return CALL(V, 1, 1, 32)
 
 // The chunks per lane and waves per row for a width, in units of 512 elements
 // (V = 8 or 4) or 64 (V = 1).  The gradient holds three tensors and dw beside the
@@ -373,29 +400,51 @@ template <typename T, typename S, int V, int P, int R> hipError_t launch_bwd(con
 // 32768 x 2560)
 template <typename T, typename S> constexpr int kVec = sizeof(T) == 4 || sizeof(S) == 4 ? 4 : 8;
 
-template <typename T, typename S, bool Q> hipError_t pick_fwd(const NormArgs &a, hipStream_t s) {
-#define SSM_CALL(V, P, R) (launch_fwd<T, S, Q, V, P, R>(a, s))
-    constexpr int W = kVec<T, S>;
-    if (wide<W, T>(a.x, a.ldx) && wide<W, S>(a.residual, a.dim) && wide<W, S>(a.residual_out, a.dim) &&
-        wide<4, float>(a.weight, a.dim) && (Q ? wide<W, uint8_t>(a.y, a.dim) : wide<W, T>(a.y, a.dim))) {
-        const int64_t units = (a.dim + 511) / 512;
-        SSM_FWD_PICK(SSM_CALL, W);
+// Whether accesses of V elements suit every tensor of a call.
+template <typename T, typename S, int V> bool fits(const NormArgs &a) {
+    return wide<V, T>(a.x, a.ldx) && wide<V, S>(a.residual, a.dim) && wide<V, S>(a.residual_out, a.dim) &&
+           wide<4, float>(a.weight, a.dim) && (a.scale ? wide<V, uint8_t>(a.y, a.dim) : wide<V, T>(a.y, a.dim));
+}
+template <typename T, typename S, int V> bool fits(const NormBwdArgs &a) {
+    return wide<V, T>(a.dy, a.dim) && wide<V, T>(a.dx, a.dim) && wide<V, S>(a.r, a.dim) && wide<V, S>(a.dres_out, a.dim) &&
+           wide<V, S>(a.dres, a.dim) && wide<4, float>(a.weight, a.dim);
+}
+
+template <typename T, typename S, bool Q, int V> hipError_t pick_fwd_v(const NormArgs &a, hipStream_t s) {
+#define SSM_CALL(V, ...) (launch_fwd<T, S, Q, V, __VA_ARGS__>(a, s))
+    if (a.ldx < kMaxSharedLd) {
+        SSM_NARROW(SSM_CALL, V);
     }
-    const int64_t units = (a.dim + 63) / 64;
-    SSM_PICK1(SSM_CALL);
+    const int64_t units = (a.dim + (V == 1 ? 63 : 511)) / (V == 1 ? 64 : 512);
+    if constexpr (V == 1)
+        SSM_PICK1(SSM_CALL);
+    else
+        SSM_FWD_PICK(SSM_CALL, V);
 #undef SSM_CALL
 }
-template <typename T, typename S> hipError_t pick_bwd(const NormBwdArgs &a, hipStream_t s) {
-#define SSM_CALL(V, P, R) (launch_bwd<T, S, V, P, R>(a, s))
-    constexpr int W = kVec<T, S>;
-    if (wide<W, T>(a.dy, a.dim) && wide<W, T>(a.dx, a.dim) && wide<W, S>(a.r, a.dim) && wide<W, S>(a.dres_out, a.dim) &&
-        wide<W, S>(a.dres, a.dim) && wide<4, float>(a.weight, a.dim)) {
-        const int64_t units = (a.dim + 511) / 512;
-        SSM_BWD_PICK(SSM_CALL, W);
-    }
-    const int64_t units = (a.dim + 63) / 64;
-    SSM_PICK1(SSM_CALL);
+template <typename T, typename S, int V> hipError_t pick_bwd_v(const NormBwdArgs &a, hipStream_t s) {
+#define SSM_CALL(V, ...) (launch_bwd<T, S, V, __VA_ARGS__>(a, s))
+    SSM_NARROW(SSM_CALL, V);
+    const int64_t units = (a.dim + (V == 1 ? 63 : 511)) / (V == 1 ? 64 : 512);
+    if constexpr (V == 1)
+        SSM_PICK1(SSM_CALL);
+    else
+        SSM_BWD_PICK(SSM_CALL, V);
 #undef SSM_CALL
+}
+template <typename T, typename S, bool Q> hipError_t pick_fwd(const NormArgs &a, hipStream_t s) {
+    constexpr int W = kVec<T, S>;
+    if (fits<T, S, W>(a)) return pick_fwd_v<T, S, Q, W>(a, s);
+    if constexpr (W == 8)
+        if (fits<T, S, 4>(a)) return pick_fwd_v<T, S, Q, 4>(a, s);
+    return pick_fwd_v<T, S, Q, 1>(a, s);
+}
+template <typename T, typename S> hipError_t pick_bwd(const NormBwdArgs &a, hipStream_t s) {
+    constexpr int W = kVec<T, S>;
+    if (fits<T, S, W>(a)) return pick_bwd_v<T, S, W>(a, s);
+    if constexpr (W == 8)
+        if (fits<T, S, 4>(a)) return pick_bwd_v<T, S, 4>(a, s);
+    return pick_bwd_v<T, S, 1>(a, s);
 }
 template <typename T, typename S> hipError_t pick_fwd_q(const NormArgs &a, hipStream_t s) {
     return a.scale ? pick_fwd<T, S, true>(a, s) : pick_fwd<T, S, false>(a, s);

@@ -41,7 +41,7 @@ def check_quant(q, scale, y, by):
 
 
 SIZES = [(1, 1), (3, 2), (5, 63), (2, 64), (7, 65), (4, 130), (9, 256), (3, 257), (130, 768), (5, 1000), (17, 1536), (3, 2049),
-         (33, 2560), (2, 4097), (6, 5120), (2, 8192), (1, 10001), (2, 16384), (1, 32768), (1, 32767)]
+         (1000, 8), (37, 16), (5, 24), (130, 32), (67, 128), (33, 200), (21, 1540), (9, 100), (3, 31), (259, 17), (33, 2560), (2, 4097), (6, 5120), (2, 8192), (1, 10001), (2, 16384), (1, 32768), (1, 32767)]
 
 
 @pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16", "bf16-f32"])
@@ -127,6 +127,15 @@ def test_strided_and_unaligned_rows(ops, io):
         dro, dwo, bdr, bdw = R.add_rms_norm_bwd(U.f64(buf).reshape(18, dim), U.f64(res).reshape(18, dim), U.f64(w), bounds=True)
         U.close(got["dx"].view(18, dim), dro, bdr)
         U.close(got["dweight"], dwo, bdw)
+
+
+def test_rows_that_share_a_wave_with_eps_zero(ops):
+    """The rows past the last one count for nothing, even where eps = 0 makes an absent row's scale infinite."""
+    dy, r, w = U.rand(1, 13, 64, dtype=BF16), U.rand(2, 13, 64, dtype=BF16), 1.0 + 0.1 * U.rand(3, 64)
+    got = ops.add_rms_norm_bwd(dy, r, w, eps=0.0)
+    dro, dwo, bdr, bdw = R.add_rms_norm_bwd(U.f64(dy), U.f64(r), U.f64(w), eps=0.0, bounds=True)
+    U.close(got["dx"], dro, bdr)
+    U.close(got["dweight"], dwo, bdw)
 
 
 def test_zero_tiny_huge_and_nan_rows(ops):
