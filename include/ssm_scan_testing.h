@@ -52,6 +52,27 @@ int ssm_testing_bwd_segments(int64_t batch, int64_t seqlen, int64_t d_inner, int
 int ssm_testing_ssd_segments(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                              int64_t dstate, int io_dtype, int *segments, int *chunks_per_segment);
 
+/*
+ * ssm_testing_gated_fwd_no_handoff, ssm_testing_gated_bwd_no_handoff --
+ * ssm_gated_scan_fwd and ssm_gated_scan_bwd (same arguments, same validation,
+ * same workspace) with every hand-over between time tiles withheld; a tile's
+ * wait gives up after `spin_limit` polls (1 .. 65536, else SSM_ERR_SHAPE).
+ * Sequences of up to 128 steps run as usual.  Longer ones: ssm_scan_status
+ * reports SSM_ERR_WAIT, and everything that depends on a tile before (in the
+ * backward: after) the given-up one is NaN.
+ */
+int ssm_testing_gated_fwd_no_handoff(const void *x, int64_t ldx, const void *g, int64_t ldg,
+                                     const float *gate_bias, const void *z, int64_t ldz, const float *h0,
+                                     void *y, float *last_state, float *ckpt, int64_t batch,
+                                     int64_t seqlen, int64_t d_inner, int io_dtype, void *workspace,
+                                     size_t workspace_bytes, uint32_t spin_limit, void *stream);
+int ssm_testing_gated_bwd_no_handoff(const void *x, int64_t ldx, const void *g, int64_t ldg,
+                                     const float *gate_bias, const void *z, int64_t ldz, const float *h0,
+                                     const void *dout, const float *dlast, const float *ckpt, void *dx,
+                                     void *dg, void *dz, float *dgate_bias, float *dh0, int64_t batch,
+                                     int64_t seqlen, int64_t d_inner, int io_dtype, void *workspace,
+                                     size_t workspace_bytes, uint32_t spin_limit, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

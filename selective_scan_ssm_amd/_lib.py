@@ -29,6 +29,7 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_workspace_bytes", "sm1_scan_fwd", "sm1_scan
            "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_state_update", "ssm_add_rms_norm_fwd",
            "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_add_rms_norm_bwd_workspace_bytes",
            "ssm_grad_norm", "ssm_grad_clip", "ssm_grad_norm_workspace_bytes",
+           "ssm_testing_gated_fwd_no_handoff", "ssm_testing_gated_bwd_no_handoff",
            "ssm_status_string", "ssm_abi_version")
 BENCH_LIB_PATH = os.path.join(PKG, "libssmbench.so")
 BENCH_EXPORTS = ("ssm_mb_copy", "ssm_mb_valu")
@@ -134,6 +135,10 @@ def _bind(lib):
     lib.ssm_grad_norm.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
     lib.ssm_grad_clip.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _sz, _vp]
     lib.ssm_grad_norm_workspace_bytes.argtypes = [_i64]
+    for name, fn in (("fwd", lib.ssm_gated_scan_fwd), ("bwd", lib.ssm_gated_scan_bwd)):
+        test = getattr(lib, f"ssm_testing_gated_{name}_no_handoff")
+        test.argtypes = fn.argtypes[:-1] + [ctypes.c_uint32, _vp]
+        test.restype = _int
     for name in ("ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_state_update", "ssm_add_rms_norm_fwd",
                  "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_grad_norm", "ssm_grad_clip"):
         getattr(lib, name).restype = _int

@@ -3,6 +3,7 @@
 // include/ssm_scan.h).  As in ssm_abi.cpp, arguments are validated before the
 // HIP runtime is touched.
 #include "ssm_scan.h"
+#include "ssm_scan_testing.h"
 
 #include <hip/hip_runtime.h>
 
@@ -175,25 +176,11 @@ int run_list(const void *const *grads, void *const *outs, const int64_t *numel, 
     return hip_status(ssm::launch_grad_clip(a, static_cast<hipStream_t>(stream)));
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t ssm_gated_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t d_inner) {
-    if (batch < 0 || seqlen < 0 || d_inner < 0) return static_cast<size_t>(-1);
-    const int64_t n = mul3(batch, seqlen / ssm::kGatedBlock + (seqlen % ssm::kGatedBlock != 0), d_inner);
-    return n < 0 ? static_cast<size_t>(-1) : static_cast<size_t>(n) * 4;
-}
-
-size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype) {
-    if (check_gated_sizes(batch, seqlen, d_inner, io_dtype)) return static_cast<size_t>(-1);
-    return ssm::gated_scan_workspace(batch, seqlen, d_inner, io_dtype == SSM_BF16);
-}
-
-int ssm_gated_scan_fwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
-                       const void *z, int64_t ldz, const float *h0, void *y, float *last_state,
-                       float *ckpt, int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype,
-                       void *workspace, size_t workspace_bytes, void *stream) {
+// spin_limit: 0, or the error-path tests' (every hand-over withheld)
+int gated_fwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+              const void *z, int64_t ldz, const float *h0, void *y, float *last_state,
+              float *ckpt, int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype,
+              void *workspace, size_t workspace_bytes, uint32_t spin_limit, void *stream) {
     if (int r = check_gated_sizes(batch, seqlen, d_inner, io_dtype)) return r;
     if (batch == 0 || d_inner == 0) return SSM_OK;
     ssm::GatedArgs a = gated_args(x, ldx, g, ldg, gate_bias, z, ldz, h0, batch, seqlen, d_inner, io_dtype, workspace,
@@ -211,20 +198,16 @@ int ssm_gated_scan_fwd(const void *x, int64_t ldx, const void *g, int64_t ldg, c
                           range(need ? workspace : nullptr, static_cast<int64_t>(need), 1)};
     if (int r = check_overlap(outs, ins)) return r;
     if (int r = check_workspace(need, workspace, workspace_bytes)) return r;
+    a.test_spin_limit = spin_limit;
     a.y = y; a.last_state = last_state; a.ckpt = ckpt;
     return hip_status(ssm::launch_gated_scan(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype) {
-    if (check_gated_sizes(batch, seqlen, d_inner, io_dtype)) return static_cast<size_t>(-1);
-    return ssm::gated_scan_bwd_workspace(batch, seqlen, d_inner, io_dtype == SSM_BF16);
-}
-
-int ssm_gated_scan_bwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
-                       const void *z, int64_t ldz, const float *h0, const void *dout,
-                       const float *dlast, const float *ckpt, void *dx, void *dg, void *dz,
-                       float *dgate_bias, float *dh0, int64_t batch, int64_t seqlen, int64_t d_inner,
-                       int io_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+int gated_bwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+              const void *z, int64_t ldz, const float *h0, const void *dout,
+              const float *dlast, const float *ckpt, void *dx, void *dg, void *dz,
+              float *dgate_bias, float *dh0, int64_t batch, int64_t seqlen, int64_t d_inner,
+              int io_dtype, void *workspace, size_t workspace_bytes, uint32_t spin_limit, void *stream) {
     if (int r = check_gated_sizes(batch, seqlen, d_inner, io_dtype)) return r;
     if (d_inner == 0) return SSM_OK;
     ssm::GatedBwdArgs b{};
@@ -251,10 +234,67 @@ int ssm_gated_scan_bwd(const void *x, int64_t ldx, const void *g, int64_t ldg, c
                           range(dh0, n_bd, 4), range(need ? workspace : nullptr, static_cast<int64_t>(need), 1)};
     if (int r = check_overlap(outs, ins)) return r;
     if (int r = check_workspace(need, workspace, workspace_bytes)) return r;
+    b.fwd.test_spin_limit = spin_limit;
     b.dout = dout; b.dlast = dlast; b.ckpt = ckpt;
     b.dx = dx; b.dg = dg; b.dz = z ? dz : nullptr;
     b.dgate_bias = dgate_bias; b.dh0 = dh0;
     return hip_status(ssm::launch_gated_scan_bwd(b, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t d_inner) {
+    if (batch < 0 || seqlen < 0 || d_inner < 0) return static_cast<size_t>(-1);
+    const int64_t n = mul3(batch, seqlen / ssm::kGatedBlock + (seqlen % ssm::kGatedBlock != 0), d_inner);
+    return n < 0 ? static_cast<size_t>(-1) : static_cast<size_t>(n) * 4;
+}
+
+size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype) {
+    if (check_gated_sizes(batch, seqlen, d_inner, io_dtype)) return static_cast<size_t>(-1);
+    return ssm::gated_scan_workspace(batch, seqlen, d_inner, io_dtype == SSM_BF16);
+}
+
+int ssm_gated_scan_fwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+                       const void *z, int64_t ldz, const float *h0, void *y, float *last_state,
+                       float *ckpt, int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+    return gated_fwd(x, ldx, g, ldg, gate_bias, z, ldz, h0, y, last_state, ckpt, batch, seqlen, d_inner, io_dtype, workspace,
+                     workspace_bytes, 0, stream);
+}
+
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype) {
+    if (check_gated_sizes(batch, seqlen, d_inner, io_dtype)) return static_cast<size_t>(-1);
+    return ssm::gated_scan_bwd_workspace(batch, seqlen, d_inner, io_dtype == SSM_BF16);
+}
+
+int ssm_gated_scan_bwd(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+                       const void *z, int64_t ldz, const float *h0, const void *dout,
+                       const float *dlast, const float *ckpt, void *dx, void *dg, void *dz,
+                       float *dgate_bias, float *dh0, int64_t batch, int64_t seqlen, int64_t d_inner,
+                       int io_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    return gated_bwd(x, ldx, g, ldg, gate_bias, z, ldz, h0, dout, dlast, ckpt, dx, dg, dz, dgate_bias, dh0, batch, seqlen, d_inner,
+                     io_dtype, workspace, workspace_bytes, 0, stream);
+}
+
+int ssm_testing_gated_fwd_no_handoff(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+                       const void *z, int64_t ldz, const float *h0, void *y, float *last_state,
+                       float *ckpt, int64_t batch, int64_t seqlen, int64_t d_inner, int io_dtype,
+                       void *workspace, size_t workspace_bytes, uint32_t spin_limit, void *stream) {
+    if (spin_limit < 1 || spin_limit > 65536) return SSM_ERR_SHAPE;
+    return gated_fwd(x, ldx, g, ldg, gate_bias, z, ldz, h0, y, last_state, ckpt, batch, seqlen, d_inner, io_dtype, workspace,
+                     workspace_bytes, spin_limit, stream);
+}
+
+int ssm_testing_gated_bwd_no_handoff(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *gate_bias,
+                       const void *z, int64_t ldz, const float *h0, const void *dout,
+                       const float *dlast, const float *ckpt, void *dx, void *dg, void *dz,
+                       float *dgate_bias, float *dh0, int64_t batch, int64_t seqlen, int64_t d_inner,
+                       int io_dtype, void *workspace, size_t workspace_bytes, uint32_t spin_limit, void *stream) {
+    if (spin_limit < 1 || spin_limit > 65536) return SSM_ERR_SHAPE;
+    return gated_bwd(x, ldx, g, ldg, gate_bias, z, ldz, h0, dout, dlast, ckpt, dx, dg, dz, dgate_bias, dh0, batch, seqlen, d_inner,
+                     io_dtype, workspace, workspace_bytes, spin_limit, stream);
 }
 
 int ssm_gated_state_update(float *state, const void *x, const void *g, const float *gate_bias,

@@ -108,6 +108,16 @@ def test_gated_sizes(lib):
     assert lib.ssm_gated_scan_bwd_workspace_bytes(2, 300, 8, F32) > 0
 
 
+@pytest.mark.parametrize("limit", [0, 65537])
+def test_testing_entries_bound_their_limit(lib, limit):
+    a = scan_args()
+    head = (a["x"], 8, a["g"], 8, a["bias"], a["z"], 8, a["h0"])
+    tail = (2, 300, 8, F32, a["ws"], a["ws_bytes"], limit, None)
+    assert lib.ssm_testing_gated_fwd_no_handoff(*head, a["y"], a["last"], a["ckpt"], *tail) == ESHAPE
+    assert lib.ssm_testing_gated_bwd_no_handoff(*head, a["dout"], a["dlast"], a["ckpt"], a["dx"], a["dg"], a["dz"], a["dbias"],
+                                                a["dh0"], *tail) == ESHAPE
+
+
 def update(lib, **over):
     f = FakeDev()
     a = dict(state=f(), x=f(), g=f(), bias=f(), z=f(), y=f(), batch=2, dim=8, io=F32)

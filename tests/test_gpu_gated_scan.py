@@ -281,6 +281,42 @@ def test_two_streams_at_once_and_a_shared_workspace_in_turn(ops):
         assert torch.equal(run(a, workspace=ws), want[0]) and torch.equal(run(b, workspace=ws), want[1])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_wait_that_gives_up_is_reported(ops, dtype):
+    """Every hand-over withheld and the waits bounded at 64 polls, from the host:
+    all kernels end, the status says so, what depends on another tile is NaN, what
+    does not is the usual result, and the next call on the workspace is right."""
+    from selective_scan_ssm_amd import _lib
+    lib, B, T, D = _lib.load(), 2, 1500, 130
+    t = inputs(B, T, D, DT[dtype])
+    kw = dict(z=t["z"], gate_bias=t["gate_bias"], h0=t["h0"])
+    io = _lib.SSM_BF16 if dtype == "bf16" else _lib.SSM_F32
+    need = lib.ssm_gated_scan_bwd_workspace_bytes(B, T, D, io)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dout = U.rand(3, B, T, D, dtype=DT[dtype])
+    ck = torch.empty(ops.gated_ckpt_shape(B, T, D), device="cuda")
+    y, last = ops.gated_scan_fwd(t["x"], t["g"], return_last_state=True, ckpt_out=ck, **kw)
+    want = ops.gated_scan_bwd(t["x"], t["g"], dout, ckpt=ck, **kw)
+    p = lambda v: None if v is None else v.data_ptr()
+    stream = torch.cuda.current_stream().cuda_stream
+    head = (p(t["x"]), D, p(t["g"]), D, p(t["gate_bias"]), p(t["z"]), D, p(t["h0"]))
+    tail = (B, T, D, io, p(ws), need, 64, stream)
+    y2, last2 = torch.empty_like(y), torch.empty_like(last)
+    assert lib.ssm_testing_gated_fwd_no_handoff(*head, p(y2), p(last2), None, *tail) == 0
+    assert ops.scan_status(ws) == _lib.SSM_ERR_WAIT
+    assert torch.equal(y2[:, :128], y[:, :128]) and bool(torch.isnan(y2[:, 128:]).all()) and bool(torch.isnan(last2).all())
+    g = [torch.empty_like(t["x"]) for _ in range(3)] + [torch.empty(D, device="cuda"), torch.empty(B, D, device="cuda")]
+    for saved in (ck, None):
+        assert lib.ssm_testing_gated_bwd_no_handoff(*head, p(dout), None, p(saved), *(p(v) for v in g), *tail) == 0
+        assert ops.scan_status(ws) == _lib.SSM_ERR_WAIT
+        assert bool(torch.isnan(g[0][:, :1408]).all()) and bool(torch.isnan(g[4]).all()) and bool(torch.isnan(g[3]).all())
+        assert torch.equal(g[0][:, 1408:], want["dx"][:, 1408:])        # the last tile has nobody to wait for
+        assert torch.equal(g[1][:, 1408:], want["dg"][:, 1408:]) == (saved is not None)
+    got = ops.gated_scan_bwd(t["x"], t["g"], dout, workspace=ws, **kw)
+    assert ops.scan_status(ws) == 0 and all(torch.equal(v, want[k]) for k, v in got.items())
+    assert torch.equal(ops.gated_scan_fwd(t["x"], t["g"], workspace=ws, **kw), y) and ops.scan_status(ws) == 0
+
+
 def test_offsets_past_32_bits(ops):
     """A batch whose projection spans 9 GB: every batch row equals a call on that row alone."""
     B, T, D = 3, 50000, 5120
