@@ -34,8 +34,8 @@ constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up
 constexpr uint32_t kReady = 0x80000000u;   // set in a published word: a decay is never negative
 constexpr int kWaves = 8;                  // waves of a tile
 constexpr int kCounters = 8;               // ticket counters, each on a cache line of its own
-constexpr int kCounterWords = 32;          // counter c is word (c + 1) kCounterWords; word 1 is the error word
-constexpr size_t kHeader = 1280;
+constexpr int kCounterWords = 32;
+constexpr size_t kHeader = 1280;           // word 1: the error word; from word kCounterWords on: the counters
 
 // ------------------------------------------------------------------- gates
 // a = sigmoid(v) and s = 1 - a = sigmoid(-v) from e = exp(-|v|): the smaller of
@@ -112,7 +112,7 @@ template <typename T> struct Cell<T, 1> {
 
 // --------------------------------------------------------------- hand-over
 struct Link {
-    uint32_t *words;                 // the header: error word, ticket counters
+    uint32_t *error, *tickets;       // the error word, the ticket counters
     uint64_t *agg, *group, *state;   // 64 VEC words per (chain, tile), (chain, group), (chain, 8 groups)
     uint32_t spin_limit;
     int publish;
@@ -124,7 +124,7 @@ __device__ __forceinline__ uint64_t wait_word(const uint64_t *p, uint64_t v, con
     uint32_t spins = 0;
     while (!(static_cast<uint32_t>(v) & kReady)) {
         if (++spins > k.spin_limit) {
-            __hip_atomic_store(&k.words[1], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(k.error, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             return 0;
         }
         __builtin_amdgcn_s_sleep(1);
@@ -153,18 +153,22 @@ __device__ __forceinline__ float word_offset(uint64_t v) {
 // read neighbouring columns together.  Fewer counters where the shares would not
 // come out even (a short share runs ahead and leaves the rest to few workgroups).
 // A workgroup starts at the counter of its XCD's number and goes on to the next
-// when that one has no tiles left; as many workgroups as tiles: each finds one.
+// when that one has no tiles left; as many workgroups as tiles: each finds one
+// (k = n_tiles, and the workgroup leaves, only where another call runs on the same
+// workspace, against the rules).
 struct Tile {
     uint32_t chain;
     int k;
 };
 __device__ __forceinline__ Tile take_tile(const Link &lk, uint32_t chains, int n_tiles, uint32_t (&shared)[2]) {
     if (threadIdx.x == 0) {
+        shared[0] = 0;
+        shared[1] = static_cast<uint32_t>(n_tiles);
         const uint32_t n = lk.counters;                              // a power of two, at most `chains`
         for (uint32_t i = 0; i < n; ++i) {
             const uint32_t c = (blockIdx.x + i) & (n - 1);
             const uint32_t first = chains * c / n, mine = chains * (c + 1) / n - first;
-            const uint32_t t = atomicAdd(&lk.words[(c + 1) * kCounterWords], 1u);
+            const uint32_t t = atomicAdd(&lk.tickets[c * kCounterWords], 1u);
             const uint32_t k = t / mine;
             if (k < static_cast<uint32_t>(n_tiles)) {
                 shared[0] = first + (t - k * mine);
@@ -323,7 +327,10 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     const int tid = threadIdx.x, lane = tid % 64;
     const int w = __builtin_amdgcn_readfirstlane(tid / 64);
     Tile tile{blockIdx.x, 0};
-    if constexpr (Multi) tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
+    if constexpr (Multi) {
+        tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
+        if (tile.k >= p.n_tiles) return;
+    }
     const uint32_t chain = tile.chain;
     const int k = tile.k;
     const int b = static_cast<int>(chain / static_cast<uint32_t>(p.n_ct));
@@ -472,7 +479,10 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     const int tid = threadIdx.x, lane = tid % 64;
     const int w = __builtin_amdgcn_readfirstlane(tid / 64);
     Tile tile{blockIdx.x, 0};
-    if constexpr (Multi) tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
+    if constexpr (Multi) {
+        tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
+        if (tile.k >= p.n_tiles) return;
+    }
     const uint32_t chain = tile.chain;
     const int k = tile.k;                            // in scan order: from the last tile down
     const int j = p.n_tiles - 1 - k;
@@ -626,13 +636,10 @@ __global__ __launch_bounds__(256) void gated_copy_kernel(const float *in, float 
     if (i < n) out[i] = in ? in[i] : 0.0f;
 }
 
-// the hand-over words (16 bytes at a time) and the header: error word, ticket counters
+// clears header and hand-over words, 16 bytes at a time
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-__global__ __launch_bounds__(256) void gated_clear_kernel(u4 *p, int64_t n, uint32_t *words, int keep_error) {
+__global__ __launch_bounds__(256) void gated_clear_kernel(u4 *p, int64_t n) {
     const u4 zero = {0, 0, 0, 0};
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < static_cast<int>(kHeader / 4); i += 256)
-            if (!(keep_error && i == 1)) words[i] = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
         p[i] = zero;
 }
@@ -686,31 +693,33 @@ Layout layout(int64_t batch, int64_t seqlen, int64_t dim) {
     return l;
 }
 
-Link make_link(const Layout &l, void *ws, uint32_t chains, uint32_t test_spin_limit) {
-    char *p = static_cast<char *>(ws);
+// error: the workspace's error word, in its first region
+Link make_link(const Layout &l, char *region, uint32_t *error, uint32_t chains, uint32_t test_spin_limit) {
     Link k;
+    k.counters = kCounters;
     // shares of at least 6 chains (12 chains on four counters: 127 us for 65536
     // steps, on two: 122 us), and even ones below 20
-    k.counters = kCounters;
     while (k.counters > 1 && (chains < 6 * k.counters || (chains % k.counters != 0 && chains < 20 * k.counters)))
         k.counters /= 2;
-    k.words = reinterpret_cast<uint32_t *>(p);
-    k.agg = reinterpret_cast<uint64_t *>(p + l.agg);
-    k.group = reinterpret_cast<uint64_t *>(p + l.group);
-    k.state = reinterpret_cast<uint64_t *>(p + l.state);
+    k.error = error;
+    k.tickets = reinterpret_cast<uint32_t *>(region) + kCounterWords;
+    k.agg = reinterpret_cast<uint64_t *>(region + l.agg);
+    k.group = reinterpret_cast<uint64_t *>(region + l.group);
+    k.state = reinterpret_cast<uint64_t *>(region + l.state);
     k.spin_limit = test_spin_limit ? test_spin_limit : kSpinLimit;
     k.publish = test_spin_limit ? 0 : 1;
     return k;
 }
-void clear(const Layout &l, const Link &k, bool keep_error, hipStream_t s) {
-    const int64_t n = static_cast<int64_t>((l.total - kHeader) / 16), wgs = (n + 255) / 256;
+uint32_t *error_word(void *workspace) { return static_cast<uint32_t *>(workspace) + 1; }
+void clear(void *region, size_t bytes, hipStream_t s) {
+    const int64_t n = static_cast<int64_t>(bytes / 16), wgs = (n + 255) / 256;
     hipLaunchKernelGGL(gated_clear_kernel, dim3(static_cast<unsigned>(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s,
-                       reinterpret_cast<u4 *>(k.agg), n, k.words, keep_error ? 1 : 0);
+                       static_cast<u4 *>(region), n);
 }
 
 bool even(const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 
-template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs &a, hipStream_t s) {
+template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs &a, bool cleared, hipStream_t s) {
     const Layout l = layout(a.batch, a.seqlen, a.dim);
     FwdParams p{};
     p.x = a.x; p.g = a.g; p.z = a.z; p.ldx = a.ldx; p.ldg = a.ldg; p.ldz = a.ldz;
@@ -722,8 +731,8 @@ template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs 
     const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     const bool z = a.z && a.y;
     if (l.n_tiles > 1) {
-        p.link = make_link(l, a.workspace, p.chains, a.test_spin_limit);
-        clear(l, p.link, false, s);
+        p.link = make_link(l, static_cast<char *>(a.workspace), error_word(a.workspace), p.chains, a.test_spin_limit);
+        if (!cleared) clear(a.workspace, l.total, s);
         if (z)
             hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, true, true, Store>), grid, block, 0, s, p);
         else
@@ -744,15 +753,16 @@ template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs 
 bool whole_lines(const void *p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 128 == 0 && row_bytes % 128 == 0; }
 
 // bf16 in pairs of channels where every row starts on 4 bytes
-hipError_t dispatch_fwd(const GatedArgs &a, hipStream_t s) {
+hipError_t dispatch_fwd(const GatedArgs &a, bool cleared, hipStream_t s) {
     const bool lines = whole_lines(a.y, a.dim * (a.bf16 ? 2 : 4));
-    if (!a.bf16) return lines ? launch_fwd<float, 1, kStream>(a, s) : launch_fwd<float, 1, kCached>(a, s);
+    if (!a.bf16) return lines ? launch_fwd<float, 1, kStream>(a, cleared, s) : launch_fwd<float, 1, kCached>(a, cleared, s);
     const bool two = even(a.x, a.ldx) && even(a.g, a.ldg) && even(a.z, a.z ? a.ldz : 0) && even(a.y, a.dim);
-    if (two) return launch_fwd<bf16_t, 2, kStream>(a, s);
-    return lines ? launch_fwd<bf16_t, 1, kStream>(a, s) : launch_fwd<bf16_t, 1, kCached>(a, s);
+    if (two) return launch_fwd<bf16_t, 2, kStream>(a, cleared, s);
+    return lines ? launch_fwd<bf16_t, 1, kStream>(a, cleared, s) : launch_fwd<bf16_t, 1, kCached>(a, cleared, s);
 }
 
-// the partial sums and checkpoints of the gradient, behind the hand-over words
+// The workspace of the gradient: the hand-over of the pass that computes the
+// checkpoints, the gradient's own, partial sums, checkpoints.
 size_t part_bytes(int64_t batch, int64_t n_tiles, int64_t dim) { return round256(static_cast<size_t>(batch * n_tiles * dim) * 4); }
 
 template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hipStream_t s) {
@@ -760,12 +770,15 @@ template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hi
     const Layout l = layout(f.batch, f.seqlen, f.dim);
     char *ws = static_cast<char *>(f.workspace);
     BwdParams p{};
-    float *part = reinterpret_cast<float *>(ws + l.total);
-    float *ckpt = reinterpret_cast<float *>(ws + l.total + part_bytes(f.batch, l.n_tiles, f.dim));
+    float *part = reinterpret_cast<float *>(ws + 2 * l.total);
+    float *ckpt = reinterpret_cast<float *>(ws + 2 * l.total + part_bytes(f.batch, l.n_tiles, f.dim));
+    // one region of hand-over words for each pass, cleared together
+    char *region = a.ckpt ? ws : ws + l.total;
+    if (l.total) clear(ws, (a.ckpt ? 1 : 2) * l.total, s);
     if (!a.ckpt) {                                   // the states entering the tiles, y unwritten
         GatedArgs q = f;
         q.y = nullptr; q.last_state = nullptr; q.ckpt = ckpt; q.z = nullptr;
-        if (hipError_t e = dispatch_fwd(q, s)) return e;
+        if (hipError_t e = dispatch_fwd(q, true, s)) return e;
     }
     p.x = f.x; p.g = f.g; p.z = f.z; p.dout = a.dout; p.ldx = f.ldx; p.ldg = f.ldg; p.ldz = f.ldz;
     p.bias = f.gate_bias; p.ckpt = a.ckpt ? a.ckpt : ckpt; p.dlast = a.dlast;
@@ -777,8 +790,7 @@ template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hi
     p.chains = static_cast<uint32_t>(f.batch * p.n_ct);
     const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     if (l.n_tiles > 1) {
-        p.link = make_link(l, ws, p.chains, f.test_spin_limit);
-        clear(l, p.link, !a.ckpt, s);
+        p.link = make_link(l, region, error_word(ws), p.chains, f.test_spin_limit);
         if (f.z)
             hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, true, true, Store>), grid, block, 0, s, p);
         else
@@ -797,7 +809,7 @@ size_t gated_scan_workspace(int64_t batch, int64_t seqlen, int64_t dim, int) { r
 
 size_t gated_scan_bwd_workspace(int64_t batch, int64_t seqlen, int64_t dim, int) {
     const Layout l = layout(batch, seqlen, dim);
-    return l.total + 2 * part_bytes(batch, l.n_tiles, dim);
+    return 2 * l.total + 2 * part_bytes(batch, l.n_tiles, dim);
 }
 
 hipError_t launch_gated_scan(const GatedArgs &a, hipStream_t s) {
@@ -808,7 +820,7 @@ hipError_t launch_gated_scan(const GatedArgs &a, hipStream_t s) {
                                a.last_state, n);
         return hipGetLastError();
     }
-    return dispatch_fwd(a, s);
+    return dispatch_fwd(a, false, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s) {
@@ -830,7 +842,7 @@ hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s) {
     if (a.dgate_bias) {
         const Layout l = layout(f.batch, f.seqlen, f.dim);
         hipLaunchKernelGGL(gated_dbias_kernel, dim3(static_cast<unsigned>((f.dim + kSumCols - 1) / kSumCols)), dim3(kSumThreads), 0, s,
-                           reinterpret_cast<const float *>(static_cast<char *>(f.workspace) + l.total), a.dgate_bias,
+                           reinterpret_cast<const float *>(static_cast<char *>(f.workspace) + 2 * l.total), a.dgate_bias,
                            f.batch * l.n_tiles, f.dim);
     }
     return hipGetLastError();

@@ -176,6 +176,33 @@ def test_no_rows(ops):
     assert not bool(ops.add_rms_norm_bwd(x, x, w)["dweight"].any())
 
 
+def test_leading_axes(ops):
+    """One row without leading axes, and three leading axes: the same rows."""
+    w = 1.0 + 0.1 * U.rand(2, 96)
+    x, res = U.rand(1, 2, 3, 5, 96, dtype=BF16), U.rand(3, 2, 3, 5, 96)
+    y, r = ops.add_rms_norm(x, w, res)
+    q, s, _ = ops.add_rms_norm_quant(x, w, res)
+    g = ops.add_rms_norm_bwd(x, res, w)
+    assert s.shape == (2, 3, 5)
+    i = (1, 2, 3)
+    y1, r1 = ops.add_rms_norm(x[i], w, res[i])
+    q1, s1, _ = ops.add_rms_norm_quant(x[i], w, res[i])
+    assert s1.shape == () and torch.equal(y1, y[i]) and torch.equal(r1, r[i]) and torch.equal(s1, s[i])
+    assert torch.equal(q1.view(torch.uint8), q[i].view(torch.uint8))
+    assert torch.equal(ops.add_rms_norm_bwd(x[i], res[i], w)["dx"], g["dx"][i])
+
+
+def test_on_another_stream(ops):
+    x, w, res = U.rand(1, 4000, 768, dtype=BF16), 1.0 + 0.1 * U.rand(2, 768), U.rand(3, 4000, 768)
+    want = ops.add_rms_norm(x, w, res)[0], ops.add_rms_norm_bwd(x, res, w)["dweight"]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = ops.add_rms_norm(x, w, res)[0], ops.add_rms_norm_bwd(x, res, w)["dweight"]
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_graph_replays(ops):
     from test_gpu_graph import replay_matches_eager
     t = dict(x=U.rand(1, 300, 768, dtype=BF16), res=U.rand(2, 300, 768), w=1.0 + 0.1 * U.rand(3, 768),

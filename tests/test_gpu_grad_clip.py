@@ -30,7 +30,9 @@ def norm_close(norm, want):
     assert abs(float(norm) - want) <= 2 * R.U * want, (float(norm), want)
 
 
-LISTS = [[1], [5, 1, 7], [16383, 16384, 16385, 3], [(33, 65), 1, 100000, 0, 17], [8] * 300, [1000003, 70001]]
+# one tensor; many tiny ones; ends around the runs of 4096; more tensors than one table holds; large ones
+LISTS = [[1], [3] * 1000, [1024, 1023, 1025, 2048, 2049, 4096, 5000], [100] * 119 + [5000], [70] * 120, [70] * 121,
+         [5, 1, 7], [16383, 16384, 16385, 3], [(33, 65), 1, 100000, 0, 17], [8] * 300, [1000003, 70001]]
 
 
 @pytest.mark.parametrize("kinds", [(F32,), (BF16,), (F32, BF16)], ids=["f32", "bf16", "mixed"])
