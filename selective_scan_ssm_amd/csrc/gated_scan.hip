@@ -482,6 +482,8 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     if constexpr (Multi) {
         tile = take_tile(p.link, p.chains, p.n_tiles, sTile);
         if (tile.k >= p.n_tiles) return;
+    } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *p.link.error = 0;                           // no wait, no clear launch before this one
     }
     const uint32_t chain = tile.chain;
     const int k = tile.k;                            // in scan order: from the last tile down
@@ -683,7 +685,7 @@ struct Layout {
 };
 Layout layout(int64_t batch, int64_t seqlen, int64_t dim) {
     Layout l;
-    l.n_tiles = (seqlen + kBlock - 1) / kBlock;
+    l.n_tiles = batch * dim > 0 ? (seqlen + kBlock - 1) / kBlock : 0;
     const int64_t n_groups = (l.n_tiles + kGroup - 1) / kGroup, n_supers = (n_groups + kGroup - 1) / kGroup;
     l.cols = (dim + 127) / 128 * 128;
     l.agg = kHeader;
@@ -762,7 +764,9 @@ hipError_t dispatch_fwd(const GatedArgs &a, bool cleared, hipStream_t s) {
 }
 
 // The workspace of the gradient: the hand-over of the pass that computes the
-// checkpoints, the gradient's own, partial sums, checkpoints.
+// checkpoints, the gradient's own, partial sums, checkpoints.  With one tile per
+// chain there is nothing to hand over, but the error word keeps its place.
+size_t parts_at(const Layout &l) { return l.n_tiles > 1 ? 2 * l.total : l.n_tiles * 256; }
 size_t part_bytes(int64_t batch, int64_t n_tiles, int64_t dim) { return round256(static_cast<size_t>(batch * n_tiles * dim) * 4); }
 
 template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hipStream_t s) {
@@ -770,8 +774,8 @@ template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hi
     const Layout l = layout(f.batch, f.seqlen, f.dim);
     char *ws = static_cast<char *>(f.workspace);
     BwdParams p{};
-    float *part = reinterpret_cast<float *>(ws + 2 * l.total);
-    float *ckpt = reinterpret_cast<float *>(ws + 2 * l.total + part_bytes(f.batch, l.n_tiles, f.dim));
+    float *part = reinterpret_cast<float *>(ws + parts_at(l));
+    float *ckpt = reinterpret_cast<float *>(ws + parts_at(l) + part_bytes(f.batch, l.n_tiles, f.dim));
     // one region of hand-over words for each pass, cleared together
     char *region = a.ckpt ? ws : ws + l.total;
     if (l.total) clear(ws, (a.ckpt ? 1 : 2) * l.total, s);
@@ -788,6 +792,7 @@ template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hi
     p.n_ct = static_cast<int>((f.dim + 63) / 64);
     p.n_tiles = static_cast<int>(l.n_tiles);
     p.chains = static_cast<uint32_t>(f.batch * p.n_ct);
+    p.link.error = error_word(ws);
     const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
     if (l.n_tiles > 1) {
         p.link = make_link(l, region, error_word(ws), p.chains, f.test_spin_limit);
@@ -809,7 +814,7 @@ size_t gated_scan_workspace(int64_t batch, int64_t seqlen, int64_t dim, int) { r
 
 size_t gated_scan_bwd_workspace(int64_t batch, int64_t seqlen, int64_t dim, int) {
     const Layout l = layout(batch, seqlen, dim);
-    return 2 * l.total + 2 * part_bytes(batch, l.n_tiles, dim);
+    return parts_at(l) + 2 * part_bytes(batch, l.n_tiles, dim);
 }
 
 hipError_t launch_gated_scan(const GatedArgs &a, hipStream_t s) {
@@ -842,7 +847,7 @@ hipError_t launch_gated_scan_bwd(const GatedBwdArgs &a, hipStream_t s) {
     if (a.dgate_bias) {
         const Layout l = layout(f.batch, f.seqlen, f.dim);
         hipLaunchKernelGGL(gated_dbias_kernel, dim3(static_cast<unsigned>((f.dim + kSumCols - 1) / kSumCols)), dim3(kSumThreads), 0, s,
-                           reinterpret_cast<const float *>(static_cast<char *>(f.workspace) + 2 * l.total), a.dgate_bias,
+                           reinterpret_cast<const float *>(static_cast<char *>(f.workspace) + parts_at(l)), a.dgate_bias,
                            f.batch * l.n_tiles, f.dim);
     }
     return hipGetLastError();

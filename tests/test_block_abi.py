@@ -106,6 +106,9 @@ def test_gated_sizes(lib):
     assert lib.ssm_gated_scan_workspace_bytes(1, 1, 1, 9) == BAD
     assert lib.ssm_gated_scan_bwd_workspace_bytes(1, 100, -4, F32) == BAD
     assert lib.ssm_gated_scan_bwd_workspace_bytes(2, 300, 8, F32) > 0
+    # an error word and its line come before the sums; nothing is run, nothing needed, without a row or a channel
+    assert lib.ssm_gated_scan_bwd_workspace_bytes(1, 1, 1, F32) >= 512
+    assert lib.ssm_gated_scan_bwd_workspace_bytes(0, 300, 8, F32) == lib.ssm_gated_scan_workspace_bytes(0, 300, 8, F32) == 0
 
 
 @pytest.mark.parametrize("limit", [0, 65537])

@@ -317,6 +317,28 @@ def test_a_wait_that_gives_up_is_reported(ops, dtype):
     assert torch.equal(ops.gated_scan_fwd(t["x"], t["g"], workspace=ws, **kw), y) and ops.scan_status(ws) == 0
 
 
+@pytest.mark.parametrize("T", [1, 128, 129])
+@pytest.mark.parametrize("saved", [False, True])
+def test_status_of_the_gradient_of_short_sequences(ops, T, saved):
+    """The error word has a place of its own in every workspace, also where a
+    sequence is one tile and nothing is handed over: the status after a call that
+    ran through is OK, whatever the workspace held and whatever the sums are."""
+    from selective_scan_ssm_amd import _lib
+    B, D = 2, 70
+    t = inputs(B, T, D, torch.float32)
+    dout = U.rand(3, B, T, D)
+    kw = dict(z=t["z"], gate_bias=t["gate_bias"], h0=t["h0"])
+    ck = None
+    if saved:
+        ck = torch.empty(ops.gated_ckpt_shape(B, T, D), device="cuda")
+        ops.gated_scan_fwd(t["x"], t["g"], ckpt_out=ck, **kw)
+    want = ops.gated_scan_bwd(t["x"], t["g"], dout, ckpt=ck, **kw)
+    ws = torch.full((_lib.load().ssm_gated_scan_bwd_workspace_bytes(B, T, D, _lib.SSM_F32),), 255, dtype=torch.uint8, device="cuda")
+    got = ops.gated_scan_bwd(t["x"], t["g"], dout, ckpt=ck, workspace=ws, **kw)
+    assert ops.scan_status(ws) == 0
+    assert all(torch.equal(v, want[k]) for k, v in got.items())
+
+
 def test_offsets_past_32_bits(ops):
     """A batch whose projection spans 9 GB: every batch row equals a call on that row alone."""
     B, T, D = 3, 50000, 5120
