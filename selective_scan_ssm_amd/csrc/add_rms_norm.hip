@@ -333,8 +333,14 @@ template <int V, typename T> bool wide(const void *p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % (V * sizeof(T)) == 0 && ld % V == 0;
 }
 
-constexpr int64_t kMaxGrid = 2048;      // workgroups: 8 of four waves per CU
-constexpr int64_t kMaxParts = 512;      // workgroups of the gradient, each with a partial sum
+// Workgroups: 16 of four waves per CU (2048 instead: 16384 x 2561 fp32 148 us
+// against 143 us, 32768 x 2560 bf16 178 against 176 us).
+constexpr int64_t kMaxGrid = 4096;
+// Workgroups of the gradient, each with a partial sum of dw: few where a sum is
+// long (with 1024, 16384 x 768 takes 37 + 5.5 us instead of 36 + 4, 2000 x 12001
+// 115 us instead of 95), enough to fill the chip where it is short (100000 x 130:
+// 50 us with 512, 36 us with 1024).
+int64_t max_parts(int64_t dim) { return dim <= 256 ? 1024 : 512; }
 
 template <typename T, typename S, bool Q, int V, int P, int R, int L = 64>
 hipError_t launch_fwd(const NormArgs &a, hipStream_t s) {
@@ -344,13 +350,13 @@ hipError_t launch_fwd(const NormArgs &a, hipStream_t s) {
                        dim3(R == 1 ? 256 : R * 64), 0, s, a);
     return hipGetLastError();
 }
-int64_t parts_of(int64_t rows, int per_wg) {
+int64_t parts_of(int64_t rows, int64_t dim, int per_wg) {
     const int64_t wgs = (rows + per_wg - 1) / per_wg;
-    return wgs < kMaxParts ? wgs : kMaxParts;
+    return wgs < max_parts(dim) ? wgs : max_parts(dim);
 }
 template <typename T, typename S, int V, int P, int R, int L = 64>
 hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
-    const int parts = static_cast<int>(parts_of(a.rows, (R == 1 ? 4 : 1) * (64 / L)));
+    const int parts = static_cast<int>(parts_of(a.rows, a.dim, (R == 1 ? 4 : 1) * (64 / L)));
     if (parts > 0)
         hipLaunchKernelGGL((norm_bwd_kernel<T, S, V, P, R, L>), dim3(parts), dim3(R == 1 ? 256 : R * 64), 0, s, a);
     hipLaunchKernelGGL(norm_dweight_kernel, dim3(static_cast<unsigned>((a.dim + kSumCols - 1) / kSumCols)),
@@ -359,15 +365,26 @@ hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Rows of up to 32 V elements share a wave.
+// Rows of up to 32 V elements share a wave (200000 x 64 bf16: 19 us against 50 us
+// with a wave each).
 #define SSM_NARROW(CALL, V)                                                        \
     if (a.dim <= 8 * V) return CALL(V, 1, 1, 8);                                   \
     if (a.dim <= 16 * V) return CALL(V, 1, 1, 16);                                 \
     if (a.dim <= 32 * V) return CALL(V, 1, 1, 32)
 
 // The chunks per lane and waves per row for a width, in units of 512 elements
-// (V = 8 or 4) or 64 (V = 1).  The gradient holds three tensors and dw beside the
-// weight, so it takes fewer chunks per lane.
+// (V = 8 or 4) or 64 (V = 1).  Few waves to a row as far as the registers go, as
+// waves that share one wait for each other at every reduction.  40M elements, us:
+//   forward   2560 wide, fp32 residual   one wave 178   four 186   (32768 rows)
+//             1537 wide, bf16            one 70         four 87    sixteen 110
+//             2561 wide, bf16 / 8 bits   four 86 / 77   sixteen 81 / 92
+//   gradient  1280 wide, bf16            one 46         four 81
+//             5120 wide, bf16            four 52        sixteen 71
+//             401 wide, bf16             one 66         four 208
+//             2561 wide, fp32            four 91        sixteen 103
+//             2048 wide, fp32            one 89         four 81
+// Above 16384 wide sixteen waves do not hold a gradient's row: up to 92 registers
+// are spilled.
 #define SSM_FWD_PICK(CALL, V)                                                      \
     return units <= 1    ? CALL(V, 8 / V, 1)                                       \
            : units <= 2  ? CALL(V, 16 / V, 1)                                      \
@@ -382,15 +399,27 @@ hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
 #define SSM_BWD_PICK(CALL, V)                                                      \
     return units <= 1    ? CALL(V, 8 / V, 1)                                       \
            : units <= 2  ? CALL(V, 16 / V, 1)                                      \
-           : units <= 4  ? CALL(V, 8 / V, 4)                                       \
+           : units <= 3  ? CALL(V, 24 / V, 1)                                      \
+           : units <= 4  ? CALL(V, (V == 8 ? 32 : 8) / V, V == 8 ? 1 : 4)          \
            : units <= 8  ? CALL(V, 16 / V, 4)                                      \
-           : units <= 16 ? CALL(V, 8 / V, 16)                                      \
+           : units <= 16 ? CALL(V, 32 / V, 4)                                      \
            : units <= 32 ? CALL(V, 16 / V, 16)                                     \
                          : CALL(V, 32 / V, 16)
-#define SSM_PICK1(CALL)                                                            \
+#define SSM_FWD_PICK1(CALL, Q)                                                     \
     return units <= 4     ? CALL(1, 4, 1)                                          \
-           : units <= 16  ? CALL(1, 4, 4)                                          \
-           : units <= 64  ? CALL(1, 4, 16)                                         \
+           : units <= 8   ? CALL(1, 8, 1)                                          \
+           : units <= 16  ? CALL(1, 16, 1)                                         \
+           : units <= 32  ? CALL(1, 32, 1)                                         \
+           : units <= 64  ? CALL(1, Q ? 16 : 4, Q ? 4 : 16)                        \
+           : units <= 128 ? CALL(1, 8, 16)                                         \
+           : units <= 256 ? CALL(1, 16, 16)                                        \
+                          : CALL(1, 32, 16)
+#define SSM_BWD_PICK1(CALL)                                                        \
+    return units <= 4     ? CALL(1, 4, 1)                                          \
+           : units <= 8   ? CALL(1, 8, 1)                                          \
+           : units <= 16  ? CALL(1, 16, 1)                                         \
+           : units <= 32  ? CALL(1, 8, 4)                                          \
+           : units <= 64  ? CALL(1, 16, 4)                                         \
            : units <= 128 ? CALL(1, 8, 16)                                         \
            : units <= 256 ? CALL(1, 16, 16)                                        \
                           : CALL(1, 32, 16)
@@ -417,7 +446,7 @@ template <typename T, typename S, bool Q, int V> hipError_t pick_fwd_v(const Nor
     }
     const int64_t units = (a.dim + (V == 1 ? 63 : 511)) / (V == 1 ? 64 : 512);
     if constexpr (V == 1)
-        SSM_PICK1(SSM_CALL);
+        SSM_FWD_PICK1(SSM_CALL, Q);
     else
         SSM_FWD_PICK(SSM_CALL, V);
 #undef SSM_CALL
@@ -427,7 +456,7 @@ template <typename T, typename S, int V> hipError_t pick_bwd_v(const NormBwdArgs
     SSM_NARROW(SSM_CALL, V);
     const int64_t units = (a.dim + (V == 1 ? 63 : 511)) / (V == 1 ? 64 : 512);
     if constexpr (V == 1)
-        SSM_PICK1(SSM_CALL);
+        SSM_BWD_PICK1(SSM_CALL);
     else
         SSM_BWD_PICK(SSM_CALL, V);
 #undef SSM_CALL
@@ -453,7 +482,7 @@ template <typename T, typename S> hipError_t pick_fwd_q(const NormArgs &a, hipSt
 }  // namespace
 
 size_t norm_bwd_workspace(int64_t rows, int64_t dim) {
-    return static_cast<size_t>(parts_of(rows, 1) * ((dim + 3) / 4 * 4)) * 4;
+    return static_cast<size_t>(parts_of(rows, dim, 1) * ((dim + 3) / 4 * 4)) * 4;
 }
 
 hipError_t launch_add_rms_norm(const NormArgs &a, hipStream_t s) {

@@ -9,11 +9,10 @@
 //   1. each wave discretises its steps and folds them into its (A, U);
 //   2. the waves' aggregates meet in LDS and give every wave its prefix and the
 //      tile its own (A, U), which is published in the workspace;
-//   3. the state entering the tile is the state entering its group of 8 tiles,
-//      folded over the published aggregates of the tiles before it in the
-//      group (one wave waits for one of them); the last tile of a group
-//      publishes the state leaving it.  The order of every fold is fixed, so
-//      results do not depend on who was first;
+//   3. the state entering the tile is folded from what the tiles before it
+//      published, on three levels (tiles, groups of 8 tiles, states after 8
+//      groups); one wave waits for one of them.  The order of every fold is
+//      fixed, so results do not depend on who was first;
 //   4. each wave replays its steps from its own entering state and writes y.
 // A tile waits only for tiles with lower tickets, which are running or done; a
 // wait is bounded as in the row scan (error word, NaN state).
@@ -21,6 +20,11 @@
 // gradient of h: e_t = d_t + c_{t+1}, tiles in falling order.  It needs the
 // states h_{t-1}: they are recomputed inside a tile from the state entering it,
 // which the forward saves (one fp32 per channel and 128 steps).
+// Bound by HBM where the tiles fill the chip: the 2.8b layer (4 x 8192 x 5120 bf16
+// with z, 1342 MB) takes 237 to 243 us, 5.5 to 5.7 TB/s, as a 16-byte copy does.
+// The 130m layer (8 x 2048 x 1536), 3072 tiles, is a few rounds of what the chip
+// holds and spends a part of its 45 + 80 us starting and draining them (4.5 TB/s).
+// Tiles of 16 waves: 328 us at the 2.8b layer, as one workgroup then fills a CU.
 #include "column_sum.h"
 #include "ssm_device.h"
 #include "ssm_kernels.h"
@@ -464,7 +468,7 @@ struct BwdParams {
 
 // One channel per lane: a step's values (a, 1 - a, x, the two factors of dout and
 // the state) take six registers per step and channel, and two workgroups per CU
-// overlap better than wider lanes at one (at the 130m layer 82 us against 97 us).
+// overlap better than wider lanes at one (at the 130m layer 80 us against 96 us).
 template <typename T, int W, bool Z, bool Multi, int Store>
 __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     using C = Cell<T, 1>;
@@ -754,12 +758,18 @@ template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs 
 // 121 us; at 2560 channels the other way round, 133 against 128 us).
 bool whole_lines(const void *p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 128 == 0 && row_bytes % 128 == 0; }
 
-// bf16 in pairs of channels where every row starts on 4 bytes
+// bf16 in pairs of channels where every row starts on 4 bytes: whole-line accesses
+// of a wave (the 2.8b layer 243 us against 248 us with one channel per lane), unless
+// the tiles are then too few for more than a few rounds on the chip (8 x 2048 x 1536,
+// 1536 tiles of pairs, 48.6 us against 45.1 us; 32768 steps of 64 channels 18.4
+// against 15.0 us).
+constexpr int64_t kPairTiles = 4096;
 hipError_t dispatch_fwd(const GatedArgs &a, bool cleared, hipStream_t s) {
     const bool lines = whole_lines(a.y, a.dim * (a.bf16 ? 2 : 4));
     if (!a.bf16) return lines ? launch_fwd<float, 1, kStream>(a, cleared, s) : launch_fwd<float, 1, kCached>(a, cleared, s);
     const bool two = even(a.x, a.ldx) && even(a.g, a.ldg) && even(a.z, a.z ? a.ldz : 0) && even(a.y, a.dim);
-    if (two) return launch_fwd<bf16_t, 2, kStream>(a, cleared, s);
+    const int64_t pair_tiles = a.batch * ((a.dim + 127) / 128) * layout(a.batch, a.seqlen, a.dim).n_tiles;
+    if (two && pair_tiles >= kPairTiles) return launch_fwd<bf16_t, 2, kStream>(a, cleared, s);
     return lines ? launch_fwd<bf16_t, 1, kStream>(a, cleared, s) : launch_fwd<bf16_t, 1, kCached>(a, cleared, s);
 }
 

@@ -23,8 +23,9 @@
 // The second pass reads what the first has just read, so the loads are ordinary
 // ones (non-temporal, the 256 MB last-level cache keeps nothing of them) and the
 // stores of the scaled values non-temporal, in whole lines: 115M bf16 values into
-// fp32 take 46 us for the sums and 127 us for the scaling (5.0 and 5.4 TB/s),
-// against 43 + 155 us with non-temporal loads and 82 + 127 us with ordinary stores.
+// fp32 take 46 us for the sums and 110 us for the scaling (5.0 and 6.3 TB/s).  When
+// this was chosen, with other runs, it was 46 + 127 us, against 43 + 155 us with
+// non-temporal loads and 82 + 127 us with ordinary stores.
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
@@ -37,7 +38,10 @@ constexpr int kEntries = 120;           // 32 bytes each: a table stays under 4 
 constexpr int64_t kMinRun = 4096;       // elements of a workgroup, at least
 constexpr int64_t kPad = 1024;          // a tensor counts as whole multiples of this many
 constexpr int64_t kSmall = 2048;        // a piece up to here is read by one wave
-constexpr int kGrid = 2048;             // workgroups (8 per CU), and partial sums
+// Workgroups (8 per CU), and partial sums.  1280 save 4 us where 15M values are read
+// and not scaled (14 + 6 us) and cost 8 us at 115M (110 us for the scaling); 4096
+// save nothing.
+constexpr int kGrid = 2048;
 
 struct Entry {
     const void *in;

@@ -81,6 +81,28 @@ def test_backward(ops, rows, dim, types):
         assert (got["dresidual"] is got["dx"]) == (io == rt)
 
 
+# every split of a row over lanes and waves, with more rows than one round of workgroups where that is cheap
+SPLITS = [(4200, 257), (30, 601), (2100, 1023), (40, 1999), (530, 2561), (9, 4001), (530, 6001), (30, 1280), (2100, 1500),
+          (600, 2048), (530, 5120), (9, 12004), (9000, 120), (5000, 250)]
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16", "bf16-f32"])
+@pytest.mark.parametrize("rows,dim", SPLITS)
+def test_rows_of_every_split(ops, rows, dim, types):
+    io, rt = types
+    x, r, w = U.rand(1, rows, dim, dtype=io), U.rand(2, rows, dim, dtype=rt, scale=2.0), 1.0 + 0.2 * U.rand(3, dim)
+    y, _ = ops.add_rms_norm(x, w, r)
+    q, sc, _ = ops.add_rms_norm_quant(x, w, r)
+    _, yo, by = R.add_rms_norm(U.f64(x), U.f64(w), U.f64(r), bounds=True)
+    U.close(y, yo, by, "y")
+    check_quant(q, sc, yo, by)
+    got = ops.add_rms_norm_bwd(x, r, w, dresidual=r)
+    dro, dwo, bdr, bdw = R.add_rms_norm_bwd(U.f64(x), U.f64(r), U.f64(w), U.f64(r), bounds=True)
+    U.close(got["dx"], dro, bdr, "dx")
+    U.close(got["dresidual"], dro, bdr, "dresidual")
+    U.close(got["dweight"], dwo, bdw, "dweight")
+
+
 def test_without_a_residual(ops):
     x, w = U.rand(1, 6, 200, dtype=BF16), 1.0 + 0.1 * U.rand(2, 200)
     y, r = ops.add_rms_norm(x, w)
