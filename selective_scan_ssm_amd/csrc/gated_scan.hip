@@ -4,8 +4,9 @@
 // One step is the affine map h -> a h + u, u = (1 - a) x, and such maps compose:
 // (A1, U1) then (A2, U2) = (A2 A1, A2 U1 + U2).  There are only batch x d_inner
 // chains, so time is cut into tiles of 128 steps x 64 lanes of channels.  A
-// workgroup of W waves takes one tile; wave w holds S = 128 / W consecutive
-// steps in registers, so every tensor is read once and written once:
+// workgroup of 8 waves takes one tile; each wave holds S = 16 consecutive steps
+// in registers, so every tensor is read once and written once (up to 64 steps
+// take a workgroup of 1, 2 or 4 waves):
 //   1. each wave discretises its steps and folds them into its (A, U);
 //   2. the waves' aggregates meet in LDS and give every wave its prefix and the
 //      tile its own (A, U), which is published in the workspace;
@@ -25,6 +26,8 @@
 // The 130m layer (8 x 2048 x 1536), 3072 tiles, is a few rounds of what the chip
 // holds and spends a part of its 45 + 80 us starting and draining them (4.5 TB/s).
 // Tiles of 16 waves: 328 us at the 2.8b layer, as one workgroup then fills a CU.
+#include <type_traits>
+
 #include "column_sum.h"
 #include "ssm_device.h"
 #include "ssm_kernels.h"
@@ -37,6 +40,7 @@ constexpr int kGroup = 8;                  // tiles of a group, and groups of a 
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up
 constexpr uint32_t kReady = 0x80000000u;   // set in a published word: a decay is never negative
 constexpr int kWaves = 8;                  // waves of a tile
+constexpr int kSteps = kBlock / kWaves;    // steps of a wave
 constexpr int kCounters = 8;               // ticket counters, each on a cache line of its own
 constexpr int kCounterWords = 32;
 constexpr size_t kHeader = 1280;           // word 1: the error word; from word kCounterWords on: the counters
@@ -323,7 +327,7 @@ __global__ __launch_bounds__(W * 64) void gated_fwd_kernel(FwdParams p) {
     using C = Cell<T, VEC>;
     using G = typename GateFor<T>::type;
     using raw = typename C::raw;
-    constexpr int S = kBlock / W;
+    constexpr int S = kSteps;
     __shared__ float2 sAgg[W][64 * VEC];
     __shared__ float2 sLink[Multi ? 2 * kGroup : 1][64 * VEC];
     __shared__ uint32_t sTile[2];
@@ -474,7 +478,7 @@ __global__ __launch_bounds__(W * 64) void gated_bwd_kernel(BwdParams p) {
     using C = Cell<T, 1>;
     using G = typename GateFor<T>::type;
     using raw = typename C::raw;
-    constexpr int S = kBlock / W;
+    constexpr int S = kSteps;
     __shared__ float2 sAgg[W][64];                   // (A, U) of the waves, forward
     __shared__ float2 sRev[W][64];                   // the reverse maps (the same A, R)
     __shared__ float2 sLink[Multi ? 2 * kGroup : 1][64];
@@ -725,6 +729,18 @@ void clear(void *region, size_t bytes, hipStream_t s) {
 
 bool even(const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; }
 
+// launch(waves, whether there are several tiles to a chain): as many waves as the
+// steps of a sequence need, in powers of two (1024 x 16 x 1536 bf16 with z: 39 us
+// instead of 168 us with eight waves to every workgroup, its gradient 80 us instead
+// of 380 us).
+template <typename F> void with_waves(int64_t seqlen, F launch) {
+    if (seqlen > kBlock) launch(std::integral_constant<int, kWaves>(), std::true_type());
+    else if (seqlen > 4 * kSteps) launch(std::integral_constant<int, 8>(), std::false_type());
+    else if (seqlen > 2 * kSteps) launch(std::integral_constant<int, 4>(), std::false_type());
+    else if (seqlen > kSteps) launch(std::integral_constant<int, 2>(), std::false_type());
+    else launch(std::integral_constant<int, 1>(), std::false_type());
+}
+
 template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs &a, bool cleared, hipStream_t s) {
     const Layout l = layout(a.batch, a.seqlen, a.dim);
     FwdParams p{};
@@ -734,20 +750,20 @@ template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs 
     p.n_ct = static_cast<int>((a.dim + 64 * VEC - 1) / (64 * VEC));
     p.n_tiles = static_cast<int>(l.n_tiles);
     p.chains = static_cast<uint32_t>(a.batch * p.n_ct);
-    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
+    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles));
     const bool z = a.z && a.y;
     if (l.n_tiles > 1) {
         p.link = make_link(l, static_cast<char *>(a.workspace), error_word(a.workspace), p.chains, a.test_spin_limit);
         if (!cleared) clear(a.workspace, l.total, s);
-        if (z)
-            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, true, true, Store>), grid, block, 0, s, p);
-        else
-            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, false, true, Store>), grid, block, 0, s, p);
-    } else if (z) {
-        hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, true, false, Store>), grid, block, 0, s, p);
-    } else {
-        hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, kWaves, false, false, Store>), grid, block, 0, s, p);
     }
+    with_waves(a.seqlen, [&](auto waves, auto multi) {
+        constexpr int W = decltype(waves)::value;
+        constexpr bool M = decltype(multi)::value;
+        if (z)
+            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, W, true, M, Store>), grid, dim3(W * 64), 0, s, p);
+        else
+            hipLaunchKernelGGL((gated_fwd_kernel<T, VEC, W, false, M, Store>), grid, dim3(W * 64), 0, s, p);
+    });
     return hipGetLastError();
 }
 
@@ -803,18 +819,16 @@ template <typename T, int Store> hipError_t launch_bwd(const GatedBwdArgs &a, hi
     p.n_tiles = static_cast<int>(l.n_tiles);
     p.chains = static_cast<uint32_t>(f.batch * p.n_ct);
     p.link.error = error_word(ws);
-    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles)), block(kWaves * 64);
-    if (l.n_tiles > 1) {
-        p.link = make_link(l, region, error_word(ws), p.chains, f.test_spin_limit);
+    const dim3 grid(static_cast<unsigned>(p.chains * l.n_tiles));
+    if (l.n_tiles > 1) p.link = make_link(l, region, error_word(ws), p.chains, f.test_spin_limit);
+    with_waves(f.seqlen, [&](auto waves, auto multi) {
+        constexpr int W = decltype(waves)::value;
+        constexpr bool M = decltype(multi)::value;
         if (f.z)
-            hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, true, true, Store>), grid, block, 0, s, p);
+            hipLaunchKernelGGL((gated_bwd_kernel<T, W, true, M, Store>), grid, dim3(W * 64), 0, s, p);
         else
-            hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, false, true, Store>), grid, block, 0, s, p);
-    } else if (f.z) {
-        hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, true, false, Store>), grid, block, 0, s, p);
-    } else {
-        hipLaunchKernelGGL((gated_bwd_kernel<T, kWaves, false, false, Store>), grid, block, 0, s, p);
-    }
+            hipLaunchKernelGGL((gated_bwd_kernel<T, W, false, M, Store>), grid, dim3(W * 64), 0, s, p);
+    });
     return hipGetLastError();
 }
 

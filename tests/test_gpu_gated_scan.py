@@ -91,6 +91,31 @@ def test_backward(ops, B, T, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 31, 32, 33, 48, 64, 65])
+def test_short_sequences(ops, T, dtype):
+    """As many waves as the steps need."""
+    for D, z in ((130, True), (65, False)):
+        t = inputs(5, T, D, DT[dtype], z=z, seed=T)
+        check_fwd(ops, t)
+        check_bwd(ops, t)
+
+
+# enough tiles that bf16 channels are taken in pairs: one tile to a chain, several, more than a state's 64
+@pytest.mark.parametrize("B,T,D,z", [(2050, 129, 2, True), (1400, 257, 6, False), (4100, 20, 130, True), (4100, 33, 64, False),
+                                     (64, 8200, 2, True), (420, 520, 130, True)])
+def test_pairs_of_channels(ops, B, T, D, z):
+    t = inputs(B, T, D, torch.bfloat16, z=z, packed=D == 130, seed=T)
+    y, last = check_fwd(ops, t)
+    # the same channels among others that rule out pairs
+    wide = {k: v if v is None or v.dim() < 3 else torch.cat([v, v[..., :1]], -1) for k, v in t.items()}
+    wide["gate_bias"], wide["h0"] = (torch.cat([t[k], t[k][..., :1]], -1) for k in ("gate_bias", "h0"))
+    x, g = wide.pop("x"), wide.pop("g")
+    assert torch.equal(ops.gated_scan_fwd(x, g, **wide)[..., :D], y)
+    if B * T * D < 1 << 22:
+        check_bwd(ops, t)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("B,T,D,z", [(2, 300, 96, True), (1, 150, 33, True), (2, 140, 64, False), (1, 40, 1, True)])
 def test_column_ranges_of_one_projection(ops, B, T, D, z, dtype):
     t = inputs(B, T, D, DT[dtype], z=z, packed=True)
