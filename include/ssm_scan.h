@@ -17,7 +17,8 @@
  *   (h0 when T = 0).
  *
  * Conventions shared by every entry point
- *   - All tensor pointers are DEVICE pointers, row-major, contiguous:
+ *   - All tensor pointers are DEVICE pointers, row-major, contiguous (except
+ *     where an entry point takes a row stride):
  *       x, delta, z, y : (batch, seqlen, d_inner)      -- io dtype
  *       B, C           : (batch, seqlen, d_state)      -- io dtype, shared by all d
  *       A              : (d_inner, d_state)            -- fp32
@@ -33,8 +34,9 @@
  *     that size is 0); its contents need not be initialised and are garbage
  *     after the call.
  *   - Aliasing: no output may overlap any input (y, last_state vs x, delta,
- *     z, B, C, h0 ...), except `state` of ssm_state_update, which is updated
- *     in place by design.
+ *     z, B, C, h0 ...), except the `state` of ssm_state_update and of
+ *     ssm_gated_state_update, which is updated in place by design, and what
+ *     ssm_add_rms_norm_* and ssm_grad_clip say of theirs.
  *   - Streams: work is enqueued on `stream` (a hipStream_t; NULL = the null
  *     stream) and the call returns without waiting.  The caller synchronises.
  *   - Errors: arguments are validated before anything is enqueued; on a
@@ -45,7 +47,9 @@
  *   - Edge cases: batch == 0 or d_inner == 0 is a no-op returning SSM_OK.
  *     seqlen == 0 writes last_state := h0 (or zeros) and leaves y untouched.
  *   - Alignment: every pointer must be aligned to its element size (4 bytes
- *     for fp32 tensors, 2 bytes for bf16 tensors), else SSM_ERR_ALIGN.
+ *     for fp32 tensors, 2 bytes for bf16 tensors), else SSM_ERR_ALIGN; the
+ *     workspaces of ssm_gated_scan_*, ssm_add_rms_norm_bwd and ssm_grad_* to
+ *     256 bytes.
  *   - Thread safety: the entry points may be called concurrently on different
  *     streams -- except ssm_scan_fwd_noalloc, whose calls share one scratch
  *     array per GPU (see there).  Their only global state is created once

@@ -23,7 +23,7 @@
 // which the forward saves (one fp32 per channel and 128 steps).
 // Bound by HBM where the tiles fill the chip: the 2.8b layer (4 x 8192 x 5120 bf16
 // with z, 1342 MB) takes 237 to 243 us, 5.5 to 5.7 TB/s, as a 16-byte copy does.
-// The 130m layer (8 x 2048 x 1536), 3072 tiles, is a few rounds of what the chip
+// The 130m layer (8 x 2048 x 1536), 8 x 16 x 24 tiles, is a few rounds of what the chip
 // holds and spends a part of its 45 + 80 us starting and draining them (4.5 TB/s).
 // Tiles of 16 waves: 328 us at the 2.8b layer, as one workgroup then fills a CU.
 #include <type_traits>
@@ -154,8 +154,8 @@ __device__ __forceinline__ float word_offset(uint64_t v) {
 
 // A workgroup's tile: chain and position k in scan order.  Tickets are taken in
 // order, so a tile only ever waits for tiles that are running or done, whatever
-// else runs on the GPU.  One counter serves one ticket in about 17 ns (a
-// 3072-tile pass that reads 200 MB took 58 us), so the chains are dealt to up to
+// else runs on the GPU.  One counter serves one ticket in about 17 ns (a pass of
+// some 3000 tiles that reads 200 MB took 58 us), so the chains are dealt to up to
 // eight counters (48 us) in runs of neighbours: with every eighth chain to a
 // counter the 2.8b layer took 258 us instead of 237, as workgroups then no longer
 // read neighbouring columns together.  Fewer counters where the shares would not
