@@ -13,6 +13,7 @@
 #include "column_sum.h"
 #include "ssm_device.h"
 #include "ssm_kernels.h"
+#include "wave_fold.h"
 
 namespace ssm {
 namespace {

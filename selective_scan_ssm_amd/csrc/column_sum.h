@@ -1,7 +1,7 @@
 // Column sums of an fp32 (rows, dim) array of partial sums, in a fixed order.
 #pragma once
 
-#include "ssm_device.h"
+#include "wave_fold.h"
 
 namespace ssm {
 
