@@ -538,7 +538,8 @@ int ssm_add_rms_norm_fwd(const void *x, int64_t ldx, const void *residual, const
  * that multiplies 8-bit rows: instead of y,
  *     scale[row] = max(max_d |y| / 448, 2^-126)          fp32
  *     q[row, d]  = e4m3(y / scale)                       (OCP e4m3, nearest even)
- * so q * scale stands for y, the row's largest value at the format's largest.
+ * with y in fp32, taken in the formula's order, and the quotient rounded to fp32
+ * first, so q * scale stands for y, the row's largest value at the format's largest.
  * A row with a NaN has a NaN scale and NaN in q.
  */
 int ssm_add_rms_norm_quant(const void *x, int64_t ldx, const void *residual, const float *weight, void *q,

@@ -268,3 +268,57 @@ def test_refusals(ops):
             bad()
     with pytest.raises(RuntimeError, match="ALIAS"):
         ops.add_rms_norm(x, w, out=x)
+
+
+
+def near_middles(dim, power=0):
+    """dim weights, the largest 1.7 * 2^power, whose quotients by the row's scale, a 448th of it in fp32, lie on or one
+    ulp beside the middle of two e4m3 numbers; the scale; and the e4m3 numbers of the fp32 quotients."""
+    top = np.ldexp(np.float32(1.7), power)
+    scale = np.maximum(top / np.float32(448.0), np.float32(2.0 ** -126))
+    e4m3 = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()    # 0 .. 448
+    middle = ((e4m3[1:] + e4m3[:-1]) / 2)[np.arange(dim) * 37 % 126]
+    w = np.minimum((middle * float(scale)).astype(np.float32), top)
+    beside = np.arange(dim) % 3
+    w = np.where(beside == 1, np.nextafter(w, np.float32(0)), np.where(beside == 2, np.nextafter(w, top), w))
+    w[dim // 2] = top
+    to8 = lambda v: torch.from_numpy(v).to(torch.float8_e4m3fn)
+    return w, scale, to8(w / scale), to8(w * (np.float32(1) / scale))
+
+
+def test_a_product_with_the_reciprocal_is_told_from_the_quotient():
+    _, _, q, by_reciprocal = near_middles(2048)
+    assert int((q.view(torch.uint8) != by_reciprocal.view(torch.uint8)).sum()) > 20
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("dim", [64, 256, 2048, 4096, 8192, 32768])
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16", "bf16-f32"])
+def test_the_8_bit_output_is_the_rounded_quotient(ops, types, dim, off):
+    """Rows of +-3 with eps = 0: the mean square is 9, its root 3 and r / 3 exactly +-1 in fp32, so y is the weight
+    (taken in the formula's order) and q = e4m3(y / scale) can be said to the bit, down to the smallest scales."""
+    io, rt = types
+    sign = torch.where(U.rand(1, 9, dim) < 0, -1.0, 1.0)
+    x = torch.zeros(9 * dim + off, dtype=io, device="cuda")[off:].view(9, dim).copy_(sign * 2)
+    res = torch.zeros(9 * dim + off, dtype=rt, device="cuda")[off:].view(9, dim).copy_(sign)
+    for power in (0, 90, -80, -84, -110, -117, -119):
+        w, scale, want, _ = near_middles(dim, power)
+        wt = torch.zeros(dim + off, device="cuda")[off:].copy_(torch.from_numpy(w))
+        q, s, _ = ops.add_rms_norm_quant(x, wt, res, eps=0.0)
+        assert bool((s.cpu() == float(scale)).all()), power
+        assert torch.equal(q.float().cpu(), want.float() * sign.cpu()), power
+    w, _, _, _ = near_middles(dim)
+    wt = torch.zeros(dim + off, device="cuda")[off:].copy_(torch.from_numpy(w))
+    assert torch.equal(ops.add_rms_norm(x, wt, res, eps=0.0)[0], (wt * sign).to(io))
+
+
+def test_an_output_past_fp32_has_an_infinite_scale(ops):
+    """The finite values of such a row are 0 in 8 bits, the infinite ones NaN; other rows have none of it."""
+    x = torch.ones(3, 64, device="cuda")
+    x[1, :8] = 8.0
+    w = torch.full((64,), 2e38, device="cuda")
+    q, s, _ = ops.add_rms_norm_quant(x, w)
+    y, _ = ops.add_rms_norm(x, w)
+    assert bool(torch.isinf(y[1, :8]).all()) and bool(torch.isfinite(y[1, 8:]).all()) and bool(torch.isinf(s[1]))
+    assert bool(torch.isnan(q[1, :8].float()).all()) and not bool(q[1, 8:].float().any())
+    assert bool((q[[0, 2]].float() == 448.0).all())
