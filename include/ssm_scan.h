@@ -557,7 +557,10 @@ int ssm_add_rms_norm_quant(const void *x, int64_t ldx, const void *residual, con
  *   dresidual     : (rows, dim) residual dtype, optional: dr, the gradient of
  *                   residual; it may be dresidual_out itself (in place)
  *   dweight       : (dim) fp32, required
- *   All contiguous.  Workspace: ssm_add_rms_norm_bwd_workspace_bytes (partial
+ *   All contiguous; ssm_add_rms_norm_bwd_strided takes r with rows ldr elements
+ *   apart (ldr >= dim, else SSM_ERR_SHAPE): the gradient at an x that the forward
+ *   read with a row stride, where there was no residual and r is x itself.
+ *   Workspace: ssm_add_rms_norm_bwd_workspace_bytes (partial
  *   sums of dweight, added in a fixed order), 256-byte aligned.
  *   rows == 0 gives a zero dweight.
  */
@@ -565,8 +568,12 @@ int ssm_add_rms_norm_bwd(const void *dy, const void *r, const float *weight, con
                          void *dx, void *dresidual, float *dweight, int64_t rows, int64_t dim, float eps,
                          int io_dtype, int residual_dtype, void *workspace, size_t workspace_bytes,
                          void *stream);
+int ssm_add_rms_norm_bwd_strided(const void *dy, const void *r, int64_t ldr, const float *weight,
+                                 const void *dresidual_out, void *dx, void *dresidual, float *dweight,
+                                 int64_t rows, int64_t dim, float eps, int io_dtype, int residual_dtype,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes ssm_add_rms_norm_bwd needs; (size_t)-1 for invalid arguments. */
+/* Workspace bytes both need; (size_t)-1 for invalid arguments. */
 size_t ssm_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
 
 /*

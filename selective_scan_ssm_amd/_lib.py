@@ -27,8 +27,8 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_workspace_bytes", "sm1_scan_fwd", "sm1_scan
            "ssd_scan_workspace_bytes", "ssm_testing_ssd_segments",
            "ssm_gated_scan_fwd", "ssm_gated_scan_workspace_bytes", "ssm_gated_ckpt_bytes", "ssm_gated_scan_bwd",
            "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_state_update", "ssm_add_rms_norm_fwd",
-           "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_add_rms_norm_bwd_workspace_bytes",
-           "ssm_grad_norm", "ssm_grad_clip", "ssm_grad_norm_workspace_bytes",
+           "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_add_rms_norm_bwd_strided",
+           "ssm_add_rms_norm_bwd_workspace_bytes", "ssm_grad_norm", "ssm_grad_clip", "ssm_grad_norm_workspace_bytes",
            "ssm_testing_gated_fwd_no_handoff", "ssm_testing_gated_bwd_no_handoff",
            "ssm_status_string", "ssm_abi_version")
 BENCH_LIB_PATH = os.path.join(PKG, "libssmbench.so")
@@ -131,6 +131,8 @@ def _bind(lib):
     lib.ssm_add_rms_norm_quant.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp]
     lib.ssm_add_rms_norm_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp,
                                          _sz, _vp]
+    lib.ssm_add_rms_norm_bwd_strided.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int,
+                                                 _vp, _sz, _vp]
     lib.ssm_add_rms_norm_bwd_workspace_bytes.argtypes = [_i64, _i64]
     lib.ssm_grad_norm.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
     lib.ssm_grad_clip.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _sz, _vp]
@@ -140,7 +142,8 @@ def _bind(lib):
         test.argtypes = fn.argtypes[:-1] + [ctypes.c_uint32, _vp]
         test.restype = _int
     for name in ("ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_state_update", "ssm_add_rms_norm_fwd",
-                 "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_grad_norm", "ssm_grad_clip"):
+                 "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_add_rms_norm_bwd_strided", "ssm_grad_norm",
+                 "ssm_grad_clip"):
         getattr(lib, name).restype = _int
     for name in ("ssm_gated_scan_workspace_bytes", "ssm_gated_ckpt_bytes", "ssm_gated_scan_bwd_workspace_bytes",
                  "ssm_add_rms_norm_bwd_workspace_bytes", "ssm_grad_norm_workspace_bytes"):

@@ -262,6 +262,7 @@ __global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_bwd_kernel(NormBwd
     constexpr uint32_t step = R * 64 * V;
     const bool inside = L == 64 || static_cast<int>(e0) < dim;       // L = 64: past dim is past the descriptor
     const uint32_t ed = inside ? sub * static_cast<uint32_t>(dim) + e0 : kNoElem;
+    const uint32_t er = inside ? sub * static_cast<uint32_t>(p.ldr) + e0 : kNoElem;
     float wt[P][V], dw[P][V];
     const rsrc_t rw = make_rsrc(p.weight, static_cast<uint32_t>(dim * 4));
 #pragma unroll
@@ -281,9 +282,9 @@ __global__ __launch_bounds__(R == 1 ? 256 : R * 64) void norm_bwd_kernel(NormBwd
         const int n = L == 64 ? 1 : static_cast<int>(p.rows - row < G ? p.rows - row : G);
         Chunk<T, V> dy[P];
         Chunk<S, V> r[P], add[P];
-        const rsrc_t rr = row_rsrc<S>(p.r, row, p.dim, dim, n), rd = row_rsrc<T>(p.dy, row, p.dim, dim, n);
+        const rsrc_t rr = row_rsrc<S>(p.r, row, p.ldr, dim, n), rd = row_rsrc<T>(p.dy, row, p.dim, dim, n);
 #pragma unroll
-        for (int c = 0; c < P; ++c) r[c].load(rr, ed + c * step);
+        for (int c = 0; c < P; ++c) r[c].load(rr, er + c * step);
 #pragma unroll
         for (int c = 0; c < P; ++c) dy[c].load(rd, ed + c * step);
         if (p.dres_out) {
@@ -454,7 +455,7 @@ template <typename T, typename S, int V> bool fits(const NormArgs &a) {
            wide<4, float>(a.weight, a.dim) && (a.scale ? wide<V, uint8_t>(a.y, a.dim) : wide<V, T>(a.y, a.dim));
 }
 template <typename T, typename S, int V> bool fits(const NormBwdArgs &a) {
-    return wide<V, T>(a.dy, a.dim) && wide<V, T>(a.dx, a.dim) && wide<V, S>(a.r, a.dim) && wide<V, S>(a.dres_out, a.dim) &&
+    return wide<V, T>(a.dy, a.dim) && wide<V, T>(a.dx, a.dim) && wide<V, S>(a.r, a.ldr) && wide<V, S>(a.dres_out, a.dim) &&
            wide<V, S>(a.dres, a.dim) && wide<4, float>(a.weight, a.dim);
 }
 
@@ -472,7 +473,9 @@ template <typename T, typename S, bool Q, int V> hipError_t pick_fwd_v(const Nor
 }
 template <typename T, typename S, int V> hipError_t pick_bwd_v(const NormBwdArgs &a, hipStream_t s) {
 #define SSM_CALL(V, ...) (launch_bwd<T, S, V, __VA_ARGS__>(a, s))
-    SSM_NARROW(SSM_CALL, V);
+    if (a.ldr < kMaxSharedLd) {
+        SSM_NARROW(SSM_CALL, V);
+    }
     const int64_t units = (a.dim + (V == 1 ? 63 : 511)) / (V == 1 ? 64 : 512);
     if constexpr (V == 1)
         SSM_BWD_PICK1(SSM_CALL);

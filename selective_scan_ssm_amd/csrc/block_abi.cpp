@@ -111,6 +111,36 @@ int check_norm(const void *x, int64_t ldx, const void *residual, const float *we
     return check_overlap(outs, ins);
 }
 
+int norm_bwd(const void *dy, const void *r, int64_t ldr, const float *weight, const void *dresidual_out, void *dx,
+             void *dresidual, float *dweight, int64_t rows, int64_t dim, float eps, int io_dtype, int residual_dtype,
+             void *workspace, size_t workspace_bytes, void *stream) {
+    if (bad_dtype2(io_dtype, residual_dtype)) return SSM_ERR_DTYPE;
+    if (rows < 0 || rows > kMaxSpan || dim < 1 || dim > SSM_MAX_NORM_DIM || mul3(rows, dim, 4) < 0)
+        return SSM_ERR_SHAPE;
+    if (rows > 1 && (ldr < dim || mul3(rows, ldr, 4) < 0)) return SSM_ERR_SHAPE;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return SSM_ERR_VALUE;
+    if (!dweight || (rows > 0 && (!dy || !r || !weight || !dx))) return SSM_ERR_NULL;
+    const size_t es = io_size(io_dtype), rs = io_size(residual_dtype);
+    if (!aligned(dy, es) || !aligned(dx, es) || !aligned(r, rs) || !aligned(dresidual_out, rs) ||
+        !aligned(dresidual, rs) || !aligned(weight, 4) || !aligned(dweight, 4))
+        return SSM_ERR_ALIGN;
+    const int64_t n = rows * dim;
+    const size_t need = ssm::norm_bwd_workspace(rows, dim);
+    const Range ins[] = {range(dy, n, es), range(r, span(rows, rows > 1 ? ldr : dim, dim), rs), range(weight, dim, 4),
+                         range(dresidual_out == dresidual ? nullptr : dresidual_out, n, rs)};
+    const Range outs[] = {range(dx, n, es), range(dresidual, n, rs), range(dweight, dim, 4),
+                          range(need ? workspace : nullptr, static_cast<int64_t>(need), 1)};
+    if (int rc = check_overlap(outs, ins)) return rc;
+    if (int rc = check_workspace(need, workspace, workspace_bytes)) return rc;
+    ssm::NormBwdArgs a{};
+    a.dy = dy; a.r = r; a.dres_out = dresidual_out; a.weight = weight;
+    a.dx = dx; a.dres = dresidual; a.dweight = dweight;
+    a.rows = rows; a.dim = dim; a.ldr = rows > 1 ? ldr : dim; a.eps = eps;
+    a.bf16 = io_dtype == SSM_BF16; a.res_bf16 = residual_dtype == SSM_BF16;
+    a.workspace = workspace;
+    return hip_status(ssm::launch_add_rms_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
 // Checks a gradient list; an output may be its own input with the same dtype
 // and otherwise overlaps nothing.
 int check_list(const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
@@ -358,30 +388,16 @@ int ssm_add_rms_norm_bwd(const void *dy, const void *r, const float *weight, con
                          void *dx, void *dresidual, float *dweight, int64_t rows, int64_t dim, float eps,
                          int io_dtype, int residual_dtype, void *workspace, size_t workspace_bytes,
                          void *stream) {
-    if (bad_dtype2(io_dtype, residual_dtype)) return SSM_ERR_DTYPE;
-    if (rows < 0 || rows > kMaxSpan || dim < 1 || dim > SSM_MAX_NORM_DIM || mul3(rows, dim, 4) < 0)
-        return SSM_ERR_SHAPE;
-    if (!(eps >= 0.0f) || std::isinf(eps)) return SSM_ERR_VALUE;
-    if (!dweight || (rows > 0 && (!dy || !r || !weight || !dx))) return SSM_ERR_NULL;
-    const size_t es = io_size(io_dtype), rs = io_size(residual_dtype);
-    if (!aligned(dy, es) || !aligned(dx, es) || !aligned(r, rs) || !aligned(dresidual_out, rs) ||
-        !aligned(dresidual, rs) || !aligned(weight, 4) || !aligned(dweight, 4))
-        return SSM_ERR_ALIGN;
-    const int64_t n = rows * dim;
-    const size_t need = ssm::norm_bwd_workspace(rows, dim);
-    const Range ins[] = {range(dy, n, es), range(r, n, rs), range(weight, dim, 4),
-                         range(dresidual_out == dresidual ? nullptr : dresidual_out, n, rs)};
-    const Range outs[] = {range(dx, n, es), range(dresidual, n, rs), range(dweight, dim, 4),
-                          range(need ? workspace : nullptr, static_cast<int64_t>(need), 1)};
-    if (int rc = check_overlap(outs, ins)) return rc;
-    if (int rc = check_workspace(need, workspace, workspace_bytes)) return rc;
-    ssm::NormBwdArgs a{};
-    a.dy = dy; a.r = r; a.dres_out = dresidual_out; a.weight = weight;
-    a.dx = dx; a.dres = dresidual; a.dweight = dweight;
-    a.rows = rows; a.dim = dim; a.eps = eps;
-    a.bf16 = io_dtype == SSM_BF16; a.res_bf16 = residual_dtype == SSM_BF16;
-    a.workspace = workspace;
-    return hip_status(ssm::launch_add_rms_norm_bwd(a, static_cast<hipStream_t>(stream)));
+    return norm_bwd(dy, r, dim, weight, dresidual_out, dx, dresidual, dweight, rows, dim, eps, io_dtype, residual_dtype,
+                    workspace, workspace_bytes, stream);
+}
+
+int ssm_add_rms_norm_bwd_strided(const void *dy, const void *r, int64_t ldr, const float *weight,
+                                 const void *dresidual_out, void *dx, void *dresidual, float *dweight, int64_t rows,
+                                 int64_t dim, float eps, int io_dtype, int residual_dtype, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    return norm_bwd(dy, r, ldr, weight, dresidual_out, dx, dresidual, dweight, rows, dim, eps, io_dtype, residual_dtype,
+                    workspace, workspace_bytes, stream);
 }
 
 size_t ssm_grad_norm_workspace_bytes(int64_t count) {

@@ -222,11 +222,11 @@ struct NormArgs {
     int bf16, res_bf16;
 };
 struct NormBwdArgs {
-    const void *dy, *r, *dres_out;
+    const void *dy, *r, *dres_out;        // rows of r ldr apart
     const float *weight;
     void *dx, *dres;
     float *dweight;
-    int64_t rows, dim;
+    int64_t rows, dim, ldr;
     float eps;
     int bf16, res_bf16;
     void *workspace;

@@ -682,8 +682,9 @@ def add_rms_norm_quant(x, weight, residual=None, eps=1e-5, residual_dtype=None, 
 
 def add_rms_norm_bwd(dy, r, weight, dresidual=None, eps=1e-5, dresidual_out=None, workspace=None):
     """Gradient of add_rms_norm at the r it returned (x itself when it returned
-    None).  dy: dL/dy (..., dim) fp32 or bf16; r: like dy, in its dtype or fp32;
-    dresidual: dL/dr from the residual stream, r's dtype, optional.  Returns a
+    None).  dy: dL/dy (..., dim) fp32 or bf16, contiguous; r: like dy, in its
+    dtype or fp32, rows evenly strided (an x that the forward took so);
+    dresidual: dL/dr from the residual stream, r's dtype, contiguous, optional.  Returns a
     dict: dx (dy's dtype), dresidual (the gradient of residual: dx itself when
     the dtypes are the same, else in r's dtype) and dweight (dim,) fp32.
     dresidual_out: where dresidual goes, may be dresidual itself."""
@@ -696,16 +697,17 @@ def add_rms_norm_bwd(dy, r, weight, dresidual=None, eps=1e-5, dresidual_out=None
     dim = shape[-1]
     rows = dy.numel() // dim if dim else 0
     pdy = _arg(dy, "dy", io, shape, dev)
+    pr, ldr = _rows(r, "r", res, shape, dev)
     dx = torch.empty_like(dy)
-    own = dresidual_out if dresidual_out is not None else (torch.empty_like(r) if res != io else None)
+    own = dresidual_out if dresidual_out is not None else (torch.empty(shape, dtype=res, device=dev) if res != io else None)
     dw = torch.empty((dim,), dtype=torch.float32, device=dev)
     ws, pws = _scratch(lib.ssm_add_rms_norm_bwd_workspace_bytes(rows, dim), "ssm_add_rms_norm_bwd_workspace_bytes",
                        workspace, dev)
-    rc = _run(dev, lib.ssm_add_rms_norm_bwd, pdy, _arg(r, "r", res, shape, dev),
+    rc = _run(dev, lib.ssm_add_rms_norm_bwd_strided, pdy, pr, ldr,
               _arg(weight, "weight", torch.float32, (dim,), dev), _arg(dresidual, "dresidual", res, shape, dev), _ptr(dx),
               _arg(own, "dresidual_out", res, shape, dev), _ptr(dw), rows, dim, eps, _IO[io], _IO[res], pws,
               0 if ws is None else ws.numel())
-    _check(rc, "ssm_add_rms_norm_bwd")
+    _check(rc, "ssm_add_rms_norm_bwd_strided")
     return dict(dx=dx, dresidual=dx if own is None else own, dweight=dw)
 
 

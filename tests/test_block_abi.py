@@ -259,3 +259,20 @@ def test_clip_workspace(lib):
 def test_status_strings_of_the_new_codes(lib):
     for code in (-10, -11):
         assert lib.ssm_status_string(code).decode().startswith("SSM_ERR_")
+
+
+def norm_bwd_strided(lib, ldr, **over):
+    a = norm_args(**over)
+    return lib.ssm_add_rms_norm_bwd_strided(a["dy"], a["r"], ldr, a["w"], a["dro"], a["dx"], a["dres"], a["dw"], a["rows"],
+                                            a["dim"], a["eps"], a["io"], a["rt"], a["ws"], a["ws_bytes"], None)
+
+
+def test_norm_bwd_strided_refuses(lib):
+    for over, code in NORM + [(dict(r=None), ENULL), (dict(r=0x7f0000000002), EALIGN), (dict(ws_bytes=8), EWS)]:
+        assert norm_bwd_strided(lib, 40000, **over) == code, over
+    for ldr in (15, 0, -16, 1 << 60):
+        assert norm_bwd_strided(lib, ldr) == ESHAPE, ldr
+    # an output between the rows of r, in the span of the last one
+    a = norm_args()
+    assert norm_bwd_strided(lib, 48, dx=a["r"] + 4 * 20) == EALIAS
+    assert norm_bwd_strided(lib, 48, dw=a["r"] + 4 * (3 * 48 + 15)) == EALIAS

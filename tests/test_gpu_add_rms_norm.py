@@ -322,3 +322,48 @@ def test_an_output_past_fp32_has_an_infinite_scale(ops):
     assert bool(torch.isinf(y[1, :8]).all()) and bool(torch.isfinite(y[1, 8:]).all()) and bool(torch.isinf(s[1]))
     assert bool(torch.isnan(q[1, :8].float()).all()) and not bool(q[1, 8:].float().any())
     assert bool((q[[0, 2]].float() == 448.0).all())
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16", "bf16-f32"])
+@pytest.mark.parametrize("rows,dim,ld,off", [(13, 64, 192, 64), (13, 64, 65, 1), (7, 1, 3, 2), (37, 24, 32, 8), (9, 100, 301, 0),
+                                             (4100, 768, 1536, 768), (33, 2561, 2600, 3), (5, 4096, 8192, 4096),
+                                             (3, 12001, 12005, 4), (2, 64, (1 << 24) + 64, 0), (1, 130, 500, 370)])
+def test_gradient_at_a_strided_row(ops, types, rows, dim, ld, off):
+    """The r of a forward without residual is x itself, rows apart as they may be."""
+    io, rt = types
+    wide = torch.empty(rows, ld, dtype=rt, device="cuda")
+    x = wide[:, off:off + dim]
+    x.copy_(U.rand(1, rows, dim))
+    wide[:, off + dim:] = float("nan")                             # what lies between the rows counts for nothing
+    wide[:, :off] = float("nan")
+    dy, dr, w = U.rand(2, rows, dim, dtype=io), U.rand(3, rows, dim, dtype=rt), 1.0 + 0.2 * U.rand(4, dim)
+    if io == rt:
+        assert ops.add_rms_norm(x, w)[1] is None
+    for add in (None, dr):
+        got, want = ops.add_rms_norm_bwd(dy, x, w, dresidual=add), ops.add_rms_norm_bwd(dy, x.contiguous(), w, dresidual=add)
+        dro, dwo, bdr, bdw = R.add_rms_norm_bwd(U.f64(dy), U.f64(x), U.f64(w), U.f64(add), bounds=True)
+        for g in (got, want):
+            U.close(g["dx"], dro, bdr, "dx")
+            U.close(g["dresidual"], dro, bdr, "dresidual")
+            U.close(g["dweight"], dwo, bdw, "dweight")
+            assert g["dresidual"].is_contiguous()
+
+
+def test_gradient_at_strided_rows_past_32_bits(ops):
+    rows, dim, ld = 300000, 64, 8192                               # 4.9 GB of bf16 between the first row and the last
+    wide = torch.empty(rows, ld, dtype=BF16, device="cuda")
+    x = wide[:, 128:128 + dim].normal_()
+    dy, w = U.rand(2, rows, dim, dtype=BF16), 1.0 + 0.1 * U.rand(3, dim)
+    got, want = ops.add_rms_norm_bwd(dy, x, w), ops.add_rms_norm_bwd(dy, x.contiguous(), w)
+    assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dweight"], want["dweight"])
+
+
+def test_gradient_refuses_overlapping_and_uneven_rows(ops):
+    x, w = U.rand(1, 4, 6, 64), torch.ones(64, device="cuda")
+    dy = x[:, :3].contiguous()
+    with pytest.raises(ValueError, match="evenly"):
+        ops.add_rms_norm_bwd(dy, x[:, :3], w)
+    with pytest.raises(ValueError, match="overlap"):
+        ops.add_rms_norm_bwd(dy, x[:1, :1].expand(4, 3, 64), w)
+    with pytest.raises(ValueError):
+        ops.add_rms_norm_bwd(dy, x[:, :3].transpose(0, 1).contiguous(), w)
