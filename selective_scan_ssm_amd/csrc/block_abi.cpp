@@ -30,12 +30,14 @@ int check_gated_sizes(int64_t batch, int64_t seqlen, int64_t dim, int io) {
     if (int r = check_dtype(io)) return r;
     if (batch < 0 || seqlen < 0 || dim < 0 || batch > kMaxGridY) return SSM_ERR_SHAPE;
     if (mul3(batch, seqlen, dim) < 0 || mul3(batch, dim, 4) < 0) return SSM_ERR_SHAPE;
-    // one block of steps is addressed with 32-bit byte offsets; the grid's lanes
-    // (up to 1024 per tile of 128 steps x 64 channels) are counted in 32 bits,
-    // which also keeps seqlen under 2^29
+    // one block of steps is addressed with 32-bit byte offsets
     if (mul3(ssm::kGatedBlock, dim, 4) < 0 || mul3(ssm::kGatedBlock, dim, 4) > kMaxSpan) return SSM_ERR_SHAPE;
-    const int64_t tiles = mul3(batch, (dim + 63) / 64, (seqlen + ssm::kGatedBlock - 1) / ssm::kGatedBlock + 1);
-    if (tiles < 0 || tiles >= (int64_t(1) << 22)) return SSM_ERR_SHAPE;
+    // a launch counts its lanes in 32 bits: those of a tile's waves (no tile at all:
+    // a copy of the states, 256 to a workgroup), which also keeps seqlen under 2^30
+    const int64_t blocks = seqlen / ssm::kGatedBlock + (seqlen % ssm::kGatedBlock != 0);
+    const int64_t lanes = seqlen == 0 ? 256 : 64 * ssm::gated_waves(seqlen);
+    const int64_t tiles = mul3(batch, (dim + 63) / 64, blocks > 0 ? blocks : 1);
+    if (tiles < 0 || tiles > (int64_t(1) << 32) / lanes - 1) return SSM_ERR_SHAPE;
     return SSM_OK;
 }
 

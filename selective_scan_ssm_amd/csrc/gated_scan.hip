@@ -40,7 +40,8 @@ constexpr int kGroup = 8;                  // tiles of a group, and groups of a 
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls before a wait gives up
 constexpr uint32_t kReady = 0x80000000u;   // set in a published word: a decay is never negative
 constexpr int kWaves = 8;                  // waves of a tile
-constexpr int kSteps = kBlock / kWaves;    // steps of a wave
+constexpr int kSteps = kGatedSteps;        // steps of a wave
+static_assert(kWaves * kSteps == kBlock, "the waves hold a tile");
 constexpr int kCounters = 8;               // ticket counters, each on a cache line of its own
 constexpr int kCounterWords = 32;
 constexpr size_t kHeader = 1280;           // word 1: the error word; from word kCounterWords on: the counters
@@ -734,11 +735,13 @@ bool even(const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4
 // instead of 168 us with eight waves to every workgroup, its gradient 80 us instead
 // of 380 us).
 template <typename F> void with_waves(int64_t seqlen, F launch) {
-    if (seqlen > kBlock) launch(std::integral_constant<int, kWaves>(), std::true_type());
-    else if (seqlen > 4 * kSteps) launch(std::integral_constant<int, 8>(), std::false_type());
-    else if (seqlen > 2 * kSteps) launch(std::integral_constant<int, 4>(), std::false_type());
-    else if (seqlen > kSteps) launch(std::integral_constant<int, 2>(), std::false_type());
-    else launch(std::integral_constant<int, 1>(), std::false_type());
+    if (seqlen > kBlock) return launch(std::integral_constant<int, kWaves>(), std::true_type());
+    switch (gated_waves(seqlen)) {
+    case 8: return launch(std::integral_constant<int, 8>(), std::false_type());
+    case 4: return launch(std::integral_constant<int, 4>(), std::false_type());
+    case 2: return launch(std::integral_constant<int, 2>(), std::false_type());
+    default: return launch(std::integral_constant<int, 1>(), std::false_type());
+    }
 }
 
 template <typename T, int VEC, int Store> hipError_t launch_fwd(const GatedArgs &a, bool cleared, hipStream_t s) {

@@ -176,6 +176,11 @@ hipError_t launch_conv1d_update(const ConvUpdateArgs &a, hipStream_t s);
 // The gated linear recurrence.  Rows of x, g, z are ldx, ldg, ldz elements
 // apart; everything else is contiguous.
 constexpr int kGatedBlock = 128;          // steps between two checkpoints
+constexpr int kGatedSteps = 16;           // steps of a wave
+// the waves of a tile's workgroup: as many as the steps need, in powers of two
+inline int gated_waves(int64_t seqlen) {
+    return seqlen > 4 * kGatedSteps ? 8 : seqlen > 2 * kGatedSteps ? 4 : seqlen > kGatedSteps ? 2 : 1;
+}
 struct GatedArgs {
     const void *x, *g, *z;                // io dtype
     int64_t ldx, ldg, ldz;

@@ -276,3 +276,17 @@ def test_norm_bwd_strided_refuses(lib):
     a = norm_args()
     assert norm_bwd_strided(lib, 48, dx=a["r"] + 4 * 20) == EALIAS
     assert norm_bwd_strided(lib, 48, dw=a["r"] + 4 * (3 * 48 + 15)) == EALIAS
+
+
+# one tile below and at 2^32 lanes: 64 to a workgroup up to 16 steps, then 128, 256, 512
+@pytest.mark.parametrize("batch,seqlen,dim,code", [
+    (40000, 16, 4096, OK), (65535, 1, 64, OK), (65535, 128, 4096, OK), (65535, 16, 65536, OK), (65535, 16, 65537, ESHAPE),
+    (32767, 17, 65536, OK), (32768, 17, 65536, ESHAPE), (16383, 64, 65536, OK), (16384, 33, 65536, ESHAPE),
+    (8191, 128, 65536, OK), (8192, 65, 65536, ESHAPE), (4095, 129, 65536, OK), (4096, 129, 65536, ESHAPE),
+    (1, (1 << 30) - 128, 64, OK), (1, (1 << 30) - 127, 64, ESHAPE), (1, 1 << 62, 64, ESHAPE), (65536, 1, 1, ESHAPE)])
+def test_gated_largest_sizes(lib, batch, seqlen, dim, code):
+    for need in (lib.ssm_gated_scan_workspace_bytes, lib.ssm_gated_scan_bwd_workspace_bytes):
+        assert (need(batch, seqlen, dim, BF16) == BAD) == (code == ESHAPE)
+    if code == ESHAPE:
+        a = scan_args(batch=batch, seqlen=seqlen, dim=dim, ldx=dim, ldg=dim, ldz=dim)
+        assert fwd(lib, a) == bwd(lib, a) == ESHAPE

@@ -401,3 +401,29 @@ def test_refusals(ops):
             bad()
     with pytest.raises(RuntimeError, match="ALIAS"):
         ops.gated_scan_fwd(x, g, out=x)
+
+
+@pytest.mark.parametrize("B,T,D", [(40000, 16, 4096), (65535, 130, 128)])
+def test_many_short_sequences(ops, B, T, D):
+    """Millions of one-wave tiles over 2.6e9 elements, and the largest batch: the first and last sequences, and the sums
+    over all of them."""
+    make = lambda: torch.empty(B, T, D, dtype=torch.bfloat16, device="cuda").normal_()
+    x, g, dout = make(), make(), make()
+    bias = U.rand(1, D).abs() * 2
+    y, last = ops.gated_scan_fwd(x, g, gate_bias=bias, return_last_state=True)
+    got = ops.gated_scan_bwd(x, g, dout, gate_bias=bias)
+    for s in (slice(0, 3), slice(B - 3, B)):
+        t = dict(x=x[s], g=g[s], z=None, gate_bias=bias, h0=None)
+        yo, lo, by, bl = R.gated_scan(**host(t), bounds=True)
+        U.close(y[s], yo, by, "y")
+        U.close(last[s], lo, bl, "last")
+        want, bound = R.gated_scan_bwd(dout=U.f64(dout[s]), **host(t), bounds=True)
+        for k in ("dx", "dg", "dh0"):
+            U.close(got[k][s], want[k], bound[k], k)
+    total = got["dg"].sum((0, 1), dtype=torch.float64)
+    # dg rounds to bf16 after it is summed: half a step of each, in quadrature over B x T values of either sign, times 8;
+    # and the fp32 additions, under 2^12 on any path
+    size = got["dg"].double().square().sum((0, 1)).sqrt() if got["dg"].numel() < 1 << 31 else \
+        torch.stack([c.double().square().sum((0, 1)) for c in got["dg"].split(4096)]).sum(0).sqrt()
+    tol = 8 * 2.0 ** -8 * size + 2.0 ** -12 * got["dg"].abs().sum((0, 1), dtype=torch.float64)
+    assert bool(((got["dgate_bias"].double() - total).abs() <= tol).all())
