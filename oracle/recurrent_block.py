@@ -69,6 +69,12 @@ def gated_scan(x, g, z=None, gate_bias=None, h0=None, bounds=False):
     return (y, h, ey, E) if bounds else (y, h)
 
 
+def _bias_additions(batch, T):
+    """Additions on any path of dgate_bias: a wave's 16 steps, a tile's 8 waves,
+    every 64th of the tiles' sums, the 64 stripes of those by halves."""
+    return 16 + 8 + -(-batch * -(-T // 128) // 64) + 6
+
+
 def gated_scan_bwd(x, g, dout, z=None, gate_bias=None, h0=None, dlast=None, bounds=False):
     """dict of dx, dg, dz, dgate_bias, dh0 (and one of their bounds)."""
     x, g, dout = (np.asarray(t, np.float64) for t in (x, g, dout))
@@ -115,8 +121,7 @@ def gated_scan_bwd(x, g, dout, z=None, gate_bias=None, h0=None, dlast=None, boun
     bd["dx"] = s * fs + np.abs(s * es) * (k + 2.0) * U + TINY * np.abs(es)
     bd["dg"] = w * (fs * np.abs(hb - x) + np.abs(es) * (eb + U * np.abs(hb - x))) + np.abs(dg) * (2.0 * k + 6.0) * U \
         + TINY * np.abs(es * (hb - x))
-    # a tree of sums with at most 256 additions on any path
-    bd["dgate_bias"] = bd["dg"].sum((0, 1)) + 256.0 * U * np.abs(dg).sum((0, 1))
+    bd["dgate_bias"] = bd["dg"].sum((0, 1)) + _bias_additions(Bt, T) * U * np.abs(dg).sum((0, 1))
     bd["dh0"] = F
     return out, bd
 
@@ -125,6 +130,13 @@ def _units(dim):
     """Additions on any path of a row's sum: at most 16 per register lane chain
     of dim / 64 values, and 16 across lanes and waves."""
     return dim / 64.0 + 24.0
+
+
+def _weight_additions(rows):
+    """Additions on any path of dweight: the rows that a lane walks (every 512th at
+    most), up to 32 rows side by side in a workgroup, up to 1024 workgroups' sums,
+    every 64th, and the stripes by halves."""
+    return -(-rows // 512) + 32 + 16 + 6
 
 
 def add_rms_norm(x, weight, residual=None, eps=1e-5, bounds=False):
@@ -152,7 +164,7 @@ def add_rms_norm_bwd(dy, r, weight, dresidual=None, eps=1e-5, bounds=False):
     k = 2.0 * _units(r.shape[-1]) + 16.0
     mag = rstd * (np.abs(w * dy) + np.abs(n) * np.abs(n * w * dy).mean(-1, keepdims=True))
     bdr = mag * k * U + np.abs(dr + add) * U
-    bdw = np.abs(dy * n).sum(0) * (0.5 * k + 256.0) * U
+    bdw = np.abs(dy * n).sum(0) * (0.5 * k + _weight_additions(len(r))) * U
     return dr + add, (dy * n).sum(0), bdr, bdw
 
 

@@ -115,3 +115,44 @@ def test_bounds_cover_an_fp32_evaluation():
         h = a * h + s * x[:, t]
         worst = max(worst, float((np.abs(h - y[:, t]) / ey[:, t]).max()))
     assert 1e-4 < worst < 0.25
+
+
+def column_sums(parts):
+    """fp32 sums of the columns: every 64th row one after the other, then the 64 stripes by halves."""
+    rows, dim = parts.shape
+    s = np.zeros((-(-rows // 64) * 64, dim), np.float32)
+    s[:rows] = parts
+    s = s.reshape(-1, 64, dim)
+    acc = np.zeros((64, dim), np.float32)
+    for r in s:
+        acc = acc + r
+    while len(acc) > 1:
+        acc = acc[0::2] + acc[1::2]
+    return acc[0]
+
+
+def test_bias_bound_counts_the_additions_of_a_large_batch():
+    """One large value and a thousand small ones in every stripe: each small one is lost where it is added."""
+    B = 65535
+    dg = np.where(np.arange(B) < 64, 1.0, 0.99 * 2.0 ** -24)
+    x, g = -np.ones((B, 1, 1)), np.zeros((B, 1, 1))            # a = 1 - a = 1/2, dg = dout / 4
+    want, bound = R.gated_scan_bwd(x, g, 4.0 * dg.reshape(B, 1, 1), bounds=True)
+    assert np.allclose(want["dgate_bias"], dg.sum(), rtol=1e-12)
+    got = column_sums(dg.astype(np.float32).reshape(B, 1))
+    assert 0.5 * bound["dgate_bias"] < np.abs(got - want["dgate_bias"]) < bound["dgate_bias"]
+
+
+def test_weight_bound_counts_the_additions_of_many_rows():
+    rows = 400000
+    dy = np.where(np.arange(rows) < 512, 1.0, 0.99 * 2.0 ** -24).reshape(rows, 1)
+    _, want, _, bound = R.add_rms_norm_bwd(dy, np.ones((rows, 1)), np.ones(1), eps=0.0, bounds=True)
+    acc = np.zeros((512, 1), np.float32)                         # a workgroup takes every 512th row
+    for i in range(0, rows, 512):
+        v = dy[i:i + 512].astype(np.float32)
+        acc[:len(v)] = acc[:len(v)] + v
+    assert 0.5 * bound[0] < abs(column_sums(acc)[0] - want[0]) < bound[0]
+
+
+def test_small_sizes_have_small_bounds():
+    """The additions are counted, not a blanket: 300 steps of two sequences take 31 of them on a path, 40 rows 55."""
+    assert R._bias_additions(2, 300) == 31 and R._weight_additions(40) == 55

@@ -427,3 +427,15 @@ def test_many_short_sequences(ops, B, T, D):
         torch.stack([c.double().square().sum((0, 1)) for c in got["dg"].split(4096)]).sum(0).sqrt()
     tol = 8 * 2.0 ** -8 * size + 2.0 ** -12 * got["dg"].abs().sum((0, 1), dtype=torch.float64)
     assert bool(((got["dgate_bias"].double() - total).abs() <= tol).all())
+
+
+def test_bias_gradient_of_the_largest_batch(ops):
+    """A thousand tiles' sums one after the other in each stripe, of one large value and small ones that are lost."""
+    B = 65535
+    dg = torch.where(torch.arange(B) < 64, 1.0, 0.99 * 2.0 ** -24).view(B, 1, 1).expand(B, 1, 3)
+    x, g, bias = -torch.ones(B, 1, 3, device="cuda"), torch.zeros(B, 1, 3, device="cuda"), torch.zeros(3, device="cuda")
+    dout = (4.0 * dg).cuda().contiguous()
+    got = ops.gated_scan_bwd(x, g, dout, gate_bias=bias)
+    want, bound = R.gated_scan_bwd(U.f64(x), U.f64(g), U.f64(dout), gate_bias=U.f64(bias), bounds=True)
+    for k in ("dx", "dg", "dgate_bias", "dh0"):
+        U.close(got[k], want[k], bound[k], k)
