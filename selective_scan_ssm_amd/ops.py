@@ -520,13 +520,17 @@ def _run(dev, fn, *args):
         return fn(*args, _raw_stream(index))
 
 
-def _scratch(need, what, workspace, dev):
+def _scratch(need, what, workspace, dev, status=False):
     """A workspace of `need` bytes: the caller's if it is large enough.  Returns
-    it (the caller holds it until the launch) and its address."""
+    it (the caller holds it until the launch) and its address.  status: the call
+    leaves an error word that scan_status reads in the caller's workspace, so a
+    smaller one is refused and not replaced."""
     if need == _BAD:
         raise RuntimeError(f"{what}: invalid arguments")
     if not need:
         return None, None
+    if status and workspace is not None and workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     return workspace, _arg(workspace, "workspace", torch.uint8, workspace.shape, dev)
@@ -535,6 +539,23 @@ def _scratch(need, what, workspace, dev):
 def gated_ckpt_shape(batch, seqlen, d_inner):
     """Shape of gated_scan_fwd's checkpoints: (batch, ceil(seqlen / 128), d_inner)."""
     return (batch, -(-seqlen // _lib.GATED_BLOCK), d_inner)
+
+
+def gated_scan_workspace_bytes(batch, seqlen, d_inner, dtype):
+    """Bytes of gated_scan_fwd's workspace (0 up to 128 steps)."""
+    return _gated_bytes(_lib.load().ssm_gated_scan_workspace_bytes, batch, seqlen, d_inner, dtype)
+
+
+def gated_scan_bwd_workspace_bytes(batch, seqlen, d_inner, dtype):
+    """Bytes of gated_scan_bwd's workspace, with or without ckpt."""
+    return _gated_bytes(_lib.load().ssm_gated_scan_bwd_workspace_bytes, batch, seqlen, d_inner, dtype)
+
+
+def _gated_bytes(fn, batch, seqlen, d_inner, dtype):
+    need = fn(batch, seqlen, d_inner, _IO[dtype])
+    if need == _BAD:
+        raise RuntimeError(f"{fn.__name__}: invalid arguments")
+    return need
 
 
 def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=False, out=None, last_state_out=None,
@@ -546,7 +567,9 @@ def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=Fals
     d_inner) fp32.  g = +inf keeps the state, g = -inf restarts it.  Returns y
     (same dtype as x) or (y, last_state fp32).  ckpt_out: an fp32 tensor of
     gated_ckpt_shape(...) that also receives the state entering every 128-step
-    block, for gated_scan_bwd(..., ckpt=ckpt_out)."""
+    block, for gated_scan_bwd(..., ckpt=ckpt_out).  workspace: a uint8 tensor of at
+    least gated_scan_workspace_bytes(...), allocated here without one; scan_status
+    reads the call's outcome in it (nothing is written up to 128 steps, which need none)."""
     lib = _lib.load()
     io, dev, shape = x.dtype, _device(x, "x"), x.shape
     if io not in _IO:
@@ -560,7 +583,7 @@ def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=Fals
     if return_last_state:
         last = last_state_out if last_state_out is not None else torch.empty((Bt, Dd), dtype=torch.float32, device=dev)
     ws, pws = _scratch(lib.ssm_gated_scan_workspace_bytes(Bt, T, Dd, _IO[io]), "ssm_gated_scan_workspace_bytes",
-                       workspace, dev)
+                       workspace, dev, status=True)
     rc = _run(dev, lib.ssm_gated_scan_fwd, px, ldx, pg, ldg, _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev), pz,
               ldz, _arg(h0, "h0", torch.float32, (Bt, Dd), dev), py,
               _arg(last, "last_state_out", torch.float32, (Bt, Dd), dev),
@@ -576,7 +599,8 @@ def gated_scan_bwd(x, g, dout, z=None, gate_bias=None, h0=None, dlast=None, ckpt
     Returns a dict: dx, dg (dtype of x), dh0 (fp32), and dz, dgate_bias (fp32)
     when z, gate_bias are given (None otherwise).  ckpt: what
     gated_scan_fwd(..., ckpt_out=) recorded on the same inputs; without it the
-    call reads x and g once more."""
+    call reads x and g once more.  workspace: as in gated_scan_fwd, of at least
+    gated_scan_bwd_workspace_bytes(...)."""
     lib = _lib.load()
     io, dev, shape = x.dtype, _device(x, "x"), x.shape
     if io not in _IO:
@@ -590,7 +614,7 @@ def gated_scan_bwd(x, g, dout, z=None, gate_bias=None, h0=None, dlast=None, ckpt
     dbias = new((Dd,), torch.float32) if gate_bias is not None else None
     dh0 = new((Bt, Dd), torch.float32)
     ws, pws = _scratch(lib.ssm_gated_scan_bwd_workspace_bytes(Bt, T, Dd, _IO[io]), "ssm_gated_scan_bwd_workspace_bytes",
-                       workspace, dev)
+                       workspace, dev, status=True)
     rc = _run(dev, lib.ssm_gated_scan_bwd, px, ldx, pg, ldg, _arg(gate_bias, "gate_bias", torch.float32, (Dd,), dev), pz,
               ldz, _arg(h0, "h0", torch.float32, (Bt, Dd), dev), _arg(dout, "dout", io, shape, dev),
               _arg(dlast, "dlast", torch.float32, (Bt, Dd), dev),

@@ -439,3 +439,18 @@ def test_bias_gradient_of_the_largest_batch(ops):
     want, bound = R.gated_scan_bwd(U.f64(x), U.f64(g), U.f64(dout), gate_bias=U.f64(bias), bounds=True)
     for k in ("dx", "dg", "dgate_bias", "dh0"):
         U.close(got[k], want[k], bound[k], k)
+
+
+def test_a_small_workspace_is_refused(ops):
+    """Not replaced: its status word would never be written."""
+    t = inputs(2, 300, 64, torch.bfloat16)
+    kw = dict(z=t["z"], gate_bias=t["gate_bias"], h0=t["h0"])
+    dout = U.rand(1, 2, 300, 64, dtype=torch.bfloat16)
+    for fn, need in ((lambda ws: ops.gated_scan_fwd(t["x"], t["g"], workspace=ws, **kw), ops.gated_scan_workspace_bytes),
+                     (lambda ws: ops.gated_scan_bwd(t["x"], t["g"], dout, workspace=ws, **kw)["dx"], ops.gated_scan_bwd_workspace_bytes)):
+        n = need(2, 300, 64, torch.bfloat16)
+        ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+        with pytest.raises(ValueError, match="are needed"):
+            fn(ws[:n - 1])
+        assert bool((ws == 0xff).all())
+        assert torch.equal(fn(ws), fn(None)) and ops.scan_status(ws) == 0
