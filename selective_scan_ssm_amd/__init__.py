@@ -7,7 +7,8 @@ The wrappers are imported lazily so that `selective_scan_ssm_amd.inputs`
 (seeded synthetic inputs) can be used without torch or the built library.
 """
 
-__all__ = ["scan_fwd", "sm1_scan_fwd", "state_update", "gated_scan_fwd", "gated_scan_bwd", "gated_state_update",
+__all__ = ["scan_fwd", "sm1_scan_fwd", "state_update", "scan_status", "gated_scan_fwd", "gated_scan_bwd",
+           "gated_state_update", "gated_ckpt_shape", "gated_scan_workspace_bytes", "gated_scan_bwd_workspace_bytes",
            "add_rms_norm", "add_rms_norm_quant", "add_rms_norm_bwd", "grad_norm", "clip_grads"]
 
 

@@ -39,3 +39,12 @@ def test_workspace_sizes(ops):
     for fn in (ops.gated_scan_workspace_bytes, ops.gated_scan_bwd_workspace_bytes):
         with pytest.raises(RuntimeError, match="invalid arguments"):
             fn(-1, 128, 64, torch.float32)
+
+
+def test_the_package_exports_what_the_block_needs(ops):
+    import selective_scan_ssm_amd as package
+    for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_state_update", "gated_ckpt_shape", "gated_scan_workspace_bytes",
+                 "gated_scan_bwd_workspace_bytes", "add_rms_norm", "add_rms_norm_quant", "add_rms_norm_bwd", "grad_norm",
+                 "clip_grads", "scan_status"):
+        assert name in package.__all__ and getattr(package, name) is getattr(ops, name), name
+    assert package.gated_ckpt_shape(2, 129, 8) == (2, 2, 8)
