@@ -83,7 +83,7 @@ typedef enum {
     SSM_ERR_ALIAS = -7,     /* an output overlaps an input                      */
     SSM_ERR_WAIT = -8,      /* a segment's bounded wait gave up (ssm_scan_status) */
     SSM_ERR_SCRATCH = -9,   /* the shape needs more than SSM_SCRATCH_BYTES (noalloc) */
-    SSM_ERR_VALUE = -10,    /* eps or max_norm is negative or not finite          */
+    SSM_ERR_VALUE = -10,    /* eps is negative or not finite, or max_norm negative or NaN */
     SSM_ERR_HOST = -11      /* host memory for checking a list could not be had   */
 } ssm_status_t;
 

@@ -88,7 +88,7 @@ const char *ssm_status_string(int status) {
     case SSM_ERR_ALIAS: return "SSM_ERR_ALIAS: an output overlaps an input";
     case SSM_ERR_WAIT: return "SSM_ERR_WAIT: a segment's bounded wait gave up; that call's outputs are invalid";
     case SSM_ERR_SCRATCH: return "SSM_ERR_SCRATCH: the shape needs more scratch than SSM_SCRATCH_BYTES (ssm_scan_fwd_noalloc)";
-    case SSM_ERR_VALUE: return "SSM_ERR_VALUE: a scalar argument is negative or not finite";
+    case SSM_ERR_VALUE: return "SSM_ERR_VALUE: eps is negative or not finite, or max_norm is negative or NaN";
     case SSM_ERR_HOST: return "SSM_ERR_HOST: host memory for checking a list could not be had";
     default: return "unknown ssm status";
     }

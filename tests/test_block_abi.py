@@ -290,3 +290,14 @@ def test_gated_largest_sizes(lib, batch, seqlen, dim, code):
     if code == ESHAPE:
         a = scan_args(batch=batch, seqlen=seqlen, dim=dim, ldx=dim, ldg=dim, ldz=dim)
         assert fwd(lib, a) == bwd(lib, a) == ESHAPE
+
+
+def test_the_value_status_says_what_is_refused(lib):
+    """An infinite max_norm is no limit and accepted; a NaN or negative one, and an eps that is not finite, are not."""
+    said = lib.ssm_status_string(EVALUE).decode()
+    assert "eps is negative or not finite" in said and "max_norm is negative or NaN" in said
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ssm_scan.h")).read()
+    assert "eps is negative or not finite, or max_norm negative or NaN" in header
+    kw = dict(ptrs=[P], numel=[4], dtypes=[0], ws=None)
+    assert clip(lib, max_norm=float("inf"), **kw) == EWS                  # past the check of values
+    assert clip(lib, max_norm=float("nan"), **kw) == clip(lib, eps=float("nan"), **kw) == EVALUE
