@@ -41,3 +41,14 @@ def guarded(shape, dtype, pad=512):
     def check():
         assert bool((buf[:pad].float() == 7.0).all()) and bool((buf[pad + n:].float() == 7.0).all()), "written outside"
     return inner, check
+
+
+def along_its_signs(loss, inputs, name, grad, h, noise):
+    """Central differences of loss(inputs) along the signs of its gradient by inputs[name]: returns the difference to
+    sum |grad|, where every value counts with its full weight, and what is allowed of it: 1e-4 for the third
+    derivative (h = 0.02 leaves up to 5e-5 of the recurrence's, in 64 bits), and 4 times `noise`, the loss's
+    rounding in quadrature, for each of the two losses."""
+    sign = (grad < 0) * -2.0 + 1.0
+    hi, lo = ({**inputs, name: inputs[name] + d * sign} for d in (h, -h))
+    want = abs(grad).sum()
+    return abs((loss(hi) - loss(lo)) / (2 * h) - want), 1e-4 * want + 4 * 2 ** 0.5 * noise / (2 * h)

@@ -156,3 +156,25 @@ def test_weight_bound_counts_the_additions_of_many_rows():
 def test_small_sizes_have_small_bounds():
     """The additions are counted, not a blanket: 300 steps of two sequences take 31 of them on a path, 40 rows 55."""
     assert R._bias_additions(2, 300) == 31 and R._weight_additions(40) == 55
+
+
+def test_differences_along_the_signs_reject_a_gradient_one_percent_off():
+    from block_util import along_its_signs
+    f = lambda seed, *shape: torch.randn(shape, generator=torch.Generator().manual_seed(seed)).double().numpy()
+    B, T, D = 2, 300, 64
+    t = dict(x=f(0, B, T, D), g=f(1, B, T, D), z=f(2, B, T, D), gate_bias=np.abs(f(5, D)) * 2.5, h0=f(6, B, D))
+    dout, dlast = f(90, B, T, D), f(91, B, D)
+    got = R.gated_scan_bwd(t["x"], t["g"], dout, t["z"], t["gate_bias"], t["h0"], dlast)
+    _, _, ey, el = R.gated_scan(**t, bounds=True)
+    noise = np.sqrt(((ey * dout) ** 2).sum() + ((el * dlast) ** 2).sum())
+
+    def loss(a):
+        y, last = R.gated_scan(**a)
+        return (y * dout).sum() + (last * dlast).sum()
+
+    for name in t:
+        off, allowed = along_its_signs(loss, t, name, got["d" + name], 0.02, noise)
+        assert off <= allowed, name
+        for factor in (0.99, 1.01):
+            off, allowed = along_its_signs(loss, t, name, got["d" + name] * factor, 0.02, noise)
+            assert off > allowed, (name, factor)

@@ -454,3 +454,20 @@ def test_a_small_workspace_is_refused(ops):
             fn(ws[:n - 1])
         assert bool((ws == 0xff).all())
         assert torch.equal(fn(ws), fn(None)) and ops.scan_status(ws) == 0
+
+
+def test_gradient_by_differences_along_its_signs(ops):
+    """As above where no terms cancel: a gradient that is off by 1% fails (test_block_oracle.py shows that it would)."""
+    t = {k: v for k, v in inputs(2, 300, 64, torch.float32).items()}
+    dout, dlast = U.rand(90, 2, 300, 64), U.rand(91, 2, 64)
+    got = ops.gated_scan_bwd(t["x"], t["g"], dout, z=t["z"], gate_bias=t["gate_bias"], h0=t["h0"], dlast=dlast)
+
+    def loss(a):
+        y, last = ops.gated_scan_fwd(a["x"], a["g"], z=a["z"], gate_bias=a["gate_bias"], h0=a["h0"], return_last_state=True)
+        return float((y.double() * dout).sum() + (last.double() * dlast).sum())
+
+    _, _, ey, el = R.gated_scan(**host(t), bounds=True)
+    noise = np.sqrt(((ey * U.f64(dout)) ** 2).sum() + ((el * U.f64(dlast)) ** 2).sum())
+    for name in ("x", "g", "z", "gate_bias", "h0"):
+        off, allowed = U.along_its_signs(loss, t, name, got["d" + name].double(), 0.02, noise)
+        assert float(off) <= float(allowed) < 0.006 * float(got["d" + name].double().abs().sum()), name
