@@ -585,6 +585,8 @@ size_t ssm_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
  *     norm = sqrt(sum over all tensors of g^2)            (64-bit sums)
  *     coef = min(1, max_norm / (norm + eps))              (a NaN norm gives NaN)
  *     out  = g * coef                                     (rounded to out's dtype)
+ *   coef is 1 wherever norm + eps <= max_norm, also with both infinite or both 0.
+ *   Finite gradients whose norm fp32 does not hold are scaled by the 64-bit norm.
  *   grads, outs    : HOST arrays of device pointers (NULL entries only where
  *                    numel is 0); numel, dtypes, out_dtypes: host arrays.  All
  *                    are read before the call returns.  outs NULL: in place.

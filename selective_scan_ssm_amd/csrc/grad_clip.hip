@@ -227,19 +227,23 @@ __device__ __forceinline__ void sumsq(const Entry *tab, int count, int64_t total
 }
 
 // every workgroup adds the partial sums, in the same order
-__device__ __forceinline__ float norm_of(const double *part, int parts) {
+__device__ __forceinline__ double norm_of(const double *part, int parts) {
     double s = 0.0;
 #pragma unroll 8
     for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
-    return static_cast<float>(sqrt(block_sum(s)));
+    return sqrt(block_sum(s));
 }
 
 __device__ __forceinline__ void clip(const Entry *tab, int count, int64_t total, int64_t run, const double *part, int parts,
                                      float max_norm, float eps, float *norm, int in_place) {
-    const float value = norm_of(part, parts);
+    const double wide = norm_of(part, parts);
+    const float value = static_cast<float>(wide);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = value;
-    float coef = max_norm / (value + eps);
-    coef = coef > 1.0f ? 1.0f : coef;                  // false for NaN, which stays
+    // finite gradients may have a norm past fp32; at or below the limit nothing is
+    // divided, so no 0 / 0 or inf / inf; a NaN norm fails both tests and stays
+    const float coef = value + eps <= max_norm         ? 1.0f
+                       : value == __builtin_inff()     ? static_cast<float>(max_norm / wide)
+                                                       : max_norm / (value + eps);
     if (coef == 1.0f && in_place) return;              // nothing changes
     walk(tab, count, total, run, [&](const Entry &e, int64_t i0, int64_t n, int t, int threads) {
         if (coef == 1.0f && e.out == e.in) return;
@@ -268,8 +272,8 @@ __global__ __launch_bounds__(kThreads) void clip_long_kernel(const Entry *tab, i
     clip(tab, count, total, run, part, parts, max_norm, eps, norm, in_place);
 }
 __global__ __launch_bounds__(kThreads) void norm_kernel(const double *part, int parts, float *norm) {
-    const float v = norm_of(part, parts);
-    if (threadIdx.x == 0) *norm = v;
+    const double v = norm_of(part, parts);
+    if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 __global__ __launch_bounds__(kThreads) void table_kernel(Table t, int count, Entry *tab) {
     if (static_cast<int>(threadIdx.x) < count) tab[threadIdx.x] = t.e[threadIdx.x];

@@ -151,3 +151,36 @@ def test_refusals(ops):
                 lambda: ops.clip_grads([g[0], g[1].cpu()], 1.0)):
         with pytest.raises((ValueError, RuntimeError)):
             bad()
+
+
+@pytest.mark.parametrize("limit", [1e38, 1.0])
+def test_a_norm_past_fp32_still_scales(ops, limit):
+    """Finite gradients whose norm fp32 does not hold: the norm is written as infinite, the coefficient is the formula's."""
+    make = lambda: [torch.full((4000,), 3e38, device="cuda"), torch.full((33,), -2e38, device="cuda").to(BF16), U.rand(1, 7)]
+    g = make()
+    host = [U.f64(t) for t in g]
+    norm, coef = R.clip(host, limit)
+    assert norm > 3.5e38
+    out = [torch.empty(t.shape, device="cuda") for t in g]
+    assert float(ops.grad_norm(g)) == float("inf") and float(ops.clip_grads(g, limit, out=out)) == float("inf")
+    own = make()
+    ops.clip_grads(own, limit)
+    for o, p, h in zip(out, own, host):
+        # a coefficient below 2^-126 is held to 2^-150
+        U.close(o, h * coef, np.abs(h) * (6 * R.U * coef + 2.0 ** -150))
+        U.close(p, h * coef, np.abs(h) * (6 * R.U * coef + 2.0 ** -150))
+
+
+def test_nothing_changes_at_or_below_the_limit_whatever_it_is(ops):
+    """norm + eps <= max_norm, also where the quotient is 0 / 0 or inf / inf."""
+    zero = [torch.zeros(100, device="cuda"), torch.zeros(9, dtype=BF16, device="cuda")]
+    assert float(ops.clip_grads(zero, 0.0, eps=0.0)) == 0.0 and not any(bool(t.any()) or bool(t.isnan().any()) for t in zero)
+    for first in (float("inf"), 3e38):
+        g = [U.rand(1, 5000), U.rand(2, 70, dtype=BF16)]
+        g[0][:40] = first
+        keep = [t.clone() for t in g]
+        assert float(ops.clip_grads(g, float("inf"))) == float("inf")
+        assert all(torch.equal(a, b) for a, b in zip(g, keep))
+    g[1][3] = float("nan")
+    ops.clip_grads(g, float("inf"))
+    assert all(bool(t.isnan().all()) for t in g)
