@@ -440,7 +440,8 @@ size_t ssd_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, i
  * from h0[b,d] (or 0); last_state[b,d] = h after the last step (h0 when
  * seqlen = 0).  An infinite gate is exact: g = +inf keeps the state (the way
  * to pad a batch of unequal lengths), g = -inf restarts it (h = x: the way to
- * pack several sequences into one row); x has to be finite there.
+ * pack several sequences into one row).  x has to be finite at such a step, and
+ * the state that a restart leaves behind too: 0 times an infinity or a NaN is NaN.
  *   x, g, z      : (batch, seqlen, d_inner) io dtype; step (b, t) starts
  *                  ldx, ldg, ldz elements after the one before it, so each may
  *                  be a column range of a wider tensor (ld >= d_inner when there
@@ -527,7 +528,8 @@ int ssm_gated_state_update(float *state, const void *x, const void *g, const flo
  *   residual_out : (rows, dim) residual dtype, optional: r rounded to it.  It
  *                  may be residual itself (updated in place); no other overlap.
  *   residual dtype: SSM_F32, or the io dtype.  r is normalised in fp32 before
- *   it is rounded.  eps finite and >= 0 (SSM_ERR_VALUE).  dim in
+ *   it is rounded; a row whose sum of squares passes fp32 (values around 1e19)
+ *   comes out as 0.  eps finite and >= 0 (SSM_ERR_VALUE).  dim in
  *   [1, SSM_MAX_NORM_DIM].
  */
 #define SSM_MAX_NORM_DIM 32768

@@ -394,8 +394,14 @@ hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
 
 // The chunks per lane and waves per row for a width, in units of 512 elements
 // (V = 8 or 4) or 64 (V = 1).  Few waves to a row as far as the registers go, as
-// waves that share one wait for each other at every reduction.  40M elements, us:
-//   forward   2560 wide, fp32 residual   one wave 178   four 186   (32768 rows)
+// waves that share one wait for each other at every reduction.  44M elements, us,
+// aligned rows (bf16 / the same to 8 bits / fp32):
+//   forward   1536 wide                  one wave 63 / 57 / 123   four 70 / 87 / 129
+//             2048 wide                  one 62 / 57 / 121        four 66 / 62 / 122
+//             2560 wide                  one 64 / 57 / 123        four 67 / 61 / 124
+//             3584 wide                  one 65 / 59 / 122        four 64 / 58 / 124
+//             4096 wide                  one 64 / 58 / 137        four 62 / 56 / 118
+// 40M elements, us:
 //             1537 wide, bf16            one 70         four 87    sixteen 110
 //             2561 wide, bf16 / 8 bits   four 86 / 77   sixteen 81 / 92
 //   gradient  1280 wide, bf16            one 46         four 81
@@ -404,7 +410,8 @@ hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
 //             2561 wide, fp32            four 91        sixteen 103
 //             2048 wide, fp32            one 89         four 81
 // Above 16384 wide sixteen waves do not hold a gradient's row: up to 92 registers
-// are spilled.
+// are spilled, and 44M elements take 225 us (bf16, 32768 wide) instead of 72 (16384
+// wide), in fp32 240 instead of 107.
 #define SSM_FWD_PICK(CALL, V)                                                      \
     return units <= 1    ? CALL(V, 8 / V, 1)                                       \
            : units <= 2  ? CALL(V, 16 / V, 1)                                      \

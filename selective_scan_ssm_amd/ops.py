@@ -564,7 +564,8 @@ def gated_scan_fwd(x, g, z=None, gate_bias=None, h0=None, return_last_state=Fals
     y = h SiLU(z) (y = h without z).  x, g, z: (batch, seqlen, d_inner) fp32 or
     bf16 with a contiguous last axis and evenly strided rows (thirds of one
     projection's output need no copy); gate_bias: (d_inner,) fp32; h0: (batch,
-    d_inner) fp32.  g = +inf keeps the state, g = -inf restarts it.  Returns y
+    d_inner) fp32.  g = +inf keeps the state, g = -inf restarts it (x finite at
+    such a step, and the state that a restart leaves behind).  Returns y
     (same dtype as x) or (y, last_state fp32).  ckpt_out: an fp32 tensor of
     gated_ckpt_shape(...) that also receives the state entering every 128-step
     block, for gated_scan_bwd(..., ckpt=ckpt_out).  workspace: a uint8 tensor of at
@@ -803,7 +804,7 @@ def clip_grads(grads, max_norm, out=None, eps=1e-6, norm_out=None, workspace=Non
     """Scales a list of contiguous fp32 / bf16 tensors by min(1, max_norm /
     (norm + eps)), norm being grad_norm(grads): in place, or into the tensors
     of `out` (same numbers of elements, fp32 or bf16 each: an optimizer's fp32 gradients
-    from bf16 ones).  Returns the norm before clipping.  The host never waits."""
+    from bf16 ones).  An infinite max_norm is no limit.  Returns the norm before clipping.  The host never waits."""
     if max_norm is None:
         raise ValueError("max_norm must be a number")
     return _clip(grads, float(max_norm), out, float(eps), norm_out, workspace)
