@@ -452,8 +452,8 @@ size_t ssd_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, i
  *   ckpt         : optional output, fp32 (batch, ceil(seqlen / 128), d_inner):
  *                  ckpt[b,j,d] is the state entering step 128 j, for
  *                  ssm_gated_scan_bwd; 4-byte aligned
- *   Sizes (SSM_ERR_SHAPE): batch <= 65535; 128 steps of a row stride (128 * ld
- *   elements) span less than 2 GiB; batch * ceil(d_inner / 64) * ceil(seqlen / 128)
+ *   Sizes (SSM_ERR_SHAPE): batch <= 65535; up to 128 steps of a sequence
+ *   (min(seqlen, 128) * ld elements) span less than 2 GiB; batch * ceil(d_inner / 64) * ceil(seqlen / 128)
  *   workgroups of 64 lanes (up to 16 steps), 128 (32), 256 (64) or 512 have fewer
  *   than 2^32 lanes.  Workspace: ssm_gated_scan_workspace_bytes, 256-byte
  *   aligned (NULL when that is 0).  Calls that overlap in time need workspaces

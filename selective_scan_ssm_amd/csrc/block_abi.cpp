@@ -46,10 +46,10 @@ int check_gated_inputs(const ssm::GatedArgs &a, int io) {
     const size_t es = io_size(io);
     const int64_t steps = a.batch * a.seqlen;
     const int64_t lds[] = {a.ldx, a.ldg, a.z ? a.ldz : a.dim};
+    const int64_t block = a.seqlen < ssm::kGatedBlock ? a.seqlen : ssm::kGatedBlock;
     for (int64_t ld : lds) {
         if (steps > 1 && ld < a.dim) return SSM_ERR_SHAPE;
-        if (steps > 1 && (mul3(ssm::kGatedBlock, ld, es) < 0 || mul3(ssm::kGatedBlock, ld, es) > kMaxSpan ||
-                          mul3(steps, ld, es) < 0))
+        if (steps > 1 && (mul3(block, ld, es) < 0 || mul3(block, ld, es) > kMaxSpan || mul3(steps, ld, es) < 0))
             return SSM_ERR_SHAPE;
     }
     if (steps > 0 && (!a.x || !a.g)) return SSM_ERR_NULL;

@@ -301,3 +301,13 @@ def test_the_value_status_says_what_is_refused(lib):
     kw = dict(ptrs=[P], numel=[4], dtypes=[0], ws=None)
     assert clip(lib, max_norm=float("inf"), **kw) == EWS                  # past the check of values
     assert clip(lib, max_norm=float("nan"), **kw) == clip(lib, eps=float("nan"), **kw) == EVALUE
+
+
+def test_gated_row_strides_of_short_sequences(lib):
+    """The first step of each of a batch's long rows is far from the next one's; a sequence itself spans little."""
+    far = dict(batch=2, dim=8, ws=None, last=None, ckpt=0x7f0000000001)          # refused after the sizes are accepted
+    for seqlen, ld, code in ((1, (1 << 29) - 1, EALIGN), (1, 1 << 29, ESHAPE), (5, 107374182, EALIGN), (5, 107374183, ESHAPE),
+                             (128, (1 << 22) - 1, EALIGN), (128, 1 << 22, ESHAPE), (4000, (1 << 22) - 1, EALIGN),
+                             (4000, 1 << 22, ESHAPE)):
+        a = scan_args(seqlen=seqlen, ldx=ld, ldg=ld, ldz=ld, **far)
+        assert fwd(lib, a) == code and bwd(lib, a) == code, (seqlen, ld)

@@ -471,3 +471,19 @@ def test_gradient_by_differences_along_its_signs(ops):
     for name in ("x", "g", "z", "gate_bias", "h0"):
         off, allowed = U.along_its_signs(loss, t, name, got["d" + name].double(), 0.02, noise)
         assert float(off) <= float(allowed) < 0.006 * float(got["d" + name].double().abs().sum()), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 3])
+def test_a_few_steps_far_apart(ops, dtype, T):
+    """A few steps of each sequence far apart in one wide buffer: 100 MB and more from row to row."""
+    B, D = 3, 66
+    flat = torch.empty(B * 150 << 20, dtype=DT[dtype], device="cuda")
+    step = flat.numel() // (B * T)
+    x, g, z = (flat.as_strided((B, T, D), (T * step, step, 1), i * 1000 + 7) for i in range(3))
+    for i, t in enumerate((x, g, z)):
+        t.copy_(U.rand(i, B, T, D))
+    assert 128 * step * x.element_size() >= 1 << 31               # more than 128 such rows could span
+    t = dict(x=x, g=g, z=z, gate_bias=U.rand(5, D).abs(), h0=U.rand(6, B, D))
+    check_fwd(ops, t)
+    check_bwd(ops, t)
