@@ -666,7 +666,7 @@ def _norm_residual(x, io, residual, residual_dtype, residual_out, dev):
 def add_rms_norm(x, weight, residual=None, eps=1e-5, residual_dtype=None, out=None, residual_out=None):
     """r = x + residual, y = r / sqrt(mean(r^2) + eps) * weight over the last
     axis.  x: (..., dim) fp32 or bf16, rows evenly strided; weight: (dim,) fp32;
-    residual: like x, in x's dtype or fp32.  Returns (y, r): y in x's dtype, r
+    residual: x's shape, contiguous, in x's dtype or fp32.  Returns (y, r): y in x's dtype, r
     in the residual's (residual_dtype when there is no residual; without either
     r is None, as it would be x itself).  residual_out may be residual, which is
     then updated in place."""
