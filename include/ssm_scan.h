@@ -34,8 +34,8 @@
  *     that size is 0); its contents need not be initialised and are garbage
  *     after the call.
  *   - Aliasing: no output may overlap any input (y, last_state vs x, delta,
- *     z, B, C, h0 ...), except the `state` of ssm_state_update and of
- *     ssm_gated_state_update, which is updated in place by design, and what
+ *     z, B, C, h0 ...), except the `state` of ssm_state_update,
+ *     ssm_gated_state_update and ssm_delta_state_update, which is updated in place by design, and what
  *     ssm_add_rms_norm_* and ssm_grad_clip say of theirs.
  *   - Streams: work is enqueued on `stream` (a hipStream_t; NULL = the null
  *     stream) and the call returns without waiting.  The caller synchronises.
@@ -48,8 +48,8 @@
  *     seqlen == 0 writes last_state := h0 (or zeros) and leaves y untouched.
  *   - Alignment: every pointer must be aligned to its element size (4 bytes
  *     for fp32 tensors, 2 bytes for bf16 tensors), else SSM_ERR_ALIGN; the
- *     workspaces of ssm_gated_scan_*, ssm_add_rms_norm_bwd and ssm_grad_* to
- *     256 bytes.
+ *     workspaces of ssm_gated_scan_*, ssm_add_rms_norm_bwd, ssm_grad_*,
+ *     ssm_delta_scan_* and ssm_group_norm_* to 256 bytes.
  *   - Thread safety: the entry points may be called concurrently on different
  *     streams -- except ssm_scan_fwd_noalloc, whose calls share one scratch
  *     array per GPU (see there).  Their only global state is created once
@@ -83,7 +83,7 @@ typedef enum {
     SSM_ERR_ALIAS = -7,     /* an output overlaps an input                      */
     SSM_ERR_WAIT = -8,      /* a segment's bounded wait gave up (ssm_scan_status) */
     SSM_ERR_SCRATCH = -9,   /* the shape needs more than SSM_SCRATCH_BYTES (noalloc) */
-    SSM_ERR_VALUE = -10,    /* eps is negative or not finite, or max_norm negative or NaN */
+    SSM_ERR_VALUE = -10,    /* eps is negative or not finite, max_norm negative or NaN, or scale not finite */
     SSM_ERR_HOST = -11      /* host memory for checking a list could not be had   */
 } ssm_status_t;
 
@@ -610,6 +610,150 @@ int ssm_grad_clip(const void *const *grads, void *const *outs, const int64_t *nu
 /* Workspace bytes both need for a list of `count` tensors; (size_t)-1 for an
  * invalid count. */
 size_t ssm_grad_norm_workspace_bytes(int64_t count);
+
+/*
+ * ssm_delta_scan_fwd -- the gated delta rule: a multi-head scan whose matrix
+ * state is corrected instead of only added to (the multi-head state of the
+ * youngju.dev guide, section 6 "Mamba 2", with a decay per step and head, and
+ * with what the state already holds under a step's key taken out before the
+ * step's value goes in).  Per sequence and value head h, with key head
+ * h / (nheads / nkheads) and the state s (headdim, dstate):
+ *     s  <- exp(g[t,h]) s
+ *     r   = v[t,h,:] - s k[t,:]
+ *     s  <- s + beta[t,h] r k[t,:]^T
+ *     y[t,h,:] = scale s q[t,:]
+ * from h0 (or 0); last_state is s after the last step (h0 where there is none).
+ * Evaluated in chunks of 64 steps on the matrix cores.
+ *   q, k : (batch, seqlen, nkheads, dstate) io dtype;  v : (batch, seqlen, nheads,
+ *          headdim) io dtype; steps are ldq, ldk, ldv elements apart, so each may
+ *          be a column range of a wider tensor (heads side by side in it)
+ *   g, beta : (batch, seqlen, nheads) fp32, contiguous.  g is the logarithm of the
+ *          decay, g <= 0 for one that does not grow; at and below -104 the decay is
+ *          0, so -inf restarts the state.  beta = 0 and g = 0 leave the state as it
+ *          is.  Keys of length at most 1 and beta in [0, 2] keep it bounded.
+ *   h0, last_state : (sequences, nheads, headdim, dstate) fp32, optional
+ *   y    : (batch, seqlen, nheads, headdim) io dtype, contiguous
+ *   ckpt : optional output, fp32, ssm_delta_ckpt_bytes: the states entering the
+ *          chunks, for ssm_delta_scan_bwd
+ *   starts : NULL: `batch` sequences of `seqlen` steps (nseq is not used).
+ *          Otherwise nseq + 1 int32 on the device, ascending, in [0, seqlen], and
+ *          batch == 1: sequence i is the rows starts[i] .. starts[i + 1] - 1 (none
+ *          where they are equal).  Rows outside every sequence are not read, and
+ *          outputs are not written there.  Starts out of order or range are brought
+ *          into it one by one: the outputs are then undefined, but no access leaves
+ *          the tensors.
+ *   Not finite values in a step of q, k, v, g or beta make the outputs of its chunk
+ *   and of the rest of its sequence undefined, those of its chunk's earlier steps
+ *   too; other sequences and heads are not touched by them.
+ *   Sizes (SSM_ERR_SHAPE): nheads a multiple of nkheads; dstate a multiple of 8 up
+ *   to 128; headdim a multiple of 8; ld* a multiple of 16 bytes and at least the
+ *   heads' width where there is more than one step; 64 steps of each tensor span
+ *   less than 2 GiB (of v and y, of a state too, in fp32); fewer than 2^24 workgroups, one per
+ *   chunk (or sequence), head and 64 channels.  scale finite (SSM_ERR_VALUE).  All tensors
+ *   16-byte aligned but g, beta and starts.  Workspace:
+ *   ssm_delta_scan_workspace_bytes, 256-byte aligned.  Sums are added in a fixed
+ *   order: results are deterministic.
+ */
+int ssm_delta_scan_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                       const float *g, const float *beta, float scale, const float *h0,
+                       const int32_t *starts, int64_t nseq, void *y, float *last_state, float *ckpt,
+                       int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t dstate,
+                       int64_t headdim, int io_dtype, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* Workspace bytes ssm_delta_scan_fwd needs (packed: whether starts are given);
+ * (size_t)-1 for invalid arguments. */
+size_t ssm_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nseq,
+                                      int64_t nkheads, int64_t nheads, int64_t dstate, int64_t headdim,
+                                      int io_dtype);
+
+/* Bytes of the states entering the chunks: slots x nheads x headdim x dstate fp32
+ * with batch * ceil(seqlen / 64) slots, or seqlen / 64 + nseq packed, where chunk j
+ * of sequence i is slot starts[i] / 64 + i + j (quotients rounded down; a few slots
+ * stay unused).  (size_t)-1 for invalid arguments. */
+size_t ssm_delta_ckpt_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nseq, int64_t nheads,
+                            int64_t dstate, int64_t headdim);
+
+/*
+ * ssm_delta_scan_bwd -- the gradient of ssm_delta_scan_fwd, exactly as defined.
+ *   Inputs: the forward's, plus
+ *     dout  : like y (contiguous)                      -- dL/dy
+ *     dlast : like last_state, optional                -- dL/dlast_state
+ *     ckpt  : what ssm_delta_scan_fwd recorded on the same inputs, or NULL: the
+ *             call then walks the chunks once more
+ *   Outputs (overwritten): dq, dk like q, k but contiguous, summed over the heads
+ *   that share a key head; dv like v, contiguous; dg, dbeta fp32; all required.
+ *   dh0 optional (written even when h0 is NULL).
+ *   Workspace: ssm_delta_scan_bwd_workspace_bytes (`saved`: whether ckpt is
+ *   given), 256-byte aligned.  Sums are added in a fixed order.
+ */
+int ssm_delta_scan_bwd(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                       const float *g, const float *beta, float scale, const float *h0,
+                       const int32_t *starts, int64_t nseq, const void *dout, const float *dlast,
+                       const float *ckpt, void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                       float *dh0, int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                       int64_t dstate, int64_t headdim, int io_dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+size_t ssm_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nseq,
+                                          int64_t nkheads, int64_t nheads, int64_t dstate,
+                                          int64_t headdim, int saved, int io_dtype);
+
+/*
+ * ssm_delta_state_update -- one decode token of the same rule: state (batch,
+ * nheads, headdim, dstate) fp32 is read and overwritten in place; q, k (batch,
+ * nkheads, dstate), v, y (batch, nheads, headdim) io dtype, g, beta (batch,
+ * nheads) fp32, all contiguous.  Sizes and alignment as above.
+ */
+int ssm_delta_state_update(float *state, const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, float scale, void *y, int64_t batch, int64_t nkheads,
+                           int64_t nheads, int64_t dstate, int64_t headdim, int io_dtype, void *stream);
+
+/*
+ * ssm_group_norm_fwd -- group norm over channels-last tensors, with an activation
+ * and a gate: the output norm of a multi-head mixer (rows = 1: every token's heads
+ * are normalised apart, then gated as in the youngju.dev guide, section 5) and the
+ * norm of feature maps (rows = height * width of a patch grid, section 9).  A group
+ * is dim / groups neighbouring channels over all rows of a batch entry:
+ *     n = (x - mean) / sqrt(var + eps)       (var: the mean of (x - mean)^2)
+ *     a = n * weight + bias
+ *     y = act(a) * SiLU(z)                   (act: SiLU if silu, else a; no factor without z)
+ *   x, z : (batch, rows, dim) io dtype, rows (in all: batch * rows of them) ldx,
+ *          ldz elements apart; z optional
+ *   weight, bias : (dim) fp32, optional (1 and 0)
+ *   y    : (batch, rows, dim) io dtype, contiguous
+ *   mean, rstd : (batch, groups) fp32, optional outputs: what the gradient takes
+ *   dim in [1, SSM_MAX_GROUP_DIM], a multiple of groups; eps finite and >= 0
+ *   (SSM_ERR_VALUE).  Sums of a group over several rows are fp64.  Workspace:
+ *   ssm_group_norm_workspace_bytes, 256-byte aligned (NULL when that is 0).
+ *   batch * rows == 0: nothing is enqueued.
+ */
+#define SSM_MAX_GROUP_DIM 1048576
+int ssm_group_norm_fwd(const void *x, int64_t ldx, const void *z, int64_t ldz, const float *weight,
+                       const float *bias, void *y, float *mean, float *rstd, int64_t batch, int64_t rows,
+                       int64_t dim, int64_t groups, float eps, int silu, int io_dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Workspace bytes; (size_t)-1 for invalid arguments. */
+size_t ssm_group_norm_workspace_bytes(int64_t batch, int64_t rows, int64_t dim, int64_t groups);
+
+/*
+ * ssm_group_norm_bwd -- the gradient of ssm_group_norm_fwd at the mean and rstd it
+ * returned (taken as functions of x).  With da = dL/da:
+ *     dx = rstd (weight da - mean(weight da) - n mean(weight da n))
+ *     dz = dy act(a) SiLU'(z),  dweight = sum da n,  dbias = sum da
+ *   dy (batch, rows, dim) io dtype, contiguous; dx the same, required; dz the same,
+ *   required when z is given; dweight, dbias (dim) fp32, optional (written even
+ *   when weight, bias are NULL).  Workspace: ssm_group_norm_bwd_workspace_bytes.
+ *   Sums are added in a fixed order.  batch * rows == 0 gives zero dweight, dbias.
+ */
+int ssm_group_norm_bwd(const void *dy, const void *x, int64_t ldx, const void *z, int64_t ldz,
+                       const float *weight, const float *bias, const float *mean, const float *rstd,
+                       void *dx, void *dz, float *dweight, float *dbias, int64_t batch, int64_t rows,
+                       int64_t dim, int64_t groups, int silu, int io_dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+size_t ssm_group_norm_bwd_workspace_bytes(int64_t batch, int64_t rows, int64_t dim, int64_t groups);
 
 /*
  * ssm_scan_status -- whether the last forward scan that used `workspace`

@@ -9,7 +9,9 @@ The wrappers are imported lazily so that `selective_scan_ssm_amd.inputs`
 
 __all__ = ["scan_fwd", "sm1_scan_fwd", "state_update", "scan_status", "gated_scan_fwd", "gated_scan_bwd",
            "gated_state_update", "gated_ckpt_shape", "gated_scan_workspace_bytes", "gated_scan_bwd_workspace_bytes",
-           "add_rms_norm", "add_rms_norm_quant", "add_rms_norm_bwd", "grad_norm", "clip_grads"]
+           "add_rms_norm", "add_rms_norm_quant", "add_rms_norm_bwd", "grad_norm", "clip_grads",
+           "delta_scan_fwd", "delta_scan_bwd", "delta_state_update", "delta_ckpt_shape", "delta_scan_workspace_bytes",
+           "delta_scan_bwd_workspace_bytes", "group_norm", "group_norm_bwd"]
 
 
 def __getattr__(name):

@@ -30,6 +30,9 @@ EXPORTS = ("ssm_scan_fwd", "ssm_scan_workspace_bytes", "sm1_scan_fwd", "sm1_scan
            "ssm_add_rms_norm_quant", "ssm_add_rms_norm_bwd", "ssm_add_rms_norm_bwd_strided",
            "ssm_add_rms_norm_bwd_workspace_bytes", "ssm_grad_norm", "ssm_grad_clip", "ssm_grad_norm_workspace_bytes",
            "ssm_testing_gated_fwd_no_handoff", "ssm_testing_gated_bwd_no_handoff",
+           "ssm_delta_scan_fwd", "ssm_delta_scan_workspace_bytes", "ssm_delta_ckpt_bytes", "ssm_delta_scan_bwd",
+           "ssm_delta_scan_bwd_workspace_bytes", "ssm_delta_state_update", "ssm_group_norm_fwd",
+           "ssm_group_norm_workspace_bytes", "ssm_group_norm_bwd", "ssm_group_norm_bwd_workspace_bytes",
            "ssm_status_string", "ssm_abi_version")
 BENCH_LIB_PATH = os.path.join(PKG, "libssmbench.so")
 BENCH_EXPORTS = ("ssm_mb_copy", "ssm_mb_valu")
@@ -38,6 +41,7 @@ SSM_ERR_WAIT = -8
 SSM_ERR_SCRATCH = -9
 SSM_SCRATCH_BYTES = 16 << 20
 GATED_BLOCK = 128            # steps between two checkpoints of the gated recurrence
+DELTA_CHUNK = 64             # steps between two checkpoints of the gated delta rule
 
 _lib = None
 _lock = threading.Lock()
@@ -147,6 +151,24 @@ def _bind(lib):
         getattr(lib, name).restype = _int
     for name in ("ssm_gated_scan_workspace_bytes", "ssm_gated_ckpt_bytes", "ssm_gated_scan_bwd_workspace_bytes",
                  "ssm_add_rms_norm_bwd_workspace_bytes", "ssm_grad_norm_workspace_bytes"):
+        getattr(lib, name).restype = _sz
+    delta_in = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _i64]
+    delta_sizes = [_i64, _i64, _i64, _i64, _i64, _i64, _int]
+    lib.ssm_delta_scan_fwd.argtypes = delta_in + [_vp, _vp, _vp] + delta_sizes + [_vp, _sz, _vp]
+    lib.ssm_delta_scan_bwd.argtypes = delta_in + [_vp] * 9 + delta_sizes + [_vp, _sz, _vp]
+    lib.ssm_delta_scan_workspace_bytes.argtypes = [_i64, _i64, _int] + delta_sizes[:-1][1:] + [_int]
+    lib.ssm_delta_scan_bwd_workspace_bytes.argtypes = [_i64, _i64, _int] + delta_sizes[:-1][1:] + [_int, _int]
+    lib.ssm_delta_ckpt_bytes.argtypes = [_i64, _i64, _int, _i64, _i64, _i64, _i64]
+    lib.ssm_delta_state_update.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp]
+    lib.ssm_group_norm_fwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _int, _int,
+                                       _vp, _sz, _vp]
+    lib.ssm_group_norm_bwd.argtypes = [_vp, _vp, _i64, _vp, _i64] + [_vp] * 8 + [_i64, _i64, _i64, _i64, _int, _int, _vp, _sz, _vp]
+    for name in ("ssm_group_norm_workspace_bytes", "ssm_group_norm_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [_i64, _i64, _i64, _i64]
+    for name in ("ssm_delta_scan_fwd", "ssm_delta_scan_bwd", "ssm_delta_state_update", "ssm_group_norm_fwd", "ssm_group_norm_bwd"):
+        getattr(lib, name).restype = _int
+    for name in ("ssm_delta_scan_workspace_bytes", "ssm_delta_scan_bwd_workspace_bytes", "ssm_delta_ckpt_bytes",
+                 "ssm_group_norm_workspace_bytes", "ssm_group_norm_bwd_workspace_bytes"):
         getattr(lib, name).restype = _sz
     lib.ssm_status_string.argtypes = [_int]
     lib.ssm_status_string.restype = ctypes.c_char_p

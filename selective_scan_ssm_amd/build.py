@@ -28,8 +28,8 @@ SOURCES = ["scan_fwd.hip", "scan_rows_bf16.hip", "scan_rows_f32.hip", "scan_rows
            "scan_rows_2d_f32.hip", "scan_general_bf16.hip", "scan_general_bf16_xf32.hip", "scan_general_f32.hip",
            "sm1_scan.hip", "state_update.hip", "scan_bwd.hip", "conv1d.hip", "scan_2d.hip",
            "ssd_scan.hip", "dt_proj.hip", "scan_noalloc.hip", "gated_scan.hip", "add_rms_norm.hip", "grad_clip.hip",
-           "ssm_abi.cpp", "block_abi.cpp"]
-ABI_SOURCES = ["ssm_abi.cpp", "block_abi.cpp"]          # host code: argument checks, then launches
+           "delta_scan.hip", "delta_bwd.hip", "group_norm.hip", "ssm_abi.cpp", "block_abi.cpp", "mixer_abi.cpp"]
+ABI_SOURCES = ["ssm_abi.cpp", "block_abi.cpp", "mixer_abi.cpp"]          # host code: argument checks, then launches
 BENCH_SOURCES = ["microbench.hip"]
 
 # Packed fp32 VALU forms are switched off (plain fp32 VALU only); code object

@@ -1,0 +1,481 @@
+// The gradient of the gated delta rule.  With dS' = dL/dS' of the state S' that a
+// chunk leaves, per chunk (all of delta_chunk.h's names; F, E lower triangular):
+//     dU = scale P^T dY + exp(G_end - G) K dS',   dX = T^T (beta dU) = dV
+//     dS = exp(G_end) dS' + scale Q^T (exp(G) dY) - K^T (exp(G) dX)
+//     F = scale (dY U^T) o Gam,   E = (dX R^T) o Gam below the diagonal,   M = -E diag(beta)
+//     dQ = scale exp(G) dY S^T + F K
+//     dK = dKe + dKw,  dKe = M K - exp(G) dX S^T,  dKw = F^T Q + M^T K + exp(G_end - G) U dS'^T
+//     dbeta_t = R_t . dU_t - k_t . (E^T K)_t
+//     dg_t = sum over t' >= t of (q . dq + k . dke - k . dkw)_t'  + <S', dS'>
+// dg's form: G_t enters every product as exp(G_t) beside q_t and the key that is
+// read with, and as exp(-G_t) beside the key that is written with, so the
+// derivative by G_t is the product with what stands beside it.  <S', dS'> =
+// exp(G_end) <S, dS'> + sum_t k_t . (exp(G_end - G) U dS'^T)_t.
+//
+// Launches: the chunks' preparation; the states entering the chunks and R (one
+// walk over the chunks, or, from saved states, all chunks at once); dS' and dX, in
+// reverse; the rest, all chunks at once.
+#include "delta_chunk.h"
+
+namespace ssm {
+namespace delta {
+namespace {
+
+struct BwdParams {
+    DeltaBwdArgs b;
+    ChunkWs ws;
+    const float *R;                // per (slot, head): (64, V)
+    float *dX, *dS;                // (64, V), (V, K)
+    float *dot;                    // (ceil(V / 16), 64): R . dU by 16 channels
+};
+
+// element (t, v0 + c) of a (64, V) chunk, t over a tile's rows
+__device__ __forceinline__ uint32_t tile_off(int tb, int i, int g, int v, int V, int64_t ld, int n, int size) {
+    const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2) + i;
+    return t < n && v < V ? static_cast<uint32_t>((t * ld + v) * size) : kOffNone;
+}
+
+// --------------------------------------------------------- dS and dX, in reverse
+template <typename T, int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(BwdParams p) {
+    constexpr int KT = KP / 16, KK = KP / 32, OB = kOpBytes<T>;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    char *const sK = smem, *const sC = sK + (4 * KK) * OB, *const sQ = sC + (2 * KT) * OB, *const sT = sQ + (2 * KT) * OB,
+         *const sP = sT + kTriBytes;
+    float *const sS = reinterpret_cast<float *>(sP + kTriBytes);
+    const DeltaArgs &a = p.b.fwd;
+    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int g = lane / 16, c = lane % 16;
+    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
+    const int64_t H = a.s.heads;
+    const int nvt = (V + 63) / 64, vt = blockIdx.x % nvt;
+    const int64_t rest = blockIdx.x / nvt, head = rest % H, kh = head / (H / a.s.kheads), seq = rest / H;
+    const Span sp = span_of(a.s, seq);
+    const int nchunks = (sp.len + kC - 1) / kC;
+    const int v0 = vt * 64 + w * 16;
+    const f32x4 zero = {0, 0, 0, 0};
+    const size_t VK = static_cast<size_t>(V) * K;
+    constexpr int es = sizeof(T);
+    f32x4 dS[KT];
+    if (p.b.dlast) {
+        load_state<KP>(dS, p.b.dlast + (seq * H + head) * VK, v0, V, K, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) dS[i] = zero;
+    }
+    for (int j = nchunks - 1; j >= 0; --j) {
+        const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC, unit = (sp.slot0 + j) * H + head;
+        const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
+        const rsrc_t rk = make_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K);
+        __syncthreads();
+        stage_rows<T, KP>(sK, rk, a.ldk, n, K);
+        stage_columns<T, KP>(sC, rk, a.ldk, n, K);
+        stage_columns<T, KP>(sQ, make_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K), a.ldq, n, K);
+        stage_copy<kTriBytes>(sT, p.ws.tt + unit * kTriBytes);
+        stage_copy<kTriBytes>(sP, p.ws.p + unit * kTriBytes);
+        if (threadIdx.x < 3 * kC) sS[threadIdx.x] = p.ws.scal[unit * 3 * kC + threadIdx.x];
+        __syncthreads();
+        store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
+        const rsrc_t rd = make_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V);
+        const rsrc_t rR = make_rsrc(p.R + unit * kC * V);
+        f32x4 dY[4], R[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dY[tb][i] = Io<T>::f32(Io<T>::load(rd, tile_off(tb, i, g, v0 + c, V, H * V, n, es), 0));
+                R[tb][i] = Io<float>::f32(Io<float>::load(rR, tile_off(tb, i, g, v0 + c, V, V, n, 4), 0));
+            }
+        const Op<T> yo[2] = {exact<T>(dY[0], dY[1]), exact<T>(dY[2], dY[3])};
+        Op2<T> so[KK];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(dS[2 * kk], dS[2 * kk + 1]);
+        f32x4 dU[4];
+        float *const dot = p.dot + (unit * ((V + 15) / 16) + v0 / 16) * kC;
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
+            f32x4 acc = zero, pd = zero;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) acc = mma(get_op(sK + (tb * KK + kk) * OB, lane, T()), so[kk], acc);
+#pragma unroll
+            for (int kk = tb / 2; kk < 2; ++kk) pd = mma(get_op2(sP + tri_up(tb, kk) * kOp2Bytes, lane, T()), yo[kk], pd);
+            dU[tb] = acc * *reinterpret_cast<const f32x4 *>(&sS[kC + t]) + pd * a.scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float d = wave_fold<16>(R[tb][i] * dU[tb][i], AddOp());
+                if (c == 0 && v0 < V) dot[t + i] = d;
+            }
+            dU[tb] = dU[tb] * *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]);
+        }
+        const Op2<T> uo[2] = {computed<T>(dU[0], dU[1]), computed<T>(dU[2], dU[3])};
+        const rsrc_t rv = make_rsrc(static_cast<T *>(p.b.dv) + (row0 * H + head) * V), rx = make_rsrc(p.dX + unit * kC * V);
+        f32x4 dX[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
+            dX[tb] = zero;
+#pragma unroll
+            for (int kk = tb / 2; kk < 2; ++kk) dX[tb] = mma(get_op2(sT + tri_up(tb, kk) * kOp2Bytes, lane, T()), uo[kk], dX[tb]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Io<T>::store(dX[tb][i], rv, tile_off(tb, i, g, v0 + c, V, H * V, n, es), 0);
+                Io<float>::store(dX[tb][i], rx, tile_off(tb, i, g, v0 + c, V, V, kC, 4), 0);
+            }
+            const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[t]);
+            dY[tb] = dY[tb] * eg * a.scale;
+            dX[tb] = dX[tb] * -eg;
+        }
+        const Op2<T> qo[2] = {computed<T>(dY[0], dY[1]), computed<T>(dY[2], dY[3])};
+        const Op2<T> xo[2] = {computed<T>(dX[0], dX[1]), computed<T>(dX[2], dX[3])};
+        const float end = sS[kC - 1];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            dS[kt] = dS[kt] * end;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                dS[kt] = mma(get_op(sQ + (kt * 2 + kk) * OB, lane, T()), qo[kk], dS[kt]);
+                dS[kt] = mma(get_op(sC + (kt * 2 + kk) * OB, lane, T()), xo[kk], dS[kt]);
+            }
+        }
+    }
+    if (p.b.dh0) store_state<KP>(dS, p.b.dh0 + (seq * H + head) * VK, v0, V, K, lane);
+}
+
+template <typename T, int KP> constexpr size_t rev_lds() {
+    return (KP / 32 * 4 + KP / 16 * 4) * kOpBytes<T> + 2 * kTriBytes + 3 * kC * 4;
+}
+
+// -------------------------------------------------------------------- the rest
+// A workgroup per (chunk, key head), over the value heads that share it; a wave
+// owns 16 of the chunk's steps as columns of transposed results (rows are the K
+// channels), so a lane holds eight neighbouring channels of one step: 16-byte
+// stores, and the row sums of dg and dbeta are sums inside a lane.  The value
+// channels are taken 32 at a time.
+
+// 32 rows (value channels v0 ..) of a (V, K) state as operands with K channels as
+// rows and the value channels along K, and the sum of products of two of them
+template <typename T, int KP> __device__ __forceinline__ float stage_states(char *dst, char *dst2, const float *S, const float *dS,
+                                                                          int v0, int V, int K) {
+    constexpr int KT = KP / 16;
+    const rsrc_t r = make_rsrc(S, static_cast<uint32_t>(static_cast<int64_t>(V) * K * 4));
+    const rsrc_t r2 = make_rsrc(dS, static_cast<uint32_t>(static_cast<int64_t>(V) * K * 4));
+    float dot = 0.0f;
+    for (int s = threadIdx.x; s < KT * 32; s += kThreads) {
+        const int tile = s / 32, c = 2 * (s % 8), g = (s / 8) % 4;
+        const int k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4;
+        f32x2 x[8], y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int v = v0 + 8 * g + j;
+            const uint32_t off = v < V && k < K ? static_cast<uint32_t>((v * K + k) * 4) : kOffNone;
+            x[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+            y[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r2, off, 0, 0));
+            dot = fmaf(x[j][0], y[j][0], fmaf(x[j][1], y[j][1], dot));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            put_op(dst + tile * kOp2Bytes, 16 * g + c + h,
+                   computed<T>(f32x4{x[0][h], x[1][h], x[2][h], x[3][h]}, f32x4{x[4][h], x[5][h], x[6][h], x[7][h]}));
+            put_op(dst2 + tile * kOp2Bytes, 16 * g + c + h,
+                   computed<T>(f32x4{y[0][h], y[1][h], y[2][h], y[3][h]}, f32x4{y[4][h], y[5][h], y[6][h], y[7][h]}));
+        }
+    }
+    return dot;
+}
+// a chunk's rows of a (64, V) fp32 workspace tensor, 32 columns from v0 on
+template <typename T> __device__ __forceinline__ void stage_values(char *dst, const float *src, int v0, int V) {
+    const rsrc_t r = make_rsrc(src);
+    const int lane = threadIdx.x % 64, f = threadIdx.x / 64;
+    const int t = row_index(f, lane % 16), v = v0 + 8 * (lane / 16);
+    const uint32_t off = v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone;
+    put_op(dst + f * kOp2Bytes, lane, computed<T>(load4(r, off), load4(r, off + 16)));
+}
+// the eight elements of an operand as floats
+__device__ __forceinline__ void floats(const Op<bf16_t> &o, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = low(o.v[i]);
+        v[2 * i + 1] = high(o.v[i]);
+    }
+}
+__device__ __forceinline__ void floats(const Op<float> &o, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = o.a[i];
+        v[4 + i] = o.b[i];
+    }
+}
+__device__ __forceinline__ void store_io8(f32x4 a, f32x4 b, rsrc_t r, uint32_t off, bf16_t) {
+    __builtin_amdgcn_raw_buffer_store_b128(exact<bf16_t>(a, b).v, r, off, 0, 0);
+}
+__device__ __forceinline__ void store_io8(f32x4 a, f32x4 b, rsrc_t r, uint32_t off, float) {
+    store4(a, r, off);
+    store4(b, r, off + 16);
+}
+// over the four lane groups that hold one column
+__device__ __forceinline__ float column_total(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+template <typename T, int KP> constexpr size_t grad_lds() {
+    constexpr size_t loop = 4 * kOpBytes<T> + 8 * kOp2Bytes + 2 * (KP / 16) * kOp2Bytes, tail = 4 * (KP / 16) * kOpBytes<T>;
+    return loop > tail ? loop : tail;
+}
+
+template <typename T, int KP, bool SHARED>
+__global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
+    using D = Decay<T>;
+    using real = typename D::real;
+    constexpr int KT = KP / 16, KK = KP / 32, OB = kOpBytes<T>;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    char *const sY = smem, *const sX = sY + 4 * OB, *const sR = sX + 4 * kOp2Bytes, *const sS = sR + 4 * kOp2Bytes,
+         *const sD = sS + KT * kOp2Bytes;
+    char *const sC = smem, *const sQ = sC + 2 * KT * OB;               // after the loop over the value channels
+    __shared__ real sG[kC];
+    __shared__ float sB[kC], sDG[kC], sTot[kWaves];
+    const DeltaArgs &a = p.b.fwd;
+    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int g = lane / 16, c = lane % 16, t = row_index(w, c);
+    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
+    const int64_t H = a.s.heads, slot = blockIdx.x / a.s.kheads, kh = blockIdx.x % a.s.kheads;
+    const int group = static_cast<int>(H / a.s.kheads);
+    const int64_t seq = sequence_of(a.s, slot);
+    const Span sp = span_of(a.s, seq);
+    const int64_t step0 = (slot - sp.slot0) * kC;
+    if (step0 < 0 || step0 >= sp.len) return;
+    const int n = sp.len - step0 < kC ? static_cast<int>(sp.len - step0) : kC;
+    const int64_t row0 = sp.row0 + step0;
+    const f32x4 zero = {0, 0, 0, 0};
+    const rsrc_t rk = make_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K);
+    const rsrc_t rq = make_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K);
+    f32x4 dqs[SHARED ? KT : 1], dks[SHARED ? KT : 1];
+    if constexpr (SHARED) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) dqs[i] = dks[i] = zero;
+    }
+    for (int hh = 0; hh < group; ++hh) {
+        const int64_t head = kh * group + hh, unit = slot * H + head;
+        const float *const scal = p.ws.scal + unit * 3 * kC;
+        __syncthreads();                                     // the head before is done with sG, sB, sDG
+        if (w == 0) {
+            const real G = lane_prefix<real>(lane < n ? D::scaled(step_log(a.g[(row0 + lane) * H + head])) : real(0), lane);
+            sG[lane] = G;
+            sB[lane] = scal[2 * kC + lane];
+        }
+        f32x4 dq[KT], ke[KT], kw[KT], FT[4], F[4], ET[4], E[4];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) dq[i] = ke[i] = kw[i] = zero;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) FT[i] = F[i] = ET[i] = E[i] = zero;
+        float tot = 0.0f;
+        const rsrc_t rd = make_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V);
+        for (int v0 = 0; v0 < V; v0 += 32) {
+            __syncthreads();
+            const int f = threadIdx.x / 64, tr = row_index(f, c), v = v0 + 8 * g;
+            put_op(sY + f * OB, lane, load_op(rd, tr < n && v < V ? static_cast<uint32_t>((tr * H * V + v) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()));
+            stage_values<T>(sX, p.dX + unit * kC * V, v0, V);
+            stage_values<T>(sR, p.R + unit * kC * V, v0, V);
+            tot += stage_states<T, KP>(sS, sD, a.ckpt + unit * V * K, p.dS + unit * V * K, v0, V, K);
+            __syncthreads();
+            const Op<T> y = get_op(sY + w * OB, lane, T());
+            const Op2<T> x = get_op2(sX + w * kOp2Bytes, lane, T()), r = get_op2(sR + w * kOp2Bytes, lane, T());
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                const Op2<T> s = get_op2(sS + kt * kOp2Bytes, lane, T()), d = get_op2(sD + kt * kOp2Bytes, lane, T());
+                dq[kt] = mma(s, y, dq[kt]);
+                ke[kt] = mma(s, x, ke[kt]);
+                kw[kt] = mma(d, r, kw[kt]);
+            }
+#pragma unroll
+            for (int ob = 0; ob < 4; ++ob) {
+                if (ob / 2 <= w / 2) {                       // rows s at or before this wave's steps
+                    const Op2<T> ro = get_op2(sR + ob * kOp2Bytes, lane, T());
+                    FT[ob] = mma(ro, y, FT[ob]);
+                    ET[ob] = mma(ro, x, ET[ob]);
+                }
+                if (ob / 2 >= w / 2) {                       // rows t at or behind them
+                    F[ob] = mma(get_op(sY + ob * OB, lane, T()), r, F[ob]);
+                    E[ob] = mma(get_op2(sX + ob * kOp2Bytes, lane, T()), r, E[ob]);
+                }
+            }
+        }
+        __syncthreads();
+        stage_columns<T, KP>(sC, rk, a.ldk, n, K);
+        stage_columns<T, KP>(sQ, rq, a.ldq, n, K);
+        const float eg = scal[t], wt = scal[kC + t], beta = sB[t], end = scal[kC - 1];
+        const real gt = sG[t];
+#pragma unroll
+        for (int ob = 0; ob < 4; ++ob)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s for FT, ET, t for F, E
+                const float before = o <= t ? D::ex(gt - sG[o]) : 0.0f, behind = o >= t ? D::ex(sG[o] - gt) : 0.0f;
+                FT[ob][i] = o <= t ? FT[ob][i] * (a.scale * before * sB[o]) : 0.0f;
+                ET[ob][i] = o < t ? ET[ob][i] * (-before * sB[o]) : 0.0f;      // M^T
+                F[ob][i] = o >= t ? F[ob][i] * (a.scale * behind * beta) : 0.0f;
+                E[ob][i] = o > t ? E[ob][i] * behind : 0.0f;
+            }
+        float qd = 0.0f, kd = 0.0f, kdw = 0.0f, kb = 0.0f, kc = 0.0f;
+        const float fq = a.scale * eg, fw = beta * wt;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            dq[kt] = dq[kt] * fq;
+            ke[kt] = ke[kt] * -eg;
+            kw[kt] = kw[kt] * fw;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kp = 0; kp < KK; ++kp) {                    // pairs of channel tiles
+            const int k0 = 32 * kp + 8 * g;
+            const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * a.ldk + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+            const uint32_t offq = t < n && k0 < K ? static_cast<uint32_t>((t * a.ldq + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+            float kv[8], qv[8];
+            floats(load_op(rk, off, T()), kv);
+            floats(load_op(rq, offq, T()), qv);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kt = 2 * kp + h;
+                f32x4 em = zero;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kc = fmaf(kv[4 * h + i], kw[kt][i], kc);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const Op<T> kcol = get_op(sC + (kt * 2 + kk) * OB, lane, T()), qcol = get_op(sQ + (kt * 2 + kk) * OB, lane, T());
+                    if (kk <= w / 2) {
+                        dq[kt] = mma(kcol, computed<T>(FT[2 * kk], FT[2 * kk + 1]), dq[kt]);
+                        ke[kt] = mma(kcol, computed<T>(ET[2 * kk], ET[2 * kk + 1]), ke[kt]);
+                    }
+                    if (kk >= w / 2) {
+                        kw[kt] = mma(qcol, computed<T>(F[2 * kk], F[2 * kk + 1]), kw[kt]);
+                        em = mma(kcol, computed<T>(E[2 * kk], E[2 * kk + 1]), em);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    kw[kt][i] = fmaf(-beta, em[i], kw[kt][i]);
+                    qd = fmaf(qv[4 * h + i], dq[kt][i], qd);
+                    kd = fmaf(kv[4 * h + i], ke[kt][i], kd);
+                    kdw = fmaf(kv[4 * h + i], kw[kt][i], kdw);
+                    kb = fmaf(kv[4 * h + i], em[i], kb);
+                }
+                ke[kt] = ke[kt] + kw[kt];
+            }
+        }
+        const float dG = column_total(qd + kd - kdw);
+        kb = column_total(kb);
+        float rd_u = 0.0f;
+        const int nt = (V + 15) / 16;
+        for (int i = g; i < nt; i += 4) rd_u += p.dot[(unit * nt + i) * kC + t];
+        rd_u = column_total(rd_u);
+        if (g == 0 && t < n) p.b.dbeta[(row0 + t) * H + head] = rd_u - kb;
+        tot = wave_fold(fmaf(end, tot, kc), AddOp());
+        if (lane == 0) sTot[w] = tot;
+        if (g == 0) sDG[t] = dG;
+        __syncthreads();
+        if (w == 0) {                                        // lane l is step 63 - l: sums from the end
+            double v = sDG[63 - lane];
+            if (lane == 0) v += static_cast<double>(sTot[0]) + sTot[1] + sTot[2] + sTot[3];
+            v = lane_prefix<double>(v, lane);
+            if (63 - lane < n) p.b.dg[(row0 + 63 - lane) * H + head] = static_cast<float>(v);
+        }
+        if constexpr (SHARED) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                dqs[i] = dqs[i] + dq[i];
+                dks[i] = dks[i] + ke[i];
+            }
+        } else {
+            const int64_t Hk = a.s.kheads;
+            const rsrc_t wq = make_rsrc(static_cast<T *>(p.b.dq) + (row0 * Hk + kh) * K), wk = make_rsrc(static_cast<T *>(p.b.dk) + (row0 * Hk + kh) * K);
+#pragma unroll
+            for (int kp = 0; kp < KK; ++kp) {
+                const int k0 = 32 * kp + 8 * g;
+                const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * Hk * K + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+                store_io8(dq[2 * kp], dq[2 * kp + 1], wq, off, T());
+                store_io8(ke[2 * kp], ke[2 * kp + 1], wk, off, T());
+            }
+        }
+    }
+    if constexpr (SHARED) {
+        const int64_t Hk = a.s.kheads;
+        const rsrc_t wq = make_rsrc(static_cast<T *>(p.b.dq) + (row0 * Hk + kh) * K), wk = make_rsrc(static_cast<T *>(p.b.dk) + (row0 * Hk + kh) * K);
+#pragma unroll
+        for (int kp = 0; kp < KK; ++kp) {
+            const int k0 = 32 * kp + 8 * g;
+            const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * Hk * K + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+            store_io8(dqs[2 * kp], dqs[2 * kp + 1], wq, off, T());
+            store_io8(dks[2 * kp], dks[2 * kp + 1], wk, off, T());
+        }
+    }
+}
+
+struct BwdWs {
+    size_t t, tt, p, scal, R, dX, dS, dot, ckpt, total;
+};
+BwdWs bwd_ws(const DeltaShape &s, bool saved) {
+    const size_t units = static_cast<size_t>(s.slots * s.heads), V = s.dv, K = s.dk;
+    BwdWs w{};
+    w.tt = w.t + align256(units * kTriBytes);
+    w.p = w.tt + align256(units * kTriBytes);
+    w.scal = w.p + align256(units * kTriBytes);
+    w.R = w.scal + align256(units * 3 * kC * 4);
+    w.dX = w.R + align256(units * kC * V * 4);
+    w.dS = w.dX + align256(units * kC * V * 4);
+    w.dot = w.dS + align256(units * V * K * 4);
+    w.ckpt = w.dot + align256(units * ((V + 15) / 16) * kC * 4);
+    w.total = w.ckpt + (saved ? 0 : align256(units * V * K * 4));
+    return w;
+}
+
+template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t s) {
+    const DeltaShape &sh = b.fwd.s;
+    const BwdWs w = bwd_ws(sh, b.fwd.ckpt != nullptr);
+    char *const base = static_cast<char *>(b.fwd.workspace);
+    BwdParams p{};
+    p.b = b;
+    p.b.fwd.last_state = nullptr;
+    p.ws = {base + w.t, base + w.p, base + w.tt, reinterpret_cast<float *>(base + w.scal)};
+    float *const R = reinterpret_cast<float *>(base + w.R);
+    p.R = R;
+    p.dX = reinterpret_cast<float *>(base + w.dX);
+    p.dS = reinterpret_cast<float *>(base + w.dS);
+    p.dot = reinterpret_cast<float *>(base + w.dot);
+    if (sh.slots > 0) {
+        if (hipError_t e = launch_prep<T, KP, true>(b.fwd, p.ws, s)) return e;
+        SeqParams q{};
+        q.a = b.fwd;
+        q.a.last_state = nullptr;
+        q.ws = p.ws;
+        q.R = R;
+        if (b.fwd.ckpt) {
+            if (hipError_t e = launch_seq<T, KP, false, true>(q, s)) return e;
+        } else {
+            q.a.ckpt = p.b.fwd.ckpt = reinterpret_cast<float *>(base + w.ckpt);
+            if (hipError_t e = launch_seq<T, KP, false, false>(q, s)) return e;
+        }
+    }
+    const int64_t nvt = (sh.dv + 63) / 64;
+    constexpr size_t rlds = rev_lds<T, KP>(), glds = grad_lds<T, KP>();
+    hipLaunchKernelGGL((delta_rev_kernel<T, KP>), dim3(static_cast<unsigned>(nvt * sh.heads * sh.nseq)), dim3(kThreads), rlds, s, p);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (sh.slots == 0) return hipSuccess;
+    const dim3 grid(static_cast<unsigned>(sh.slots * sh.kheads));
+    if (sh.heads == sh.kheads) hipLaunchKernelGGL((delta_grad_kernel<T, KP, false>), grid, dim3(kThreads), glds, s, p);
+    else hipLaunchKernelGGL((delta_grad_kernel<T, KP, true>), grid, dim3(kThreads), glds, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace delta
+
+size_t delta_scan_bwd_workspace(const DeltaShape &s, bool saved) {
+    return s.slots * s.heads > 0 ? delta::bwd_ws(s, saved).total : 0;
+}
+hipError_t launch_delta_scan_bwd(const DeltaBwdArgs &b, hipStream_t s) {
+    using namespace delta;
+    if (b.fwd.bf16) return b.fwd.s.dk > 64 ? run<bf16_t, 128>(b, s) : run<bf16_t, 64>(b, s);
+    return b.fwd.s.dk > 64 ? run<float, 128>(b, s) : run<float, 64>(b, s);
+}
+
+}  // namespace ssm

@@ -255,4 +255,70 @@ struct ClipArgs {
 size_t grad_norm_workspace(int64_t count);
 hipError_t launch_grad_clip(const ClipArgs &a, hipStream_t s);
 
+// The gated delta rule.  Steps of q, k, v are ldq, ldk, ldv elements apart;
+// everything else is contiguous.
+constexpr int kDeltaChunk = 64;           // steps between two checkpoints
+constexpr int kDeltaMaxState = 128;       // channels of a key
+struct DeltaShape {
+    const int32_t *starts;                // packed: nseq + 1 first rows, else null
+    int64_t nseq, seqlen;                 // sequences, steps of each (packed: rows in all)
+    int64_t kheads, heads, dk, dv;
+    int64_t slots;                        // chunks in all (packed: an upper bound)
+};
+struct DeltaArgs {
+    DeltaShape s;
+    const void *q, *k, *v;                // io dtype
+    int64_t ldq, ldk, ldv;
+    const float *g, *beta, *h0;
+    void *y;
+    float *last_state, *ckpt;
+    float scale;
+    int bf16;
+    void *workspace;
+};
+struct DeltaBwdArgs {
+    DeltaArgs fwd;                        // y, last_state unused; ckpt is read
+    const void *dout;
+    const float *dlast;
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dh0;
+};
+struct DeltaStepArgs {
+    float *state;
+    const void *q, *k, *v;
+    const float *g, *beta;
+    void *y;
+    int64_t batch, kheads, heads, dk, dv;
+    float scale;
+    int bf16;
+};
+size_t delta_scan_workspace(const DeltaShape &s);
+size_t delta_scan_bwd_workspace(const DeltaShape &s, bool saved);
+hipError_t launch_delta_scan(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_scan_bwd(const DeltaBwdArgs &a, hipStream_t s);
+hipError_t launch_delta_update(const DeltaStepArgs &a, hipStream_t s);
+
+// Group norm, channels last.
+struct GroupNormArgs {
+    const void *x, *z;                    // io dtype (batch, rows, dim), rows ldx, ldz apart; z may be null
+    int64_t ldx, ldz;
+    const float *weight, *bias;           // may be null
+    void *y;
+    float *mean, *rstd;                   // (batch, groups); may be null in the forward
+    int64_t batch, rows, dim, groups;
+    float eps;
+    int silu, bf16;
+    void *workspace;
+};
+struct GroupNormBwdArgs {
+    GroupNormArgs fwd;                    // y, eps unused; mean and rstd are read
+    const void *dy;
+    void *dx, *dz;
+    float *dweight, *dbias;
+};
+size_t group_norm_workspace(int64_t batch, int64_t rows, int64_t dim, int64_t groups);
+size_t group_norm_bwd_workspace(int64_t batch, int64_t rows, int64_t dim, int64_t groups);
+hipError_t launch_group_norm(const GroupNormArgs &a, hipStream_t s);
+hipError_t launch_group_norm_bwd(const GroupNormBwdArgs &a, hipStream_t s);
+
 }  // namespace ssm

@@ -808,3 +808,230 @@ def clip_grads(grads, max_norm, out=None, eps=1e-6, norm_out=None, workspace=Non
     if max_norm is None:
         raise ValueError("max_norm must be a number")
     return _clip(grads, float(max_norm), out, float(eps), norm_out, workspace)
+
+
+# ------------------------------------------- the gated delta rule, group norm
+def _heads(t, name, dtype, shape, dev):
+    """The address of t (batch, seqlen, heads, width) and the stride between its
+    steps: a step's heads lie side by side, and the steps are evenly strided."""
+    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr(), shape[2] * shape[3]
+    _device(t, name)
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    st, width = t.stride(), shape[2] * shape[3]
+    if (shape[3] > 1 and st[3] != 1) or (shape[2] > 1 and st[2] != shape[3]):
+        raise ValueError(f"{name} must have the heads of a step side by side")
+    if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+        raise ValueError(f"the steps of {name} must be evenly strided")
+    ld = st[1] if shape[1] > 1 else (st[0] if shape[0] > 1 else width)
+    if ld < width:
+        raise ValueError(f"the steps of {name} overlap")
+    return t.data_ptr(), ld
+
+
+def _delta_shape(q, v, starts):
+    """batch, seqlen, packed, nseq, nkheads, nheads, dstate, headdim."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be (batch, seqlen, heads, width)")
+    Bt, T, Hk, K = q.shape
+    H, V = v.shape[2:]
+    if starts is None:
+        return Bt, T, 0, Bt, Hk, H, K, V
+    if starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must hold one value more than there are sequences")
+    return Bt, T, 1, starts.shape[0] - 1, Hk, H, K, V
+
+
+def delta_ckpt_shape(q, v, starts=None):
+    """Shape of delta_scan_fwd's checkpoints for these inputs: (slots, nheads,
+    headdim, dstate) with batch * ceil(seqlen / 64) slots, or seqlen // 64 +
+    sequences for packed ones (chunk j of sequence i: slot starts[i] // 64 + i + j)."""
+    Bt, T, packed, nseq, _, H, K, V = _delta_shape(q, v, starts)
+    C = _lib.DELTA_CHUNK
+    slots = (T // C + nseq if nseq and T else 0) if packed else Bt * -(-T // C)
+    return (slots, H, V, K)
+
+
+def delta_scan_workspace_bytes(q, v, starts=None):
+    """Bytes of delta_scan_fwd's workspace for these inputs."""
+    return _delta_bytes(_lib.load().ssm_delta_scan_workspace_bytes, *_delta_shape(q, v, starts), _IO[q.dtype])
+
+
+def delta_scan_bwd_workspace_bytes(q, v, starts=None, saved=False):
+    """Bytes of delta_scan_bwd's workspace for these inputs (saved: with ckpt)."""
+    return _delta_bytes(_lib.load().ssm_delta_scan_bwd_workspace_bytes, *_delta_shape(q, v, starts), int(saved), _IO[q.dtype])
+
+
+def _delta_bytes(fn, *args):
+    need = fn(*args)
+    if need == _BAD:
+        raise RuntimeError(f"{fn.__name__}: invalid arguments")
+    return need
+
+
+def _delta_inputs(q, k, v, g, beta, scale, h0, starts):
+    """What both directions pass first, the sizes, and the state's shape."""
+    io, dev = q.dtype, _device(q, "q")
+    if io not in _IO:
+        raise ValueError("q must be float32 or bfloat16")
+    sizes = _delta_shape(q, v, starts)
+    Bt, T, packed, nseq, Hk, H, K, V = sizes
+    pq, ldq = _heads(q, "q", io, q.shape, dev)
+    pk, ldk = _heads(k, "k", io, q.shape, dev)
+    pv, ldv = _heads(v, "v", io, torch.Size((Bt, T, H, V)), dev)
+    ends = (nseq, H, V, K)
+    head = (pq, ldq, pk, ldk, pv, ldv, _arg(g, "g", torch.float32, (Bt, T, H), dev),
+            _arg(beta, "beta", torch.float32, (Bt, T, H), dev), K ** -0.5 if scale is None else float(scale),
+            _arg(h0, "h0", torch.float32, ends, dev),
+            _arg(starts, "starts", torch.int32, None if starts is None else starts.shape, dev), nseq)
+    return io, dev, sizes, ends, head
+
+
+def delta_scan_fwd(q, k, v, g, beta, scale=None, h0=None, starts=None, return_last_state=False, out=None,
+                   last_state_out=None, ckpt_out=None, workspace=None):
+    """Gated delta rule.  Per value head, with its state s (headdim, dstate):
+    s <- exp(g) s, r = v - s k, s <- s + beta r k^T, y = scale s q (scale: dstate
+    ** -0.5 if None).  q, k: (batch, seqlen, nkheads, dstate), v: (batch, seqlen,
+    nheads, headdim) fp32 or bf16, each step's heads side by side and the steps evenly strided
+    (column ranges of one projection need no copy; their strides and addresses multiples of 16 bytes);
+    g (the decay's logarithm), beta: (batch, seqlen, nheads) fp32; h0: (sequences, nheads, headdim, dstate) fp32.
+    nheads is a multiple of nkheads: neighbouring value heads share a key head.
+    dstate: a multiple of 8 up to 128; headdim: a multiple of 8.
+    starts: int32 (sequences + 1) on the device, ascending, with batch 1: sequence
+    i is the rows starts[i] .. starts[i + 1] - 1; rows outside of all are neither
+    read nor written (they stay as they are in `out`, undefined without it).
+    Returns y (same dtype as v) or (y, last_state fp32).  ckpt_out: an fp32 tensor
+    of delta_ckpt_shape(...) that also receives the states entering the 64-step
+    chunks, for delta_scan_bwd(..., ckpt=ckpt_out).  workspace: a uint8 tensor of
+    at least delta_scan_workspace_bytes(...), allocated here without one."""
+    lib = _lib.load()
+    io, dev, (Bt, T, packed, nseq, Hk, H, K, V), ends, head = _delta_inputs(q, k, v, g, beta, scale, h0, starts)
+    y = out if out is not None else torch.empty((Bt, T, H, V), dtype=io, device=dev)
+    last = None
+    if return_last_state:
+        last = last_state_out if last_state_out is not None else torch.empty(ends, dtype=torch.float32, device=dev)
+    ws, pws = _scratch(lib.ssm_delta_scan_workspace_bytes(Bt, T, packed, nseq, Hk, H, K, V, _IO[io]),
+                       "ssm_delta_scan_workspace_bytes", workspace, dev)
+    rc = _run(dev, lib.ssm_delta_scan_fwd, *head, _arg(y, "out", io, (Bt, T, H, V), dev),
+              _arg(last, "last_state_out", torch.float32, ends, dev),
+              _arg(ckpt_out, "ckpt_out", torch.float32, None if ckpt_out is None else delta_ckpt_shape(q, v, starts), dev),
+              Bt, T, Hk, H, K, V, _IO[io], pws, 0 if ws is None else ws.numel())
+    _check(rc, "ssm_delta_scan_fwd")
+    return (y, last) if return_last_state else y
+
+
+def delta_scan_bwd(q, k, v, g, beta, dout, scale=None, h0=None, starts=None, dlast=None, ckpt=None, workspace=None):
+    """Gradient of delta_scan_fwd.  Same inputs, plus dout = dL/dy (contiguous, like
+    y) and dlast = dL/dlast_state (optional).  Returns a dict: dq, dk, dv (dtype of
+    q, contiguous; dq and dk summed over the heads that share a key head), dg, dbeta,
+    dh0 (fp32).  Rows outside of every sequence are not written.  ckpt: what
+    delta_scan_fwd(..., ckpt_out=) recorded on the same inputs; without it the call
+    walks the chunks once more.  workspace: as in delta_scan_fwd, of at least
+    delta_scan_bwd_workspace_bytes(...)."""
+    lib = _lib.load()
+    io, dev, (Bt, T, packed, nseq, Hk, H, K, V), ends, head = _delta_inputs(q, k, v, g, beta, scale, h0, starts)
+    new = lambda size, dtype: torch.empty(size, dtype=dtype, device=dev)
+    dq, dk, dv = new((Bt, T, Hk, K), io), new((Bt, T, Hk, K), io), new((Bt, T, H, V), io)
+    dg, dbeta, dh0 = new((Bt, T, H), torch.float32), new((Bt, T, H), torch.float32), new(ends, torch.float32)
+    ws, pws = _scratch(lib.ssm_delta_scan_bwd_workspace_bytes(Bt, T, packed, nseq, Hk, H, K, V, int(ckpt is not None), _IO[io]),
+                       "ssm_delta_scan_bwd_workspace_bytes", workspace, dev)
+    rc = _run(dev, lib.ssm_delta_scan_bwd, *head, _arg(dout, "dout", io, (Bt, T, H, V), dev),
+              _arg(dlast, "dlast", torch.float32, ends, dev),
+              _arg(ckpt, "ckpt", torch.float32, None if ckpt is None else delta_ckpt_shape(q, v, starts), dev),
+              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), Bt, T, Hk, H, K, V, _IO[io], pws,
+              0 if ws is None else ws.numel())
+    _check(rc, "ssm_delta_scan_bwd")
+    return dict(dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta, dh0=dh0)
+
+
+def delta_state_update(state, q, k, v, g, beta, scale=None, out=None):
+    """One decode token of delta_scan_fwd; `state` (batch, nheads, headdim, dstate)
+    fp32 is updated in place.  q, k: (batch, nkheads, dstate), v: (batch, nheads,
+    headdim) fp32 or bf16, g, beta: (batch, nheads) fp32, all contiguous.  Returns y (batch, nheads, headdim)."""
+    lib = _lib.load()
+    io, dev, shape = v.dtype, _device(v, "v"), v.shape
+    if io not in _IO or len(shape) != 3 or q.dim() != 3:
+        raise ValueError("q, k, v must be float32 or bfloat16 (batch, heads, width)")
+    Bt, H, V = shape
+    Hk, K = q.shape[1:]
+    y, py = _out(out, "out", v, io, shape, dev)
+    rc = _run(dev, lib.ssm_delta_state_update, _arg(state, "state", torch.float32, (Bt, H, V, K), dev),
+              _arg(q, "q", io, (Bt, Hk, K), dev), _arg(k, "k", io, (Bt, Hk, K), dev), _arg(v, "v", io, shape, dev),
+              _arg(g, "g", torch.float32, (Bt, H), dev), _arg(beta, "beta", torch.float32, (Bt, H), dev),
+              K ** -0.5 if scale is None else float(scale), py, Bt, Hk, H, K, V, _IO[io])
+    _check(rc, "ssm_delta_state_update")
+    return y
+
+
+_ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _norm_view(x, name):
+    """batch, rows and channels of a channels-last tensor (batch, ..., dim)."""
+    if x.dim() < 2:
+        raise ValueError(f"{name} must be (batch, ..., dim)")
+    n = 1
+    for size in x.shape[1:-1]:
+        n *= size
+    return x.shape[0], n, x.shape[-1]
+
+
+def group_norm(x, groups, weight=None, bias=None, z=None, activation=None, eps=1e-5, return_stats=False, out=None,
+               workspace=None):
+    """Group norm over a channels-last tensor, with an activation and a gate.
+    x: (batch, ..., dim) fp32 or bf16, rows evenly strided; the statistics are over
+    dim / groups neighbouring channels and the axes between (a (tokens, dim) tensor:
+    every token's groups apart).  y = act((x - mean) * rstd * weight + bias) *
+    SiLU(z): activation None or "silu", z like x (no factor without it); weight,
+    bias: (dim,) fp32, 1 and 0 without.  Returns y (contiguous), or (y, mean, rstd)
+    with mean, rstd (batch, groups) fp32 for group_norm_bwd."""
+    lib = _lib.load()
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO:
+        raise ValueError("x must be float32 or bfloat16")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    N, R, C = _norm_view(x, "x")
+    px, ldx = _rows(x, "x", io, shape, dev)
+    pz, ldz = _rows(z, "z", io, shape, dev)
+    y, py = _out(out, "out", x, io, shape, dev)
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = (torch.empty((N, groups), dtype=torch.float32, device=dev) for _ in range(2))
+    ws, pws = _scratch(lib.ssm_group_norm_workspace_bytes(N, R, C, groups), "ssm_group_norm_workspace_bytes", workspace, dev)
+    rc = _run(dev, lib.ssm_group_norm_fwd, px, ldx, pz, ldz, _arg(weight, "weight", torch.float32, (C,), dev),
+              _arg(bias, "bias", torch.float32, (C,), dev), py, _ptr(mean), _ptr(rstd), N, R, C, groups, eps,
+              _ACTIVATIONS[activation], _IO[io], pws, 0 if ws is None else ws.numel())
+    _check(rc, "ssm_group_norm_fwd")
+    return (y, mean, rstd) if return_stats else y
+
+
+def group_norm_bwd(dy, x, mean, rstd, groups, weight=None, bias=None, z=None, activation=None, workspace=None):
+    """Gradient of group_norm at the mean and rstd it returned.  dy: like y,
+    contiguous; the rest as there.  Returns a dict: dx, dz (None without z) in x's
+    dtype, contiguous; dweight, dbias (dim,) fp32 (None without weight, bias)."""
+    lib = _lib.load()
+    io, dev, shape = x.dtype, _device(x, "x"), x.shape
+    if io not in _IO:
+        raise ValueError("x must be float32 or bfloat16")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    N, R, C = _norm_view(x, "x")
+    px, ldx = _rows(x, "x", io, shape, dev)
+    pz, ldz = _rows(z, "z", io, shape, dev)
+    new = lambda size, dtype: torch.empty(size, dtype=dtype, device=dev)
+    dx, dz = new(shape, io), new(shape, io) if z is not None else None
+    dw, db = (new((C,), torch.float32) if t is not None else None for t in (weight, bias))
+    ws, pws = _scratch(lib.ssm_group_norm_bwd_workspace_bytes(N, R, C, groups), "ssm_group_norm_bwd_workspace_bytes", workspace,
+                       dev)
+    rc = _run(dev, lib.ssm_group_norm_bwd, _arg(dy, "dy", io, shape, dev), px, ldx, pz, ldz,
+              _arg(weight, "weight", torch.float32, (C,), dev), _arg(bias, "bias", torch.float32, (C,), dev),
+              _arg(mean, "mean", torch.float32, (N, groups), dev), _arg(rstd, "rstd", torch.float32, (N, groups), dev), _ptr(dx),
+              _ptr(dz), _ptr(dw), _ptr(db), N, R, C, groups, _ACTIVATIONS[activation], _IO[io], pws, 0 if ws is None else ws.numel())
+    _check(rc, "ssm_group_norm_bwd")
+    return dict(dx=dx, dz=dz, dweight=dw, dbias=db)
