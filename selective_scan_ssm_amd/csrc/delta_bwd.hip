@@ -29,19 +29,22 @@ struct BwdParams {
     float *dot;                    // (ceil(V / 16), 64): R . dU by 16 channels
 };
 
-// element (t, v0 + c) of a (64, V) chunk, t over a tile's rows
-__device__ __forceinline__ uint32_t tile_off(int tb, int i, int g, int v, int V, int64_t ld, int n, int size) {
-    const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2) + i;
-    return t < n && v < V ? static_cast<uint32_t>((t * ld + v) * size) : kOffNone;
-}
+// What get_col reads of a chunk that is used with steps along K only.
+template <typename T, int KP> struct QSide : Cols<T, KP> {};
+template <int KP> struct QSide<bf16_t, KP> : Rows<bf16_t, KP> {
+    static __device__ __forceinline__ uint32_t offsets(int64_t ld, int K) { return Rows<bf16_t, KP>::offset(ld, K); }
+};
 
 // --------------------------------------------------------- dS and dX, in reverse
-template <typename T, int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(BwdParams p) {
-    constexpr int KT = KP / 16, KK = KP / 32, OB = kOpBytes<T>;
+template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 2 : 1))) void delta_rev_kernel(BwdParams p) {
+    constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    char *const sK = smem, *const sC = sK + (4 * KK) * OB, *const sQ = sC + (2 * KT) * OB, *const sT = sQ + (2 * KT) * OB,
-         *const sP = sT + kTriBytes;
-    float *const sS = reinterpret_cast<float *>(sP + kTriBytes);
+    // bf16 keeps rows of keys and queries and reads them transposed as well; fp32 also keeps the keys' columns, and of
+    // the queries the columns alone
+    char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sQ = sC + Cols<T, KP>::kBytes,
+         *const sT = sQ + QSide<T, KP>::kBytes, *const sP = sT + kTriBytes;
+    char *const sY = sP + kTriBytes;
+    float *const sS = reinterpret_cast<float *>(sY + Values<T>::kBytes);
     const DeltaArgs &a = p.b.fwd;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
@@ -62,44 +65,72 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) void delta_
 #pragma unroll
         for (int i = 0; i < KT; ++i) dS[i] = zero;
     }
+    // the next chunk's data, a chunk ahead, as in the forward
+    Rows<T, KP> nK;
+    Cols<T, KP> nC;
+    QSide<T, KP> nQ;
+    Copy<kTriBytes> nT, nP;
+    float nS;
+    Values<T> nY;
+    const uint32_t okr = Rows<T, KP>::offset(a.ldk, K);
+    const auto okc = Cols<T, KP>::offsets(a.ldk, K);
+    const auto oqc = QSide<T, KP>::offsets(a.ldq, K);
+    const int ldy = static_cast<int>(H * V);
+    const uint32_t oy = Values<T>::offset(ldy, V - vt * 64, w, lane);
+    const uint32_t oR = v0 + c < V ? static_cast<uint32_t>((8 * g * V + v0 + c) * 4) : kOffNone;
+    auto prefetch = [&](int j) {
+        const int jj = j >= 0 ? j : 0;
+        const int64_t row0 = sp.row0 + static_cast<int64_t>(jj) * kC, unit = (sp.slot0 + jj) * H + head;
+        const int n = j >= 0 ? (sp.len - j * kC < kC ? sp.len - j * kC : kC) : 0;
+        const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, es);
+        const rsrc_t rd = chunk_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V + vt * 64, n, ldy, V - vt * 64, es);
+        nK.load(rk, a.ldk, okr);
+        nY.load(rd, ldy, oy);
+        nT.load(p.ws.tt + unit * kTriBytes);
+        nP.load(p.ws.p + unit * kTriBytes);
+        nS = p.ws.scal[unit * 3 * kC + (threadIdx.x < 3 * kC ? threadIdx.x : 0)];
+        nC.load(rk, a.ldk, okc);
+        nQ.load(chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, es), a.ldq, oqc);
+    };
+    if (nchunks > 0) prefetch(nchunks - 1);
     for (int j = nchunks - 1; j >= 0; --j) {
         const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC, unit = (sp.slot0 + j) * H + head;
         const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
-        const rsrc_t rk = make_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K);
+        __syncthreads();                                   // the chunk before is done with LDS
+        nK.put(sK);
+        nC.put(sC);
+        nQ.put(sQ);
+        nT.put(sT);
+        nP.put(sP);
+        if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
+        nY.put(sY);
+        const Values<T> cY = nY;
         __syncthreads();
-        stage_rows<T, KP>(sK, rk, a.ldk, n, K);
-        stage_columns<T, KP>(sC, rk, a.ldk, n, K);
-        stage_columns<T, KP>(sQ, make_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K), a.ldq, n, K);
-        stage_copy<kTriBytes>(sT, p.ws.tt + unit * kTriBytes);
-        stage_copy<kTriBytes>(sP, p.ws.p + unit * kTriBytes);
-        if (threadIdx.x < 3 * kC) sS[threadIdx.x] = p.ws.scal[unit * 3 * kC + threadIdx.x];
-        __syncthreads();
+        const rsrc_t rR = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+        f32x4 R[4];                                        // needed late in the chunk
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            R[i / 4][i % 4] = Io<float>::f32(Io<float>::load(rR, oR + static_cast<uint32_t>((32 * (i / 8) + i % 8) * V * 4), 0));
         store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
-        const rsrc_t rd = make_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V);
-        const rsrc_t rR = make_rsrc(p.R + unit * kC * V);
-        f32x4 dY[4], R[4];
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dY[tb][i] = Io<T>::f32(Io<T>::load(rd, tile_off(tb, i, g, v0 + c, V, H * V, n, es), 0));
-                R[tb][i] = Io<float>::f32(Io<float>::load(rR, tile_off(tb, i, g, v0 + c, V, V, n, 4), 0));
-            }
-        const Op<T> yo[2] = {exact<T>(dY[0], dY[1]), exact<T>(dY[2], dY[3])};
+        prefetch(j - 1);
+        const Op<T> yo[2] = {cY.op(sY, 0, w, lane), cY.op(sY, 1, w, lane)};
         Op2<T> so[KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(dS[2 * kk], dS[2 * kk + 1]);
-        f32x4 dU[4];
+        f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero};
         float *const dot = p.dot + (unit * ((V + 15) / 16) + v0 / 16) * kC;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) dU[tb] = mma(get_row(sK + (tb * KK + kk) * RB, lane, T()), so[kk], dU[tb]);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 2 * kk + 2; ++tb) pd[tb] = mma(get_op2(sP + tri_up(tb, kk) * kOp2Bytes, lane, T()), yo[kk], pd[tb]);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
             const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
-            f32x4 acc = zero, pd = zero;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) acc = mma(get_op(sK + (tb * KK + kk) * OB, lane, T()), so[kk], acc);
-#pragma unroll
-            for (int kk = tb / 2; kk < 2; ++kk) pd = mma(get_op2(sP + tri_up(tb, kk) * kOp2Bytes, lane, T()), yo[kk], pd);
-            dU[tb] = acc * *reinterpret_cast<const f32x4 *>(&sS[kC + t]) + pd * a.scale;
+            dU[tb] = dU[tb] * *reinterpret_cast<const f32x4 *>(&sS[kC + t]) + pd[tb] * a.scale;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float d = wave_fold<16>(R[tb][i] * dU[tb][i], AddOp());
@@ -108,20 +139,26 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) void delta_
             dU[tb] = dU[tb] * *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]);
         }
         const Op2<T> uo[2] = {computed<T>(dU[0], dU[1]), computed<T>(dU[2], dU[3])};
-        const rsrc_t rv = make_rsrc(static_cast<T *>(p.b.dv) + (row0 * H + head) * V), rx = make_rsrc(p.dX + unit * kC * V);
-        f32x4 dX[4];
+        const rsrc_t rv = chunk_rsrc(static_cast<T *>(p.b.dv) + (row0 * H + head) * V, n, ldy, V, es);
+        const rsrc_t rx = make_rsrc(p.dX + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+        // dX for the state, and transposed for stores of four channels
+        f32x4 dX[4] = {zero, zero, zero, zero}, xt[4] = {zero, zero, zero, zero}, dY[4];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 2 * kk + 2; ++tb) {
+                const Op2<T> tt = get_op2(sT + tri_up(tb, kk) * kOp2Bytes, lane, T());
+                dX[tb] = mma(tt, uo[kk], dX[tb]);
+                xt[tb] = mma(uo[kk], tt, xt[tb]);
+            }
+        tiles(yo[0], dY[0], dY[1]);
+        tiles(yo[1], dY[2], dY[3]);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-            const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
-            dX[tb] = zero;
-#pragma unroll
-            for (int kk = tb / 2; kk < 2; ++kk) dX[tb] = mma(get_op2(sT + tri_up(tb, kk) * kOp2Bytes, lane, T()), uo[kk], dX[tb]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Io<T>::store(dX[tb][i], rv, tile_off(tb, i, g, v0 + c, V, H * V, n, es), 0);
-                Io<float>::store(dX[tb][i], rx, tile_off(tb, i, g, v0 + c, V, V, kC, 4), 0);
-            }
-            const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[t]);
+            const int t = row_index(tb, c), v = v0 + 4 * g;
+            store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * es) : kOffNone, T());
+            store4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[32 * (tb / 2) + 8 * g + 4 * (tb % 2)]);
             dY[tb] = dY[tb] * eg * a.scale;
             dX[tb] = dX[tb] * -eg;
         }
@@ -129,20 +166,21 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) void delta_
         const Op2<T> xo[2] = {computed<T>(dX[0], dX[1]), computed<T>(dX[2], dX[3])};
         const float end = sS[kC - 1];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            dS[kt] = dS[kt] * end;
+        for (int kt = 0; kt < KT; ++kt) dS[kt] = dS[kt] * end;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                dS[kt] = mma(get_op(sQ + (kt * 2 + kk) * OB, lane, T()), qo[kk], dS[kt]);
-                dS[kt] = mma(get_op(sC + (kt * 2 + kk) * OB, lane, T()), xo[kk], dS[kt]);
-            }
-        }
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) dS[kt] = mma(get_col<KP>(sQ, sQ, kt, kk, lane, T()), qo[kk], dS[kt]);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) dS[kt] = mma(get_col<KP>(sK, sC, kt, kk, lane, T()), xo[kk], dS[kt]);
     }
     if (p.b.dh0) store_state<KP>(dS, p.b.dh0 + (seq * H + head) * VK, v0, V, K, lane);
 }
 
 template <typename T, int KP> constexpr size_t rev_lds() {
-    return (KP / 32 * 4 + KP / 16 * 4) * kOpBytes<T> + 2 * kTriBytes + 3 * kC * 4;
+    return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + QSide<T, KP>::kBytes + 2 * kTriBytes + 3 * kC * 4 + Values<T>::kBytes;
 }
 
 // -------------------------------------------------------------------- the rest
@@ -219,7 +257,7 @@ __device__ __forceinline__ float column_total(float v) {
 }
 
 template <typename T, int KP> constexpr size_t grad_lds() {
-    constexpr size_t loop = 4 * kOpBytes<T> + 8 * kOp2Bytes + 2 * (KP / 16) * kOp2Bytes, tail = 4 * (KP / 16) * kOpBytes<T>;
+    constexpr size_t loop = 4 * kOpBytes<T> + 8 * kOp2Bytes + 2 * (KP / 16) * kOp2Bytes, tail = 2 * QSide<T, KP>::kBytes;
     return loop > tail ? loop : tail;
 }
 
@@ -231,7 +269,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char *const sY = smem, *const sX = sY + 4 * OB, *const sR = sX + 4 * kOp2Bytes, *const sS = sR + 4 * kOp2Bytes,
          *const sD = sS + KT * kOp2Bytes;
-    char *const sC = smem, *const sQ = sC + 2 * KT * OB;               // after the loop over the value channels
+    char *const sC = smem, *const sQ = sC + QSide<T, KP>::kBytes;      // after the loop over the value channels
     __shared__ real sG[kC];
     __shared__ float sB[kC], sDG[kC], sTot[kWaves];
     const DeltaArgs &a = p.b.fwd;
@@ -247,8 +285,8 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     const int n = sp.len - step0 < kC ? static_cast<int>(sp.len - step0) : kC;
     const int64_t row0 = sp.row0 + step0;
     const f32x4 zero = {0, 0, 0, 0};
-    const rsrc_t rk = make_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K);
-    const rsrc_t rq = make_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K);
+    const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, sizeof(T));
+    const rsrc_t rq = chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, sizeof(T));
     f32x4 dqs[SHARED ? KT : 1], dks[SHARED ? KT : 1];
     if constexpr (SHARED) {
 #pragma unroll
@@ -301,8 +339,11 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
             }
         }
         __syncthreads();
-        stage_columns<T, KP>(sC, rk, a.ldk, n, K);
-        stage_columns<T, KP>(sQ, rq, a.ldq, n, K);
+        QSide<T, KP> side;
+        side.load(rk, a.ldk, QSide<T, KP>::offsets(a.ldk, K));
+        side.put(sC);
+        side.load(rq, a.ldq, QSide<T, KP>::offsets(a.ldq, K));
+        side.put(sQ);
         const float eg = scal[t], wt = scal[kC + t], beta = sB[t], end = scal[kC - 1];
         const real gt = sG[t];
 #pragma unroll
@@ -341,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
                 for (int i = 0; i < 4; ++i) kc = fmaf(kv[4 * h + i], kw[kt][i], kc);
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    const Op<T> kcol = get_op(sC + (kt * 2 + kk) * OB, lane, T()), qcol = get_op(sQ + (kt * 2 + kk) * OB, lane, T());
+                    const Op<T> kcol = get_col<KP>(sC, sC, kt, kk, lane, T()), qcol = get_col<KP>(sQ, sQ, kt, kk, lane, T());
                     if (kk <= w / 2) {
                         dq[kt] = mma(kcol, computed<T>(FT[2 * kk], FT[2 * kk + 1]), dq[kt]);
                         ke[kt] = mma(kcol, computed<T>(ET[2 * kk], ET[2 * kk + 1]), ke[kt]);

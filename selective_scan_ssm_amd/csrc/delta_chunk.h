@@ -172,12 +172,12 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
 //   OUT: y is computed (else the states, and R, alone).
 //   ONE: a workgroup does a single chunk from its checkpoint (R of all chunks at once).
 template <typename T, int KP, bool OUT, bool ONE>
-__global__ __launch_bounds__(kThreads) void delta_seq_kernel(SeqParams p) {
-    constexpr int KT = KP / 16, KK = KP / 32, OB = kOpBytes<T>;
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 2 : 1))) void delta_seq_kernel(SeqParams p) {
+    constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    char *const sK = smem, *const sC = sK + (4 * KK) * OB, *const sT = sC + (2 * KT) * OB;
+    char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sT = sC + Cols<T, KP>::kBytes;
     float *const sS = reinterpret_cast<float *>(sT + kTriBytes);
-    char *const sP = sT + kTriBytes + 3 * kC * 4, *const sQ = sP + kTriBytes;
+    char *const sV = sT + kTriBytes + 3 * kC * 4, *const sP = sV + Values<T>::kBytes, *const sQ = sP + kTriBytes;
     const DeltaArgs &a = p.a;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
@@ -208,63 +208,98 @@ __global__ __launch_bounds__(kThreads) void delta_seq_kernel(SeqParams p) {
 #pragma unroll
         for (int i = 0; i < KT; ++i) S[i] = zero;
     }
+    // the next chunk's data, a chunk ahead; past the last one all of it is out of range
+    Rows<T, KP> nK, nQ;
+    Cols<T, KP> nC;
+    Copy<kTriBytes> nT, nP;
+    float nS;
+    Values<T> nV;
+    const uint32_t okr = Rows<T, KP>::offset(a.ldk, K), oqr = Rows<T, KP>::offset(a.ldq, K);
+    const auto okc = Cols<T, KP>::offsets(a.ldk, K);
+    const int ldv = static_cast<int>(a.ldv);
+    const uint32_t ov = Values<T>::offset(ldv, V - vt * 64, w, lane);
+    auto prefetch = [&](int j) {
+        const int jj = j < j1 ? j : j1 - 1;
+        const int64_t row0 = sp.row0 + static_cast<int64_t>(jj) * kC, unit = (sp.slot0 + jj) * H + head;
+        const int n = j < j1 ? (sp.len - j * kC < kC ? sp.len - j * kC : kC) : 0;
+        const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, sizeof(T));
+        const rsrc_t rv = chunk_rsrc(static_cast<const T *>(a.v) + row0 * a.ldv + head * V + vt * 64, n, a.ldv, V - vt * 64, sizeof(T));
+        nK.load(rk, a.ldk, okr);
+        nV.load(rv, ldv, ov);
+        nT.load(p.ws.t + unit * kTriBytes);
+        nS = p.ws.scal[unit * 3 * kC + (threadIdx.x < 3 * kC ? threadIdx.x : 0)];
+        if constexpr (OUT) {
+            nQ.load(chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, sizeof(T)), a.ldq, oqr);
+            nP.load(p.ws.p + unit * kTriBytes);
+        }
+        if constexpr (!ONE) nC.load(rk, a.ldk, okc);
+    };
+    if (j0 < j1) prefetch(j0);
     for (int j = j0; j < j1; ++j) {
         const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC, unit = (sp.slot0 + j) * H + head;
         const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
-        const rsrc_t rk = make_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K);
-        __syncthreads();
-        stage_rows<T, KP>(sK, rk, a.ldk, n, K);
-        stage_columns<T, KP>(sC, rk, a.ldk, n, K);
-        stage_copy<kTriBytes>(sT, p.ws.t + unit * kTriBytes);
-        if (threadIdx.x < 3 * kC) sS[threadIdx.x] = p.ws.scal[unit * 3 * kC + threadIdx.x];
+        __syncthreads();                                   // the chunk before is done with LDS
+        nK.put(sK);
+        nT.put(sT);
+        if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
         if constexpr (OUT) {
-            stage_rows<T, KP>(sQ, make_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K), a.ldq, n, K);
-            stage_copy<kTriBytes>(sP, p.ws.p + unit * kTriBytes);
+            nQ.put(sQ);
+            nP.put(sP);
         }
+        if constexpr (!ONE) nC.put(sC);
+        nV.put(sV);
+        const Values<T> cV = nV;
         __syncthreads();
-        if constexpr (!ONE)
+        if constexpr (!ONE) {
             if (a.ckpt) store_state<KP>(S, a.ckpt + unit * VK, v0, V, K, lane);
-        const rsrc_t rv = make_rsrc(static_cast<const T *>(a.v) + row0 * a.ldv + head * V);
-        f32x4 X[4];
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2) + i;
-                const uint32_t off = t < n && v0 + c < V ? static_cast<uint32_t>((t * a.ldv + v0 + c) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-                X[tb][i] = Io<T>::f32(Io<T>::load(rv, off, 0));
-            }
+            prefetch(j + 1);
+        }
         Op2<T> so[KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(S[2 * kk], S[2 * kk + 1]);
+        f32x4 ks[4] = {zero, zero, zero, zero};
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) ks[tb] = mma(get_row(sK + (tb * KK + kk) * RB, lane, T()), so[kk], ks[tb]);
+        f32x4 X[4];
+        tiles(cV.op(sV, 0, w, lane), X[0], X[1]);
+        tiles(cV.op(sV, 1, w, lane), X[2], X[3]);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-            f32x4 acc = zero;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) acc = mma(get_op(sK + (tb * KK + kk) * OB, lane, T()), so[kk], acc);
             const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[32 * (tb / 2) + 8 * g + 4 * (tb % 2)]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) X[tb][i] = fmaf(-eg[i], acc[i], X[tb][i]);
+            for (int i = 0; i < 4; ++i) X[tb][i] = fmaf(-eg[i], ks[tb][i], X[tb][i]);
+        }
+        f32x4 y[OUT ? 4 : 1];                              // transposed: rows are channels, columns steps
+        if constexpr (OUT) {
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) y[tb] = zero;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) y[tb] = mma(so[kk], get_row(sQ + (tb * KK + kk) * RB, lane, T()), y[tb]);
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) y[tb] = y[tb] * sS[row_index(tb, c)];
         }
         const Op2<T> xo[2] = {computed<T>(X[0], X[1]), computed<T>(X[2], X[3])};
-        f32x4 R[4];
+        if constexpr (!OUT) {                              // R, transposed, for stores of four channels
+            const rsrc_t rr = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+            f32x4 rt[4] = {zero, zero, zero, zero};
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            R[tb] = zero;
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int kk = 0; kk <= tb / 2; ++kk) R[tb] = mma(get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), xo[kk], R[tb]);
-        }
-        if (p.R) {
-            const rsrc_t rr = make_rsrc(p.R + unit * kC * V);
+                for (int tb = 2 * kk; tb < 4; ++tb) rt[tb] = mma(xo[kk], get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), rt[tb]);
+            const int v = v0 + 4 * g;
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2) + i;
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(R[tb][i]), rr, v0 + c < V ? static_cast<uint32_t>((t * V + v0 + c) * 4) : kOffNone, 0, 0);
-                }
+            for (int tb = 0; tb < 4; ++tb) store4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
         }
         if constexpr (ONE) return;
+        f32x4 R[4] = {zero, zero, zero, zero};
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int tb = 2 * kk; tb < 4; ++tb) R[tb] = mma(get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), xo[kk], R[tb]);
         f32x4 W[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
@@ -276,33 +311,30 @@ __global__ __launch_bounds__(kThreads) void delta_seq_kernel(SeqParams p) {
             const Op2<T> uo[2] = {computed<T>(R[0], R[1]), computed<T>(R[2], R[3])};
             const rsrc_t ry = make_rsrc(static_cast<T *>(a.y) + (row0 * H + head) * V);
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {               // transposed: rows are channels, columns steps
-                f32x4 acc = zero;
-                const int t = row_index(tb, c);
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) acc = mma(so[kk], get_op(sQ + (tb * KK + kk) * OB, lane, T()), acc);
-                acc = acc * sS[t];
+                for (int tb = 2 * kk; tb < 4; ++tb) y[tb] = mma(uo[kk], get_op2(sP + tri_low(tb, kk) * kOp2Bytes, lane, T()), y[tb]);
 #pragma unroll
-                for (int kk = 0; kk <= tb / 2; ++kk) acc = mma(uo[kk], get_op2(sP + tri_low(tb, kk) * kOp2Bytes, lane, T()), acc);
-                const int v = v0 + 4 * g;
-                store_io4(acc * a.scale, ry, t < n && v < V ? static_cast<uint32_t>((t * H * V + v) * static_cast<int64_t>(sizeof(T))) : kOffNone, T());
+            for (int tb = 0; tb < 4; ++tb) {
+                const int t = row_index(tb, c), v = v0 + 4 * g;
+                store_io4(y[tb] * a.scale, ry, t < n && v < V ? static_cast<uint32_t>((t * H * V + v) * static_cast<int64_t>(sizeof(T))) : kOffNone, T());
             }
         }
         const Op2<T> wo[2] = {computed<T>(W[0], W[1]), computed<T>(W[2], W[3])};
         const float end = sS[kC - 1];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            S[kt] = S[kt] * end;
+        for (int kt = 0; kt < KT; ++kt) S[kt] = S[kt] * end;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) S[kt] = mma(get_op(sC + (kt * 2 + kk) * OB, lane, T()), wo[kk], S[kt]);
-        }
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) S[kt] = mma(get_col<KP>(sK, sC, kt, kk, lane, T()), wo[kk], S[kt]);
     }
     if constexpr (!ONE)
         if (a.last_state) store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
 }
 
 template <typename T, int KP, bool OUT> constexpr size_t seq_lds() {
-    return (KP / 32 * 4 + KP / 16 * 2) * kOpBytes<T> + kTriBytes + 3 * kC * 4 + (OUT ? kTriBytes + KP / 32 * 4 * kOpBytes<T> : 0);
+    return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + kTriBytes + 3 * kC * 4 + Values<T>::kBytes + (OUT ? kTriBytes + Rows<T, KP>::kBytes : 0);
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }

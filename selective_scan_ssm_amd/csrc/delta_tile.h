@@ -131,6 +131,21 @@ __device__ __forceinline__ void put_op(char *p, int lane, const Op2<float> &o) {
     *reinterpret_cast<f32x4 *>(p + 1024 + lane * 16) = o.b;
 }
 
+// Rows of keys and queries in LDS, operands with channels along K.  bf16: lane
+// groups lie 320 bytes apart, so that the transposing read of a 4 x 16 block (lane l
+// of 16 names row l / 4, piece l % 4 of four channels, and gets column l of the four
+// rows) finds its 16 pieces in different banks.
+template <typename T> constexpr int kRowBytes = kOpBytes<T>;
+template <> inline constexpr int kRowBytes<bf16_t> = 4 * 320;
+__device__ __forceinline__ Op<bf16_t> get_row(const char *p, int lane, bf16_t) {
+    return {*reinterpret_cast<const u32x4 *>(p + lane / 16 * 320 + lane % 16 * 16)};
+}
+__device__ __forceinline__ Op<float> get_row(const char *p, int lane, float) { return get_op(p, lane, 0.0f); }
+__device__ __forceinline__ void put_row(char *p, int lane, const Op<bf16_t> &o) {
+    *reinterpret_cast<u32x4 *>(p + lane / 16 * 320 + lane % 16 * 16) = o.v;
+}
+__device__ __forceinline__ void put_row(char *p, int lane, const Op<float> &o) { put_op(p, lane, o); }
+
 // ------------------------------------------------------------- global memory
 __device__ __forceinline__ f32x4 load4(rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
@@ -241,43 +256,168 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Rows of a chunk of q or k as operands in LDS: slot (tile, kk) holds steps
-// row_index(tile, c), channels 32 kk + 8 g ...  Rows from n on and channels from K
-// on are zeros.  ld in elements; r starts at the chunk's first row.
-template <typename T, int KP> __device__ __forceinline__ void stage_rows(char *dst, rsrc_t r, int64_t ld, int n, int K) {
-    constexpr int KK = KP / 32;
-#pragma unroll
-    for (int i = 0; i < 4 * KK * 64 / kThreads; ++i) {
-        const int s = i * kThreads + threadIdx.x, lane = s % 64, f = s / 64;
-        const int t = row_index(f / KK, lane % 16), k = 32 * (f % KK) + 8 * (lane / 16);
-        const uint32_t off = t < n && k < K ? static_cast<uint32_t>((t * ld + k) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-        put_op(dst + f * kOpBytes<T>, lane, load_op(r, off, T()));
-    }
+// What a workgroup of the recurrence holds of a chunk in LDS.  Each part is loaded
+// into registers (load) a chunk ahead of the LDS writes (put), so the memory
+// latency runs beside the chunk before.
+
+// A chunk's n steps of one head, from its first element: what lies behind the last
+// step reads as 0, so offsets inside a chunk do not depend on how long it is.
+__device__ __forceinline__ rsrc_t chunk_rsrc(const void *p, int n, int64_t ld, int width, int size) {
+    return make_rsrc(p, n > 0 ? static_cast<uint32_t>(((n - 1) * static_cast<int>(ld) + width) * size) : 0u);
 }
-// The same chunk with steps along K: slot (tile, kk) holds channels (rows)
-// row_index within 32-channel pairs of tiles, steps 32 kk + 8 g ...
-template <typename T, int KP> __device__ __forceinline__ void stage_columns(char *dst, rsrc_t r, int64_t ld, int n, int K) {
-    constexpr int KT = KP / 16;
-#pragma unroll
-    for (int i = 0; i < KT * 2 * 32 / kThreads; ++i) {
-        const int s = i * kThreads + threadIdx.x, f = s / 32, pair = s % 8, g = (s / 8) % 4;
-        const int tile = f / 2, kk = f % 2, c = 2 * pair;
-        const int k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4, t0 = 32 * kk + 8 * g;
-        Columns<T> w;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w.load(r, j, t0 + j < n && k < K ? static_cast<uint32_t>(((t0 + j) * ld + k) * static_cast<int64_t>(sizeof(T))) : kOffNone);
-        w.put(dst + f * kOpBytes<T>, 16 * g + c);
+// Rows of q or k as operands: slot (tile, kk) holds steps row_index(tile, c),
+// channels 32 kk + 8 g ...  Channels from K on are zeros.  ld in elements.
+template <typename T, int KP> struct Rows {
+    static constexpr int KK = KP / 32, N = 4 * KK * 64 / kThreads, kBytes = 4 * KK * kRowBytes<T>;
+    static constexpr int kTiles = kWaves / KK;                 // tiles that the threads cover at a time
+    Op<T> v[N];
+    // the thread's offset in the first tiles; the others are whole rows further on
+    static __device__ __forceinline__ uint32_t offset(int64_t ld, int K) {
+        const int lane = threadIdx.x % 64, f = threadIdx.x / 64;
+        const int t = row_index(f / KK, lane % 16), k = 32 * (f % KK) + 8 * (lane / 16);
+        return k < K ? static_cast<uint32_t>((t * static_cast<int>(ld) + k) * static_cast<int>(sizeof(T))) : kOffNone;
     }
+    __device__ __forceinline__ void load(rsrc_t r, int64_t ld, uint32_t off) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = load_op(r, off + static_cast<uint32_t>(row_index(i * kTiles, 0) * static_cast<int>(ld) * static_cast<int>(sizeof(T))), T());
+    }
+    __device__ __forceinline__ void put(char *dst) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = i * kThreads + threadIdx.x;
+            put_row(dst + s / 64 * kRowBytes<T>, s % 64, v[i]);
+        }
+    }
+};
+// The same chunk with steps along K: slot (tile, kk) holds channels row_index (of
+// each 32) as rows, steps 32 kk + 8 g ...  fp32 only: bf16 reads the rows' copy
+// transposed, which saves eight narrow loads a thread and 16 KB of LDS.
+template <typename T, int KP> struct Cols {
+    static constexpr int KT = KP / 16, N = KT * 2 * 32 / kThreads, kBytes = 2 * KT * kOpBytes<T>;
+    Columns<T> v[N];
+    static __device__ __forceinline__ uint32_t offset(int64_t ld, int i, int K) {
+        const int s = i * kThreads + threadIdx.x, f = s / 32, c = 2 * (s % 8), g = (s / 8) % 4;
+        const int tile = f / 2, k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4, t0 = 32 * (f % 2) + 8 * g;
+        return k < K ? static_cast<uint32_t>((t0 * static_cast<int>(ld) + k) * static_cast<int>(sizeof(T))) : kOffNone;
+    }
+    struct Offsets {
+        uint32_t at[N];
+    };
+    static __device__ __forceinline__ Offsets offsets(int64_t ld, int K) {
+        Offsets o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.at[i] = offset(ld, i, K);
+        return o;
+    }
+    __device__ __forceinline__ void load(rsrc_t r, int64_t ld, const Offsets &o) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i].load(r, j, o.at[i] + static_cast<uint32_t>(j * static_cast<int>(ld) * static_cast<int>(sizeof(T))));
+    }
+    __device__ __forceinline__ void put(char *dst) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = i * kThreads + threadIdx.x, f = s / 32;
+            v[i].put(dst + f * kOpBytes<T>, 16 * ((s / 8) % 4) + 2 * (s % 8));
+        }
+    }
+};
+template <int KP> struct Cols<bf16_t, KP> {
+    static constexpr int kBytes = 0;
+    struct Offsets {};
+    static __device__ __forceinline__ Offsets offsets(int64_t, int) { return {}; }
+    __device__ __forceinline__ void load(rsrc_t, int64_t, const Offsets &) {}
+    __device__ __forceinline__ void put(char *) const {}
+};
+// channels of tile kt as rows, steps 32 kk + 8 g ... along K, from the rows or the columns in LDS
+template <int KP> __device__ __forceinline__ Op<bf16_t> get_col(const char *rows, const char *, int kt, int kk, int lane, bf16_t) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    using lds = __attribute__((address_space(3))) s16x4 *;
+    const int l = lane % 16;
+    const char *const p = rows + (l % 4) * 320 + (4 * (lane / 16) + l / 4) * 16 + (2 * kk * (KP / 32) + kt / 2) * kRowBytes<bf16_t> + kt % 2 * 8;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(p)));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(p + KP / 32 * kRowBytes<bf16_t>)));
+    const u32x2 u = __builtin_bit_cast(u32x2, a), v = __builtin_bit_cast(u32x2, b);
+    return {u32x4{u[0], u[1], v[0], v[1]}};
+}
+template <int KP> __device__ __forceinline__ Op<float> get_col(const char *, const char *cols, int kt, int kk, int lane, float) {
+    return get_op(cols + (kt * 2 + kk) * kOpBytes<float>, lane, 0.0f);
+}
+// A chunk's steps of the workgroup's 64 value channels; a wave gets its 16 of them as
+// the columns of accumulator tiles, or as an operand with steps along K.  bf16 goes
+// through LDS (two 16-byte loads a thread instead of sixteen 2-byte ones) and is
+// read transposed, fp32 straight to the lanes.  w: the wave; V: channels from the
+// workgroup's first on.
+template <typename T> struct Values;
+template <> struct Values<bf16_t> {
+    static constexpr int kBytes = 8 * kRowBytes<bf16_t>;
+    Op<bf16_t> v[2];
+    static __device__ __forceinline__ uint32_t offset(int ld, int V, int, int) {
+        const int lane = threadIdx.x % 64, f = threadIdx.x / 64, t = row_index(f / 2, lane % 16), c = 32 * (f % 2) + 8 * (lane / 16);
+        return c < V ? static_cast<uint32_t>((t * ld + c) * 2) : kOffNone;
+    }
+    __device__ __forceinline__ void load(rsrc_t r, int ld, uint32_t off) {
+        v[0] = load_op(r, off, bf16_t());
+        v[1] = load_op(r, off + static_cast<uint32_t>(32 * ld * 2), bf16_t());
+    }
+    __device__ __forceinline__ void put(char *dst) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) put_row(dst + (4 * i + threadIdx.x / 64) * kRowBytes<bf16_t>, threadIdx.x % 64, v[i]);
+    }
+    // steps 32 p ..
+    __device__ __forceinline__ Op<bf16_t> op(const char *src, int p, int w, int lane) const {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        using lds = __attribute__((address_space(3))) s16x4 *;
+        const int l = lane % 16, piece = l % 4;
+        const char *const q = src + (4 * p + w / 2) * kRowBytes<bf16_t> + (2 * (w % 2) + piece / 2) * 320 + (4 * (lane / 16) + l / 4) * 16 + piece % 2 * 8;
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q))));
+        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q + 2 * kRowBytes<bf16_t>))));
+        return {u32x4{a[0], a[1], b[0], b[1]}};
+    }
+};
+template <> struct Values<float> {
+    static constexpr int kBytes = 0;
+    float v[16];
+    static __device__ __forceinline__ uint32_t offset(int ld, int V, int w, int lane) {
+        const int c = 16 * w + lane % 16;
+        return c < V ? static_cast<uint32_t>((8 * (lane / 16) * ld + c) * 4) : kOffNone;
+    }
+    __device__ __forceinline__ void load(rsrc_t r, int ld, uint32_t off) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = Io<float>::f32(Io<float>::load(r, off + static_cast<uint32_t>((32 * (i / 8) + i % 8) * ld * 4), 0));
+    }
+    __device__ __forceinline__ void put(char *) const {}
+    __device__ __forceinline__ Op<float> op(const char *, int p, int, int) const {
+        return {f32x4{v[8 * p], v[8 * p + 1], v[8 * p + 2], v[8 * p + 3]}, f32x4{v[8 * p + 4], v[8 * p + 5], v[8 * p + 6], v[8 * p + 7]}};
+    }
+};
+// an operand's eight elements as the registers of a pair of tiles
+__device__ __forceinline__ void tiles(const Op<bf16_t> &o, f32x4 &a, f32x4 &b) {
+    a = f32x4{low(o.v[0]), high(o.v[0]), low(o.v[1]), high(o.v[1])};
+    b = f32x4{low(o.v[2]), high(o.v[2]), low(o.v[3]), high(o.v[3])};
+}
+__device__ __forceinline__ void tiles(const Op<float> &o, f32x4 &a, f32x4 &b) {
+    a = o.a;
+    b = o.b;
 }
 // bytes from the workspace as they are
-template <int BYTES> __device__ __forceinline__ void stage_copy(char *dst, const char *src) {
+template <int BYTES> struct Copy {
+    static constexpr int N = BYTES / (16 * kThreads);
     static_assert(BYTES % (16 * kThreads) == 0, "whole pieces");
+    u32x4 v[N];
+    __device__ __forceinline__ void load(const char *src) {
+        const rsrc_t r = make_rsrc(src, BYTES);
 #pragma unroll
-    for (int i = 0; i < BYTES / (16 * kThreads); ++i)
-        *reinterpret_cast<u32x4 *>(dst + (i * kThreads + threadIdx.x) * 16) =
-            *reinterpret_cast<const u32x4 *>(src + (i * kThreads + threadIdx.x) * 16);
-}
+        for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (i * kThreads + threadIdx.x) * 16, 0, 0);
+    }
+    __device__ __forceinline__ void put(char *dst) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(dst + (i * kThreads + threadIdx.x) * 16) = v[i];
+    }
+};
 
 // A wave's 16 columns of a state, (V, K) in memory with K contiguous, as tiles
 // whose rows are K: columns v0 + c, pairs of tiles of 32 channels.
