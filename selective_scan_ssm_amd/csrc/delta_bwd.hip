@@ -15,7 +15,7 @@
 // Launches: the chunks' preparation; the states entering the chunks and R (one
 // walk over the chunks, or, from saved states, all chunks at once); dS' and dX, in
 // reverse; the rest, all chunks at once.
-#include "delta_chunk.h"
+#include "delta_flow.h"
 
 namespace ssm {
 namespace delta {
@@ -44,7 +44,7 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
     char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sQ = sC + Cols<T, KP>::kBytes,
          *const sT = sQ + QSide<T, KP>::kBytes, *const sP = sT + kTriBytes;
     char *const sY = sP + kTriBytes;
-    float *const sS = reinterpret_cast<float *>(sY + Values<T>::kBytes);
+    float *const sS = reinterpret_cast<float *>(sY + Values<T, 1>::kBytes);
     const DeltaArgs &a = p.b.fwd;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
@@ -71,12 +71,12 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
     QSide<T, KP> nQ;
     Copy<kTriBytes> nT, nP;
     float nS;
-    Values<T> nY;
+    Values<T, 1> nY;
     const uint32_t okr = Rows<T, KP>::offset(a.ldk, K);
     const auto okc = Cols<T, KP>::offsets(a.ldk, K);
     const auto oqc = QSide<T, KP>::offsets(a.ldq, K);
     const int ldy = static_cast<int>(H * V);
-    const uint32_t oy = Values<T>::offset(ldy, V - vt * 64, w, lane);
+    const uint32_t oy = Values<T, 1>::offset(ldy, V - vt * 64, w, lane);
     const uint32_t oR = v0 + c < V ? static_cast<uint32_t>((8 * g * V + v0 + c) * 4) : kOffNone;
     auto prefetch = [&](int j) {
         const int jj = j >= 0 ? j : 0;
@@ -104,7 +104,7 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
         nP.put(sP);
         if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
         nY.put(sY);
-        const Values<T> cY = nY;
+        const Values<T, 1> cY = nY;
         __syncthreads();
         const rsrc_t rR = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
         f32x4 R[4];                                        // needed late in the chunk
@@ -180,7 +180,7 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
 }
 
 template <typename T, int KP> constexpr size_t rev_lds() {
-    return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + QSide<T, KP>::kBytes + 2 * kTriBytes + 3 * kC * 4 + Values<T>::kBytes;
+    return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + QSide<T, KP>::kBytes + 2 * kTriBytes + 3 * kC * 4 + Values<T, 1>::kBytes;
 }
 
 // -------------------------------------------------------------------- the rest
@@ -452,9 +452,9 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
 }
 
 struct BwdWs {
-    size_t t, tt, p, scal, R, dX, dS, dot, ckpt, total;
+    size_t t, tt, p, scal, R, dX, dS, dot, ckpt, ends, maps, total;
 };
-BwdWs bwd_ws(const DeltaShape &s, bool saved) {
+BwdWs bwd_ws(const DeltaShape &s, const Plan &plan, bool saved) {
     const size_t units = static_cast<size_t>(s.slots * s.heads), V = s.dv, K = s.dk;
     BwdWs w{};
     w.tt = w.t + align256(units * kTriBytes);
@@ -465,13 +465,16 @@ BwdWs bwd_ws(const DeltaShape &s, bool saved) {
     w.dS = w.dX + align256(units * kC * V * 4);
     w.dot = w.dS + align256(units * V * K * 4);
     w.ckpt = w.dot + align256(units * ((V + 15) / 16) * kC * 4);
-    w.total = w.ckpt + (saved ? 0 : align256(units * V * K * 4));
+    w.ends = w.ckpt + (saved ? 0 : align256(units * V * K * 4));
+    w.maps = w.ends + ends_bytes(s, plan);
+    w.total = w.maps + maps_bytes(s, plan);
     return w;
 }
 
 template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t s) {
     const DeltaShape &sh = b.fwd.s;
-    const BwdWs w = bwd_ws(sh, b.fwd.ckpt != nullptr);
+    const Plan plan = plan_of(sh, b.fwd.bf16);
+    const BwdWs w = bwd_ws(sh, plan, b.fwd.ckpt != nullptr);
     char *const base = static_cast<char *>(b.fwd.workspace);
     BwdParams p{};
     p.b = b;
@@ -489,11 +492,18 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
         q.a.last_state = nullptr;
         q.ws = p.ws;
         q.R = R;
+        q.cps = plan.cps;
+        q.wide = plan.wide;
+        q.wide_ends = plan.wide_ends;
+        q.segments = plan.segments;
+        q.ends = reinterpret_cast<float *>(base + w.ends);
+        q.maps = base + w.maps;
         if (b.fwd.ckpt) {
-            if (hipError_t e = launch_seq<T, KP, false, true>(q, s)) return e;
+            if (hipError_t e = launch_seq<T, KP, kOne, 1>(q, s)) return e;
         } else {
             q.a.ckpt = p.b.fwd.ckpt = reinterpret_cast<float *>(base + w.ckpt);
-            if (hipError_t e = launch_seq<T, KP, false, false>(q, s)) return e;
+            if (hipError_t e = launch_segments<T, KP>(q, s)) return e;
+            if (hipError_t e = launch_walk<T, KP, kSave>(q, s)) return e;
         }
     }
     const int64_t nvt = (sh.dv + 63) / 64;
@@ -510,8 +520,8 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
 }  // namespace
 }  // namespace delta
 
-size_t delta_scan_bwd_workspace(const DeltaShape &s, bool saved) {
-    return s.slots * s.heads > 0 ? delta::bwd_ws(s, saved).total : 0;
+size_t delta_scan_bwd_workspace(const DeltaShape &s, int bf16, bool saved) {
+    return s.slots * s.heads > 0 ? delta::bwd_ws(s, delta::plan_of(s, bf16), saved).total : 0;
 }
 hipError_t launch_delta_scan_bwd(const DeltaBwdArgs &b, hipStream_t s) {
     using namespace delta;

@@ -19,8 +19,15 @@ struct ChunkWs {
 struct SeqParams {
     DeltaArgs a;
     ChunkWs ws;
-    float *R;                       // per (slot, head): (64, V) fp32, or null
+    float *R;                       // per (slot, head): (64, V) fp32
+    int cps;                        // chunks of a time segment
+    bool wide, wide_ends;           // see Plan
+    int64_t segments;               // slots of segments
+    float *ends;                    // per (segment, head): (V, K) fp32, the state it leaves
+    char *maps;                     // per (segment, head): its transition as operands
 };
+// Operands of a segment's transition: (KP / 32, KP / 16) of them.
+template <int KP> constexpr int64_t kMapBytes = static_cast<int64_t>(KP / 32) * (KP / 16) * kOp2Bytes;
 
 // ---------------------------------------------------------------- preparation
 // A wave per (chunk, head).  With Gam_ts = exp(G_t - G_s) (s <= t):
@@ -162,81 +169,143 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
 }
 
 // ------------------------------------------------------------------ recurrence
-// A workgroup owns (sequence, head, 64 value channels) and walks the chunks; a wave
-// keeps 16 channels' state (K x 16, fp32) in accumulator tiles.  A chunk, with S
-// the state entering it:
+// A workgroup owns (sequence's time segment, head, 64 CT value channels) and walks the
+// chunks; a wave keeps 16 channels' state (K x 16, fp32) in accumulator tiles.  A
+// chunk, with S the state entering it:
 //     X = V - exp(G) K S,  R = T X,  U = beta R
 //     Y = scale (exp(G) Q S + P U),  S <- exp(G_end) S + K^T (exp(G_end - G) U)
 // Every product's computed operand comes from the accumulators of the one before;
-// K, K^T, Q, T and P are shared by the waves through LDS.
-//   OUT: y is computed (else the states, and R, alone).
-//   ONE: a workgroup does a single chunk from its checkpoint (R of all chunks at once).
-template <typename T, int KP, bool OUT, bool ONE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 2 : 1))) void delta_seq_kernel(SeqParams p) {
+// K, Q, T and P are shared by the waves through LDS.
+//
+// A sequence is one segment where there are heads enough to fill the GPU.  Else it
+// is cut: kEnds finds what every segment but the last leaves from zero, and its
+// transition (the state is an affine function of the one entering: 64 channels more
+// that start as columns of the identity, with V = 0); delta_carry_kernel joins them,
+// and the pass proper starts every segment from the state it is entered with.
+enum Mode {
+    kOut,       // y (and the states entering the chunks, for a gradient to come)
+    kSave,      // the states entering the chunks, and R
+    kOne,       // R of one chunk from its saved state, all chunks at once
+    kEnds       // the segments' ends
+};
+template <typename T, int KP, Mode MODE, int CT>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && CT == 1 ? 2 : 1))) void delta_seq_kernel(SeqParams p) {
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
+    constexpr bool OUT = MODE == kOut, ONE = MODE == kOne;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sT = sC + Cols<T, KP>::kBytes;
     float *const sS = reinterpret_cast<float *>(sT + kTriBytes);
-    char *const sV = sT + kTriBytes + 3 * kC * 4, *const sP = sV + Values<T>::kBytes, *const sQ = sP + kTriBytes;
+    char *const sV = sT + kTriBytes + 3 * kC * 4, *const sP = sV + Values<T, CT>::kBytes, *const sQ = sP + kTriBytes;
     const DeltaArgs &a = p.a;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
     const int64_t H = a.s.heads;
-    const int nvt = (V + 63) / 64;
-    const int vt = blockIdx.x % nvt;
-    const int64_t rest = blockIdx.x / nvt, head = rest % H, kh = head / (H / a.s.kheads);
-    const int64_t seq = ONE ? sequence_of(a.s, rest / H) : rest / H;
-    const Span sp = span_of(a.s, seq);
-    const int nchunks = (sp.len + kC - 1) / kC;
-    int j0 = 0, j1 = nchunks;
+    constexpr int kWide = 64 * CT;
+    const int nvt = (V + kWide - 1) / kWide, tiles_n = MODE == kEnds ? nvt + (KP + kWide - 1) / kWide : nvt;
+    const int tile = blockIdx.x % tiles_n;
+    const int64_t rest = blockIdx.x / tiles_n, head = rest % H, kh = head / (H / a.s.kheads), id = rest / H;
+    Span sp;
+    int64_t seq;
+    int j0, j1;
+    bool first = true, last = true;
     if constexpr (ONE) {
-        const int64_t j = rest / H - sp.slot0;
-        if (j < 0 || j >= nchunks) return;
+        seq = sequence_of(a.s, id);
+        sp = span_of(a.s, seq);
+        const int64_t j = id - sp.slot0;
+        if (j < 0 || j * kC >= sp.len) return;
         j0 = static_cast<int>(j);
         j1 = j0 + 1;
+    } else {
+        const Segment sg = segment_of(a.s, id, p.cps, sp);
+        if (!sg.used) return;
+        seq = sg.seq;
+        j0 = sg.j0;
+        j1 = sg.j1;
+        first = sg.s == 0;
+        last = sg.last;
     }
-    const int v0 = vt * 64 + w * 16;
+    const bool transition = MODE == kEnds && tile >= nvt;
+    if (MODE == kEnds && (last || (first && transition))) return;
+    const int vt = transition ? 0 : tile;
+    const int v0 = vt * kWide + w * 16 * CT;               // the wave's first channel
     const f32x4 zero = {0, 0, 0, 0};
     const size_t VK = static_cast<size_t>(V) * K;
-    f32x4 S[KT];
-    if constexpr (ONE) {
-        load_state<KP>(S, a.ckpt + ((sp.slot0 + j0) * H + head) * VK, v0, V, K, lane);
-    } else if (a.h0) {
-        load_state<KP>(S, a.h0 + (seq * H + head) * VK, v0, V, K, lane);
-    } else {
+    f32x4 S[CT][KT];
 #pragma unroll
-        for (int i = 0; i < KT; ++i) S[i] = zero;
+    for (int ct = 0; ct < CT; ++ct) {
+        const int v = v0 + 16 * ct;
+        if constexpr (ONE) {
+            load_state<KP>(S[ct], a.ckpt + ((sp.slot0 + j0) * H + head) * VK, v, V, K, lane);
+        } else if (transition) {
+            const int col = (tile - nvt) * kWide + (w * CT + ct) * 16 + c;
+#pragma unroll
+            for (int q = 0; q < KK; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    S[ct][2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
+                    S[ct][2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
+                }
+        } else if (MODE != kEnds && !first) {
+            load_state<KP>(S[ct], p.ends + ((id - 1) * H + head) * VK, v, V, K, lane);
+        } else if (first && a.h0) {
+            load_state<KP>(S[ct], a.h0 + (seq * H + head) * VK, v, V, K, lane);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) S[ct][i] = zero;
+        }
     }
     // the next chunk's data, a chunk ahead; past the last one all of it is out of range
     Rows<T, KP> nK, nQ;
     Cols<T, KP> nC;
     Copy<kTriBytes> nT, nP;
     float nS;
-    Values<T> nV;
+    Values<T, CT> nV;
     const uint32_t okr = Rows<T, KP>::offset(a.ldk, K), oqr = Rows<T, KP>::offset(a.ldq, K);
     const auto okc = Cols<T, KP>::offsets(a.ldk, K);
     const int ldv = static_cast<int>(a.ldv);
-    const uint32_t ov = Values<T>::offset(ldv, V - vt * 64, w, lane);
-    auto prefetch = [&](int j) {
-        const int jj = j < j1 ? j : j1 - 1;
-        const int64_t row0 = sp.row0 + static_cast<int64_t>(jj) * kC, unit = (sp.slot0 + jj) * H + head;
-        const int n = j < j1 ? (sp.len - j * kC < kC ? sp.len - j * kC : kC) : 0;
-        const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, sizeof(T));
-        const rsrc_t rv = chunk_rsrc(static_cast<const T *>(a.v) + row0 * a.ldv + head * V + vt * 64, n, a.ldv, V - vt * 64, sizeof(T));
+    const uint32_t ov = Values<T, CT>::offset(ldv, V - vt * kWide, w, lane);
+    // addresses move on by whole chunks; loads are issued in two parts, each beside products, as a chunk's loads take
+    // the memory pipe longer than the waves can queue them
+    const T *pk = static_cast<const T *>(a.k) + (sp.row0 + static_cast<int64_t>(j0) * kC) * a.ldk + kh * K;
+    const T *pq = static_cast<const T *>(a.q) + (sp.row0 + static_cast<int64_t>(j0) * kC) * a.ldq + kh * K;
+    const T *pv = static_cast<const T *>(a.v) + (sp.row0 + static_cast<int64_t>(j0) * kC) * a.ldv + head * V + vt * kWide;
+    int64_t unit = (sp.slot0 + j0) * H + head;             // of the chunk at hand
+    const char *pt = p.ws.t + unit * kTriBytes, *pp = p.ws.p + unit * kTriBytes;
+    const float *ps = p.ws.scal + unit * 3 * kC;
+    int left = sp.len - j0 * kC;
+    const int tS = threadIdx.x < 3 * kC ? threadIdx.x : 0;
+    auto prefetch1 = [&]() {
+        const int n = left < kC ? left : kC;
+        const rsrc_t rk = chunk_rsrc(pk, n, a.ldk, K, sizeof(T));
         nK.load(rk, a.ldk, okr);
-        nV.load(rv, ldv, ov);
-        nT.load(p.ws.t + unit * kTriBytes);
-        nS = p.ws.scal[unit * 3 * kC + (threadIdx.x < 3 * kC ? threadIdx.x : 0)];
-        if constexpr (OUT) {
-            nQ.load(chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, sizeof(T)), a.ldq, oqr);
-            nP.load(p.ws.p + unit * kTriBytes);
-        }
-        if constexpr (!ONE) nC.load(rk, a.ldk, okc);
+        nC.load(rk, a.ldk, okc);
+        nT.load(pt);
     };
-    if (j0 < j1) prefetch(j0);
-    for (int j = j0; j < j1; ++j) {
-        const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC, unit = (sp.slot0 + j) * H + head;
+    auto prefetch2 = [&]() {
+        const int n = left < kC ? left : kC;
+        nV.load(chunk_rsrc(pv, transition ? 0 : n, a.ldv, V - vt * kWide, sizeof(T)), ldv, ov);
+        nS = ps[tS];
+        if constexpr (OUT) {
+            nQ.load(chunk_rsrc(pq, n, a.ldq, K, sizeof(T)), a.ldq, oqr);
+            nP.load(pp);
+        }
+        left -= kC;
+        if (left > 0) {                                    // else what is loaded is not used: the last chunk's again
+            pk += kC * a.ldk;
+            pq += kC * a.ldq;
+            pv += kC * a.ldv;
+            pt += H * kTriBytes;
+            pp += H * kTriBytes;
+            ps += H * 3 * kC;
+        }
+    };
+    if (j0 < j1) {
+        prefetch1();
+        prefetch2();
+    }
+    for (int j = j0; j < j1; ++j, unit += H) {
+        const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC;
         const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
         __syncthreads();                                   // the chunk before is done with LDS
         nK.put(sK);
@@ -246,95 +315,226 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
             nQ.put(sQ);
             nP.put(sP);
         }
-        if constexpr (!ONE) nC.put(sC);
+        nC.put(sC);
         nV.put(sV);
-        const Values<T> cV = nV;
+        const Values<T, CT> cV = nV;
         __syncthreads();
         if constexpr (!ONE) {
-            if (a.ckpt) store_state<KP>(S, a.ckpt + unit * VK, v0, V, K, lane);
-            prefetch(j + 1);
-        }
-        Op2<T> so[KK];
+            if (MODE != kEnds && a.ckpt) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(S[2 * kk], S[2 * kk + 1]);
-        f32x4 ks[4] = {zero, zero, zero, zero};
+                for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * VK, v0 + 16 * ct, V, K, lane);
+            }
+        }
+        Op2<T> so[CT][KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) ks[tb] = mma(get_row(sK + (tb * KK + kk) * RB, lane, T()), so[kk], ks[tb]);
-        f32x4 X[4];
-        tiles(cV.op(sV, 0, w, lane), X[0], X[1]);
-        tiles(cV.op(sV, 1, w, lane), X[2], X[3]);
+            for (int ct = 0; ct < CT; ++ct) so[ct][kk] = computed<T>(S[ct][2 * kk], S[ct][2 * kk + 1]);
+        f32x4 ks[CT][4];
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[32 * (tb / 2) + 8 * g + 4 * (tb % 2)]);
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) X[tb][i] = fmaf(-eg[i], ks[tb][i], X[tb][i]);
-        }
-        f32x4 y[OUT ? 4 : 1];                              // transposed: rows are channels, columns steps
+            for (int tb = 0; tb < 4; ++tb) ks[ct][tb] = zero;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                const Op<T> f = get_row(sK + (tb * KK + kk) * RB, lane, T());
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) ks[ct][tb] = mma(f, so[ct][kk], ks[ct][tb]);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!ONE) prefetch1();
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 y[OUT ? CT : 1][4];                          // transposed: rows are channels, columns steps
         if constexpr (OUT) {
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) y[tb] = zero;
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) y[ct][tb] = zero;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb) y[tb] = mma(so[kk], get_row(sQ + (tb * KK + kk) * RB, lane, T()), y[tb]);
+                for (int tb = 0; tb < 4; ++tb) {
+                    const Op<T> f = get_row(sQ + (tb * KK + kk) * RB, lane, T());
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) y[tb] = y[tb] * sS[row_index(tb, c)];
-        }
-        const Op2<T> xo[2] = {computed<T>(X[0], X[1]), computed<T>(X[2], X[3])};
-        if constexpr (!OUT) {                              // R, transposed, for stores of four channels
-            const rsrc_t rr = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
-            f32x4 rt[4] = {zero, zero, zero, zero};
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int tb = 2 * kk; tb < 4; ++tb) rt[tb] = mma(xo[kk], get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), rt[tb]);
-            const int v = v0 + 4 * g;
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) store4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
-        }
-        if constexpr (ONE) return;
-        f32x4 R[4] = {zero, zero, zero, zero};
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int tb = 2 * kk; tb < 4; ++tb) R[tb] = mma(get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), xo[kk], R[tb]);
-        f32x4 W[4];
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
-            R[tb] = R[tb] * *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]);       // U
-            W[tb] = R[tb] * *reinterpret_cast<const f32x4 *>(&sS[kC + t]);
-        }
-        if constexpr (OUT) {
-            const Op2<T> uo[2] = {computed<T>(R[0], R[1]), computed<T>(R[2], R[3])};
-            const rsrc_t ry = make_rsrc(static_cast<T *>(a.y) + (row0 * H + head) * V);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int tb = 2 * kk; tb < 4; ++tb) y[tb] = mma(uo[kk], get_op2(sP + tri_low(tb, kk) * kOp2Bytes, lane, T()), y[tb]);
+                    for (int ct = 0; ct < CT; ++ct) y[ct][tb] = mma(so[ct][kk], f, y[ct][tb]);
+                }
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
-                const int t = row_index(tb, c), v = v0 + 4 * g;
-                store_io4(y[tb] * a.scale, ry, t < n && v < V ? static_cast<uint32_t>((t * H * V + v) * static_cast<int64_t>(sizeof(T))) : kOffNone, T());
+                const float e = sS[row_index(tb, c)];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[ct][tb] = y[ct][tb] * e;
             }
         }
-        const Op2<T> wo[2] = {computed<T>(W[0], W[1]), computed<T>(W[2], W[3])};
-        const float end = sS[kC - 1];
+        Op2<T> xo[CT][2];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] = S[kt] * end;
+        for (int q = 0; q < 2; ++q) {                      // 32 steps
+            const f32x4 e0 = *reinterpret_cast<const f32x4 *>(&sS[32 * q + 8 * g]), e1 = *reinterpret_cast<const f32x4 *>(&sS[32 * q + 8 * g + 4]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                f32x4 x0, x1;
+                tiles(cV.op(sV, q, w * CT + ct, lane), x0, x1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x0[i] = fmaf(-e0[i], ks[ct][2 * q][i], x0[i]);
+                    x1[i] = fmaf(-e1[i], ks[ct][2 * q + 1][i], x1[i]);
+                }
+                xo[ct][q] = computed<T>(x0, x1);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!ONE) prefetch2();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == kSave || ONE) {              // R, transposed, for stores of four channels
+            const rsrc_t rr = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+            f32x4 rt[CT][4];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) rt[ct][tb] = zero;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int tb = 2 * kk; tb < 4; ++tb)
+                        rt[ct][tb] = mma(xo[ct][kk], get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), rt[ct][tb]);
+                const int v = v0 + 16 * ct + 4 * g;
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) store4(rt[ct][tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
+            }
+        }
+        if constexpr (ONE) return;
+        f32x4 R[CT][4];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) R[ct][tb] = zero;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) S[kt] = mma(get_col<KP>(sK, sC, kt, kk, lane, T()), wo[kk], S[kt]);
+            for (int tb = 2 * kk; tb < 4; ++tb) {
+                const Op2<T> f = get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T());
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) R[ct][tb] = mma(f, xo[ct][kk], R[ct][tb]);
+            }
+        Op2<T> uo[OUT ? CT : 1][2], wo[CT][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = 32 * q + 8 * g;
+            const f32x4 b0 = *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]), b1 = *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t + 4]);
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&sS[kC + t]), w1 = *reinterpret_cast<const f32x4 *>(&sS[kC + t + 4]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const f32x4 u0 = R[ct][2 * q] * b0, u1 = R[ct][2 * q + 1] * b1;
+                if constexpr (OUT) uo[ct][q] = computed<T>(u0, u1);
+                wo[ct][q] = computed<T>(u0 * w0, u1 * w1);
+            }
+        }
+        if constexpr (OUT) {
+            const rsrc_t ry = chunk_rsrc(static_cast<T *>(a.y) + (row0 * H + head) * V, n, H * V, V, sizeof(T));
+            const int ldy = static_cast<int>(H) * V;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int tb = 2 * kk; tb < 4; ++tb) {
+                    const Op2<T> f = get_op2(sP + tri_low(tb, kk) * kOp2Bytes, lane, T());
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) y[ct][tb] = mma(uo[ct][kk], f, y[ct][tb]);
+                }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int v = v0 + 16 * ct + 4 * g;
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb)
+                    store_io4(y[ct][tb] * a.scale, ry, v < V ? static_cast<uint32_t>((row_index(tb, c) * ldy + v) * static_cast<int>(sizeof(T))) : kOffNone, T());
+            }
+        }
+        const float end = sS[kC - 1];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) S[ct][kt] = S[ct][kt] * end;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                const Op<T> f = get_col<KP>(sK, sC, kt, kk, lane, T());
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[ct][kt] = mma(f, wo[ct][kk], S[ct][kt]);
+            }
     }
-    if constexpr (!ONE)
-        if (a.last_state) store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
+    if constexpr (MODE == kEnds) {
+        if (!transition) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], p.ends + (id * H + head) * VK, v0 + 16 * ct, V, K, lane);
+            return;
+        }
+        // columns n of the map, turned into operands with n along K
+        constexpr int LM = KP + 4;
+        float *const sM = reinterpret_cast<float *>(smem);
+        __syncthreads();
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < KT; ++q)
+                *reinterpret_cast<f32x4 *>(&sM[(16 * (w * CT + ct) + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[ct][q];
+        __syncthreads();
+        char *const out = p.maps + (id * H + head) * kMapBytes<KP>;
+        const int n0 = (tile - nvt) * kWide, nk = KP - n0 < kWide ? (KP - n0) / 32 : kWide / 32;
+        for (int f = w; f < nk * KT; f += kWaves) {
+            const int kk = f / KT, kt = f % KT, k = row_index(kt, c);
+            f32x4 x, y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = sM[(32 * kk + 8 * g + i) * LM + k];
+                y[i] = sM[(32 * kk + 8 * g + 4 + i) * LM + k];
+            }
+            put_op(out + ((n0 / 32 + kk) * KT + kt) * kOp2Bytes, lane, computed<T>(x, y));
+        }
+    } else if constexpr (!ONE) {
+        if (last && a.last_state) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.last_state + (seq * H + head) * VK, v0 + 16 * ct, V, K, lane);
+        }
+    }
 }
 
-template <typename T, int KP, bool OUT> constexpr size_t seq_lds() {
-    return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + kTriBytes + 3 * kC * 4 + Values<T>::kBytes + (OUT ? kTriBytes + Rows<T, KP>::kBytes : 0);
+template <typename T, int KP, Mode MODE, int CT> constexpr size_t seq_lds() {
+    constexpr size_t n = Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + kTriBytes + 3 * kC * 4 + Values<T, CT>::kBytes +
+                         (MODE == kOut ? kTriBytes + Rows<T, KP>::kBytes : 0), m = MODE == kEnds ? 64 * CT * (KP + 4) * 4 : 0;
+    return n > m ? n : m;
+}
+
+// What the segments leave, one after the other: from the state that the one before
+// leaves, through the transition, plus what it leaves from zero.  A wave per
+// (sequence, head, 16 value channels).
+template <typename T, int KP> __global__ __launch_bounds__(64) void delta_carry_kernel(SeqParams p) {
+    constexpr int KT = KP / 16, KK = KP / 32;
+    const DeltaArgs &a = p.a;
+    const int lane = threadIdx.x, K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
+    const int64_t H = a.s.heads;
+    const int nt = (V + 15) / 16, v0 = blockIdx.x % nt * 16;
+    const int64_t rest = blockIdx.x / nt, head = rest % H, seq = rest / H;
+    const Span sp = span_of(a.s, seq);
+    const int nc = (sp.len + kC - 1) / kC, ns = (nc + p.cps - 1) / p.cps;
+    const int64_t first = a.s.starts ? sp.slot0 / p.cps + seq : seq * (ns > 0 ? ns : 1);
+    const size_t VK = static_cast<size_t>(V) * K;
+    if (ns < 3) return;
+    f32x4 S[KT];
+    load_state<KP>(S, p.ends + (first * H + head) * VK, v0, V, K, lane);
+    for (int s = 1; s < ns - 1; ++s) {
+        const int64_t at = (first + s) * H + head;
+        const char *const m = p.maps + at * kMapBytes<KP>;
+        Op2<T> so[KK];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(S[2 * kk], S[2 * kk + 1]);
+        load_state<KP>(S, p.ends + at * VK, v0, V, K, lane);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) S[kt] = mma(get_op2(m + (kk * KT + kt) * kOp2Bytes, lane, T()), so[kk], S[kt]);
+        store_state<KP>(S, p.ends + at * VK, v0, V, K, lane);
+    }
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -345,12 +545,71 @@ template <typename T, int KP, bool BWD> hipError_t launch_prep(const DeltaArgs &
                        0, s, a, ws);
     return hipGetLastError();
 }
-template <typename T, int KP, bool OUT, bool ONE> hipError_t launch_seq(const SeqParams &p, hipStream_t s) {
-    const int64_t nvt = (p.a.s.dv + 63) / 64;
-    const int64_t grid = nvt * p.a.s.heads * (ONE ? p.a.s.slots : p.a.s.nseq);
-    constexpr size_t lds = seq_lds<T, KP, OUT>();
-    hipLaunchKernelGGL((delta_seq_kernel<T, KP, OUT, ONE>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
+template <typename T, int KP, Mode MODE, int CT> hipError_t launch_seq(const SeqParams &p, hipStream_t s) {
+    constexpr int wide = 64 * CT;
+    const int64_t nvt = (p.a.s.dv + wide - 1) / wide;
+    const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * (MODE == kOne ? p.a.s.slots : p.segments);
+    constexpr size_t lds = seq_lds<T, KP, MODE, CT>();
+    hipLaunchKernelGGL((delta_seq_kernel<T, KP, MODE, CT>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
     return hipGetLastError();
+}
+template <typename T, int KP> hipError_t launch_carry(const SeqParams &p, hipStream_t s) {
+    const int64_t grid = (p.a.s.dv + 15) / 16 * p.a.s.heads * p.a.s.nseq;
+    hipLaunchKernelGGL((delta_carry_kernel<T, KP>), dim3(static_cast<unsigned>(grid)), dim3(64), 0, s, p);
+    return hipGetLastError();
+}
+
+// ----------------------------------------------------------------- time segments
+// The chunks of a segment (INT32_MAX: sequences are not cut), the segments' slots, and
+// whether bf16's workgroups hold 128 value channels (eight waves) instead of 64.
+struct Plan {
+    int cps;
+    int64_t segments;
+    bool wide, wide_ends;
+};
+// The cheapest of some ways to cut, by what a chunk takes a workgroup alone on its CU
+// (us, at 128 and at 64 key channels): 64 value channels 2.75 and 1.95, 128 of them 5
+// and 3.2; without the output 1.8 and 1.3, 4 and 2.5; fp32 11.5 and 5.4, 7.5 and
+// 3.6; a step of the join 7.5 and 1.  Packed sequences count as equally long.
+// Measured, us a call, bf16: 2 x 8192 steps of 40 heads of 128 x 128, 64 channels to a
+// workgroup, 1 / 2 / 3 segments 511 / 629 / 626, 128 channels 588 / 574 / 495 to 590 (the clock
+// gives way when every CU is at work for long); 65536 steps of 8 heads of 64 x 64,
+// 1 / 8 / 16 / 32 / 64 segments 2002 / 565 / 367 / 334 / 369.  Under 16 chunks a sequence
+// stays whole: two launches more cost what is won.
+inline Plan plan_of(const DeltaShape &s, int bf16) {
+    const bool big = s.dk > 64;
+    const double c4 = bf16 ? (big ? 2.75 : 1.95) : (big ? 11.5 : 5.4), c8 = big ? 5.0 : 3.2;
+    const double e4 = bf16 ? (big ? 1.8 : 1.3) : (big ? 7.5 : 3.6), e8 = big ? 4.0 : 2.5, step = big ? 7.5 : 1.0;
+    const int64_t nc = s.nseq > 0 ? (s.slots + s.nseq - 1) / s.nseq : 0, units = s.heads * s.nseq;
+    const int64_t t4 = (s.dv + 63) / 64, t8 = (s.dv + 127) / 128, k4 = big ? 2 : 1, k8 = 1;
+    const bool may = bf16 && s.dv > 64;
+    auto rounds = [](int64_t n) { return static_cast<double>((n + 255) / 256); };
+    Plan best{0x7fffffff, s.nseq, false, false};
+    double least = -1.0;
+    for (int64_t n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
+        if (n > 1 && (nc < 16 || nc < 4 * n)) break;
+        const int64_t cps = (nc + n - 1) / n;
+        const double out4 = rounds(t4 * units * n) * c4, out8 = rounds(t8 * units * n) * c8;
+        const double ends4 = rounds(units * (t4 * (n - 1) + k4 * (n - 2))) * e4, ends8 = rounds(units * (t8 * (n - 1) + k8 * (n - 2))) * e8;
+        Plan p{0x7fffffff, s.nseq, may && out8 < out4, may && ends8 < ends4};
+        double cost = cps * (p.wide ? out8 : out4);
+        if (n > 1) {
+            cost += cps * (p.wide_ends ? ends8 : ends4) + (n - 2) * step + 15.0;
+            p.cps = static_cast<int>(cps);
+            p.segments = s.packed ? s.slots / cps + s.nseq : s.nseq * ((nc + cps - 1) / cps);
+        }
+        if (least < 0.0 || cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
+}
+inline size_t ends_bytes(const DeltaShape &s, const Plan &p) {
+    return p.segments == s.nseq ? 0 : align256(static_cast<size_t>(p.segments * s.heads * s.dv * s.dk) * 4);
+}
+inline size_t maps_bytes(const DeltaShape &s, const Plan &p) {
+    return p.segments == s.nseq ? 0 : align256(static_cast<size_t>(p.segments * s.heads) * (s.dk > 64 ? kMapBytes<128> : kMapBytes<64>));
 }
 
 }  // namespace

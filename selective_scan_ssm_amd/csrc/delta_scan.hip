@@ -1,33 +1,44 @@
 // The gated delta rule: whole sequences (chunks of 64 steps on the matrix cores)
 // and one decode token.  Per value head, with its state S (V x K, fp32):
 //     S <- exp(g_t) S,  r = v_t - S k_t,  S <- S + beta_t r k_t^T,  y_t = scale S q_t
-#include "delta_chunk.h"
+#include "delta_flow.h"
 
 namespace ssm {
 namespace delta {
 namespace {
 
 struct FwdWs {
-    size_t t, p, scal, total;
+    size_t t, p, scal, ends, maps, total;
 };
-FwdWs fwd_ws(const DeltaShape &s) {
+FwdWs fwd_ws(const DeltaShape &s, const Plan &plan) {
     const size_t units = static_cast<size_t>(s.slots * s.heads);
     FwdWs w{};
     w.p = w.t + align256(units * kTriBytes);
     w.scal = w.p + align256(units * kTriBytes);
-    w.total = w.scal + align256(units * 3 * kC * 4);
+    w.ends = w.scal + align256(units * 3 * kC * 4);
+    w.maps = w.ends + ends_bytes(s, plan);
+    w.total = w.maps + maps_bytes(s, plan);
     return w;
 }
 
 template <typename T, int KP> hipError_t run(const DeltaArgs &a, hipStream_t s) {
-    const FwdWs w = fwd_ws(a.s);
+    const Plan plan = plan_of(a.s, a.bf16);
+    const FwdWs w = fwd_ws(a.s, plan);
     char *const base = static_cast<char *>(a.workspace);
     SeqParams p{};
     p.a = a;
     p.ws = {base + w.t, base + w.p, nullptr, reinterpret_cast<float *>(base + w.scal)};
-    if (a.s.slots > 0)
+    p.cps = plan.cps;
+    p.wide = plan.wide;
+    p.wide_ends = plan.wide_ends;
+    p.segments = plan.segments;
+    p.ends = reinterpret_cast<float *>(base + w.ends);
+    p.maps = base + w.maps;
+    if (a.s.slots > 0) {
         if (hipError_t e = launch_prep<T, KP, false>(a, p.ws, s)) return e;
-    return launch_seq<T, KP, true, false>(p, s);
+        if (hipError_t e = launch_segments<T, KP>(p, s)) return e;
+    }
+    return launch_walk<T, KP, kOut>(p, s);
 }
 
 // ------------------------------------------------------------------- one token
@@ -104,7 +115,7 @@ template <typename T> hipError_t update(const DeltaStepArgs &a, hipStream_t s) {
 }  // namespace
 }  // namespace delta
 
-size_t delta_scan_workspace(const DeltaShape &s) { return s.slots * s.heads > 0 ? delta::fwd_ws(s).total : 0; }
+size_t delta_scan_workspace(const DeltaShape &s, int bf16) { return s.slots * s.heads > 0 ? delta::fwd_ws(s, delta::plan_of(s, bf16)).total : 0; }
 
 hipError_t launch_delta_scan(const DeltaArgs &a, hipStream_t s) {
     using namespace delta;

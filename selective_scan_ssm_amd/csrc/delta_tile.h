@@ -250,6 +250,41 @@ __device__ __forceinline__ int64_t sequence_of(const DeltaShape &s, int64_t slot
     return lo;
 }
 
+// Time segments: a sequence's chunks cut into runs of cps.  Segment s of sequence i
+// is slot (first chunk's slot) / cps + i + s, which again leaves every sequence room.
+struct Segment {
+    int64_t seq;
+    int s, j0, j1;                                     // of the sequence; its chunks
+    bool used, last;
+};
+__device__ __forceinline__ Segment segment_of(const DeltaShape &sh, int64_t id, int cps, Span &sp) {
+    Segment g;
+    int64_t first;
+    if (!sh.starts) {
+        const int64_t nc = (sh.seqlen + kC - 1) / kC, ns = nc > cps ? (nc + cps - 1) / cps : 1;
+        g.seq = id / ns;
+        first = g.seq * ns;
+    } else {
+        int64_t lo = 0, hi = sh.nseq - 1;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            if (((clamp_start(sh, mid) >> 6) + mid) / cps + mid <= id) lo = mid;
+            else hi = mid - 1;
+        }
+        g.seq = lo;
+        first = ((clamp_start(sh, lo) >> 6) + lo) / cps + lo;
+    }
+    sp = span_of(sh, g.seq);
+    const int nc = (sp.len + kC - 1) / kC;
+    const int64_t s = id - first;
+    g.used = s == 0 || (s > 0 && s * cps < nc);
+    g.s = static_cast<int>(s);
+    g.j0 = g.used ? g.s * cps : 0;
+    g.j1 = g.j0 + cps < nc ? g.j0 + cps : nc;
+    g.last = g.j1 == nc;
+    return g;
+}
+
 __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -345,39 +380,38 @@ template <int KP> __device__ __forceinline__ Op<bf16_t> get_col(const char *rows
 template <int KP> __device__ __forceinline__ Op<float> get_col(const char *, const char *cols, int kt, int kk, int lane, float) {
     return get_op(cols + (kt * 2 + kk) * kOpBytes<float>, lane, 0.0f);
 }
-// A chunk's steps of the workgroup's 64 value channels; a wave gets its 16 of them as
+// A chunk's steps of the workgroup's 64 CT value channels; a wave gets 16 of them as
 // the columns of accumulator tiles, or as an operand with steps along K.  bf16 goes
-// through LDS (two 16-byte loads a thread instead of sixteen 2-byte ones) and is
-// read transposed, fp32 straight to the lanes.  w: the wave; V: channels from the
-// workgroup's first on.
-template <typename T> struct Values;
-template <> struct Values<bf16_t> {
-    static constexpr int kBytes = 8 * kRowBytes<bf16_t>;
-    Op<bf16_t> v[2];
+// through LDS (16-byte loads instead of 2-byte ones) and is read transposed, fp32
+// straight to the lanes (CT = 1).  V: channels from the workgroup's first on.
+template <typename T, int CT> struct Values;
+template <int CT> struct Values<bf16_t, CT> {
+    static constexpr int N = 2 * CT, kBytes = 4 * N * kRowBytes<bf16_t>;
+    Op<bf16_t> v[N];
     static __device__ __forceinline__ uint32_t offset(int ld, int V, int, int) {
-        const int lane = threadIdx.x % 64, f = threadIdx.x / 64, t = row_index(f / 2, lane % 16), c = 32 * (f % 2) + 8 * (lane / 16);
+        const int lane = threadIdx.x % 64, f = threadIdx.x / 64, t = row_index(f / N, lane % 16), c = 32 * (f % N) + 8 * (lane / 16);
         return c < V ? static_cast<uint32_t>((t * ld + c) * 2) : kOffNone;
     }
     __device__ __forceinline__ void load(rsrc_t r, int ld, uint32_t off) {
-        v[0] = load_op(r, off, bf16_t());
-        v[1] = load_op(r, off + static_cast<uint32_t>(32 * ld * 2), bf16_t());
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = load_op(r, off + static_cast<uint32_t>(row_index(i * 4 / N, 0) * ld * 2), bf16_t());
     }
     __device__ __forceinline__ void put(char *dst) const {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) put_row(dst + (4 * i + threadIdx.x / 64) * kRowBytes<bf16_t>, threadIdx.x % 64, v[i]);
+        for (int i = 0; i < N; ++i) put_row(dst + (4 * i + threadIdx.x / 64) * kRowBytes<bf16_t>, threadIdx.x % 64, v[i]);
     }
-    // steps 32 p ..
-    __device__ __forceinline__ Op<bf16_t> op(const char *src, int p, int w, int lane) const {
+    // steps 32 p .. of column tile ct
+    __device__ __forceinline__ Op<bf16_t> op(const char *src, int p, int ct, int lane) const {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         using lds = __attribute__((address_space(3))) s16x4 *;
         const int l = lane % 16, piece = l % 4;
-        const char *const q = src + (4 * p + w / 2) * kRowBytes<bf16_t> + (2 * (w % 2) + piece / 2) * 320 + (4 * (lane / 16) + l / 4) * 16 + piece % 2 * 8;
+        const char *const q = src + (2 * p * N + ct / 2) * kRowBytes<bf16_t> + (2 * (ct % 2) + piece / 2) * 320 + (4 * (lane / 16) + l / 4) * 16 + piece % 2 * 8;
         const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q))));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q + 2 * kRowBytes<bf16_t>))));
+        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q + N * kRowBytes<bf16_t>))));
         return {u32x4{a[0], a[1], b[0], b[1]}};
     }
 };
-template <> struct Values<float> {
+template <> struct Values<float, 1> {
     static constexpr int kBytes = 0;
     float v[16];
     static __device__ __forceinline__ uint32_t offset(int ld, int V, int w, int lane) {

@@ -59,6 +59,7 @@ int check_delta(ssm::DeltaShape &s, int64_t batch, int64_t seqlen, bool packed, 
                 int64_t dk, int64_t dv, int io) {
     if (int r = check_heads(kheads, heads, dk, dv, io)) return r;
     if (batch < 0 || seqlen < 0 || seqlen > kMaxSpan || (packed && (batch != 1 || nseq < 0))) return SSM_ERR_SHAPE;
+    s.packed = packed ? 1 : 0;
     s.nseq = packed ? nseq : batch;
     s.seqlen = seqlen;
     s.kheads = kheads; s.heads = heads; s.dk = dk; s.dv = dv;
@@ -139,7 +140,7 @@ size_t ssm_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int packed,
                                       int64_t dstate, int64_t headdim, int io_dtype) {
     ssm::DeltaShape s{};
     if (check_delta(s, batch, seqlen, packed != 0, nseq, nkheads, nheads, dstate, headdim, io_dtype)) return kBad;
-    return ssm::delta_scan_workspace(s);
+    return ssm::delta_scan_workspace(s, io_dtype == SSM_BF16);
 }
 
 int ssm_delta_scan_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, const float *g,
@@ -158,7 +159,7 @@ int ssm_delta_scan_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk, c
     if (in.rows > 0 && !y) return SSM_ERR_NULL;
     const void *wide[] = {y, last_state};
     if (!all_aligned(wide, 16)) return SSM_ERR_ALIGN;
-    const size_t need = ssm::delta_scan_workspace(a.s);
+    const size_t need = ssm::delta_scan_workspace(a.s, a.bf16);
     const Range ins[] = {in.q, in.k, in.v, in.g, in.beta, in.h0, in.starts};
     const Range outs[] = {range(y, in.rows * nheads * headdim, in.es), range(last_state, in.ends, 4),
                           range(ckpt, a.s.slots * nheads * dstate * headdim, 4),
@@ -173,7 +174,7 @@ size_t ssm_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int pac
                                           int64_t dstate, int64_t headdim, int saved, int io_dtype) {
     ssm::DeltaShape s{};
     if (check_delta(s, batch, seqlen, packed != 0, nseq, nkheads, nheads, dstate, headdim, io_dtype)) return kBad;
-    return ssm::delta_scan_bwd_workspace(s, saved != 0);
+    return ssm::delta_scan_bwd_workspace(s, io_dtype == SSM_BF16, saved != 0);
 }
 
 int ssm_delta_scan_bwd(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, const float *g,
@@ -195,7 +196,7 @@ int ssm_delta_scan_bwd(const void *q, int64_t ldq, const void *k, int64_t ldk, c
     const void *wide[] = {dout, dlast, dq, dk, dv, dh0};
     const void *words[] = {dg, dbeta};
     if (!all_aligned(wide, 16) || !all_aligned(words, 4)) return SSM_ERR_ALIGN;
-    const size_t need = ssm::delta_scan_bwd_workspace(a.s, ckpt != nullptr);
+    const size_t need = ssm::delta_scan_bwd_workspace(a.s, a.bf16, ckpt != nullptr);
     const int64_t nk = in.rows * nkheads * dstate, nv = in.rows * nheads * headdim, nh = in.rows * nheads;
     const Range ins[] = {in.q, in.k, in.v, in.g, in.beta, in.h0, in.starts, range(dout, nv, in.es), range(dlast, in.ends, 4),
                          range(ckpt, a.s.slots * nheads * dstate * headdim, 4)};

@@ -260,7 +260,8 @@ hipError_t launch_grad_clip(const ClipArgs &a, hipStream_t s);
 constexpr int kDeltaChunk = 64;           // steps between two checkpoints
 constexpr int kDeltaMaxState = 128;       // channels of a key
 struct DeltaShape {
-    const int32_t *starts;                // packed: nseq + 1 first rows, else null
+    int packed;
+    const int32_t *starts;                // packed: nseq + 1 first rows, else null (sizes alone: null too)
     int64_t nseq, seqlen;                 // sequences, steps of each (packed: rows in all)
     int64_t kheads, heads, dk, dv;
     int64_t slots;                        // chunks in all (packed: an upper bound)
@@ -292,8 +293,8 @@ struct DeltaStepArgs {
     float scale;
     int bf16;
 };
-size_t delta_scan_workspace(const DeltaShape &s);
-size_t delta_scan_bwd_workspace(const DeltaShape &s, bool saved);
+size_t delta_scan_workspace(const DeltaShape &s, int bf16);
+size_t delta_scan_bwd_workspace(const DeltaShape &s, int bf16, bool saved);
 hipError_t launch_delta_scan(const DeltaArgs &a, hipStream_t s);
 hipError_t launch_delta_scan_bwd(const DeltaBwdArgs &a, hipStream_t s);
 hipError_t launch_delta_update(const DeltaStepArgs &a, hipStream_t s);
