@@ -32,9 +32,10 @@ template <int KP> constexpr int64_t kMapBytes = static_cast<int64_t>(KP / 32) * 
 // ---------------------------------------------------------------- preparation
 // A wave per (chunk, head).  With Gam_ts = exp(G_t - G_s) (s <= t):
 //     N = stril(K K^T o Gam) diag(beta),  T = (I + N)^-1,  P = tril(Q K^T o Gam)
-// T is found column by column, one column per lane, by forward substitution: the
-// rows of N are the same for all lanes (LDS broadcasts), T never leaves the
-// registers until it is done.
+// T's 16 x 16 diagonal blocks come from forward substitution, one column to a lane, the
+// others from them in fp32 products on the matrix cores: stable whatever the keys,
+// unlike powers of N.  One column of all 64 steps to a lane instead, with 2016
+// multiplications and 504 LDS broadcasts: 10240 chunks of 64 x 128 145 us.
 template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a, ChunkWs ws) {
     using D = Decay<T>;
     using real = typename D::real;
@@ -96,23 +97,59 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
             *reinterpret_cast<f32x4 *>(&sN[w][t][s0]) = acc;
         }
     wave_sync();
-    // column `lane` of T: x_t = [t == lane] - sum_{s < t} N_ts x_s
-    float x[kC];
+    // the diagonal blocks' inverses D, one block to 16 lanes, one column to a lane:
+    // x_t = [t == c] - sum_{s < t} N_ts x_s; each takes its block's place in sN
+    {
+        float x[16];
 #pragma unroll
-    for (int t = 0; t < kC; ++t) {
-        float v = t == lane ? 1.0f : 0.0f;
+        for (int t = 0; t < 16; ++t) {
+            float v = t == c ? 1.0f : 0.0f;
 #pragma unroll
-        for (int s = 0; s < t; s += 4) {
-            const f32x4 nrow = *reinterpret_cast<const f32x4 *>(&sN[w][t][s]);
+            for (int s = 0; s < t; s += 4) {
+                const f32x4 nrow = *reinterpret_cast<const f32x4 *>(&sN[w][16 * g + t][16 * g + s]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (s + i < t) v = fmaf(-nrow[i], x[s + i], v);
+                for (int i = 0; i < 4; ++i)
+                    if (s + i < t) v = fmaf(-nrow[i], x[s + i], v);
+            }
+            x[t] = v;
         }
-        x[t] = v;
+        wave_sync();
+#pragma unroll
+        for (int t = 0; t < 16; ++t) sN[w][16 * g + t][16 * g + c] = x[t];
     }
     wave_sync();
+    // T_ij = -D_i sum_{j <= m < i} N_im T_mj, in fp32 products of 16 x 16 blocks: the right factor is always an
+    // accumulator tile (rows 4 g + i, column c), taken along K in that order; the left one is four floats of a row
+    {
+        auto left = [&](int i, int m) { return *reinterpret_cast<const f32x4 *>(&sN[w][16 * i + c][16 * m + 4 * g]); };
+        auto product = [](f32x4 l, f32x4 r, f32x4 acc) {
 #pragma unroll
-    for (int t = 0; t < kC; ++t) sN[w][t][lane] = x[t];
+            for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(l[i], r[i], acc, 0, 0, 0);
+            return acc;
+        };
+        f32x4 t[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) t[i][i][h] = sN[w][16 * i + 4 * g + h][16 * i + c];
+#pragma unroll
+        for (int d = 1; d < 4; ++d)
+#pragma unroll
+            for (int j = 0; j + d < 4; ++j) {
+                const int i = j + d;
+                f32x4 z = zero;
+#pragma unroll
+                for (int m = j; m < i; ++m) z = product(left(i, m), t[m][j], z);
+                t[i][j] = product(-left(i, i), z, zero);
+            }
+        wave_sync();
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < i; ++j)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) sN[w][16 * i + 4 * g + h][16 * j + c] = t[i][j][h];
+    }
     wave_sync();
     char *const to = ws.t + unit * kTriBytes;
 #pragma unroll
