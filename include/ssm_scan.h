@@ -633,8 +633,8 @@ size_t ssm_grad_norm_workspace_bytes(int64_t count);
  *          is.  Keys of length at most 1 and beta in [0, 2] keep it bounded.
  *   h0, last_state : (sequences, nheads, headdim, dstate) fp32, optional
  *   y    : (batch, seqlen, nheads, headdim) io dtype, contiguous
- *   ckpt : optional output, fp32, ssm_delta_ckpt_bytes: the states entering the
- *          chunks, for ssm_delta_scan_bwd
+ *   ckpt : optional output, fp32, ssm_delta_ckpt_bytes: per chunk the state that
+ *          enters it and the r of its steps, for ssm_delta_scan_bwd
  *   starts : NULL: `batch` sequences of `seqlen` steps (nseq is not used).
  *          Otherwise nseq + 1 int32 on the device, ascending, in [0, seqlen], and
  *          batch == 1: sequence i is the rows starts[i] .. starts[i + 1] - 1 (none
@@ -667,9 +667,10 @@ size_t ssm_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int packed,
                                       int64_t nkheads, int64_t nheads, int64_t dstate, int64_t headdim,
                                       int io_dtype);
 
-/* Bytes of the states entering the chunks: slots x nheads x headdim x dstate fp32
- * with batch * ceil(seqlen / 64) slots, or seqlen / 64 + nseq packed, where chunk j
- * of sequence i is slot starts[i] / 64 + i + j (quotients rounded down; a few slots
+/* Bytes of ckpt: slots x nheads x headdim x (dstate + 64) fp32, per slot and head the
+ * state (headdim, dstate), then r (64, headdim; rows past the sequence's end are 0).
+ * batch * ceil(seqlen / 64) slots, or seqlen / 64 + nseq packed, where chunk j of
+ * sequence i is slot starts[i] / 64 + i + j (quotients rounded down; a few slots
  * stay unused).  (size_t)-1 for invalid arguments. */
 size_t ssm_delta_ckpt_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nseq, int64_t nheads,
                             int64_t dstate, int64_t headdim);

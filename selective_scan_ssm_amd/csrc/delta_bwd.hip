@@ -2,19 +2,20 @@
 // chunk leaves, per chunk (all of delta_chunk.h's names; F, E lower triangular):
 //     dU = scale P^T dY + exp(G_end - G) K dS',   dX = T^T (beta dU) = dV
 //     dS = exp(G_end) dS' + scale Q^T (exp(G) dY) - K^T (exp(G) dX)
-//     F = scale (dY U^T) o Gam,   E = (dX R^T) o Gam below the diagonal,   M = -E diag(beta)
-//     dQ = scale exp(G) dY S^T + F K
-//     dK = dKe + dKw,  dKe = M K - exp(G) dX S^T,  dKw = F^T Q + M^T K + exp(G_end - G) U dS'^T
-//     dbeta_t = R_t . dU_t - k_t . (E^T K)_t
-//     dg_t = sum over t' >= t of (q . dq + k . dke - k . dkw)_t'  + <S', dS'>
+//     F = scale (dY R^T) o Gam,   E = (dX R^T) o Gam below the diagonal,   M = -E diag(beta)
+//     dQ = scale exp(G) dY S^T + F diag(beta) K
+//     dK = dKe + beta Z,  dKe = M K - exp(G) dX S^T,  Z = F^T Q - E^T K + exp(G_end - G) R dS'^T
+//     dbeta_t = k_t . Z_t
+//     dg_t = sum over t' >= t of (q . dq + k . dke - beta k . z)_t'  + <S', dS'>
 // dg's form: G_t enters every product as exp(G_t) beside q_t and the key that is
 // read with, and as exp(-G_t) beside the key that is written with, so the
 // derivative by G_t is the product with what stands beside it.  <S', dS'> =
-// exp(G_end) <S, dS'> + sum_t k_t . (exp(G_end - G) U dS'^T)_t.
+// exp(G_end) <S, dS'> + sum_t beta k_t . (exp(G_end - G) R dS'^T)_t.  Z is the gradient by
+// the key that is written with, before beta; dbeta needs neither dU nor a division.
 //
-// Launches: the chunks' preparation; the states entering the chunks and R (one
-// walk over the chunks, or, from saved states, all chunks at once); dS' and dX, in
-// reverse; the rest, all chunks at once.
+// Launches: the chunks' preparation; without saved ones, the states entering the
+// chunks and R, in a walk over the chunks; dS' and dX, in reverse; the rest, all
+// chunks at once.
 #include "delta_flow.h"
 
 namespace ssm {
@@ -24,9 +25,7 @@ namespace {
 struct BwdParams {
     DeltaBwdArgs b;
     ChunkWs ws;
-    const float *R;                // per (slot, head): (64, V)
-    float *dX, *dS;                // (64, V), (V, K)
-    float *dot;                    // (ceil(V / 16), 64): R . dU by 16 channels
+    float *dX, *dS;                // per (slot, head): (64, V), (V, K)
 };
 
 // What get_col reads of a chunk that is used with steps along K only.
@@ -36,11 +35,11 @@ template <int KP> struct QSide<bf16_t, KP> : Rows<bf16_t, KP> {
 };
 
 // --------------------------------------------------------- dS and dX, in reverse
-template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 2 : 1))) void delta_rev_kernel(BwdParams p) {
+template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(BwdParams p) {
+    using T = float;
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    // bf16 keeps rows of keys and queries and reads them transposed as well; fp32 also keeps the keys' columns, and of
-    // the queries the columns alone
+    // rows and columns of the keys, columns of the queries
     char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sQ = sC + Cols<T, KP>::kBytes,
          *const sT = sQ + QSide<T, KP>::kBytes, *const sP = sT + kTriBytes;
     char *const sY = sP + kTriBytes;
@@ -77,7 +76,6 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
     const auto oqc = QSide<T, KP>::offsets(a.ldq, K);
     const int ldy = static_cast<int>(H * V);
     const uint32_t oy = Values<T, 1>::offset(ldy, V - vt * 64, w, lane);
-    const uint32_t oR = v0 + c < V ? static_cast<uint32_t>((8 * g * V + v0 + c) * 4) : kOffNone;
     auto prefetch = [&](int j) {
         const int jj = j >= 0 ? j : 0;
         const int64_t row0 = sp.row0 + static_cast<int64_t>(jj) * kC, unit = (sp.slot0 + jj) * H + head;
@@ -106,11 +104,6 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
         nY.put(sY);
         const Values<T, 1> cY = nY;
         __syncthreads();
-        const rsrc_t rR = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
-        f32x4 R[4];                                        // needed late in the chunk
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            R[i / 4][i % 4] = Io<float>::f32(Io<float>::load(rR, oR + static_cast<uint32_t>((32 * (i / 8) + i % 8) * V * 4), 0));
         store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
         prefetch(j - 1);
         const Op<T> yo[2] = {cY.op(sY, 0, w, lane), cY.op(sY, 1, w, lane)};
@@ -118,7 +111,6 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(dS[2 * kk], dS[2 * kk + 1]);
         f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero};
-        float *const dot = p.dot + (unit * ((V + 15) / 16) + v0 / 16) * kC;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -131,11 +123,6 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
         for (int tb = 0; tb < 4; ++tb) {
             const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
             dU[tb] = dU[tb] * *reinterpret_cast<const f32x4 *>(&sS[kC + t]) + pd[tb] * a.scale;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float d = wave_fold<16>(R[tb][i] * dU[tb][i], AddOp());
-                if (c == 0 && v0 < V) dot[t + i] = d;
-            }
             dU[tb] = dU[tb] * *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]);
         }
         const Op2<T> uo[2] = {computed<T>(dU[0], dU[1]), computed<T>(dU[2], dU[3])};
@@ -179,8 +166,192 @@ template <typename T, int KP> __global__ __launch_bounds__(kThreads) __attribute
     if (p.b.dh0) store_state<KP>(dS, p.b.dh0 + (seq * H + head) * VK, v0, V, K, lane);
 }
 
-template <typename T, int KP> constexpr size_t rev_lds() {
+template <int KP> constexpr size_t rev_lds() {
+    using T = float;
     return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + QSide<T, KP>::kBytes + 2 * kTriBytes + 3 * kC * 4 + Values<T, 1>::kBytes;
+}
+
+// The same in bf16 io, as in delta_flow.h: a fifth (ninth) wave loads.  The buffer's
+// parts hold T^T, P^T and the columns of dY where the forward has T, P and V.
+template <int KP, int NW>
+__global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 3 : 2, NW == 8 ? 3 : 2))) void delta_rev_flow_kernel(BwdParams p) {
+    using T = bf16_t;
+    using B = FlowBuf<KP, 1, NW>;
+    constexpr int KT = KP / 16, KK = KP / 32, kWide = 16 * NW;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const DeltaArgs &a = p.b.fwd;
+    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int g = lane / 16, c = lane % 16;
+    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
+    const int64_t H = a.s.heads, per_tile = H * a.s.nseq;
+    const int vt = static_cast<int>(blockIdx.x / per_tile);
+    const int64_t rest = blockIdx.x % per_tile, head = rest % H, kh = head / (H / a.s.kheads), seq = rest / H;
+    const Span sp = span_of(a.s, seq);
+    const int nch = (sp.len + kC - 1) / kC;
+    const int64_t lastrow = sp.row0 + static_cast<int64_t>(nch - 1) * kC, lastunit = (sp.slot0 + nch - 1) * H + head;
+    const int ldy = static_cast<int>(H) * V;
+
+    if (w == NW) {                                         // the loading wave
+        const FlowLoader<KP, 1, NW> ld(a.ldk, a.ldq, ldy, K, V - vt * kWide);
+        const T *pk = static_cast<const T *>(a.k) + lastrow * a.ldk + kh * K, *pq = static_cast<const T *>(a.q) + lastrow * a.ldq + kh * K;
+        const T *pv = static_cast<const T *>(p.b.dout) + (lastrow * H + head) * V + vt * kWide;
+        const char *pt = p.ws.tt + lastunit * kTriBytes, *pp = p.ws.p + lastunit * kTriBytes;
+        const float *ps = p.ws.scal + lastunit * 3 * kC;
+        for (int j = 0; j < nch; ++j) {
+            char *const buf = smem + j % 2 * B::bytes;
+            const int n = j == 0 ? sp.len - (nch - 1) * kC : kC;
+            ld.template rows<KK>(buf, chunk_rsrc(pk, n, a.ldk, K, 2), ld.k, ld.ldk);
+            ld.template rows<B::kv>(buf + B::v, chunk_rsrc(pv, n, ldy, V - vt * kWide, 2), ld.v, ld.ldv);
+            ld.template copy<kTriBytes>(buf + B::p, pp);
+            ld.scalars(buf + B::s, ps);
+            ld.template copy<kTriBytes>(buf + B::t, pt);
+            ld.template rows<KK>(buf + B::q, chunk_rsrc(pq, n, a.ldq, K, 2), ld.q, ld.ldq);
+            pk -= kC * a.ldk;
+            pq -= kC * a.ldq;
+            pv -= static_cast<int64_t>(kC) * ldy;
+            pt -= H * kTriBytes;
+            pp -= H * kTriBytes;
+            ps -= H * 3 * kC;
+            flow_loaded();
+            flow_barrier();
+        }
+        return;
+    }
+
+    const int v0 = vt * kWide + w * 16;
+    const f32x4 zero = {0, 0, 0, 0};
+    const size_t VK = static_cast<size_t>(V) * K;
+    const int at = flow_at(lane), tat = flow_tr_at(lane);
+    constexpr bool AHEAD = NW == 4;
+    auto fence = [] {
+        if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 dS[KT];
+    if (p.b.dlast) {
+        load_state<KP>(dS, p.b.dlast + (seq * H + head) * VK, v0, V, K, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) dS[i] = zero;
+    }
+    int64_t unit = lastunit;
+    T *pdv = static_cast<T *>(p.b.dv) + (lastrow * H + head) * V;
+    for (int j = 0; j < nch; ++j, unit -= H, pdv -= static_cast<int64_t>(kC) * ldy) {
+        const char *const buf = smem + j % 2 * B::bytes;
+        const float *const sS = reinterpret_cast<const float *>(buf + B::s);
+        const int n = j == 0 ? sp.len - (nch - 1) * kC : kC;
+        flow_barrier();
+        store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
+        Op<T> fk[2][4], yo[2];
+        Op2<T> so[2], fp[AHEAD ? 6 : 1], ft[AHEAD ? 6 : 1];
+        auto read_rows = [&](int kk) {
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) fk[kk % 2][tb] = flow_row(buf + (tb * KK + kk) * 1024, at);
+        };
+        f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero};
+        if constexpr (AHEAD) {
+            read_rows(0);
+#pragma unroll
+            for (int f = 0; f < 6; ++f) fp[f] = get_op2(buf + B::p + f * kOp2Bytes, lane, T());
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) yo[q] = flow_value<B::kv>(buf + B::v, lane, q, w);
+        fence();
+        so[0] = computed<T>(dS[0], dS[1]);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            if constexpr (!AHEAD) read_rows(kk);
+            else if (kk + 1 < KK) read_rows(kk + 1);
+            fence();
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) dU[tb] = mma(fk[kk % 2][tb], so[kk % 2], dU[tb]);
+            if (kk + 1 < KK) so[(kk + 1) % 2] = computed<T>(dS[2 * kk + 2], dS[2 * kk + 3]);
+            fence();
+        }
+#pragma unroll
+        for (int f = 0; f < (AHEAD ? 6 : 0); ++f) ft[f] = get_op2(buf + B::t + f * kOp2Bytes, lane, T());
+        f32x4 eg[4], ew[4], eb[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            const int t = 32 * (tb / 2) + 8 * g + 4 * (tb % 2);
+            eg[tb] = *reinterpret_cast<const f32x4 *>(&sS[t]);
+            ew[tb] = *reinterpret_cast<const f32x4 *>(&sS[kC + t]);
+            eb[tb] = *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]);
+        }
+        const float end = sS[kC - 1];
+        fence();
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 2 * kk + 2; ++tb) {
+                Op2<T> f;
+                if constexpr (AHEAD) f = fp[tri_up(tb, kk)];
+                else f = get_op2(buf + B::p + tri_up(tb, kk) * kOp2Bytes, lane, T());
+                pd[tb] = mma(f, yo[kk], pd[tb]);
+            }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) dU[tb] = (dU[tb] * ew[tb] + pd[tb] * a.scale) * eb[tb];
+        const Op2<T> uo[2] = {computed<T>(dU[0], dU[1]), computed<T>(dU[2], dU[3])};
+        f32x4 dY[4];
+        tiles(yo[0], dY[0], dY[1]);
+        tiles(yo[1], dY[2], dY[3]);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) dY[tb] = dY[tb] * eg[tb] * a.scale;
+        const Op2<T> qo[2] = {computed<T>(dY[0], dY[1]), computed<T>(dY[2], dY[3])};
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) dS[kt] = dS[kt] * end;
+        fence();
+        Op<T> fc[KT];
+        auto read_cols = [&](const char *rows, int kk) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) fc[kt] = flow_col<KP>(rows, tat, kt, kk);
+        };
+        if constexpr (AHEAD) read_cols(buf + B::q, 0);
+        fence();
+        // dX for the state, and transposed for stores of four channels
+        f32x4 dX[4] = {zero, zero, zero, zero}, xt[4] = {zero, zero, zero, zero};
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int tb = 0; tb < 2 * kk + 2; ++tb) {
+                Op2<T> f;
+                if constexpr (AHEAD) f = ft[tri_up(tb, kk)];
+                else f = get_op2(buf + B::t + tri_up(tb, kk) * kOp2Bytes, lane, T());
+                dX[tb] = mma(f, uo[kk], dX[tb]);
+                xt[tb] = mma(uo[kk], f, xt[tb]);
+            }
+        auto add_cols = [&](const char *rows, int kk, const Op2<T> &o) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                if constexpr (!AHEAD) fc[kt] = flow_col<KP>(rows, tat, kt, kk);
+                dS[kt] = mma(fc[kt], o, dS[kt]);
+            }
+        };
+        add_cols(buf + B::q, 0, qo[0]);
+        fence();
+        if constexpr (AHEAD) read_cols(buf + B::q, 1);
+        fence();
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) dX[tb] = dX[tb] * -eg[tb];
+        const Op2<T> xo[2] = {computed<T>(dX[0], dX[1]), computed<T>(dX[2], dX[3])};
+        const rsrc_t rv = chunk_rsrc(pdv, n, ldy, V, 2), rx = make_rsrc(p.dX + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+        const int v = v0 + 4 * g;
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+            const int t = row_index(tb, c);
+            store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * 2) : kOffNone, T());
+            store4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+        }
+        add_cols(buf + B::q, 1, qo[1]);
+        fence();
+        if constexpr (AHEAD) read_cols(buf, 0);
+        fence();
+        add_cols(buf, 0, xo[0]);
+        fence();
+        if constexpr (AHEAD) read_cols(buf, 1);
+        fence();
+        add_cols(buf, 1, xo[1]);
+    }
+    if (p.b.dh0) store_state<KP>(dS, p.b.dh0 + (seq * H + head) * VK, v0, V, K, lane);
 }
 
 // -------------------------------------------------------------------- the rest
@@ -287,6 +458,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     const f32x4 zero = {0, 0, 0, 0};
     const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, sizeof(T));
     const rsrc_t rq = chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, sizeof(T));
+    const size_t VK = static_cast<size_t>(V) * K;
     f32x4 dqs[SHARED ? KT : 1], dks[SHARED ? KT : 1];
     if constexpr (SHARED) {
 #pragma unroll
@@ -294,7 +466,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     }
     for (int hh = 0; hh < group; ++hh) {
         const int64_t head = kh * group + hh, unit = slot * H + head;
-        const float *const scal = p.ws.scal + unit * 3 * kC;
+        const float *const scal = p.ws.scal + unit * 3 * kC, *const saved = a.ckpt + unit * (VK + kC * V);
         __syncthreads();                                     // the head before is done with sG, sB, sDG
         if (w == 0) {
             const real G = lane_prefix<real>(lane < n ? D::scaled(step_log(a.g[(row0 + lane) * H + head])) : real(0), lane);
@@ -313,8 +485,8 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
             const int f = threadIdx.x / 64, tr = row_index(f, c), v = v0 + 8 * g;
             put_op(sY + f * OB, lane, load_op(rd, tr < n && v < V ? static_cast<uint32_t>((tr * H * V + v) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()));
             stage_values<T>(sX, p.dX + unit * kC * V, v0, V);
-            stage_values<T>(sR, p.R + unit * kC * V, v0, V);
-            tot += stage_states<T, KP>(sS, sD, a.ckpt + unit * V * K, p.dS + unit * V * K, v0, V, K);
+            stage_values<T>(sR, saved + VK, v0, V);
+            tot += stage_states<T, KP>(sS, sD, saved, p.dS + unit * VK, v0, V, K);
             __syncthreads();
             const Op<T> y = get_op(sY + w * OB, lane, T());
             const Op2<T> x = get_op2(sX + w * kOp2Bytes, lane, T()), r = get_op2(sR + w * kOp2Bytes, lane, T());
@@ -352,18 +524,18 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
             for (int i = 0; i < 4; ++i) {
                 const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s for FT, ET, t for F, E
                 const float before = o <= t ? D::ex(gt - sG[o]) : 0.0f, behind = o >= t ? D::ex(sG[o] - gt) : 0.0f;
-                FT[ob][i] = o <= t ? FT[ob][i] * (a.scale * before * sB[o]) : 0.0f;
+                FT[ob][i] = o <= t ? FT[ob][i] * (a.scale * before * sB[o]) : 0.0f;    // (F diag(beta))^T
                 ET[ob][i] = o < t ? ET[ob][i] * (-before * sB[o]) : 0.0f;      // M^T
-                F[ob][i] = o >= t ? F[ob][i] * (a.scale * behind * beta) : 0.0f;
-                E[ob][i] = o > t ? E[ob][i] * behind : 0.0f;
+                F[ob][i] = o >= t ? F[ob][i] * (a.scale * behind) : 0.0f;
+                E[ob][i] = o > t ? E[ob][i] * -behind : 0.0f;
             }
-        float qd = 0.0f, kd = 0.0f, kdw = 0.0f, kb = 0.0f, kc = 0.0f;
-        const float fq = a.scale * eg, fw = beta * wt;
+        float qd = 0.0f, kd = 0.0f, kz = 0.0f, kc = 0.0f;
+        const float fq = a.scale * eg;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             dq[kt] = dq[kt] * fq;
             ke[kt] = ke[kt] * -eg;
-            kw[kt] = kw[kt] * fw;
+            kw[kt] = kw[kt] * wt;                            // Z
         }
         __syncthreads();
 #pragma unroll
@@ -377,7 +549,6 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int kt = 2 * kp + h;
-                f32x4 em = zero;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) kc = fmaf(kv[4 * h + i], kw[kt][i], kc);
 #pragma unroll
@@ -389,28 +560,22 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
                     }
                     if (kk >= w / 2) {
                         kw[kt] = mma(qcol, computed<T>(F[2 * kk], F[2 * kk + 1]), kw[kt]);
-                        em = mma(kcol, computed<T>(E[2 * kk], E[2 * kk + 1]), em);
+                        kw[kt] = mma(kcol, computed<T>(E[2 * kk], E[2 * kk + 1]), kw[kt]);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    kw[kt][i] = fmaf(-beta, em[i], kw[kt][i]);
                     qd = fmaf(qv[4 * h + i], dq[kt][i], qd);
                     kd = fmaf(kv[4 * h + i], ke[kt][i], kd);
-                    kdw = fmaf(kv[4 * h + i], kw[kt][i], kdw);
-                    kb = fmaf(kv[4 * h + i], em[i], kb);
+                    kz = fmaf(kv[4 * h + i], kw[kt][i], kz);
                 }
-                ke[kt] = ke[kt] + kw[kt];
+                ke[kt] = ke[kt] + kw[kt] * beta;
             }
         }
-        const float dG = column_total(qd + kd - kdw);
-        kb = column_total(kb);
-        float rd_u = 0.0f;
-        const int nt = (V + 15) / 16;
-        for (int i = g; i < nt; i += 4) rd_u += p.dot[(unit * nt + i) * kC + t];
-        rd_u = column_total(rd_u);
-        if (g == 0 && t < n) p.b.dbeta[(row0 + t) * H + head] = rd_u - kb;
-        tot = wave_fold(fmaf(end, tot, kc), AddOp());
+        const float dG = column_total(fmaf(-beta, kz, qd + kd));
+        kz = column_total(kz);
+        if (g == 0 && t < n) p.b.dbeta[(row0 + t) * H + head] = kz;
+        tot = wave_fold(fmaf(end, tot, beta * kc), AddOp());
         if (lane == 0) sTot[w] = tot;
         if (g == 0) sDG[t] = dG;
         __syncthreads();
@@ -451,23 +616,42 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     }
 }
 
+// bf16: 64 value channels to a workgroup while the CUs hold them all, else 128
+template <int KP, int NW> hipError_t launch_rev_flow(const BwdParams &p, hipStream_t s) {
+    constexpr int wide = 16 * NW;
+    const DeltaShape &sh = p.b.fwd.s;
+    constexpr size_t lds = 2 * FlowBuf<KP, 1, NW>::bytes;
+    hipLaunchKernelGGL((delta_rev_flow_kernel<KP, NW>), dim3(static_cast<unsigned>((sh.dv + wide - 1) / wide * sh.heads * sh.nseq)),
+                       dim3(kFlowThreads<NW>), lds, s, p);
+    return hipGetLastError();
+}
+template <typename T, int KP> hipError_t launch_rev(const BwdParams &p, hipStream_t s) {
+    const DeltaShape &sh = p.b.fwd.s;
+    const int64_t n = (sh.dv + 63) / 64 * sh.heads * sh.nseq;
+    if constexpr (sizeof(T) == 2) {
+        return sh.dv > 64 && n > 256 ? launch_rev_flow<KP, 8>(p, s) : launch_rev_flow<KP, 4>(p, s);
+    } else {
+        constexpr size_t lds = rev_lds<KP>();
+        hipLaunchKernelGGL((delta_rev_kernel<KP>), dim3(static_cast<unsigned>(n)), dim3(kThreads), lds, s, p);
+        return hipGetLastError();
+    }
+}
+
 struct BwdWs {
-    size_t t, tt, p, scal, R, dX, dS, dot, ckpt, ends, maps, total;
+    size_t t, tt, p, scal, dX, dS, ckpt, ends, maps, total;
 };
 BwdWs bwd_ws(const DeltaShape &s, const Plan &plan, bool saved) {
     const size_t units = static_cast<size_t>(s.slots * s.heads), V = s.dv, K = s.dk;
     BwdWs w{};
-    w.tt = w.t + align256(units * kTriBytes);
+    w.tt = w.t + (saved ? 0 : align256(units * kTriBytes));
     w.p = w.tt + align256(units * kTriBytes);
     w.scal = w.p + align256(units * kTriBytes);
-    w.R = w.scal + align256(units * 3 * kC * 4);
-    w.dX = w.R + align256(units * kC * V * 4);
+    w.dX = w.scal + align256(units * 3 * kC * 4);
     w.dS = w.dX + align256(units * kC * V * 4);
-    w.dot = w.dS + align256(units * V * K * 4);
-    w.ckpt = w.dot + align256(units * ((V + 15) / 16) * kC * 4);
-    w.ends = w.ckpt + (saved ? 0 : align256(units * V * K * 4));
-    w.maps = w.ends + ends_bytes(s, plan);
-    w.total = w.maps + maps_bytes(s, plan);
+    w.ckpt = w.dS + align256(units * V * K * 4);
+    w.ends = w.ckpt + (saved ? 0 : align256(units * static_cast<size_t>(delta_ckpt_stride(K, V)) * 4));
+    w.maps = w.ends + (saved ? 0 : ends_bytes(s, plan));
+    w.total = w.maps + (saved ? 0 : maps_bytes(s, plan));
     return w;
 }
 
@@ -479,39 +663,31 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
     BwdParams p{};
     p.b = b;
     p.b.fwd.last_state = nullptr;
-    p.ws = {base + w.t, base + w.p, base + w.tt, reinterpret_cast<float *>(base + w.scal)};
-    float *const R = reinterpret_cast<float *>(base + w.R);
-    p.R = R;
+    p.ws = {b.fwd.ckpt ? nullptr : base + w.t, base + w.p, base + w.tt, reinterpret_cast<float *>(base + w.scal)};
     p.dX = reinterpret_cast<float *>(base + w.dX);
     p.dS = reinterpret_cast<float *>(base + w.dS);
-    p.dot = reinterpret_cast<float *>(base + w.dot);
     if (sh.slots > 0) {
         if (hipError_t e = launch_prep<T, KP, true>(b.fwd, p.ws, s)) return e;
-        SeqParams q{};
-        q.a = b.fwd;
-        q.a.last_state = nullptr;
-        q.ws = p.ws;
-        q.R = R;
-        q.cps = plan.cps;
-        q.wide = plan.wide;
-        q.wide_ends = plan.wide_ends;
-        q.segments = plan.segments;
-        q.ends = reinterpret_cast<float *>(base + w.ends);
-        q.maps = base + w.maps;
-        if (b.fwd.ckpt) {
-            if (hipError_t e = launch_seq<T, KP, kOne, 1>(q, s)) return e;
-        } else {
+        if (!b.fwd.ckpt) {
+            SeqParams q{};
+            q.a = b.fwd;
+            q.a.last_state = nullptr;
+            q.ws = p.ws;
+            q.cps = plan.cps;
+            q.wide = plan.wide;
+            q.wide_ends = plan.wide_ends;
+            q.segments = plan.segments;
+            q.ends = reinterpret_cast<float *>(base + w.ends);
+            q.maps = base + w.maps;
             q.a.ckpt = p.b.fwd.ckpt = reinterpret_cast<float *>(base + w.ckpt);
             if (hipError_t e = launch_segments<T, KP>(q, s)) return e;
             if (hipError_t e = launch_walk<T, KP, kSave>(q, s)) return e;
         }
     }
-    const int64_t nvt = (sh.dv + 63) / 64;
-    constexpr size_t rlds = rev_lds<T, KP>(), glds = grad_lds<T, KP>();
-    hipLaunchKernelGGL((delta_rev_kernel<T, KP>), dim3(static_cast<unsigned>(nvt * sh.heads * sh.nseq)), dim3(kThreads), rlds, s, p);
-    if (hipError_t e = hipGetLastError()) return e;
+    if (hipError_t e = launch_rev<T, KP>(p, s)) return e;
     if (sh.slots == 0) return hipSuccess;
     const dim3 grid(static_cast<unsigned>(sh.slots * sh.kheads));
+    constexpr size_t glds = grad_lds<T, KP>();
     if (sh.heads == sh.kheads) hipLaunchKernelGGL((delta_grad_kernel<T, KP, false>), grid, dim3(kThreads), glds, s, p);
     else hipLaunchKernelGGL((delta_grad_kernel<T, KP, true>), grid, dim3(kThreads), glds, s, p);
     return hipGetLastError();

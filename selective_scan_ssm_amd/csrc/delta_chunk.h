@@ -19,7 +19,6 @@ struct ChunkWs {
 struct SeqParams {
     DeltaArgs a;
     ChunkWs ws;
-    float *R;                       // per (slot, head): (64, V) fp32
     int cps;                        // chunks of a time segment
     bool wide, wide_ends;           // see Plan
     int64_t segments;               // slots of segments
@@ -152,6 +151,7 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
     }
     wave_sync();
     char *const to = ws.t + unit * kTriBytes;
+    if (!BWD || ws.t)                                  // the gradient needs T itself only where it walks forward first
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
@@ -220,15 +220,17 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
 // that start as columns of the identity, with V = 0); delta_carry_kernel joins them,
 // and the pass proper starts every segment from the state it is entered with.
 enum Mode {
-    kOut,       // y (and the states entering the chunks, for a gradient to come)
-    kSave,      // the states entering the chunks, and R
-    kOne,       // R of one chunk from its saved state, all chunks at once
+    kOut,       // y
+    kTrain,     // y, and for the gradient to come the states entering the chunks, and R
+    kSave,      // these alone
     kEnds       // the segments' ends
 };
+constexpr bool has_out(Mode m) { return m == kOut || m == kTrain; }
+constexpr bool has_save(Mode m) { return m == kTrain || m == kSave; }
 template <typename T, int KP, Mode MODE, int CT>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && CT == 1 ? 2 : 1))) void delta_seq_kernel(SeqParams p) {
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
-    constexpr bool OUT = MODE == kOut, ONE = MODE == kOne;
+    constexpr bool OUT = has_out(MODE), SAVE = has_save(MODE);
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sT = sC + Cols<T, KP>::kBytes;
     float *const sS = reinterpret_cast<float *>(sT + kTriBytes);
@@ -243,25 +245,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
     const int tile = blockIdx.x % tiles_n;
     const int64_t rest = blockIdx.x / tiles_n, head = rest % H, kh = head / (H / a.s.kheads), id = rest / H;
     Span sp;
-    int64_t seq;
-    int j0, j1;
-    bool first = true, last = true;
-    if constexpr (ONE) {
-        seq = sequence_of(a.s, id);
-        sp = span_of(a.s, seq);
-        const int64_t j = id - sp.slot0;
-        if (j < 0 || j * kC >= sp.len) return;
-        j0 = static_cast<int>(j);
-        j1 = j0 + 1;
-    } else {
-        const Segment sg = segment_of(a.s, id, p.cps, sp);
-        if (!sg.used) return;
-        seq = sg.seq;
-        j0 = sg.j0;
-        j1 = sg.j1;
-        first = sg.s == 0;
-        last = sg.last;
-    }
+    const Segment sg = segment_of(a.s, id, p.cps, sp);
+    if (!sg.used) return;
+    const int64_t seq = sg.seq;
+    const int j0 = sg.j0, j1 = sg.j1;
+    const bool first = sg.s == 0, last = sg.last;
     const bool transition = MODE == kEnds && tile >= nvt;
     if (MODE == kEnds && (last || (first && transition))) return;
     const int vt = transition ? 0 : tile;
@@ -272,9 +260,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int v = v0 + 16 * ct;
-        if constexpr (ONE) {
-            load_state<KP>(S[ct], a.ckpt + ((sp.slot0 + j0) * H + head) * VK, v, V, K, lane);
-        } else if (transition) {
+        if (transition) {
             const int col = (tile - nvt) * kWide + (w * CT + ct) * 16 + c;
 #pragma unroll
             for (int q = 0; q < KK; ++q)
@@ -356,11 +342,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
         nV.put(sV);
         const Values<T, CT> cV = nV;
         __syncthreads();
-        if constexpr (!ONE) {
-            if (MODE != kEnds && a.ckpt) {
+        if constexpr (SAVE) {
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * VK, v0 + 16 * ct, V, K, lane);
-            }
+            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * (VK + kC * V), v0 + 16 * ct, V, K, lane);
         }
         Op2<T> so[CT][KK];
 #pragma unroll
@@ -381,7 +365,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
                 for (int ct = 0; ct < CT; ++ct) ks[ct][tb] = mma(f, so[ct][kk], ks[ct][tb]);
             }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!ONE) prefetch1();
+        prefetch1();
         __builtin_amdgcn_sched_barrier(0);
         f32x4 y[OUT ? CT : 1][4];                          // transposed: rows are channels, columns steps
         if constexpr (OUT) {
@@ -421,10 +405,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!ONE) prefetch2();
+        prefetch2();
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (MODE == kSave || ONE) {              // R, transposed, for stores of four channels
-            const rsrc_t rr = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+        if constexpr (SAVE) {                              // R, transposed, for stores of four channels
+            const rsrc_t rr = make_rsrc(a.ckpt + unit * (VK + kC * V) + VK, static_cast<uint32_t>(kC * V * 4));
             f32x4 rt[CT][4];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
@@ -440,7 +424,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
                 for (int tb = 0; tb < 4; ++tb) store4(rt[ct][tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
             }
         }
-        if constexpr (ONE) return;
         f32x4 R[CT][4];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
@@ -528,7 +511,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
             }
             put_op(out + ((n0 / 32 + kk) * KT + kt) * kOp2Bytes, lane, computed<T>(x, y));
         }
-    } else if constexpr (!ONE) {
+    } else {
         if (last && a.last_state) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.last_state + (seq * H + head) * VK, v0 + 16 * ct, V, K, lane);
@@ -538,7 +521,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
 
 template <typename T, int KP, Mode MODE, int CT> constexpr size_t seq_lds() {
     constexpr size_t n = Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + kTriBytes + 3 * kC * 4 + Values<T, CT>::kBytes +
-                         (MODE == kOut ? kTriBytes + Rows<T, KP>::kBytes : 0), m = MODE == kEnds ? 64 * CT * (KP + 4) * 4 : 0;
+                         (has_out(MODE) ? kTriBytes + Rows<T, KP>::kBytes : 0), m = MODE == kEnds ? 64 * CT * (KP + 4) * 4 : 0;
     return n > m ? n : m;
 }
 
@@ -585,7 +568,7 @@ template <typename T, int KP, bool BWD> hipError_t launch_prep(const DeltaArgs &
 template <typename T, int KP, Mode MODE, int CT> hipError_t launch_seq(const SeqParams &p, hipStream_t s) {
     constexpr int wide = 64 * CT;
     const int64_t nvt = (p.a.s.dv + wide - 1) / wide;
-    const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * (MODE == kOne ? p.a.s.slots : p.segments);
+    const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * p.segments;
     constexpr size_t lds = seq_lds<T, KP, MODE, CT>();
     hipLaunchKernelGGL((delta_seq_kernel<T, KP, MODE, CT>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
     return hipGetLastError();

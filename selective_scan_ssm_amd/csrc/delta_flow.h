@@ -109,8 +109,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     using T = bf16_t;
     using B = FlowBuf<KP, CT, NW>;
     constexpr int KT = KP / 16, KK = KP / 32;
-    constexpr bool OUT = MODE == kOut;
-    static_assert(MODE != kOne, "a chunk alone has nothing to load ahead");
+    constexpr bool OUT = has_out(MODE), SAVE = has_save(MODE);
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const DeltaArgs &a = p.a;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -203,9 +202,9 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         const char *const buf = smem + j % 2 * B::bytes;
         const float *const sS = reinterpret_cast<const float *>(buf + B::s);
         flow_barrier();
-        if (MODE != kEnds && a.ckpt) {
+        if constexpr (SAVE) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * VK, v0 + 16 * ct, V, K, lane);
+            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * (VK + kC * V), v0 + 16 * ct, V, K, lane);
         }
         // With a wave to a SIMD the reads of LDS are issued a product ahead of their use, and held there by `fence`: left
         // to itself the compiler reads each operand where it is used and waits for it.  Eight waves cover one another's
@@ -307,8 +306,8 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) R[ct][tb] = zero;
-        if constexpr (MODE == kSave) {                     // R, transposed, for stores of four channels
-            const rsrc_t rr = make_rsrc(p.R + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+        if constexpr (SAVE) {                              // R, transposed, for stores of four channels
+            const rsrc_t rr = make_rsrc(a.ckpt + unit * (VK + kC * V) + VK, static_cast<uint32_t>(kC * V * 4));
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 f32x4 rt[4] = {zero, zero, zero, zero};

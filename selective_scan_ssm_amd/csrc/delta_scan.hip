@@ -38,7 +38,7 @@ template <typename T, int KP> hipError_t run(const DeltaArgs &a, hipStream_t s) 
         if (hipError_t e = launch_prep<T, KP, false>(a, p.ws, s)) return e;
         if (hipError_t e = launch_segments<T, KP>(p, s)) return e;
     }
-    return launch_walk<T, KP, kOut>(p, s);
+    return a.ckpt && a.s.slots > 0 ? launch_walk<T, KP, kTrain>(p, s) : launch_walk<T, KP, kOut>(p, s);
 }
 
 // ------------------------------------------------------------------- one token

@@ -73,7 +73,7 @@ int check_delta(ssm::DeltaShape &s, int64_t batch, int64_t seqlen, bool packed, 
     // workgroups of 256 lanes per chunk (sequence), head and 64 channels
     const int64_t groups = mul3(slots, heads, tiles);
     if (groups < 0 || groups > kMaxLanes / 256) return SSM_ERR_SHAPE;
-    if (mul3(groups, 64 * 64, 8) < 0 || mul3(mul3(slots, heads, dv), dk, 8) < 0 || mul3(batch * seqlen, heads, (dk > dv ? dk : dv) * 4) < 0)
+    if (mul3(groups, 64 * 64, 8) < 0 || mul3(mul3(slots, heads, dv), dk + C, 8) < 0 || mul3(batch * seqlen, heads, (dk > dv ? dk : dv) * 4) < 0)
         return SSM_ERR_SHAPE;
     return SSM_OK;
 }
@@ -133,7 +133,7 @@ size_t ssm_delta_ckpt_bytes(int64_t batch, int64_t seqlen, int packed, int64_t n
                             int64_t headdim) {
     ssm::DeltaShape s{};
     if (check_delta(s, batch, seqlen, packed != 0, nseq, nheads, nheads, dstate, headdim, SSM_F32)) return kBad;
-    return static_cast<size_t>(s.slots * s.heads) * static_cast<size_t>(dstate * headdim) * 4;
+    return static_cast<size_t>(s.slots * s.heads) * static_cast<size_t>(ssm::delta_ckpt_stride(dstate, headdim)) * 4;
 }
 
 size_t ssm_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nseq, int64_t nkheads, int64_t nheads,
@@ -162,7 +162,7 @@ int ssm_delta_scan_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk, c
     const size_t need = ssm::delta_scan_workspace(a.s, a.bf16);
     const Range ins[] = {in.q, in.k, in.v, in.g, in.beta, in.h0, in.starts};
     const Range outs[] = {range(y, in.rows * nheads * headdim, in.es), range(last_state, in.ends, 4),
-                          range(ckpt, a.s.slots * nheads * dstate * headdim, 4),
+                          range(ckpt, a.s.slots * nheads * ssm::delta_ckpt_stride(dstate, headdim), 4),
                           range(need ? workspace : nullptr, static_cast<int64_t>(need), 1)};
     if (int r = check_overlap(outs, ins)) return r;
     if (int r = check_workspace(need, workspace, workspace_bytes)) return r;
@@ -199,7 +199,7 @@ int ssm_delta_scan_bwd(const void *q, int64_t ldq, const void *k, int64_t ldk, c
     const size_t need = ssm::delta_scan_bwd_workspace(a.s, a.bf16, ckpt != nullptr);
     const int64_t nk = in.rows * nkheads * dstate, nv = in.rows * nheads * headdim, nh = in.rows * nheads;
     const Range ins[] = {in.q, in.k, in.v, in.g, in.beta, in.h0, in.starts, range(dout, nv, in.es), range(dlast, in.ends, 4),
-                         range(ckpt, a.s.slots * nheads * dstate * headdim, 4)};
+                         range(ckpt, a.s.slots * nheads * ssm::delta_ckpt_stride(dstate, headdim), 4)};
     const Range outs[] = {range(dq, nk, in.es), range(dk, nk, in.es), range(dv, nv, in.es), range(dg, nh, 4), range(dbeta, nh, 4),
                           range(dh0, in.ends, 4), range(need ? workspace : nullptr, static_cast<int64_t>(need), 1)};
     if (int r = check_overlap(outs, ins)) return r;

@@ -272,11 +272,12 @@ struct DeltaArgs {
     int64_t ldq, ldk, ldv;
     const float *g, *beta, *h0;
     void *y;
-    float *last_state, *ckpt;
+    float *last_state, *ckpt;             // ckpt: per (chunk, head) the state entering it (dv, dk), then R (64, dv)
     float scale;
     int bf16;
     void *workspace;
 };
+inline __host__ __device__ int64_t delta_ckpt_stride(int64_t dk, int64_t dv) { return dv * (dk + kDeltaChunk); }
 struct DeltaBwdArgs {
     DeltaArgs fwd;                        // y, last_state unused; ckpt is read
     const void *dout;

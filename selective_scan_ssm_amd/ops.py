@@ -849,12 +849,14 @@ def _delta_shape(q, v, starts):
 
 def delta_ckpt_shape(q, v, starts=None):
     """Shape of delta_scan_fwd's checkpoints for these inputs: (slots, nheads,
-    headdim, dstate) with batch * ceil(seqlen / 64) slots, or seqlen // 64 +
-    sequences for packed ones (chunk j of sequence i: slot starts[i] // 64 + i + j)."""
+    headdim * (dstate + 64)), per chunk and head the state entering it (headdim,
+    dstate) and the corrections r of its steps (64, headdim).  batch *
+    ceil(seqlen / 64) slots, or seqlen // 64 + sequences for packed ones (chunk j of
+    sequence i: slot starts[i] // 64 + i + j)."""
     Bt, T, packed, nseq, _, H, K, V = _delta_shape(q, v, starts)
     C = _lib.DELTA_CHUNK
     slots = (T // C + nseq if nseq and T else 0) if packed else Bt * -(-T // C)
-    return (slots, H, V, K)
+    return (slots, H, V * (K + C))
 
 
 def delta_scan_workspace_bytes(q, v, starts=None):
@@ -906,8 +908,8 @@ def delta_scan_fwd(q, k, v, g, beta, scale=None, h0=None, starts=None, return_la
     i is the rows starts[i] .. starts[i + 1] - 1; rows outside of all are neither
     read nor written (they stay as they are in `out`, undefined without it).
     Returns y (same dtype as v) or (y, last_state fp32).  ckpt_out: an fp32 tensor
-    of delta_ckpt_shape(...) that also receives the states entering the 64-step
-    chunks, for delta_scan_bwd(..., ckpt=ckpt_out).  workspace: a uint8 tensor of
+    of delta_ckpt_shape(...) that also receives what delta_scan_bwd needs of each
+    64-step chunk, for delta_scan_bwd(..., ckpt=ckpt_out).  workspace: a uint8 tensor of
     at least delta_scan_workspace_bytes(...), allocated here without one."""
     lib = _lib.load()
     io, dev, (Bt, T, packed, nseq, Hk, H, K, V), ends, head = _delta_inputs(q, k, v, g, beta, scale, h0, starts)

@@ -41,7 +41,8 @@ def check_fwd(ops, t, scale=0.3, want_ckpt=True):
     D.close(y, yo, io, T, "y", size=scale * D.rms(st) * K ** 0.5 * D.rms(U.f64(t["q"])))
     D.close(last, st[-1], io, T, "last", size=D.rms(st))
     if want_ckpt and T:
-        D.close(ck.unflatten(0, (B, -1)), np.moveaxis(st[:T:64], 0, 1), io, T, "ckpt", size=D.rms(st))
+        states = ck[..., :V * K].unflatten(-1, (V, K)).unflatten(0, (B, -1)).contiguous()
+        D.close(states, np.moveaxis(st[:T:64], 0, 1), io, T, "ckpt", size=D.rms(st))
     return y, last, ck
 
 

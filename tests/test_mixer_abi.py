@@ -107,8 +107,8 @@ def test_delta_empty(lib):
 
 
 def test_delta_sizes(lib):
-    assert lib.ssm_delta_ckpt_bytes(2, 130, 0, 0, 4, 8, 16) == 2 * 3 * 4 * 8 * 16 * 4
-    assert lib.ssm_delta_ckpt_bytes(1, 130, 1, 5, 4, 8, 16) == (2 + 5) * 4 * 8 * 16 * 4
+    assert lib.ssm_delta_ckpt_bytes(2, 130, 0, 0, 4, 8, 16) == 2 * 3 * 4 * 16 * (8 + 64) * 4
+    assert lib.ssm_delta_ckpt_bytes(1, 130, 1, 5, 4, 8, 16) == (2 + 5) * 4 * 16 * (8 + 64) * 4
     assert lib.ssm_delta_ckpt_bytes(2, 130, 1, 5, 4, 8, 16) == BAD
     assert lib.ssm_delta_ckpt_bytes(2, 0, 0, 0, 4, 8, 16) == 0
     for fn, extra in ((lib.ssm_delta_scan_workspace_bytes, ()), (lib.ssm_delta_scan_bwd_workspace_bytes, (0,)),

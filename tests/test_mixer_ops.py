@@ -28,10 +28,10 @@ def test_exports(ops):
 def test_shapes_and_sizes(ops):
     lib = _lib.load()
     q, v = torch.empty(2, 130, 2, 8), torch.empty(2, 130, 4, 16)
-    assert ops.delta_ckpt_shape(q, v) == (6, 4, 16, 8)
+    assert ops.delta_ckpt_shape(q, v) == (6, 4, 16 * (8 + 64))
     starts = torch.zeros(6, dtype=torch.int32)
-    assert ops.delta_ckpt_shape(q[:1], v[:1], starts) == (2 + 5, 4, 16, 8)
-    assert ops.delta_ckpt_shape(q[:1, :0], v[:1, :0], starts) == (0, 4, 16, 8)
+    assert ops.delta_ckpt_shape(q[:1], v[:1], starts) == (2 + 5, 4, 16 * (8 + 64))
+    assert ops.delta_ckpt_shape(q[:1, :0], v[:1, :0], starts) == (0, 4, 16 * (8 + 64))
     assert ops.delta_scan_workspace_bytes(q, v) == lib.ssm_delta_scan_workspace_bytes(2, 130, 0, 2, 2, 4, 8, 16, 0)
     assert ops.delta_scan_bwd_workspace_bytes(q, v, saved=True) == lib.ssm_delta_scan_bwd_workspace_bytes(2, 130, 0, 2, 2, 4, 8, 16, 1, 0)
     with pytest.raises(RuntimeError, match="invalid arguments"):
