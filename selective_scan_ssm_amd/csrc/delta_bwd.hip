@@ -31,7 +31,7 @@ struct BwdParams {
 // What get_col reads of a chunk that is used with steps along K only.
 template <typename T, int KP> struct QSide : Cols<T, KP> {};
 template <int KP> struct QSide<bf16_t, KP> : Rows<bf16_t, KP> {
-    static __device__ __forceinline__ uint32_t offsets(int64_t ld, int K) { return Rows<bf16_t, KP>::offset(ld, K); }
+    static __device__ __forceinline__ uint32_t offsets(int64_t ld, int K, int thread) { return Rows<bf16_t, KP>::offset(ld, K, thread); }
 };
 
 // --------------------------------------------------------- dS and dX, in reverse
@@ -71,9 +71,9 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
     Copy<kTriBytes> nT, nP;
     float nS;
     Values<T, 1> nY;
-    const uint32_t okr = Rows<T, KP>::offset(a.ldk, K);
-    const auto okc = Cols<T, KP>::offsets(a.ldk, K);
-    const auto oqc = QSide<T, KP>::offsets(a.ldq, K);
+    const uint32_t okr = Rows<T, KP>::offset(a.ldk, K, threadIdx.x);
+    const auto okc = Cols<T, KP>::offsets(a.ldk, K, threadIdx.x);
+    const auto oqc = QSide<T, KP>::offsets(a.ldq, K, threadIdx.x);
     const int ldy = static_cast<int>(H * V);
     const uint32_t oy = Values<T, 1>::offset(ldy, V - vt * 64, w, lane);
     auto prefetch = [&](int j) {
@@ -95,9 +95,9 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
         const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC, unit = (sp.slot0 + j) * H + head;
         const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
         __syncthreads();                                   // the chunk before is done with LDS
-        nK.put(sK);
-        nC.put(sC);
-        nQ.put(sQ);
+        nK.put(sK, threadIdx.x);
+        nC.put(sC, threadIdx.x);
+        nQ.put(sQ, threadIdx.x);
         nT.put(sT);
         nP.put(sP);
         if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
@@ -355,50 +355,84 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 }
 
 // -------------------------------------------------------------------- the rest
-// A workgroup per (chunk, key head), over the value heads that share it; a wave
-// owns 16 of the chunk's steps as columns of transposed results (rows are the K
-// channels), so a lane holds eight neighbouring channels of one step: 16-byte
-// stores, and the row sums of dg and dbeta are sums inside a lane.  The value
-// channels are taken 32 at a time.
+// A workgroup per (chunk, key head), over the value heads that share it; a pair of
+// waves (w, w + 4) owns 16 of the chunk's steps as columns of transposed results (rows
+// are the K channels), each wave half of the channels: a lane holds eight neighbouring
+// channels of one step, so stores have 16 bytes and the row sums of dg and dbeta are sums
+// inside a lane.  Of the chunk's four decayed products wave w makes the two with the
+// pair's steps as t, wave w + 4 the two with them as s; they exchange them through LDS.
+// The value channels are taken 32 at a time, the next ones loaded meanwhile.
+constexpr int kGradThreads = 512;
 
-// 32 rows (value channels v0 ..) of a (V, K) state as operands with K channels as
-// rows and the value channels along K, and the sum of products of two of them
-template <typename T, int KP> __device__ __forceinline__ float stage_states(char *dst, char *dst2, const float *S, const float *dS,
-                                                                          int v0, int V, int K) {
-    constexpr int KT = KP / 16;
-    const rsrc_t r = make_rsrc(S, static_cast<uint32_t>(static_cast<int64_t>(V) * K * 4));
-    const rsrc_t r2 = make_rsrc(dS, static_cast<uint32_t>(static_cast<int64_t>(V) * K * 4));
-    float dot = 0.0f;
-    for (int s = threadIdx.x; s < KT * 32; s += kThreads) {
-        const int tile = s / 32, c = 2 * (s % 8), g = (s / 8) % 4;
+// half of a computed operand's eight elements in LDS
+template <typename T> __device__ __forceinline__ void put_half(char *p, int lane, int half, f32x4 v);
+template <> __device__ __forceinline__ void put_half<float>(char *p, int lane, int half, f32x4 v) {
+    *reinterpret_cast<f32x4 *>(p + half * 1024 + lane * 16) = v;
+}
+template <> __device__ __forceinline__ void put_half<bf16_t>(char *p, int lane, int half, f32x4 v) {
+    const u32x2 hi = {pack2(v[0], v[1]), pack2(v[2], v[3])};
+    *reinterpret_cast<u32x2 *>(p + lane * 16 + half * 8) = hi;
+    *reinterpret_cast<u32x2 *>(p + 1024 + lane * 16 + half * 8) =
+        u32x2{pack2(v[0] - low(hi[0]), v[1] - high(hi[0])), pack2(v[2] - low(hi[1]), v[3] - high(hi[1]))};
+}
+
+// What a thread holds of 32 value channels: two channels of four rows of S and of dS', one
+// row's eight channels of dX (waves 0 .. 3) or R (waves 4 .. 7) and of dY (waves 0 .. 3).
+template <typename T, int KP> struct GradStage {
+    static constexpr int kSlots = 2 * KP;                  // two channels of eight rows each, in halves
+    f32x2 s[4], d[4];
+    f32x4 x[2];
+    Op<T> y;
+    struct At {
+        uint32_t state, value, out, row;                   // offsets of value channel 0
+        int v4, v8;                                        // the first value channels of the halves and the eights
+    };
+    static __device__ __forceinline__ At at(int64_t ldy, int K, int V, int n) {
+        const int i = threadIdx.x % kSlots, tile = i / 32, c = 2 * (i % 8), half = threadIdx.x / kSlots;
         const int k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4;
-        f32x2 x[8], y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int v = v0 + 8 * g + j;
-            const uint32_t off = v < V && k < K ? static_cast<uint32_t>((v * K + k) * 4) : kOffNone;
-            x[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
-            y[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r2, off, 0, 0));
-            dot = fmaf(x[j][0], y[j][0], fmaf(x[j][1], y[j][1], dot));
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            put_op(dst + tile * kOp2Bytes, 16 * g + c + h,
-                   computed<T>(f32x4{x[0][h], x[1][h], x[2][h], x[3][h]}, f32x4{x[4][h], x[5][h], x[6][h], x[7][h]}));
-            put_op(dst2 + tile * kOp2Bytes, 16 * g + c + h,
-                   computed<T>(f32x4{y[0][h], y[1][h], y[2][h], y[3][h]}, f32x4{y[4][h], y[5][h], y[6][h], y[7][h]}));
-        }
+        const int lane = threadIdx.x % 64, t = row_index(threadIdx.x / 64 % 4, lane % 16);
+        At o;
+        o.v4 = 8 * ((i / 8) % 4) + 4 * half;
+        o.v8 = 8 * (lane / 16);
+        o.state = half < 2 && k < K ? static_cast<uint32_t>((o.v4 * K + k) * 4) : kOffNone;
+        o.row = static_cast<uint32_t>(K * 4);
+        o.value = static_cast<uint32_t>((t * V + o.v8) * 4);
+        o.out = t < n && threadIdx.x < 256 ? static_cast<uint32_t>((t * ldy + o.v8) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+        return o;
     }
-    return dot;
-}
-// a chunk's rows of a (64, V) fp32 workspace tensor, 32 columns from v0 on
-template <typename T> __device__ __forceinline__ void stage_values(char *dst, const float *src, int v0, int V) {
-    const rsrc_t r = make_rsrc(src);
-    const int lane = threadIdx.x % 64, f = threadIdx.x / 64;
-    const int t = row_index(f, lane % 16), v = v0 + 8 * (lane / 16);
-    const uint32_t off = v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone;
-    put_op(dst + f * kOp2Bytes, lane, computed<T>(load4(r, off), load4(r, off + 16)));
-}
+    __device__ __forceinline__ void load(rsrc_t rs, rsrc_t rd, rsrc_t rx, rsrc_t ry, const At &o, int v0, int V) {
+        const uint32_t state = o.state == kOffNone ? kOffNone : o.state + static_cast<uint32_t>(v0) * o.row;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t off = v0 + o.v4 + j < V ? state + j * o.row : kOffNone;
+            s[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
+            d[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rd, off, 0, 0));
+        }
+        const bool in = v0 + o.v8 < V;
+        const uint32_t off = in ? o.value + static_cast<uint32_t>(v0 * 4) : kOffNone;
+        x[0] = load4(rx, off);
+        x[1] = load4(rx, off + 16);
+        y = load_op(ry, in && o.out != kOffNone ? o.out + static_cast<uint32_t>(v0 * static_cast<int>(sizeof(T))) : kOffNone, T());
+    }
+    // into LDS as operands; the thread's part of <S, dS'>
+    __device__ __forceinline__ float put(char *sS, char *sD, char *sX, char *sY) const {
+        const int i = threadIdx.x % kSlots, half = threadIdx.x / kSlots, lane = threadIdx.x % 64, w = threadIdx.x / 64;
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dot = fmaf(s[j][0], d[j][0], fmaf(s[j][1], d[j][1], dot));
+        if (half < 2) {
+            const int to = i / 32 * kOp2Bytes, at = 16 * ((i / 8) % 4) + 2 * (i % 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                put_half<T>(sS + to, at + h, half, f32x4{s[0][h], s[1][h], s[2][h], s[3][h]});
+                put_half<T>(sD + to, at + h, half, f32x4{d[0][h], d[1][h], d[2][h], d[3][h]});
+            }
+        }
+        put_op(sX + w * kOp2Bytes, lane, computed<T>(x[0], x[1]));
+        if (w < 4) put_op(sY + w * kOpBytes<T>, lane, y);
+        return dot;
+    }
+};
 // the eight elements of an operand as floats
 __device__ __forceinline__ void floats(const Op<bf16_t> &o, float (&v)[8]) {
 #pragma unroll
@@ -427,24 +461,41 @@ __device__ __forceinline__ float column_total(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-template <typename T, int KP> constexpr size_t grad_lds() {
-    constexpr size_t loop = 4 * kOpBytes<T> + 8 * kOp2Bytes + 2 * (KP / 16) * kOp2Bytes, tail = 2 * QSide<T, KP>::kBytes;
-    return loop > tail ? loop : tail;
+template <typename T, int KP>
+__device__ __forceinline__ void store_keys(const BwdParams &p, const f32x4 *dq, const f32x4 *dk, int64_t row0, int64_t kh, int t, int wh,
+                                           int g, int n) {
+    constexpr int KK = KP / 64;
+    const int64_t Hk = p.b.fwd.s.kheads, K = p.b.fwd.s.dk;
+    const rsrc_t wq = make_rsrc(static_cast<T *>(p.b.dq) + (row0 * Hk + kh) * K), wk = make_rsrc(static_cast<T *>(p.b.dk) + (row0 * Hk + kh) * K);
+#pragma unroll
+    for (int kp = 0; kp < KK; ++kp) {
+        const int k0 = 32 * (wh * KK + kp) + 8 * g;
+        const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * Hk * K + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+        store_io8(dq[2 * kp], dq[2 * kp + 1], wq, off, T());
+        store_io8(dk[2 * kp], dk[2 * kp + 1], wk, off, T());
+    }
 }
 
+// LDS: what the loop over the value channels reads, then the decayed products in its
+// place; the chunk's keys and queries
+template <typename T, int KP> constexpr int grad_loop() { return 4 * kOpBytes<T> + 8 * kOp2Bytes + 2 * (KP / 16) * kOp2Bytes; }
+template <typename T, int KP> constexpr int grad_main() { return grad_loop<T, KP>() > 24 * kOp2Bytes ? grad_loop<T, KP>() : 24 * kOp2Bytes; }
+template <typename T, int KP> constexpr size_t grad_lds() { return grad_main<T, KP>() + 2 * QSide<T, KP>::kBytes; }
+
 template <typename T, int KP, bool SHARED>
-__global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
+__global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(BwdParams p) {
     using D = Decay<T>;
     using real = typename D::real;
-    constexpr int KT = KP / 16, KK = KP / 32, OB = kOpBytes<T>;
+    constexpr int KT = KP / 32, KK = KP / 64, OB = kOpBytes<T>;    // a wave's half of the channels
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    char *const sY = smem, *const sX = sY + 4 * OB, *const sR = sX + 4 * kOp2Bytes, *const sS = sR + 4 * kOp2Bytes,
-         *const sD = sS + KT * kOp2Bytes;
-    char *const sC = smem, *const sQ = sC + QSide<T, KP>::kBytes;      // after the loop over the value channels
+    char *const sX = smem, *const sR = sX + 4 * kOp2Bytes, *const sS = sR + 4 * kOp2Bytes, *const sD = sS + 2 * KT * kOp2Bytes,
+         *const sY = sD + 2 * KT * kOp2Bytes;
+    char *const sFT = smem, *const sET = sFT + 6 * kOp2Bytes, *const sF = sET + 6 * kOp2Bytes, *const sE = sF + 6 * kOp2Bytes;
+    char *const sC = smem + grad_main<T, KP>(), *const sQ = sC + QSide<T, KP>::kBytes;
     __shared__ real sG[kC];
-    __shared__ float sB[kC], sDG[kC], sTot[kWaves];
+    __shared__ float sB[kC], sQK[2][kC], sZ[2][kC], sTot[8];
     const DeltaArgs &a = p.b.fwd;
-    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = wave % 4, wh = wave / 4;
     const int g = lane / 16, c = lane % 16, t = row_index(w, c);
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
     const int64_t H = a.s.heads, slot = blockIdx.x / a.s.kheads, kh = blockIdx.x % a.s.kheads;
@@ -456,9 +507,24 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     const int n = sp.len - step0 < kC ? static_cast<int>(sp.len - step0) : kC;
     const int64_t row0 = sp.row0 + step0;
     const f32x4 zero = {0, 0, 0, 0};
+    const size_t VK = static_cast<size_t>(V) * K;
     const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, sizeof(T));
     const rsrc_t rq = chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, sizeof(T));
-    const size_t VK = static_cast<size_t>(V) * K;
+    const auto at = GradStage<T, KP>::at(H * V, K, V, n);
+    GradStage<T, KP> st;
+    auto load = [&](int64_t head, int v0) {
+        const int64_t unit = slot * H + head;
+        const float *const saved = a.ckpt + unit * (VK + kC * V);
+        st.load(make_rsrc(saved, static_cast<uint32_t>(VK * 4)), make_rsrc(p.dS + unit * VK, static_cast<uint32_t>(VK * 4)),
+                make_rsrc(wh ? saved + VK : p.dX + unit * kC * V), make_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V), at, v0, V);
+    };
+    {
+        QSide<T, KP> side;
+        const int64_t ld = wh ? a.ldq : a.ldk;
+        side.load(wh ? rq : rk, ld, QSide<T, KP>::offsets(ld, K, threadIdx.x % kThreads));
+        load(kh * group, 0);
+        side.put(wh ? sQ : sC, threadIdx.x % kThreads);
+    }
     f32x4 dqs[SHARED ? KT : 1], dks[SHARED ? KT : 1];
     if constexpr (SHARED) {
 #pragma unroll
@@ -466,69 +532,71 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
     }
     for (int hh = 0; hh < group; ++hh) {
         const int64_t head = kh * group + hh, unit = slot * H + head;
-        const float *const scal = p.ws.scal + unit * 3 * kC, *const saved = a.ckpt + unit * (VK + kC * V);
-        __syncthreads();                                     // the head before is done with sG, sB, sDG
-        if (w == 0) {
+        const float *const scal = p.ws.scal + unit * 3 * kC;
+        if (wave == 0) {
             const real G = lane_prefix<real>(lane < n ? D::scaled(step_log(a.g[(row0 + lane) * H + head])) : real(0), lane);
             sG[lane] = G;
             sB[lane] = scal[2 * kC + lane];
         }
-        f32x4 dq[KT], ke[KT], kw[KT], FT[4], F[4], ET[4], E[4];
+        const float eg = scal[t], wt = scal[kC + t], end = scal[kC - 1];
+        // A: (F diag(beta))^T or F, B: M^T or -E
+        f32x4 dq[KT], ke[KT], kw[KT], A[4], B[4];
 #pragma unroll
         for (int i = 0; i < KT; ++i) dq[i] = ke[i] = kw[i] = zero;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) FT[i] = F[i] = ET[i] = E[i] = zero;
+        for (int i = 0; i < 4; ++i) A[i] = B[i] = zero;
         float tot = 0.0f;
-        const rsrc_t rd = make_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V);
         for (int v0 = 0; v0 < V; v0 += 32) {
-            __syncthreads();
-            const int f = threadIdx.x / 64, tr = row_index(f, c), v = v0 + 8 * g;
-            put_op(sY + f * OB, lane, load_op(rd, tr < n && v < V ? static_cast<uint32_t>((tr * H * V + v) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()));
-            stage_values<T>(sX, p.dX + unit * kC * V, v0, V);
-            stage_values<T>(sR, saved + VK, v0, V);
-            tot += stage_states<T, KP>(sS, sD, saved, p.dS + unit * VK, v0, V, K);
+            tot += st.put(sS, sD, sX, sY);                   // sX's waves 4 .. 7 write sR
+            if (v0 + 32 < V) load(head, v0 + 32);
+            else if (hh + 1 < group) load(head + 1, 0);
             __syncthreads();
             const Op<T> y = get_op(sY + w * OB, lane, T());
             const Op2<T> x = get_op2(sX + w * kOp2Bytes, lane, T()), r = get_op2(sR + w * kOp2Bytes, lane, T());
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
-                const Op2<T> s = get_op2(sS + kt * kOp2Bytes, lane, T()), d = get_op2(sD + kt * kOp2Bytes, lane, T());
+                const Op2<T> s = get_op2(sS + (wh * KT + kt) * kOp2Bytes, lane, T()), d = get_op2(sD + (wh * KT + kt) * kOp2Bytes, lane, T());
                 dq[kt] = mma(s, y, dq[kt]);
                 ke[kt] = mma(s, x, ke[kt]);
                 kw[kt] = mma(d, r, kw[kt]);
             }
 #pragma unroll
             for (int ob = 0; ob < 4; ++ob) {
-                if (ob / 2 <= w / 2) {                       // rows s at or before this wave's steps
+                if (wh == 0 && ob / 2 <= w / 2) {            // rows s at or before the pair's steps
                     const Op2<T> ro = get_op2(sR + ob * kOp2Bytes, lane, T());
-                    FT[ob] = mma(ro, y, FT[ob]);
-                    ET[ob] = mma(ro, x, ET[ob]);
+                    A[ob] = mma(ro, y, A[ob]);
+                    B[ob] = mma(ro, x, B[ob]);
                 }
-                if (ob / 2 >= w / 2) {                       // rows t at or behind them
-                    F[ob] = mma(get_op(sY + ob * OB, lane, T()), r, F[ob]);
-                    E[ob] = mma(get_op2(sX + ob * kOp2Bytes, lane, T()), r, E[ob]);
+                if (wh == 1 && ob / 2 >= w / 2) {            // rows t at or behind them
+                    A[ob] = mma(get_op(sY + ob * OB, lane, T()), r, A[ob]);
+                    B[ob] = mma(get_op2(sX + ob * kOp2Bytes, lane, T()), r, B[ob]);
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
-        QSide<T, KP> side;
-        side.load(rk, a.ldk, QSide<T, KP>::offsets(a.ldk, K));
-        side.put(sC);
-        side.load(rq, a.ldq, QSide<T, KP>::offsets(a.ldq, K));
-        side.put(sQ);
-        const float eg = scal[t], wt = scal[kC + t], beta = sB[t], end = scal[kC - 1];
+        const float beta = sB[t];
         const real gt = sG[t];
 #pragma unroll
         for (int ob = 0; ob < 4; ++ob)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s for FT, ET, t for F, E
-                const float before = o <= t ? D::ex(gt - sG[o]) : 0.0f, behind = o >= t ? D::ex(sG[o] - gt) : 0.0f;
-                FT[ob][i] = o <= t ? FT[ob][i] * (a.scale * before * sB[o]) : 0.0f;    // (F diag(beta))^T
-                ET[ob][i] = o < t ? ET[ob][i] * (-before * sB[o]) : 0.0f;      // M^T
-                F[ob][i] = o >= t ? F[ob][i] * (a.scale * behind) : 0.0f;
-                E[ob][i] = o > t ? E[ob][i] * -behind : 0.0f;
+                const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s or t
+                const bool in = wh ? o >= t : o <= t;
+                const float d = in ? D::ex(wh ? sG[o] - gt : gt - sG[o]) * (wh ? 1.0f : sB[o]) : 0.0f;
+                A[ob][i] = in ? A[ob][i] * (a.scale * d) : 0.0f;
+                B[ob][i] = in && o != t ? B[ob][i] * -d : 0.0f;
             }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            if (wh == 0 && kk <= w / 2) {
+                put_op(sFT + tri_low(w, kk) * kOp2Bytes, lane, computed<T>(A[2 * kk], A[2 * kk + 1]));
+                put_op(sET + tri_low(w, kk) * kOp2Bytes, lane, computed<T>(B[2 * kk], B[2 * kk + 1]));
+            }
+            if (wh == 1 && kk >= w / 2) {
+                put_op(sF + tri_up(w, kk) * kOp2Bytes, lane, computed<T>(A[2 * kk], A[2 * kk + 1]));
+                put_op(sE + tri_up(w, kk) * kOp2Bytes, lane, computed<T>(B[2 * kk], B[2 * kk + 1]));
+            }
+        }
         float qd = 0.0f, kd = 0.0f, kz = 0.0f, kc = 0.0f;
         const float fq = a.scale * eg;
 #pragma unroll
@@ -537,53 +605,72 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
             ke[kt] = ke[kt] * -eg;
             kw[kt] = kw[kt] * wt;                            // Z
         }
+        float kv[KK][8], qv[KK][8];
+#pragma unroll
+        for (int kp = 0; kp < KK; ++kp) {
+            const int k0 = 32 * (wh * KK + kp) + 8 * g;
+            floats(load_op(rk, k0 < K ? static_cast<uint32_t>((t * a.ldk + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()), kv[kp]);
+            floats(load_op(rq, k0 < K ? static_cast<uint32_t>((t * a.ldq + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()), qv[kp]);
+        }
         __syncthreads();
 #pragma unroll
-        for (int kp = 0; kp < KK; ++kp) {                    // pairs of channel tiles
-            const int k0 = 32 * kp + 8 * g;
-            const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * a.ldk + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-            const uint32_t offq = t < n && k0 < K ? static_cast<uint32_t>((t * a.ldq + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-            float kv[8], qv[8];
-            floats(load_op(rk, off, T()), kv);
-            floats(load_op(rq, offq, T()), qv);
+        for (int kp = 0; kp < KK; ++kp)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kc = fmaf(kv[kp][4 * h + i], kw[2 * kp + h][i], kc);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            if (kk <= w / 2) {
+                const Op2<T> ft = get_op2(sFT + tri_low(w, kk) * kOp2Bytes, lane, T()), et = get_op2(sET + tri_low(w, kk) * kOp2Bytes, lane, T());
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    const Op<T> kcol = get_col<KP>(sC, sC, wh * KT + kt, kk, lane, T());
+                    dq[kt] = mma(kcol, ft, dq[kt]);
+                    ke[kt] = mma(kcol, et, ke[kt]);
+                }
+            }
+            if (kk >= w / 2) {
+                const Op2<T> f = get_op2(sF + tri_up(w, kk) * kOp2Bytes, lane, T()), e = get_op2(sE + tri_up(w, kk) * kOp2Bytes, lane, T());
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    kw[kt] = mma(get_col<KP>(sQ, sQ, wh * KT + kt, kk, lane, T()), f, kw[kt]);
+                    kw[kt] = mma(get_col<KP>(sC, sC, wh * KT + kt, kk, lane, T()), e, kw[kt]);
+                }
+            }
+        }
+#pragma unroll
+        for (int kp = 0; kp < KK; ++kp)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int kt = 2 * kp + h;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) kc = fmaf(kv[4 * h + i], kw[kt][i], kc);
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    const Op<T> kcol = get_col<KP>(sC, sC, kt, kk, lane, T()), qcol = get_col<KP>(sQ, sQ, kt, kk, lane, T());
-                    if (kk <= w / 2) {
-                        dq[kt] = mma(kcol, computed<T>(FT[2 * kk], FT[2 * kk + 1]), dq[kt]);
-                        ke[kt] = mma(kcol, computed<T>(ET[2 * kk], ET[2 * kk + 1]), ke[kt]);
-                    }
-                    if (kk >= w / 2) {
-                        kw[kt] = mma(qcol, computed<T>(F[2 * kk], F[2 * kk + 1]), kw[kt]);
-                        kw[kt] = mma(kcol, computed<T>(E[2 * kk], E[2 * kk + 1]), kw[kt]);
-                    }
-                }
-#pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    qd = fmaf(qv[4 * h + i], dq[kt][i], qd);
-                    kd = fmaf(kv[4 * h + i], ke[kt][i], kd);
-                    kz = fmaf(kv[4 * h + i], kw[kt][i], kz);
+                    qd = fmaf(qv[kp][4 * h + i], dq[kt][i], qd);
+                    kd = fmaf(kv[kp][4 * h + i], ke[kt][i], kd);
+                    kz = fmaf(kv[kp][4 * h + i], kw[kt][i], kz);
                 }
                 ke[kt] = ke[kt] + kw[kt] * beta;
             }
-        }
-        const float dG = column_total(fmaf(-beta, kz, qd + kd));
-        kz = column_total(kz);
-        if (g == 0 && t < n) p.b.dbeta[(row0 + t) * H + head] = kz;
+        const float qk = column_total(qd + kd), z = column_total(kz);
         tot = wave_fold(fmaf(end, tot, beta * kc), AddOp());
-        if (lane == 0) sTot[w] = tot;
-        if (g == 0) sDG[t] = dG;
+        if (lane == 0) sTot[wave] = tot;
+        if (g == 0) {
+            sQK[wh][t] = qk;
+            sZ[wh][t] = z;
+        }
         __syncthreads();
-        if (w == 0) {                                        // lane l is step 63 - l: sums from the end
-            double v = sDG[63 - lane];
-            if (lane == 0) v += static_cast<double>(sTot[0]) + sTot[1] + sTot[2] + sTot[3];
+        if (wave == 0) {                                     // lane l is step 63 - l: sums from the end
+            const int l = 63 - lane;
+            const float zl = sZ[0][l] + sZ[1][l];
+            double v = static_cast<double>(sQK[0][l]) + sQK[1][l] - static_cast<double>(sB[l]) * zl;
+            if (lane == 0)
+                for (int i = 0; i < 8; ++i) v += sTot[i];
             v = lane_prefix<double>(v, lane);
-            if (63 - lane < n) p.b.dg[(row0 + 63 - lane) * H + head] = static_cast<float>(v);
+            if (l < n) {
+                p.b.dg[(row0 + l) * H + head] = static_cast<float>(v);
+                p.b.dbeta[(row0 + l) * H + head] = zl;
+            }
         }
         if constexpr (SHARED) {
 #pragma unroll
@@ -592,28 +679,10 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(BwdParams p) {
                 dks[i] = dks[i] + ke[i];
             }
         } else {
-            const int64_t Hk = a.s.kheads;
-            const rsrc_t wq = make_rsrc(static_cast<T *>(p.b.dq) + (row0 * Hk + kh) * K), wk = make_rsrc(static_cast<T *>(p.b.dk) + (row0 * Hk + kh) * K);
-#pragma unroll
-            for (int kp = 0; kp < KK; ++kp) {
-                const int k0 = 32 * kp + 8 * g;
-                const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * Hk * K + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-                store_io8(dq[2 * kp], dq[2 * kp + 1], wq, off, T());
-                store_io8(ke[2 * kp], ke[2 * kp + 1], wk, off, T());
-            }
+            store_keys<T, KP>(p, dq, ke, row0, kh, t, wh, g, n);
         }
     }
-    if constexpr (SHARED) {
-        const int64_t Hk = a.s.kheads;
-        const rsrc_t wq = make_rsrc(static_cast<T *>(p.b.dq) + (row0 * Hk + kh) * K), wk = make_rsrc(static_cast<T *>(p.b.dk) + (row0 * Hk + kh) * K);
-#pragma unroll
-        for (int kp = 0; kp < KK; ++kp) {
-            const int k0 = 32 * kp + 8 * g;
-            const uint32_t off = t < n && k0 < K ? static_cast<uint32_t>((t * Hk * K + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-            store_io8(dqs[2 * kp], dqs[2 * kp + 1], wq, off, T());
-            store_io8(dks[2 * kp], dks[2 * kp + 1], wk, off, T());
-        }
-    }
+    if constexpr (SHARED) store_keys<T, KP>(p, dqs, dks, row0, kh, t, wh, g, n);
 }
 
 // bf16: 64 value channels to a workgroup while the CUs hold them all, else 128
@@ -688,8 +757,8 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
     if (sh.slots == 0) return hipSuccess;
     const dim3 grid(static_cast<unsigned>(sh.slots * sh.kheads));
     constexpr size_t glds = grad_lds<T, KP>();
-    if (sh.heads == sh.kheads) hipLaunchKernelGGL((delta_grad_kernel<T, KP, false>), grid, dim3(kThreads), glds, s, p);
-    else hipLaunchKernelGGL((delta_grad_kernel<T, KP, true>), grid, dim3(kThreads), glds, s, p);
+    if (sh.heads == sh.kheads) hipLaunchKernelGGL((delta_grad_kernel<T, KP, false>), grid, dim3(kGradThreads), glds, s, p);
+    else hipLaunchKernelGGL((delta_grad_kernel<T, KP, true>), grid, dim3(kGradThreads), glds, s, p);
     return hipGetLastError();
 }
 

@@ -284,8 +284,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
     Copy<kTriBytes> nT, nP;
     float nS;
     Values<T, CT> nV;
-    const uint32_t okr = Rows<T, KP>::offset(a.ldk, K), oqr = Rows<T, KP>::offset(a.ldq, K);
-    const auto okc = Cols<T, KP>::offsets(a.ldk, K);
+    const uint32_t okr = Rows<T, KP>::offset(a.ldk, K, threadIdx.x), oqr = Rows<T, KP>::offset(a.ldq, K, threadIdx.x);
+    const auto okc = Cols<T, KP>::offsets(a.ldk, K, threadIdx.x);
     const int ldv = static_cast<int>(a.ldv);
     const uint32_t ov = Values<T, CT>::offset(ldv, V - vt * kWide, w, lane);
     // addresses move on by whole chunks; loads are issued in two parts, each beside products, as a chunk's loads take
@@ -331,14 +331,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
         const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC;
         const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
         __syncthreads();                                   // the chunk before is done with LDS
-        nK.put(sK);
+        nK.put(sK, threadIdx.x);
         nT.put(sT);
         if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
         if constexpr (OUT) {
-            nQ.put(sQ);
+            nQ.put(sQ, threadIdx.x);
             nP.put(sP);
         }
-        nC.put(sC);
+        nC.put(sC, threadIdx.x);
         nV.put(sV);
         const Values<T, CT> cV = nV;
         __syncthreads();

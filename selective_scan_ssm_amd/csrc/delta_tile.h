@@ -307,8 +307,8 @@ template <typename T, int KP> struct Rows {
     static constexpr int kTiles = kWaves / KK;                 // tiles that the threads cover at a time
     Op<T> v[N];
     // the thread's offset in the first tiles; the others are whole rows further on
-    static __device__ __forceinline__ uint32_t offset(int64_t ld, int K) {
-        const int lane = threadIdx.x % 64, f = threadIdx.x / 64;
+    static __device__ __forceinline__ uint32_t offset(int64_t ld, int K, int thread) {
+        const int lane = thread % 64, f = thread / 64;
         const int t = row_index(f / KK, lane % 16), k = 32 * (f % KK) + 8 * (lane / 16);
         return k < K ? static_cast<uint32_t>((t * static_cast<int>(ld) + k) * static_cast<int>(sizeof(T))) : kOffNone;
     }
@@ -317,10 +317,10 @@ template <typename T, int KP> struct Rows {
         for (int i = 0; i < N; ++i)
             v[i] = load_op(r, off + static_cast<uint32_t>(row_index(i * kTiles, 0) * static_cast<int>(ld) * static_cast<int>(sizeof(T))), T());
     }
-    __device__ __forceinline__ void put(char *dst) const {
+    __device__ __forceinline__ void put(char *dst, int thread) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int s = i * kThreads + threadIdx.x;
+            const int s = i * kThreads + thread;
             put_row(dst + s / 64 * kRowBytes<T>, s % 64, v[i]);
         }
     }
@@ -331,18 +331,18 @@ template <typename T, int KP> struct Rows {
 template <typename T, int KP> struct Cols {
     static constexpr int KT = KP / 16, N = KT * 2 * 32 / kThreads, kBytes = 2 * KT * kOpBytes<T>;
     Columns<T> v[N];
-    static __device__ __forceinline__ uint32_t offset(int64_t ld, int i, int K) {
-        const int s = i * kThreads + threadIdx.x, f = s / 32, c = 2 * (s % 8), g = (s / 8) % 4;
+    static __device__ __forceinline__ uint32_t offset(int64_t ld, int i, int K, int thread) {
+        const int s = i * kThreads + thread, f = s / 32, c = 2 * (s % 8), g = (s / 8) % 4;
         const int tile = f / 2, k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4, t0 = 32 * (f % 2) + 8 * g;
         return k < K ? static_cast<uint32_t>((t0 * static_cast<int>(ld) + k) * static_cast<int>(sizeof(T))) : kOffNone;
     }
     struct Offsets {
         uint32_t at[N];
     };
-    static __device__ __forceinline__ Offsets offsets(int64_t ld, int K) {
+    static __device__ __forceinline__ Offsets offsets(int64_t ld, int K, int thread) {
         Offsets o;
 #pragma unroll
-        for (int i = 0; i < N; ++i) o.at[i] = offset(ld, i, K);
+        for (int i = 0; i < N; ++i) o.at[i] = offset(ld, i, K, thread);
         return o;
     }
     __device__ __forceinline__ void load(rsrc_t r, int64_t ld, const Offsets &o) {
@@ -351,10 +351,10 @@ template <typename T, int KP> struct Cols {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i].load(r, j, o.at[i] + static_cast<uint32_t>(j * static_cast<int>(ld) * static_cast<int>(sizeof(T))));
     }
-    __device__ __forceinline__ void put(char *dst) const {
+    __device__ __forceinline__ void put(char *dst, int thread) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int s = i * kThreads + threadIdx.x, f = s / 32;
+            const int s = i * kThreads + thread, f = s / 32;
             v[i].put(dst + f * kOpBytes<T>, 16 * ((s / 8) % 4) + 2 * (s % 8));
         }
     }
@@ -362,9 +362,9 @@ template <typename T, int KP> struct Cols {
 template <int KP> struct Cols<bf16_t, KP> {
     static constexpr int kBytes = 0;
     struct Offsets {};
-    static __device__ __forceinline__ Offsets offsets(int64_t, int) { return {}; }
+    static __device__ __forceinline__ Offsets offsets(int64_t, int, int) { return {}; }
     __device__ __forceinline__ void load(rsrc_t, int64_t, const Offsets &) {}
-    __device__ __forceinline__ void put(char *) const {}
+    __device__ __forceinline__ void put(char *, int) const {}
 };
 // channels of tile kt as rows, steps 32 kk + 8 g ... along K, from the rows or the columns in LDS
 template <int KP> __device__ __forceinline__ Op<bf16_t> get_col(const char *rows, const char *, int kt, int kk, int lane, bf16_t) {
