@@ -7,10 +7,10 @@
 //
 // HBM-bound.  With one row to a statistic (a norm per token and head) a group lies
 // in the registers of a few lanes, and every tensor is read once and written once.
-// Otherwise a batch entry is cut into runs of rows; the first pass leaves partial
-// sums of each run in the workspace, a small kernel adds them in a fixed order, and
-// the second pass reads the inputs again.  The forward's sums of x and x^2 are
-// taken in fp64, so that a mean far from 0 costs the variance nothing.
+// Otherwise, where a few groups of a batch entry fit a workgroup's registers, it keeps
+// them there over both passes.  Else a batch entry is cut into runs of rows; the
+// first pass leaves each run's sums in the workspace, and the second adds them up, in a
+// fixed order, and reads the inputs again.
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 #include "wave_fold.h"
@@ -20,9 +20,10 @@ namespace {
 
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
-constexpr int kRunGroups = 2048;        // workgroups that the runs of rows are cut for: eight per CU
 
 // V consecutive io elements
 template <typename T, int V> struct Vec;
@@ -54,21 +55,20 @@ template <typename T, int V> __device__ __forceinline__ void store_vec(T *p, con
         else
 #pragma unroll
             for (int i = 0; i < V; ++i) q[i] = __float_as_uint(v[i]);
-        *reinterpret_cast<typename Vec<T, V>::raw *>(p) = q;
+        __builtin_nontemporal_store(q, reinterpret_cast<typename Vec<T, V>::raw *>(p));
     } else if constexpr (V == 1) {
         *reinterpret_cast<uint16_t *>(p) = from_f32<bf16_t>(v[0]).bits;
     } else {
         uint32_t u[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i)
-            u[i] = static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i]).bits) |
-                   (static_cast<uint32_t>(from_f32<bf16_t>(v[2 * i + 1]).bits) << 16);
+            u[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * i], v[2 * i + 1]}, bf2));
         typename Vec<T, V>::raw q;
         if constexpr (V == 2) q = u[0];
         else
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) q[i] = u[i];
-        *reinterpret_cast<typename Vec<T, V>::raw *>(p) = q;
+        __builtin_nontemporal_store(q, reinterpret_cast<typename Vec<T, V>::raw *>(p));
     }
 }
 
@@ -127,21 +127,34 @@ template <typename T, int V, int P, int L, bool BWD> __global__ __launch_bounds_
     const bool act = a.silu != 0, gate = a.z != nullptr;
     const float inv = 1.0f / static_cast<float>(D);
     using raw = typename Vec<T, V>::raw;
-    for (int64_t row = first * 4 + w; row < a.batch; row += step * 4) {
+    struct Row {
+        raw x[P], z[P], d[P];
+    } next;
+    auto load = [&](int64_t row) {
         const T *const px = static_cast<const T *>(a.x) + row * a.ldx + group * D;
         const T *const pz = static_cast<const T *>(a.z) + row * a.ldz + group * D;
         const T *const pd = static_cast<const T *>(b.dy) + row * a.dim + group * D;
-        raw rx[P], rz[P], rd[P];
 #pragma unroll
         for (int c = 0; c < P; ++c) {
             const int e = e0 + c * L * V;
-            rx[c] = rz[c] = rd[c] = raw{};
+            next.x[c] = next.z[c] = next.d[c] = raw{};
             if (in[c]) {
-                rx[c] = load_vec<T, V>(px + e);
-                if (gate) rz[c] = load_vec<T, V>(pz + e);
-                if constexpr (BWD) rd[c] = load_vec<T, V>(pd + e);
+                next.x[c] = load_vec<T, V>(px + e);
+                if (gate) next.z[c] = load_vec<T, V>(pz + e);
+                if constexpr (BWD) next.d[c] = load_vec<T, V>(pd + e);
             }
         }
+    };
+    if (first * 4 + w < a.batch) load(first * 4 + w);
+    for (int64_t row = first * 4 + w; row < a.batch; row += step * 4) {
+        raw rx[P], rz[P], rd[P];
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+            rx[c] = next.x[c];
+            rz[c] = next.z[c];
+            rd[c] = next.d[c];
+        }
+        if (row + step * 4 < a.batch) load(row + step * 4);
         float x[P][V];
 #pragma unroll
         for (int c = 0; c < P; ++c) unpack<T, V>(rx[c], x[c]);
@@ -165,7 +178,7 @@ template <typename T, int V, int P, int L, bool BWD> __global__ __launch_bounds_
                     const float d = in[c] ? x[c][i] - mean : 0.0f;
                     s = fmaf(d, d, s);
                 }
-            rstd = 1.0f / sqrtf(fmaf(wave_fold<L>(s, AddOp()), inv, a.eps));
+            rstd = rsqrtf(fmaf(wave_fold<L>(s, AddOp()), inv, a.eps));
             if (lane % L == 0 && group < a.groups) {
                 if (a.mean) a.mean[row * a.groups + group] = mean;
                 if (a.rstd) a.rstd[row * a.groups + group] = rstd;
@@ -239,266 +252,476 @@ template <typename T, int V, int P, int L, bool BWD> __global__ __launch_bounds_
 // ------------------------------------------------------ many rows to a statistic
 // A block is up to 256 vectors of V channels of a row (whole groups, or a part of
 // one); a workgroup takes one run of rows of one block.
+// Runs are cut for as many workgroups as the CUs hold at once: four of 8 waves a CU in 64
+// registers a lane, two in the 128 that the gradient of wide vectors needs.
+constexpr int kRunGroups = 1024;
+constexpr int grad_waves(int V) { return V > 2 ? 4 : 8; }
+constexpr int grad_groups(int V) { return 128 * grad_waves(V); }
+constexpr int kRunThreads = 512, kRunWaves = kRunThreads / 64, kLanes = 256;
 struct Runs {
-    int64_t runs, per;            // of a batch entry; rows of a run
-    int64_t blocks;               // of a row
+    int64_t per;                  // rows of a run
+    int runs;                     // of a batch entry
+    int blocks;                   // of a row
     int bc;                       // channels of a block
     int per_group;                // blocks of a group where one is wider than a block, else 1
-    int64_t total;                // workgroups' worth of work
+    int D;                        // channels of a group
+    bool whole;                   // a run is a whole batch entry, and fits the workgroup's registers
 };
-// channels of a block: as many whole groups as 256 lanes hold, or an even part of a group
-Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V) {
-    const int64_t D = dim / groups, most = static_cast<int64_t>(kThreads) * V;
+// Whole entries: a thread holds up to kHeld vectors of x (and z), the gradient half as
+// many (beside dy's, and the sums), and a block is the fewest groups that are eight
+// vectors wide (128 bytes at full width: a cache line).
+constexpr int kHeld = 8, kHeldGrad = 4;
+Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V, int held, int target) {
+    const int D = static_cast<int>(dim / groups), most = kLanes * V;
     Runs r{};
+    r.D = D;
+    r.per_group = 1;
+    const int64_t want = (8 * V + D - 1) / D, few = want < groups ? want : groups, few_lanes = few * D / V;
+    if (few_lanes <= kLanes && rows <= kRunThreads / few_lanes * held) {
+        r.bc = static_cast<int>(few * D);
+        r.blocks = static_cast<int>((groups + few - 1) / few);
+        r.runs = 1;
+        r.per = rows;
+        r.whole = true;
+        return r;
+    }
     if (D <= most) {
         r.bc = static_cast<int>(most / D * D < dim ? most / D * D : dim);
-        r.per_group = 1;
-        r.blocks = (dim + r.bc - 1) / r.bc;
+        r.blocks = static_cast<int>((dim + r.bc - 1) / r.bc);
     } else {
-        r.per_group = static_cast<int>((D + most - 1) / most);
-        r.bc = static_cast<int>(most);
-        r.blocks = groups * r.per_group;
+        r.per_group = (D + most - 1) / most;
+        r.bc = most;
+        r.blocks = static_cast<int>(groups * r.per_group);
     }
-    const int64_t lanes = (r.bc + V - 1) / V, ty = kThreads / lanes;
-    int64_t n = kRunGroups / (batch * r.blocks > 0 ? batch * r.blocks : 1);
+    const int64_t lanes = (r.bc + V - 1) / V, ty = kRunThreads / lanes;
+    int64_t n = target / (batch * r.blocks > 0 ? batch * r.blocks : 1);
     const int64_t most_runs = (rows + 4 * ty - 1) / (4 * ty);
     n = n < 1 ? 1 : (n > most_runs ? most_runs : n);
     r.per = (rows + n - 1) / n;
-    r.runs = r.per > 0 ? (rows + r.per - 1) / r.per : 0;
-    r.total = batch * r.runs * r.blocks;
+    r.runs = r.per > 0 ? static_cast<int>((rows + r.per - 1) / r.per) : 0;
     return r;
 }
 // where a workgroup's item lies and what a thread has of it
 struct Item {
-    int64_t n, run, block, row0, row1;
+    int64_t row0, rows;                    // the run's first row (of all batch entries'), its rows
+    int run, block;
     int lanes, ty_count, tx, ty, ch;       // lanes of a row, rows at a time, the thread's place, its first channel
-    int64_t group;                         // of the thread's channels
+    int groups, dv, q;                     // groups of the block, lanes of each, the thread's
+    int slot, group;                       // the first of the block's partial sums; the thread's group
     bool in;
 };
-template <int V> __device__ __forceinline__ Item item_of(const GroupNormArgs &a, const Runs &r, int64_t id) {
+template <int V> __device__ __forceinline__ Item item_of(const GroupNormArgs &a, const Runs &r, int64_t n) {
     Item t;
+    const int dim = static_cast<int>(a.dim), id = static_cast<int>(blockIdx.x);
     t.block = id % r.blocks;
-    t.run = id / r.blocks % r.runs;
-    t.n = id / r.blocks / r.runs;
+    t.run = id / r.blocks;
     t.row0 = t.run * r.per;
-    t.row1 = t.row0 + r.per < a.rows ? t.row0 + r.per : a.rows;
-    const int64_t D = a.dim / a.groups;
-    int64_t c0 = t.block * r.bc, c1 = c0 + r.bc < a.dim ? c0 + r.bc : a.dim;
+    t.rows = t.row0 + r.per < a.rows ? r.per : a.rows - t.row0;
+    t.row0 += n * a.rows;
+    int c0 = t.block * r.bc, c1 = c0 + r.bc < dim ? c0 + r.bc : dim;
+    t.slot = t.block * (r.bc / r.D);
     if (r.per_group > 1) {
-        const int64_t g = t.block / r.per_group;
-        c0 = g * D + t.block % r.per_group * r.bc;
-        c1 = c0 + r.bc < (g + 1) * D ? c0 + r.bc : (g + 1) * D;
+        const int g = t.block / r.per_group;
+        c0 = g * r.D + t.block % r.per_group * r.bc;
+        c1 = c0 + r.bc < (g + 1) * r.D ? c0 + r.bc : (g + 1) * r.D;
+        t.slot = t.block;
     }
-    t.lanes = static_cast<int>((c1 - c0) / V);
-    t.ty_count = kThreads / t.lanes;
-    t.tx = threadIdx.x % t.lanes;
-    t.ty = threadIdx.x / t.lanes;
+    t.lanes = (c1 - c0) / V;
+    t.ty_count = kRunThreads / t.lanes;
+    t.tx = static_cast<int>(threadIdx.x) % t.lanes;
+    t.ty = static_cast<int>(threadIdx.x) / t.lanes;
     t.in = t.ty < t.ty_count;
-    t.ch = static_cast<int>(c0) + t.tx * V;
-    t.group = t.ch / D;
+    t.ch = c0 + t.tx * V;
+    t.dv = r.per_group > 1 ? t.lanes : r.D / V;
+    t.groups = t.lanes / t.dv;
+    t.q = t.tx / t.dv;
+    t.group = t.ch / r.D;
     return t;
 }
+// A thread's vectors of a tensor: its first row's, rows apart by `step` elements
+template <typename T> struct Walk {
+    T *p;
+    int64_t step;
+    __device__ __forceinline__ Walk(void *base, int64_t ld, const Item &t)
+        : p(static_cast<T *>(base) + (t.row0 + t.ty) * ld + t.ch), step(t.ty_count * ld) {}
+    __device__ __forceinline__ Walk(const void *base, int64_t ld, const Item &t) : Walk(const_cast<void *>(base), ld, t) {}
+    __device__ __forceinline__ T *next() {
+        T *const q = p;
+        p += step;
+        return q;
+    }
+};
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
     return v;
 }
+template <int V> __device__ __forceinline__ void params_of(const GroupNormArgs &a, int ch, Affine (&p)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = {a.weight ? a.weight[ch + i] : 1.0f, a.bias ? a.bias[ch + i] : 0.0f};
+}
 
-// sums of x and x^2 of each run and group (part of a group): part[(n, run), block's groups]
-template <typename T, int V> __global__ __launch_bounds__(kThreads) void group_stats_kernel(GroupNormArgs a, Runs r, double *part) {
-    __shared__ double s1[kThreads], s2[kThreads];
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-    const int64_t slots = a.groups * r.per_group;
-    const int D = static_cast<int>(a.dim / a.groups);
-    for (int64_t id = blockIdx.x; id < r.total; id += gridDim.x) {
-        const Item t = item_of<V>(a, r, id);
+// Two sums over the threads of each group of a block, in a fixed order: a wave per
+// group adds its lanes of every row of threads.
+struct Totals {
+    double s1[kRunThreads], s2[kRunThreads], t1[kLanes], t2[kLanes];
+};
+__device__ __forceinline__ void group_totals(Totals &m, const Item &t, double u, double v) {
+    const int lane = threadIdx.x % 64;
+    __syncthreads();
+    m.s1[threadIdx.x] = u;
+    m.s2[threadIdx.x] = v;
+    __syncthreads();
+    for (int q = threadIdx.x / 64; q < t.groups; q += kRunWaves) {
+        double x = 0.0, y = 0.0;
+        for (int e = lane; e < t.dv * t.ty_count; e += 64) {
+            const int o = e / t.dv * t.lanes + q * t.dv + e % t.dv;
+            x += m.s1[o];
+            y += m.s2[o];
+        }
+        x = wave_sum(x);
+        y = wave_sum(y);
+        if (lane == 0) {
+            m.t1[q] = x;
+            m.t2[q] = y;
+        }
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void put_totals(const Totals &m, const GroupNormArgs &a, const Runs &r, const Item &t, int64_t n, double *part) {
+    const int q = static_cast<int>(threadIdx.x);
+    if (q >= t.groups) return;
+    double *const o = part + 2 * ((n * r.runs + t.run) * a.groups * r.per_group + t.slot + q);
+    o[0] = m.t1[q];
+    o[1] = m.t2[q];
+}
+// The runs' sums of the block's groups, added by each workgroup that needs them for
+// itself: a launch less, for a few KB out of the L2.  Up to 64 lanes to a group.
+__device__ __forceinline__ void add_runs(Totals &m, const GroupNormArgs &a, const Runs &r, const Item &t, int64_t n, const double *part) {
+    int lg = 64;
+    while (lg * t.groups > kRunThreads) lg /= 2;
+    const int q = static_cast<int>(threadIdx.x) / lg, l = static_cast<int>(threadIdx.x) % lg, row = static_cast<int>(a.groups) * r.per_group;
+    double x = 0.0, y = 0.0;
+    if (q < t.groups) {
+        const double *const p = part + 2 * (n * r.runs * row + (r.per_group > 1 ? t.block / r.per_group * r.per_group : t.slot + q));
+        if (r.per_group == 1) {
+#pragma unroll 4
+            for (int e = l; e < r.runs; e += lg) {
+                x += p[2ll * e * row];
+                y += p[2ll * e * row + 1];
+            }
+        } else {
+            for (int e = l; e < r.runs * r.per_group; e += lg) {
+                const double *const o = p + 2ll * (e / r.per_group * row + e % r.per_group);
+                x += o[0];
+                y += o[1];
+            }
+        }
+    }
+    for (int o = lg / 2; o > 0; o /= 2) {
+        x += __shfl_xor(x, o);
+        y += __shfl_xor(y, o);
+    }
+    __syncthreads();
+    if (l == 0 && q < t.groups) {
+        m.t1[q] = x;
+        m.t2[q] = y;
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void put_stats(const GroupNormArgs &a, const Runs &r, const Item &t, int64_t n, float mean, float rstd) {
+    if (t.run != 0 || t.ty != 0 || t.tx % t.dv != 0 || (r.per_group > 1 && t.block % r.per_group != 0)) return;
+    if (a.mean) a.mean[n * a.groups + t.group] = mean;
+    if (a.rstd) a.rstd[n * a.groups + t.group] = rstd;
+}
+
+// Sums of x - x0 and its square over a run, x0 the thread's first value, in fp32 over
+// a vector and fp64 beyond, then of x and x^2: x - x0 is about as large as the group's
+// spread, so a mean far from 0 costs the variance nothing.  (All in fp64 the pass took
+// 35 us over 134 MB instead of 28.)
+template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void group_stats_kernel(GroupNormArgs a, Runs r, double *part) {
+    __shared__ Totals m;
+    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
+        const Item t = item_of<V>(a, r, n);
         double u = 0.0, v = 0.0;
-        if (t.in) {
-            const T *const p = static_cast<const T *>(a.x) + t.n * a.rows * a.ldx + t.ch;
-#pragma unroll 4
-            for (int64_t row = t.row0 + t.ty; row < t.row1; row += t.ty_count) {
-                float x[V];
-                unpack<T, V>(load_vec<T, V>(p + row * a.ldx), x);
+        if (t.in && t.ty < t.rows) {
+            Walk<const T> px(a.x, a.ldx, t);
+            const T *const first = px.p;
+            const float x0 = to_f32(*first);
+            for (int64_t left = t.rows - t.ty; left > 0; left -= 4 * t.ty_count) {
+                typename Vec<T, V>::raw q[4];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const double d = x[i];
-                    u += d;
-                    v = fma(d, d, v);
+                for (int j = 0; j < 4; ++j) {
+                    const T *const at = px.next();
+                    q[j] = load_vec<T, V>(left > j * t.ty_count ? at : first);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float x[V], su = 0.0f, sv = 0.0f;
+                    unpack<T, V>(q[j], x);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float d = left > j * t.ty_count ? x[i] - x0 : 0.0f;
+                        su += d;
+                        sv = fmaf(d, d, sv);
+                    }
+                    u += su;
+                    v += sv;
                 }
             }
+            const double count = static_cast<double>((t.rows - t.ty + t.ty_count - 1) / t.ty_count * V), z = x0;
+            v += z * (2.0 * u + count * z);
+            u += count * z;
         }
-        __syncthreads();
-        s1[threadIdx.x] = u;
-        s2[threadIdx.x] = v;
-        __syncthreads();
-        // a wave per group of the block: its lanes of every row of threads
-        const int dv = r.per_group > 1 ? t.lanes : D / V, ngr = t.lanes / dv;
-        for (int q = w; q < ngr; q += 4) {
-            double x = 0.0, y = 0.0;
-            for (int e = lane; e < dv * t.ty_count; e += 64) {
-                const int o = e / dv * t.lanes + q * dv + e % dv;
-                x += s1[o];
-                y += s2[o];
-            }
-            x = wave_sum(x);
-            y = wave_sum(y);
-            if (lane == 0) {
-                const int64_t slot = r.per_group > 1 ? t.block : t.block * (r.bc / D) + q;
-                double *const o = part + 2 * ((t.n * r.runs + t.run) * slots + slot);
-                o[0] = x;
-                o[1] = y;
-            }
-        }
+        group_totals(m, t, u, v);
+        put_totals(m, a, r, t, n, part);
     }
 }
-// mean and rstd of a group, a wave each
-__global__ __launch_bounds__(kThreads) void group_stats_end_kernel(GroupNormArgs a, Runs r, const double *part, float *mean, float *rstd) {
-    const int lane = threadIdx.x % 64;
+template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribute__((amdgpu_waves_per_eu(8, 8))) void group_apply_kernel(GroupNormArgs a, Runs r, const double *part) {
+    __shared__ Totals m;
+    const bool act = a.silu != 0, gate = a.z != nullptr;
     const double inv = 1.0 / (static_cast<double>(a.rows) * static_cast<double>(a.dim / a.groups));
-    for (int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64; id < a.batch * a.groups; id += gridDim.x * 4ll) {
-        const int64_t n = id / a.groups, g = id % a.groups;
-        double x = 0.0, y = 0.0;
-        for (int64_t e = lane; e < r.runs * r.per_group; e += 64) {
-            const double *const o = part + 2 * (((n * r.runs + e / r.per_group) * a.groups + g) * r.per_group + e % r.per_group);
-            x += o[0];
-            y += o[1];
-        }
-        x = wave_sum(x) * inv;
-        y = wave_sum(y) * inv - x * x;
-        if (lane == 0) {
-            const float rs = static_cast<float>(1.0 / sqrt((y < 0.0 ? 0.0 : y) + static_cast<double>(a.eps)));
-            mean[id] = static_cast<float>(x);
-            rstd[id] = rs;
-            if (a.mean && a.mean != mean) a.mean[id] = static_cast<float>(x);
-            if (a.rstd && a.rstd != rstd) a.rstd[id] = rs;
-        }
-    }
-}
-template <typename T, int V>
-__global__ __launch_bounds__(kThreads) void group_apply_kernel(GroupNormArgs a, Runs r, const float *mean, const float *rstd) {
-    const bool act = a.silu != 0, gate = a.z != nullptr;
-    for (int64_t id = blockIdx.x; id < r.total; id += gridDim.x) {
-        const Item t = item_of<V>(a, r, id);
+    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
+        const Item t = item_of<V>(a, r, n);
+        add_runs(m, a, r, t, n, part);
         if (!t.in) continue;
+        const double mu = m.t1[t.q] * inv, var = m.t2[t.q] * inv - mu * mu;
+        const float mean = static_cast<float>(mu);
+        const float rstd = static_cast<float>(1.0 / sqrt((var < 0.0 ? 0.0 : var) + static_cast<double>(a.eps)));
+        put_stats(a, r, t, n, mean, rstd);
         Affine p[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = {a.weight ? a.weight[t.ch + i] : 1.0f, a.bias ? a.bias[t.ch + i] : 0.0f};
-        const float m = mean[t.n * a.groups + t.group], s = rstd[t.n * a.groups + t.group];
-        const T *const px = static_cast<const T *>(a.x) + t.n * a.rows * a.ldx + t.ch;
-        const T *const pz = static_cast<const T *>(a.z) + t.n * a.rows * a.ldz + t.ch;
-        T *const py = static_cast<T *>(a.y) + t.n * a.rows * a.dim + t.ch;
-#pragma unroll 4
-        for (int64_t row = t.row0 + t.ty; row < t.row1; row += t.ty_count) {
+        params_of<V>(a, t.ch, p);
+        Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t);
+        Walk<T> py(a.y, a.dim, t);
+#pragma unroll 2
+        for (int64_t left = t.rows - t.ty; left > 0; left -= t.ty_count) {
             float x[V], z[V] = {};
-            unpack<T, V>(load_vec<T, V>(px + row * a.ldx), x);
-            if (gate) unpack<T, V>(load_vec<T, V>(pz + row * a.ldz), z);
+            unpack<T, V>(load_vec<T, V>(px.next()), x);
+            if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = forward((x[i] - m) * s, p[i], act, gate, z[i]);
-            store_vec<T, V>(py + row * a.dim, x);
+            for (int i = 0; i < V; ++i) x[i] = forward((x[i] - mean) * rstd, p[i], act, gate, z[i]);
+            store_vec<T, V>(py.next(), x);
         }
     }
 }
-
-// the gradient's sums of da and da n of each run and channel: part[(n, run), 2, dim]
-template <typename T, int V> __global__ __launch_bounds__(kThreads) void group_sums_kernel(GroupNormBwdArgs b, Runs r, float *part) {
-    const GroupNormArgs &a = b.fwd;
-    __shared__ float sA[kThreads][V + 1], sB[kThreads][V + 1];
+// Whole batch entries in registers: one launch, one pass
+template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void group_whole_kernel(GroupNormArgs a, Runs r) {
+    __shared__ Totals m;
     const bool act = a.silu != 0, gate = a.z != nullptr;
-    for (int64_t id = blockIdx.x; id < r.total; id += gridDim.x) {
-        const Item t = item_of<V>(a, r, id);
-        float u[V] = {}, v[V] = {};
-        if (t.in) {
-            Affine p[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) p[i] = {a.weight ? a.weight[t.ch + i] : 1.0f, a.bias ? a.bias[t.ch + i] : 0.0f};
-            const float m = a.mean[t.n * a.groups + t.group], s = a.rstd[t.n * a.groups + t.group];
-            const T *const px = static_cast<const T *>(a.x) + t.n * a.rows * a.ldx + t.ch;
-            const T *const pz = static_cast<const T *>(a.z) + t.n * a.rows * a.ldz + t.ch;
-            const T *const pd = static_cast<const T *>(b.dy) + t.n * a.rows * a.dim + t.ch;
-#pragma unroll 4
-            for (int64_t row = t.row0 + t.ty; row < t.row1; row += t.ty_count) {
-                float x[V], z[V] = {}, d[V], dz = 0.0f;
-                unpack<T, V>(load_vec<T, V>(px + row * a.ldx), x);
-                unpack<T, V>(load_vec<T, V>(pd + row * a.dim), d);
-                if (gate) unpack<T, V>(load_vec<T, V>(pz + row * a.ldz), z);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float n = (x[i] - m) * s, da = backward(n, d[i], p[i], act, gate, z[i], dz);
-                    u[i] += da;
-                    v[i] = fmaf(da, n, v[i]);
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sA[threadIdx.x][i] = u[i];
-            sB[threadIdx.x][i] = v[i];
-        }
-        __syncthreads();
-        float *const o = part + (t.n * r.runs + t.run) * 2 * a.dim + (t.ch - t.tx * V);
-        for (int c = threadIdx.x; c < t.lanes * V; c += kThreads) {
-            float x = 0.0f, y = 0.0f;
-            for (int q = 0; q < t.ty_count; ++q) {
-                x += sA[q * t.lanes + c / V][c % V];
-                y += sB[q * t.lanes + c / V][c % V];
-            }
-            o[c] = x;
-            o[a.dim + c] = y;
-        }
-    }
-}
-// mean(w da) and mean(w da n) of a group, a wave each
-__global__ __launch_bounds__(kThreads) void group_sums_end_kernel(GroupNormArgs a, int64_t runs, const float *part, float *coef) {
-    const int lane = threadIdx.x % 64;
-    const int64_t D = a.dim / a.groups;
-    const double inv = 1.0 / (static_cast<double>(a.rows) * static_cast<double>(D));
-    for (int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64; id < a.batch * a.groups; id += gridDim.x * 4ll) {
-        const int64_t n = id / a.groups, g = id % a.groups;
-        double x = 0.0, y = 0.0;
-        for (int64_t e = lane; e < runs * D; e += 64) {
-            const int64_t c = g * D + e % D;
-            const float *const o = part + (n * runs + e / D) * 2 * a.dim + c;
-            const double wc = a.weight ? a.weight[c] : 1.0f;
-            x += wc * o[0];
-            y += wc * o[a.dim];
-        }
-        x = wave_sum(x) * inv;
-        y = wave_sum(y) * inv;
-        if (lane == 0) {
-            coef[2 * id] = static_cast<float>(x);
-            coef[2 * id + 1] = static_cast<float>(y);
-        }
-    }
-}
-template <typename T, int V> __global__ __launch_bounds__(kThreads) void group_grad_kernel(GroupNormBwdArgs b, Runs r, const float *coef) {
-    const GroupNormArgs &a = b.fwd;
-    const bool act = a.silu != 0, gate = a.z != nullptr;
-    for (int64_t id = blockIdx.x; id < r.total; id += gridDim.x) {
-        const Item t = item_of<V>(a, r, id);
-        if (!t.in) continue;
+    const double inv = 1.0 / (static_cast<double>(a.rows) * static_cast<double>(a.dim / a.groups));
+    using raw = typename Vec<T, V>::raw;
+    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
+        const Item t = item_of<V>(a, r, n);
+        Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t);
+        Walk<T> py(a.y, a.dim, t);
+        raw qx[kHeld], qz[kHeld];
         Affine p[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = {a.weight ? a.weight[t.ch + i] : 1.0f, a.bias ? a.bias[t.ch + i] : 0.0f};
-        const int64_t ng = t.n * a.groups + t.group;
-        const float m = a.mean[ng], s = a.rstd[ng], m1 = coef[2 * ng], m2 = coef[2 * ng + 1];
-        const int64_t row = t.n * a.rows;
-        const T *const px = static_cast<const T *>(a.x) + row * a.ldx + t.ch, *const pz = static_cast<const T *>(a.z) + row * a.ldz + t.ch;
-        const T *const pd = static_cast<const T *>(b.dy) + row * a.dim + t.ch;
-        T *const po = static_cast<T *>(b.dx) + row * a.dim + t.ch, *const pzo = static_cast<T *>(b.dz) + row * a.dim + t.ch;
-#pragma unroll 4
-        for (int64_t q = t.row0 + t.ty; q < t.row1; q += t.ty_count) {
-            float x[V], z[V] = {}, d[V], dz[V];
-            unpack<T, V>(load_vec<T, V>(px + q * a.ldx), x);
-            unpack<T, V>(load_vec<T, V>(pd + q * a.dim), d);
-            if (gate) unpack<T, V>(load_vec<T, V>(pz + q * a.ldz), z);
+        for (int j = 0; j < kHeld; ++j) {
+            const bool in = t.in && t.ty + j * t.ty_count < t.rows;
+            qx[j] = qz[j] = raw{};
+            const T *const ax = px.next(), *const az = pz.next();
+            if (in) qx[j] = load_vec<T, V>(ax);
+            if (in && gate) qz[j] = load_vec<T, V>(az);
+        }
+        params_of<V>(a, t.ch, p);
+        double u = 0.0, v = 0.0;                             // fp32 over a vector, fp64 beyond
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            float x[V], s = 0.0f;
+            unpack<T, V>(qx[j], x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += x[i];
+            u += s;
+        }
+        group_totals(m, t, u, 0.0);
+        const float mean = static_cast<float>(m.t1[t.q] * inv);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            float x[V], s = 0.0f;
+            unpack<T, V>(qx[j], x);
+            const bool in = t.in && t.ty + j * t.ty_count < t.rows;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float n = (x[i] - m) * s, da = backward(n, d[i], p[i], act, gate, z[i], dz[i]);
-                x[i] = s * (da * p[i].w - fmaf(n, m2, m1));
+                const float d = in ? x[i] - mean : 0.0f;
+                s = fmaf(d, d, s);
             }
-            store_vec<T, V>(po + q * a.dim, x);
-            if (gate) store_vec<T, V>(pzo + q * a.dim, dz);
+            v += s;
+        }
+        group_totals(m, t, v, 0.0);
+        const float rstd = static_cast<float>(1.0 / sqrt(m.t1[t.q] * inv + static_cast<double>(a.eps)));
+        if (t.in) put_stats(a, r, t, n, mean, rstd);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            T *const ay = py.next();
+            if (!t.in || t.ty + j * t.ty_count >= t.rows) continue;
+            float x[V], z[V];
+            unpack<T, V>(qx[j], x);
+            unpack<T, V>(qz[j], z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = forward((x[i] - mean) * rstd, p[i], act, gate, z[i]);
+            store_vec<T, V>(ay, x);
+        }
+    }
+}
+
+// Sums over a workgroup's rows of each channel of the block, to o and o + dim
+template <int V> struct ChannelSums {
+    float a[kRunThreads][V + 1], b[kRunThreads][V + 1];
+};
+template <int V> __device__ __forceinline__ void channel_sums(ChannelSums<V> &m, const Item &t, const float (&u)[V], const float (&v)[V], float *o, int64_t dim) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        m.a[threadIdx.x][i] = u[i];
+        m.b[threadIdx.x][i] = v[i];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < t.lanes * V; c += kRunThreads) {
+        float x = 0.0f, y = 0.0f;
+        for (int q = 0; q < t.ty_count; ++q) {
+            x += m.a[q * t.lanes + c / V][c % V];
+            y += m.b[q * t.lanes + c / V][c % V];
+        }
+        o[c] = x;
+        o[dim + c] = y;
+    }
+}
+// A thread's sums of w da and w da n
+template <int V> __device__ __forceinline__ void weighted(const Affine (&p)[V], const float (&u)[V], const float (&v)[V], double &x, double &y) {
+    x = y = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x += static_cast<double>(p[i].w) * u[i];
+        y += static_cast<double>(p[i].w) * v[i];
+    }
+}
+// The gradient's sums of da and da n of each run and channel, (n, run), 2, dim, and of
+// w da and w da n of each run and group
+template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribute__((amdgpu_waves_per_eu(grad_waves(V), grad_waves(V)))) void group_sums_kernel(GroupNormBwdArgs b, Runs r, double *part, float *chan) {
+    const GroupNormArgs &a = b.fwd;
+    __shared__ union { ChannelSums<V> c; Totals t; } m;
+    const bool act = a.silu != 0, gate = a.z != nullptr;
+    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
+        const Item t = item_of<V>(a, r, n);
+        float u[V] = {}, v[V] = {};
+        Affine p[V];
+        params_of<V>(a, t.ch, p);
+        if (t.in) {
+            const float mean = a.mean[n * a.groups + t.group], rstd = a.rstd[n * a.groups + t.group];
+            Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
+#pragma unroll 2
+            for (int64_t left = t.rows - t.ty; left > 0; left -= t.ty_count) {
+                float x[V], z[V] = {}, d[V], dz = 0.0f;
+                unpack<T, V>(load_vec<T, V>(px.next()), x);
+                unpack<T, V>(load_vec<T, V>(pd.next()), d);
+                if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz);
+                    u[i] += da;
+                    v[i] = fmaf(da, nx, v[i]);
+                }
+            }
+        }
+        if (chan) channel_sums<V>(m.c, t, u, v, chan + (n * r.runs + t.run) * 2 * a.dim + (t.ch - t.tx * V), a.dim);
+        double x, y;
+        weighted<V>(p, u, v, x, y);
+        group_totals(m.t, t, x, y);
+        put_totals(m.t, a, r, t, n, part);
+    }
+}
+template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribute__((amdgpu_waves_per_eu(grad_waves(V), grad_waves(V)))) void group_grad_kernel(GroupNormBwdArgs b, Runs r, const double *part) {
+    const GroupNormArgs &a = b.fwd;
+    __shared__ Totals m;
+    const bool act = a.silu != 0, gate = a.z != nullptr;
+    const double inv = 1.0 / (static_cast<double>(a.rows) * static_cast<double>(a.dim / a.groups));
+    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
+        const Item t = item_of<V>(a, r, n);
+        add_runs(m, a, r, t, n, part);
+        if (!t.in) continue;
+        Affine p[V];
+        params_of<V>(a, t.ch, p);
+        const int64_t ng = n * a.groups + t.group;
+        const float mean = a.mean[ng], rstd = a.rstd[ng], m1 = static_cast<float>(m.t1[t.q] * inv), m2 = static_cast<float>(m.t2[t.q] * inv);
+        Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
+        Walk<T> po(b.dx, a.dim, t), pzo(b.dz, a.dim, t);
+#pragma unroll 2
+        for (int64_t left = t.rows - t.ty; left > 0; left -= t.ty_count) {
+            float x[V], z[V] = {}, d[V], dz[V];
+            unpack<T, V>(load_vec<T, V>(px.next()), x);
+            unpack<T, V>(load_vec<T, V>(pd.next()), d);
+            if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz[i]);
+                x[i] = rstd * (da * p[i].w - fmaf(nx, m2, m1));
+            }
+            store_vec<T, V>(po.next(), x);
+            if (gate) store_vec<T, V>(pzo.next(), dz);
+        }
+    }
+}
+// The gradient of whole batch entries in registers; the channels' sums are (n, 2, dim)
+template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void group_whole_grad_kernel(GroupNormBwdArgs b, Runs r, float *chan) {
+    const GroupNormArgs &a = b.fwd;
+    __shared__ union { ChannelSums<V> c; Totals t; } m;
+    const bool act = a.silu != 0, gate = a.z != nullptr;
+    const double inv = 1.0 / (static_cast<double>(a.rows) * static_cast<double>(a.dim / a.groups));
+    using raw = typename Vec<T, V>::raw;
+    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
+        const Item t = item_of<V>(a, r, n);
+        const int64_t ng = n * a.groups + t.group;
+        Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
+        Walk<T> po(b.dx, a.dim, t), pzo(b.dz, a.dim, t);
+        raw qx[kHeldGrad], qz[kHeldGrad], qd[kHeldGrad];
+        Affine p[V];
+#pragma unroll
+        for (int j = 0; j < kHeldGrad; ++j) {
+            const bool in = t.in && t.ty + j * t.ty_count < t.rows;
+            qx[j] = qz[j] = qd[j] = raw{};
+            const T *const ax = px.next(), *const az = pz.next(), *const ad = pd.next();
+            if (in) qx[j] = load_vec<T, V>(ax);
+            if (in) qd[j] = load_vec<T, V>(ad);
+            if (in && gate) qz[j] = load_vec<T, V>(az);
+        }
+        params_of<V>(a, t.ch, p);
+        const float mean = a.mean[ng], rstd = a.rstd[ng];
+        float u[V] = {}, v[V] = {};
+#pragma unroll
+        for (int j = 0; j < kHeldGrad; ++j) {
+            float x[V], z[V], d[V], dz = 0.0f;
+            unpack<T, V>(qx[j], x);
+            unpack<T, V>(qd[j], d);
+            unpack<T, V>(qz[j], z);
+            const bool in = t.in && t.ty + j * t.ty_count < t.rows;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float nx = in ? (x[i] - mean) * rstd : 0.0f, da = in ? backward(nx, d[i], p[i], act, gate, z[i], dz) : 0.0f;
+                u[i] += da;
+                v[i] = fmaf(da, nx, v[i]);
+            }
+        }
+        if (chan) channel_sums<V>(m.c, t, u, v, chan + n * 2 * a.dim + (t.ch - t.tx * V), a.dim);
+        double s1, s2;
+        weighted<V>(p, u, v, s1, s2);
+        group_totals(m.t, t, s1, s2);
+        const float m1 = static_cast<float>(m.t.t1[t.q] * inv), m2 = static_cast<float>(m.t.t2[t.q] * inv);
+#pragma unroll
+        for (int j = 0; j < kHeldGrad; ++j) {
+            T *const ao = po.next(), *const az = pzo.next();
+            if (!t.in || t.ty + j * t.ty_count >= t.rows) continue;
+            float x[V], z[V], d[V], dz[V];
+            unpack<T, V>(qx[j], x);
+            unpack<T, V>(qd[j], d);
+            unpack<T, V>(qz[j], z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz[i]);
+                x[i] = rstd * (da * p[i].w - fmaf(nx, m2, m1));
+            }
+            store_vec<T, V>(ao, x);
+            if (gate) store_vec<T, V>(az, dz);
         }
     }
 }
@@ -571,7 +794,11 @@ template <typename T, int V, bool BWD> hipError_t run_rows_of(const GroupNormBwd
     if (n <= 128) return run_rows<T, V, 2, 64, BWD>(b, s);
     return run_rows<T, V, 4, 64, BWD>(b, s);
 }
-unsigned grid_of(int64_t items) { return static_cast<unsigned>(items < (1 << 20) ? items : (1 << 20)); }
+size_t chan_bytes(int64_t batch, const Runs &r, int64_t dim) { return align256(static_cast<size_t>(batch * r.runs) * 2 * dim * 4); }
+size_t part_bytes(int64_t batch, const Runs &r, int64_t groups) {
+    return r.whole ? 0 : align256(static_cast<size_t>(batch * r.runs * groups * r.per_group) * 16);
+}
+dim3 grid_of(int64_t batch, const Runs &r) { return dim3(static_cast<unsigned>(r.blocks * r.runs), static_cast<unsigned>(batch < 65535 ? batch : 65535)); }
 
 template <typename T, int V> hipError_t run_fwd(const GroupNormArgs &a, hipStream_t s) {
     if (row_form(a.rows, a.dim, a.groups, V)) {
@@ -579,34 +806,34 @@ template <typename T, int V> hipError_t run_fwd(const GroupNormArgs &a, hipStrea
         b.fwd = a;
         return run_rows_of<T, V, false>(b, s);
     }
-    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V);
-    char *const ws = static_cast<char *>(a.workspace);
-    const size_t ng = static_cast<size_t>(a.batch * a.groups);
-    float *const mean = reinterpret_cast<float *>(ws), *const rstd = reinterpret_cast<float *>(ws + align256(ng * 4));
-    double *const part = reinterpret_cast<double *>(ws + 2 * align256(ng * 4));
-    hipLaunchKernelGGL((group_stats_kernel<T, V>), dim3(grid_of(r.total)), dim3(kThreads), 0, s, a, r, part);
+    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeld, kRunGroups);
+    if (r.whole) {
+        hipLaunchKernelGGL((group_whole_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, a, r);
+        return hipGetLastError();
+    }
+    double *const part = static_cast<double *>(a.workspace);
+    hipLaunchKernelGGL((group_stats_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, a, r, part);
     if (hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL(group_stats_end_kernel, dim3(grid_of((a.batch * a.groups + 3) / 4)), dim3(kThreads), 0, s, a, r, part, mean, rstd);
-    if (hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL((group_apply_kernel<T, V>), dim3(grid_of(r.total)), dim3(kThreads), 0, s, a, r, mean, rstd);
+    hipLaunchKernelGGL((group_apply_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, a, r, part);
     return hipGetLastError();
 }
 template <typename T, int V> hipError_t run_bwd(const GroupNormBwdArgs &b, hipStream_t s) {
     const GroupNormArgs &a = b.fwd;
     if (row_form(a.rows, a.dim, a.groups, V)) return run_rows_of<T, V, true>(b, s);
-    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V);
-    char *const ws = static_cast<char *>(a.workspace);
-    float *const coef = reinterpret_cast<float *>(ws), *const part = reinterpret_cast<float *>(ws + align256(a.batch * a.groups * 8));
-    hipLaunchKernelGGL((group_sums_kernel<T, V>), dim3(grid_of(r.total)), dim3(kThreads), 0, s, b, r, part);
+    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeldGrad, grad_groups(V));
+    const bool params = b.dweight || b.dbias;
+    float *const chan = params ? static_cast<float *>(a.workspace) : nullptr;
+    double *const part = reinterpret_cast<double *>(static_cast<char *>(a.workspace) + chan_bytes(a.batch, r, a.dim));
+    if (r.whole) hipLaunchKernelGGL((group_whole_grad_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, b, r, chan);
+    else hipLaunchKernelGGL((group_sums_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, b, r, part, chan);
     if (hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL(group_sums_end_kernel, dim3(grid_of((a.batch * a.groups + 3) / 4)), dim3(kThreads), 0, s, a, r.runs, part, coef);
-    if (hipError_t e = hipGetLastError()) return e;
-    if (b.dweight || b.dbias) {
-        hipLaunchKernelGGL(group_params_kernel, dim3(static_cast<unsigned>((2 * a.dim + 15) / 16)), dim3(1024), 0, s, part, b.dbias, b.dweight,
-                           a.batch * r.runs, a.dim);
+    if (!r.whole) {
+        hipLaunchKernelGGL((group_grad_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, b, r, part);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    hipLaunchKernelGGL((group_grad_kernel<T, V>), dim3(grid_of(r.total)), dim3(kThreads), 0, s, b, r, coef);
+    if (!params) return hipSuccess;
+    hipLaunchKernelGGL(group_params_kernel, dim3(static_cast<unsigned>((2 * a.dim + 15) / 16)), dim3(1024), 0, s, chan, b.dbias, b.dweight,
+                       a.batch * r.runs, a.dim);
     return hipGetLastError();
 }
 
@@ -615,11 +842,9 @@ template <typename T, int V> hipError_t run_bwd(const GroupNormBwdArgs &b, hipSt
 // The largest over the widths that a call may choose.
 size_t group_norm_workspace(int64_t batch, int64_t rows, int64_t dim, int64_t groups) {
     size_t most = 0;
-    const size_t ng = static_cast<size_t>(batch * groups);
     for (int v = 1; v <= 8; v *= 2) {
-        if (row_form(rows, dim, groups, v)) continue;
-        const Runs r = runs_of(batch, rows, dim, groups, v);
-        const size_t n = 2 * align256(ng * 4) + align256(static_cast<size_t>(batch * r.runs * groups * r.per_group) * 16);
+        if (dim / groups % v || row_form(rows, dim, groups, v)) continue;
+        const size_t n = part_bytes(batch, runs_of(batch, rows, dim, groups, v, kHeld, kRunGroups), groups);
         most = n > most ? n : most;
     }
     return most;
@@ -627,12 +852,13 @@ size_t group_norm_workspace(int64_t batch, int64_t rows, int64_t dim, int64_t gr
 size_t group_norm_bwd_workspace(int64_t batch, int64_t rows, int64_t dim, int64_t groups) {
     size_t most = 0;
     for (int v = 1; v <= 8; v *= 2) {
+        if (dim / groups % v) continue;
         size_t n;
         if (row_form(rows, dim, groups, v)) {
             n = static_cast<size_t>(row_first(batch, (groups + 7) / 8)) * 2 * dim * 4;      // at most 8 groups to a wave
         } else {
-            const Runs r = runs_of(batch, rows, dim, groups, v);
-            n = align256(static_cast<size_t>(batch * groups) * 8) + static_cast<size_t>(batch * r.runs) * 2 * dim * 4;
+            const Runs r = runs_of(batch, rows, dim, groups, v, kHeldGrad, grad_groups(v));
+            n = chan_bytes(batch, r, dim) + part_bytes(batch, r, groups);
         }
         most = n > most ? n : most;
     }

@@ -3,7 +3,8 @@
 Tolerances.  mean and rstd: with one row a group's sums are fp32, at most
 D / 64 + 12 additions on any path, so the mean is off by (D / 64 + 12) U of
 mean|x|, and rstd by as much relatively, plus 8 U of its own operations; over
-several rows the sums are fp64 and one rounding is left.  An element: (x - mean)
+several rows up to 8 neighbouring values are added in fp32, the rest in fp64: 8 U of
+mean|x| and two roundings.  An element: (x - mean)
 rstd is off by U (|x| + |mean|) rstd for the difference, the statistics' errors and
 4 roundings; the activation multiplies that by its slope (at most 1.1, twice with
 the gate) and adds its own error, an exponential's, a sum's and a quotient's:
@@ -47,7 +48,7 @@ def bound_of(x, mean, rstd, groups, w, b, z, silu):
     N, R, C = x.shape
     D = C // groups
     rep = lambda t: np.repeat(t, D, axis=-1)[:, None]
-    k = (D / 64.0 + 12.0) if R == 1 else 2.0
+    k = (D / 64.0 + 12.0) if R == 1 else 10.0
     ax = np.abs(x).reshape(N, R, groups, D).mean((1, 3))
     n = (x - rep(mean)) * rep(rstd)
     en = EPS * ((np.abs(x) + np.abs(rep(mean)) + k * rep(ax)) * rep(rstd) + (2.0 * k + 12.0) * np.abs(n))
@@ -74,7 +75,7 @@ def check(ops, t, groups, silu=False, eps=1e-5, seed=40, shape=None, grads=True)
     xo, zo, w, b = f(x), f(t["z"]), U.f64(t["weight"]), U.f64(t["bias"])
     yo, mo, ro = M.group_norm(xo, groups, w, b, zo, silu, eps)
     D = C // groups
-    k = (D / 64.0 + 12.0) if R == 1 else 2.0
+    k = (D / 64.0 + 12.0) if R == 1 else 10.0
     ax = np.abs(xo).reshape(N, R, groups, D).mean((1, 3))
     assert (np.abs(U.f64(mean) - mo) <= k * EPS * ax + 2.0 ** -126).all()
     # rstd: of the sum of squares, and the mean's own error enters squared beside eps
@@ -139,7 +140,9 @@ def test_one_row(ops, N, C, G, dtype):
 
 # several rows: one to many runs, groups narrower and wider than a workgroup's lanes
 MAPS = [(1, 2, 8, 1), (2, 3, 24, 3), (3, 196, 96, 8), (1, 1000, 6, 2), (2, 49, 320, 32), (1, 64, 2304, 4), (4, 9, 33, 11), (2, 777, 192, 32),
-        (1, 5, 5000, 1), (1, 4096, 64, 4), (40, 16, 16, 16), (2, 30, 9000, 3), (1, 3, 4098, 2)]
+        (1, 5, 5000, 1), (1, 4096, 64, 4), (40, 16, 16, 16), (2, 30, 9000, 3), (1, 3, 4098, 2),
+        # around the most rows of a batch entry whose groups stay in registers, forward and gradient
+        (2, 256, 64, 4), (1, 257, 64, 4), (2, 512, 64, 8), (1, 513, 64, 8), (3, 600, 20, 2)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -139,7 +139,7 @@ def test_update_refuses(lib, over, code):
 
 def norm_args(**over):
     f = FakeDev()
-    a = dict(x=f(), ldx=24, z=f(), ldz=24, w=f(), b=f(), y=f(), mean=f(), rstd=f(), batch=3, rows=5, dim=24, groups=4, eps=1e-5, silu=1,
+    a = dict(x=f(), ldx=24, z=f(), ldz=24, w=f(), b=f(), y=f(), mean=f(), rstd=f(), batch=3, rows=5000, dim=24, groups=4, eps=1e-5, silu=1,
              io=F32, ws=f(), ws_bytes=64 * MB, dy=f(), dx=f(), dz=f(), dw=f(), db=f())
     a.update(over)
     return a
@@ -188,6 +188,7 @@ def test_norm_overlaps_and_empty(lib):
 def test_norm_sizes(lib):
     for fn in (lib.ssm_group_norm_workspace_bytes, lib.ssm_group_norm_bwd_workspace_bytes):
         assert fn(3, 5, 24, 5) == BAD and fn(-1, 5, 24, 4) == BAD and fn(0, 5, 24, 4) == 0
-        assert 0 < fn(3, 5, 24, 4) < BAD
-    assert lib.ssm_group_norm_workspace_bytes(4096, 1, 24, 4) == 0          # a row's groups stay in registers
+        assert 0 < fn(3, 5000, 24, 4) < BAD
+    for rows in (1, 5):                                                     # the groups stay in registers
+        assert lib.ssm_group_norm_workspace_bytes(4096, rows, 24, 4) == 0
     assert lib.ssm_group_norm_bwd_workspace_bytes(4096, 1, 24, 4) > 0
