@@ -144,7 +144,7 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
         for (int tb = 0; tb < 4; ++tb) {
             const int t = row_index(tb, c), v = v0 + 4 * g;
             store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * es) : kOffNone, T());
-            store4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            stream4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
             const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[32 * (tb / 2) + 8 * g + 4 * (tb % 2)]);
             dY[tb] = dY[tb] * eg * a.scale;
             dX[tb] = dX[tb] * -eg;
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         for (int tb = 0; tb < 4; ++tb) {
             const int t = row_index(tb, c);
             store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * 2) : kOffNone, T());
-            store4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            stream4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
         }
         add_cols(buf + B::q, 1, qo[1]);
         fence();

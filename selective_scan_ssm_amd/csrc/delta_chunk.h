@@ -421,7 +421,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
                         rt[ct][tb] = mma(xo[ct][kk], get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), rt[ct][tb]);
                 const int v = v0 + 16 * ct + 4 * g;
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb) store4(rt[ct][tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
+                for (int tb = 0; tb < 4; ++tb) stream4(rt[ct][tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
             }
         }
         f32x4 R[CT][4];

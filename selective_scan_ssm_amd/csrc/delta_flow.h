@@ -317,7 +317,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
                     for (int tb = 2 * kk; tb < 4; ++tb) rt[tb] = mma(xo[ct][kk], t_op(tri_low(tb, kk)), rt[tb]);
                 const int v = v0 + 16 * ct + 4 * g;
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb) store4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
+                for (int tb = 0; tb < 4; ++tb) stream4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
             }
         }
 #pragma unroll
