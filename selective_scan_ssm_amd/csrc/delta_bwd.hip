@@ -29,7 +29,7 @@ struct BwdParams {
 };
 
 // What get_col reads of a chunk that is used with steps along K only.
-template <typename T, int KP> struct QSide : Cols<T, KP> {};
+template <typename T, int KP> struct QSide : Cols<KP> {};
 template <int KP> struct QSide<bf16_t, KP> : Rows<bf16_t, KP> {
     static __device__ __forceinline__ uint32_t offsets(int64_t ld, int K, int thread) { return Rows<bf16_t, KP>::offset(ld, K, thread); }
 };
@@ -40,10 +40,9 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     // rows and columns of the keys, columns of the queries
-    char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sQ = sC + Cols<T, KP>::kBytes,
+    char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sQ = sC + Cols<KP>::kBytes,
          *const sT = sQ + QSide<T, KP>::kBytes, *const sP = sT + kTriBytes;
-    char *const sY = sP + kTriBytes;
-    float *const sS = reinterpret_cast<float *>(sY + Values<T, 1>::kBytes);
+    float *const sS = reinterpret_cast<float *>(sP + kTriBytes);
     const DeltaArgs &a = p.b.fwd;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
@@ -66,16 +65,16 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
     }
     // the next chunk's data, a chunk ahead, as in the forward
     Rows<T, KP> nK;
-    Cols<T, KP> nC;
+    Cols<KP> nC;
     QSide<T, KP> nQ;
     Copy<kTriBytes> nT, nP;
     float nS;
-    Values<T, 1> nY;
+    Values nY;
     const uint32_t okr = Rows<T, KP>::offset(a.ldk, K, threadIdx.x);
-    const auto okc = Cols<T, KP>::offsets(a.ldk, K, threadIdx.x);
+    const auto okc = Cols<KP>::offsets(a.ldk, K, threadIdx.x);
     const auto oqc = QSide<T, KP>::offsets(a.ldq, K, threadIdx.x);
     const int ldy = static_cast<int>(H * V);
-    const uint32_t oy = Values<T, 1>::offset(ldy, V - vt * 64, w, lane);
+    const uint32_t oy = Values::offset(ldy, V - vt * 64, w, lane);
     auto prefetch = [&](int j) {
         const int jj = j >= 0 ? j : 0;
         const int64_t row0 = sp.row0 + static_cast<int64_t>(jj) * kC, unit = (sp.slot0 + jj) * H + head;
@@ -101,12 +100,11 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
         nT.put(sT);
         nP.put(sP);
         if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
-        nY.put(sY);
-        const Values<T, 1> cY = nY;
+        const Values cY = nY;
         __syncthreads();
         store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
         prefetch(j - 1);
-        const Op<T> yo[2] = {cY.op(sY, 0, w, lane), cY.op(sY, 1, w, lane)};
+        const Op<T> yo[2] = {cY.op(0), cY.op(1)};
         Op2<T> so[KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(dS[2 * kk], dS[2 * kk + 1]);
@@ -168,7 +166,7 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
 
 template <int KP> constexpr size_t rev_lds() {
     using T = float;
-    return Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + QSide<T, KP>::kBytes + 2 * kTriBytes + 3 * kC * 4 + Values<T, 1>::kBytes;
+    return Rows<T, KP>::kBytes + Cols<KP>::kBytes + QSide<T, KP>::kBytes + 2 * kTriBytes + 3 * kC * 4;
 }
 
 // The same in bf16 io, as in delta_flow.h: a fifth (ninth) wave loads.  The buffer's
@@ -176,7 +174,7 @@ template <int KP> constexpr size_t rev_lds() {
 template <int KP, int NW>
 __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 3 : 2, NW == 8 ? 3 : 2))) void delta_rev_flow_kernel(BwdParams p) {
     using T = bf16_t;
-    using B = FlowBuf<KP, 1, NW>;
+    using B = FlowBuf<KP, NW>;
     constexpr int KT = KP / 16, KK = KP / 32, kWide = 16 * NW;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const DeltaArgs &a = p.b.fwd;
@@ -192,7 +190,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     const int ldy = static_cast<int>(H) * V;
 
     if (w == NW) {                                         // the loading wave
-        const FlowLoader<KP, 1, NW> ld(a.ldk, a.ldq, ldy, K, V - vt * kWide);
+        const FlowLoader<KP, NW> ld(a.ldk, a.ldq, ldy, K, V - vt * kWide);
         const T *pk = static_cast<const T *>(a.k) + lastrow * a.ldk + kh * K, *pq = static_cast<const T *>(a.q) + lastrow * a.ldq + kh * K;
         const T *pv = static_cast<const T *>(p.b.dout) + (lastrow * H + head) * V + vt * kWide;
         const char *pt = p.ws.tt + lastunit * kTriBytes, *pp = p.ws.p + lastunit * kTriBytes;
@@ -689,7 +687,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(BwdParams p) {
 template <int KP, int NW> hipError_t launch_rev_flow(const BwdParams &p, hipStream_t s) {
     constexpr int wide = 16 * NW;
     const DeltaShape &sh = p.b.fwd.s;
-    constexpr size_t lds = 2 * FlowBuf<KP, 1, NW>::bytes;
+    constexpr size_t lds = 2 * FlowBuf<KP, NW>::bytes;
     hipLaunchKernelGGL((delta_rev_flow_kernel<KP, NW>), dim3(static_cast<unsigned>((sh.dv + wide - 1) / wide * sh.heads * sh.nseq)),
                        dim3(kFlowThreads<NW>), lds, s, p);
     return hipGetLastError();

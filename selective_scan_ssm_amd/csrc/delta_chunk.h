@@ -1,6 +1,6 @@
 // The two passes that the gated delta rule and its gradient share: what a chunk
 // needs of its keys and queries alone (delta_prep_kernel), and the recurrence over
-// the chunks (delta_seq_kernel).
+// the chunks (delta_seq_kernel for fp32, delta_flow.h for bf16).
 #pragma once
 
 #include "delta_tile.h"
@@ -206,9 +206,10 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
 }
 
 // ------------------------------------------------------------------ recurrence
-// A workgroup owns (sequence's time segment, head, 64 CT value channels) and walks the
-// chunks; a wave keeps 16 channels' state (K x 16, fp32) in accumulator tiles.  A
-// chunk, with S the state entering it:
+// A workgroup owns (sequence's time segment, head, 64 value channels) and walks the
+// chunks; a wave keeps 16 channels' state (K x 16, fp32) in accumulator tiles.  This
+// kernel is fp32's; bf16's has a wave that loads (delta_flow.h).  A chunk, with S the
+// state entering it:
 //     X = V - exp(G) K S,  R = T X,  U = beta R
 //     Y = scale (exp(G) Q S + P U),  S <- exp(G_end) S + K^T (exp(G_end - G) U)
 // Every product's computed operand comes from the accumulators of the one before;
@@ -227,20 +228,20 @@ enum Mode {
 };
 constexpr bool has_out(Mode m) { return m == kOut || m == kTrain; }
 constexpr bool has_save(Mode m) { return m == kTrain || m == kSave; }
-template <typename T, int KP, Mode MODE, int CT>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && CT == 1 ? 2 : 1))) void delta_seq_kernel(SeqParams p) {
+template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_seq_kernel(SeqParams p) {
+    using T = float;
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
     constexpr bool OUT = has_out(MODE), SAVE = has_save(MODE);
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sT = sC + Cols<T, KP>::kBytes;
+    char *const sK = smem, *const sC = sK + Rows<T, KP>::kBytes, *const sT = sC + Cols<KP>::kBytes;
     float *const sS = reinterpret_cast<float *>(sT + kTriBytes);
-    char *const sV = sT + kTriBytes + 3 * kC * 4, *const sP = sV + Values<T, CT>::kBytes, *const sQ = sP + kTriBytes;
+    char *const sP = sT + kTriBytes + 3 * kC * 4, *const sQ = sP + kTriBytes;
     const DeltaArgs &a = p.a;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
     const int64_t H = a.s.heads;
-    constexpr int kWide = 64 * CT;
+    constexpr int kWide = 64;
     const int nvt = (V + kWide - 1) / kWide, tiles_n = MODE == kEnds ? nvt + (KP + kWide - 1) / kWide : nvt;
     const int tile = blockIdx.x % tiles_n;
     const int64_t rest = blockIdx.x / tiles_n, head = rest % H, kh = head / (H / a.s.kheads), id = rest / H;
@@ -253,41 +254,37 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
     const bool transition = MODE == kEnds && tile >= nvt;
     if (MODE == kEnds && (last || (first && transition))) return;
     const int vt = transition ? 0 : tile;
-    const int v0 = vt * kWide + w * 16 * CT;               // the wave's first channel
+    const int v0 = vt * kWide + w * 16;                    // the wave's first channel
     const f32x4 zero = {0, 0, 0, 0};
     const size_t VK = static_cast<size_t>(V) * K;
-    f32x4 S[CT][KT];
+    f32x4 S[KT];
+    if (transition) {
+        const int col = (tile - nvt) * kWide + w * 16 + c;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int v = v0 + 16 * ct;
-        if (transition) {
-            const int col = (tile - nvt) * kWide + (w * CT + ct) * 16 + c;
+        for (int q = 0; q < KK; ++q)
 #pragma unroll
-            for (int q = 0; q < KK; ++q)
+            for (int i = 0; i < 4; ++i) {
+                S[2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
+                S[2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
+            }
+    } else if (MODE != kEnds && !first) {
+        load_state<KP>(S, p.ends + ((id - 1) * H + head) * VK, v0, V, K, lane);
+    } else if (first && a.h0) {
+        load_state<KP>(S, a.h0 + (seq * H + head) * VK, v0, V, K, lane);
+    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    S[ct][2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
-                    S[ct][2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
-                }
-        } else if (MODE != kEnds && !first) {
-            load_state<KP>(S[ct], p.ends + ((id - 1) * H + head) * VK, v, V, K, lane);
-        } else if (first && a.h0) {
-            load_state<KP>(S[ct], a.h0 + (seq * H + head) * VK, v, V, K, lane);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KT; ++i) S[ct][i] = zero;
-        }
+        for (int i = 0; i < KT; ++i) S[i] = zero;
     }
     // the next chunk's data, a chunk ahead; past the last one all of it is out of range
     Rows<T, KP> nK, nQ;
-    Cols<T, KP> nC;
+    Cols<KP> nC;
     Copy<kTriBytes> nT, nP;
     float nS;
-    Values<T, CT> nV;
+    Values nV;
     const uint32_t okr = Rows<T, KP>::offset(a.ldk, K, threadIdx.x), oqr = Rows<T, KP>::offset(a.ldq, K, threadIdx.x);
-    const auto okc = Cols<T, KP>::offsets(a.ldk, K, threadIdx.x);
+    const auto okc = Cols<KP>::offsets(a.ldk, K, threadIdx.x);
     const int ldv = static_cast<int>(a.ldv);
-    const uint32_t ov = Values<T, CT>::offset(ldv, V - vt * kWide, w, lane);
+    const uint32_t ov = Values::offset(ldv, V - vt * kWide, w, lane);
     // addresses move on by whole chunks; loads are issued in two parts, each beside products, as a chunk's loads take
     // the memory pipe longer than the waves can queue them
     const T *pk = static_cast<const T *>(a.k) + (sp.row0 + static_cast<int64_t>(j0) * kC) * a.ldk + kh * K;
@@ -339,116 +336,92 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
             nP.put(sP);
         }
         nC.put(sC, threadIdx.x);
-        nV.put(sV);
-        const Values<T, CT> cV = nV;
+        const Values cV = nV;
         __syncthreads();
-        if constexpr (SAVE) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * (VK + kC * V), v0 + 16 * ct, V, K, lane);
-        }
-        Op2<T> so[CT][KK];
+        if constexpr (SAVE) store_state<KP>(S, a.ckpt + unit * (VK + kC * V), v0, V, K, lane);
+        Op2<T> so[KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
+            so[kk] = computed<T>(S[2 * kk], S[2 * kk + 1]);
+        f32x4 ks[4];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) so[ct][kk] = computed<T>(S[ct][2 * kk], S[ct][2 * kk + 1]);
-        f32x4 ks[CT][4];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) ks[ct][tb] = zero;
+        for (int tb = 0; tb < 4; ++tb) ks[tb] = zero;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
                 const Op<T> f = get_row(sK + (tb * KK + kk) * RB, lane, T());
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) ks[ct][tb] = mma(f, so[ct][kk], ks[ct][tb]);
+                ks[tb] = mma(f, so[kk], ks[tb]);
             }
         __builtin_amdgcn_sched_barrier(0);
         prefetch1();
         __builtin_amdgcn_sched_barrier(0);
-        f32x4 y[OUT ? CT : 1][4];                          // transposed: rows are channels, columns steps
+        f32x4 y[4];                          // transposed: rows are channels, columns steps
         if constexpr (OUT) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb) y[ct][tb] = zero;
+            for (int tb = 0; tb < 4; ++tb) y[tb] = zero;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) {
                     const Op<T> f = get_row(sQ + (tb * KK + kk) * RB, lane, T());
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[ct][tb] = mma(so[ct][kk], f, y[ct][tb]);
+                    y[tb] = mma(so[kk], f, y[tb]);
                 }
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
                 const float e = sS[row_index(tb, c)];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) y[ct][tb] = y[ct][tb] * e;
+                y[tb] = y[tb] * e;
             }
         }
-        Op2<T> xo[CT][2];
+        Op2<T> xo[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {                      // 32 steps
             const f32x4 e0 = *reinterpret_cast<const f32x4 *>(&sS[32 * q + 8 * g]), e1 = *reinterpret_cast<const f32x4 *>(&sS[32 * q + 8 * g + 4]);
+            f32x4 x0, x1;
+            tiles(cV.op(q), x0, x1);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                f32x4 x0, x1;
-                tiles(cV.op(sV, q, w * CT + ct, lane), x0, x1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x0[i] = fmaf(-e0[i], ks[ct][2 * q][i], x0[i]);
-                    x1[i] = fmaf(-e1[i], ks[ct][2 * q + 1][i], x1[i]);
-                }
-                xo[ct][q] = computed<T>(x0, x1);
+            for (int i = 0; i < 4; ++i) {
+                x0[i] = fmaf(-e0[i], ks[2 * q][i], x0[i]);
+                x1[i] = fmaf(-e1[i], ks[2 * q + 1][i], x1[i]);
             }
+            xo[q] = computed<T>(x0, x1);
         }
         __builtin_amdgcn_sched_barrier(0);
         prefetch2();
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (SAVE) {                              // R, transposed, for stores of four channels
             const rsrc_t rr = make_rsrc(a.ckpt + unit * (VK + kC * V) + VK, static_cast<uint32_t>(kC * V * 4));
-            f32x4 rt[CT][4];
+            f32x4 rt[4];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
+            for (int tb = 0; tb < 4; ++tb) rt[tb] = zero;
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb) rt[ct][tb] = zero;
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
+                for (int tb = 2 * kk; tb < 4; ++tb)
+                    rt[tb] = mma(xo[kk], get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), rt[tb]);
+            const int v = v0 + 4 * g;
 #pragma unroll
-                    for (int tb = 2 * kk; tb < 4; ++tb)
-                        rt[ct][tb] = mma(xo[ct][kk], get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T()), rt[ct][tb]);
-                const int v = v0 + 16 * ct + 4 * g;
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb) stream4(rt[ct][tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
-            }
+            for (int tb = 0; tb < 4; ++tb) stream4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
         }
-        f32x4 R[CT][4];
+        f32x4 R[4];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) R[ct][tb] = zero;
+        for (int tb = 0; tb < 4; ++tb) R[tb] = zero;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int tb = 2 * kk; tb < 4; ++tb) {
                 const Op2<T> f = get_op2(sT + tri_low(tb, kk) * kOp2Bytes, lane, T());
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) R[ct][tb] = mma(f, xo[ct][kk], R[ct][tb]);
+                R[tb] = mma(f, xo[kk], R[tb]);
             }
-        Op2<T> uo[OUT ? CT : 1][2], wo[CT][2];
+        Op2<T> uo[2], wo[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int t = 32 * q + 8 * g;
             const f32x4 b0 = *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t]), b1 = *reinterpret_cast<const f32x4 *>(&sS[2 * kC + t + 4]);
             const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&sS[kC + t]), w1 = *reinterpret_cast<const f32x4 *>(&sS[kC + t + 4]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const f32x4 u0 = R[ct][2 * q] * b0, u1 = R[ct][2 * q + 1] * b1;
-                if constexpr (OUT) uo[ct][q] = computed<T>(u0, u1);
-                wo[ct][q] = computed<T>(u0 * w0, u1 * w1);
-            }
+            const f32x4 u0 = R[2 * q] * b0, u1 = R[2 * q + 1] * b1;
+            if constexpr (OUT) uo[q] = computed<T>(u0, u1);
+            wo[q] = computed<T>(u0 * w0, u1 * w1);
         }
         if constexpr (OUT) {
             const rsrc_t ry = chunk_rsrc(static_cast<T *>(a.y) + (row0 * H + head) * V, n, H * V, V, sizeof(T));
@@ -458,35 +431,27 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
 #pragma unroll
                 for (int tb = 2 * kk; tb < 4; ++tb) {
                     const Op2<T> f = get_op2(sP + tri_low(tb, kk) * kOp2Bytes, lane, T());
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[ct][tb] = mma(uo[ct][kk], f, y[ct][tb]);
+                    y[tb] = mma(uo[kk], f, y[tb]);
                 }
+            const int v = v0 + 4 * g;
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int v = v0 + 16 * ct + 4 * g;
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb)
-                    store_io4(y[ct][tb] * a.scale, ry, v < V ? static_cast<uint32_t>((row_index(tb, c) * ldy + v) * static_cast<int>(sizeof(T))) : kOffNone, T());
-            }
+            for (int tb = 0; tb < 4; ++tb)
+                store_io4(y[tb] * a.scale, ry, v < V ? static_cast<uint32_t>((row_index(tb, c) * ldy + v) * static_cast<int>(sizeof(T))) : kOffNone, T());
         }
         const float end = sS[kC - 1];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) S[ct][kt] = S[ct][kt] * end;
+        for (int kt = 0; kt < KT; ++kt) S[kt] = S[kt] * end;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 const Op<T> f = get_col<KP>(sK, sC, kt, kk, lane, T());
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) S[ct][kt] = mma(f, wo[ct][kk], S[ct][kt]);
+                S[kt] = mma(f, wo[kk], S[kt]);
             }
     }
     if constexpr (MODE == kEnds) {
         if (!transition) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], p.ends + (id * H + head) * VK, v0 + 16 * ct, V, K, lane);
+            store_state<KP>(S, p.ends + (id * H + head) * VK, v0, V, K, lane);
             return;
         }
         // columns n of the map, turned into operands with n along K
@@ -494,10 +459,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
         float *const sM = reinterpret_cast<float *>(smem);
         __syncthreads();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int q = 0; q < KT; ++q)
-                *reinterpret_cast<f32x4 *>(&sM[(16 * (w * CT + ct) + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[ct][q];
+        for (int q = 0; q < KT; ++q)
+            *reinterpret_cast<f32x4 *>(&sM[(16 * w + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[q];
         __syncthreads();
         char *const out = p.maps + (id * H + head) * kMapBytes<KP>;
         const int n0 = (tile - nvt) * kWide, nk = KP - n0 < kWide ? (KP - n0) / 32 : kWide / 32;
@@ -513,15 +476,15 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof
         }
     } else {
         if (last && a.last_state) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.last_state + (seq * H + head) * VK, v0 + 16 * ct, V, K, lane);
+            store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
         }
     }
 }
 
-template <typename T, int KP, Mode MODE, int CT> constexpr size_t seq_lds() {
-    constexpr size_t n = Rows<T, KP>::kBytes + Cols<T, KP>::kBytes + kTriBytes + 3 * kC * 4 + Values<T, CT>::kBytes +
-                         (has_out(MODE) ? kTriBytes + Rows<T, KP>::kBytes : 0), m = MODE == kEnds ? 64 * CT * (KP + 4) * 4 : 0;
+template <int KP, Mode MODE> constexpr size_t seq_lds() {
+    using T = float;
+    constexpr size_t n = Rows<T, KP>::kBytes + Cols<KP>::kBytes + kTriBytes + 3 * kC * 4 +
+                         (has_out(MODE) ? kTriBytes + Rows<T, KP>::kBytes : 0), m = MODE == kEnds ? 64 * (KP + 4) * 4 : 0;
     return n > m ? n : m;
 }
 
@@ -565,12 +528,12 @@ template <typename T, int KP, bool BWD> hipError_t launch_prep(const DeltaArgs &
                        0, s, a, ws);
     return hipGetLastError();
 }
-template <typename T, int KP, Mode MODE, int CT> hipError_t launch_seq(const SeqParams &p, hipStream_t s) {
-    constexpr int wide = 64 * CT;
+template <int KP, Mode MODE> hipError_t launch_seq(const SeqParams &p, hipStream_t s) {
+    constexpr int wide = 64;
     const int64_t nvt = (p.a.s.dv + wide - 1) / wide;
     const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * p.segments;
-    constexpr size_t lds = seq_lds<T, KP, MODE, CT>();
-    hipLaunchKernelGGL((delta_seq_kernel<T, KP, MODE, CT>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
+    constexpr size_t lds = seq_lds<KP, MODE>();
+    hipLaunchKernelGGL((delta_seq_kernel<KP, MODE>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
     return hipGetLastError();
 }
 template <typename T, int KP> hipError_t launch_carry(const SeqParams &p, hipStream_t s) {

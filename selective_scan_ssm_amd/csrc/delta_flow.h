@@ -1,14 +1,17 @@
-// The recurrence over the chunks in bf16 io: four waves compute, a fifth loads.
+// The recurrence over the chunks in bf16 io: four (or eight) waves compute, one more loads.
 //
 // A chunk's keys, queries, values and shared operands are 50 to 73 KB, which take the
 // memory pipe one to two thousand clocks; waves that also compute stood still for
-// as long, since a wave's instructions issue in order.  The fifth wave moves them
+// as long, since a wave's instructions issue in order.  The extra wave moves them
 // from global memory into one of two LDS buffers directly (no registers, no LDS
-// writes), a chunk ahead, and one barrier per chunk hands them over.  2 x 8192 steps of 40
-// heads of 128 x 128: see delta_scan.hip for what each form measured.
+// writes), a chunk ahead, and one barrier per chunk hands them over.
 //
-// Two tiles of 16 value channels to a wave (CT = 2) share every operand read from
-// LDS; headdim <= 64 leaves one.
+// 2 x 8192 steps of 40 heads of 128 x 128 (160 workgroups), the walk: the four waves loading
+// for themselves 636 us a call, with the fifth wave 467; now 350 us of kernel, 2.75 us a
+// chunk.  What bounds it: each wave reads the chunk's 91 KB of operands from LDS (four waves
+// 2900 clocks of the CU's LDS) and issues 132 products (2100 clocks), in a chain from S to
+// the next S that leaves little of them side by side.  32 columns to a wave, for half of the
+// reads, 3.9 to 6 us a chunk: one wave to a SIMD has no one to cover its waits.
 #pragma once
 
 #include "delta_chunk.h"
@@ -23,9 +26,9 @@ template <int NW> constexpr int kFlowThreads = 64 * (NW + 1);
 // In an operand lane (g, c) finds its 16 bytes at 256 g + 16 (c ^ 4 g): the
 // transposing read of a 4 x 16 block then touches 16 different places, and a plain
 // one is a permutation of each 256 bytes.
-template <int KP, int CT, int NW> struct FlowBuf {
+template <int KP, int NW> struct FlowBuf {
     static constexpr int KK = KP / 32, KT = KP / 16;
-    static constexpr int rows = 4 * KK * 1024, kv = CT * NW / 2, values = 4 * kv * 1024;
+    static constexpr int rows = 4 * KK * 1024, kv = NW / 2, values = 4 * kv * 1024;
     static constexpr int q = rows, t = 2 * rows, p = t + kTriBytes, v = p + kTriBytes, s = v + values, bytes = s + 3 * kC * 4;
 };
 __device__ __forceinline__ int flow_at(int lane) { return lane / 16 * 256 + ((lane % 16) ^ (lane / 16 * 4)) * 16; }
@@ -59,8 +62,8 @@ __device__ __forceinline__ void flow_barrier() { asm volatile("s_waitcnt lgkmcnt
 __device__ __forceinline__ void flow_loaded() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The loading wave's part.
-template <int KP, int CT, int NW> struct FlowLoader {
-    using B = FlowBuf<KP, CT, NW>;
+template <int KP, int NW> struct FlowLoader {
+    using B = FlowBuf<KP, NW>;
     using lds = __attribute__((address_space(3))) void *;
     static constexpr int KK = B::KK;
     int lane, r;                                   // r: the step that lane's 16 bytes belong to, in tile 0
@@ -104,10 +107,10 @@ template <int KP, int CT, int NW> struct FlowLoader {
     }
 };
 
-template <int KP, Mode MODE, int CT, int NW>
+template <int KP, Mode MODE, int NW>
 __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 3 : 2, NW == 8 ? 3 : 2))) void delta_flow_kernel(SeqParams p) {
     using T = bf16_t;
-    using B = FlowBuf<KP, CT, NW>;
+    using B = FlowBuf<KP, NW>;
     constexpr int KT = KP / 16, KK = KP / 32;
     constexpr bool OUT = has_out(MODE), SAVE = has_save(MODE);
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     const int g = lane / 16, c = lane % 16;
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
     const int64_t H = a.s.heads;
-    constexpr int kWide = 16 * NW * CT;
+    constexpr int kWide = 16 * NW;
     const int nvt = (V + kWide - 1) / kWide, tiles_n = MODE == kEnds ? nvt + (KP + kWide - 1) / kWide : nvt;
     // a segment's tiles lie a whole number of segments apart: on the same XCD where that is a multiple of eight, and
     // those that find nothing to do are spread evenly
@@ -134,7 +137,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     const int nch = sg.j1 - sg.j0;
 
     if (w == NW) {                                     // the loading wave
-        const FlowLoader<KP, CT, NW> ld(a.ldk, a.ldq, a.ldv, K, V - vt * kWide);
+        const FlowLoader<KP, NW> ld(a.ldk, a.ldq, a.ldv, K, V - vt * kWide);
         const T *pk = static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, *pq = static_cast<const T *>(a.q) + row0 * a.ldq + kh * K;
         const T *pv = static_cast<const T *>(a.v) + row0 * a.ldv + head * V + vt * kWide;
         const char *pt = p.ws.t + unit0 * kTriBytes, *pp = p.ws.p + unit0 * kTriBytes;
@@ -168,31 +171,27 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         return;
     }
 
-    const int v0 = vt * kWide + w * 16 * CT;               // the wave's first channel
+    const int v0 = vt * kWide + w * 16;                    // the wave's first channel
     const f32x4 zero = {0, 0, 0, 0};
     const size_t VK = static_cast<size_t>(V) * K;
     const int at = flow_at(lane), tat = flow_tr_at(lane);
-    f32x4 S[CT][KT];
+    f32x4 S[KT];
+    if (transition) {
+        const int col = (tile - nvt) * kWide + w * 16 + c;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int v = v0 + 16 * ct;
-        if (transition) {
-            const int col = (tile - nvt) * kWide + (w * CT + ct) * 16 + c;
+        for (int q = 0; q < KK; ++q)
 #pragma unroll
-            for (int q = 0; q < KK; ++q)
+            for (int i = 0; i < 4; ++i) {
+                S[2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
+                S[2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
+            }
+    } else if (MODE != kEnds && !first) {
+        load_state<KP>(S, p.ends + ((id - 1) * H + head) * VK, v0, V, K, lane);
+    } else if (first && a.h0) {
+        load_state<KP>(S, a.h0 + (seq * H + head) * VK, v0, V, K, lane);
+    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    S[ct][2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
-                    S[ct][2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
-                }
-        } else if (MODE != kEnds && !first) {
-            load_state<KP>(S[ct], p.ends + ((id - 1) * H + head) * VK, v, V, K, lane);
-        } else if (first && a.h0) {
-            load_state<KP>(S[ct], a.h0 + (seq * H + head) * VK, v, V, K, lane);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KT; ++i) S[ct][i] = zero;
-        }
+        for (int i = 0; i < KT; ++i) S[i] = zero;
     }
     int64_t unit = unit0;
     const int ldy = static_cast<int>(H) * V;
@@ -202,10 +201,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         const char *const buf = smem + j % 2 * B::bytes;
         const float *const sS = reinterpret_cast<const float *>(buf + B::s);
         flow_barrier();
-        if constexpr (SAVE) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.ckpt + unit * (VK + kC * V), v0 + 16 * ct, V, K, lane);
-        }
+        if constexpr (SAVE) store_state<KP>(S, a.ckpt + unit * (VK + kC * V), v0, V, K, lane);
         // With a wave to a SIMD the reads of LDS are issued a product ahead of their use, and held there by `fence`: left
         // to itself the compiler reads each operand where it is used and waits for it.  Eight waves cover one another's
         // waits, and have not the registers.
@@ -213,16 +209,14 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         auto fence = [] {
             if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0);
         };
-        f32x4 ks[CT][4], y[OUT ? CT : 1][4];               // y transposed: rows are channels, columns steps
+        f32x4 ks[4], y[4];                                 // y transposed: rows are channels, columns steps
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                ks[ct][tb] = zero;
-                if constexpr (OUT) y[ct][tb] = zero;
-            }
-        Op<T> fk[2][4], fq[2][4], fv[CT][2];
-        Op2<T> ft[AHEAD ? 6 : 1], so[2][CT];
+        for (int tb = 0; tb < 4; ++tb) {
+            ks[tb] = zero;
+            if constexpr (OUT) y[tb] = zero;
+        }
+        Op<T> fk[2][4], fq[2][4], fv[2];
+        Op2<T> ft[AHEAD ? 6 : 1], so[2];
         f32x4 e[4];
         auto t_op = [&](int f) {
             if constexpr (AHEAD) return ft[f];
@@ -237,8 +231,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         };
         if constexpr (AHEAD) read_rows(0);
         fence();
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) so[0][ct] = computed<T>(S[ct][0], S[ct][1]);
+        so[0] = computed<T>(S[0], S[1]);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             if constexpr (!AHEAD) read_rows(kk);
@@ -248,30 +241,21 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 #pragma unroll
                 for (int f = 0; f < (AHEAD ? 6 : 0); ++f) ft[f] = get_op2(buf + B::t + f * kOp2Bytes, lane, T());
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) fv[ct][q] = flow_value<B::kv>(buf + B::v, lane, q, w * CT + ct);
+                for (int q = 0; q < 2; ++q) fv[q] = flow_value<B::kv>(buf + B::v, lane, q, w);
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) e[tb] = *reinterpret_cast<const f32x4 *>(&sS[32 * (tb / 2) + 8 * g + 4 * (tb % 2)]);
             }
             fence();
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) ks[ct][tb] = mma(fk[kk % 2][tb], so[kk % 2][ct], ks[ct][tb]);
+            for (int tb = 0; tb < 4; ++tb) ks[tb] = mma(fk[kk % 2][tb], so[kk % 2], ks[tb]);
             if constexpr (OUT) {
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[ct][tb] = mma(so[kk % 2][ct], fq[kk % 2][tb], y[ct][tb]);
+                for (int tb = 0; tb < 4; ++tb) y[tb] = mma(so[kk % 2], fq[kk % 2][tb], y[tb]);
             }
-            if (kk + 1 < KK) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) so[(kk + 1) % 2][ct] = computed<T>(S[ct][2 * kk + 2], S[ct][2 * kk + 3]);
-            }
+            if (kk + 1 < KK) so[(kk + 1) % 2] = computed<T>(S[2 * kk + 2], S[2 * kk + 3]);
             fence();
         }
-        Op2<T> fp[OUT && AHEAD ? 6 : 1], xo[CT][2];
+        Op2<T> fp[OUT && AHEAD ? 6 : 1], xo[2];
         float ey[OUT ? 4 : 1];
         f32x4 eb[4], ew[4];
         const float end = sS[kC - 1];
@@ -289,65 +273,53 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         }
         fence();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+        for (int q = 0; q < 2; ++q) {                      // 32 steps
+            f32x4 x0, x1;
+            tiles(fv[q], x0, x1);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {                  // 32 steps
-                f32x4 x0, x1;
-                tiles(fv[ct][q], x0, x1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x0[i] = fmaf(-e[2 * q][i], ks[ct][2 * q][i], x0[i]);
-                    x1[i] = fmaf(-e[2 * q + 1][i], ks[ct][2 * q + 1][i], x1[i]);
-                }
-                xo[ct][q] = computed<T>(x0, x1);
+            for (int i = 0; i < 4; ++i) {
+                x0[i] = fmaf(-e[2 * q][i], ks[2 * q][i], x0[i]);
+                x1[i] = fmaf(-e[2 * q + 1][i], ks[2 * q + 1][i], x1[i]);
             }
-        f32x4 R[CT][4];
+            xo[q] = computed<T>(x0, x1);
+        }
+        f32x4 R[4];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) R[ct][tb] = zero;
+        for (int tb = 0; tb < 4; ++tb) R[tb] = zero;
         if constexpr (SAVE) {                              // R, transposed, for stores of four channels
             const rsrc_t rr = make_rsrc(a.ckpt + unit * (VK + kC * V) + VK, static_cast<uint32_t>(kC * V * 4));
+            f32x4 rt[4] = {zero, zero, zero, zero};
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                f32x4 rt[4] = {zero, zero, zero, zero};
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
+                for (int tb = 2 * kk; tb < 4; ++tb) rt[tb] = mma(xo[kk], t_op(tri_low(tb, kk)), rt[tb]);
+            const int v = v0 + 4 * g;
 #pragma unroll
-                    for (int tb = 2 * kk; tb < 4; ++tb) rt[tb] = mma(xo[ct][kk], t_op(tri_low(tb, kk)), rt[tb]);
-                const int v = v0 + 16 * ct + 4 * g;
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb) stream4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
-            }
+            for (int tb = 0; tb < 4; ++tb) stream4(rt[tb], rr, v < V ? static_cast<uint32_t>((row_index(tb, c) * V + v) * 4) : kOffNone);
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int tb = 2 * kk; tb < 4; ++tb) {
                 const Op2<T> f = t_op(tri_low(tb, kk));
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) R[ct][tb] = mma(f, xo[ct][kk], R[ct][tb]);
+                R[tb] = mma(f, xo[kk], R[tb]);
             }
         if constexpr (OUT) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb) y[ct][tb] = y[ct][tb] * ey[tb];
+            for (int tb = 0; tb < 4; ++tb) y[tb] = y[tb] * ey[tb];
         }
         fence();
         Op<T> fc[KT];                                      // the first 32 steps' columns
 #pragma unroll
         for (int kt = 0; kt < (AHEAD ? KT : 0); ++kt) fc[kt] = flow_col<KP>(buf, tat, kt, 0);
         fence();
-        Op2<T> uo[OUT ? CT : 1][2], wo[CT][2];
+        Op2<T> uo[2], wo[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const f32x4 u0 = R[ct][2 * q] * eb[2 * q], u1 = R[ct][2 * q + 1] * eb[2 * q + 1];
-                if constexpr (OUT) uo[ct][q] = computed<T>(u0, u1);
-                wo[ct][q] = computed<T>(u0 * ew[2 * q], u1 * ew[2 * q + 1]);
-            }
+        for (int q = 0; q < 2; ++q) {
+            const f32x4 u0 = R[2 * q] * eb[2 * q], u1 = R[2 * q + 1] * eb[2 * q + 1];
+            if constexpr (OUT) uo[q] = computed<T>(u0, u1);
+            wo[q] = computed<T>(u0 * ew[2 * q], u1 * ew[2 * q + 1]);
+        }
         if constexpr (OUT) {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
@@ -356,14 +328,11 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
                     Op2<T> f;
                     if constexpr (AHEAD) f = fp[tri_low(tb, kk)];
                     else f = get_op2(buf + B::p + tri_low(tb, kk) * kOp2Bytes, lane, T());
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[ct][tb] = mma(uo[ct][kk], f, y[ct][tb]);
+                    y[tb] = mma(uo[kk], f, y[tb]);
                 }
         }
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) S[ct][kt] = S[ct][kt] * end;
+        for (int kt = 0; kt < KT; ++kt) S[kt] = S[kt] * end;
         fence();
         Op<T> fd[KT];
 #pragma unroll
@@ -372,30 +341,24 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             if constexpr (!AHEAD) fc[kt] = flow_col<KP>(buf, tat, kt, 0);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) S[ct][kt] = mma(fc[kt], wo[ct][0], S[ct][kt]);
+            S[kt] = mma(fc[kt], wo[0], S[kt]);
         }
         if constexpr (OUT) {
             const rsrc_t ry = chunk_rsrc(py, left < kC ? left : kC, ldy, V, 2);
+            const int v = v0 + 4 * g;
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int v = v0 + 16 * ct + 4 * g;
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb)
-                    store_io4(y[ct][tb] * a.scale, ry, v < V ? static_cast<uint32_t>((row_index(tb, c) * ldy + v) * 2) : kOffNone, T());
-            }
+            for (int tb = 0; tb < 4; ++tb)
+                store_io4(y[tb] * a.scale, ry, v < V ? static_cast<uint32_t>((row_index(tb, c) * ldy + v) * 2) : kOffNone, T());
         }
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             if constexpr (!AHEAD) fd[kt] = flow_col<KP>(buf, tat, kt, 1);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) S[ct][kt] = mma(fd[kt], wo[ct][1], S[ct][kt]);
+            S[kt] = mma(fd[kt], wo[1], S[kt]);
         }
     }
     if constexpr (MODE == kEnds) {
         if (!transition) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], p.ends + (id * H + head) * VK, v0 + 16 * ct, V, K, lane);
+            store_state<KP>(S, p.ends + (id * H + head) * VK, v0, V, K, lane);
             return;
         }
         // columns n of the map, turned into operands with n along K
@@ -404,10 +367,8 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         float *const sM = reinterpret_cast<float *>(smem);
         flow_barrier();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int q = 0; q < KT; ++q)
-                *reinterpret_cast<f32x4 *>(&sM[(16 * (w * CT + ct) + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[ct][q];
+        for (int q = 0; q < KT; ++q)
+            *reinterpret_cast<f32x4 *>(&sM[(16 * w + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[q];
         flow_barrier();
         char *const out = p.maps + (id * H + head) * kMapBytes<KP>;
         const int n0 = (tile - nvt) * kWide, nk = KP - n0 < kWide ? (KP - n0) / 32 : kWide / 32;
@@ -422,24 +383,23 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
             put_op(out + ((n0 / 32 + kk) * KT + kt) * kOp2Bytes, lane, computed<T>(x, y));
         }
     } else if (last && a.last_state) {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) store_state<KP>(S[ct], a.last_state + (seq * H + head) * VK, v0 + 16 * ct, V, K, lane);
+        store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
     }
 }
 
-template <int KP, Mode MODE, int CT, int NW> hipError_t launch_flow(const SeqParams &p, hipStream_t s) {
-    constexpr int wide = 16 * NW * CT;
+template <int KP, Mode MODE, int NW> hipError_t launch_flow(const SeqParams &p, hipStream_t s) {
+    constexpr int wide = 16 * NW;
     const int64_t nvt = (p.a.s.dv + wide - 1) / wide;
     const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * p.segments;
-    constexpr size_t lds = 2 * FlowBuf<KP, CT, NW>::bytes;
-    hipLaunchKernelGGL((delta_flow_kernel<KP, MODE, CT, NW>), dim3(static_cast<unsigned>(grid)), dim3(kFlowThreads<NW>), lds, s, p);
+    constexpr size_t lds = 2 * FlowBuf<KP, NW>::bytes;
+    hipLaunchKernelGGL((delta_flow_kernel<KP, MODE, NW>), dim3(static_cast<unsigned>(grid)), dim3(kFlowThreads<NW>), lds, s, p);
     return hipGetLastError();
 }
 
 // A walk over all chunks: bf16 with a loading wave, fp32 without.
 template <typename T, int KP, Mode MODE> hipError_t launch_walk(const SeqParams &p, hipStream_t s) {
-    if constexpr (sizeof(T) == 4) return launch_seq<T, KP, MODE, 1>(p, s);
-    else return (MODE == kEnds ? p.wide_ends : p.wide) ? launch_flow<KP, MODE, 1, 8>(p, s) : launch_flow<KP, MODE, 1, 4>(p, s);
+    if constexpr (sizeof(T) == 4) return launch_seq<KP, MODE>(p, s);
+    else return (MODE == kEnds ? p.wide_ends : p.wide) ? launch_flow<KP, MODE, 8>(p, s) : launch_flow<KP, MODE, 4>(p, s);
 }
 // the states that the segments are entered with, where there is more than one
 template <typename T, int KP> hipError_t launch_segments(const SeqParams &p, hipStream_t s) {

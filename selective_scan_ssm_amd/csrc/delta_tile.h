@@ -169,23 +169,8 @@ __device__ __forceinline__ void store_io4(f32x4 v, rsrc_t r, uint32_t off, bf16_
 }
 __device__ __forceinline__ void store_io4(f32x4 v, rsrc_t r, uint32_t off, float) { store4(v, r, off); }
 
-// Eight rows of two neighbouring columns, as the two columns' operand elements.
-template <typename T> struct Columns;
-template <> struct Columns<bf16_t> {
-    uint32_t w[8];
-    __device__ __forceinline__ void load(rsrc_t r, int j, uint32_t off) { w[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
-    __device__ __forceinline__ void put(char *p, int lane) const {
-        u32x4 a, b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = (w[2 * i] & 0xffffu) | (w[2 * i + 1] << 16);
-            b[i] = (w[2 * i] >> 16) | (w[2 * i + 1] & 0xffff0000u);
-        }
-        put_op(p, lane, Op<bf16_t>{a});
-        put_op(p, lane + 1, Op<bf16_t>{b});
-    }
-};
-template <> struct Columns<float> {
+// Eight rows of two neighbouring fp32 columns, as the two columns' operand elements.
+struct Columns {
     f32x2 w[8];
     __device__ __forceinline__ void load(rsrc_t r, int j, uint32_t off) {
         w[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
@@ -332,10 +317,11 @@ template <typename T, int KP> struct Rows {
 };
 // The same chunk with steps along K: slot (tile, kk) holds channels row_index (of
 // each 32) as rows, steps 32 kk + 8 g ...  fp32 only: bf16 reads the rows' copy
-// transposed, which saves eight narrow loads a thread and 16 KB of LDS.
-template <typename T, int KP> struct Cols {
+// transposed.
+template <int KP> struct Cols {
+    using T = float;
     static constexpr int KT = KP / 16, N = KT * 2 * 32 / kThreads, kBytes = 2 * KT * kOpBytes<T>;
-    Columns<T> v[N];
+    Columns v[N];
     static __device__ __forceinline__ uint32_t offset(int64_t ld, int i, int K, int thread) {
         const int s = i * kThreads + thread, f = s / 32, c = 2 * (s % 8), g = (s / 8) % 4;
         const int tile = f / 2, k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4, t0 = 32 * (f % 2) + 8 * g;
@@ -364,13 +350,6 @@ template <typename T, int KP> struct Cols {
         }
     }
 };
-template <int KP> struct Cols<bf16_t, KP> {
-    static constexpr int kBytes = 0;
-    struct Offsets {};
-    static __device__ __forceinline__ Offsets offsets(int64_t, int, int) { return {}; }
-    __device__ __forceinline__ void load(rsrc_t, int64_t, const Offsets &) {}
-    __device__ __forceinline__ void put(char *, int) const {}
-};
 // channels of tile kt as rows, steps 32 kk + 8 g ... along K, from the rows or the columns in LDS
 template <int KP> __device__ __forceinline__ Op<bf16_t> get_col(const char *rows, const char *, int kt, int kk, int lane, bf16_t) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -385,39 +364,9 @@ template <int KP> __device__ __forceinline__ Op<bf16_t> get_col(const char *rows
 template <int KP> __device__ __forceinline__ Op<float> get_col(const char *, const char *cols, int kt, int kk, int lane, float) {
     return get_op(cols + (kt * 2 + kk) * kOpBytes<float>, lane, 0.0f);
 }
-// A chunk's steps of the workgroup's 64 CT value channels; a wave gets 16 of them as
-// the columns of accumulator tiles, or as an operand with steps along K.  bf16 goes
-// through LDS (16-byte loads instead of 2-byte ones) and is read transposed, fp32
-// straight to the lanes (CT = 1).  V: channels from the workgroup's first on.
-template <typename T, int CT> struct Values;
-template <int CT> struct Values<bf16_t, CT> {
-    static constexpr int N = 2 * CT, kBytes = 4 * N * kRowBytes<bf16_t>;
-    Op<bf16_t> v[N];
-    static __device__ __forceinline__ uint32_t offset(int ld, int V, int, int) {
-        const int lane = threadIdx.x % 64, f = threadIdx.x / 64, t = row_index(f / N, lane % 16), c = 32 * (f % N) + 8 * (lane / 16);
-        return c < V ? static_cast<uint32_t>((t * ld + c) * 2) : kOffNone;
-    }
-    __device__ __forceinline__ void load(rsrc_t r, int ld, uint32_t off) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = load_op(r, off + static_cast<uint32_t>(row_index(i * 4 / N, 0) * ld * 2), bf16_t());
-    }
-    __device__ __forceinline__ void put(char *dst) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) put_row(dst + (4 * i + threadIdx.x / 64) * kRowBytes<bf16_t>, threadIdx.x % 64, v[i]);
-    }
-    // steps 32 p .. of column tile ct
-    __device__ __forceinline__ Op<bf16_t> op(const char *src, int p, int ct, int lane) const {
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
-        using lds = __attribute__((address_space(3))) s16x4 *;
-        const int l = lane % 16, piece = l % 4;
-        const char *const q = src + (2 * p * N + ct / 2) * kRowBytes<bf16_t> + (2 * (ct % 2) + piece / 2) * 320 + (4 * (lane / 16) + l / 4) * 16 + piece % 2 * 8;
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q))));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(const_cast<char *>(q + N * kRowBytes<bf16_t>))));
-        return {u32x4{a[0], a[1], b[0], b[1]}};
-    }
-};
-template <> struct Values<float, 1> {
-    static constexpr int kBytes = 0;
+// A chunk's steps of a wave's 16 fp32 value channels, as the columns of accumulator
+// tiles, or as an operand with steps along K.  V: channels from the workgroup's first on.
+struct Values {
     float v[16];
     static __device__ __forceinline__ uint32_t offset(int ld, int V, int w, int lane) {
         const int c = 16 * w + lane % 16;
@@ -428,8 +377,7 @@ template <> struct Values<float, 1> {
         for (int i = 0; i < 16; ++i)
             v[i] = Io<float>::f32(Io<float>::load(r, off + static_cast<uint32_t>((32 * (i / 8) + i % 8) * ld * 4), 0));
     }
-    __device__ __forceinline__ void put(char *) const {}
-    __device__ __forceinline__ Op<float> op(const char *, int p, int, int) const {
+    __device__ __forceinline__ Op<float> op(int p) const {
         return {f32x4{v[8 * p], v[8 * p + 1], v[8 * p + 2], v[8 * p + 3]}, f32x4{v[8 * p + 4], v[8 * p + 5], v[8 * p + 6], v[8 * p + 7]}};
     }
 };
