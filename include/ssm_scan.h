@@ -83,7 +83,7 @@ typedef enum {
     SSM_ERR_ALIAS = -7,     /* an output overlaps an input                      */
     SSM_ERR_WAIT = -8,      /* a segment's bounded wait gave up (ssm_scan_status) */
     SSM_ERR_SCRATCH = -9,   /* the shape needs more than SSM_SCRATCH_BYTES (noalloc) */
-    SSM_ERR_VALUE = -10,    /* eps is negative or not finite, max_norm negative or NaN, or scale not finite */
+    SSM_ERR_VALUE = -10,    /* eps is negative or not finite, or max_norm negative or NaN, or scale not finite */
     SSM_ERR_HOST = -11      /* host memory for checking a list could not be had   */
 } ssm_status_t;
 
@@ -725,7 +725,8 @@ int ssm_delta_state_update(float *state, const void *q, const void *k, const voi
  *   y    : (batch, rows, dim) io dtype, contiguous
  *   mean, rstd : (batch, groups) fp32, optional outputs: what the gradient takes
  *   dim in [1, SSM_MAX_GROUP_DIM], a multiple of groups; eps finite and >= 0
- *   (SSM_ERR_VALUE).  Sums of a group over several rows are fp64.  Workspace:
+ *   (SSM_ERR_VALUE).  Over several rows up to 8 neighbouring values are added in
+ *   fp32, the rest in fp64.  Workspace:
  *   ssm_group_norm_workspace_bytes, 256-byte aligned (NULL when that is 0).
  *   batch * rows == 0: nothing is enqueued.
  */

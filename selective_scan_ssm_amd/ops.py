@@ -8,6 +8,7 @@ RuntimeError.  Every step of the computation runs in the library's kernels.
 from __future__ import annotations
 
 import array
+import functools
 import operator
 from typing import Optional
 
@@ -983,6 +984,12 @@ def _norm_view(x, name):
     return x.shape[0], n, x.shape[-1]
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(bwd, N, R, C, groups):
+    lib = _lib.load()
+    return (lib.ssm_group_norm_bwd_workspace_bytes if bwd else lib.ssm_group_norm_workspace_bytes)(N, R, C, groups)
+
+
 def group_norm(x, groups, weight=None, bias=None, z=None, activation=None, eps=1e-5, return_stats=False, out=None,
                workspace=None):
     """Group norm over a channels-last tensor, with an activation and a gate.
@@ -991,7 +998,7 @@ def group_norm(x, groups, weight=None, bias=None, z=None, activation=None, eps=1
     every token's groups apart).  y = act((x - mean) * rstd * weight + bias) *
     SiLU(z): activation None or "silu", z like x (no factor without it); weight,
     bias: (dim,) fp32, 1 and 0 without.  Returns y (contiguous), or (y, mean, rstd)
-    with mean, rstd (batch, groups) fp32 for group_norm_bwd."""
+    with mean, rstd (batch, groups) fp32 for group_norm_bwd (NaN where there are no rows)."""
     lib = _lib.load()
     io, dev, shape = x.dtype, _device(x, "x"), x.shape
     if io not in _IO:
@@ -1004,8 +1011,11 @@ def group_norm(x, groups, weight=None, bias=None, z=None, activation=None, eps=1
     y, py = _out(out, "out", x, io, shape, dev)
     mean = rstd = None
     if return_stats:
-        mean, rstd = (torch.empty((N, groups), dtype=torch.float32, device=dev) for _ in range(2))
-    ws, pws = _scratch(lib.ssm_group_norm_workspace_bytes(N, R, C, groups), "ssm_group_norm_workspace_bytes", workspace, dev)
+        mean = torch.empty((N, groups), dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
+        if not R:                                              # statistics of nothing
+            mean.fill_(float("nan")), rstd.fill_(float("nan"))
+    ws, pws = _scratch(_norm_bytes(False, N, R, C, groups), "ssm_group_norm_workspace_bytes", workspace, dev)
     rc = _run(dev, lib.ssm_group_norm_fwd, px, ldx, pz, ldz, _arg(weight, "weight", torch.float32, (C,), dev),
               _arg(bias, "bias", torch.float32, (C,), dev), py, _ptr(mean), _ptr(rstd), N, R, C, groups, eps,
               _ACTIVATIONS[activation], _IO[io], pws, 0 if ws is None else ws.numel())
@@ -1029,7 +1039,7 @@ def group_norm_bwd(dy, x, mean, rstd, groups, weight=None, bias=None, z=None, ac
     new = lambda size, dtype: torch.empty(size, dtype=dtype, device=dev)
     dx, dz = new(shape, io), new(shape, io) if z is not None else None
     dw, db = (new((C,), torch.float32) if t is not None else None for t in (weight, bias))
-    ws, pws = _scratch(lib.ssm_group_norm_bwd_workspace_bytes(N, R, C, groups), "ssm_group_norm_bwd_workspace_bytes", workspace,
+    ws, pws = _scratch(_norm_bytes(True, N, R, C, groups), "ssm_group_norm_bwd_workspace_bytes", workspace,
                        dev)
     rc = _run(dev, lib.ssm_group_norm_bwd, _arg(dy, "dy", io, shape, dev), px, ldx, pz, ldz,
               _arg(weight, "weight", torch.float32, (C,), dev), _arg(bias, "bias", torch.float32, (C,), dev),
