@@ -648,8 +648,8 @@ size_t ssm_grad_norm_workspace_bytes(int64_t count);
  *   Sizes (SSM_ERR_SHAPE): nheads a multiple of nkheads; dstate a multiple of 8 up
  *   to 128; headdim a multiple of 8; ld* a multiple of 16 bytes and at least the
  *   heads' width where there is more than one step; 64 steps of each tensor span
- *   less than 2 GiB (of v and y, of a state too, in fp32); fewer than 2^24 workgroups, one per
- *   chunk (or sequence), head and 64 channels.  scale finite (SSM_ERR_VALUE).  All tensors
+ *   less than 2 GiB (of v and y, of a state too, in fp32); at most 7456540 workgroups, one
+ *   per chunk (or sequence), head and 64 channels.  scale finite (SSM_ERR_VALUE).  All tensors
  *   16-byte aligned but g, beta and starts.  Workspace:
  *   ssm_delta_scan_workspace_bytes, 256-byte aligned.  Sums are added in a fixed
  *   order: results are deterministic.

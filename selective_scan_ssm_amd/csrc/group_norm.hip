@@ -269,14 +269,18 @@ struct Runs {
 };
 // Whole entries: a thread holds up to kHeld vectors of x (and z), the gradient half as
 // many (beside dy's, and the sums), and a block is the fewest groups that are eight
-// vectors wide (128 bytes at full width: a cache line).
+// vectors wide (128 bytes at full width: a cache line) and, of few rows, give every thread one.
 constexpr int kHeld = 8, kHeldGrad = 4;
 Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V, int held, int target) {
     const int D = static_cast<int>(dim / groups), most = kLanes * V;
     Runs r{};
     r.D = D;
     r.per_group = 1;
-    const int64_t want = (8 * V + D - 1) / D, few = want < groups ? want : groups, few_lanes = few * D / V;
+    const int64_t lanes1 = (D + V - 1) / V, busy = rows > 0 ? (kRunThreads < kLanes * rows ? kRunThreads / rows : kLanes) / lanes1 : 0;
+    int64_t few = (8 * V + D - 1) / D;
+    few = few > busy ? few : busy;
+    few = few < groups ? few : groups;
+    const int64_t few_lanes = few * lanes1;
     if (few_lanes <= kLanes && rows <= kRunThreads / few_lanes * held) {
         r.bc = static_cast<int>(few * D);
         r.blocks = static_cast<int>((groups + few - 1) / few);
@@ -798,7 +802,11 @@ size_t chan_bytes(int64_t batch, const Runs &r, int64_t dim) { return align256(s
 size_t part_bytes(int64_t batch, const Runs &r, int64_t groups) {
     return r.whole ? 0 : align256(static_cast<size_t>(batch * r.runs * groups * r.per_group) * 16);
 }
-dim3 grid_of(int64_t batch, const Runs &r) { return dim3(static_cast<unsigned>(r.blocks * r.runs), static_cast<unsigned>(batch < 65535 ? batch : 65535)); }
+// batch entries on y, as many as a launch's 2^32 lanes allow
+dim3 grid_of(int64_t batch, const Runs &r) {
+    const int64_t x = static_cast<int64_t>(r.blocks) * r.runs, fit = ((int64_t(1) << 32) - 1) / (x * kRunThreads), most = fit < 65535 ? fit : 65535;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(batch < most ? batch : most));
+}
 
 template <typename T, int V> hipError_t run_fwd(const GroupNormArgs &a, hipStream_t s) {
     if (row_form(a.rows, a.dim, a.groups, V)) {

@@ -1014,7 +1014,8 @@ def group_norm(x, groups, weight=None, bias=None, z=None, activation=None, eps=1
         mean = torch.empty((N, groups), dtype=torch.float32, device=dev)
         rstd = torch.empty_like(mean)
         if not R:                                              # statistics of nothing
-            mean.fill_(float("nan")), rstd.fill_(float("nan"))
+            mean.fill_(float("nan"))
+            rstd.fill_(float("nan"))
     ws, pws = _scratch(_norm_bytes(False, N, R, C, groups), "ssm_group_norm_workspace_bytes", workspace, dev)
     rc = _run(dev, lib.ssm_group_norm_fwd, px, ldx, pz, ldz, _arg(weight, "weight", torch.float32, (C,), dev),
               _arg(bias, "bias", torch.float32, (C,), dev), py, _ptr(mean), _ptr(rstd), N, R, C, groups, eps,

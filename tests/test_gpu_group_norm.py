@@ -142,7 +142,9 @@ def test_one_row(ops, N, C, G, dtype):
 MAPS = [(1, 2, 8, 1), (2, 3, 24, 3), (3, 196, 96, 8), (1, 1000, 6, 2), (2, 49, 320, 32), (1, 64, 2304, 4), (4, 9, 33, 11), (2, 777, 192, 32),
         (1, 5, 5000, 1), (1, 4096, 64, 4), (40, 16, 16, 16), (2, 30, 9000, 3), (1, 3, 4098, 2),
         # around the most rows of a batch entry whose groups stay in registers, forward and gradient
-        (2, 256, 64, 4), (1, 257, 64, 4), (2, 512, 64, 8), (1, 513, 64, 8), (3, 600, 20, 2)]
+        (2, 256, 64, 4), (1, 257, 64, 4), (2, 512, 64, 8), (1, 513, 64, 8), (3, 600, 20, 2),
+        # few rows of many groups
+        (5, 2, 1536, 12), (3, 4, 40, 40), (2, 2, 2056, 2), (1, 3, 1000, 500)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -205,6 +207,17 @@ def test_empty(ops):
         y, mean, rstd = ops.group_norm(x, 2, w, w, return_stats=True)
         got = ops.group_norm_bwd(x, x, mean, rstd, 2, w, w)
         assert y.shape == shape and not bool(got["dweight"].any()) and not bool(got["dbias"].any())
+        assert bool(torch.isnan(mean).all()) and bool(torch.isnan(rstd).all())
+
+
+def test_many_groups_of_one_channel(ops):
+    """Groups of one channel over more batch entries than a launch's second axis holds."""
+    t = inputs(66000, 2, 16, torch.float32)
+    y, mean, rstd = ops.group_norm(t["x"], 16, t["weight"], t["bias"], return_stats=True)
+    m = t["x"].double().mean(1)
+    assert float((mean.double() - m).abs().max()) <= 10 * EPS * float(t["x"].abs().max())
+    again = ops.group_norm(t["x"][65990:], 16, t["weight"], t["bias"])
+    assert torch.equal(again, y[65990:])
 
 
 def test_large_batches_and_wide_offsets(ops):
