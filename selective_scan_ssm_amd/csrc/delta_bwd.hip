@@ -353,81 +353,72 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 }
 
 // -------------------------------------------------------------------- the rest
-// A workgroup per (chunk, key head), over the value heads that share it; a pair of
-// waves (w, w + 4) owns 16 of the chunk's steps as columns of transposed results (rows
-// are the K channels), each wave half of the channels: a lane holds eight neighbouring
-// channels of one step, so stores have 16 bytes and the row sums of dg and dbeta are sums
-// inside a lane.  Of the chunk's four decayed products wave w makes the two with the
-// pair's steps as t, wave w + 4 the two with them as s; they exchange them through LDS.
-// The value channels are taken 32 at a time, the next ones loaded meanwhile.
-constexpr int kGradThreads = 512;
+// A workgroup takes (chunk, key head) after (chunk, key head), over the value heads that
+// share it; a pair of waves (w, w + 4) owns 16 of the chunk's steps as columns of
+// transposed results (rows are the K channels), each wave half of the channels: a lane
+// holds eight neighbouring channels of one step, so stores have 16 bytes and the row
+// sums of dg and dbeta are sums inside a lane.  Of the chunk's four decayed products
+// wave w makes the two with the pair's steps as t, wave w + 4 the two with them as s;
+// they exchange them through LDS.
+//
+// The value channels are taken 32 at a time.  Four more waves bring them from global
+// memory, as operands, into one of two LDS buffers: a wave that computes and loads
+// stands still for as long as its loads queue, which at the memory's rate is longer than
+// all it computes.  3072 chunks of 128 x 128 (bytes: 148 us): every wave loading for itself
+// 404 us with four waves, 267 with eight.
+constexpr int kGradThreads = 768, kGradWaves = 8;
 
-// half of a computed operand's eight elements in LDS
-template <typename T> __device__ __forceinline__ void put_half(char *p, int lane, int half, f32x4 v);
-template <> __device__ __forceinline__ void put_half<float>(char *p, int lane, int half, f32x4 v) {
-    *reinterpret_cast<f32x4 *>(p + half * 1024 + lane * 16) = v;
-}
-template <> __device__ __forceinline__ void put_half<bf16_t>(char *p, int lane, int half, f32x4 v) {
-    const u32x2 hi = {pack2(v[0], v[1]), pack2(v[2], v[3])};
-    *reinterpret_cast<u32x2 *>(p + lane * 16 + half * 8) = hi;
-    *reinterpret_cast<u32x2 *>(p + 1024 + lane * 16 + half * 8) =
-        u32x2{pack2(v[0] - low(hi[0]), v[1] - high(hi[0])), pack2(v[2] - low(hi[1]), v[3] - high(hi[1]))};
-}
-
-// What a thread holds of 32 value channels: two channels of four rows of S and of dS', one
-// row's eight channels of dX (waves 0 .. 3) or R (waves 4 .. 7) and of dY (waves 0 .. 3).
+// What a loading thread holds of 32 value channels: two channels of eight rows of S and of
+// dS', one row's eight channels of dX, R and dY.
 template <typename T, int KP> struct GradStage {
-    static constexpr int kSlots = 2 * KP;                  // two channels of eight rows each, in halves
-    f32x2 s[4], d[4];
-    f32x4 x[2];
+    static constexpr int kSlots = 2 * KP;
+    f32x2 s[8], d[8];
+    f32x4 x[2], r[2];
     Op<T> y;
-    struct At {
-        uint32_t state, value, out, row;                   // offsets of value channel 0
-        int v4, v8;                                        // the first value channels of the halves and the eights
-    };
-    static __device__ __forceinline__ At at(int64_t ldy, int K, int V, int n) {
-        const int i = threadIdx.x % kSlots, tile = i / 32, c = 2 * (i % 8), half = threadIdx.x / kSlots;
-        const int k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4;
-        const int lane = threadIdx.x % 64, t = row_index(threadIdx.x / 64 % 4, lane % 16);
-        At o;
-        o.v4 = 8 * ((i / 8) % 4) + 4 * half;
-        o.v8 = 8 * (lane / 16);
-        o.state = half < 2 && k < K ? static_cast<uint32_t>((o.v4 * K + k) * 4) : kOffNone;
-        o.row = static_cast<uint32_t>(K * 4);
-        o.value = static_cast<uint32_t>((t * V + o.v8) * 4);
-        o.out = t < n && threadIdx.x < 256 ? static_cast<uint32_t>((t * ldy + o.v8) * static_cast<int64_t>(sizeof(T))) : kOffNone;
-        return o;
+    int i, v8;                                             // of the 256 threads; the first value channel
+    uint32_t state, row, value, out;                       // offsets of value channel 0
+    __device__ __forceinline__ GradStage(int thread, int64_t ldy, int K, int V) : i(thread) {
+        const int c = 2 * (i % 8), tile = i / 32, k = 32 * (tile / 2) + 8 * (c / 4) + 4 * (tile % 2) + c % 4;
+        const int t = row_index(i / 64, i % 16);
+        v8 = 8 * (i / 16 % 4);
+        state = i < kSlots && k < K ? static_cast<uint32_t>((8 * (i / 8 % 4) * K + k) * 4) : kOffNone;
+        row = static_cast<uint32_t>(K * 4);
+        value = static_cast<uint32_t>((t * V + v8) * 4);
+        out = static_cast<uint32_t>((t * ldy + v8) * static_cast<int64_t>(sizeof(T)));
     }
-    __device__ __forceinline__ void load(rsrc_t rs, rsrc_t rd, rsrc_t rx, rsrc_t ry, const At &o, int v0, int V) {
-        const uint32_t state = o.state == kOffNone ? kOffNone : o.state + static_cast<uint32_t>(v0) * o.row;
+    __device__ __forceinline__ void load(rsrc_t rs, rsrc_t rd, rsrc_t rx, rsrc_t rr, rsrc_t ry, int v0, int V) {
+        const int v = v0 + 8 * (i / 8 % 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t off = v0 + o.v4 + j < V ? state + j * o.row : kOffNone;
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t off = state != kOffNone && v + j < V ? state + (v0 + j) * row : kOffNone;
             s[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
             d[j] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rd, off, 0, 0));
         }
-        const bool in = v0 + o.v8 < V;
-        const uint32_t off = in ? o.value + static_cast<uint32_t>(v0 * 4) : kOffNone;
+        const bool in = v0 + v8 < V;
+        const uint32_t off = in ? value + static_cast<uint32_t>(v0 * 4) : kOffNone;
         x[0] = load4(rx, off);
         x[1] = load4(rx, off + 16);
-        y = load_op(ry, in && o.out != kOffNone ? o.out + static_cast<uint32_t>(v0 * static_cast<int>(sizeof(T))) : kOffNone, T());
+        r[0] = load4(rr, off);
+        r[1] = load4(rr, off + 16);
+        y = load_op(ry, in ? out + static_cast<uint32_t>(v0 * static_cast<int>(sizeof(T))) : kOffNone, T());
     }
     // into LDS as operands; the thread's part of <S, dS'>
-    __device__ __forceinline__ float put(char *sS, char *sD, char *sX, char *sY) const {
-        const int i = threadIdx.x % kSlots, half = threadIdx.x / kSlots, lane = threadIdx.x % 64, w = threadIdx.x / 64;
+    __device__ __forceinline__ float put(char *sX, char *sR, char *sS, char *sD, char *sY) const {
+        const int lane = i % 64, w = i / 64;
         float dot = 0.0f;
+        if (i < kSlots) {
+            const int to = i / 32 * kOp2Bytes, at = 16 * (i / 8 % 4) + 2 * (i % 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dot = fmaf(s[j][0], d[j][0], fmaf(s[j][1], d[j][1], dot));
-        if (half < 2) {
-            const int to = i / 32 * kOp2Bytes, at = 16 * ((i / 8) % 4) + 2 * (i % 8);
+            for (int j = 0; j < 8; ++j) dot = fmaf(s[j][0], d[j][0], fmaf(s[j][1], d[j][1], dot));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                put_half<T>(sS + to, at + h, half, f32x4{s[0][h], s[1][h], s[2][h], s[3][h]});
-                put_half<T>(sD + to, at + h, half, f32x4{d[0][h], d[1][h], d[2][h], d[3][h]});
+                put_op(sS + to, at + h, computed<T>(f32x4{s[0][h], s[1][h], s[2][h], s[3][h]}, f32x4{s[4][h], s[5][h], s[6][h], s[7][h]}));
+                put_op(sD + to, at + h, computed<T>(f32x4{d[0][h], d[1][h], d[2][h], d[3][h]}, f32x4{d[4][h], d[5][h], d[6][h], d[7][h]}));
             }
         }
         put_op(sX + w * kOp2Bytes, lane, computed<T>(x[0], x[1]));
-        if (w < 4) put_op(sY + w * kOpBytes<T>, lane, y);
+        put_op(sR + w * kOp2Bytes, lane, computed<T>(r[0], r[1]));
+        put_op(sY + w * kOpBytes<T>, lane, y);
         return dot;
     }
 };
@@ -474,213 +465,314 @@ __device__ __forceinline__ void store_keys(const BwdParams &p, const f32x4 *dq, 
     }
 }
 
-// LDS: what the loop over the value channels reads, then the decayed products in its
-// place; the chunk's keys and queries
-template <typename T, int KP> constexpr int grad_loop() { return 4 * kOpBytes<T> + 8 * kOp2Bytes + 2 * (KP / 16) * kOp2Bytes; }
-template <typename T, int KP> constexpr int grad_main() { return grad_loop<T, KP>() > 24 * kOp2Bytes ? grad_loop<T, KP>() : 24 * kOp2Bytes; }
-template <typename T, int KP> constexpr size_t grad_lds() { return grad_main<T, KP>() + 2 * QSide<T, KP>::kBytes; }
+// LDS: buffers of 32 value channels, the decayed products in place of the last; the
+// chunk's keys and queries.  Two buffers but for the widest fp32 form.
+template <typename T, int KP> struct GradBuf {
+    static constexpr int x = 0, r = 4 * kOp2Bytes, s = 8 * kOp2Bytes, d = s + KP / 16 * kOp2Bytes, y = d + KP / 16 * kOp2Bytes;
+    static constexpr int loop = y + 4 * kOpBytes<T>, bytes = loop > 24 * kOp2Bytes ? loop : 24 * kOp2Bytes;
+    static constexpr int ft = 0, et = 6 * kOp2Bytes, f = 12 * kOp2Bytes, e = 18 * kOp2Bytes;
+    static constexpr int n = sizeof(T) == 4 && KP > 64 ? 1 : 2;
+    static constexpr int k = n * bytes, q = k + QSide<T, KP>::kBytes, all = q + QSide<T, KP>::kBytes;
+};
+// eight channels of one step, channels 32 kk + 8 g ..: bf16 has them as rows in LDS
+__device__ __forceinline__ Op<bf16_t> own_row(const char *rows, int tile, int lane, rsrc_t, uint32_t, bf16_t) {
+    return get_row(rows + tile * kRowBytes<bf16_t>, lane, bf16_t());
+}
+__device__ __forceinline__ Op<float> own_row(const char *, int, int, rsrc_t r, uint32_t off, float) { return load_op(r, off, 0.0f); }
 
 template <typename T, int KP, bool SHARED>
-__global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(BwdParams p) {
+__global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3, 3))) void delta_grad_kernel(BwdParams p) {
     using D = Decay<T>;
     using real = typename D::real;
+    using B = GradBuf<T, KP>;
     constexpr int KT = KP / 32, KK = KP / 64, OB = kOpBytes<T>;    // a wave's half of the channels
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    char *const sX = smem, *const sR = sX + 4 * kOp2Bytes, *const sS = sR + 4 * kOp2Bytes, *const sD = sS + 2 * KT * kOp2Bytes,
-         *const sY = sD + 2 * KT * kOp2Bytes;
-    char *const sFT = smem, *const sET = sFT + 6 * kOp2Bytes, *const sF = sET + 6 * kOp2Bytes, *const sE = sF + 6 * kOp2Bytes;
-    char *const sC = smem + grad_main<T, KP>(), *const sQ = sC + QSide<T, KP>::kBytes;
+    char *const sC = smem + B::k, *const sQ = smem + B::q;
     __shared__ real sG[kC];
-    __shared__ float sB[kC], sQK[2][kC], sZ[2][kC], sTot[8];
+    __shared__ float sScal[3 * kC], sQK[2][kC], sZ[2][kC], sTot[kGradWaves], sDot[4];
+    const float *const sB = sScal + 2 * kC;
     const DeltaArgs &a = p.b.fwd;
-    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = wave % 4, wh = wave / 4;
-    const int g = lane / 16, c = lane % 16, t = row_index(w, c);
-    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
-    const int64_t H = a.s.heads, slot = blockIdx.x / a.s.kheads, kh = blockIdx.x % a.s.kheads;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv), stages = (V + 31) / 32;
+    const int64_t H = a.s.heads, units = a.s.slots * a.s.kheads;
     const int group = static_cast<int>(H / a.s.kheads);
-    const int64_t seq = sequence_of(a.s, slot);
-    const Span sp = span_of(a.s, seq);
-    const int64_t step0 = (slot - sp.slot0) * kC;
-    if (step0 < 0 || step0 >= sp.len) return;
-    const int n = sp.len - step0 < kC ? static_cast<int>(sp.len - step0) : kC;
-    const int64_t row0 = sp.row0 + step0;
-    const f32x4 zero = {0, 0, 0, 0};
     const size_t VK = static_cast<size_t>(V) * K;
-    const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, sizeof(T));
-    const rsrc_t rq = chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, sizeof(T));
-    const auto at = GradStage<T, KP>::at(H * V, K, V, n);
-    GradStage<T, KP> st;
-    auto load = [&](int64_t head, int v0) {
-        const int64_t unit = slot * H + head;
-        const float *const saved = a.ckpt + unit * (VK + kC * V);
-        st.load(make_rsrc(saved, static_cast<uint32_t>(VK * 4)), make_rsrc(p.dS + unit * VK, static_cast<uint32_t>(VK * 4)),
-                make_rsrc(wh ? saved + VK : p.dX + unit * kC * V), make_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V), at, v0, V);
+    struct Place {
+        int64_t id, slot, kh, row0;                        // id < 0: none
+        int n;
     };
-    {
-        QSide<T, KP> side;
-        const int64_t ld = wh ? a.ldq : a.ldk;
-        side.load(wh ? rq : rk, ld, QSide<T, KP>::offsets(ld, K, threadIdx.x % kThreads));
-        load(kh * group, 0);
-        side.put(wh ? sQ : sC, threadIdx.x % kThreads);
+    auto find = [&](int64_t id) {                            // the workgroup's next (chunk, key head)
+        Place c{};
+        for (; id < units; id += gridDim.x) {
+            c.slot = id / a.s.kheads;
+            c.kh = id % a.s.kheads;
+            const Span sp = span_of(a.s, sequence_of(a.s, c.slot));
+            const int64_t step0 = (c.slot - sp.slot0) * kC;
+            if (step0 < 0 || step0 >= sp.len) continue;
+            c.n = sp.len - step0 < kC ? static_cast<int>(sp.len - step0) : kC;
+            c.row0 = sp.row0 + step0;
+            c.id = id;
+            return c;
+        }
+        c.id = -1;
+        return c;
+    };
+    auto rows_of = [&](const void *t, int64_t ld, const Place &c) {
+        return chunk_rsrc(static_cast<const T *>(t) + c.row0 * ld + c.kh * K, c.n, ld, K, sizeof(T));
+    };
+    auto buffer = [&](int i) { return smem + (B::n == 2 ? i % 2 : 0) * B::bytes; };
+    Place here = find(blockIdx.x);
+    if (here.id < 0) return;
+    int at = 0;                                              // stages so far
+
+    // Barriers of a head, which all twelve waves pass: one per stage (it is in LDS, and the one before done with; with
+    // one buffer a second, done with this one), the loop's end, the decayed products, the end.
+    if (wave >= kGradWaves) {                                // the loading waves
+        const int thread = threadIdx.x - 64 * kGradWaves, pw = wave - kGradWaves;
+        GradStage<T, KP> st(thread, H * V, K, V);
+        auto load = [&](const Place &c, int64_t head, int v0) {
+            const int64_t unit = c.slot * H + head;
+            const float *const saved = a.ckpt + unit * (VK + kC * V);
+            st.load(make_rsrc(saved, static_cast<uint32_t>(VK * 4)), make_rsrc(p.dS + unit * VK, static_cast<uint32_t>(VK * 4)),
+                    make_rsrc(p.dX + unit * kC * V), make_rsrc(saved + VK),
+                    chunk_rsrc(static_cast<const T *>(p.b.dout) + (c.row0 * H + head) * V, c.n, H * V, V, sizeof(T)), v0, V);
+        };
+        auto put = [&](int i) {
+            char *const to = buffer(i);
+            return st.put(to + B::x, to + B::r, to + B::s, to + B::d, to + B::y);
+        };
+        const auto ok = QSide<T, KP>::offsets(a.ldk, K, thread), oq = QSide<T, KP>::offsets(a.ldq, K, thread);
+        load(here, here.kh * group, 0);
+        float tot = put(0);
+        while (true) {
+            const Place next = find(here.id + gridDim.x);
+            QSide<T, KP> k, q;
+            k.load(rows_of(a.k, a.ldk, here), a.ldk, ok);
+            q.load(rows_of(a.q, a.ldq, here), a.ldq, oq);
+            for (int hh = 0; hh < group; ++hh) {
+                const int64_t head = here.kh * group + hh, unit = here.slot * H + head;
+                const bool more = hh + 1 < group || next.id >= 0;
+                float step = 0.0f, scal[3];
+                if (pw == 0) {
+                    if (lane < here.n) step = a.g[(here.row0 + lane) * H + head];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) scal[i] = p.ws.scal[unit * 3 * kC + i * kC + lane];
+                }
+                for (int i = 0; i < stages; ++i, ++at) {
+                    if (i + 1 < stages) load(here, head, 32 * (i + 1));
+                    else if (hh + 1 < group) load(here, head + 1, 0);
+                    else if (next.id >= 0) load(next, next.kh * group, 0);
+                    flow_barrier();
+                    // what the head's end needs, now that everyone is done with the head before
+                    if (i + 1 == stages) {
+                        tot = wave_fold(tot, AddOp());
+                        if (lane == 0) sDot[pw] = tot;
+                    }
+                    if (i == 0) {
+                        if (hh == 0) {
+                            k.put(sC, thread);
+                            q.put(sQ, thread);
+                        }
+                        if (pw == 0) {
+                            sG[lane] = lane_prefix<real>(lane < here.n ? D::scaled(step_log(step)) : real(0), lane);
+#pragma unroll
+                            for (int j = 0; j < 3; ++j) sScal[j * kC + lane] = scal[j];
+                        }
+                    }
+                    if (B::n == 1) flow_barrier();
+                    if (i + 1 < stages) tot += put(at + 1);
+                }
+                if (B::n == 2) flow_barrier();
+                flow_barrier();
+                if (B::n == 2 && more) tot = put(at);
+                flow_barrier();
+                if (B::n == 1 && more) tot = put(at);
+            }
+            if (next.id < 0) return;
+            here = next;
+        }
     }
-    f32x4 dqs[SHARED ? KT : 1], dks[SHARED ? KT : 1];
-    if constexpr (SHARED) {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) dqs[i] = dks[i] = zero;
-    }
-    for (int hh = 0; hh < group; ++hh) {
-        const int64_t head = kh * group + hh, unit = slot * H + head;
-        const float *const scal = p.ws.scal + unit * 3 * kC;
-        if (wave == 0) {
-            const real G = lane_prefix<real>(lane < n ? D::scaled(step_log(a.g[(row0 + lane) * H + head])) : real(0), lane);
-            sG[lane] = G;
-            sB[lane] = scal[2 * kC + lane];
-        }
-        const float eg = scal[t], wt = scal[kC + t], end = scal[kC - 1];
-        // A: (F diag(beta))^T or F, B: M^T or -E
-        f32x4 dq[KT], ke[KT], kw[KT], A[4], B[4];
-#pragma unroll
-        for (int i = 0; i < KT; ++i) dq[i] = ke[i] = kw[i] = zero;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) A[i] = B[i] = zero;
-        float tot = 0.0f;
-        for (int v0 = 0; v0 < V; v0 += 32) {
-            tot += st.put(sS, sD, sX, sY);                   // sX's waves 4 .. 7 write sR
-            if (v0 + 32 < V) load(head, v0 + 32);
-            else if (hh + 1 < group) load(head + 1, 0);
-            __syncthreads();
-            const Op<T> y = get_op(sY + w * OB, lane, T());
-            const Op2<T> x = get_op2(sX + w * kOp2Bytes, lane, T()), r = get_op2(sR + w * kOp2Bytes, lane, T());
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const Op2<T> s = get_op2(sS + (wh * KT + kt) * kOp2Bytes, lane, T()), d = get_op2(sD + (wh * KT + kt) * kOp2Bytes, lane, T());
-                dq[kt] = mma(s, y, dq[kt]);
-                ke[kt] = mma(s, x, ke[kt]);
-                kw[kt] = mma(d, r, kw[kt]);
-            }
-#pragma unroll
-            for (int ob = 0; ob < 4; ++ob) {
-                if (wh == 0 && ob / 2 <= w / 2) {            // rows s at or before the pair's steps
-                    const Op2<T> ro = get_op2(sR + ob * kOp2Bytes, lane, T());
-                    A[ob] = mma(ro, y, A[ob]);
-                    B[ob] = mma(ro, x, B[ob]);
-                }
-                if (wh == 1 && ob / 2 >= w / 2) {            // rows t at or behind them
-                    A[ob] = mma(get_op(sY + ob * OB, lane, T()), r, A[ob]);
-                    B[ob] = mma(get_op2(sX + ob * kOp2Bytes, lane, T()), r, B[ob]);
-                }
-            }
-            __syncthreads();
-        }
-        const float beta = sB[t];
-        const real gt = sG[t];
-#pragma unroll
-        for (int ob = 0; ob < 4; ++ob)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s or t
-                const bool in = wh ? o >= t : o <= t;
-                const float d = in ? D::ex(wh ? sG[o] - gt : gt - sG[o]) * (wh ? 1.0f : sB[o]) : 0.0f;
-                A[ob][i] = in ? A[ob][i] * (a.scale * d) : 0.0f;
-                B[ob][i] = in && o != t ? B[ob][i] * -d : 0.0f;
-            }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            if (wh == 0 && kk <= w / 2) {
-                put_op(sFT + tri_low(w, kk) * kOp2Bytes, lane, computed<T>(A[2 * kk], A[2 * kk + 1]));
-                put_op(sET + tri_low(w, kk) * kOp2Bytes, lane, computed<T>(B[2 * kk], B[2 * kk + 1]));
-            }
-            if (wh == 1 && kk >= w / 2) {
-                put_op(sF + tri_up(w, kk) * kOp2Bytes, lane, computed<T>(A[2 * kk], A[2 * kk + 1]));
-                put_op(sE + tri_up(w, kk) * kOp2Bytes, lane, computed<T>(B[2 * kk], B[2 * kk + 1]));
-            }
-        }
-        float qd = 0.0f, kd = 0.0f, kz = 0.0f, kc = 0.0f;
-        const float fq = a.scale * eg;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            dq[kt] = dq[kt] * fq;
-            ke[kt] = ke[kt] * -eg;
-            kw[kt] = kw[kt] * wt;                            // Z
-        }
-        float kv[KK][8], qv[KK][8];
-#pragma unroll
-        for (int kp = 0; kp < KK; ++kp) {
-            const int k0 = 32 * (wh * KK + kp) + 8 * g;
-            floats(load_op(rk, k0 < K ? static_cast<uint32_t>((t * a.ldk + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()), kv[kp]);
-            floats(load_op(rq, k0 < K ? static_cast<uint32_t>((t * a.ldq + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone, T()), qv[kp]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kp = 0; kp < KK; ++kp)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) kc = fmaf(kv[kp][4 * h + i], kw[2 * kp + h][i], kc);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            if (kk <= w / 2) {
-                const Op2<T> ft = get_op2(sFT + tri_low(w, kk) * kOp2Bytes, lane, T()), et = get_op2(sET + tri_low(w, kk) * kOp2Bytes, lane, T());
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const Op<T> kcol = get_col<KP>(sC, sC, wh * KT + kt, kk, lane, T());
-                    dq[kt] = mma(kcol, ft, dq[kt]);
-                    ke[kt] = mma(kcol, et, ke[kt]);
-                }
-            }
-            if (kk >= w / 2) {
-                const Op2<T> f = get_op2(sF + tri_up(w, kk) * kOp2Bytes, lane, T()), e = get_op2(sE + tri_up(w, kk) * kOp2Bytes, lane, T());
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    kw[kt] = mma(get_col<KP>(sQ, sQ, wh * KT + kt, kk, lane, T()), f, kw[kt]);
-                    kw[kt] = mma(get_col<KP>(sC, sC, wh * KT + kt, kk, lane, T()), e, kw[kt]);
-                }
-            }
-        }
-#pragma unroll
-        for (int kp = 0; kp < KK; ++kp)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int kt = 2 * kp + h;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    qd = fmaf(qv[kp][4 * h + i], dq[kt][i], qd);
-                    kd = fmaf(kv[kp][4 * h + i], ke[kt][i], kd);
-                    kz = fmaf(kv[kp][4 * h + i], kw[kt][i], kz);
-                }
-                ke[kt] = ke[kt] + kw[kt] * beta;
-            }
-        const float qk = column_total(qd + kd), z = column_total(kz);
-        tot = wave_fold(fmaf(end, tot, beta * kc), AddOp());
-        if (lane == 0) sTot[wave] = tot;
-        if (g == 0) {
-            sQK[wh][t] = qk;
-            sZ[wh][t] = z;
-        }
-        __syncthreads();
-        if (wave == 0) {                                     // lane l is step 63 - l: sums from the end
-            const int l = 63 - lane;
-            const float zl = sZ[0][l] + sZ[1][l];
-            double v = static_cast<double>(sQK[0][l]) + sQK[1][l] - static_cast<double>(sB[l]) * zl;
-            if (lane == 0)
-                for (int i = 0; i < 8; ++i) v += sTot[i];
-            v = lane_prefix<double>(v, lane);
-            if (l < n) {
-                p.b.dg[(row0 + l) * H + head] = static_cast<float>(v);
-                p.b.dbeta[(row0 + l) * H + head] = zl;
-            }
-        }
+
+    const int w = wave % 4, wh = wave / 4, g = lane / 16, c = lane % 16, t = row_index(w, c);
+    const f32x4 zero = {0, 0, 0, 0};
+    while (true) {
+        const Place next = find(here.id + gridDim.x);
+        f32x4 dqs[SHARED ? KT : 1], dks[SHARED ? KT : 1];
         if constexpr (SHARED) {
 #pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                dqs[i] = dqs[i] + dq[i];
-                dks[i] = dks[i] + ke[i];
-            }
-        } else {
-            store_keys<T, KP>(p, dq, ke, row0, kh, t, wh, g, n);
+            for (int i = 0; i < KT; ++i) dqs[i] = dks[i] = zero;
         }
+        for (int hh = 0; hh < group; ++hh) {
+            const int64_t head = here.kh * group + hh;
+            // A: (F diag(beta))^T or F, B: M^T or -E
+            f32x4 dq[KT], ke[KT], kw[KT], A[4], E[4];
+#pragma unroll
+            for (int i = 0; i < KT; ++i) dq[i] = ke[i] = kw[i] = zero;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) A[i] = E[i] = zero;
+            for (int i = 0; i < stages; ++i, ++at) {
+                const char *const from = buffer(at);
+                flow_barrier();
+                // operands are read from LDS a product ahead of their use
+                Op2<T> sd[2][2];
+                auto read = [&](int kt) {
+                    sd[kt % 2][0] = get_op2(from + B::s + (wh * KT + kt) * kOp2Bytes, lane, T());
+                    sd[kt % 2][1] = get_op2(from + B::d + (wh * KT + kt) * kOp2Bytes, lane, T());
+                };
+                const Op<T> y = get_op(from + B::y + w * OB, lane, T());
+                const Op2<T> x = get_op2(from + B::x + w * kOp2Bytes, lane, T()), r = get_op2(from + B::r + w * kOp2Bytes, lane, T());
+                read(0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    if (kt + 1 < KT) read(kt + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    dq[kt] = mma(sd[kt % 2][0], y, dq[kt]);
+                    ke[kt] = mma(sd[kt % 2][0], x, ke[kt]);
+                    kw[kt] = mma(sd[kt % 2][1], r, kw[kt]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    if (wh == 0 && kk <= w / 2) {            // rows s at or before the pair's steps
+                        const char *const f = from + B::r + 2 * kk * kOp2Bytes;
+                        const Op2<T> r0 = get_op2(f, lane, T()), r1 = get_op2(f + kOp2Bytes, lane, T());
+                        A[2 * kk] = mma(r0, y, A[2 * kk]);
+                        A[2 * kk + 1] = mma(r1, y, A[2 * kk + 1]);
+                        E[2 * kk] = mma(r0, x, E[2 * kk]);
+                        E[2 * kk + 1] = mma(r1, x, E[2 * kk + 1]);
+                    }
+                    if (wh == 1 && kk >= w / 2) {            // rows t at or behind them
+                        const char *const f = from + B::x + 2 * kk * kOp2Bytes, *const fy = from + B::y + 2 * kk * OB;
+                        const Op<T> y0 = get_op(fy, lane, T()), y1 = get_op(fy + OB, lane, T());
+                        const Op2<T> x0 = get_op2(f, lane, T()), x1 = get_op2(f + kOp2Bytes, lane, T());
+                        A[2 * kk] = mma(y0, r, A[2 * kk]);
+                        A[2 * kk + 1] = mma(y1, r, A[2 * kk + 1]);
+                        E[2 * kk] = mma(x0, r, E[2 * kk]);
+                        E[2 * kk + 1] = mma(x1, r, E[2 * kk + 1]);
+                    }
+                }
+                if (B::n == 1) flow_barrier();
+            }
+            if (B::n == 2) flow_barrier();
+            char *const to = buffer(at - 1);
+            const float eg = sScal[t], wt = sScal[kC + t], beta = sB[t], end = sScal[kC - 1];
+            const real gt = sG[t];
+#pragma unroll
+            for (int ob = 0; ob < 4; ++ob)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s or t
+                    const bool in = wh ? o >= t : o <= t;
+                    const real go = sG[o];                   // no branch: the reads of LDS side by side
+                    const float bo = sB[o], d = D::ex(in ? (wh ? go - gt : gt - go) : real(0)) * (wh ? 1.0f : bo);
+                    A[ob][i] = in ? A[ob][i] * (a.scale * d) : 0.0f;
+                    E[ob][i] = in && o != t ? E[ob][i] * -d : 0.0f;
+                }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                if (wh == 0 && kk <= w / 2) {
+                    put_op(to + B::ft + tri_low(w, kk) * kOp2Bytes, lane, computed<T>(A[2 * kk], A[2 * kk + 1]));
+                    put_op(to + B::et + tri_low(w, kk) * kOp2Bytes, lane, computed<T>(E[2 * kk], E[2 * kk + 1]));
+                }
+                if (wh == 1 && kk >= w / 2) {
+                    put_op(to + B::f + tri_up(w, kk) * kOp2Bytes, lane, computed<T>(A[2 * kk], A[2 * kk + 1]));
+                    put_op(to + B::e + tri_up(w, kk) * kOp2Bytes, lane, computed<T>(E[2 * kk], E[2 * kk + 1]));
+                }
+            }
+            float qd = 0.0f, kd = 0.0f, kz = 0.0f, kc = 0.0f;
+            const float fq = a.scale * eg;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                dq[kt] = dq[kt] * fq;
+                ke[kt] = ke[kt] * -eg;
+                kw[kt] = kw[kt] * wt;                        // Z
+            }
+            flow_barrier();
+            float kv[KK][8], qv[KK][8];
+#pragma unroll
+            for (int kp = 0; kp < KK; ++kp) {
+                const int kk = wh * KK + kp, k0 = 32 * kk + 8 * g, tile = w * (KP / 32) + kk;
+                const uint32_t ok = k0 < K ? static_cast<uint32_t>((t * a.ldk + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+                const uint32_t oq = k0 < K ? static_cast<uint32_t>((t * a.ldq + k0) * static_cast<int64_t>(sizeof(T))) : kOffNone;
+                floats(own_row(sC, tile, lane, rows_of(a.k, a.ldk, here), ok, T()), kv[kp]);
+                floats(own_row(sQ, tile, lane, rows_of(a.q, a.ldq, here), oq, T()), qv[kp]);
+            }
+#pragma unroll
+            for (int kp = 0; kp < KK; ++kp)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kc = fmaf(kv[kp][4 * h + i], kw[2 * kp + h][i], kc);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                if (kk <= w / 2) {
+                    const Op2<T> ft = get_op2(to + B::ft + tri_low(w, kk) * kOp2Bytes, lane, T()), et = get_op2(to + B::et + tri_low(w, kk) * kOp2Bytes, lane, T());
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const Op<T> kcol = get_col<KP>(sC, sC, wh * KT + kt, kk, lane, T());
+                        dq[kt] = mma(kcol, ft, dq[kt]);
+                        ke[kt] = mma(kcol, et, ke[kt]);
+                    }
+                }
+                if (kk >= w / 2) {
+                    const Op2<T> f = get_op2(to + B::f + tri_up(w, kk) * kOp2Bytes, lane, T()), e = get_op2(to + B::e + tri_up(w, kk) * kOp2Bytes, lane, T());
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
+                        kw[kt] = mma(get_col<KP>(sQ, sQ, wh * KT + kt, kk, lane, T()), f, kw[kt]);
+                        kw[kt] = mma(get_col<KP>(sC, sC, wh * KT + kt, kk, lane, T()), e, kw[kt]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int kp = 0; kp < KK; ++kp)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int kt = 2 * kp + h;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        qd = fmaf(qv[kp][4 * h + i], dq[kt][i], qd);
+                        kd = fmaf(kv[kp][4 * h + i], ke[kt][i], kd);
+                        kz = fmaf(kv[kp][4 * h + i], kw[kt][i], kz);
+                    }
+                    ke[kt] = ke[kt] + kw[kt] * beta;
+                }
+            const float qk = column_total(qd + kd), z = column_total(kz);
+            kc = wave_fold(beta * kc, AddOp());
+            if (lane == 0) sTot[wave] = kc;
+            if (g == 0) {
+                sQK[wh][t] = qk;
+                sZ[wh][t] = z;
+            }
+            flow_barrier();
+            if (wave == 0) {                                 // lane l is step 63 - l: sums from the end
+                const int l = 63 - lane;
+                const float zl = sZ[0][l] + sZ[1][l];
+                double v = static_cast<double>(sQK[0][l]) + sQK[1][l] - static_cast<double>(sB[l]) * zl;
+                if (lane == 0) {
+                    v += static_cast<double>(end) * (static_cast<double>(sDot[0]) + sDot[1] + sDot[2] + sDot[3]);
+                    for (int i = 0; i < kGradWaves; ++i) v += sTot[i];
+                }
+                v = lane_prefix<double>(v, lane);
+                if (l < here.n) {
+                    p.b.dg[(here.row0 + l) * H + head] = static_cast<float>(v);
+                    p.b.dbeta[(here.row0 + l) * H + head] = zl;
+                }
+            }
+            if constexpr (SHARED) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    dqs[i] = dqs[i] + dq[i];
+                    dks[i] = dks[i] + ke[i];
+                }
+            } else {
+                store_keys<T, KP>(p, dq, ke, here.row0, here.kh, t, wh, g, here.n);
+            }
+        }
+        if constexpr (SHARED) store_keys<T, KP>(p, dqs, dks, here.row0, here.kh, t, wh, g, here.n);
+        if (next.id < 0) return;
+        here = next;
     }
-    if constexpr (SHARED) store_keys<T, KP>(p, dqs, dks, row0, kh, t, wh, g, n);
 }
 
 // bf16: 64 value channels to a workgroup while the CUs hold them all, else 128
@@ -753,8 +845,9 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
     }
     if (hipError_t e = launch_rev<T, KP>(p, s)) return e;
     if (sh.slots == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(sh.slots * sh.kheads));
-    constexpr size_t glds = grad_lds<T, KP>();
+    constexpr size_t glds = GradBuf<T, KP>::all;
+    const int64_t units = sh.slots * sh.kheads;
+    const dim3 grid(static_cast<unsigned>(units < 256 ? units : 256));       // one to a CU
     if (sh.heads == sh.kheads) hipLaunchKernelGGL((delta_grad_kernel<T, KP, false>), grid, dim3(kGradThreads), glds, s, p);
     else hipLaunchKernelGGL((delta_grad_kernel<T, KP, true>), grid, dim3(kGradThreads), glds, s, p);
     return hipGetLastError();
