@@ -364,8 +364,8 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 // The value channels are taken 32 at a time.  Four more waves bring them from global
 // memory, as operands, into one of two LDS buffers: a wave that computes and loads
 // stands still for as long as its loads queue, which at the memory's rate is longer than
-// all it computes.  3072 chunks of 128 x 128 (bytes: 148 us): every wave loading for itself
-// 404 us with four waves, 267 with eight.
+// all it computes.  3072 chunks of 128 x 128 (bytes: 148 us at a copy's rate): every wave
+// loading for itself 404 us with four waves, 267 with eight; now 227.
 constexpr int kGradThreads = 768, kGradWaves = 8;
 
 // What a loading thread holds of 32 value channels: two channels of eight rows of S and of
@@ -775,7 +775,9 @@ __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3,
     }
 }
 
-// bf16: 64 value channels to a workgroup while the CUs hold them all, else 128
+// bf16: 64 value channels to a workgroup, 128 where only those let every CU have one.
+// Gradient calls, 128 x 128: 8 x 2048 steps of 12 heads (192 narrow workgroups), this kernel 175 us
+// against 247 wide; 16 x 2048 of 12 (384), the call 944 against 899; 24 x 1024 of 12 (576) 656 against 701.
 template <int KP, int NW> hipError_t launch_rev_flow(const BwdParams &p, hipStream_t s) {
     constexpr int wide = 16 * NW;
     const DeltaShape &sh = p.b.fwd.s;
@@ -788,7 +790,8 @@ template <typename T, int KP> hipError_t launch_rev(const BwdParams &p, hipStrea
     const DeltaShape &sh = p.b.fwd.s;
     const int64_t n = (sh.dv + 63) / 64 * sh.heads * sh.nseq;
     if constexpr (sizeof(T) == 2) {
-        return sh.dv > 64 && n > 256 ? launch_rev_flow<KP, 8>(p, s) : launch_rev_flow<KP, 4>(p, s);
+        const bool wide = sh.dv > 64 && n > 256 && (sh.dv + 127) / 128 * sh.heads * sh.nseq <= 256;
+        return wide ? launch_rev_flow<KP, 8>(p, s) : launch_rev_flow<KP, 4>(p, s);
     } else {
         constexpr size_t lds = rev_lds<KP>();
         hipLaunchKernelGGL((delta_rev_kernel<KP>), dim3(static_cast<unsigned>(n)), dim3(kThreads), lds, s, p);

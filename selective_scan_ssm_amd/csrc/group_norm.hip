@@ -11,6 +11,11 @@
 // them there over both passes.  Else a batch entry is cut into runs of rows; the
 // first pass leaves each run's sums in the workspace, and the second adds them up, in a
 // fixed order, and reads the inputs again.
+//
+// Measured (a copy: 5.6 TB/s): 16384 tokens of 40 heads of 128, bf16 with a gate, 503 MB 103 us
+// (4.9 TB/s; 114 without the next row's loads ahead), its gradient at 12 heads 252 MB 53 us; 16 maps of
+// 8192 x 512 27 us for the sums and 59 for the second pass (268 MB); 196 x 96 fp32 in one launch 7 us, in
+// three 14.
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 #include "wave_fold.h"
@@ -442,7 +447,7 @@ __device__ __forceinline__ void put_stats(const GroupNormArgs &a, const Runs &r,
 // Sums of x - x0 and its square over a run, x0 the thread's first value, in fp32 over
 // a vector and fp64 beyond, then of x and x^2: x - x0 is about as large as the group's
 // spread, so a mean far from 0 costs the variance nothing.  (All in fp64 the pass took
-// 35 us over 134 MB instead of 28.)
+// 35 us over 134 MB instead of 27.)
 template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void group_stats_kernel(GroupNormArgs a, Runs r, double *part) {
     __shared__ Totals m;
     for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {

@@ -82,6 +82,19 @@ def test_forward_and_backward(ops, size, dtype):
     check_bwd(ops, t, dlast=T % 4 != 0, ckpt=ck)
 
 
+# more chunks and key heads than CUs, one and several blocks of value channels; more workgroups of 64 value channels than
+# CUs, where those of 128 are fewer
+MANY = [(11, 130, 9, 18, 32, 24), (11, 130, 27, 27, 16, 40), (13, 70, 12, 12, 32, 128), (22, 10, 6, 6, 128, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_more_work_than_the_gpu_holds(ops, size, dtype):
+    t = D.delta_inputs(*size, DT[dtype], seed=5)
+    _, _, ck = check_fwd(ops, t)
+    check_bwd(ops, t, ckpt=ck)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_sequence(ops, dtype):
     t = D.delta_inputs(1, 3000, 1, 2, 64, 32, DT[dtype], packed=True)

@@ -173,11 +173,18 @@ def test_unaligned_bases(ops, R, dtype):
     check(ops, t, 4, silu=True)
 
 
-@pytest.mark.parametrize("R", [1, 50])
+@pytest.mark.parametrize("R", [1, 50, 3000])
 def test_far_means(ops, R):
     """A mean of some thousand standard deviations."""
     t = inputs(2, R, 128, torch.float32, offset=0.0)
     t["x"] = t["x"] + 4096.0
+    check(ops, t, 4)
+
+
+@pytest.mark.parametrize("R", [50, 3000])
+def test_first_values_far_from_the_rest(ops, R):
+    t = inputs(2, R, 128, torch.float32)
+    t["x"][:, :8] = 3e4
     check(ops, t, 4)
 
 
