@@ -506,18 +506,40 @@ template <typename T, int KP> __global__ __launch_bounds__(64) void delta_carry_
     if (ns < 3) return;
     f32x4 S[KT];
     load_state<KP>(S, p.ends + (first * H + head) * VK, v0, V, K, lane);
-    for (int s = 1; s < ns - 1; ++s) {
-        const int64_t at = (first + s) * H + head;
+    // a step is little more than the latency of its loads: as many steps ahead as registers hold
+    constexpr int AHEAD = KP > 64 ? 1 : 3;
+    struct Step {
+        Op2<T> map[KK][KT];
+        f32x4 end[KT];
+    } next[AHEAD];
+    auto fetch = [&](Step &f, int s) {
+        const int64_t at = (first + (s < ns - 1 ? s : ns - 2)) * H + head;
         const char *const m = p.maps + at * kMapBytes<KP>;
-        Op2<T> so[KK];
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(S[2 * kk], S[2 * kk + 1]);
-        load_state<KP>(S, p.ends + at * VK, v0, V, K, lane);
+        load_state<KP>(f.end, p.ends + at * VK, v0, V, K, lane);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) S[kt] = mma(get_op2(m + (kk * KT + kt) * kOp2Bytes, lane, T()), so[kk], S[kt]);
-        store_state<KP>(S, p.ends + at * VK, v0, V, K, lane);
+            for (int kt = 0; kt < KT; ++kt) f.map[kk][kt] = get_op2(m + (kk * KT + kt) * kOp2Bytes, lane, T());
+    };
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) fetch(next[d], 1 + d);
+    for (int s0 = 1; s0 < ns - 1; s0 += AHEAD) {
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            const int s = s0 + d;
+            if (s >= ns - 1) return;
+            Op2<T> so[KK];
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) so[kk] = computed<T>(S[2 * kk], S[2 * kk + 1]);
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) S[kt] = next[d].end[kt];
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) S[kt] = mma(next[d].map[kk][kt], so[kk], S[kt]);
+            store_state<KP>(S, p.ends + ((first + s) * H + head) * VK, v0, V, K, lane);
+            fetch(next[d], s + AHEAD);
+        }
     }
 }
 
