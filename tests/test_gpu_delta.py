@@ -196,6 +196,40 @@ def test_packed_sequences(ops, lens, dtype):
             D.close(ya, yo, DT[dtype], m, "y", size=0.3 * D.rms(st))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 2, 32, 24), (2, 2, 96, 80)], ids=["32x24", "96x80"])
+def test_one_packed_sequence_far_longer_than_the_rest(ops, size, dtype):
+    """Long enough for the longest to be cut in time."""
+    Hk, H, K, V = size
+    lens = [40, 1300, 3, 0, 200, 64, 1, 700]
+    total, io = sum(lens), DT[dtype]
+    t = D.delta_inputs(1, total, Hk, H, K, V, io, n=len(lens), seed=9)
+    at = np.cumsum([0] + lens)
+    starts = torch.tensor(at, dtype=torch.int32, device="cuda")
+    dy, dl = U.rand(50, 1, total, H, V, dtype=io), U.rand(51, len(lens), H, V, K, scale=0.3)
+    ck = torch.empty(ops.delta_ckpt_shape(t["q"], t["v"], starts), device="cuda")
+    kw = dict(scale=0.3, h0=t["h0"], starts=starts)
+    y, last = ops.delta_scan_fwd(*args(t), return_last_state=True, ckpt_out=ck, **kw)
+    got = ops.delta_scan_bwd(*args(t), dy, dlast=dl, **kw)
+    saved = ops.delta_scan_bwd(*args(t), dy, dlast=dl, ckpt=ck, **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[n], saved[n]) for n in got)
+    for i, m in enumerate(lens):
+        rows = slice(int(at[i]), int(at[i + 1]))
+        one = D.host({name: t[name][:, rows] for name in NAMES})
+        h0 = U.f64(t["h0"][i:i + 1])
+        yo, st = M.delta_rule(scale=0.3, h0=h0, **one)
+        D.close(last[i:i + 1], st[-1], io, m, "last", size=D.rms(st))
+        if not m:
+            continue
+        D.close(y[:, rows], yo, io, m, "y", size=0.3 * D.rms(st) * K ** 0.5 * D.rms(one["q"]))
+        want = M.delta_rule_bwd(scale=0.3, dy=U.f64(dy[:, rows]), dlast=U.f64(dl[i:i + 1]), h0=h0, **one)
+        sizes = dict(dg=8.0 * D.rms(want["dg_terms"]), dbeta=D.rms(want["dbeta_terms"]))
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            D.close(got[n][:, rows], want[n], io, m, n, size=sizes.get(n))
+        D.close(got["dh0"][i:i + 1], want["dh0"], io, m, "dh0")
+
+
 def test_many_empty_sequences(ops):
     n = 1000
     at = torch.zeros(n + 1, dtype=torch.int32)
