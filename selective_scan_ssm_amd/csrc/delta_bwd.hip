@@ -14,8 +14,8 @@
 // the key that is written with, before beta; dbeta needs neither dU nor a division.
 //
 // Launches: the chunks' preparation; without saved ones, the states entering the
-// chunks and R, in a walk over the chunks; dS' and dX, in reverse; the rest, all
-// chunks at once.
+// chunks and R, in a walk over the chunks; dS' and dX, in a walk backwards, cut into
+// time segments as the forward is; the rest, all chunks at once.
 #include "delta_flow.h"
 
 namespace ssm {
@@ -26,7 +26,68 @@ struct BwdParams {
     DeltaBwdArgs b;
     ChunkWs ws;
     float *dX, *dS;                // per (slot, head): (64, V), (V, K)
+    SeqParams seq;                 // the time segments, their ends and transitions
 };
+// A segment of the walk backwards: where it starts and what it has to do.
+struct RevPart {
+    int64_t head, kh, seq, id, lastrow, lastunit;
+    int tile, vt, nch, n;          // n: steps of the chunk that it starts with
+    bool first, last, transition, used;
+};
+template <int KP, bool ENDS, int NW> __device__ __forceinline__ RevPart rev_part(const BwdParams &p) {
+    constexpr int wide = 16 * NW;
+    const DeltaShape &sh = p.b.fwd.s;
+    const int64_t H = sh.heads;
+    const int nvt = (static_cast<int>(sh.dv) + wide - 1) / wide, tiles = ENDS ? nvt + (KP + wide - 1) / wide : nvt;
+    const int64_t per_tile = gridDim.x / tiles, rest = blockIdx.x % per_tile;
+    RevPart r{};
+    r.tile = static_cast<int>(blockIdx.x / per_tile);
+    r.head = rest % H;
+    r.kh = r.head / (H / sh.kheads);
+    r.id = rest / H;
+    Span sp;
+    const Segment sg = segment_of(sh, r.id, p.seq.cps, sp);
+    r.seq = sg.seq;
+    r.first = sg.s == 0;
+    r.last = sg.last;
+    r.transition = ENDS && r.tile >= nvt;
+    r.used = sg.used && !(ENDS && (r.first || (r.last && r.transition)));
+    r.vt = r.transition ? 0 : r.tile;
+    r.tile -= nvt;
+    r.nch = sg.j1 - sg.j0;
+    r.n = sp.len - (sg.j1 - 1) * kC < kC ? sp.len - (sg.j1 - 1) * kC : kC;
+    r.lastrow = sp.row0 + static_cast<int64_t>(sg.j1 - 1) * kC;
+    r.lastunit = (sp.slot0 + sg.j1 - 1) * H + r.head;
+    return r;
+}
+template <int KP, bool ENDS> __device__ __forceinline__ void rev_start(f32x4 (&dS)[KP / 16], const BwdParams &p, const RevPart &r, int wide, int v0, int w, int lane) {
+    const DeltaArgs &a = p.b.fwd;
+    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
+    const size_t VK = static_cast<size_t>(V) * K;
+    if (r.transition) {
+        unit_columns<KP>(dS, r.tile * wide + w * 16, lane);
+    } else if (!ENDS && !r.last) {
+        load_state<KP>(dS, p.seq.ends + ((r.id + 1) * a.s.heads + r.head) * VK, v0, V, K, lane);
+    } else if (r.last && p.b.dlast) {
+        load_state<KP>(dS, p.b.dlast + (r.seq * a.s.heads + r.head) * VK, v0, V, K, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < KP / 16; ++i) dS[i] = f32x4{0, 0, 0, 0};
+    }
+}
+template <typename T, int KP, bool ENDS, int NW>
+__device__ __forceinline__ void rev_end(const f32x4 (&dS)[KP / 16], const BwdParams &p, const RevPart &r, char *smem, int v0, int w, int lane) {
+    const DeltaArgs &a = p.b.fwd;
+    const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
+    const size_t VK = static_cast<size_t>(V) * K;
+    const int64_t unit = r.id * a.s.heads + r.head;
+    if constexpr (ENDS) {
+        if (r.transition) store_map<T, KP, NW>(dS, smem, w, lane, p.seq.maps + unit * kMapBytes<KP>, r.tile * 16 * NW);
+        else store_state<KP>(dS, p.seq.ends + unit * VK, v0, V, K, lane);
+    } else if (r.first && p.b.dh0) {
+        store_state<KP>(dS, p.b.dh0 + (r.seq * a.s.heads + r.head) * VK, v0, V, K, lane);
+    }
+}
 
 // What get_col reads of a chunk that is used with steps along K only.
 template <typename T, int KP> struct QSide : Cols<KP> {};
@@ -35,7 +96,7 @@ template <int KP> struct QSide<bf16_t, KP> : Rows<bf16_t, KP> {
 };
 
 // --------------------------------------------------------- dS and dX, in reverse
-template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(BwdParams p) {
+template <int KP, bool ENDS> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(BwdParams p) {
     using T = float;
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -48,21 +109,15 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
     const int g = lane / 16, c = lane % 16;
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
     const int64_t H = a.s.heads;
-    const int nvt = (V + 63) / 64, vt = blockIdx.x % nvt;
-    const int64_t rest = blockIdx.x / nvt, head = rest % H, kh = head / (H / a.s.kheads), seq = rest / H;
-    const Span sp = span_of(a.s, seq);
-    const int nchunks = (sp.len + kC - 1) / kC;
-    const int v0 = vt * 64 + w * 16;
+    const RevPart r = rev_part<KP, ENDS, kWaves>(p);
+    if (!r.used) return;
+    const int64_t head = r.head, kh = r.kh;
+    const int v0 = r.vt * 64 + w * 16;
     const f32x4 zero = {0, 0, 0, 0};
     const size_t VK = static_cast<size_t>(V) * K;
     constexpr int es = sizeof(T);
     f32x4 dS[KT];
-    if (p.b.dlast) {
-        load_state<KP>(dS, p.b.dlast + (seq * H + head) * VK, v0, V, K, lane);
-    } else {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) dS[i] = zero;
-    }
+    rev_start<KP, ENDS>(dS, p, r, 64, v0, w, lane);
     // the next chunk's data, a chunk ahead, as in the forward
     Rows<T, KP> nK;
     Cols<KP> nC;
@@ -74,13 +129,12 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
     const auto okc = Cols<KP>::offsets(a.ldk, K, threadIdx.x);
     const auto oqc = QSide<T, KP>::offsets(a.ldq, K, threadIdx.x);
     const int ldy = static_cast<int>(H * V);
-    const uint32_t oy = Values::offset(ldy, V - vt * 64, w, lane);
-    auto prefetch = [&](int j) {
-        const int jj = j >= 0 ? j : 0;
-        const int64_t row0 = sp.row0 + static_cast<int64_t>(jj) * kC, unit = (sp.slot0 + jj) * H + head;
-        const int n = j >= 0 ? (sp.len - j * kC < kC ? sp.len - j * kC : kC) : 0;
+    const uint32_t oy = Values::offset(ldy, V - r.vt * 64, w, lane);
+    auto prefetch = [&](int j) {                           // the j-th chunk from the end; past the first one nothing is read
+        const int jj = j < r.nch ? j : r.nch - 1, n = j < r.nch ? (j == 0 ? r.n : kC) : 0;
+        const int64_t row0 = r.lastrow - static_cast<int64_t>(jj) * kC, unit = r.lastunit - jj * H;
         const rsrc_t rk = chunk_rsrc(static_cast<const T *>(a.k) + row0 * a.ldk + kh * K, n, a.ldk, K, es);
-        const rsrc_t rd = chunk_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V + vt * 64, n, ldy, V - vt * 64, es);
+        const rsrc_t rd = chunk_rsrc(static_cast<const T *>(p.b.dout) + (row0 * H + head) * V + r.vt * 64, r.transition ? 0 : n, ldy, V - r.vt * 64, es);
         nK.load(rk, a.ldk, okr);
         nY.load(rd, ldy, oy);
         nT.load(p.ws.tt + unit * kTriBytes);
@@ -89,10 +143,10 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
         nC.load(rk, a.ldk, okc);
         nQ.load(chunk_rsrc(static_cast<const T *>(a.q) + row0 * a.ldq + kh * K, n, a.ldq, K, es), a.ldq, oqc);
     };
-    if (nchunks > 0) prefetch(nchunks - 1);
-    for (int j = nchunks - 1; j >= 0; --j) {
-        const int64_t row0 = sp.row0 + static_cast<int64_t>(j) * kC, unit = (sp.slot0 + j) * H + head;
-        const int n = sp.len - j * kC < kC ? sp.len - j * kC : kC;
+    if (r.nch > 0) prefetch(0);
+    for (int j = 0; j < r.nch; ++j) {
+        const int64_t row0 = r.lastrow - static_cast<int64_t>(j) * kC, unit = r.lastunit - j * H;
+        const int n = j == 0 ? r.n : kC;
         __syncthreads();                                   // the chunk before is done with LDS
         nK.put(sK, threadIdx.x);
         nC.put(sC, threadIdx.x);
@@ -102,8 +156,8 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
         if (threadIdx.x < 3 * kC) sS[threadIdx.x] = nS;
         const Values cY = nY;
         __syncthreads();
-        store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
-        prefetch(j - 1);
+        if constexpr (!ENDS) store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
+        prefetch(j + 1);
         const Op<T> yo[2] = {cY.op(0), cY.op(1)};
         Op2<T> so[KK];
 #pragma unroll
@@ -134,15 +188,17 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
             for (int tb = 0; tb < 2 * kk + 2; ++tb) {
                 const Op2<T> tt = get_op2(sT + tri_up(tb, kk) * kOp2Bytes, lane, T());
                 dX[tb] = mma(tt, uo[kk], dX[tb]);
-                xt[tb] = mma(uo[kk], tt, xt[tb]);
+                if constexpr (!ENDS) xt[tb] = mma(uo[kk], tt, xt[tb]);
             }
         tiles(yo[0], dY[0], dY[1]);
         tiles(yo[1], dY[2], dY[3]);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-            const int t = row_index(tb, c), v = v0 + 4 * g;
-            store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * es) : kOffNone, T());
-            stream4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            if constexpr (!ENDS) {
+                const int t = row_index(tb, c), v = v0 + 4 * g;
+                store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * es) : kOffNone, T());
+                stream4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            }
             const f32x4 eg = *reinterpret_cast<const f32x4 *>(&sS[32 * (tb / 2) + 8 * g + 4 * (tb % 2)]);
             dY[tb] = dY[tb] * eg * a.scale;
             dX[tb] = dX[tb] * -eg;
@@ -161,7 +217,7 @@ template <int KP> __global__ __launch_bounds__(kThreads) void delta_rev_kernel(B
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) dS[kt] = mma(get_col<KP>(sK, sC, kt, kk, lane, T()), xo[kk], dS[kt]);
     }
-    if (p.b.dh0) store_state<KP>(dS, p.b.dh0 + (seq * H + head) * VK, v0, V, K, lane);
+    rev_end<T, KP, ENDS, kWaves>(dS, p, r, smem, v0, w, lane);
 }
 
 template <int KP> constexpr size_t rev_lds() {
@@ -171,7 +227,7 @@ template <int KP> constexpr size_t rev_lds() {
 
 // The same in bf16 io, as in delta_flow.h: a fifth (ninth) wave loads.  The buffer's
 // parts hold T^T, P^T and the columns of dY where the forward has T, P and V.
-template <int KP, int NW>
+template <int KP, bool ENDS, int NW>
 __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 3 : 2, NW == 8 ? 3 : 2))) void delta_rev_flow_kernel(BwdParams p) {
     using T = bf16_t;
     using B = FlowBuf<KP, NW>;
@@ -181,13 +237,11 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
-    const int64_t H = a.s.heads, per_tile = H * a.s.nseq;
-    const int vt = static_cast<int>(blockIdx.x / per_tile);
-    const int64_t rest = blockIdx.x % per_tile, head = rest % H, kh = head / (H / a.s.kheads), seq = rest / H;
-    const Span sp = span_of(a.s, seq);
-    const int nch = (sp.len + kC - 1) / kC;
-    const int64_t lastrow = sp.row0 + static_cast<int64_t>(nch - 1) * kC, lastunit = (sp.slot0 + nch - 1) * H + head;
-    const int ldy = static_cast<int>(H) * V;
+    const int64_t H = a.s.heads;
+    const RevPart r = rev_part<KP, ENDS, NW>(p);
+    if (!r.used) return;
+    const int64_t head = r.head, kh = r.kh, lastrow = r.lastrow, lastunit = r.lastunit;
+    const int vt = r.vt, nch = r.nch, ldy = static_cast<int>(H) * V;
 
     if (w == NW) {                                         // the loading wave
         const FlowLoader<KP, NW> ld(a.ldk, a.ldq, ldy, K, V - vt * kWide);
@@ -197,9 +251,9 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         const float *ps = p.ws.scal + lastunit * 3 * kC;
         for (int j = 0; j < nch; ++j) {
             char *const buf = smem + j % 2 * B::bytes;
-            const int n = j == 0 ? sp.len - (nch - 1) * kC : kC;
+            const int n = j == 0 ? r.n : kC;
             ld.template rows<KK>(buf, chunk_rsrc(pk, n, a.ldk, K, 2), ld.k, ld.ldk);
-            ld.template rows<B::kv>(buf + B::v, chunk_rsrc(pv, n, ldy, V - vt * kWide, 2), ld.v, ld.ldv);
+            ld.template rows<B::kv>(buf + B::v, chunk_rsrc(pv, r.transition ? 0 : n, ldy, V - vt * kWide, 2), ld.v, ld.ldv);
             ld.template copy<kTriBytes>(buf + B::p, pp);
             ld.scalars(buf + B::s, ps);
             ld.template copy<kTriBytes>(buf + B::t, pt);
@@ -211,6 +265,10 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
             pp -= H * kTriBytes;
             ps -= H * 3 * kC;
             flow_loaded();
+            flow_barrier();
+        }
+        if (r.transition) {
+            flow_barrier();
             flow_barrier();
         }
         return;
@@ -225,20 +283,15 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0);
     };
     f32x4 dS[KT];
-    if (p.b.dlast) {
-        load_state<KP>(dS, p.b.dlast + (seq * H + head) * VK, v0, V, K, lane);
-    } else {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) dS[i] = zero;
-    }
+    rev_start<KP, ENDS>(dS, p, r, kWide, v0, w, lane);
     int64_t unit = lastunit;
     T *pdv = static_cast<T *>(p.b.dv) + (lastrow * H + head) * V;
     for (int j = 0; j < nch; ++j, unit -= H, pdv -= static_cast<int64_t>(kC) * ldy) {
         const char *const buf = smem + j % 2 * B::bytes;
         const float *const sS = reinterpret_cast<const float *>(buf + B::s);
-        const int n = j == 0 ? sp.len - (nch - 1) * kC : kC;
+        const int n = j == 0 ? r.n : kC;
         flow_barrier();
-        store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
+        if constexpr (!ENDS) store_state<KP>(dS, p.dS + unit * VK, v0, V, K, lane);
         Op<T> fk[2][4], yo[2];
         Op2<T> so[2], fp[AHEAD ? 6 : 1], ft[AHEAD ? 6 : 1];
         auto read_rows = [&](int kk) {
@@ -315,7 +368,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
                 if constexpr (AHEAD) f = ft[tri_up(tb, kk)];
                 else f = get_op2(buf + B::t + tri_up(tb, kk) * kOp2Bytes, lane, T());
                 dX[tb] = mma(f, uo[kk], dX[tb]);
-                xt[tb] = mma(uo[kk], f, xt[tb]);
+                if constexpr (!ENDS) xt[tb] = mma(uo[kk], f, xt[tb]);
             }
         auto add_cols = [&](const char *rows, int kk, const Op2<T> &o) {
 #pragma unroll
@@ -331,13 +384,15 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) dX[tb] = dX[tb] * -eg[tb];
         const Op2<T> xo[2] = {computed<T>(dX[0], dX[1]), computed<T>(dX[2], dX[3])};
-        const rsrc_t rv = chunk_rsrc(pdv, n, ldy, V, 2), rx = make_rsrc(p.dX + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
-        const int v = v0 + 4 * g;
+        if constexpr (!ENDS) {
+            const rsrc_t rv = chunk_rsrc(pdv, n, ldy, V, 2), rx = make_rsrc(p.dX + unit * kC * V, static_cast<uint32_t>(kC * V * 4));
+            const int v = v0 + 4 * g;
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-            const int t = row_index(tb, c);
-            store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * 2) : kOffNone, T());
-            stream4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            for (int tb = 0; tb < 4; ++tb) {
+                const int t = row_index(tb, c);
+                store_io4(xt[tb], rv, v < V ? static_cast<uint32_t>((t * ldy + v) * 2) : kOffNone, T());
+                stream4(xt[tb], rx, v < V ? static_cast<uint32_t>((t * V + v) * 4) : kOffNone);
+            }
         }
         add_cols(buf + B::q, 1, qo[1]);
         fence();
@@ -349,7 +404,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
         fence();
         add_cols(buf, 1, xo[1]);
     }
-    if (p.b.dh0) store_state<KP>(dS, p.b.dh0 + (seq * H + head) * VK, v0, V, K, lane);
+    rev_end<T, KP, ENDS, NW>(dS, p, r, smem, v0, w, lane);
 }
 
 // -------------------------------------------------------------------- the rest
@@ -778,25 +833,30 @@ __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3,
 // bf16: 64 value channels to a workgroup, 128 where only those let every CU have one.
 // Gradient calls, 128 x 128: 8 x 2048 steps of 12 heads (192 narrow workgroups), this kernel 175 us
 // against 247 wide; 16 x 2048 of 12 (384), the call 944 against 899; 24 x 1024 of 12 (576) 656 against 701.
-template <int KP, int NW> hipError_t launch_rev_flow(const BwdParams &p, hipStream_t s) {
-    constexpr int wide = 16 * NW;
+template <typename T, int KP, bool ENDS> hipError_t launch_rev(const BwdParams &p, hipStream_t s) {
     const DeltaShape &sh = p.b.fwd.s;
-    constexpr size_t lds = 2 * FlowBuf<KP, NW>::bytes;
-    hipLaunchKernelGGL((delta_rev_flow_kernel<KP, NW>), dim3(static_cast<unsigned>((sh.dv + wide - 1) / wide * sh.heads * sh.nseq)),
-                       dim3(kFlowThreads<NW>), lds, s, p);
+    auto groups = [&](int wide) { return ((sh.dv + wide - 1) / wide + (ENDS ? (KP + wide - 1) / wide : 0)) * sh.heads * p.seq.segments; };
+    if constexpr (sizeof(T) == 4) {
+        constexpr size_t lds = rev_lds<KP>();
+        hipLaunchKernelGGL((delta_rev_kernel<KP, ENDS>), dim3(static_cast<unsigned>(groups(64))), dim3(kThreads), lds, s, p);
+    } else if (sh.dv > 64 && groups(64) > 256 && groups(128) <= 256) {
+        constexpr size_t lds = 2 * FlowBuf<KP, 8>::bytes;
+        hipLaunchKernelGGL((delta_rev_flow_kernel<KP, ENDS, 8>), dim3(static_cast<unsigned>(groups(128))), dim3(kFlowThreads<8>), lds, s, p);
+    } else {
+        constexpr size_t lds = 2 * FlowBuf<KP, 4>::bytes;
+        hipLaunchKernelGGL((delta_rev_flow_kernel<KP, ENDS, 4>), dim3(static_cast<unsigned>(groups(64))), dim3(kFlowThreads<4>), lds, s, p);
+    }
     return hipGetLastError();
 }
-template <typename T, int KP> hipError_t launch_rev(const BwdParams &p, hipStream_t s) {
-    const DeltaShape &sh = p.b.fwd.s;
-    const int64_t n = (sh.dv + 63) / 64 * sh.heads * sh.nseq;
-    if constexpr (sizeof(T) == 2) {
-        const bool wide = sh.dv > 64 && n > 256 && (sh.dv + 127) / 128 * sh.heads * sh.nseq <= 256;
-        return wide ? launch_rev_flow<KP, 8>(p, s) : launch_rev_flow<KP, 4>(p, s);
-    } else {
-        constexpr size_t lds = rev_lds<KP>();
-        hipLaunchKernelGGL((delta_rev_kernel<KP>), dim3(static_cast<unsigned>(n)), dim3(kThreads), lds, s, p);
-        return hipGetLastError();
+// The walk backwards, cut in time where the forward is.  The gradient call with saved chunks,
+// uncut and cut: 65536 steps of 8 heads of 64 x 64 bf16 3004 and 769 us, 16384 of 4 of 128 x 128 886 and 292, 8192 of 4
+// of 64 x 64 fp32 1060 and 177.
+template <typename T, int KP> hipError_t launch_back(const BwdParams &p, hipStream_t s) {
+    if (p.seq.segments != p.b.fwd.s.nseq) {
+        if (hipError_t e = launch_rev<T, KP, true>(p, s)) return e;
+        if (hipError_t e = launch_carry<T, KP, true>(p.seq, s)) return e;
     }
+    return launch_rev<T, KP, false>(p, s);
 }
 
 struct BwdWs {
@@ -812,8 +872,8 @@ BwdWs bwd_ws(const DeltaShape &s, const Plan &plan, bool saved) {
     w.dS = w.dX + align256(units * kC * V * 4);
     w.ckpt = w.dS + align256(units * V * K * 4);
     w.ends = w.ckpt + (saved ? 0 : align256(units * static_cast<size_t>(delta_ckpt_stride(K, V)) * 4));
-    w.maps = w.ends + (saved ? 0 : ends_bytes(s, plan));
-    w.total = w.maps + (saved ? 0 : maps_bytes(s, plan));
+    w.maps = w.ends + ends_bytes(s, plan);
+    w.total = w.maps + maps_bytes(s, plan);
     return w;
 }
 
@@ -828,25 +888,25 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
     p.ws = {b.fwd.ckpt ? nullptr : base + w.t, base + w.p, base + w.tt, reinterpret_cast<float *>(base + w.scal)};
     p.dX = reinterpret_cast<float *>(base + w.dX);
     p.dS = reinterpret_cast<float *>(base + w.dS);
+    SeqParams &q = p.seq;
+    q.a = b.fwd;
+    q.a.last_state = nullptr;
+    q.ws = p.ws;
+    q.cps = plan.cps;
+    q.wide = plan.wide;
+    q.wide_ends = plan.wide_ends;
+    q.segments = plan.segments;
+    q.ends = reinterpret_cast<float *>(base + w.ends);
+    q.maps = base + w.maps;
     if (sh.slots > 0) {
         if (hipError_t e = launch_prep<T, KP, true>(b.fwd, p.ws, s)) return e;
         if (!b.fwd.ckpt) {
-            SeqParams q{};
-            q.a = b.fwd;
-            q.a.last_state = nullptr;
-            q.ws = p.ws;
-            q.cps = plan.cps;
-            q.wide = plan.wide;
-            q.wide_ends = plan.wide_ends;
-            q.segments = plan.segments;
-            q.ends = reinterpret_cast<float *>(base + w.ends);
-            q.maps = base + w.maps;
             q.a.ckpt = p.b.fwd.ckpt = reinterpret_cast<float *>(base + w.ckpt);
             if (hipError_t e = launch_segments<T, KP>(q, s)) return e;
             if (hipError_t e = launch_walk<T, KP, kSave>(q, s)) return e;
         }
     }
-    if (hipError_t e = launch_rev<T, KP>(p, s)) return e;
+    if (hipError_t e = launch_back<T, KP>(p, s)) return e;
     if (sh.slots == 0) return hipSuccess;
     constexpr size_t glds = GradBuf<T, KP>::all;
     const int64_t units = sh.slots * sh.kheads;

@@ -229,6 +229,39 @@ enum Mode {
 };
 constexpr bool has_out(Mode m) { return m == kOut || m == kTrain; }
 constexpr bool has_save(Mode m) { return m == kTrain || m == kSave; }
+// A wave's 16 columns n of a segment's transition, as operands with n along K; by all
+// waves of a workgroup whose first column is n0.
+template <typename T, int KP, int NW> __device__ __forceinline__ void store_map(const f32x4 (&S)[KP / 16], char *smem, int w, int lane, char *out, int n0) {
+    constexpr int KT = KP / 16, LM = KP + 4, kWide = 16 * NW;
+    float *const sM = reinterpret_cast<float *>(smem);
+    const int g = lane / 16, c = lane % 16;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < KT; ++q) *reinterpret_cast<f32x4 *>(&sM[(16 * w + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[q];
+    __syncthreads();
+    const int nk = KP - n0 < kWide ? (KP - n0) / 32 : kWide / 32;
+    for (int f = w; f < nk * KT; f += NW) {
+        const int kk = f / KT, kt = f % KT, k = row_index(kt, c);
+        f32x4 x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = sM[(32 * kk + 8 * g + i) * LM + k];
+            y[i] = sM[(32 * kk + 8 * g + 4 + i) * LM + k];
+        }
+        put_op(out + ((n0 / 32 + kk) * KT + kt) * kOp2Bytes, lane, computed<T>(x, y));
+    }
+}
+// columns col0 + c of the identity
+template <int KP> __device__ __forceinline__ void unit_columns(f32x4 (&S)[KP / 16], int col0, int lane) {
+    const int g = lane / 16, col = col0 + lane % 16;
+#pragma unroll
+    for (int q = 0; q < KP / 32; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            S[2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
+            S[2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
+        }
+}
 template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_seq_kernel(SeqParams p) {
     using T = float;
     constexpr int KT = KP / 16, KK = KP / 32, RB = kRowBytes<T>;
@@ -260,14 +293,7 @@ template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_s
     const size_t VK = static_cast<size_t>(V) * K;
     f32x4 S[KT];
     if (transition) {
-        const int col = (tile - nvt) * kWide + w * 16 + c;
-#pragma unroll
-        for (int q = 0; q < KK; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                S[2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
-                S[2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
-            }
+        unit_columns<KP>(S, (tile - nvt) * kWide + w * 16, lane);
     } else if (MODE != kEnds && !first) {
         load_state<KP>(S, p.ends + ((id - 1) * H + head) * VK, v0, V, K, lane);
     } else if (first && a.h0) {
@@ -455,26 +481,7 @@ template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_s
             store_state<KP>(S, p.ends + (id * H + head) * VK, v0, V, K, lane);
             return;
         }
-        // columns n of the map, turned into operands with n along K
-        constexpr int LM = KP + 4;
-        float *const sM = reinterpret_cast<float *>(smem);
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < KT; ++q)
-            *reinterpret_cast<f32x4 *>(&sM[(16 * w + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[q];
-        __syncthreads();
-        char *const out = p.maps + (id * H + head) * kMapBytes<KP>;
-        const int n0 = (tile - nvt) * kWide, nk = KP - n0 < kWide ? (KP - n0) / 32 : kWide / 32;
-        for (int f = w; f < nk * KT; f += kWaves) {
-            const int kk = f / KT, kt = f % KT, k = row_index(kt, c);
-            f32x4 x, y;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = sM[(32 * kk + 8 * g + i) * LM + k];
-                y[i] = sM[(32 * kk + 8 * g + 4 + i) * LM + k];
-            }
-            put_op(out + ((n0 / 32 + kk) * KT + kt) * kOp2Bytes, lane, computed<T>(x, y));
-        }
+        store_map<T, KP, kWaves>(S, smem, w, lane, p.maps + (id * H + head) * kMapBytes<KP>, (tile - nvt) * kWide);
     } else {
         if (last && a.last_state) {
             store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
@@ -490,9 +497,9 @@ template <int KP, Mode MODE> constexpr size_t seq_lds() {
 }
 
 // What the segments leave, one after the other: from the state that the one before
-// leaves, through the transition, plus what it leaves from zero.  A wave per
-// (sequence, head, 16 value channels).
-template <typename T, int KP> __global__ __launch_bounds__(64) void delta_carry_kernel(SeqParams p) {
+// leaves, through the transition, plus what it leaves from zero.  REV: from the last one
+// on, for the gradient.  A wave per (sequence, head, 16 value channels).
+template <typename T, int KP, bool REV> __global__ __launch_bounds__(64) void delta_carry_kernel(SeqParams p) {
     constexpr int KT = KP / 16, KK = KP / 32;
     const DeltaArgs &a = p.a;
     const int lane = threadIdx.x, K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
@@ -505,7 +512,8 @@ template <typename T, int KP> __global__ __launch_bounds__(64) void delta_carry_
     const size_t VK = static_cast<size_t>(V) * K;
     if (ns < 3) return;
     f32x4 S[KT];
-    load_state<KP>(S, p.ends + (first * H + head) * VK, v0, V, K, lane);
+    auto unit = [&](int s) { return (first + (REV ? ns - 1 - s : s)) * H + head; };
+    load_state<KP>(S, p.ends + unit(0) * VK, v0, V, K, lane);
     // a step is little more than the latency of its loads: as many steps ahead as registers hold
     constexpr int AHEAD = KP > 64 ? 1 : 3;
     struct Step {
@@ -513,7 +521,7 @@ template <typename T, int KP> __global__ __launch_bounds__(64) void delta_carry_
         f32x4 end[KT];
     } next[AHEAD];
     auto fetch = [&](Step &f, int s) {
-        const int64_t at = (first + (s < ns - 1 ? s : ns - 2)) * H + head;
+        const int64_t at = unit(s < ns - 1 ? s : ns - 2);
         const char *const m = p.maps + at * kMapBytes<KP>;
         load_state<KP>(f.end, p.ends + at * VK, v0, V, K, lane);
 #pragma unroll
@@ -537,7 +545,7 @@ template <typename T, int KP> __global__ __launch_bounds__(64) void delta_carry_
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) S[kt] = mma(next[d].map[kk][kt], so[kk], S[kt]);
-            store_state<KP>(S, p.ends + ((first + s) * H + head) * VK, v0, V, K, lane);
+            store_state<KP>(S, p.ends + unit(s) * VK, v0, V, K, lane);
             fetch(next[d], s + AHEAD);
         }
     }
@@ -559,9 +567,9 @@ template <int KP, Mode MODE> hipError_t launch_seq(const SeqParams &p, hipStream
     hipLaunchKernelGGL((delta_seq_kernel<KP, MODE>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
     return hipGetLastError();
 }
-template <typename T, int KP> hipError_t launch_carry(const SeqParams &p, hipStream_t s) {
+template <typename T, int KP, bool REV> hipError_t launch_carry(const SeqParams &p, hipStream_t s) {
     const int64_t grid = (p.a.s.dv + 15) / 16 * p.a.s.heads * p.a.s.nseq;
-    hipLaunchKernelGGL((delta_carry_kernel<T, KP>), dim3(static_cast<unsigned>(grid)), dim3(64), 0, s, p);
+    hipLaunchKernelGGL((delta_carry_kernel<T, KP, REV>), dim3(static_cast<unsigned>(grid)), dim3(64), 0, s, p);
     return hipGetLastError();
 }
 

@@ -177,14 +177,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     const int at = flow_at(lane), tat = flow_tr_at(lane);
     f32x4 S[KT];
     if (transition) {
-        const int col = (tile - nvt) * kWide + w * 16 + c;
-#pragma unroll
-        for (int q = 0; q < KK; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                S[2 * q][i] = 32 * q + 8 * g + i == col ? 1.0f : 0.0f;
-                S[2 * q + 1][i] = 32 * q + 8 * g + 4 + i == col ? 1.0f : 0.0f;
-            }
+        unit_columns<KP>(S, (tile - nvt) * kWide + w * 16, lane);
     } else if (MODE != kEnds && !first) {
         load_state<KP>(S, p.ends + ((id - 1) * H + head) * VK, v0, V, K, lane);
     } else if (first && a.h0) {
@@ -361,27 +354,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
             store_state<KP>(S, p.ends + (id * H + head) * VK, v0, V, K, lane);
             return;
         }
-        // columns n of the map, turned into operands with n along K
-        constexpr int LM = KP + 4;
-        static_assert(kWide * LM * 4 <= 2 * B::bytes, "the map fits the buffers");
-        float *const sM = reinterpret_cast<float *>(smem);
-        flow_barrier();
-#pragma unroll
-        for (int q = 0; q < KT; ++q)
-            *reinterpret_cast<f32x4 *>(&sM[(16 * w + c) * LM + 32 * (q / 2) + 8 * g + 4 * (q % 2)]) = S[q];
-        flow_barrier();
-        char *const out = p.maps + (id * H + head) * kMapBytes<KP>;
-        const int n0 = (tile - nvt) * kWide, nk = KP - n0 < kWide ? (KP - n0) / 32 : kWide / 32;
-        for (int f = w; f < nk * KT; f += NW) {
-            const int kk = f / KT, kt = f % KT, k = row_index(kt, c);
-            f32x4 x, y;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = sM[(32 * kk + 8 * g + i) * LM + k];
-                y[i] = sM[(32 * kk + 8 * g + 4 + i) * LM + k];
-            }
-            put_op(out + ((n0 / 32 + kk) * KT + kt) * kOp2Bytes, lane, computed<T>(x, y));
-        }
+        store_map<T, KP, NW>(S, smem, w, lane, p.maps + (id * H + head) * kMapBytes<KP>, (tile - nvt) * kWide);
     } else if (last && a.last_state) {
         store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
     }
@@ -405,7 +378,7 @@ template <typename T, int KP, Mode MODE> hipError_t launch_walk(const SeqParams 
 template <typename T, int KP> hipError_t launch_segments(const SeqParams &p, hipStream_t s) {
     if (p.segments == p.a.s.nseq) return hipSuccess;
     if (hipError_t e = launch_walk<T, KP, kEnds>(p, s)) return e;
-    return launch_carry<T, KP>(p, s);
+    return launch_carry<T, KP, false>(p, s);
 }
 
 }  // namespace
