@@ -601,7 +601,7 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
     Plan best{0x7fffffff, s.nseq, false, false};
     double least = -1.0;
     for (int64_t n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
-        if (n > 1 && (nc < 16 || nc < 4 * n)) break;
+        if (n > 1 && (nc < 12 || nc < 3 * n)) break;
         const int64_t cps = (nc + n - 1) / n;
         const double out4 = rounds(t4 * units * n) * c4, out8 = rounds(t8 * units * n) * c8;
         const double ends4 = rounds(units * (t4 * (n - 1) + k4 * (n - 2))) * e4, ends8 = rounds(units * (t8 * (n - 1) + k8 * (n - 2))) * e8;
