@@ -584,12 +584,15 @@ struct Plan {
 // The cheapest of some ways to cut, by what a chunk takes a workgroup alone on its CU
 // (us, at 128 and at 64 key channels): 64 value channels 2.75 and 1.95, 128 of them 5
 // and 3.2; without the output 1.8 and 1.3, 4 and 2.5; fp32 11.5 and 5.4, 7.5 and
-// 3.6; a step of the join 7.5 and 1.  Packed sequences count as equally long.
+// 3.6; a step of the join 7.5 and 1.  Packed sequences count as equally long
+// at first.
 // Measured, us a call, bf16: 2 x 8192 steps of 40 heads of 128 x 128, 64 channels to a
 // workgroup, 1 / 2 / 3 segments 511 / 629 / 626, 128 channels 588 / 574 / 495 to 590 (the clock
 // gives way when every CU is at work for long); 65536 steps of 8 heads of 64 x 64,
-// 1 / 8 / 16 / 32 / 64 segments 2002 / 565 / 367 / 334 / 369.  Under 16 chunks a sequence
-// stays whole: two launches more cost what is won.
+// 1 / 8 / 16 / 32 / 64 segments 2002 / 565 / 367 / 334 / 369; fp32, the gradient of 2 x 777 steps of 6
+// heads of 64 x 64 (13 chunks), kernels, 1 / 3 / 4 segments 242 / 214 / 192.  Under 12 chunks a
+// sequence stays whole: two launches more cost what is won.  The gradient's walk backwards is
+// cut alike.
 inline Plan plan_of(const DeltaShape &s, int bf16) {
     const bool big = s.dk > 64;
     const double c4 = bf16 ? (big ? 2.75 : 1.95) : (big ? 11.5 : 5.4), c8 = big ? 5.0 : 3.2;
