@@ -419,7 +419,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 // The value channels are taken 32 at a time.  Four more waves bring them from global
 // memory, as operands, into one of two LDS buffers: a wave that computes and loads
 // stands still for as long as its loads queue, which at the memory's rate is longer than
-// all it computes.  3072 chunks of 128 x 128 (bytes: 148 us at a copy's rate): every wave
+// all it computes.  8 x 2048 steps of 12 heads of 128 x 128 (bytes: 148 us at a copy's rate): every wave
 // loading for itself 404 us with four waves, 267 with eight; now 227.
 constexpr int kGradThreads = 768, kGradWaves = 8;
 

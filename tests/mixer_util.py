@@ -25,14 +25,15 @@ import torch
 EPS = {torch.float32: 2.0 ** -20, torch.bfloat16: 2.0 ** -17}
 
 
-def close(got, want, io, steps, name, size=None):
-    """got against want: io the inputs' type, size the root mean square that the error is measured by (want's)."""
+def close(got, want, io, steps, name, size=None, half=None):
+    """got against want: io the inputs' type, size the root mean square that the error is measured by (want's), half the
+    rounding of the outputs' type (got's)."""
     g = U.f64(got)
     assert g.shape == want.shape, (name, g.shape, want.shape)
     if g.size == 0:
         return
     assert np.isfinite(g).all(), f"{name}: not finite"
-    half = U.HALF_STEP[got.dtype]
+    half = U.HALF_STEP[got.dtype] if half is None else half
     rms = max(float(np.sqrt(np.mean(want * want))), 0.0 if size is None else size)
     t = EPS[io] * 2.0 * np.sqrt(5.0 * max(1, -(-steps // 64))) * rms + 2.0 ** -126
     d = np.abs(g - want) - half * np.abs(want)

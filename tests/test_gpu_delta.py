@@ -230,6 +230,39 @@ def test_one_packed_sequence_far_longer_than_the_rest(ops, size, dtype):
         D.close(got["dh0"][i:i + 1], want["dh0"], io, m, "dh0")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(24, 24, 64, 128), (12, 24, 128, 128), (6, 6, 128, 200)], ids=lambda s: "x".join(map(str, s)))
+def test_a_cut_sequence_is_its_pieces(ops, size, dtype):
+    """A sequence that is cut in time against pieces too short for it, each from the state (gradient) that the one before
+    (behind) it leaves.  Each side keeps the tolerance against the exact values, so twice that between them; and each is
+    rounded to the outputs' type by itself, v (1 + d) with |d| at most half a step, so they are up to two halves apart:
+    |v (1 + d) - v (1 + e)| <= |v| (|d| + |e|)."""
+    Hk, H, K, V = size
+    T, P, io = 3000, 600, DT[dtype]
+    t = D.delta_inputs(1, T, Hk, H, K, V, io, seed=3)
+    dy, dl = U.rand(50, 1, T, H, V, dtype=io), U.rand(51, 1, H, V, K, scale=0.3)
+    ck = torch.empty(ops.delta_ckpt_shape(t["q"], t["v"]), device="cuda")
+    y, last = ops.delta_scan_fwd(*args(t), scale=0.3, h0=t["h0"], return_last_state=True, ckpt_out=ck)
+    got = ops.delta_scan_bwd(*args(t), dy, scale=0.3, h0=t["h0"], dlast=dl, ckpt=ck)
+    part = lambda i: [t[n][:, i:i + P].contiguous() for n in NAMES]
+    states, ys, grads = [t["h0"]], [], []
+    for i in range(0, T, P):
+        yi, si = ops.delta_scan_fwd(*part(i), scale=0.3, h0=states[-1], return_last_state=True)
+        states.append(si)
+        ys.append(yi)
+    for i in reversed(range(0, T, P)):
+        g = ops.delta_scan_bwd(*part(i), dy[:, i:i + P].contiguous(), scale=0.3, h0=states[i // P], dlast=dl)
+        dl = g["dh0"]
+        grads.insert(0, g)
+    want = {n: torch.cat([g[n] for g in grads], 1) for n in ("dq", "dk", "dv", "dg", "dbeta")}
+    want.update(y=torch.cat(ys, 1), last=states[-1], dh0=dl)
+    got.update(y=y, last=last)
+    for n, w in want.items():
+        half, w, g = U.HALF_STEP[got[n].dtype], U.f64(w), U.f64(got[n])
+        g = g - np.clip(g - w, -half * np.abs(w), half * np.abs(w))            # the second half; close() has the first
+        D.close(torch.from_numpy(g).to("cuda"), w, io, T, n, size=2.0 * D.rms(w) * (4.0 if n == "dg" else 1.0), half=half)
+
+
 def test_many_empty_sequences(ops):
     n = 1000
     at = torch.zeros(n + 1, dtype=torch.int32)
@@ -241,11 +274,12 @@ def test_many_empty_sequences(ops):
     assert torch.equal(last[:499], t["h0"][:499]) and torch.equal(last[500:], t["h0"][500:])
 
 
-def test_starts_out_of_order_stay_inside(ops):
+@pytest.mark.parametrize("T", [200, 2000])
+def test_starts_out_of_order_stay_inside(ops, T):
     """Bad starts are brought into range on the device: the call ends, and nothing outside the tensors is written."""
-    t = D.delta_inputs(1, 200, 1, 2, 32, 24, torch.float32, state=False)
-    y, guard = U.guarded((1, 200, 2, 24), torch.float32)
-    for bad in ([0, 150, 40, 200], [-50, 10, 900, 3], [2 ** 31 - 1, -2 ** 31, 200, 100], [200, 200, 0, 0]):
+    t = D.delta_inputs(1, T, 1, 2, 32, 24, torch.float32, state=False)
+    y, guard = U.guarded((1, T, 2, 24), torch.float32)
+    for bad in ([0, 150, 40, T], [-50, 10, 4 * T, 3], [2 ** 31 - 1, -2 ** 31, T, 100], [T, T, 0, 0]):
         s = torch.tensor(bad, dtype=torch.int64).to(torch.int32).cuda()
         _, last = ops.delta_scan_fwd(*args(t), starts=s, out=y, return_last_state=True)
         ops.delta_scan_bwd(*args(t), t["v"].contiguous(), starts=s)
