@@ -628,7 +628,9 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
         int64_t cps = nc > work ? nc : work;
         cps = cps > 8 ? cps : 8;
         const int64_t segments = s.slots / cps + s.nseq;
-        if (longest >= 2 * cps && segments * s.dv * s.dk * 4 <= s.slots * 2 * kTriBytes) {
+        // taken that the longest is half of all: its chunks beyond cps against the ends' pass and the join
+        const double won = (longest / 2 - cps) * (best.wide ? c8 : c4), lost = cps * e4 + 15.0 + longest / (2 * cps) * step;
+        if (won > lost && segments * s.dv * s.dk * 4 <= s.slots * 2 * kTriBytes) {
             best.cps = static_cast<int>(cps);
             best.segments = segments;
         }
