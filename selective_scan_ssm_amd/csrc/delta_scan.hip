@@ -71,7 +71,7 @@ template <typename T, int L, int M> __global__ __launch_bounds__(kThreads) void 
             q[i] = to_f32(pq[4 * l + i]);
         }
     }
-    const float alpha = expm1_accurate(step_log(a.g[bh])) + 1.0f, beta = a.beta[bh];
+    const float alpha = exp_accurate(step_log(a.g[bh])), beta = a.beta[bh];
     float kq = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) kq = fmaf(k[i], q[i], kq);

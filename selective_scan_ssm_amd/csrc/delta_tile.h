@@ -189,6 +189,21 @@ struct Columns {
 constexpr float kMinLog = -104.0f;
 __device__ __forceinline__ float step_log(float g) { return g < kMinLog ? kMinLog : g; }   // NaN stays
 
+// e^d to 4 U relative (U = 2^-24) down to fp32's subnormals: d = k ln 2 + r with |r| <= ln 2 / 2, r taken in fp64
+// (d itself in fp32 would cost |d| / 2 U), e^r by its Taylor series through r^7 (truncation < 6e-9), scaled by 2^k.
+// expm1(d) + 1 is no substitute: near -1 expm1 has steps of U, which at d = -10 are 4e-4 of the result and at -17 all of it.
+__device__ __forceinline__ float exp_accurate(double d) {
+    const double k = __builtin_rint(d * 1.4426950408889634);
+    const float r = static_cast<float>(fma(-k, 0.6931471805599453, d));
+    float q = fmaf(r, 1.0f / 5040.0f, 1.0f / 720.0f);
+    q = fmaf(r, q, 1.0f / 120.0f);
+    q = fmaf(r, q, 1.0f / 24.0f);
+    q = fmaf(r, q, 1.0f / 6.0f);
+    q = fmaf(r, q, 0.5f);
+    q = fmaf(r, q, 1.0f);
+    return __builtin_amdgcn_ldexpf(fmaf(r, q, 1.0f), static_cast<int>(k));
+}
+
 template <typename T> struct Decay;
 template <> struct Decay<bf16_t> {
     using real = float;
@@ -198,7 +213,7 @@ template <> struct Decay<bf16_t> {
 template <> struct Decay<float> {
     using real = double;
     static __device__ __forceinline__ double scaled(float g) { return static_cast<double>(g); }
-    static __device__ __forceinline__ float ex(double d) { return expm1_accurate(static_cast<float>(d)) + 1.0f; }
+    static __device__ __forceinline__ float ex(double d) { return exp_accurate(d); }
 };
 template <typename R> __device__ __forceinline__ R lane_prefix(R v, int lane) {
 #pragma unroll
