@@ -538,12 +538,11 @@ __device__ __forceinline__ Op<float> own_row(const char *, int, int, rsrc_t r, u
 template <typename T, int KP, bool SHARED>
 __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3, 3))) void delta_grad_kernel(BwdParams p) {
     using D = Decay<T>;
-    using real = typename D::real;
     using B = GradBuf<T, KP>;
     constexpr int KT = KP / 32, KK = KP / 64, OB = kOpBytes<T>;    // a wave's half of the channels
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char *const sC = smem + B::k, *const sQ = smem + B::q;
-    __shared__ real sG[kC];
+    __shared__ typename D::Sum sG[kC];
     __shared__ float sScal[3 * kC], sQK[2][kC], sZ[2][kC], sTot[kGradWaves], sDot[4];
     const float *const sB = sScal + 2 * kC;
     const DeltaArgs &a = p.b.fwd;
@@ -629,7 +628,7 @@ __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3,
                             q.put(sQ, thread);
                         }
                         if (pw == 0) {
-                            sG[lane] = lane_prefix<real>(lane < here.n ? D::scaled(step_log(step)) : real(0), lane);
+                            sG[lane] = D::sum(lane_prefix(lane < here.n ? D::scaled(step_log(step)) : 0.0, lane));
 #pragma unroll
                             for (int j = 0; j < 3; ++j) sScal[j * kC + lane] = scal[j];
                         }
@@ -712,15 +711,15 @@ __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3,
             if (B::n == 2) flow_barrier();
             char *const to = buffer(at - 1);
             const float eg = sScal[t], wt = sScal[kC + t], beta = sB[t], end = sScal[kC - 1];
-            const real gt = sG[t];
+            const typename D::Sum gt = sG[t];
 #pragma unroll
             for (int ob = 0; ob < 4; ++ob)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int o = 32 * (ob / 2) + 8 * g + 4 * (ob % 2) + i;      // the row: s or t
                     const bool in = wh ? o >= t : o <= t;
-                    const real go = sG[o];                   // no branch: the reads of LDS side by side
-                    const float bo = sB[o], d = D::ex(in ? (wh ? go - gt : gt - go) : real(0)) * (wh ? 1.0f : bo);
+                    const typename D::Sum go = sG[o];                   // no branch: the reads of LDS side by side
+                    const float bo = sB[o], d = D::ex(in ? (wh ? D::minus(go, gt) : D::minus(gt, go)) : 0.0f) * (wh ? 1.0f : bo);
                     A[ob][i] = in ? A[ob][i] * (a.scale * d) : 0.0f;
                     E[ob][i] = in && o != t ? E[ob][i] * -d : 0.0f;
                 }
@@ -808,7 +807,7 @@ __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3,
                     v += static_cast<double>(end) * (static_cast<double>(sDot[0]) + sDot[1] + sDot[2] + sDot[3]);
                     for (int i = 0; i < kGradWaves; ++i) v += sTot[i];
                 }
-                v = lane_prefix<double>(v, lane);
+                v = lane_prefix(v, lane);
                 if (l < here.n) {
                     p.b.dg[(here.row0 + l) * H + head] = static_cast<float>(v);
                     p.b.dbeta[(here.row0 + l) * H + head] = zl;

@@ -38,11 +38,10 @@ template <int KP> constexpr int64_t kMapBytes = static_cast<int64_t>(KP / 32) * 
 // of T and P are written).
 template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a, ChunkWs ws) {
     using D = Decay<T>;
-    using real = typename D::real;
     constexpr int KK = KP / 32;
     constexpr int LN = 68;                             // floats of a row of N: 16-byte rows, four banks apart
     __shared__ __attribute__((aligned(16))) float sN[kWaves][kC][LN];
-    __shared__ real sG[kWaves][kC];
+    __shared__ double sG[kWaves][kC];
     __shared__ float sB[kWaves][kC];
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, c = lane % 16;
@@ -57,9 +56,9 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
     const int64_t row0 = sp.row0 + step0;
 
     const int64_t at = (row0 + (lane < n ? lane : 0)) * a.s.heads + head;
-    const real G = lane_prefix<real>(lane < n ? D::scaled(step_log(a.g[at])) : real(0), lane);
+    const double G = lane_prefix(lane < n ? D::scaled(step_log(a.g[at])) : 0.0, lane);
     const float beta = lane < n ? a.beta[at] : 0.0f;
-    const real end = __shfl(G, 63);
+    const double end = __shfl(G, 63);
     float *scal = ws.scal + unit * 3 * kC;
     scal[lane] = D::ex(G);
     scal[kC + lane] = D::ex(end - G);
@@ -91,7 +90,7 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) acc = mma(k[sb][kk], k[tb][kk], acc);
             const int t = row_index(tb, c), s0 = 32 * (sb / 2) + 8 * g + 4 * (sb % 2);
-            const real gt = sG[w][t];
+            const double gt = sG[w][t];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = s0 + i < t ? acc[i] * D::ex(gt - sG[w][s0 + i]) * sB[w][s0 + i] : 0.0f;
             *reinterpret_cast<f32x4 *>(&sN[w][t][s0]) = acc;
@@ -187,7 +186,7 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
         for (int kk = BWD ? rb / 2 : 0; kk < (BWD ? 2 : rb / 2 + 1); ++kk) {
             f32x4 acc[2];
             const int r = row_index(rb, c);
-            const real gr = sG[w][r];
+            const double gr = sG[w][r];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 acc[h] = zero;
@@ -198,7 +197,7 @@ template <typename T, int KP, bool BWD> __global__ __launch_bounds__(kThreads) v
                 for (int i = 0; i < 4; ++i) {
                     const int o = 32 * kk + 8 * g + 4 * h + i;         // the other index
                     const bool in = BWD ? r <= o : o <= r;
-                    const real d = BWD ? sG[w][o] - gr : gr - sG[w][o];
+                    const double d = BWD ? sG[w][o] - gr : gr - sG[w][o];
                     acc[h][i] = in ? acc[h][i] * D::ex(d) : 0.0f;
                 }
             }

@@ -182,9 +182,12 @@ struct Columns {
 };
 
 // ---------------------------------------------------------- decay of the steps
-// Prefix sums of g over a chunk and exponentials of their differences: fp32 in
-// log2 units for bf16 io, fp64 for fp32 io, where |G| 2^-24 lost in each
-// difference would show.  A step's g is taken as at least kMinLog: exp(-104) is
+// Prefix sums of g over a chunk are fp64, and their differences rounded only relative
+// to themselves: a sum behind a few restarts or strong decays is in the thousands, and in
+// fp32 each difference would lose |G| U of it for good (behind 48 restarts 4e-4 of a decay).
+// bf16 io takes them in log2 units, for the hardware's exponential, and the gradient's
+// per-chunk part, which has no registers left, as two floats (8 x 2048 steps of 12 heads 226 to 233 us,
+// as with fp32 sums alone; with fp64 ones 248).  A step's g is taken as at least kMinLog: exp(-104) is
 // already 0 in fp32, so nothing changes, and -inf (a restart) leaves finite sums.
 constexpr float kMinLog = -104.0f;
 __device__ __forceinline__ float step_log(float g) { return g < kMinLog ? kMinLog : g; }   // NaN stays
@@ -206,19 +209,27 @@ __device__ __forceinline__ float exp_accurate(double d) {
 
 template <typename T> struct Decay;
 template <> struct Decay<bf16_t> {
-    using real = float;
-    static __device__ __forceinline__ float scaled(float g) { return g * kLog2e; }
+    using Sum = f32x2;                                 // hi + lo
+    static __device__ __forceinline__ double scaled(float g) { return g * 1.4426950408889634; }
+    static __device__ __forceinline__ Sum sum(double G) {
+        const float hi = static_cast<float>(G);
+        return {hi, static_cast<float>(G - hi)};
+    }
+    static __device__ __forceinline__ float minus(Sum a, Sum b) { return (a[0] - b[0]) + (a[1] - b[1]); }
     static __device__ __forceinline__ float ex(float d) { return fast_exp2(d); }
+    static __device__ __forceinline__ float ex(double d) { return fast_exp2(static_cast<float>(d)); }
 };
 template <> struct Decay<float> {
-    using real = double;
+    using Sum = double;
     static __device__ __forceinline__ double scaled(float g) { return static_cast<double>(g); }
+    static __device__ __forceinline__ Sum sum(double G) { return G; }
+    static __device__ __forceinline__ double minus(Sum a, Sum b) { return a - b; }
     static __device__ __forceinline__ float ex(double d) { return exp_accurate(d); }
 };
-template <typename R> __device__ __forceinline__ R lane_prefix(R v, int lane) {
+__device__ __forceinline__ double lane_prefix(double v, int lane) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const R u = __shfl_up(v, o);
+        const double u = __shfl_up(v, o);
         if (lane >= o) v += u;
     }
     return v;

@@ -116,3 +116,36 @@ def test_a_cut_sequence_only_decays(ops, dtype):
     a = np.exp(G)[..., None, None]
     for name, t, s in (("last", last, U.f64(h0)), ("dh0", dh0, U.f64(dl))):
         within(t, a * s, each * a * np.abs(s) + TINY, name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("restart", [float("-inf"), -104.0, -90.0])
+def test_steps_behind_many_restarts(ops, restart, dtype):
+    """A state written behind many restarts (padding on the left) decays as if they had not been there."""
+    K, V, H, T, io = 32, 24, 6, 64, DT[dtype]
+    n = 47                                                                 # the last restart
+    g = -(U.rand(9, 1, T, H).abs() * 0.1 + 0.003)
+    g[:, :n + 1] = restart
+    beta = torch.zeros(1, T, H, device="cuda")
+    beta[:, n] = 1.0
+    k = torch.zeros(1, T, H, K, device="cuda")
+    k[..., 3] = 1.0
+    v = U.rand(3, 1, T, H, V, dtype=io)
+    y, last = ops.delta_scan_fwd(k.to(io), k.to(io), v, g, beta, scale=0.5, return_last_state=True)
+    dl = U.rand(6, 1, H, V, K)
+    got = ops.delta_scan_bwd(k.to(io), k.to(io), v, g, beta, torch.zeros_like(v), scale=0.5, dlast=dl)
+    G = np.concatenate([np.zeros((1, 1, H)), np.cumsum(U.f64(g)[:, n + 1:], 1)], 1)
+    a, vn = np.exp(G), U.f64(v)[:, n]                                      # (1, T - n, H), (1, H, V)
+    want = np.zeros((1, H, V, K))
+    want[..., 3] = a[:, -1, :, None] * vn
+    # U and U exp(G_end - G) are computed operands (two bf16 terms), the decay is rounded twice
+    rel = 8 * EPS + (0.0 if dtype == "f32" else 2.0 ** -17)
+    within(last, want, rel * np.abs(want) + TINY, "last")
+    wy = 0.5 * a[..., None] * vn[:, None]
+    within(y[:, n:], wy, (2 * rel + U.HALF_STEP[io]) * np.abs(wy) + TINY, "y")
+    # dbeta = <dlast, last>, dg of the steps behind the same: V products that are operands on both sides
+    dot, terms = ((U.f64(dl) * t).sum((-1, -2)) for t in (want, np.abs(np.sign(U.f64(dl)) * want)))
+    allowed = (3 * rel + (V + 64) * EPS) * terms + TINY
+    within(got["dbeta"][:, n], dot, allowed, "dbeta")
+    for t in range(n + 1, T):
+        within(got["dg"][:, t], dot, allowed, f"dg at {t}")
