@@ -848,6 +848,11 @@ def _delta_shape(q, v, starts):
     return Bt, T, 1, starts.shape[0] - 1, Hk, H, K, V
 
 
+def _delta_scale(scale, K):
+    """The scale of y; no key channels (K = 0) are left to the library to refuse."""
+    return float(scale) if scale is not None else K ** -0.5 if K else 1.0
+
+
 def delta_ckpt_shape(q, v, starts=None):
     """Shape of delta_scan_fwd's checkpoints for these inputs: (slots, nheads,
     headdim * (dstate + 64)), per chunk and head the state entering it (headdim,
@@ -889,7 +894,7 @@ def _delta_inputs(q, k, v, g, beta, scale, h0, starts):
     pv, ldv = _heads(v, "v", io, torch.Size((Bt, T, H, V)), dev)
     ends = (nseq, H, V, K)
     head = (pq, ldq, pk, ldk, pv, ldv, _arg(g, "g", torch.float32, (Bt, T, H), dev),
-            _arg(beta, "beta", torch.float32, (Bt, T, H), dev), K ** -0.5 if scale is None else float(scale),
+            _arg(beta, "beta", torch.float32, (Bt, T, H), dev), _delta_scale(scale, K),
             _arg(h0, "h0", torch.float32, ends, dev),
             _arg(starts, "starts", torch.int32, None if starts is None else starts.shape, dev), nseq)
     return io, dev, sizes, ends, head
@@ -966,7 +971,7 @@ def delta_state_update(state, q, k, v, g, beta, scale=None, out=None):
     rc = _run(dev, lib.ssm_delta_state_update, _arg(state, "state", torch.float32, (Bt, H, V, K), dev),
               _arg(q, "q", io, (Bt, Hk, K), dev), _arg(k, "k", io, (Bt, Hk, K), dev), _arg(v, "v", io, shape, dev),
               _arg(g, "g", torch.float32, (Bt, H), dev), _arg(beta, "beta", torch.float32, (Bt, H), dev),
-              K ** -0.5 if scale is None else float(scale), py, Bt, Hk, H, K, V, _IO[io])
+              _delta_scale(scale, K), py, Bt, Hk, H, K, V, _IO[io])
     _check(rc, "ssm_delta_state_update")
     return y
 

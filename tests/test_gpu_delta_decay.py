@@ -149,3 +149,11 @@ def test_steps_behind_many_restarts(ops, restart, dtype):
     within(got["dbeta"][:, n], dot, allowed, "dbeta")
     for t in range(n + 1, T):
         within(got["dg"][:, t], dot, allowed, f"dg at {t}")
+
+
+def test_no_key_channels_are_refused_as_a_shape(ops):
+    q, v, g = torch.zeros(1, 4, 2, 0, device="cuda"), torch.zeros(1, 4, 2, 8, device="cuda"), torch.zeros(1, 4, 2, device="cuda")
+    with pytest.raises(RuntimeError, match="invalid arguments|SHAPE"):
+        ops.delta_scan_fwd(q, q, v, g, g)
+    with pytest.raises(RuntimeError, match="SHAPE"):
+        ops.delta_state_update(torch.zeros(1, 2, 8, 0, device="cuda"), q[:, 0], q[:, 0], v[:, 0], g[:, 0], g[:, 0])
