@@ -599,6 +599,8 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
     const int64_t nc = s.nseq > 0 ? (s.slots + s.nseq - 1) / s.nseq : 0, units = s.heads * s.nseq;
     const int64_t t4 = (s.dv + 63) / 64, t8 = (s.dv + 127) / 128, k4 = big ? 2 : 1, k8 = 1;
     const bool may = bf16 && s.dv > 64;
+    // the pass over the segments' ends, the launch with the most workgroups, has to hold them
+    auto fits = [&](int64_t segments) { return (t4 + k4) * s.heads * segments <= kDeltaMaxGroups; };
     auto rounds = [](int64_t n) { return static_cast<double>((n + 255) / 256); };
     Plan best{0x7fffffff, s.nseq, false, false};
     double least = -1.0;
@@ -613,6 +615,7 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
             cost += cps * (p.wide_ends ? ends8 : ends4) + (n - 2) * step + 15.0;
             p.cps = static_cast<int>(cps);
             p.segments = s.packed ? s.slots / cps + s.nseq : s.nseq * ((nc + cps - 1) / cps);
+            if (!fits(p.segments)) break;
         }
         if (least < 0.0 || cost < least) {
             least = cost;
@@ -629,7 +632,7 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
         const int64_t segments = s.slots / cps + s.nseq;
         // taken that the longest is half of all: its chunks beyond cps against the ends' pass and the join
         const double won = (longest / 2 - cps) * (best.wide ? c8 : c4), lost = cps * e4 + 15.0 + longest / (2 * cps) * step;
-        if (won > lost && segments * s.dv * s.dk * 4 <= s.slots * 2 * kTriBytes) {
+        if (won > lost && fits(segments) && segments * s.dv * s.dk * 4 <= s.slots * 2 * kTriBytes) {
             best.cps = static_cast<int>(cps);
             best.segments = segments;
         }

@@ -70,9 +70,9 @@ int check_delta(ssm::DeltaShape &s, int64_t batch, int64_t seqlen, bool packed, 
     if (seqlen == 0) s.slots = 0;
     const int64_t tiles = (dv + 63) / 64;
     const int64_t slots = s.slots > s.nseq ? s.slots : s.nseq;
-    // workgroups of up to 576 lanes per chunk (sequence), head and 64 channels
+    // workgroups per chunk (sequence), head and 64 channels
     const int64_t groups = mul3(slots, heads, tiles);
-    if (groups < 0 || groups > kMaxLanes / 576) return SSM_ERR_SHAPE;
+    if (groups < 0 || groups > ssm::kDeltaMaxGroups) return SSM_ERR_SHAPE;
     if (mul3(groups, 64 * 64, 8) < 0 || mul3(mul3(slots, heads, dv), dk + C, 8) < 0 || mul3(batch * seqlen, heads, (dk > dv ? dk : dv) * 4) < 0)
         return SSM_ERR_SHAPE;
     return SSM_OK;

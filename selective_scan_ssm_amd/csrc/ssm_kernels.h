@@ -259,6 +259,8 @@ hipError_t launch_grad_clip(const ClipArgs &a, hipStream_t s);
 // everything else is contiguous.
 constexpr int kDeltaChunk = 64;           // steps between two checkpoints
 constexpr int kDeltaMaxState = 128;       // channels of a key
+// workgroups of a launch, which counts its lanes in 32 bits: the walks have up to 576 to a workgroup
+constexpr int64_t kDeltaMaxGroups = ((int64_t(1) << 32) - 1) / 576;
 struct DeltaShape {
     int packed;
     const int32_t *starts;                // packed: nseq + 1 first rows, else null (sizes alone: null too)

@@ -1,0 +1,39 @@
+"""Sizes of the delta rule's workspaces at the edges of what the header admits (CPU only)."""
+import os
+
+import pytest
+
+from selective_scan_ssm_amd import _lib
+
+F32, BF16 = 0, 1
+BAD = (1 << 64) - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from selective_scan_ssm_amd import build
+        build.build()
+    return _lib.load()
+
+
+def whole(slots, heads):
+    """The workspace of sequences that are not cut in time: per chunk and head T and P (12 KB each) and 192 floats."""
+    return 2 * 12288 * slots * heads + 768 * slots * heads
+
+
+# most of the sequences empty, one of millions of steps: the pass over the segments' ends has two or three workgroups to a
+# segment, of 256 (fp32) or 320 lanes
+@pytest.mark.parametrize("io,dk,seqlen,nseq", [(BF16, 8, 7_000_000, 7_300_000), (F32, 72, 7_000_000, 7_300_000), (BF16, 72, 7_000_000, 5_000_000),
+                                               (BF16, 128, 7_000_000, 7_300_000)])
+def test_more_segments_than_a_launch_holds_are_not_cut(lib, io, dk, seqlen, nseq):
+    slots = seqlen // 64 + nseq
+    need = lib.ssm_delta_scan_workspace_bytes(1, seqlen, 1, nseq, 1, 1, dk, 8, io)
+    groups = 1 + (1 if dk <= 64 else 2)
+    assert slots * groups * (256 if io == F32 else 320) > (1 << 32) - 1
+    assert need != BAD and need - whole(slots, 1) < 3 * 256
+
+
+def test_fewer_are_cut(lib):
+    need = lib.ssm_delta_scan_workspace_bytes(1, 3_800_000, 1, 1000, 1, 1, 8, 8, BF16)
+    assert need != BAD and need > whole(3_800_000 // 64 + 1000, 1) + 1000 * 256
