@@ -444,10 +444,15 @@ __device__ __forceinline__ void put_stats(const GroupNormArgs &a, const Runs &r,
     if (a.rstd) a.rstd[n * a.groups + t.group] = rstd;
 }
 
+// The first value of the thread's group in batch entry n.
+template <typename T> __device__ __forceinline__ float pivot_of(const GroupNormArgs &a, const Item &t, int D, int64_t n) {
+    return to_f32(static_cast<const T *>(a.x)[n * a.rows * a.ldx + static_cast<int64_t>(t.group) * D]);
+}
 // Sums of x - x0 and its square over a run, x0 the thread's first value, in fp32 over
-// a vector and fp64 beyond, then of x and x^2: x - x0 is about as large as the group's
-// spread, so a mean far from 0 costs the variance nothing.  (All in fp64 the pass took
-// 35 us over 134 MB instead of 27.)
+// a vector and fp64 beyond, then about the group's first value instead, which all runs and
+// threads share: x - x0 is about as large as the group's spread, and a mean far from 0 costs
+// the variance nothing (sums of x^2 themselves would cost it mean^2 2^-52, beside eps).  (All in
+// fp64 the pass took 35 us over 134 MB instead of 27.)
 template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void group_stats_kernel(GroupNormArgs a, Runs r, double *part) {
     __shared__ Totals m;
     for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
@@ -478,7 +483,7 @@ template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void grou
                     v += sv;
                 }
             }
-            const double count = static_cast<double>((t.rows - t.ty + t.ty_count - 1) / t.ty_count * V), z = x0;
+            const double count = static_cast<double>((t.rows - t.ty + t.ty_count - 1) / t.ty_count * V), z = static_cast<double>(x0) - pivot_of<T>(a, t, r.D, n);
             v += z * (2.0 * u + count * z);
             u += count * z;
         }
@@ -494,8 +499,8 @@ template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribu
         const Item t = item_of<V>(a, r, n);
         add_runs(m, a, r, t, n, part);
         if (!t.in) continue;
-        const double mu = m.t1[t.q] * inv, var = m.t2[t.q] * inv - mu * mu;
-        const float mean = static_cast<float>(mu);
+        const double mu = m.t1[t.q] * inv, var = m.t2[t.q] * inv - mu * mu;      // about the pivot
+        const float mean = static_cast<float>(pivot_of<T>(a, t, r.D, n) + mu);
         const float rstd = static_cast<float>(1.0 / sqrt((var < 0.0 ? 0.0 : var) + static_cast<double>(a.eps)));
         put_stats(a, r, t, n, mean, rstd);
         Affine p[V];

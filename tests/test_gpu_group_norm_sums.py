@@ -1,0 +1,42 @@
+"""The group norm's statistics far from zero."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_util as U
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_scan_ssm_amd import _lib, ops
+    _lib.load()
+    return ops
+
+
+# entries whose groups stay in registers, and that are cut into runs of rows
+@pytest.mark.parametrize("R", [2, 20, 64, 1500, 3000])
+@pytest.mark.parametrize("C,groups", [(64, 4), (30, 2), (2100, 2)])
+def test_groups_far_from_zero_with_next_to_no_spread(ops, R, C, groups):
+    """Values whose mean is a fp32 number, so that (x - mean) is exact and the statistics are good to their own
+    roundings: the sums' 10 U, and 8 U for the square root and the quotient."""
+    x = torch.full((2, R, C), 100004.0, device="cuda")
+    D = C // groups
+    x[0, ::2, :D] += 2.0 ** -6                                             # x = c, c + 2^-6 in turn: variance 2^-14
+    x[1, :, D:] = 16777213.0                                               # 24 bits long
+    b = U.rand(1, C)
+    y, mean, rstd = ops.group_norm(x, groups, bias=b, eps=1e-5, return_stats=True)
+    m, v = np.full((2, groups), 100004.0), np.zeros((2, groups))
+    m[0, 0], v[0, 0] = 100004.0 + 2.0 ** -7, 2.0 ** -14
+    m[1, 1:] = 16777213.0
+    assert np.array_equal(U.f64(mean), m)
+    want = 1.0 / np.sqrt(v + float(np.float32(1e-5)))
+    assert (np.abs(U.f64(rstd) - want) <= 18 * EPS * want).all()
+    rep = lambda t: np.repeat(t, D, axis=-1)[:, None]
+    yo = (U.f64(x) - rep(m)) * rep(want) + U.f64(b)
+    U.close(y, yo, 30 * EPS * (np.abs(yo) + np.abs(U.f64(b))), "y")
