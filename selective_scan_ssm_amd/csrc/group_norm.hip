@@ -263,6 +263,10 @@ constexpr int kRunGroups = 1024;
 constexpr int grad_waves(int V) { return V > 2 ? 4 : 8; }
 constexpr int grad_groups(int V) { return 128 * grad_waves(V); }
 constexpr int kRunThreads = 512, kRunWaves = kRunThreads / 64, kLanes = 256;
+// The gradient's sums over rows: a thread adds at most kSumRows rows in fp32 before a sum moves
+// on, into fp64 where it is a group's and where threads, runs and entries meet, into a second fp32
+// sum of at most kSumRows where it is a channel's: one-signed terms lose 2 kSumRows U at most, not U per row.
+constexpr int kSumRows = 128;
 struct Runs {
     int64_t per;                  // rows of a run
     int runs;                     // of a batch entry
@@ -276,7 +280,9 @@ struct Runs {
 // many (beside dy's, and the sums), and a block is the fewest groups that are eight
 // vectors wide (128 bytes at full width: a cache line) and, of few rows, give every thread one.
 constexpr int kHeld = 8, kHeldGrad = 4;
-Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V, int held, int target) {
+constexpr int64_t kAnyRows = int64_t(1) << 40, kMostGradRows = kSumRows * kSumRows;
+// most_rows: the rows that a thread may take of a run.
+Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V, int held, int target, int64_t most_rows) {
     const int D = static_cast<int>(dim / groups), most = kLanes * V;
     Runs r{};
     r.D = D;
@@ -305,7 +311,9 @@ Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V, in
     const int64_t lanes = (r.bc + V - 1) / V, ty = kRunThreads / lanes;
     int64_t n = target / (batch * r.blocks > 0 ? batch * r.blocks : 1);
     const int64_t most_runs = (rows + 4 * ty - 1) / (4 * ty);
-    n = n < 1 ? 1 : (n > most_runs ? most_runs : n);
+    const int64_t least = (rows + most_rows * ty - 1) / (most_rows * ty);
+    n = n < least ? least : (n > most_runs ? most_runs : n);
+    n = n < 1 ? 1 : n;
     r.per = (rows + n - 1) / n;
     r.runs = r.per > 0 ? static_cast<int>((rows + r.per - 1) / r.per) : 0;
     return r;
@@ -592,18 +600,17 @@ template <int V> __device__ __forceinline__ void channel_sums(ChannelSums<V> &m,
     }
     __syncthreads();
     for (int c = threadIdx.x; c < t.lanes * V; c += kRunThreads) {
-        float x = 0.0f, y = 0.0f;
+        double x = 0.0, y = 0.0;
         for (int q = 0; q < t.ty_count; ++q) {
             x += m.a[q * t.lanes + c / V][c % V];
             y += m.b[q * t.lanes + c / V][c % V];
         }
-        o[c] = x;
-        o[dim + c] = y;
+        o[c] = static_cast<float>(x);
+        o[dim + c] = static_cast<float>(y);
     }
 }
-// A thread's sums of w da and w da n
+// A thread's sums of w da and w da n, added to x and y
 template <int V> __device__ __forceinline__ void weighted(const Affine (&p)[V], const float (&u)[V], const float (&v)[V], double &x, double &y) {
-    x = y = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         x += static_cast<double>(p[i].w) * u[i];
@@ -619,29 +626,38 @@ template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribu
     for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
         const Item t = item_of<V>(a, r, n);
         float u[V] = {}, v[V] = {};
+        double s1 = 0.0, s2 = 0.0;
         Affine p[V];
         params_of<V>(a, t.ch, p);
         if (t.in) {
             const float mean = a.mean[n * a.groups + t.group], rstd = a.rstd[n * a.groups + t.group];
             Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
+            for (int64_t left = t.rows - t.ty; left > 0;) {
+                const int64_t stop = left > kSumRows * t.ty_count ? left - kSumRows * t.ty_count : 0;
+                float su[V] = {}, sv[V] = {};
 #pragma unroll 2
-            for (int64_t left = t.rows - t.ty; left > 0; left -= t.ty_count) {
-                float x[V], z[V] = {}, d[V], dz = 0.0f;
-                unpack<T, V>(load_vec<T, V>(px.next()), x);
-                unpack<T, V>(load_vec<T, V>(pd.next()), d);
-                if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
+                for (; left > stop; left -= t.ty_count) {
+                    float x[V], z[V] = {}, d[V], dz = 0.0f;
+                    unpack<T, V>(load_vec<T, V>(px.next()), x);
+                    unpack<T, V>(load_vec<T, V>(pd.next()), d);
+                    if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz);
+                        su[i] += da;
+                        sv[i] = fmaf(da, nx, sv[i]);
+                    }
+                }
+                weighted<V>(p, su, sv, s1, s2);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz);
-                    u[i] += da;
-                    v[i] = fmaf(da, nx, v[i]);
+                    u[i] += su[i];
+                    v[i] += sv[i];
                 }
             }
         }
         if (chan) channel_sums<V>(m.c, t, u, v, chan + (n * r.runs + t.run) * 2 * a.dim + (t.ch - t.tx * V), a.dim);
-        double x, y;
-        weighted<V>(p, u, v, x, y);
-        group_totals(m.t, t, x, y);
+        group_totals(m.t, t, s1, s2);
         put_totals(m.t, a, r, t, n, part);
     }
 }
@@ -717,7 +733,7 @@ template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void grou
             }
         }
         if (chan) channel_sums<V>(m.c, t, u, v, chan + n * 2 * a.dim + (t.ch - t.tx * V), a.dim);
-        double s1, s2;
+        double s1 = 0.0, s2 = 0.0;
         weighted<V>(p, u, v, s1, s2);
         group_totals(m.t, t, s1, s2);
         const float m1 = static_cast<float>(m.t.t1[t.q] * inv), m2 = static_cast<float>(m.t.t2[t.q] * inv);
@@ -740,12 +756,12 @@ template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void grou
     }
 }
 // dweight and dbias from (rows, 2, dim) partial sums (da first, or da n first), in a
-// fixed order: 16 columns to a workgroup, 64 stripes of rows
+// fixed order and in fp64: 16 columns to a workgroup, 64 stripes of rows
 __global__ __launch_bounds__(1024) void group_params_kernel(const float *part, float *first, float *second, int64_t rows, int64_t dim) {
-    __shared__ float sums[64][17];
+    __shared__ double sums[64][17];
     const int col = threadIdx.x % 16, stripe = threadIdx.x / 16;
     const int64_t d = static_cast<int64_t>(blockIdx.x) * 16 + col;
-    float s = 0.0f;
+    double s = 0.0;
     if (d < 2 * dim) {
 #pragma unroll 8
         for (int64_t r = stripe; r < rows; r += 64) s += part[r * 2 * dim + d];
@@ -753,11 +769,11 @@ __global__ __launch_bounds__(1024) void group_params_kernel(const float *part, f
     sums[stripe][col] = s;
     __syncthreads();
     const int w = threadIdx.x / 64, lane = threadIdx.x % 64;
-    s = wave_fold(sums[lane][w], AddOp());
+    s = wave_sum(sums[lane][w]);
     const int64_t o = static_cast<int64_t>(blockIdx.x) * 16 + w;
     if (lane == 0 && o < 2 * dim) {
         float *const to = o < dim ? first : second;
-        if (to) to[o < dim ? o : o - dim] = s;
+        if (to) to[o < dim ? o : o - dim] = static_cast<float>(s);
     }
 }
 
@@ -782,15 +798,20 @@ int width(const GroupNormBwdArgs &b) {
 // for it (the workspace's size does not know the addresses).
 constexpr int kMaxChunks = 4;
 bool row_form(int64_t rows, int64_t dim, int64_t groups, int v) { return rows == 1 && dim / groups <= 64 * v * kMaxChunks; }
-int64_t row_first(int64_t batch, int64_t units) {          // workgroups that share a unit's rows
-    const int64_t most = (batch + 3) / 4, n = kRowWorkgroups / units > 0 ? kRowWorkgroups / units : 1;
+// Workgroups that share a unit's rows: as many as fill the GPU; for the gradient at least so many
+// that a wave adds up kSumRows rows at most, as far as a launch's 2^32 lanes go.
+int64_t row_first(int64_t batch, int64_t units, bool bwd) {
+    const int64_t most = (batch + 3) / 4, lanes = ((int64_t(1) << 32) - 1) / kThreads / units;
+    int64_t n = kRowWorkgroups / units, least = bwd ? (batch + 4 * kSumRows - 1) / (4 * kSumRows) : 1;
+    least = least < lanes ? least : lanes;
+    n = n > least ? n : least;
     return n < most ? n : most;
 }
 
 template <typename T, int V, int P, int L, bool BWD> hipError_t run_rows(const GroupNormBwdArgs &b, hipStream_t s) {
     const GroupNormArgs &a = b.fwd;
     constexpr int GW = 64 / L;
-    const int64_t units = (a.groups + GW - 1) / GW, first = row_first(a.batch, units);
+    const int64_t units = (a.groups + GW - 1) / GW, first = row_first(a.batch, units, BWD);
     float *const part = static_cast<float *>(a.workspace);
     hipLaunchKernelGGL((group_row_kernel<T, V, P, L, BWD>), dim3(static_cast<unsigned>(units * first)), dim3(kThreads), 0, s, b, part);
     if (hipError_t e = hipGetLastError()) return e;
@@ -824,7 +845,7 @@ template <typename T, int V> hipError_t run_fwd(const GroupNormArgs &a, hipStrea
         b.fwd = a;
         return run_rows_of<T, V, false>(b, s);
     }
-    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeld, kRunGroups);
+    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeld, kRunGroups, kAnyRows);
     if (r.whole) {
         hipLaunchKernelGGL((group_whole_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, a, r);
         return hipGetLastError();
@@ -838,7 +859,7 @@ template <typename T, int V> hipError_t run_fwd(const GroupNormArgs &a, hipStrea
 template <typename T, int V> hipError_t run_bwd(const GroupNormBwdArgs &b, hipStream_t s) {
     const GroupNormArgs &a = b.fwd;
     if (row_form(a.rows, a.dim, a.groups, V)) return run_rows_of<T, V, true>(b, s);
-    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeldGrad, grad_groups(V));
+    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeldGrad, grad_groups(V), kMostGradRows);
     const bool params = b.dweight || b.dbias;
     float *const chan = params ? static_cast<float *>(a.workspace) : nullptr;
     double *const part = reinterpret_cast<double *>(static_cast<char *>(a.workspace) + chan_bytes(a.batch, r, a.dim));
@@ -862,7 +883,7 @@ size_t group_norm_workspace(int64_t batch, int64_t rows, int64_t dim, int64_t gr
     size_t most = 0;
     for (int v = 1; v <= 8; v *= 2) {
         if (dim / groups % v || row_form(rows, dim, groups, v)) continue;
-        const size_t n = part_bytes(batch, runs_of(batch, rows, dim, groups, v, kHeld, kRunGroups), groups);
+        const size_t n = part_bytes(batch, runs_of(batch, rows, dim, groups, v, kHeld, kRunGroups, kAnyRows), groups);
         most = n > most ? n : most;
     }
     return most;
@@ -873,9 +894,9 @@ size_t group_norm_bwd_workspace(int64_t batch, int64_t rows, int64_t dim, int64_
         if (dim / groups % v) continue;
         size_t n;
         if (row_form(rows, dim, groups, v)) {
-            n = static_cast<size_t>(row_first(batch, (groups + 7) / 8)) * 2 * dim * 4;      // at most 8 groups to a wave
+            n = static_cast<size_t>(row_first(batch, (groups + 7) / 8, true)) * 2 * dim * 4;      // at most 8 groups to a wave
         } else {
-            const Runs r = runs_of(batch, rows, dim, groups, v, kHeldGrad, grad_groups(v));
+            const Runs r = runs_of(batch, rows, dim, groups, v, kHeldGrad, grad_groups(v), kMostGradRows);
             n = chan_bytes(batch, r, dim) + part_bytes(batch, r, groups);
         }
         most = n > most ? n : most;

@@ -1,4 +1,4 @@
-"""The group norm's statistics far from zero."""
+"""The group norm's sums where they are long or far from zero."""
 import numpy as np
 import pytest
 
@@ -40,3 +40,34 @@ def test_groups_far_from_zero_with_next_to_no_spread(ops, R, C, groups):
     rep = lambda t: np.repeat(t, D, axis=-1)[:, None]
     yo = (U.f64(x) - rep(m)) * rep(want) + U.f64(b)
     U.close(y, yo, 30 * EPS * (np.abs(yo) + np.abs(U.f64(b))), "y")
+
+
+def one_signed(ops, N, R, D, groups):
+    """dy = 1 and x = 1/2 throughout, with mean 0 and rstd 1: da is SiLU's slope at weight / 2 + bias, the same in all
+    rows, and its sums are N R of it.  At most 128 values are added in fp32 before a sum moves on, 128 such sums after
+    it, some threads' and waves' sums and one more rounding of each: 300 U; the slope itself is off by
+    (2 |a| + 40) U relative to 1.1, its largest value."""
+    C = D * groups
+    shape = (N, R, C) if R > 1 else (N, C)
+    x = torch.full(shape, 0.5, dtype=torch.bfloat16, device="cuda")
+    dy = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
+    w, b = U.rand(1, C), U.rand(2, C)
+    got = ops.group_norm_bwd(dy, x, torch.zeros(N, groups, device="cuda"), torch.ones(N, groups, device="cuda"), groups, w, b,
+                             activation="silu")
+    a = 0.5 * U.f64(w) + U.f64(b)
+    s = 1.0 / (1.0 + np.exp(-a))
+    da = s * (1.0 + a * (1.0 - s))
+    allowed = N * R * EPS * (300.0 * np.abs(da) + 1.1 * (2.0 * np.abs(a) + 40.0))
+    for name, f in (("dbias", 1.0), ("dweight", 0.5)):
+        over = np.abs(U.f64(got[name]) - f * N * R * da) / (f * allowed)
+        assert over.max() <= 1.0, f"{name}: {over.max():.3g} times what is allowed"
+
+
+def test_one_signed_gradients_over_many_rows(ops):
+    """More workgroups than the GPU holds before any entry is cut: 4096 rows to a thread."""
+    one_signed(ops, 17, 8192, 255, 64)
+
+
+def test_one_signed_gradients_over_many_tokens(ops):
+    """Groups that fill the GPU by themselves: 4096 tokens to a wave."""
+    one_signed(ops, 16384, 1, 2, 16384)
