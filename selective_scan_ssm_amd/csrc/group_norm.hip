@@ -20,6 +20,8 @@
 #include "ssm_kernels.h"
 #include "wave_fold.h"
 
+#include <type_traits>
+
 namespace ssm {
 namespace {
 
@@ -275,6 +277,7 @@ struct Runs {
     int per_group;                // blocks of a group where one is wider than a block, else 1
     int D;                        // channels of a group
     bool whole;                   // a run is a whole batch entry, and fits the workgroup's registers
+    int64_t fold;                 // batch entries whose channel sums a workgroup of the gradient adds up
 };
 // Whole entries: a thread holds up to kHeld vectors of x (and z), the gradient half as
 // many (beside dy's, and the sums), and a block is the fewest groups that are eight
@@ -318,6 +321,18 @@ Runs runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V, in
     r.runs = r.per > 0 ? static_cast<int>((rows + r.per - 1) / r.per) : 0;
     return r;
 }
+// The gradient's runs.  Where entries have fewer rows than kSumRows and are more than fill the GPU, a
+// workgroup takes several one after the other, kSumRows rows at most, and leaves one partial sum per channel of
+// them all.  (With one per entry, 16384 x 5120 of one row took 676 MB of them, four times a bf16 x, and 1820 us
+// a call; this way 1280.  Long entries are better spread: 600 x 1024 x 2048 2900 us one by one, 3060 two by two.)
+Runs grad_runs_of(int64_t batch, int64_t rows, int64_t dim, int64_t groups, int V) {
+    Runs r = runs_of(batch, rows, dim, groups, V, kHeldGrad, grad_groups(V), kMostGradRows);
+    const int64_t full = (batch * r.blocks * r.runs + grad_groups(V) - 1) / grad_groups(V), most = rows > 0 ? kSumRows / rows : 1;
+    r.fold = full < most ? full : most;
+    r.fold = r.fold > 1 ? r.fold : 1;
+    return r;
+}
+int64_t folds(int64_t batch, const Runs &r) { return (batch + r.fold - 1) / r.fold; }
 // where a workgroup's item lies and what a thread has of it
 struct Item {
     int64_t row0, rows;                    // the run's first row (of all batch entries'), its rows
@@ -617,48 +632,53 @@ template <int V> __device__ __forceinline__ void weighted(const Affine (&p)[V], 
         y += static_cast<double>(p[i].w) * v[i];
     }
 }
-// The gradient's sums of da and da n of each run and channel, (n, run), 2, dim, and of
-// w da and w da n of each run and group
-template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribute__((amdgpu_waves_per_eu(grad_waves(V), grad_waves(V)))) void group_sums_kernel(GroupNormBwdArgs b, Runs r, double *part, float *chan) {
+// The gradient's sums of da and da n of each run and channel over r.fold entries, (fold, run), 2, dim, and of
+// w da and w da n of each entry, run and group
+// FOLD: r.fold is more than 1; else the loop over a fold costs registers (12 x 3025 x 192 41 us a call, with it 44)
+template <typename T, int V, bool FOLD> __global__ __launch_bounds__(kRunThreads) __attribute__((amdgpu_waves_per_eu(grad_waves(V), grad_waves(V)))) void group_sums_kernel(GroupNormBwdArgs b, Runs r, double *part, float *chan) {
     const GroupNormArgs &a = b.fwd;
     __shared__ union { ChannelSums<V> c; Totals t; } m;
     const bool act = a.silu != 0, gate = a.z != nullptr;
-    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
-        const Item t = item_of<V>(a, r, n);
-        float u[V] = {}, v[V] = {};
-        double s1 = 0.0, s2 = 0.0;
+    const int64_t fold = FOLD ? r.fold : 1;
+    for (int64_t n0 = blockIdx.y * fold; n0 < a.batch; n0 += gridDim.y * fold) {
+        Item t = item_of<V>(a, r, n0);
         Affine p[V];
         params_of<V>(a, t.ch, p);
-        if (t.in) {
-            const float mean = a.mean[n * a.groups + t.group], rstd = a.rstd[n * a.groups + t.group];
-            Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
-            for (int64_t left = t.rows - t.ty; left > 0;) {
-                const int64_t stop = left > kSumRows * t.ty_count ? left - kSumRows * t.ty_count : 0;
-                float su[V] = {}, sv[V] = {};
+        float u[V] = {}, v[V] = {};
+        const int64_t n1 = FOLD ? (n0 + fold < a.batch ? n0 + fold : a.batch) : n0 + 1;
+        for (int64_t n = n0; n < n1; ++n, t.row0 += a.rows) {
+            double s1 = 0.0, s2 = 0.0;
+            if (t.in) {
+                const float mean = a.mean[n * a.groups + t.group], rstd = a.rstd[n * a.groups + t.group];
+                Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
+                for (int64_t left = t.rows - t.ty; left > 0;) {
+                    const int64_t stop = left > kSumRows * t.ty_count ? left - kSumRows * t.ty_count : 0;
+                    float su[V] = {}, sv[V] = {};
 #pragma unroll 2
-                for (; left > stop; left -= t.ty_count) {
-                    float x[V], z[V] = {}, d[V], dz = 0.0f;
-                    unpack<T, V>(load_vec<T, V>(px.next()), x);
-                    unpack<T, V>(load_vec<T, V>(pd.next()), d);
-                    if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
+                    for (; left > stop; left -= t.ty_count) {
+                        float x[V], z[V] = {}, d[V], dz = 0.0f;
+                        unpack<T, V>(load_vec<T, V>(px.next()), x);
+                        unpack<T, V>(load_vec<T, V>(pd.next()), d);
+                        if (gate) unpack<T, V>(load_vec<T, V>(pz.next()), z);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz);
+                            su[i] += da;
+                            sv[i] = fmaf(da, nx, sv[i]);
+                        }
+                    }
+                    weighted<V>(p, su, sv, s1, s2);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz);
-                        su[i] += da;
-                        sv[i] = fmaf(da, nx, sv[i]);
+                        u[i] += su[i];
+                        v[i] += sv[i];
                     }
                 }
-                weighted<V>(p, su, sv, s1, s2);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    u[i] += su[i];
-                    v[i] += sv[i];
-                }
             }
+            group_totals(m.t, t, s1, s2);
+            put_totals(m.t, a, r, t, n, part);
         }
-        if (chan) channel_sums<V>(m.c, t, u, v, chan + (n * r.runs + t.run) * 2 * a.dim + (t.ch - t.tx * V), a.dim);
-        group_totals(m.t, t, s1, s2);
-        put_totals(m.t, a, r, t, n, part);
+        if (chan) channel_sums<V>(m.c, t, u, v, chan + (n0 / fold * r.runs + t.run) * 2 * a.dim + (t.ch - t.tx * V), a.dim);
     }
 }
 template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribute__((amdgpu_waves_per_eu(grad_waves(V), grad_waves(V)))) void group_grad_kernel(GroupNormBwdArgs b, Runs r, const double *part) {
@@ -692,67 +712,77 @@ template <typename T, int V> __global__ __launch_bounds__(kRunThreads) __attribu
         }
     }
 }
-// The gradient of whole batch entries in registers; the channels' sums are (n, 2, dim)
-template <typename T, int V> __global__ __launch_bounds__(kRunThreads) void group_whole_grad_kernel(GroupNormBwdArgs b, Runs r, float *chan) {
+// The gradient of whole batch entries in registers; the channels' sums are (fold, 2, dim)
+template <typename T, int V, bool FOLD> __global__ __launch_bounds__(kRunThreads) void group_whole_grad_kernel(GroupNormBwdArgs b, Runs r, float *chan) {
     const GroupNormArgs &a = b.fwd;
     __shared__ union { ChannelSums<V> c; Totals t; } m;
     const bool act = a.silu != 0, gate = a.z != nullptr;
     const double inv = 1.0 / (static_cast<double>(a.rows) * static_cast<double>(a.dim / a.groups));
     using raw = typename Vec<T, V>::raw;
-    for (int64_t n = blockIdx.y; n < a.batch; n += gridDim.y) {
-        const Item t = item_of<V>(a, r, n);
-        const int64_t ng = n * a.groups + t.group;
-        Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
-        Walk<T> po(b.dx, a.dim, t), pzo(b.dz, a.dim, t);
-        raw qx[kHeldGrad], qz[kHeldGrad], qd[kHeldGrad];
+    const int64_t fold = FOLD ? r.fold : 1;
+    for (int64_t n0 = blockIdx.y * fold; n0 < a.batch; n0 += gridDim.y * fold) {
+        Item t = item_of<V>(a, r, n0);
         Affine p[V];
-#pragma unroll
-        for (int j = 0; j < kHeldGrad; ++j) {
-            const bool in = t.in && t.ty + j * t.ty_count < t.rows;
-            qx[j] = qz[j] = qd[j] = raw{};
-            const T *const ax = px.next(), *const az = pz.next(), *const ad = pd.next();
-            if (in) qx[j] = load_vec<T, V>(ax);
-            if (in) qd[j] = load_vec<T, V>(ad);
-            if (in && gate) qz[j] = load_vec<T, V>(az);
-        }
         params_of<V>(a, t.ch, p);
-        const float mean = a.mean[ng], rstd = a.rstd[ng];
-        float u[V] = {}, v[V] = {};
+        float cu[V] = {}, cv[V] = {};
+        const int64_t n1 = FOLD ? (n0 + fold < a.batch ? n0 + fold : a.batch) : n0 + 1;
+        for (int64_t n = n0; n < n1; ++n, t.row0 += a.rows) {
+            const int64_t ng = n * a.groups + t.group;
+            Walk<const T> px(a.x, a.ldx, t), pz(a.z, a.ldz, t), pd(b.dy, a.dim, t);
+            Walk<T> po(b.dx, a.dim, t), pzo(b.dz, a.dim, t);
+            raw qx[kHeldGrad], qz[kHeldGrad], qd[kHeldGrad];
 #pragma unroll
-        for (int j = 0; j < kHeldGrad; ++j) {
-            float x[V], z[V], d[V], dz = 0.0f;
-            unpack<T, V>(qx[j], x);
-            unpack<T, V>(qd[j], d);
-            unpack<T, V>(qz[j], z);
-            const bool in = t.in && t.ty + j * t.ty_count < t.rows;
+            for (int j = 0; j < kHeldGrad; ++j) {
+                const bool in = t.in && t.ty + j * t.ty_count < t.rows;
+                qx[j] = qz[j] = qd[j] = raw{};
+                const T *const ax = px.next(), *const az = pz.next(), *const ad = pd.next();
+                if (in) qx[j] = load_vec<T, V>(ax);
+                if (in) qd[j] = load_vec<T, V>(ad);
+                if (in && gate) qz[j] = load_vec<T, V>(az);
+            }
+            const float mean = a.mean[ng], rstd = a.rstd[ng];
+            float u[V] = {}, v[V] = {};
+#pragma unroll
+            for (int j = 0; j < kHeldGrad; ++j) {
+                float x[V], z[V], d[V], dz = 0.0f;
+                unpack<T, V>(qx[j], x);
+                unpack<T, V>(qd[j], d);
+                unpack<T, V>(qz[j], z);
+                const bool in = t.in && t.ty + j * t.ty_count < t.rows;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float nx = in ? (x[i] - mean) * rstd : 0.0f, da = in ? backward(nx, d[i], p[i], act, gate, z[i], dz) : 0.0f;
+                    u[i] += da;
+                    v[i] = fmaf(da, nx, v[i]);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float nx = in ? (x[i] - mean) * rstd : 0.0f, da = in ? backward(nx, d[i], p[i], act, gate, z[i], dz) : 0.0f;
-                u[i] += da;
-                v[i] = fmaf(da, nx, v[i]);
+                cu[i] += u[i];
+                cv[i] += v[i];
+            }
+            double s1 = 0.0, s2 = 0.0;
+            weighted<V>(p, u, v, s1, s2);
+            group_totals(m.t, t, s1, s2);
+            const float m1 = static_cast<float>(m.t.t1[t.q] * inv), m2 = static_cast<float>(m.t.t2[t.q] * inv);
+#pragma unroll
+            for (int j = 0; j < kHeldGrad; ++j) {
+                T *const ao = po.next(), *const az = pzo.next();
+                if (!t.in || t.ty + j * t.ty_count >= t.rows) continue;
+                float x[V], z[V], d[V], dz[V];
+                unpack<T, V>(qx[j], x);
+                unpack<T, V>(qd[j], d);
+                unpack<T, V>(qz[j], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz[i]);
+                    x[i] = rstd * (da * p[i].w - fmaf(nx, m2, m1));
+                }
+                store_vec<T, V>(ao, x);
+                if (gate) store_vec<T, V>(az, dz);
             }
         }
-        if (chan) channel_sums<V>(m.c, t, u, v, chan + n * 2 * a.dim + (t.ch - t.tx * V), a.dim);
-        double s1 = 0.0, s2 = 0.0;
-        weighted<V>(p, u, v, s1, s2);
-        group_totals(m.t, t, s1, s2);
-        const float m1 = static_cast<float>(m.t.t1[t.q] * inv), m2 = static_cast<float>(m.t.t2[t.q] * inv);
-#pragma unroll
-        for (int j = 0; j < kHeldGrad; ++j) {
-            T *const ao = po.next(), *const az = pzo.next();
-            if (!t.in || t.ty + j * t.ty_count >= t.rows) continue;
-            float x[V], z[V], d[V], dz[V];
-            unpack<T, V>(qx[j], x);
-            unpack<T, V>(qd[j], d);
-            unpack<T, V>(qz[j], z);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float nx = (x[i] - mean) * rstd, da = backward(nx, d[i], p[i], act, gate, z[i], dz[i]);
-                x[i] = rstd * (da * p[i].w - fmaf(nx, m2, m1));
-            }
-            store_vec<T, V>(ao, x);
-            if (gate) store_vec<T, V>(az, dz);
-        }
+        if (chan) channel_sums<V>(m.c, t, cu, cv, chan + n0 / fold * 2 * a.dim + (t.ch - t.tx * V), a.dim);
     }
 }
 // dweight and dbias from (rows, 2, dim) partial sums (da first, or da n first), in a
@@ -829,11 +859,11 @@ template <typename T, int V, bool BWD> hipError_t run_rows_of(const GroupNormBwd
     if (n <= 128) return run_rows<T, V, 2, 64, BWD>(b, s);
     return run_rows<T, V, 4, 64, BWD>(b, s);
 }
-size_t chan_bytes(int64_t batch, const Runs &r, int64_t dim) { return align256(static_cast<size_t>(batch * r.runs) * 2 * dim * 4); }
+size_t chan_bytes(int64_t batch, const Runs &r, int64_t dim) { return align256(static_cast<size_t>(folds(batch, r) * r.runs) * 2 * dim * 4); }
 size_t part_bytes(int64_t batch, const Runs &r, int64_t groups) {
     return r.whole ? 0 : align256(static_cast<size_t>(batch * r.runs * groups * r.per_group) * 16);
 }
-// batch entries on y, as many as a launch's 2^32 lanes allow
+// batch entries (folds) on y, as many as a launch's 2^32 lanes allow
 dim3 grid_of(int64_t batch, const Runs &r) {
     const int64_t x = static_cast<int64_t>(r.blocks) * r.runs, fit = ((int64_t(1) << 32) - 1) / (x * kRunThreads), most = fit < 65535 ? fit : 65535;
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>(batch < most ? batch : most));
@@ -859,12 +889,18 @@ template <typename T, int V> hipError_t run_fwd(const GroupNormArgs &a, hipStrea
 template <typename T, int V> hipError_t run_bwd(const GroupNormBwdArgs &b, hipStream_t s) {
     const GroupNormArgs &a = b.fwd;
     if (row_form(a.rows, a.dim, a.groups, V)) return run_rows_of<T, V, true>(b, s);
-    const Runs r = runs_of(a.batch, a.rows, a.dim, a.groups, V, kHeldGrad, grad_groups(V), kMostGradRows);
+    const Runs r = grad_runs_of(a.batch, a.rows, a.dim, a.groups, V);
     const bool params = b.dweight || b.dbias;
     float *const chan = params ? static_cast<float *>(a.workspace) : nullptr;
     double *const part = reinterpret_cast<double *>(static_cast<char *>(a.workspace) + chan_bytes(a.batch, r, a.dim));
-    if (r.whole) hipLaunchKernelGGL((group_whole_grad_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, b, r, chan);
-    else hipLaunchKernelGGL((group_sums_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, b, r, part, chan);
+    const dim3 grid = grid_of(folds(a.batch, r), r);
+    auto first = [&](auto fold) {
+        constexpr bool FOLD = decltype(fold)::value;
+        if (r.whole) hipLaunchKernelGGL((group_whole_grad_kernel<T, V, FOLD>), grid, dim3(kRunThreads), 0, s, b, r, chan);
+        else hipLaunchKernelGGL((group_sums_kernel<T, V, FOLD>), grid, dim3(kRunThreads), 0, s, b, r, part, chan);
+    };
+    if (r.fold > 1) first(std::true_type{});
+    else first(std::false_type{});
     if (hipError_t e = hipGetLastError()) return e;
     if (!r.whole) {
         hipLaunchKernelGGL((group_grad_kernel<T, V>), grid_of(a.batch, r), dim3(kRunThreads), 0, s, b, r, part);
@@ -872,7 +908,7 @@ template <typename T, int V> hipError_t run_bwd(const GroupNormBwdArgs &b, hipSt
     }
     if (!params) return hipSuccess;
     hipLaunchKernelGGL(group_params_kernel, dim3(static_cast<unsigned>((2 * a.dim + 15) / 16)), dim3(1024), 0, s, chan, b.dbias, b.dweight,
-                       a.batch * r.runs, a.dim);
+                       folds(a.batch, r) * r.runs, a.dim);
     return hipGetLastError();
 }
 
@@ -896,7 +932,7 @@ size_t group_norm_bwd_workspace(int64_t batch, int64_t rows, int64_t dim, int64_
         if (row_form(rows, dim, groups, v)) {
             n = static_cast<size_t>(row_first(batch, (groups + 7) / 8, true)) * 2 * dim * 4;      // at most 8 groups to a wave
         } else {
-            const Runs r = runs_of(batch, rows, dim, groups, v, kHeldGrad, grad_groups(v), kMostGradRows);
+            const Runs r = grad_runs_of(batch, rows, dim, groups, v);
             n = chan_bytes(batch, r, dim) + part_bytes(batch, r, groups);
         }
         most = n > most ? n : most;

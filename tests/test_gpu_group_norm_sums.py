@@ -1,12 +1,14 @@
-"""The group norm's sums where they are long or far from zero."""
+"""The group norm's sums where they are long, far from zero, or over many batch entries."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import block_util as U
+import test_gpu_group_norm as G
 
 pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 EPS = 2.0 ** -24
 
 
@@ -40,6 +42,17 @@ def test_groups_far_from_zero_with_next_to_no_spread(ops, R, C, groups):
     rep = lambda t: np.repeat(t, D, axis=-1)[:, None]
     yo = (U.f64(x) - rep(m)) * rep(want) + U.f64(b)
     U.close(y, yo, 30 * EPS * (np.abs(yo) + np.abs(U.f64(b))), "y")
+
+
+# batch entries that share workgroups in the gradient: one wide row, few rows, rows beyond a workgroup's registers
+FOLDED = [(1500, 1, 4104, 1), (1100, 1, 5000, 2), (3000, 4, 40, 40), (2500, 2, 256, 4), (600, 64, 264, 1), (1030, 65, 130, 2),
+          (40000, 2, 24, 3)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,R,C,groups", FOLDED)
+def test_many_entries(ops, N, R, C, groups, dtype):
+    G.check(ops, G.inputs(N, R, C, DT[dtype], gate=R % 2 == 0, affine=True, seed=R), groups, silu=R != 2)
 
 
 def one_signed(ops, N, R, D, groups):

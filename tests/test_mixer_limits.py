@@ -1,4 +1,4 @@
-"""Sizes of the delta rule's workspaces at the edges of what the header admits (CPU only)."""
+"""Sizes of the delta rule's and the group norm's workspaces at the edges of what the header admits (CPU only)."""
 import os
 
 import pytest
@@ -37,3 +37,12 @@ def test_more_segments_than_a_launch_holds_are_not_cut(lib, io, dk, seqlen, nseq
 def test_fewer_are_cut(lib):
     need = lib.ssm_delta_scan_workspace_bytes(1, 3_800_000, 1, 1000, 1, 1, 8, 8, BF16)
     assert need != BAD and need > whole(3_800_000 // 64 + 1000, 1) + 1000 * 256
+
+
+# (batch, rows, dim, groups): a layer norm of wide rows, two rows to an entry, a narrow map, head norms
+@pytest.mark.parametrize("N,R,C,groups", [(16384, 1, 5120, 1), (65536, 2, 4096, 1), (16384, 1, 2048, 1), (1 << 20, 4, 96, 8), (1 << 20, 1, 1536, 12),
+                                          (1 << 16, 64, 256, 2)])
+def test_the_gradient_keeps_no_partial_sums_per_entry(lib, N, R, C, groups):
+    """What the partial sums take is a part of x, not more than it."""
+    need = lib.ssm_group_norm_bwd_workspace_bytes(N, R, C, groups)
+    assert need != BAD and need <= N * R * C * 2 // 2
