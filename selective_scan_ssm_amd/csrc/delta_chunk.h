@@ -588,10 +588,11 @@ struct Plan {
 // Measured, us a call, bf16: 2 x 8192 steps of 40 heads of 128 x 128, 64 channels to a
 // workgroup, 1 / 2 / 3 segments 511 / 629 / 626, 128 channels 588 / 574 / 495 to 590 (the clock
 // gives way when every CU is at work for long); 65536 steps of 8 heads of 64 x 64,
-// 1 / 8 / 16 / 32 / 64 segments 2002 / 565 / 367 / 334 / 369; fp32, the gradient of 2 x 777 steps of 6
-// heads of 64 x 64 (13 chunks), kernels, 1 / 3 / 4 segments 242 / 214 / 192.  Under 12 chunks a
-// sequence stays whole: two launches more cost what is won.  The gradient's walk backwards is
-// cut alike.
+// 1 / 8 / 16 / 32 / 64 segments 2002 / 565 / 367 / 334 / 369.  Short sequences, 4 heads of 64 x 64: 12 chunks
+// in bf16 35 whole, 33 in four, 31 in six, 16 in fp32 120 whole, 75 in four, 61 in sixteen, their gradients 258, 167,
+// 129; 128 x 128 in bf16, 12 chunks, 42 whole, 48 in two.  Under 12 chunks a sequence stays whole, so that its results
+// are to the bit what they are between others: for bf16 the model would leave it so, in fp32 it costs
+// 59 us instead of 46 at 6 chunks, 83 instead of 55 at 10.  The gradient's walk backwards is cut alike.
 inline Plan plan_of(const DeltaShape &s, int bf16) {
     const bool big = s.dk > 64;
     const double c4 = bf16 ? (big ? 2.75 : 1.95) : (big ? 11.5 : 5.4), c8 = big ? 5.0 : 3.2;
@@ -605,7 +606,7 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
     Plan best{0x7fffffff, s.nseq, false, false};
     double least = -1.0;
     for (int64_t n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
-        if (n > 1 && (nc < 12 || nc < 3 * n)) break;
+        if (n > 1 && (nc < 12 || n > nc)) break;
         const int64_t cps = (nc + n - 1) / n;
         const double out4 = rounds(t4 * units * n) * c4, out8 = rounds(t8 * units * n) * c8;
         const double ends4 = rounds(units * (t4 * (n - 1) + k4 * (n - 2))) * e4, ends8 = rounds(units * (t8 * (n - 1) + k8 * (n - 2))) * e8;

@@ -39,6 +39,19 @@ def test_fewer_are_cut(lib):
     assert need != BAD and need > whole(3_800_000 // 64 + 1000, 1) + 1000 * 256
 
 
+@pytest.mark.parametrize("io,dk", [(F32, 64), (F32, 128), (BF16, 64), (BF16, 128)])
+def test_sequences_under_twelve_chunks_stay_whole(lib, io, dk):
+    """Their results are then the same between others, cut or not."""
+    for batch, T in ((1, 64), (1, 705 - 1), (3, 704)):
+        need = lib.ssm_delta_scan_workspace_bytes(batch, T, 0, 0, 4, 4, dk, dk, io)
+        assert 0 <= need - whole(batch * -(-T // 64), 4) < 3 * 256
+    chunks = 16
+    need = lib.ssm_delta_scan_workspace_bytes(1, 64 * chunks, 0, 0, 4, 4, dk, dk, F32)
+    # fp32: two chunks to a segment, or one; a state and a transition where one ends that is not the last
+    ends = (need - whole(chunks, 4)) // (4 * (dk * dk * 4 + (dk // 32) * (dk // 16) * 2048))
+    assert ends >= 7
+
+
 # (batch, rows, dim, groups): a layer norm of wide rows, two rows to an entry, a narrow map, head norms
 @pytest.mark.parametrize("N,R,C,groups", [(16384, 1, 5120, 1), (65536, 2, 4096, 1), (16384, 1, 2048, 1), (1 << 20, 4, 96, 8), (1 << 20, 1, 1536, 12),
                                           (1 << 16, 64, 256, 2)])
