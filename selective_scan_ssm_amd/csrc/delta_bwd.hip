@@ -30,7 +30,7 @@ struct BwdParams {
 };
 // A segment of the walk backwards: where it starts and what it has to do.
 struct RevPart {
-    int64_t head, kh, seq, id, lastrow, lastunit;
+    int64_t head, kh, seq, edge, lastrow, lastunit;
     int tile, vt, nch, n;          // n: steps of the chunk that it starts with
     bool first, last, transition, used;
 };
@@ -44,14 +44,14 @@ template <int KP, bool ENDS, int NW> __device__ __forceinline__ RevPart rev_part
     r.tile = static_cast<int>(blockIdx.x / per_tile);
     r.head = rest % H;
     r.kh = r.head / (H / sh.kheads);
-    r.id = rest / H;
     Span sp;
-    const Segment sg = segment_of(sh, r.id, p.seq.cps, sp);
+    const Segment sg = segment_of<ENDS ? kBehindEdges : kAllSegments>(sh, rest / H, p.seq.edges, p.seq.cps, sp);
     r.seq = sg.seq;
+    r.edge = sg.edge;
     r.first = sg.s == 0;
     r.last = sg.last;
     r.transition = ENDS && r.tile >= nvt;
-    r.used = sg.used && !(ENDS && (r.first || (r.last && r.transition)));
+    r.used = sg.used && !(ENDS && r.last && r.transition);
     r.vt = r.transition ? 0 : r.tile;
     r.tile -= nvt;
     r.nch = sg.j1 - sg.j0;
@@ -67,7 +67,7 @@ template <int KP, bool ENDS> __device__ __forceinline__ void rev_start(f32x4 (&d
     if (r.transition) {
         unit_columns<KP>(dS, r.tile * wide + w * 16, lane);
     } else if (!ENDS && !r.last) {
-        load_state<KP>(dS, p.seq.ends + ((r.id + 1) * a.s.heads + r.head) * VK, v0, V, K, lane);
+        load_state<KP>(dS, p.seq.ends + ((r.edge + 1) * a.s.heads + r.head) * VK, v0, V, K, lane);
     } else if (r.last && p.b.dlast) {
         load_state<KP>(dS, p.b.dlast + (r.seq * a.s.heads + r.head) * VK, v0, V, K, lane);
     } else {
@@ -80,7 +80,7 @@ __device__ __forceinline__ void rev_end(const f32x4 (&dS)[KP / 16], const BwdPar
     const DeltaArgs &a = p.b.fwd;
     const int K = static_cast<int>(a.s.dk), V = static_cast<int>(a.s.dv);
     const size_t VK = static_cast<size_t>(V) * K;
-    const int64_t unit = r.id * a.s.heads + r.head;
+    const int64_t unit = r.edge * a.s.heads + r.head;
     if constexpr (ENDS) {
         if (r.transition) store_map<T, KP, NW>(dS, smem, w, lane, p.seq.maps + unit * kMapBytes<KP>, r.tile * 16 * NW);
         else store_state<KP>(dS, p.seq.ends + unit * VK, v0, V, K, lane);
@@ -834,7 +834,7 @@ __global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(3,
 // against 247 wide; 16 x 2048 of 12 (384), the call 944 against 899; 24 x 1024 of 12 (576) 656 against 701.
 template <typename T, int KP, bool ENDS> hipError_t launch_rev(const BwdParams &p, hipStream_t s) {
     const DeltaShape &sh = p.b.fwd.s;
-    auto groups = [&](int wide) { return ((sh.dv + wide - 1) / wide + (ENDS ? (KP + wide - 1) / wide : 0)) * sh.heads * p.seq.segments; };
+    auto groups = [&](int wide) { return ((sh.dv + wide - 1) / wide + (ENDS ? (KP + wide - 1) / wide : 0)) * sh.heads * (ENDS ? p.seq.edges : p.seq.segments); };
     if constexpr (sizeof(T) == 4) {
         constexpr size_t lds = rev_lds<KP>();
         hipLaunchKernelGGL((delta_rev_kernel<KP, ENDS>), dim3(static_cast<unsigned>(groups(64))), dim3(kThreads), lds, s, p);
@@ -895,6 +895,7 @@ template <typename T, int KP> hipError_t run(const DeltaBwdArgs &b, hipStream_t 
     q.wide = plan.wide;
     q.wide_ends = plan.wide_ends;
     q.segments = plan.segments;
+    q.edges = plan.edges;
     q.ends = reinterpret_cast<float *>(base + w.ends);
     q.maps = base + w.maps;
     if (sh.slots > 0) {

@@ -21,9 +21,9 @@ struct SeqParams {
     ChunkWs ws;
     int cps;                        // chunks of a time segment
     bool wide, wide_ends;           // see Plan
-    int64_t segments;               // slots of segments
-    float *ends;                    // per (segment, head): (V, K) fp32, the state it leaves
-    char *maps;                     // per (segment, head): its transition as operands
+    int64_t segments, edges;        // and their borders (see Segment)
+    float *ends;                    // per (border, head): (V, K) fp32, the state that passes it
+    char *maps;                     // per (border, head): the transition of the segment that ends there, as operands
 };
 // Operands of a segment's transition: (KP / 32, KP / 16) of them.
 template <int KP> constexpr int64_t kMapBytes = static_cast<int64_t>(KP / 32) * (KP / 16) * kOp2Bytes;
@@ -279,13 +279,13 @@ template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_s
     const int tile = blockIdx.x % tiles_n;
     const int64_t rest = blockIdx.x / tiles_n, head = rest % H, kh = head / (H / a.s.kheads), id = rest / H;
     Span sp;
-    const Segment sg = segment_of(a.s, id, p.cps, sp);
+    const Segment sg = segment_of<MODE == kEnds ? kBeforeEdges : kAllSegments>(a.s, id, p.edges, p.cps, sp);
     if (!sg.used) return;
     const int64_t seq = sg.seq;
     const int j0 = sg.j0, j1 = sg.j1;
     const bool first = sg.s == 0, last = sg.last;
     const bool transition = MODE == kEnds && tile >= nvt;
-    if (MODE == kEnds && (last || (first && transition))) return;
+    if (MODE == kEnds && first && transition) return;
     const int vt = transition ? 0 : tile;
     const int v0 = vt * kWide + w * 16;                    // the wave's first channel
     const f32x4 zero = {0, 0, 0, 0};
@@ -294,7 +294,7 @@ template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_s
     if (transition) {
         unit_columns<KP>(S, (tile - nvt) * kWide + w * 16, lane);
     } else if (MODE != kEnds && !first) {
-        load_state<KP>(S, p.ends + ((id - 1) * H + head) * VK, v0, V, K, lane);
+        load_state<KP>(S, p.ends + (sg.edge * H + head) * VK, v0, V, K, lane);
     } else if (first && a.h0) {
         load_state<KP>(S, a.h0 + (seq * H + head) * VK, v0, V, K, lane);
     } else {
@@ -477,10 +477,10 @@ template <int KP, Mode MODE> __global__ __launch_bounds__(kThreads) void delta_s
     }
     if constexpr (MODE == kEnds) {
         if (!transition) {
-            store_state<KP>(S, p.ends + (id * H + head) * VK, v0, V, K, lane);
+            store_state<KP>(S, p.ends + ((sg.edge + 1) * H + head) * VK, v0, V, K, lane);
             return;
         }
-        store_map<T, KP, kWaves>(S, smem, w, lane, p.maps + (id * H + head) * kMapBytes<KP>, (tile - nvt) * kWide);
+        store_map<T, KP, kWaves>(S, smem, w, lane, p.maps + ((sg.edge + 1) * H + head) * kMapBytes<KP>, (tile - nvt) * kWide);
     } else {
         if (last && a.last_state) {
             store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
@@ -507,11 +507,11 @@ template <typename T, int KP, bool REV> __global__ __launch_bounds__(64) void de
     const int64_t rest = blockIdx.x / nt, head = rest % H, seq = rest / H;
     const Span sp = span_of(a.s, seq);
     const int nc = (sp.len + kC - 1) / kC, ns = (nc + p.cps - 1) / p.cps;
-    const int64_t first = a.s.starts ? sp.slot0 / p.cps + seq : seq * (ns > 0 ? ns : 1);
-    const size_t VK = static_cast<size_t>(V) * K;
     if (ns < 3) return;
+    const int64_t first = first_edge(a.s, seq, sp.slot0, ns, p.cps);
+    const size_t VK = static_cast<size_t>(V) * K;
     f32x4 S[KT];
-    auto unit = [&](int s) { return (first + (REV ? ns - 1 - s : s)) * H + head; };
+    auto unit = [&](int s) { return (first + (REV ? ns - 2 - s : s)) * H + head; };
     load_state<KP>(S, p.ends + unit(0) * VK, v0, V, K, lane);
     // a step is little more than the latency of its loads: as many steps ahead as registers hold
     constexpr int AHEAD = KP > 64 ? 1 : 3;
@@ -561,7 +561,7 @@ template <typename T, int KP, bool BWD> hipError_t launch_prep(const DeltaArgs &
 template <int KP, Mode MODE> hipError_t launch_seq(const SeqParams &p, hipStream_t s) {
     constexpr int wide = 64;
     const int64_t nvt = (p.a.s.dv + wide - 1) / wide;
-    const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * p.segments;
+    const int64_t grid = (MODE == kEnds ? (nvt + (KP + wide - 1) / wide) * p.edges : nvt * p.segments) * p.a.s.heads;
     constexpr size_t lds = seq_lds<KP, MODE>();
     hipLaunchKernelGGL((delta_seq_kernel<KP, MODE>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), lds, s, p);
     return hipGetLastError();
@@ -573,11 +573,11 @@ template <typename T, int KP, bool REV> hipError_t launch_carry(const SeqParams 
 }
 
 // ----------------------------------------------------------------- time segments
-// The chunks of a segment (INT32_MAX: sequences are not cut), the segments' slots, and
+// The chunks of a segment (INT32_MAX: sequences are not cut), the segments' slots and their borders', and
 // whether bf16's workgroups hold 128 value channels (eight waves) instead of 64.
 struct Plan {
     int cps;
-    int64_t segments;
+    int64_t segments, edges;
     bool wide, wide_ends;
 };
 // The cheapest of some ways to cut, by what a chunk takes a workgroup alone on its CU
@@ -593,6 +593,8 @@ struct Plan {
 // 129; 128 x 128 in bf16, 12 chunks, 42 whole, 48 in two.  Under 12 chunks a sequence stays whole, so that its results
 // are to the bit what they are between others: for bf16 the model would leave it so, in fp32 it costs
 // 59 us instead of 46 at 6 chunks, 83 instead of 55 at 10.  The gradient's walk backwards is cut alike.
+inline int64_t map_bytes(const DeltaShape &s) { return s.dk > 64 ? kMapBytes<128> : kMapBytes<64>; }
+inline int64_t edge_bytes(const DeltaShape &s) { return s.dv * s.dk * 4 + map_bytes(s); }      // of a border and head
 inline Plan plan_of(const DeltaShape &s, int bf16) {
     const bool big = s.dk > 64;
     const double c4 = bf16 ? (big ? 2.75 : 1.95) : (big ? 11.5 : 5.4), c8 = big ? 5.0 : 3.2;
@@ -600,23 +602,24 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
     const int64_t nc = s.nseq > 0 ? (s.slots + s.nseq - 1) / s.nseq : 0, units = s.heads * s.nseq;
     const int64_t t4 = (s.dv + 63) / 64, t8 = (s.dv + 127) / 128, k4 = big ? 2 : 1, k8 = 1;
     const bool may = bf16 && s.dv > 64;
-    // the pass over the segments' ends, the launch with the most workgroups, has to hold them
-    auto fits = [&](int64_t segments) { return (t4 + k4) * s.heads * segments <= kDeltaMaxGroups; };
+    // what a launch holds: the walk over the segments, the pass over their ends
+    auto fits = [&](int64_t edges) { return t4 * s.heads * (s.nseq + edges) <= kDeltaMaxGroups && (t4 + k4) * s.heads * edges <= kDeltaMaxGroups; };
     auto rounds = [](int64_t n) { return static_cast<double>((n + 255) / 256); };
-    Plan best{0x7fffffff, s.nseq, false, false};
+    Plan best{0x7fffffff, s.nseq, 0, false, false};
     double least = -1.0;
     for (int64_t n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
         if (n > 1 && (nc < 12 || n > nc)) break;
         const int64_t cps = (nc + n - 1) / n;
         const double out4 = rounds(t4 * units * n) * c4, out8 = rounds(t8 * units * n) * c8;
         const double ends4 = rounds(units * (t4 * (n - 1) + k4 * (n - 2))) * e4, ends8 = rounds(units * (t8 * (n - 1) + k8 * (n - 2))) * e8;
-        Plan p{0x7fffffff, s.nseq, may && out8 < out4, may && ends8 < ends4};
+        Plan p{0x7fffffff, s.nseq, 0, may && out8 < out4, may && ends8 < ends4};
         double cost = cps * (p.wide ? out8 : out4);
         if (n > 1) {
             cost += cps * (p.wide_ends ? ends8 : ends4) + (n - 2) * step + 15.0;
             p.cps = static_cast<int>(cps);
-            p.segments = s.packed ? s.slots / cps + s.nseq : s.nseq * ((nc + cps - 1) / cps);
-            if (!fits(p.segments)) break;
+            p.edges = s.packed ? s.slots / cps : s.nseq * ((nc + cps - 1) / cps - 1);
+            p.segments = s.nseq + p.edges;
+            if (!fits(p.edges)) break;
         }
         if (least < 0.0 || cost < least) {
             least = cost;
@@ -624,27 +627,31 @@ inline Plan plan_of(const DeltaShape &s, int bf16) {
         }
     }
     // Packed sequences of which one may be much longer than the average would all wait for that one: those beyond the
-    // average, beyond what keeps every CU at work and beyond 8 chunks are cut, if the segments' ends take no more memory
+    // average, beyond what keeps every CU at work and beyond 8 chunks are cut, if what the borders keep takes no more memory
     // than T and P.  9 sequences of 1 to 24 chunks, 12 heads of 96 x 80, fp32: 293 us a call whole, 238 cut at 9 chunks, 275 at 7.
     if (s.packed && best.segments == s.nseq && s.nseq > 0) {
         const int64_t longest = (s.seqlen + kC - 1) / kC, work = (s.slots * s.heads * (best.wide ? t8 : t4) + 255) / 256;
         int64_t cps = nc > work ? nc : work;
         cps = cps > 8 ? cps : 8;
-        const int64_t segments = s.slots / cps + s.nseq;
-        // taken that the longest is half of all: its chunks beyond cps against the ends' pass and the join
+        const int64_t edges = s.slots / cps, segments = s.nseq + edges;
+        // the lengths are on the device; taken that the longest is half of all: its chunks beyond cps against the ends' pass
+        // and the join.  What is wrong with that costs two launches and some workgroups that find nothing: 4 heads of 128 x 128
+        // in bf16, 64 sequences of 64 steps 27 whole, 33 so planned, 8 of 512 38 and 41; with a 65th one of 3000 130 and 101
+        // (fp32 567 and 241), one of 4000 with 20 of 16 144 and 103
         const double won = (longest / 2 - cps) * (best.wide ? c8 : c4), lost = cps * e4 + 15.0 + longest / (2 * cps) * step;
-        if (won > lost && fits(segments) && segments * s.dv * s.dk * 4 <= s.slots * 2 * kTriBytes) {
+        if (won > lost && fits(edges) && edges * edge_bytes(s) <= s.slots * 2 * kTriBytes) {
             best.cps = static_cast<int>(cps);
             best.segments = segments;
+            best.edges = edges;
         }
     }
     return best;
 }
 inline size_t ends_bytes(const DeltaShape &s, const Plan &p) {
-    return p.segments == s.nseq ? 0 : align256(static_cast<size_t>(p.segments * s.heads * s.dv * s.dk) * 4);
+    return align256(static_cast<size_t>(p.edges * s.heads * s.dv * s.dk) * 4);
 }
 inline size_t maps_bytes(const DeltaShape &s, const Plan &p) {
-    return p.segments == s.nseq ? 0 : align256(static_cast<size_t>(p.segments * s.heads) * (s.dk > 64 ? kMapBytes<128> : kMapBytes<64>));
+    return align256(static_cast<size_t>(p.edges * s.heads * map_bytes(s)));
 }
 
 }  // namespace

@@ -121,17 +121,16 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     const int64_t H = a.s.heads;
     constexpr int kWide = 16 * NW;
     const int nvt = (V + kWide - 1) / kWide, tiles_n = MODE == kEnds ? nvt + (KP + kWide - 1) / kWide : nvt;
-    // a segment's tiles lie a whole number of segments apart: on the same XCD where that is a multiple of eight, and
-    // those that find nothing to do are spread evenly
+    // a segment's tiles lie a whole number of segments apart: on the same XCD where that is a multiple of eight
     const int64_t per_tile = gridDim.x / tiles_n;
     const int tile = static_cast<int>(blockIdx.x / per_tile);
     const int64_t rest = blockIdx.x % per_tile, head = rest % H, kh = head / (H / a.s.kheads), id = rest / H;
     Span sp;
-    const Segment sg = segment_of(a.s, id, p.cps, sp);
+    const Segment sg = segment_of<MODE == kEnds ? kBeforeEdges : kAllSegments>(a.s, id, p.edges, p.cps, sp);
     if (!sg.used) return;
     const int64_t seq = sg.seq;
     const bool first = sg.s == 0, last = sg.last, transition = MODE == kEnds && tile >= nvt;
-    if (MODE == kEnds && (last || (first && transition))) return;
+    if (MODE == kEnds && first && transition) return;
     const int vt = transition ? 0 : tile;
     const int64_t row0 = sp.row0 + static_cast<int64_t>(sg.j0) * kC, unit0 = (sp.slot0 + sg.j0) * H + head;
     const int nch = sg.j1 - sg.j0;
@@ -179,7 +178,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     if (transition) {
         unit_columns<KP>(S, (tile - nvt) * kWide + w * 16, lane);
     } else if (MODE != kEnds && !first) {
-        load_state<KP>(S, p.ends + ((id - 1) * H + head) * VK, v0, V, K, lane);
+        load_state<KP>(S, p.ends + (sg.edge * H + head) * VK, v0, V, K, lane);
     } else if (first && a.h0) {
         load_state<KP>(S, a.h0 + (seq * H + head) * VK, v0, V, K, lane);
     } else {
@@ -351,10 +350,10 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
     }
     if constexpr (MODE == kEnds) {
         if (!transition) {
-            store_state<KP>(S, p.ends + (id * H + head) * VK, v0, V, K, lane);
+            store_state<KP>(S, p.ends + ((sg.edge + 1) * H + head) * VK, v0, V, K, lane);
             return;
         }
-        store_map<T, KP, NW>(S, smem, w, lane, p.maps + (id * H + head) * kMapBytes<KP>, (tile - nvt) * kWide);
+        store_map<T, KP, NW>(S, smem, w, lane, p.maps + ((sg.edge + 1) * H + head) * kMapBytes<KP>, (tile - nvt) * kWide);
     } else if (last && a.last_state) {
         store_state<KP>(S, a.last_state + (seq * H + head) * VK, v0, V, K, lane);
     }
@@ -363,7 +362,7 @@ __global__ __launch_bounds__(kFlowThreads<NW>) __attribute__((amdgpu_waves_per_e
 template <int KP, Mode MODE, int NW> hipError_t launch_flow(const SeqParams &p, hipStream_t s) {
     constexpr int wide = 16 * NW;
     const int64_t nvt = (p.a.s.dv + wide - 1) / wide;
-    const int64_t grid = (MODE == kEnds ? nvt + (KP + wide - 1) / wide : nvt) * p.a.s.heads * p.segments;
+    const int64_t grid = (MODE == kEnds ? (nvt + (KP + wide - 1) / wide) * p.edges : nvt * p.segments) * p.a.s.heads;
     constexpr size_t lds = 2 * FlowBuf<KP, NW>::bytes;
     hipLaunchKernelGGL((delta_flow_kernel<KP, MODE, NW>), dim3(static_cast<unsigned>(grid)), dim3(kFlowThreads<NW>), lds, s, p);
     return hipGetLastError();

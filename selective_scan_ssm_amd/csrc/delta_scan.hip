@@ -32,6 +32,7 @@ template <typename T, int KP> hipError_t run(const DeltaArgs &a, hipStream_t s) 
     p.wide = plan.wide;
     p.wide_ends = plan.wide_ends;
     p.segments = plan.segments;
+    p.edges = plan.edges;
     p.ends = reinterpret_cast<float *>(base + w.ends);
     p.maps = base + w.maps;
     if (a.s.slots > 0) {

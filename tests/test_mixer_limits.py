@@ -22,16 +22,17 @@ def whole(slots, heads):
     return 2 * 12288 * slots * heads + 768 * slots * heads
 
 
-# most of the sequences empty, one of millions of steps: the pass over the segments' ends has two or three workgroups to a
-# segment, of 256 (fp32) or 320 lanes
+# most of the sequences empty, one of millions of steps: the pass over the segments' ends has two or three workgroups of
+# 256 (fp32) or 320 lanes to a border between two segments, the walk over the segments one to each and to each sequence
 @pytest.mark.parametrize("io,dk,seqlen,nseq", [(BF16, 8, 7_000_000, 7_300_000), (F32, 72, 7_000_000, 7_300_000), (BF16, 72, 7_000_000, 5_000_000),
                                                (BF16, 128, 7_000_000, 7_300_000)])
-def test_more_segments_than_a_launch_holds_are_not_cut(lib, io, dk, seqlen, nseq):
+def test_segments_fit_a_launch(lib, io, dk, seqlen, nseq):
     slots = seqlen // 64 + nseq
     need = lib.ssm_delta_scan_workspace_bytes(1, seqlen, 1, nseq, 1, 1, dk, 8, io)
-    groups = 1 + (1 if dk <= 64 else 2)
-    assert slots * groups * (256 if io == F32 else 320) > (1 << 32) - 1
-    assert need != BAD and need - whole(slots, 1) < 3 * 256
+    assert need != BAD
+    groups, lanes, keys = 1 + (1 if dk <= 64 else 2), 256 if io == F32 else 320, 64 if dk <= 64 else 128
+    borders = (need - whole(slots, 1)) // (8 * dk * 4 + keys // 32 * (keys // 16) * 2048)
+    assert groups * lanes * borders < 1 << 32 and lanes * (nseq + borders) < 1 << 32
 
 
 def test_fewer_are_cut(lib):
@@ -50,6 +51,15 @@ def test_sequences_under_twelve_chunks_stay_whole(lib, io, dk):
     # fp32: two chunks to a segment, or one; a state and a transition where one ends that is not the last
     ends = (need - whole(chunks, 4)) // (4 * (dk * dk * 4 + (dk // 32) * (dk // 16) * 2048))
     assert ends >= 7
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_sequences_that_are_not_cut_keep_nothing_at_their_ends(lib, io):
+    """A state and a transition are kept between two segments of a sequence, of which eight chunks make one at least."""
+    seqlen, nseq = 41000, 300
+    slots = seqlen // 64 + nseq
+    need = lib.ssm_delta_scan_workspace_bytes(1, seqlen, 1, nseq, 2, 2, 64, 64, io)
+    assert whole(slots, 2) < need <= whole(slots, 2) + slots // 8 * 2 * (64 * 64 * 4 + 2 * 4 * 2048) + 5 * 256
 
 
 # (batch, rows, dim, groups): a layer norm of wide rows, two rows to an entry, a narrow map, head norms
