@@ -629,7 +629,8 @@ size_t ssm_grad_norm_workspace_bytes(int64_t count);
  *          be a column range of a wider tensor (heads side by side in it)
  *   g, beta : (batch, seqlen, nheads) fp32, contiguous.  g is the logarithm of the
  *          decay, g <= 0 for one that does not grow; at and below -104 the decay is
- *          0, so -inf restarts the state.  beta = 0 and g = 0 leave the state as it
+ *          0, so -inf restarts the state (below fp32's smallest normal number it may
+ *          be).  beta = 0 and g = 0 leave the state as it
  *          is.  Keys of length at most 1 and beta in [0, 2] keep it bounded.
  *   h0, last_state : (sequences, nheads, headdim, dstate) fp32, optional
  *   y    : (batch, seqlen, nheads, headdim) io dtype, contiguous
@@ -651,8 +652,16 @@ size_t ssm_grad_norm_workspace_bytes(int64_t count);
  *   less than 2 GiB (of v and y, of a state too, in fp32); at most 7456540 workgroups, one
  *   per chunk (or sequence), head and 64 channels.  scale finite (SSM_ERR_VALUE).  All tensors
  *   16-byte aligned but g, beta and starts.  Workspace:
- *   ssm_delta_scan_workspace_bytes, 256-byte aligned.  Sums are added in a fixed
- *   order: results are deterministic.
+ *   ssm_delta_scan_workspace_bytes, 256-byte aligned: 25 KB per 64 steps and head, and
+ *   where sequences are cut in time a state and a transition per cut and head (128 x
+ *   128: 128 KB).
+ *   Precision: states, sums and decays are fp32 or fp64.  fp32 io multiplies in fp32.
+ *   In bf16 io computed values enter products with 17 bits: fp32 outputs (last_state;
+ *   dg, dbeta, dh0 of the gradient) are off by some 5e-6 of their size, bf16 ones by
+ *   their rounding; a caller who needs those to fp32's own precision passes fp32 io.
+ *   Sums are added in a fixed order: the same call gives the same bits.  How a sequence
+ *   of 12 chunks or more is cut goes by all sequences of the call (so does a shorter
+ *   one's among packed ones), and its last bits with it.
  */
 int ssm_delta_scan_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                        const float *g, const float *beta, float scale, const float *h0,
@@ -686,7 +695,10 @@ size_t ssm_delta_ckpt_bytes(int64_t batch, int64_t seqlen, int packed, int64_t n
  *   that share a key head; dv like v, contiguous; dg, dbeta fp32; all required.
  *   dh0 optional (written even when h0 is NULL).
  *   Workspace: ssm_delta_scan_bwd_workspace_bytes (`saved`: whether ckpt is
- *   given), 256-byte aligned.  Sums are added in a fixed order.
+ *   given), 256-byte aligned: per 64 steps and head 25 KB and 4 headdim (dstate + 64)
+ *   bytes (128 x 128: 124 KB in all), without ckpt 12 KB more and what ckpt would take
+ *   (98 KB); cuts as above.
+ *   Precision and order of sums as in the forward.
  */
 int ssm_delta_scan_bwd(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                        const float *g, const float *beta, float scale, const float *h0,
@@ -725,8 +737,9 @@ int ssm_delta_state_update(float *state, const void *q, const void *k, const voi
  *   y    : (batch, rows, dim) io dtype, contiguous
  *   mean, rstd : (batch, groups) fp32, optional outputs: what the gradient takes
  *   dim in [1, SSM_MAX_GROUP_DIM], a multiple of groups; eps finite and >= 0
- *   (SSM_ERR_VALUE).  Over several rows up to 8 neighbouring values are added in
- *   fp32, the rest in fp64.  Workspace:
+ *   (SSM_ERR_VALUE).  One row: sums in fp32, of x, then of (x - mean)^2.  Over several
+ *   rows up to 8 neighbouring values are added in fp32, the rest in fp64.  Squares are
+ *   taken in fp32: a spread beyond 1e19 gives rstd 0.  Workspace:
  *   ssm_group_norm_workspace_bytes, 256-byte aligned (NULL when that is 0).
  *   batch * rows == 0: nothing is enqueued.
  */
@@ -746,8 +759,10 @@ size_t ssm_group_norm_workspace_bytes(int64_t batch, int64_t rows, int64_t dim, 
  *     dz = dy act(a) SiLU'(z),  dweight = sum da n,  dbias = sum da
  *   dy (batch, rows, dim) io dtype, contiguous; dx the same, required; dz the same,
  *   required when z is given; dweight, dbias (dim) fp32, optional (written even
- *   when weight, bias are NULL).  Workspace: ssm_group_norm_bwd_workspace_bytes.
- *   Sums are added in a fixed order.  batch * rows == 0 gives zero dweight, dbias.
+ *   when weight, bias are NULL).  Workspace: ssm_group_norm_bwd_workspace_bytes, at
+ *   most about the size of a bf16 x, of large batches far less.  At most 128 rows are
+ *   added in fp32 before a sum moves on, and 128 of those.  Sums are added in a fixed
+ *   order.  batch * rows == 0 gives zero dweight, dbias.
  */
 int ssm_group_norm_bwd(const void *dy, const void *x, int64_t ldx, const void *z, int64_t ldz,
                        const float *weight, const float *bias, const float *mean, const float *rstd,

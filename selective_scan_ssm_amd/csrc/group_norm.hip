@@ -786,7 +786,7 @@ template <typename T, int V, bool FOLD> __global__ __launch_bounds__(kRunThreads
     }
 }
 // dweight and dbias from (rows, 2, dim) partial sums (da first, or da n first), in a
-// fixed order and in fp64: 16 columns to a workgroup, 64 stripes of rows
+// fixed order: 16 columns to a workgroup, 64 stripes of rows (column_sum.h's way, but in fp64 and to two outputs)
 __global__ __launch_bounds__(1024) void group_params_kernel(const float *part, float *first, float *second, int64_t rows, int64_t dim) {
     __shared__ double sums[64][17];
     const int col = threadIdx.x % 16, stripe = threadIdx.x / 16;
