@@ -84,3 +84,23 @@ def test_one_signed_gradients_over_many_rows(ops):
 def test_one_signed_gradients_over_many_tokens(ops):
     """Groups that fill the GPU by themselves: 4096 tokens to a wave."""
     one_signed(ops, 16384, 1, 2, 16384)
+
+
+def test_more_entries_than_a_launch_has_rows_of(ops):
+    """Entries too long to share workgroups, more than a launch's second axis holds."""
+    G.check(ops, G.inputs(66000, 65, 1, torch.float32, seed=7), 1)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("R,C", [(3000, 64), (2, 4100)])
+def test_a_bad_first_value_stays_in_its_group(ops, R, C, bad):
+    """The first value of a group is what its runs' sums are joined about."""
+    D = C // 4
+    t = G.inputs(3, R, C, torch.float32, seed=5)
+    clean = ops.group_norm(t["x"], 4, t["weight"], t["bias"])
+    t["x"][1, 0, D] = bad
+    y, mean, rstd = ops.group_norm(t["x"], 4, t["weight"], t["bias"], return_stats=True)
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[1, :, D:2 * D] = True
+    assert bool(torch.isnan(y[1, 0, D])) and torch.equal(y[~hit], clean[~hit])
+    assert int(torch.isfinite(mean).sum()) == 11 and not bool(torch.isfinite(rstd[1, 1]))
