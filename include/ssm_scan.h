@@ -657,8 +657,9 @@ size_t ssm_grad_norm_workspace_bytes(int64_t count);
  *   128: 128 KB).
  *   Precision: states, sums and decays are fp32 or fp64.  fp32 io multiplies in fp32.
  *   In bf16 io computed values enter products with 17 bits: fp32 outputs (last_state;
- *   dg, dbeta, dh0 of the gradient) are off by some 5e-6 of their size, bf16 ones by
- *   their rounding; a caller who needs those to fp32's own precision passes fp32 io.
+ *   dg, dbeta, dh0 of the gradient) are off by some 5e-6 of their size in the root
+ *   mean square, single values by some times that, bf16 ones by their rounding; a
+ *   caller who needs them to fp32's own precision passes fp32 io.
  *   Sums are added in a fixed order: the same call gives the same bits.  How a sequence
  *   of 12 chunks or more is cut goes by all sequences of the call (so does a shorter
  *   one's among packed ones), and its last bits with it.

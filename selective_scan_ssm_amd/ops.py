@@ -917,8 +917,8 @@ def delta_scan_fwd(q, k, v, g, beta, scale=None, h0=None, starts=None, return_la
     of delta_ckpt_shape(...) that also receives what delta_scan_bwd needs of each
     64-step chunk, for delta_scan_bwd(..., ckpt=ckpt_out).  workspace: a uint8 tensor of
     at least delta_scan_workspace_bytes(...), allocated here without one.
-    bf16 inputs: fp32 outputs are off by some 5e-6 of their size (products of computed values have 17 bits), as
-    the gradient's; in fp32 both are good to fp32's rounding."""
+    bf16 inputs: fp32 outputs, the gradient's too, are off by some 5e-6 of their size in the root mean square (products
+    of computed values have 17 bits); fp32 inputs are multiplied in fp32."""
     lib = _lib.load()
     io, dev, (Bt, T, packed, nseq, Hk, H, K, V), ends, head = _delta_inputs(q, k, v, g, beta, scale, h0, starts)
     y = out if out is not None else torch.empty((Bt, T, H, V), dtype=io, device=dev)
